@@ -30,7 +30,18 @@ enum KernelKind : int32_t {
   KK_GRAM_SPACE = 9,
   KK_GRAM32 = 10,
   KK_GRAM32_REDUCE = 11,
-  KK_COUNT = 12
+  KK_EMBED_FWD = 12,
+  KK_EMBED_ZERO = 13,
+  KK_EMBED_SORT = 14,
+  KK_EMBED_SUM = 15,
+  KK_EMBED_JOIN = 16,
+  KK_LN_FWD = 17,
+  KK_LN_BWD = 18,
+  KK_LN_REDUCE = 19,
+  KK_DISTILL_FWD = 20,
+  KK_DISTILL_BWD = 21,
+  KK_DISTILL_STEP = 22,
+  KK_COUNT = 23
 };
 
 // Launch bookkeeping (libmuon.cu): counts launches and, while tracing, records an event pair.

@@ -1481,6 +1481,17 @@ const char *muon_kernel_name(int32_t kind) {
     case KK_GRAM_SPACE: return "ns_gram_space";
     case KK_GRAM32: return "ns_gram_f32";
     case KK_GRAM32_REDUCE: return "ns_gram_f32_reduce";
+    case KK_EMBED_FWD: return "embedding_forward";
+    case KK_EMBED_ZERO: return "embedding_zero";
+    case KK_EMBED_SORT: return "embedding_sort";
+    case KK_EMBED_SUM: return "embedding_sum";
+    case KK_EMBED_JOIN: return "embedding_join";
+    case KK_LN_FWD: return "layernorm_forward";
+    case KK_LN_BWD: return "layernorm_backward";
+    case KK_LN_REDUCE: return "layernorm_reduce";
+    case KK_DISTILL_FWD: return "distill_forward";
+    case KK_DISTILL_BWD: return "distill_backward";
+    case KK_DISTILL_STEP: return "distill_forward_backward";
     default: return "unknown";
   }
 }

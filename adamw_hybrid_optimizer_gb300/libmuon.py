@@ -26,6 +26,8 @@ MUON_ERR_TIMEOUT = 8
 
 MUON_F32 = 0
 MUON_BF16 = 1
+MUON_I32 = 0
+MUON_I64 = 1
 MUON_MAX_NS_STEPS = 32
 
 # the C signatures, checked against include/libmuon.h by tests/test_abi.py
@@ -84,6 +86,26 @@ SIGNATURES = {
     "ns_poly": (ctypes.c_int, [_vp, _vp, _c_int64, _c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp,
                                ctypes.c_size_t, _vp]),
     "ns_apply": (ctypes.c_int, [_vp, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "embedding_forward": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64,
+                                         _c_int64, _c_int64, _c_int64, ctypes.c_float, _vp]),
+    "embedding_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
+    "embedding_backward": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64,
+                                          _c_int64, _c_int64, _c_int64, ctypes.c_float, _c_int64, ctypes.c_int, _vp,
+                                          ctypes.c_size_t, _vp]),
+    "layernorm_forward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, _vp, ctypes.c_int, _vp, ctypes.c_int,
+                                         _c_int64, _vp, _vp, _c_int64, _c_int64, ctypes.c_float, _vp]),
+    "layernorm_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64]),
+    "layernorm_backward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int,
+                                          _vp, _vp, _vp, _c_int64, _vp, _vp, ctypes.c_int, ctypes.c_int, _c_int64,
+                                          _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "distill_forward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
+                                       _vp, _c_int64, _c_int64, _c_int64, ctypes.c_float, _vp]),
+    "distill_backward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
+                                        _vp, _vp, ctypes.c_int, _c_int64, _c_int64, _c_int64, _c_int64,
+                                        ctypes.c_float, _vp]),
+    "distill_forward_backward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _vp, ctypes.c_int,
+                                                _vp, ctypes.c_float, _vp, _vp, _vp, ctypes.c_int, _c_int64, _c_int64,
+                                                _c_int64, _c_int64, ctypes.c_float, _vp]),
     "muon_plan_buckets": (ctypes.c_int, [_c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "muon_autotune": (ctypes.c_int, [ctypes.POINTER(muon_bucket), ctypes.c_int, ctypes.POINTER(muon_hparams), _vp,
                                      ctypes.c_size_t, _vp]),
@@ -340,6 +362,168 @@ def ns_apply(h, x, out, ws, stream=None):
     K, m, n = x.shape
     _check(lib().ns_apply(h.data_ptr(), x.data_ptr(), out.data_ptr(), K, m, n, ws.data_ptr(),
                           ws.numel() * ws.element_size(), _stream(stream)), "ns_apply")
+
+
+# ------------------------------------------------------------------------------------------------------------
+# The operators around the AdamW tensors: embedding lookup, layer norm, distillation loss, and their gradients.
+# Matrices are 2-D tensors with contiguous columns; their row pitch is passed on. Shapes are checked here, since the
+# C calls cannot see them; everything else is checked there.
+# ------------------------------------------------------------------------------------------------------------
+
+
+def _itype_code(t) -> int:
+    import torch
+    if t.dtype == torch.int32:
+        return MUON_I32
+    if t.dtype == torch.int64:
+        return MUON_I64
+    raise MuonError(MUON_ERR_DTYPE, f"dtype {t.dtype}")
+
+
+def _matrix(t, name: str, where: str, shape=None) -> int:
+    """The row pitch of a 2-D CUDA tensor with contiguous columns (and of the given shape)."""
+    if t.dim() != 2 or not t.is_cuda or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{where}: {name} must be a 2-D CUDA tensor" + (f" of shape {shape}" if shape else ""))
+    rows, cols = t.shape
+    pitch, col = t.stride()
+    if cols > 1 and col != 1:
+        raise ValueError(f"{where}: {name} needs contiguous columns")
+    return pitch if rows > 1 else max(pitch, cols)
+
+
+def _vector(t, name: str, where: str, n: int, dtype=None) -> Optional[int]:
+    """The data pointer of an optional contiguous CUDA tensor of n elements (and of the given dtype)."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor of {n} elements"
+                         + (f" of {dtype}" if dtype is not None else ""))
+    return t.data_ptr()
+
+
+def embedding_forward(ids, table, out, scale: float = 1.0, stream=None):
+    """out[i] = scale * table[ids[i]]; ids: int32 or int64 of any shape, table (V, D), out (ids.numel(), D)."""
+    n, (V, D) = ids.numel(), table.shape
+    ldt = _matrix(table, "table", "embedding_forward")
+    ldo = _matrix(out, "out", "embedding_forward", (n, D))
+    st = lib().embedding_forward(_vector(ids, "ids", "embedding_forward", n), _itype_code(ids), table.data_ptr(),
+                                 _dtype_code(table), ldt, out.data_ptr(), _dtype_code(out), ldo, n, V, D, scale,
+                                 _stream(stream))
+    _check(st, "embedding_forward")
+
+
+def embedding_workspace_bytes(n: int, V: int, D: int) -> int:
+    return int(lib().embedding_workspace_bytes(int(n), int(V), int(D)))
+
+
+def embedding_backward(ids, dout, dtable, ws, scale: float = 1.0, padding_idx: int = -1, accumulate: bool = False,
+                       stream=None):
+    """dtable[v] = scale * the sum of dout's rows whose id is v; accumulate=True adds it to what dtable holds."""
+    n, (V, D) = ids.numel(), dtable.shape
+    ldo = _matrix(dout, "dout", "embedding_backward", (n, D))
+    ldg = _matrix(dtable, "dtable", "embedding_backward")
+    st = lib().embedding_backward(_vector(ids, "ids", "embedding_backward", n), _itype_code(ids), dout.data_ptr(),
+                                  _dtype_code(dout), ldo, dtable.data_ptr(), _dtype_code(dtable), ldg, n, V, D, scale,
+                                  padding_idx, int(bool(accumulate)), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  _stream(stream))
+    _check(st, "embedding_backward")
+
+
+def layernorm_forward(x, weight, bias, y, mean, rstd, eps: float = 1e-5, stream=None):
+    """y = layer norm of x's rows; weight and bias (one dtype) may be None, and so may mean and rstd (fp32, N)."""
+    import torch
+    N, D = x.shape
+    ldx = _matrix(x, "x", "layernorm_forward")
+    ldy = _matrix(y, "y", "layernorm_forward", (N, D))
+    wdt = _dtype_code(weight) if weight is not None else _dtype_code(bias) if bias is not None else MUON_F32
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("layernorm_forward: weight and bias of one dtype")
+    st = lib().layernorm_forward(x.data_ptr(), _dtype_code(x), ldx, _vector(weight, "weight", "layernorm_forward", D),
+                                 _vector(bias, "bias", "layernorm_forward", D), wdt, y.data_ptr(), _dtype_code(y), ldy,
+                                 _vector(mean, "mean", "layernorm_forward", N, torch.float32),
+                                 _vector(rstd, "rstd", "layernorm_forward", N, torch.float32), N, D, eps,
+                                 _stream(stream))
+    _check(st, "layernorm_forward")
+
+
+def layernorm_workspace_bytes(N: int, D: int) -> int:
+    return int(lib().layernorm_workspace_bytes(int(N), int(D)))
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, accumulate: bool = False, stream=None):
+    """Layer norm's gradients from the forward pass's mean and rstd; dx, dweight and dbias may be None (and ws, if the
+    latter two are). accumulate=True adds dweight and dbias to what they hold."""
+    import torch
+    N, D = x.shape
+    where = "layernorm_backward"
+    ldx = _matrix(x, "x", where)
+    lddy = _matrix(dy, "dy", where, (N, D))
+    lddx = D
+    if dx is not None:
+        lddx = _matrix(dx, "dx", where, (N, D))
+        if dx.dtype != x.dtype:
+            raise ValueError("layernorm_backward: dx has the dtype of x")
+    g = dweight if dweight is not None else dbias
+    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
+        raise ValueError("layernorm_backward: dweight and dbias of one dtype")
+    st = lib().layernorm_backward(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x), ldx,
+                                  _vector(weight, "weight", where, D),
+                                  _dtype_code(weight) if weight is not None else MUON_F32,
+                                  _vector(mean, "mean", where, N, torch.float32),
+                                  _vector(rstd, "rstd", where, N, torch.float32),
+                                  dx.data_ptr() if dx is not None else None, lddx,
+                                  _vector(dweight, "dweight", where, D), _vector(dbias, "dbias", where, D),
+                                  _dtype_code(g) if g is not None else MUON_F32, int(bool(accumulate)), N, D,
+                                  ws.data_ptr() if ws is not None else None,
+                                  ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream))
+    _check(st, where)
+
+
+def _distill(where, logits, t_idx, t_val, weights, stats):
+    import torch
+    N, V = logits.shape
+    ldz = _matrix(logits, "logits", where)
+    if t_idx.dim() != 2 or t_idx.shape[0] != N or t_idx.shape != t_val.shape:
+        raise ValueError(f"{where}: t_idx and t_val must both be ({N}, K)")
+    K = t_idx.shape[1]
+    return (N, V, K, (logits.data_ptr(), _dtype_code(logits), ldz, _vector(t_idx, "t_idx", where, N * K),
+                      _itype_code(t_idx), _vector(t_val, "t_val", where, N * K), _dtype_code(t_val),
+                      _vector(weights, "weights", where, N, torch.float32)),
+            _vector(stats, "stats", where, 2 * N, torch.float32))
+
+
+def distill_forward(logits, t_idx, t_val, temperature: float, weights, losses, stats, stream=None):
+    """losses[i] = weights[i] * T^2 * KL(teacher's top entries || student) of row i; stats (N, 2) for the backward pass.
+
+    logits (N, V); t_idx, t_val (N, K) contiguous; weights None or fp32 (N); losses fp32 (N)."""
+    import torch
+    N, V, K, head, st_ptr = _distill("distill_forward", logits, t_idx, t_val, weights, stats)
+    st = lib().distill_forward(*head, _vector(losses, "losses", "distill_forward", N, torch.float32), st_ptr, N, V, K,
+                               temperature, _stream(stream))
+    _check(st, "distill_forward")
+
+
+def distill_backward(logits, t_idx, t_val, temperature: float, weights, stats, grad, dlogits, stream=None):
+    """dlogits[i] = grad[i] * d losses[i] / d logits[i]; grad None (all 1) or fp32 (N). dlogits may be logits."""
+    import torch
+    N, V, K, head, st_ptr = _distill("distill_backward", logits, t_idx, t_val, weights, stats)
+    ldd = _matrix(dlogits, "dlogits", "distill_backward", (N, V))
+    st = lib().distill_backward(*head, st_ptr, _vector(grad, "grad", "distill_backward", N, torch.float32),
+                                dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature, _stream(stream))
+    _check(st, "distill_backward")
+
+
+def distill_forward_backward(logits, t_idx, t_val, temperature: float, weights, grad_scale: float, losses, stats,
+                             dlogits, stream=None):
+    """distill_forward and distill_backward (with grad_scale for every row's grad) in one call."""
+    import torch
+    where = "distill_forward_backward"
+    N, V, K, head, st_ptr = _distill(where, logits, t_idx, t_val, weights, stats)
+    ldd = _matrix(dlogits, "dlogits", where, (N, V))
+    st = lib().distill_forward_backward(*head, grad_scale, _vector(losses, "losses", where, N, torch.float32), st_ptr,
+                                        dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature,
+                                        _stream(stream))
+    _check(st, where)
 
 
 def muon_plan_buckets(shapes: Sequence[Tuple[int, int]]):

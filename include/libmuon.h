@@ -52,6 +52,9 @@ typedef enum {
 
 typedef enum { MUON_F32 = 0, MUON_BF16 = 1 } muon_dtype;
 
+/* Integer type of token ids and vocabulary indices. */
+typedef enum { MUON_I32 = 0, MUON_I64 = 1 } muon_itype;
+
 #define MUON_MAX_NS_STEPS 32
 
 /* Muon hyperparameters ([P2] "Muon: orthogonalising the update"; [P3] "Key options"). */
@@ -306,6 +309,100 @@ muon_status ns_poly(const void *g, void *h, int64_t K, int64_t m, float a, float
                     size_t ws_bytes, muon_stream_t stream);
 muon_status ns_apply(const void *h, const void *x, void *out, int64_t K, int64_t m, int64_t n, void *ws,
                      size_t ws_bytes, muon_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------------------
+ * The operators whose weights the AdamW half of the step updates ([P2] "Muon: orthogonalising the update": embedding,
+ * output layer and vectors stay on AdamW): the embedding lookup, layer norm and a loss at the vocabulary head, each
+ * with its gradients, which adamw_step_grouped takes as they are written. The pages name the tensors, not these
+ * operators' kernels. For all of them: a matrix has contiguous columns and a row pitch in elements (ld..., at least
+ * its columns); pointers need the alignment of their element type (MUON_ERR_ALIGNMENT otherwise), and 16-byte
+ * aligned pointers with pitches that are multiples of 8 take the vectorised path; sums are fp32, rounded once when
+ * stored; no sum goes through an atomic, so the same inputs give the same bits. A call with no rows launches
+ * nothing (backward calls still write the weights' gradients, as zeros) and may pass null for the empty arrays.
+ * ------------------------------------------------------------------------------------------------------------ */
+
+/* out_i = scale * table[ids[i]] for i < n. An id outside [0, V) names no row: its output is zeros.
+ *   ids    device, n of itype.   table  device V x D of tdt, pitch ldt.   out  device n x D of odt, pitch ldo.
+ * Limits: n <= 2^27, V <= 2^30, D <= 65536 (MUON_ERR_SHAPE). */
+muon_status embedding_forward(const void *ids, muon_itype itype, const void *table, muon_dtype tdt, int64_t ldt,
+                              void *out, muon_dtype odt, int64_t ldo, int64_t n, int64_t V, int64_t D, float scale,
+                              muon_stream_t stream);
+
+/* Bytes of workspace embedding_backward needs: the sorted ids and positions (twice), the sort's counts, and the
+ * partial sums of ids that occur often. 0 for n < 0, V < 1 or D < 1. */
+size_t embedding_workspace_bytes(int64_t n, int64_t V, int64_t D);
+
+/* The table's gradient: dtable_v = scale * sum over i with ids[i] = v of dout_i, added in increasing i. Ids outside
+ * [0, V) and ids equal to padding_idx (-1: none) contribute nothing.
+ *   dout    device n x D of odt, pitch ldo.   dtable  device V x D of gdt, pitch ldg.
+ *   accumulate  0: every row of dtable is written (zeros where no id names it). Else: the sums are added to what
+ *               dtable holds, and rows that no id names are not touched.
+ *   ws      device workspace of ws_bytes >= embedding_workspace_bytes(n, V, D), 256-byte aligned, no initialisation.
+ * Limits as for embedding_forward. */
+muon_status embedding_backward(const void *ids, muon_itype itype, const void *dout, muon_dtype odt, int64_t ldo,
+                               void *dtable, muon_dtype gdt, int64_t ldg, int64_t n, int64_t V, int64_t D, float scale,
+                               int64_t padding_idx, int accumulate, void *ws, size_t ws_bytes, muon_stream_t stream);
+
+/* Layer norm of N rows of D: y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps), var the mean of
+ * (x - mean)^2.
+ *   x       device N x D of xdt, pitch ldx.   y  device N x D of ydt, pitch ldy; may be x itself (same dtype and
+ *           pitch).
+ *   weight, bias  device, D of wdt each; either may be NULL (1 and 0).
+ *   mean, rstd    device fp32, N each, kept for the backward pass; either may be NULL.
+ * Limits: N <= 2^30, D <= 2^20 (MUON_ERR_SHAPE). */
+muon_status layernorm_forward(const void *x, muon_dtype xdt, int64_t ldx, const void *weight, const void *bias,
+                              muon_dtype wdt, void *y, muon_dtype ydt, int64_t ldy, float *mean, float *rstd, int64_t N,
+                              int64_t D, float eps, muon_stream_t stream);
+
+/* Bytes of workspace layernorm_backward needs for dweight or dbias: fp32 partial rows of both. 0 for N < 0 or D < 1. */
+size_t layernorm_workspace_bytes(int64_t N, int64_t D);
+
+/* Layer norm's gradients, from x and the mean and rstd of the forward pass: with xh = (x - mean) rstd and
+ * g = dy weight, dx = rstd (g - mean(g) - xh mean(g xh)), dweight = sum over rows of dy xh, dbias = sum of dy.
+ *   dy      device N x D of ydt, pitch lddy.   x as in the forward pass.   weight  NULL: 1.
+ *   dx      device N x D of xdt, pitch lddx, or NULL; may be dy or x itself (same dtype and pitch).
+ *   dweight, dbias  device, D of gdt each; either may be NULL. Not all three outputs may be NULL.
+ *   accumulate  0: dweight and dbias are written. Else: the sums are added to what they hold.
+ *   ws      device workspace of ws_bytes >= layernorm_workspace_bytes(N, D), 256-byte aligned, no initialisation;
+ *           may be NULL if dweight and dbias are. */
+muon_status layernorm_backward(const void *dy, muon_dtype ydt, int64_t lddy, const void *x, muon_dtype xdt, int64_t ldx,
+                               const void *weight, muon_dtype wdt, const float *mean, const float *rstd, void *dx,
+                               int64_t lddx, void *dweight, void *dbias, muon_dtype gdt, int accumulate, int64_t N,
+                               int64_t D, void *ws, size_t ws_bytes, muon_stream_t stream);
+
+/* Distillation from a teacher's top logits: for each of N rows, with q = softmax(t / T) over the row's valid teacher
+ * entries (index in [0, V), value above -inf) and p = softmax(z / T) over the V student logits,
+ *   losses_i = weights_i * T^2 * sum_k q_k (log q_k - log p_{idx_k}),
+ * the Kullback-Leibler divergence of p from q with the usual factor T^2. A row of weight 0 (padding) or with no
+ * valid entry has loss 0, stats 0 and gradient 0, and its logits do not matter (NaN included). Student logits of
+ * -inf are masked entries of the vocabulary (p = 0; a loss of +inf if a q there is not 0); a row of nothing else
+ * gives NaN. Entries of one row that name the same index add up.
+ *   logits  device N x V of zdt, pitch ldz.
+ *   t_idx   device N x K of itype, contiguous.   t_val  device N x K of tdt, contiguous, in any order.
+ *   weights device fp32, N, or NULL (all 1).
+ *   losses  device fp32, N.   stats  device fp32, N x 2, kept for the backward pass: m = max z and
+ *           l = log sum exp((z - m) / T).
+ * Limits: 1e-4 <= temperature <= 1e4; K <= 1024, N, V <= 2^30 (MUON_ERR_SHAPE). */
+muon_status distill_forward(const void *logits, muon_dtype zdt, int64_t ldz, const void *t_idx, muon_itype itype,
+                            const void *t_val, muon_dtype tdt, const float *weights, float *losses, float *stats,
+                            int64_t N, int64_t V, int64_t K, float temperature, muon_stream_t stream);
+
+/* The logits' gradient from distill_forward's stats: dlogits_ij = grad_i * weights_i * T * (p_ij - q_ij).
+ *   grad    device fp32, N: the gradient that reaches each row's loss, or NULL (all 1).
+ *   dlogits device N x V of ddt, pitch ldd; may be logits itself (same dtype and pitch), else must not overlap it. */
+muon_status distill_backward(const void *logits, muon_dtype zdt, int64_t ldz, const void *t_idx, muon_itype itype,
+                             const void *t_val, muon_dtype tdt, const float *weights, const float *stats,
+                             const float *grad, void *dlogits, muon_dtype ddt, int64_t ldd, int64_t N, int64_t V,
+                             int64_t K, float temperature, muon_stream_t stream);
+
+/* Both in one call, for a training step whose loss is grad_scale * sum of losses: losses and stats as
+ * distill_forward writes them, dlogits as distill_backward writes it with grad = grad_scale for every row. The
+ * logits are read from device memory once. */
+muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t ldz, const void *t_idx,
+                                     muon_itype itype, const void *t_val, muon_dtype tdt, const float *weights,
+                                     float grad_scale, float *losses, float *stats, void *dlogits, muon_dtype ddt,
+                                     int64_t ldd, int64_t N, int64_t V, int64_t K, float temperature,
+                                     muon_stream_t stream);
 
 /* Shape bucketing, host only ([P1] "Parameter Processing and Padding": stacking into (K, ...);
  * [P4] section 2.2 "Batching"). Groups n matrices by exact (rows, cols), buckets numbered in
