@@ -9,13 +9,22 @@
 // A row of weight 0, or without a valid entry, has loss 0 and gradient 0, and its logits are not used. m and l are
 // kept apart (stats), so that p = exp((z - m) / T - l) keeps its precision for logits of any size. All three forms
 // are bound by bandwidth: forward reads the logits once, with a running maximum and sum; backward reads them once
-// and writes the gradient; the joint form does both on one row in the same block, so that its second reading comes
-// from L2.
+// and writes the gradient; the joint form keeps a row in shared memory between its two passes.
+//
+// A row is cut into granules of eight logits on 16-byte boundaries of memory: a row whose start is not on one (an odd
+// vocabulary) has a short granule at each end, and everything between is whole vectors.
+//
+//   distill_forward_kernel   a cluster of 1 to 8 blocks per row, each with a slice of it: few rows still fill the GPU
+//   distill_backward_kernel  a block per row and slice
+//   distill_joint_kernel     a cluster per row, the slices in shared memory; while a thread writes the gradient of a
+//                            granule it starts the copy of the next row's granule into the same place
+//   distill_reread_kernel    the joint form for rows that do not fit: a block per row, which reads it twice
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -27,6 +36,7 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_K = 1024;
+constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct DistillArgs {
@@ -36,50 +46,118 @@ struct DistillArgs {
   float *losses, *stats;      // stats: N x 2 (m, l), written by the forward forms, read by backward
   void *dz;
   long long ldz, ldd, N;
-  int V, K, itype, tdt;
+  int V, K, itype, tdt, slices;
   float inv_t, temp, grad_scale;
 };
 
-// The row's teacher entries: index (-1: none), q, and the student's logit there (read before dz overwrites it).
-struct Teacher {
-  int idx[MAX_K];
-  float q[MAX_K], z[MAX_K];
+// exp(x * c), c = log2(e) / T; the difference x is taken in the logits' own unit, where it is exact or nearly so
+__device__ __forceinline__ float exp_scaled(float x, float c) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * c));
+  return y;
+}
+
+// ------------------------------------------------------------------------------------------ running softmax
+
+// A maximum and the sum of exp((x - m) c) below it.
+struct Soft {
+  float m, s;
 };
 
-__device__ __forceinline__ float block_max(float v, float *red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < WARPS; ++w) v = fmaxf(v, red[w]);
-  __syncthreads();
-  return v;
+__device__ __forceinline__ Soft merge(const Soft &a, const Soft &b, float c) {
+  const float m = fmaxf(a.m, b.m), ref = m == -INFINITY ? 0.f : m;
+  return {m, fmaf(a.s, exp_scaled(a.m - ref, c), b.s * exp_scaled(b.m - ref, c))};
 }
 
-__device__ __forceinline__ float block_sum(float v, float *red) {
-  v = warp_sum(v);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = 0.f;
+__device__ __forceinline__ Soft warp_merge(Soft a, float c) {
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) v += red[w];
-  __syncthreads();
-  return v;
+  for (int o = 16; o > 0; o >>= 1)
+    a = merge(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, c);
+  return a;
 }
 
-// exp(x * c), c = log2(e) / T; the difference x is taken in the logits' own unit, where it is exact or nearly so
-__device__ __forceinline__ float exp_scaled(float x, float c) { return exp2f(x * c); }
+// Eight logits; a granule of -inf leaves the sum alone.
+__device__ __forceinline__ void online8(const float *f, float c, Soft &a) {
+  float mx = f[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) mx = fmaxf(mx, f[e]);
+  if (mx > a.m) {
+    a.s *= exp_scaled(a.m - mx, c);
+    a.m = mx;
+  }
+  const float ref = a.m == -INFINITY ? 0.f : a.m;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a.s += exp_scaled(f[e] - ref, c);
+}
 
-// Loads the row's teacher entries and makes q. Returns whether the row has a valid one; lse_t: the log of the
-// teacher's sum, tmax its largest value.
-template <typename ZT>
-__device__ __forceinline__ bool load_teacher(const DistillArgs &a, long long row, const ZT *z, Teacher &s, float *red,
-                                             float &tmax, float &sum) {
+// ------------------------------------------------------------------------------------------ granules
+
+// Granules of one row. VEC: granule g holds logits 8 g - shift + e, where shift is the row's start past a boundary
+// (the same for z and dz, whose pitches differ by a multiple of eight); otherwise shift is 0 and every access is
+// of one element.
+struct Granules {
+  int shift, count, V;
+  __device__ __forceinline__ int first(int g) const { return 8 * g - shift; }
+  __device__ __forceinline__ bool whole(int g) const { return first(g) >= 0 && first(g) + 8 <= V; }
+};
+
+template <bool VEC>
+__device__ __forceinline__ Granules granules(long long row, long long ld, int V) {
+  const int shift = VEC ? static_cast<int>((row * ld) & 7) : 0;
+  return {shift, (V + shift + 7) / 8, V};
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_granule(const T *p, const Granules &G, int g, float *f) {
+  const int j = G.first(g);
+  if (VEC && G.whole(g)) {
+    load8(p + j, f);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = j + e >= 0 && j + e < G.V ? load1(p, j + e) : -INFINITY;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, const float *f) {
+  const int j = G.first(g);
+  if (VEC && G.whole(g)) {
+    store8(p + j, f);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (j + e >= 0 && j + e < G.V) store1(p, j + e, f[e]);
+}
+
+template <typename DT, bool VEC>
+__device__ __forceinline__ void zero_granules(DT *dz, const Granules &G, int g0, int g1) {
+  const float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int g = g0 + threadIdx.x; g < g1; g += THREADS) store_granule<DT, VEC>(dz, G, g, f);
+}
+
+// ------------------------------------------------------------------------------------------ the teacher's entries
+
+// A row's entries in (dynamic) shared memory, K of each: index (-1: none), value, and the student's logit there, read
+// before dz overwrites it (for indices in [lo, hi) only: those of the block's slice, where others may be writing).
+struct Teacher {
+  int *idx;
+  float *t, *z;
+};
+
+__device__ __forceinline__ Teacher teacher_at(void *smem, int K) {
+  int *idx = static_cast<int *>(smem);
+  const int pad = (K + 3) & ~3;
+  return {idx, reinterpret_cast<float *>(idx + pad), reinterpret_cast<float *>(idx + 2 * pad)};
+}
+constexpr size_t teacher_bytes(int K) { return static_cast<size_t>((K + 3) & ~3) * 12; }
+
+// Loads the thread's entries and returns their softmax sum. ALL: the student's logits of every entry, not of [lo, hi).
+template <typename ZT, bool ALL>
+__device__ __forceinline__ Soft load_teacher(const DistillArgs &a, long long row, const ZT *z, const Teacher &s, int lo,
+                                             int hi, float c) {
   const long long at = row * a.K;
-  float mx = -INFINITY;
-  bool any = false;
+  Soft sum{-INFINITY, 0.f};
   for (int k = threadIdx.x; k < a.K; k += THREADS) {
     const long long id = a.itype == MUON_I32 ? static_cast<long long>(static_cast<const int *>(a.t_idx)[at + k])
                                              : static_cast<const long long *>(a.t_idx)[at + k];
@@ -87,202 +165,402 @@ __device__ __forceinline__ bool load_teacher(const DistillArgs &a, long long row
                                       : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.t_val)[at + k]);
     const bool ok = id >= 0 && id < a.V && !(t == -INFINITY);   // a NaN is kept, and shows in the loss
     s.idx[k] = ok ? static_cast<int>(id) : -1;
-    s.q[k] = t;
-    s.z[k] = ok ? load1(z, id) : 0.f;
-    if (ok) {
-      mx = fmaxf(mx, t);
-      any = true;
-    }
+    s.t[k] = t;
+    s.z[k] = ok && (ALL || (id >= lo && id < hi)) ? load1(z, id) : 0.f;
+    if (ok) sum = merge(sum, {t, 1.f}, c);   // a NaN value goes into the sum through its own exponential
+    if (ok && t != t) sum.s = t;
   }
-  any = __syncthreads_or(any);
-  tmax = block_max(mx, red);
-  const float c = a.inv_t * LOG2E;
+  // the padding that subtract_teacher's vectors read
+  for (int k = a.K + threadIdx.x; k < ((a.K + 3) & ~3); k += THREADS) s.idx[k] = -1;
+  return sum;
+}
+
+// One exchange for the student's and the teacher's sums: every warp puts its pair, and after one barrier every warp
+// merges all of them. Calls alternate between two buffers.
+struct BlockRed {
+  float4 buf[2][WARPS];
+  float loss[2][WARPS];
+};
+
+// A thread can write a buffer again only after the barrier of the call in between, which every reader of that buffer
+// has reached.
+__device__ __forceinline__ void merge_all(BlockRed &r, int turn, float c, Soft &student, Soft &teacher) {
+  student = warp_merge(student, c);
+  teacher = warp_merge(teacher, c);
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) r.buf[turn][threadIdx.x / 32] = make_float4(student.m, student.s, teacher.m, teacher.s);
+  __syncthreads();
+  const float4 v = lane < WARPS ? r.buf[turn][lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  student = warp_merge({v.x, v.y}, c);
+  teacher = warp_merge({v.z, v.w}, c);
+}
+
+// The thread's part of sum_k q_k (log q_k - (z_k - m) / T); an entry whose q is 0 adds nothing, whatever the student
+// gives it.
+__device__ __forceinline__ float loss_part(const DistillArgs &a, const Teacher &s, const Soft &teacher, float m,
+                                           float c) {
+  const float tl = logf(teacher.s), tinv = 1.f / teacher.s;
   float part = 0.f;
-  for (int k = threadIdx.x; k < a.K; k += THREADS)
-    if (s.idx[k] >= 0) part += exp_scaled(s.q[k] - tmax, c);
-  sum = block_sum(part, red);
-  return any;
+  for (int k = threadIdx.x; k < a.K; k += THREADS) {
+    if (s.idx[k] < 0) continue;
+    const float d = s.t[k] - teacher.m;
+    const float q = exp_scaled(d, c) * tinv;
+    if (!(q == 0.f)) part = fmaf(q, (d * a.inv_t - tl) - (s.z[k] - m) * a.inv_t, part);
+  }
+  return warp_sum(part);
 }
 
-// Eight logits to a running (max, sum); a chunk of -inf leaves both alone.
-__device__ __forceinline__ void online8(const float *f, float c, float &m, float &s) {
-  float mx = f[0];
-#pragma unroll
-  for (int e = 1; e < 8; ++e) mx = fmaxf(mx, f[e]);
-  if (mx > m) {
-    s *= exp_scaled(m - mx, c);
-    m = mx;
-  }
-  const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) s += exp_scaled(f[e] - ref, c);
+__device__ __forceinline__ void store_loss(const DistillArgs &a, long long row, float w, const float *parts,
+                                           const Soft &student) {
+  float kl = 0.f;
+  for (int i = 0; i < WARPS; ++i) kl += parts[i];
+  const float l = logf(student.s);
+  a.losses[row] = w * a.temp * a.temp * (kl + l);
+  a.stats[2 * row] = student.m;
+  a.stats[2 * row + 1] = l;
 }
 
-// m and the sum of exp((z - m) / T) over the row. A row of nothing but -inf has no softmax: its sum is NaN.
-template <typename ZT, bool VEC>
-__device__ __forceinline__ void row_stats(const ZT *z, int V, float c, float *red, float &m, float &sum) {
-  float mt = -INFINITY, st = 0.f;
-  constexpr int U = 4;
-  int j0 = 0;
-  if constexpr (VEC) {
-    const int whole = V / (THREADS * 8 * U) * (THREADS * 8 * U);
-    for (; j0 < whole; j0 += THREADS * 8 * U) {
-      float f[U][8];
-#pragma unroll
-      for (int u = 0; u < U; ++u) load8(z + j0 + (u * THREADS + threadIdx.x) * 8, f[u]);
-#pragma unroll
-      for (int u = 0; u < U; ++u) online8(f[u], c, mt, st);
-    }
-    for (; j0 + THREADS * 8 <= V; j0 += THREADS * 8) {
-      float f[8];
-      load8(z + j0 + threadIdx.x * 8, f);
-      online8(f, c, mt, st);
-    }
-  }
-  for (; j0 < V; j0 += THREADS * 8) {
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = j0 + e * THREADS + threadIdx.x;
-      f[e] = j < V ? load1(z, j) : -INFINITY;
-    }
-    online8(f, c, mt, st);
-  }
-  m = block_max(mt, red);
-  const float ref = m == -INFINITY ? 0.f : m;
-  sum = block_sum(st * exp_scaled(mt - ref, c), red);
-  if (m == -INFINITY) sum = NAN;
+__device__ __forceinline__ void store_nothing(const DistillArgs &a, long long row) {
+  a.losses[row] = 0.f;
+  a.stats[2 * row] = 0.f;
+  a.stats[2 * row + 1] = 0.f;
 }
 
-// dz over columns [a0, a1): scale * (exp((z - m) / T) * inv - q), the q part by the entries themselves afterwards.
-template <typename ZT, typename DT, bool VEC>
-__device__ __forceinline__ void write_grad(const ZT *z, DT *dz, int V, float c, float m, float inv, float scale) {
-  int j0 = 0;
-  const float si = scale * inv;
-  if constexpr (VEC) {
-    for (; j0 + THREADS * 8 <= V; j0 += THREADS * 8) {
-      const int j = j0 + threadIdx.x * 8;
-      float f[8];
-      load8(z + j, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = exp_scaled(f[e] - m, c) * si;
-      store8(dz + j, f);
-    }
-  }
-  for (; j0 < V; j0 += THREADS * 8) {
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = j0 + e * THREADS + threadIdx.x;
-      if (j < V) f[e] = load1(z, j);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = j0 + e * THREADS + threadIdx.x;
-      if (j < V) store1(dz, j, exp_scaled(f[e] - m, c) * si);
-    }
-  }
-}
-
-template <typename DT>
-__device__ __forceinline__ void zero_row(DT *dz, int V) {
-  for (int j = threadIdx.x; j < V; j += THREADS) store1(dz, j, 0.f);
-}
-
-// The teacher's entries of a row whose p parts are written: the first entry of each index subtracts the q of all
+// Where the p parts of columns [lo, hi) are written: the first entry of each index there subtracts the q of all
 // entries of that index.
 template <typename DT>
-__device__ __forceinline__ void subtract_teacher(const DistillArgs &a, const Teacher &s, DT *dz, float c, float m,
-                                                 float inv, float scale, float tmax, float tinv) {
+__device__ __forceinline__ void subtract_teacher(const DistillArgs &a, const Teacher &s, DT *dz, int lo, int hi,
+                                                 float c, float m, float inv, float scale, const Soft &teacher) {
+  const float tinv = 1.f / teacher.s;
   for (int k = threadIdx.x; k < a.K; k += THREADS) {
     const int id = s.idx[k];
-    if (id < 0) continue;
+    if (id < lo || id >= hi) continue;   // absent entries are -1, below every lo
     bool first = true;
     float q = 0.f;
-    for (int i = 0; i < a.K; ++i) {
-      if (s.idx[i] != id) continue;
-      if (i < k) {
-        first = false;
-        break;
+    for (int i = 0; i < a.K; i += 4) {
+      const int4 v = *reinterpret_cast<const int4 *>(s.idx + i);
+      if (v.x != id && v.y != id && v.z != id && v.w != id) continue;
+      const int u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (u[e] != id) continue;
+        if (i + e < k) first = false;
+        q += exp_scaled(s.t[i + e] - teacher.m, c) * tinv;
       }
-      q += exp_scaled(s.q[i] - tmax, c) * tinv;
     }
     if (first) store1(dz, id, scale * (exp_scaled(s.z[k] - m, c) * inv - q));
   }
 }
 
-// GRAD false: losses and stats. GRAD true: dz too.
-template <typename ZT, typename DT, bool VEC, bool GRAD>
-__global__ void __launch_bounds__(THREADS) distill_forward_kernel(const DistillArgs a) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_launch_dependents();
-  __shared__ Teacher s;
-  __shared__ float red[WARPS];
-  const float c = a.inv_t * LOG2E;
-  for (long long row = blockIdx.x; row < a.N; row += gridDim.x) {
-    const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
-    DT *dz = GRAD ? static_cast<DT *>(a.dz) + row * a.ldd : nullptr;
-    const float w = a.weights != nullptr ? a.weights[row] : 1.f;
-    float tmax, tsum;
-    if (w == 0.f || !load_teacher(a, row, z, s, red, tmax, tsum)) {   // the same for the whole block
-      if (threadIdx.x == 0) {
-        a.losses[row] = 0.f;
-        a.stats[2 * row] = 0.f;
-        a.stats[2 * row + 1] = 0.f;
-      }
-      if constexpr (GRAD) zero_row(dz, a.V);
-      continue;
+// A row of nothing but -inf has no softmax.
+__device__ __forceinline__ void no_softmax(Soft &student) {
+  if (student.m == -INFINITY) student.s = NAN;
+}
+
+// ------------------------------------------------------------------------------------------ clusters
+
+__device__ __forceinline__ float2 load_remote(const float2 *p, unsigned rank) {
+  const uint32_t at = mapa_shared(smem_u32(p), rank);
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+// The student's sums of all slices of the row: every block puts its own and reads the others', in rank order, so that
+// all blocks get the same bits. `put` alternates between two places like the block's own exchange.
+__device__ __forceinline__ void merge_cluster(float2 *put, int blocks, float c, Soft &student) {
+  if (threadIdx.x == 0) *put = make_float2(student.m, student.s);
+  cluster_sync();
+  Soft all{-INFINITY, 0.f};
+  for (int r = 0; r < blocks; ++r) {
+    const float2 v = load_remote(put, r);
+    all = merge(all, {v.x, v.y}, c);
+  }
+  student = all;
+}
+
+// ------------------------------------------------------------------------------------------ kernels
+
+// The block's granules [g0, g1) of a row, four vectors at a time in flight.
+template <typename ZT, bool VEC>
+__device__ __forceinline__ Soft stream_soft(const ZT *z, const Granules &G, int g0, int g1, float c) {
+  Soft a{-INFINITY, 0.f};
+  constexpr int U = 4;
+  int g = g0 + threadIdx.x;
+  for (; g + (U - 1) * THREADS < g1; g += U * THREADS) {
+    float f[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_granule<ZT, VEC>(z, G, g + u * THREADS, f[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) online8(f[u], c, a);
+  }
+  for (; g < g1; g += THREADS) {
+    float f[8];
+    load_granule<ZT, VEC>(z, G, g, f);
+    online8(f, c, a);
+  }
+  return a;
+}
+
+// dz of granules [g0, g1), without the q part: si * exp((z - m) / T).
+template <typename ZT, typename DT, bool VEC>
+__device__ __forceinline__ void stream_grad(const ZT *z, DT *dz, const Granules &G, int g0, int g1, float c, float m,
+                                            float si) {
+  constexpr int U = 4;
+  int g = g0 + threadIdx.x;
+  for (; g + (U - 1) * THREADS < g1; g += U * THREADS) {
+    float f[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_granule<ZT, VEC>(z, G, g + u * THREADS, f[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[u][e] = exp_scaled(f[u][e] - m, c) * si;
+      store_granule<DT, VEC>(dz, G, g + u * THREADS, f[u]);
     }
-    float m, sum;
-    row_stats<ZT, VEC>(z, a.V, c, red, m, sum);
-    const float l = logf(sum), tl = logf(tsum), tinv = 1.f / tsum;
-    float part = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += THREADS) {
-      if (s.idx[k] < 0) continue;
-      const float d = s.q[k] - tmax;
-      const float q = exp_scaled(d, c) * tinv;
-      // an entry whose q is 0 adds nothing, whatever the student gives it
-      if (!(q == 0.f)) part = fmaf(q, (d * a.inv_t - tl) - (s.z[k] - m) * a.inv_t, part);
-    }
-    const float kl = block_sum(part, red) + l;
-    if (threadIdx.x == 0) {
-      a.losses[row] = w * a.temp * a.temp * kl;
-      a.stats[2 * row] = m;
-      a.stats[2 * row + 1] = l;
-    }
-    if constexpr (GRAD) {
-      const float scale = a.grad_scale * w * a.temp, inv = 1.f / sum;
-      write_grad<ZT, DT, VEC>(z, dz, a.V, c, m, inv, scale);
-      __syncthreads();
-      subtract_teacher(a, s, dz, c, m, inv, scale, tmax, tinv);
-    }
-    __syncthreads();   // the next row reuses s
+  }
+  for (; g < g1; g += THREADS) {
+    float f[8];
+    load_granule<ZT, VEC>(z, G, g, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = exp_scaled(f[e] - m, c) * si;
+    store_granule<DT, VEC>(dz, G, g, f);
   }
 }
 
-template <typename ZT, typename DT, bool VEC>
-__global__ void __launch_bounds__(THREADS) distill_backward_kernel(const DistillArgs a) {
+__device__ __forceinline__ float weight_of(const DistillArgs &a, long long row) {
+  return a.weights != nullptr ? a.weights[row] : 1.f;
+}
+
+template <typename ZT, bool VEC>
+__global__ void __launch_bounds__(THREADS, 2) distill_forward_kernel(const DistillArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  __shared__ Teacher s;
-  __shared__ float red[WARPS];
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ BlockRed red;
+  __shared__ float2 put;
+  const Teacher s = teacher_at(smem, a.K);
   const float c = a.inv_t * LOG2E;
-  for (long long row = blockIdx.x; row < a.N; row += gridDim.x) {
-    const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
+  const int slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const long long row = blockIdx.x / slices;
+  const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
+  const float w = weight_of(a, row);
+  if (w == 0.f) {   // the same for the whole cluster
+    if (rank == 0 && threadIdx.x == 0) store_nothing(a, row);
+    return;
+  }
+  const Granules G = granules<VEC>(row, a.ldz, a.V);
+  const int g0 = static_cast<int>(static_cast<long long>(G.count) * rank / slices);
+  const int g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices);
+  Soft teacher{-INFINITY, 0.f};
+  if (rank == 0) teacher = load_teacher<ZT, true>(a, row, z, s, 0, 0, c);
+  Soft student = stream_soft<ZT, VEC>(z, G, g0, g1, c);
+  merge_all(red, 0, c, student, teacher);
+  if (slices > 1) merge_cluster(&put, slices, c, student);
+  if (rank == 0) {
+    no_softmax(student);
+    const float part = loss_part(a, s, teacher, student.m, c);
+    if (threadIdx.x % 32 == 0) red.loss[0][threadIdx.x / 32] = part;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      if (teacher.s == 0.f) store_nothing(a, row);
+      else store_loss(a, row, w, red.loss[0], student);
+    }
+  }
+  if (slices > 1) cluster_sync();   // no block leaves while another reads its shared memory
+}
+
+template <typename ZT, typename DT, bool VEC>
+__global__ void __launch_bounds__(THREADS, 2) distill_backward_kernel(const DistillArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ BlockRed red;
+  const Teacher s = teacher_at(smem, a.K);
+  const float c = a.inv_t * LOG2E;
+  const long long row = blockIdx.x / a.slices;
+  const int rank = static_cast<int>(blockIdx.x - row * a.slices);
+  const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
+  DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
+  const Granules G = granules<VEC>(row, a.ldz, a.V);
+  const int g0 = static_cast<int>(static_cast<long long>(G.count) * rank / a.slices);
+  const int g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / a.slices);
+  const int lo = max(G.first(g0), 0), hi = min(G.first(g1), a.V);
+  const float w = weight_of(a, row);
+  if (w == 0.f) {
+    zero_granules<DT, VEC>(dz, G, g0, g1);
+    return;
+  }
+  Soft teacher = load_teacher<ZT, false>(a, row, z, s, lo, hi, c), student{-INFINITY, 0.f};
+  const float m = a.stats[2 * row], inv = expf(-a.stats[2 * row + 1]);
+  const float scale = (a.grad != nullptr ? a.grad[row] : 1.f) * w * a.temp;
+  merge_all(red, 0, c, student, teacher);   // its barrier also ends the reads of z that dz may overwrite
+  if (teacher.s == 0.f) {
+    zero_granules<DT, VEC>(dz, G, g0, g1);
+    return;
+  }
+  stream_grad<ZT, DT, VEC>(z, dz, G, g0, g1, c, m, scale * inv);
+  __syncthreads();
+  subtract_teacher(a, s, dz, lo, hi, c, m, inv, scale, teacher);
+}
+
+// The joint form without room for the row: a block per row, whose second reading is left to L2.
+template <typename ZT, typename DT, bool VEC>
+__global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const DistillArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ BlockRed red;
+  const Teacher s = teacher_at(smem, a.K);
+  const float c = a.inv_t * LOG2E;
+  const long long row = blockIdx.x;
+  const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
+  DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
+  const Granules G = granules<VEC>(row, a.ldz, a.V);
+  const float w = weight_of(a, row);
+  if (w == 0.f) {
+    if (threadIdx.x == 0) store_nothing(a, row);
+    zero_granules<DT, VEC>(dz, G, 0, G.count);
+    return;
+  }
+  Soft teacher = load_teacher<ZT, true>(a, row, z, s, 0, 0, c);
+  Soft student = stream_soft<ZT, VEC>(z, G, 0, G.count, c);
+  merge_all(red, 0, c, student, teacher);
+  if (teacher.s == 0.f) {
+    if (threadIdx.x == 0) store_nothing(a, row);
+    zero_granules<DT, VEC>(dz, G, 0, G.count);
+    return;
+  }
+  no_softmax(student);
+  const float part = loss_part(a, s, teacher, student.m, c);
+  if (threadIdx.x % 32 == 0) red.loss[0][threadIdx.x / 32] = part;
+  const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s;
+  stream_grad<ZT, DT, VEC>(z, dz, G, 0, G.count, c, student.m, scale * inv);
+  __syncthreads();
+  if (threadIdx.x == 0) store_loss(a, row, w, red.loss[0], student);
+  subtract_teacher(a, s, dz, 0, a.V, c, student.m, inv, scale, teacher);
+}
+
+// ------------------------------------------------------------------------------------------ joint form
+
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Granule `at` of the slice in shared memory: its 16-byte pieces are THREADS * ... apart, so that a warp's accesses to
+// one piece are contiguous. Every place is written and read by one thread only, so a thread's own wait is all the
+// ordering it needs.
+template <typename ZT>
+struct Kept {
+  static constexpr int PIECES = sizeof(ZT) * 8 / 16;
+  float4 *base;
+  int room;   // granules
+  __device__ __forceinline__ float4 *piece(int at, int p) const { return base + p * room + at; }
+  __device__ __forceinline__ void fetch(const ZT *z, const Granules &G, int g, int at) const {
+    if (G.whole(g)) {
+      const float4 *src = reinterpret_cast<const float4 *>(z + G.first(g));
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p) copy_async16(piece(at, p), src + p);
+    }
+  }
+  __device__ __forceinline__ void get(const ZT *z, const Granules &G, int g, int at, float *f) const {
+    if (G.whole(g)) {
+      float4 r[PIECES];
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p) r[p] = *piece(at, p);
+      load8(reinterpret_cast<const ZT *>(r), f);
+    } else {   // the row's two ends are read where they are
+      load_granule<ZT, false>(z, G, g, f);
+    }
+  }
+};
+
+template <typename ZT, typename DT>
+__global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const DistillArgs a, int room) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ BlockRed red;
+  __shared__ float2 put[2];
+  const Kept<ZT> kept{reinterpret_cast<float4 *>(smem), room};
+  const Teacher s = teacher_at(smem + static_cast<size_t>(room) * sizeof(ZT) * 8, a.K);
+  const float c = a.inv_t * LOG2E;
+  const int slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const long long step = gridDim.x / slices;
+  long long row = blockIdx.x / slices;
+  int turn = 0;
+  auto z_of = [&](long long r) { return static_cast<const ZT *>(a.z) + r * a.ldz; };
+  auto from = [&](const Granules &G) { return static_cast<int>(static_cast<long long>(G.count) * rank / slices); };
+  auto to = [&](const Granules &G) { return static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices); };
+  float w_next = row < a.N ? weight_of(a, row) : 0.f;
+  if (w_next != 0.f) {
+    const Granules G = granules<true>(row, a.ldz, a.V);
+    const int g0 = from(G), g1 = to(G);
+    for (int g = g0 + threadIdx.x; g < g1; g += THREADS) kept.fetch(z_of(row), G, g, g - g0);
+  }
+  copy_async_commit();
+  for (; row < a.N; row += step) {
+    const ZT *z = z_of(row);
     DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
-    const float w = a.weights != nullptr ? a.weights[row] : 1.f;
-    float tmax, tsum;
-    if (w == 0.f || !load_teacher(a, row, z, s, red, tmax, tsum)) {
-      zero_row(dz, a.V);
+    const Granules G = granules<true>(row, a.ldz, a.V);
+    const int g0 = from(G), g1 = to(G);
+    const int lo = max(G.first(g0), 0), hi = min(G.first(g1), a.V);
+    const float w = w_next;
+    const long long next = row + step;
+    w_next = next < a.N ? weight_of(a, next) : 0.f;
+    const Granules Gn = granules<true>(next, a.ldz, a.V);
+    const int n0 = from(Gn), n1 = next < a.N && w_next != 0.f ? to(Gn) : n0;
+    const ZT *zn = z_of(next);
+    const bool used = w != 0.f;   // the same for the whole cluster
+    Soft teacher{-INFINITY, 0.f}, student{-INFINITY, 0.f};
+    if (used) {
+      teacher = load_teacher<ZT, true>(a, row, z, s, 0, 0, c);
+      copy_async_wait_all();
+      for (int g = g0 + threadIdx.x; g < g1; g += THREADS) {
+        float f[8];
+        kept.get(z, G, g, g - g0, f);
+        online8(f, c, student);
+      }
+      merge_all(red, turn, c, student, teacher);
+      if (slices > 1) merge_cluster(&put[turn], slices, c, student);
+    }
+    const bool live = used && !(teacher.s == 0.f);
+    if (!live) {
+      if (rank == 0 && threadIdx.x == 0) store_nothing(a, row);
+      zero_granules<DT, true>(dz, G, g0, g1);
+      for (int at = threadIdx.x; at < n1 - n0; at += THREADS) kept.fetch(zn, Gn, n0 + at, at);
+      copy_async_commit();
+      if (used) turn ^= 1;
       continue;
     }
-    const float m = a.stats[2 * row], inv = expf(-a.stats[2 * row + 1]);
-    const float scale = (a.grad != nullptr ? a.grad[row] : 1.f) * w * a.temp;
-    write_grad<ZT, DT, VEC>(z, dz, a.V, c, m, inv, scale);
+    no_softmax(student);
+    if (rank == 0) {
+      const float part = loss_part(a, s, teacher, student.m, c);
+      if (threadIdx.x % 32 == 0) red.loss[turn][threadIdx.x / 32] = part;
+    }
+    const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s, si = scale * inv;
+    const int most = max(g1 - g0, n1 - n0);
+    for (int at = threadIdx.x; at < most; at += THREADS) {
+      if (at < g1 - g0) {
+        float f[8];
+        kept.get(z, G, g0 + at, at, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = exp_scaled(f[e] - student.m, c) * si;
+        store_granule<DT, true>(dz, G, g0 + at, f);
+      }
+      // the granule's values have gone into the store: its place may take the next row's
+      if (at < n1 - n0) kept.fetch(zn, Gn, n0 + at, at);
+    }
+    copy_async_commit();
     __syncthreads();
-    subtract_teacher(a, s, dz, c, m, inv, scale, tmax, 1.f / tsum);
-    __syncthreads();
+    if (rank == 0 && threadIdx.x == 0) store_loss(a, row, w, red.loss[turn], student);
+    subtract_teacher(a, s, dz, lo, hi, c, student.m, inv, scale, teacher);
+    __syncthreads();   // the next row's entries take the place of these
+    turn ^= 1;
   }
+  if (slices > 1) cluster_sync();   // no block leaves while another reads its shared memory
 }
 
 // ------------------------------------------------------------------------------------------ host
@@ -299,7 +577,7 @@ muon_status check_distill(const void *logits, muon_dtype zdt, int64_t ldz, const
   if (N > 0 && (logits == nullptr || t_idx == nullptr || t_val == nullptr || stats == nullptr))
     return MUON_ERR_INVALID_ARG;
   if (!(temperature >= 1e-4f && temperature <= 1e4f)) return MUON_ERR_INVALID_ARG;
-  if (N > (1ll << 30) || V > (1ll << 30) || K > MAX_K) return MUON_ERR_SHAPE;
+  if (N > (1ll << 30) || V > (1ll << 30) || N * V > (1ll << 40) || K > MAX_K) return MUON_ERR_SHAPE;
   if (!dtype_ok(zdt) || !dtype_ok(tdt) || (itype != MUON_I32 && itype != MUON_I64)) return MUON_ERR_DTYPE;
   if (!natural(logits, zdt) || !natural(t_val, tdt) || !natural(weights, MUON_F32) || !natural(stats, MUON_F32) ||
       (reinterpret_cast<uintptr_t>(t_idx) & (itype == MUON_I32 ? 3 : 7)) != 0)
@@ -326,18 +604,116 @@ DistillArgs distill_args(const void *logits, int64_t ldz, const void *t_idx, muo
   return a;
 }
 
-dim3 row_grid(int64_t N) { return dim3(static_cast<unsigned>(std::min<long long>(N, device_sm_count() * 64))); }
+// A dependent launch of clusters of `cluster` blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), long long blocks, int cluster, size_t smem, cudaStream_t s,
+                            Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
-template <typename ZT, typename DT, bool GRAD>
-cudaError_t launch_fwd(const DistillArgs &a, bool vec, cudaStream_t s) {
-  return vec ? launch_pdl(distill_forward_kernel<ZT, DT, true, GRAD>, row_grid(a.N), dim3(THREADS), 0, s, a)
-             : launch_pdl(distill_forward_kernel<ZT, DT, false, GRAD>, row_grid(a.N), dim3(THREADS), 0, s, a);
+// Blocks per row: as many as it takes to give every multiprocessor `per_sm` blocks, each with at least `least` logits.
+int row_slices(const DistillArgs &a, int per_sm, int least, int most) {
+  const long long want = static_cast<long long>(device_sm_count()) * per_sm;
+  int n = 1;
+  while (n < most && a.N * n < want && a.V / (2 * n) >= least) n *= 2;
+  return n;
+}
+
+template <typename ZT>
+cudaError_t launch_fwd(DistillArgs a, bool vec, cudaStream_t s) {
+  a.slices = row_slices(a, 2, 4096, MAX_CLUSTER);
+  const size_t smem = teacher_bytes(a.K);
+  return vec ? launch_clusters(distill_forward_kernel<ZT, true>, a.N * a.slices, a.slices, smem, s, a)
+             : launch_clusters(distill_forward_kernel<ZT, false>, a.N * a.slices, a.slices, smem, s, a);
 }
 
 template <typename ZT, typename DT>
-cudaError_t launch_bwd(const DistillArgs &a, bool vec, cudaStream_t s) {
-  return vec ? launch_pdl(distill_backward_kernel<ZT, DT, true>, row_grid(a.N), dim3(THREADS), 0, s, a)
-             : launch_pdl(distill_backward_kernel<ZT, DT, false>, row_grid(a.N), dim3(THREADS), 0, s, a);
+cudaError_t launch_bwd(DistillArgs a, bool vec, cudaStream_t s) {
+  // a block's start (its teacher entries) is paid back by some 32 Ki logits
+  a.slices = row_slices(a, 3, 4096, MAX_CLUSTER);
+  while (a.V / a.slices > 65536) a.slices *= 2;
+  const size_t smem = teacher_bytes(a.K);
+  const dim3 grid(static_cast<unsigned>(a.N * a.slices)), block(THREADS);
+  return vec ? launch_pdl(distill_backward_kernel<ZT, DT, true>, grid, block, smem, s, a)
+             : launch_pdl(distill_backward_kernel<ZT, DT, false>, grid, block, smem, s, a);
+}
+
+constexpr int SM_SHARED = 227 * 1024;          // what blocks of one multiprocessor can have together
+constexpr int BLOCK_SHARED = 2048;             // a block's static share and the system's, rounded up
+std::mutex g_joint_mu;
+
+// Clusters of this shape that the GPU holds at once (a persistent grid of more would leave the rest for last).
+template <typename ZT, typename DT>
+cudaError_t joint_clusters(int cluster, size_t smem, int *n) {
+  static int cached[MAX_CLUSTER + 1][3];       // by cluster size and blocks per multiprocessor; 0: not asked yet
+  auto kernel = distill_joint_kernel<ZT, DT>;
+  std::lock_guard<std::mutex> lk(g_joint_mu);
+  const int per_sm = static_cast<int>(std::min<size_t>(2, SM_SHARED / (smem + BLOCK_SHARED)));
+  int &c = cached[cluster][per_sm];
+  if (c == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SM_SHARED - BLOCK_SHARED);
+    if (e != cudaSuccess) return e;
+    if (cluster == 1) {
+      c = device_sm_count() * per_sm;
+    } else {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+      cfg.blockDim = dim3(THREADS);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&c, kernel, &cfg);
+      if (e != cudaSuccess) {
+        c = 0;
+        return e;
+      }
+    }
+  }
+  *n = std::max(1, c);
+  return cudaSuccess;
+}
+
+template <typename ZT, typename DT>
+cudaError_t launch_step(DistillArgs a, bool vec, cudaStream_t s) {
+  const size_t entries = teacher_bytes(a.K);
+  // slices of at most half a multiprocessor's shared memory, or of all of it where eight of those are too few
+  const size_t granule = 8 * sizeof(ZT), granules = (static_cast<size_t>(a.V) + 7 + 7) / 8;
+  const size_t half = (SM_SHARED / 2 - BLOCK_SHARED - entries) / granule, all = (SM_SHARED - BLOCK_SHARED - entries) / granule;
+  int slices = row_slices(a, 2, 4096, MAX_CLUSTER);
+  while (slices < MAX_CLUSTER && (granules + slices - 1) / slices + 1 > half) ++slices;
+  const size_t room = (granules + slices - 1) / slices + 1;
+  if (!vec || room > all) {
+    const dim3 grid(static_cast<unsigned>(a.N)), block(THREADS);
+    return vec ? launch_pdl(distill_reread_kernel<ZT, DT, true>, grid, block, entries, s, a)
+               : launch_pdl(distill_reread_kernel<ZT, DT, false>, grid, block, entries, s, a);
+  }
+  a.slices = slices;
+  const size_t smem = room * granule + entries;
+  int clusters = 0;
+  const cudaError_t e = joint_clusters<ZT, DT>(slices, smem, &clusters);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(distill_joint_kernel<ZT, DT>, std::min<long long>(a.N, clusters) * slices, slices, smem, s, a,
+                         static_cast<int>(room));
 }
 
 }  // namespace
@@ -360,10 +736,10 @@ muon_status distill_forward(const void *logits, muon_dtype zdt, int64_t ldz, con
   DistillArgs a = distill_args(logits, ldz, t_idx, itype, t_val, tdt, weights, N, V, K, temperature);
   a.losses = losses;
   a.stats = stats;
-  const bool vec = aligned16(logits) && ldz % 8 == 0;
+  const bool vec = aligned16(logits);
   launch_begin(KK_DISTILL_FWD, s);
-  const cudaError_t e = zdt == MUON_F32 ? launch_fwd<float, float, false>(a, vec, s)
-                                        : launch_fwd<__nv_bfloat16, float, false>(a, vec, s);
+  const cudaError_t e = zdt == MUON_F32 ? launch_fwd<float>(a, vec, s)
+                                        : launch_fwd<__nv_bfloat16>(a, vec, s);
   launch_end(s);
   return status_of(e);
 }
@@ -386,7 +762,7 @@ muon_status distill_backward(const void *logits, muon_dtype zdt, int64_t ldz, co
   a.grad = grad;
   a.dz = dlogits;
   a.ldd = ldd;
-  const bool vec = aligned16(logits) && ldz % 8 == 0 && aligned16(dlogits) && ldd % 8 == 0;
+  const bool vec = aligned16(logits) && aligned16(dlogits) && (ldz - ldd) % 8 == 0;
   launch_begin(KK_DISTILL_BWD, s);
   cudaError_t e;
   if (zdt == MUON_F32)
@@ -419,14 +795,14 @@ muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t
   a.dz = dlogits;
   a.ldd = ldd;
   a.grad_scale = grad_scale;
-  const bool vec = aligned16(logits) && ldz % 8 == 0 && aligned16(dlogits) && ldd % 8 == 0;
+  const bool vec = aligned16(logits) && aligned16(dlogits) && (ldz - ldd) % 8 == 0;
   launch_begin(KK_DISTILL_STEP, s);
   cudaError_t e;
   if (zdt == MUON_F32)
-    e = ddt == MUON_F32 ? launch_fwd<float, float, true>(a, vec, s) : launch_fwd<float, __nv_bfloat16, true>(a, vec, s);
+    e = ddt == MUON_F32 ? launch_step<float, float>(a, vec, s) : launch_step<float, __nv_bfloat16>(a, vec, s);
   else
-    e = ddt == MUON_F32 ? launch_fwd<__nv_bfloat16, float, true>(a, vec, s)
-                        : launch_fwd<__nv_bfloat16, __nv_bfloat16, true>(a, vec, s);
+    e = ddt == MUON_F32 ? launch_step<__nv_bfloat16, float>(a, vec, s)
+                        : launch_step<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
   launch_end(s);
   return status_of(e);
 }

@@ -382,7 +382,7 @@ muon_status layernorm_backward(const void *dy, muon_dtype ydt, int64_t lddy, con
  *   weights device fp32, N, or NULL (all 1).
  *   losses  device fp32, N.   stats  device fp32, N x 2, kept for the backward pass: m = max z and
  *           l = log sum exp((z - m) / T).
- * Limits: 1e-4 <= temperature <= 1e4; K <= 1024, N, V <= 2^30 (MUON_ERR_SHAPE). */
+ * Limits: 1e-4 <= temperature <= 1e4; K <= 1024, N, V <= 2^30, N * V <= 2^40 (MUON_ERR_SHAPE). */
 muon_status distill_forward(const void *logits, muon_dtype zdt, int64_t ldz, const void *t_idx, muon_itype itype,
                             const void *t_val, muon_dtype tdt, const float *weights, float *losses, float *stats,
                             int64_t N, int64_t V, int64_t K, float temperature, muon_stream_t stream);
