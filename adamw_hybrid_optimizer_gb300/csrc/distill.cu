@@ -57,6 +57,15 @@ __device__ __forceinline__ float exp_scaled(float x, float c) {
   return y;
 }
 
+// exp_scaled of both differences from m
+__device__ __forceinline__ float2 exp2_scaled(float2 x, float m, float c) {
+  const float2 v = __fmul2_rn(__fadd2_rn(x, make_float2(-m, -m)), make_float2(c, c));
+  float2 y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(v.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(v.y));
+  return y;
+}
+
 // ------------------------------------------------------------------------------------------ running softmax
 
 // A maximum and the sum of exp((x - m) c) below it.
@@ -76,28 +85,47 @@ __device__ __forceinline__ Soft warp_merge(Soft a, float c) {
   return a;
 }
 
-// Eight logits; a granule of -inf leaves the sum alone.
-__device__ __forceinline__ void online8(const float *f, float c, Soft &a) {
-  float mx = f[0];
+// A thread's running sum, as a pair.
+struct Run {
+  float m = -INFINITY;
+  float2 s = {0.f, 0.f};
+  // Eight logits; a granule of -inf leaves the sum alone.
+  __device__ __forceinline__ void add(const Oct &o, float c) {
+    const float mx = fmaxf(fmaxf(fmaxf(o.p[0].x, o.p[0].y), fmaxf(o.p[1].x, o.p[1].y)),
+                           fmaxf(fmaxf(o.p[2].x, o.p[2].y), fmaxf(o.p[3].x, o.p[3].y)));
+    if (mx > m) {
+      const float f = exp_scaled(m - mx, c);
+      s = __fmul2_rn(s, make_float2(f, f));
+      m = mx;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-  for (int e = 1; e < 8; ++e) mx = fmaxf(mx, f[e]);
-  if (mx > a.m) {
-    a.s *= exp_scaled(a.m - mx, c);
-    a.m = mx;
+    for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, exp2_scaled(o.p[i], ref, c));
   }
-  const float ref = a.m == -INFINITY ? 0.f : a.m;
+  __device__ __forceinline__ Soft soft() const { return {m, s.x + s.y}; }
+};
+
+// si * exp((z - m) / T) of eight logits
+__device__ __forceinline__ Oct grad_of(Oct o, float m, float c, float si) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a.s += exp_scaled(f[e] - ref, c);
+  for (int i = 0; i < 4; ++i) o.p[i] = __fmul2_rn(exp2_scaled(o.p[i], m, c), make_float2(si, si));
+  return o;
 }
 
 // ------------------------------------------------------------------------------------------ granules
 
 // Granules of one row. VEC: granule g holds logits 8 g - shift + e, where shift is the row's start past a boundary
 // (the same for z and dz, whose pitches differ by a multiple of eight); otherwise shift is 0 and every access is
-// of one element.
+// of one element. All granules but the first and the last are whole.
 struct Granules {
   int shift, count, V;
   __device__ __forceinline__ int first(int g) const { return 8 * g - shift; }
+  __device__ __forceinline__ bool inner(int g) const {
+    return static_cast<unsigned>(g - 1) < static_cast<unsigned>(max(count - 2, 0));
+  }
+  __device__ __forceinline__ bool has(int g, int e) const {
+    return first(g) + e >= 0 && first(g) + e < V;
+  }
   __device__ __forceinline__ bool whole(int g) const { return first(g) >= 0 && first(g) + 8 <= V; }
 };
 
@@ -107,34 +135,85 @@ __device__ __forceinline__ Granules granules(long long row, long long ld, int V)
   return {shift, (V + shift + 7) / 8, V};
 }
 
+template <typename T>
+__device__ __forceinline__ T neg_inf();
+template <>
+__device__ __forceinline__ float neg_inf<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 neg_inf<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff80); }
+
+// Places that the row does not have read as -inf.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_granule(const T *p, const Granules &G, int g, float *f) {
-  const int j = G.first(g);
-  if (VEC && G.whole(g)) {
-    load8(p + j, f);
+__device__ __forceinline__ void load_granule(const T *p, const Granules &G, int g, Raw8<T> &r) {
+  if (VEC && (G.inner(g) || G.whole(g))) {
+    r.load(p + G.first(g));
     return;
   }
+  T f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = j + e >= 0 && j + e < G.V ? load1(p, j + e) : -INFINITY;
+  for (int e = 0; e < 8; ++e) {
+    f[e] = neg_inf<T>();
+    if (G.has(g, e)) f[e] = p[G.first(g) + e];
+  }
+  r.set(f);
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, const float *f) {
-  const int j = G.first(g);
-  if (VEC && G.whole(g)) {
-    store8(p + j, f);
+__device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, const Oct &o) {
+  if (VEC && (G.inner(g) || G.whole(g))) {
+    store_oct(p + G.first(g), o);
     return;
   }
+  const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (j + e >= 0 && j + e < G.V) store1(p, j + e, f[e]);
+    if (G.has(g, e)) store1(p, G.first(g) + e, f[e]);
 }
 
 template <typename DT, bool VEC>
 __device__ __forceinline__ void zero_granules(DT *dz, const Granules &G, int g0, int g1) {
-  const float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int g = g0 + threadIdx.x; g < g1; g += THREADS) store_granule<DT, VEC>(dz, G, g, f);
+  Oct o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.p[i] = make_float2(0.f, 0.f);
+  for (int g = g0 + threadIdx.x; g < g1; g += THREADS) store_granule<DT, VEC>(dz, G, g, o);
 }
+
+// A thread's granules g0 + threadIdx.x, + THREADS, ... below g1, in batches: while one is used the loads of the next
+// are in flight.
+template <typename ZT, bool VEC>
+struct Stream {
+  static constexpr int U = sizeof(ZT) == 2 ? 4 : 2;
+  const ZT *z;
+  const Granules &G;
+  int g, g1;
+  Raw8<ZT> a[U], b[U];
+  __device__ __forceinline__ void fetch(Raw8<ZT> *r, int at) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at + u * THREADS < g1) load_granule<ZT, VEC>(z, G, at + u * THREADS, r[u]);
+  }
+  __device__ __forceinline__ Stream(const ZT *z_, const Granules &G_, int g0, int g1_)
+      : z(z_), G(G_), g(g0 + static_cast<int>(threadIdx.x)), g1(g1_) {
+    fetch(a, g);
+  }
+  template <typename F>
+  __device__ __forceinline__ void use(const Raw8<ZT> *r, F &&f) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (g + u * THREADS < g1) f(g + u * THREADS, r[u].get());
+    g += U * THREADS;
+  }
+  template <typename F>
+  __device__ __forceinline__ void run(F &&f) {
+    while (g < g1) {
+      fetch(b, g + U * THREADS);
+      use(a, f);
+      if (g >= g1) break;
+      fetch(a, g + U * THREADS);
+      use(b, f);
+    }
+  }
+};
 
 // ------------------------------------------------------------------------------------------ the teacher's entries
 
@@ -152,25 +231,50 @@ __device__ __forceinline__ Teacher teacher_at(void *smem, int K) {
 }
 constexpr size_t teacher_bytes(int K) { return static_cast<size_t>((K + 3) & ~3) * 12; }
 
-// Loads the thread's entries and returns their softmax sum. ALL: the student's logits of every entry, not of [lo, hi).
+// One entry as loaded. ok: it is valid.
+struct Entry {
+  long long id;
+  float t, z;
+  bool ok;
+};
+
+__device__ __forceinline__ Entry load_entry(const DistillArgs &a, long long row, int k) {
+  const long long at = row * a.K + k;
+  Entry e;
+  e.id = a.itype == MUON_I32 ? static_cast<long long>(static_cast<const int *>(a.t_idx)[at])
+                             : static_cast<const long long *>(a.t_idx)[at];
+  e.t = a.tdt == MUON_F32 ? static_cast<const float *>(a.t_val)[at]
+                          : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.t_val)[at]);
+  e.ok = e.id >= 0 && e.id < a.V && !(e.t == -INFINITY);   // a NaN is kept, and shows in the loss
+  return e;
+}
+
 template <typename ZT, bool ALL>
-__device__ __forceinline__ Soft load_teacher(const DistillArgs &a, long long row, const ZT *z, const Teacher &s, int lo,
-                                             int hi, float c) {
-  const long long at = row * a.K;
+__device__ __forceinline__ float entry_logit(const Entry &e, const ZT *z, int lo, int hi) {
+  return e.ok && (ALL || (e.id >= lo && e.id < hi)) ? load1(z, e.id) : 0.f;
+}
+
+// Puts entry k in its place and adds it to the thread's part of the teacher's sum. A NaN value goes into the sum as
+// it is.
+__device__ __forceinline__ void put_entry(const Teacher &s, int k, const Entry &e, float c, Soft &sum) {
+  s.idx[k] = e.ok ? static_cast<int>(e.id) : -1;
+  s.t[k] = e.t;
+  s.z[k] = e.z;
+  if (e.ok) sum = merge(sum, {e.t, e.t == e.t ? 1.f : e.t}, c);
+}
+
+// A thread's first entry (k = threadIdx.x) is loaded ahead; the rest of a long list, and the padding that
+// subtract_teacher's vectors read, when the first is put.
+template <typename ZT, bool ALL>
+__device__ __forceinline__ Soft put_teacher(const DistillArgs &a, long long row, const ZT *z, const Teacher &s, int lo,
+                                            int hi, float c, const Entry &ahead) {
   Soft sum{-INFINITY, 0.f};
-  for (int k = threadIdx.x; k < a.K; k += THREADS) {
-    const long long id = a.itype == MUON_I32 ? static_cast<long long>(static_cast<const int *>(a.t_idx)[at + k])
-                                             : static_cast<const long long *>(a.t_idx)[at + k];
-    const float t = a.tdt == MUON_F32 ? static_cast<const float *>(a.t_val)[at + k]
-                                      : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.t_val)[at + k]);
-    const bool ok = id >= 0 && id < a.V && !(t == -INFINITY);   // a NaN is kept, and shows in the loss
-    s.idx[k] = ok ? static_cast<int>(id) : -1;
-    s.t[k] = t;
-    s.z[k] = ok && (ALL || (id >= lo && id < hi)) ? load1(z, id) : 0.f;
-    if (ok) sum = merge(sum, {t, 1.f}, c);   // a NaN value goes into the sum through its own exponential
-    if (ok && t != t) sum.s = t;
+  if (static_cast<int>(threadIdx.x) < a.K) put_entry(s, threadIdx.x, ahead, c, sum);
+  for (int k = THREADS + threadIdx.x; k < a.K; k += THREADS) {
+    Entry e = load_entry(a, row, k);
+    e.z = entry_logit<ZT, ALL>(e, z, lo, hi);
+    put_entry(s, k, e, c, sum);
   }
-  // the padding that subtract_teacher's vectors read
   for (int k = a.K + threadIdx.x; k < ((a.K + 3) & ~3); k += THREADS) s.idx[k] = -1;
   return sum;
 }
@@ -281,53 +385,6 @@ __device__ __forceinline__ void merge_cluster(float2 *put, int blocks, float c, 
 
 // ------------------------------------------------------------------------------------------ kernels
 
-// The block's granules [g0, g1) of a row, four vectors at a time in flight.
-template <typename ZT, bool VEC>
-__device__ __forceinline__ Soft stream_soft(const ZT *z, const Granules &G, int g0, int g1, float c) {
-  Soft a{-INFINITY, 0.f};
-  constexpr int U = 4;
-  int g = g0 + threadIdx.x;
-  for (; g + (U - 1) * THREADS < g1; g += U * THREADS) {
-    float f[U][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u) load_granule<ZT, VEC>(z, G, g + u * THREADS, f[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u) online8(f[u], c, a);
-  }
-  for (; g < g1; g += THREADS) {
-    float f[8];
-    load_granule<ZT, VEC>(z, G, g, f);
-    online8(f, c, a);
-  }
-  return a;
-}
-
-// dz of granules [g0, g1), without the q part: si * exp((z - m) / T).
-template <typename ZT, typename DT, bool VEC>
-__device__ __forceinline__ void stream_grad(const ZT *z, DT *dz, const Granules &G, int g0, int g1, float c, float m,
-                                            float si) {
-  constexpr int U = 4;
-  int g = g0 + threadIdx.x;
-  for (; g + (U - 1) * THREADS < g1; g += U * THREADS) {
-    float f[U][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u) load_granule<ZT, VEC>(z, G, g + u * THREADS, f[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[u][e] = exp_scaled(f[u][e] - m, c) * si;
-      store_granule<DT, VEC>(dz, G, g + u * THREADS, f[u]);
-    }
-  }
-  for (; g < g1; g += THREADS) {
-    float f[8];
-    load_granule<ZT, VEC>(z, G, g, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = exp_scaled(f[e] - m, c) * si;
-    store_granule<DT, VEC>(dz, G, g, f);
-  }
-}
-
 __device__ __forceinline__ float weight_of(const DistillArgs &a, long long row) {
   return a.weights != nullptr ? a.weights[row] : 1.f;
 }
@@ -344,17 +401,23 @@ __global__ void __launch_bounds__(THREADS, 2) distill_forward_kernel(const Disti
   const int slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long long row = blockIdx.x / slices;
   const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
+  const Granules G = granules<VEC>(row, a.ldz, a.V);
+  const int g0 = static_cast<int>(static_cast<long long>(G.count) * rank / slices);
+  const int g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices);
+  const bool entry = rank == 0 && static_cast<int>(threadIdx.x) < a.K;
   const float w = weight_of(a, row);
+  Entry e{};
+  if (entry) e = load_entry(a, row, threadIdx.x);
   if (w == 0.f) {   // the same for the whole cluster
     if (rank == 0 && threadIdx.x == 0) store_nothing(a, row);
     return;
   }
-  const Granules G = granules<VEC>(row, a.ldz, a.V);
-  const int g0 = static_cast<int>(static_cast<long long>(G.count) * rank / slices);
-  const int g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices);
-  Soft teacher{-INFINITY, 0.f};
-  if (rank == 0) teacher = load_teacher<ZT, true>(a, row, z, s, 0, 0, c);
-  Soft student = stream_soft<ZT, VEC>(z, G, g0, g1, c);
+  Stream<ZT, VEC> stream(z, G, g0, g1);
+  if (entry) e.z = entry_logit<ZT, true>(e, z, 0, 0);
+  Run run;
+  stream.run([&](int, const Oct &o) { run.add(o, c); });
+  Soft student = run.soft(), teacher{-INFINITY, 0.f};
+  if (rank == 0) teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
   merge_all(red, 0, c, student, teacher);
   if (slices > 1) merge_cluster(&put, slices, c, student);
   if (rank == 0) {
@@ -387,19 +450,23 @@ __global__ void __launch_bounds__(THREADS, 2) distill_backward_kernel(const Dist
   const int g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / a.slices);
   const int lo = max(G.first(g0), 0), hi = min(G.first(g1), a.V);
   const float w = weight_of(a, row);
+  Entry e{};
+  if (static_cast<int>(threadIdx.x) < a.K) e = load_entry(a, row, threadIdx.x);
   if (w == 0.f) {
     zero_granules<DT, VEC>(dz, G, g0, g1);
     return;
   }
-  Soft teacher = load_teacher<ZT, false>(a, row, z, s, lo, hi, c), student{-INFINITY, 0.f};
-  const float m = a.stats[2 * row], inv = expf(-a.stats[2 * row + 1]);
-  const float scale = (a.grad != nullptr ? a.grad[row] : 1.f) * w * a.temp;
+  Stream<ZT, VEC> stream(z, G, g0, g1);
+  const float m = a.stats[2 * row], l = a.stats[2 * row + 1], up = a.grad != nullptr ? a.grad[row] : 1.f;
+  if (static_cast<int>(threadIdx.x) < a.K) e.z = entry_logit<ZT, false>(e, z, lo, hi);
+  Soft teacher = put_teacher<ZT, false>(a, row, z, s, lo, hi, c, e), student{-INFINITY, 0.f};
   merge_all(red, 0, c, student, teacher);   // its barrier also ends the reads of z that dz may overwrite
   if (teacher.s == 0.f) {
     zero_granules<DT, VEC>(dz, G, g0, g1);
     return;
   }
-  stream_grad<ZT, DT, VEC>(z, dz, G, g0, g1, c, m, scale * inv);
+  const float inv = expf(-l), scale = up * w * a.temp;
+  stream.run([&](int g, const Oct &o) { store_granule<DT, VEC>(dz, G, g, grad_of(o, m, c, scale * inv)); });
   __syncthreads();
   subtract_teacher(a, s, dz, lo, hi, c, m, inv, scale, teacher);
 }
@@ -418,13 +485,20 @@ __global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const Distil
   DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
   const Granules G = granules<VEC>(row, a.ldz, a.V);
   const float w = weight_of(a, row);
+  Entry e{};
+  if (static_cast<int>(threadIdx.x) < a.K) e = load_entry(a, row, threadIdx.x);
   if (w == 0.f) {
     if (threadIdx.x == 0) store_nothing(a, row);
     zero_granules<DT, VEC>(dz, G, 0, G.count);
     return;
   }
-  Soft teacher = load_teacher<ZT, true>(a, row, z, s, 0, 0, c);
-  Soft student = stream_soft<ZT, VEC>(z, G, 0, G.count, c);
+  if (static_cast<int>(threadIdx.x) < a.K) e.z = entry_logit<ZT, true>(e, z, 0, 0);
+  Run run;
+  {
+    Stream<ZT, VEC> stream(z, G, 0, G.count);
+    stream.run([&](int, const Oct &o) { run.add(o, c); });
+  }
+  Soft student = run.soft(), teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
   merge_all(red, 0, c, student, teacher);
   if (teacher.s == 0.f) {
     if (threadIdx.x == 0) store_nothing(a, row);
@@ -435,7 +509,8 @@ __global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const Distil
   const float part = loss_part(a, s, teacher, student.m, c);
   if (threadIdx.x % 32 == 0) red.loss[0][threadIdx.x / 32] = part;
   const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s;
-  stream_grad<ZT, DT, VEC>(z, dz, G, 0, G.count, c, student.m, scale * inv);
+  Stream<ZT, VEC> stream(z, G, 0, G.count);
+  stream.run([&](int g, const Oct &o) { store_granule<DT, VEC>(dz, G, g, grad_of(o, student.m, c, scale * inv)); });
   __syncthreads();
   if (threadIdx.x == 0) store_loss(a, row, w, red.loss[0], student);
   subtract_teacher(a, s, dz, 0, a.V, c, student.m, inv, scale, teacher);
@@ -443,37 +518,42 @@ __global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const Distil
 
 // ------------------------------------------------------------------------------------------ joint form
 
-__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// Granule `at` of the slice in shared memory: its 16-byte pieces are THREADS * ... apart, so that a warp's accesses to
-// one piece are contiguous. Every place is written and read by one thread only, so a thread's own wait is all the
-// ordering it needs.
+// Granule `at` of the slice in shared memory, in 16-byte pieces `room` apart, so that a warp's accesses to one piece
+// are contiguous. Every place is written and read by one thread only, so a thread's own wait is all the ordering it
+// needs.
 template <typename ZT>
 struct Kept {
-  static constexpr int PIECES = sizeof(ZT) * 8 / 16;
-  float4 *base;
+  static constexpr int PIECES = Raw8<ZT>::PIECES;
+  uint4 *base;
   int room;   // granules
-  __device__ __forceinline__ float4 *piece(int at, int p) const { return base + p * room + at; }
-  __device__ __forceinline__ void fetch(const ZT *z, const Granules &G, int g, int at) const {
-    if (G.whole(g)) {
-      const float4 *src = reinterpret_cast<const float4 *>(z + G.first(g));
+  // z: row `row` of N. A granule that the row has only part of is copied whole where the rest of it lies in the rows
+  // around (V >= 8), whose values get() leaves out; only the ends of the whole matrix are read element by element.
+  __device__ __forceinline__ void fetch(const ZT *z, const Granules &G, int g, int at, bool first_row,
+                                        bool last_row) const {
+    if (G.inner(g) || ((G.first(g) >= 0 || !first_row) && (G.first(g) + 8 <= G.V || !last_row))) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(z + G.first(g));
 #pragma unroll
-      for (int p = 0; p < PIECES; ++p) copy_async16(piece(at, p), src + p);
+      for (int p = 0; p < PIECES; ++p) copy_async16(base + p * room + at, src + p);
+    } else {
+      Raw8<ZT> r;
+      load_granule<ZT, false>(z, G, g, r);
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p) base[p * room + at] = r.w[p];
     }
   }
-  __device__ __forceinline__ void get(const ZT *z, const Granules &G, int g, int at, float *f) const {
-    if (G.whole(g)) {
-      float4 r[PIECES];
+  __device__ __forceinline__ Oct get(const Granules &G, int g, int at) const {
+    Raw8<ZT> r;
 #pragma unroll
-      for (int p = 0; p < PIECES; ++p) r[p] = *piece(at, p);
-      load8(reinterpret_cast<const ZT *>(r), f);
-    } else {   // the row's two ends are read where they are
-      load_granule<ZT, false>(z, G, g, f);
+    for (int p = 0; p < PIECES; ++p) r.w[p] = base[p * room + at];
+    Oct o = r.get();
+    if (!G.inner(g)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!G.has(g, 2 * i)) o.p[i].x = -INFINITY;
+        if (!G.has(g, 2 * i + 1)) o.p[i].y = -INFINITY;
+      }
     }
+    return o;
   }
 };
 
@@ -484,53 +564,63 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ BlockRed red;
   __shared__ float2 put[2];
-  const Kept<ZT> kept{reinterpret_cast<float4 *>(smem), room};
-  const Teacher s = teacher_at(smem + static_cast<size_t>(room) * sizeof(ZT) * 8, a.K);
+  const Kept<ZT> kept{reinterpret_cast<uint4 *>(smem), room};
+  unsigned char *entries = smem + static_cast<size_t>(room) * sizeof(ZT) * 8;
   const float c = a.inv_t * LOG2E;
   const int slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long long step = gridDim.x / slices;
   long long row = blockIdx.x / slices;
   int turn = 0;
+  const bool entry = static_cast<int>(threadIdx.x) < a.K;
   auto z_of = [&](long long r) { return static_cast<const ZT *>(a.z) + r * a.ldz; };
   auto from = [&](const Granules &G) { return static_cast<int>(static_cast<long long>(G.count) * rank / slices); };
   auto to = [&](const Granules &G) { return static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices); };
-  float w_next = row < a.N ? weight_of(a, row) : 0.f;
+  float w_next = weight_of(a, row);   // the grid has no more clusters than there are rows
+  Entry e_next{};
+  if (entry) e_next = load_entry(a, row, threadIdx.x);
   if (w_next != 0.f) {
     const Granules G = granules<true>(row, a.ldz, a.V);
-    const int g0 = from(G), g1 = to(G);
-    for (int g = g0 + threadIdx.x; g < g1; g += THREADS) kept.fetch(z_of(row), G, g, g - g0);
+    const int g0 = from(G), n = to(G) - g0;
+    for (int at = threadIdx.x; at < n; at += THREADS)
+      kept.fetch(z_of(row), G, g0 + at, at, row == 0, row + 1 == a.N);
   }
   copy_async_commit();
+  if (entry) e_next.z = entry_logit<ZT, true>(e_next, z_of(row), 0, 0);
   for (; row < a.N; row += step) {
-    const ZT *z = z_of(row);
     DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
     const Granules G = granules<true>(row, a.ldz, a.V);
-    const int g0 = from(G), g1 = to(G);
-    const int lo = max(G.first(g0), 0), hi = min(G.first(g1), a.V);
+    const int g0 = from(G), n = to(G) - g0;
+    const int lo = max(G.first(g0), 0), hi = min(G.first(g0 + n), a.V);
     const float w = w_next;
+    const Entry e = e_next;
+    // the next row: its weight and entries now, its logits and the entries' own as this one's gradient is written
     const long long next = row + step;
-    w_next = next < a.N ? weight_of(a, next) : 0.f;
+    const bool more = next < a.N;
+    if (more) {
+      w_next = weight_of(a, next);
+      if (entry) e_next = load_entry(a, next, threadIdx.x);
+    }
     const Granules Gn = granules<true>(next, a.ldz, a.V);
-    const int n0 = from(Gn), n1 = next < a.N && w_next != 0.f ? to(Gn) : n0;
+    const int n0 = from(Gn);
     const ZT *zn = z_of(next);
     const bool used = w != 0.f;   // the same for the whole cluster
+    const Teacher s = teacher_at(entries + turn * teacher_bytes(a.K), a.K);
     Soft teacher{-INFINITY, 0.f}, student{-INFINITY, 0.f};
     if (used) {
-      teacher = load_teacher<ZT, true>(a, row, z, s, 0, 0, c);
-      copy_async_wait_all();
-      for (int g = g0 + threadIdx.x; g < g1; g += THREADS) {
-        float f[8];
-        kept.get(z, G, g, g - g0, f);
-        online8(f, c, student);
-      }
+      Run run;
+      copy_async_wait<0>();
+      for (int at = threadIdx.x; at < n; at += THREADS) run.add(kept.get(G, g0 + at, at), c);
+      student = run.soft();
+      teacher = put_teacher<ZT, true>(a, row, z_of(row), s, 0, 0, c, e);
       merge_all(red, turn, c, student, teacher);
       if (slices > 1) merge_cluster(&put[turn], slices, c, student);
     }
-    const bool live = used && !(teacher.s == 0.f);
-    if (!live) {
+    const int nn = more && w_next != 0.f ? to(Gn) - n0 : 0;
+    if (more && entry) e_next.z = entry_logit<ZT, true>(e_next, zn, 0, 0);
+    if (!used || teacher.s == 0.f) {
       if (rank == 0 && threadIdx.x == 0) store_nothing(a, row);
-      zero_granules<DT, true>(dz, G, g0, g1);
-      for (int at = threadIdx.x; at < n1 - n0; at += THREADS) kept.fetch(zn, Gn, n0 + at, at);
+      zero_granules<DT, true>(dz, G, g0, g0 + n);
+      for (int at = threadIdx.x; at < nn; at += THREADS) kept.fetch(zn, Gn, n0 + at, at, false, next + 1 == a.N);
       copy_async_commit();
       if (used) turn ^= 1;
       continue;
@@ -541,23 +631,16 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
       if (threadIdx.x % 32 == 0) red.loss[turn][threadIdx.x / 32] = part;
     }
     const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s, si = scale * inv;
-    const int most = max(g1 - g0, n1 - n0);
-    for (int at = threadIdx.x; at < most; at += THREADS) {
-      if (at < g1 - g0) {
-        float f[8];
-        kept.get(z, G, g0 + at, at, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = exp_scaled(f[e] - student.m, c) * si;
-        store_granule<DT, true>(dz, G, g0 + at, f);
-      }
+    for (int at = threadIdx.x; at < max(n, nn); at += THREADS) {
+      if (at < n) store_granule<DT, true>(dz, G, g0 + at, grad_of(kept.get(G, g0 + at, at), student.m, c, si));
       // the granule's values have gone into the store: its place may take the next row's
-      if (at < n1 - n0) kept.fetch(zn, Gn, n0 + at, at);
+      if (at < nn) kept.fetch(zn, Gn, n0 + at, at, false, next + 1 == a.N);
     }
     copy_async_commit();
+    // what follows may run beside the next row: it has its own half of everything shared
     __syncthreads();
     if (rank == 0 && threadIdx.x == 0) store_loss(a, row, w, red.loss[turn], student);
     subtract_teacher(a, s, dz, lo, hi, c, student.m, inv, scale, teacher);
-    __syncthreads();   // the next row's entries take the place of these
     turn ^= 1;
   }
   if (slices > 1) cluster_sync();   // no block leaves while another reads its shared memory
@@ -695,20 +778,20 @@ cudaError_t joint_clusters(int cluster, size_t smem, int *n) {
 
 template <typename ZT, typename DT>
 cudaError_t launch_step(DistillArgs a, bool vec, cudaStream_t s) {
-  const size_t entries = teacher_bytes(a.K);
+  const size_t entries = teacher_bytes(a.K), both = 2 * entries;
   // slices of at most half a multiprocessor's shared memory, or of all of it where eight of those are too few
   const size_t granule = 8 * sizeof(ZT), granules = (static_cast<size_t>(a.V) + 7 + 7) / 8;
-  const size_t half = (SM_SHARED / 2 - BLOCK_SHARED - entries) / granule, all = (SM_SHARED - BLOCK_SHARED - entries) / granule;
+  const size_t half = (SM_SHARED / 2 - BLOCK_SHARED - both) / granule, all = (SM_SHARED - BLOCK_SHARED - both) / granule;
   int slices = row_slices(a, 2, 4096, MAX_CLUSTER);
   while (slices < MAX_CLUSTER && (granules + slices - 1) / slices + 1 > half) ++slices;
   const size_t room = (granules + slices - 1) / slices + 1;
-  if (!vec || room > all) {
+  if (!vec || room > all || a.V < 8) {
     const dim3 grid(static_cast<unsigned>(a.N)), block(THREADS);
     return vec ? launch_pdl(distill_reread_kernel<ZT, DT, true>, grid, block, entries, s, a)
                : launch_pdl(distill_reread_kernel<ZT, DT, false>, grid, block, entries, s, a);
   }
   a.slices = slices;
-  const size_t smem = room * granule + entries;
+  const size_t smem = room * granule + both;
   int clusters = 0;
   const cudaError_t e = joint_clusters<ZT, DT>(slices, smem, &clusters);
   if (e != cudaSuccess) return e;

@@ -60,43 +60,6 @@ __device__ __forceinline__ bool has(const Cols &c, int k, int e) {
   return (VEC ? 8 * k : 8 * k + e) < c.count;
 }
 
-// Eight values as loaded, converted only when they are used: the next row waits in half the registers.
-template <typename XT>
-struct Raw8;
-template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void get(float *f) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-  __device__ __forceinline__ void load(const float *p) {
-    a = reinterpret_cast<const float4 *>(p)[0];
-    b = reinterpret_cast<const float4 *>(p)[1];
-  }
-  __device__ __forceinline__ void set(const float *f) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
-  }
-};
-template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 w;
-  __device__ __forceinline__ void get(float *f) const {
-    const unsigned u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(u[e] << 16);
-      f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-    }
-  }
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void set(const __nv_bfloat16 *f) {
-    const unsigned short *h = reinterpret_cast<const unsigned short *>(f);
-    w = make_uint4(h[0] | (static_cast<unsigned>(h[1]) << 16), h[2] | (static_cast<unsigned>(h[3]) << 16),
-                   h[4] | (static_cast<unsigned>(h[5]) << 16), h[6] | (static_cast<unsigned>(h[7]) << 16));
-  }
-};
-
 template <typename XT>
 __device__ __forceinline__ XT zero_of() { return XT(0.f); }
 template <>
@@ -120,7 +83,8 @@ __device__ __forceinline__ void load_chunk(const XT *p, const Cols &c, int k, Ra
 }
 
 template <typename XT, bool VEC>
-__device__ __forceinline__ void store_chunk(XT *p, const Cols &c, int k, const float *f) {
+__device__ __forceinline__ void store_chunk(XT *p, const Cols &c, int k, const Oct &o) {
+  const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
   if constexpr (VEC) {
     if (has<true>(c, k, 0)) store8(p + col<true>(c, k, 0), f);
   } else {
@@ -132,46 +96,105 @@ __device__ __forceinline__ void store_chunk(XT *p, const Cols &c, int k, const f
 
 // The thread's weights (or biases): `absent` where there are none.
 template <bool VEC>
-__device__ __forceinline__ void param_chunk(const void *p, int dt, const Cols &c, int k, float absent, float *f) {
+__device__ __forceinline__ Oct param_chunk(const void *p, int dt, const Cols &c, int k, float absent) {
+  Oct o;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = absent;
-  if (p == nullptr) return;
+  for (int i = 0; i < 4; ++i) o.p[i] = make_float2(absent, absent);
+  if (p == nullptr) return o;
   if constexpr (VEC) {
-    if (!has<true>(c, k, 0)) return;
-    if (dt == MUON_F32) load8(static_cast<const float *>(p) + col<true>(c, k, 0), f);
-    else load8(static_cast<const __nv_bfloat16 *>(p) + col<true>(c, k, 0), f);
+    if (!has<true>(c, k, 0)) return o;
+    if (dt == MUON_F32) {
+      Raw8<float> r;
+      r.load(static_cast<const float *>(p) + col<true>(c, k, 0));
+      return r.get();
+    }
+    Raw8<__nv_bfloat16> r;
+    r.load(static_cast<const __nv_bfloat16 *>(p) + col<true>(c, k, 0));
+    return r.get();
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (has<false>(c, k, e)) f[e] = param_at(p, dt, col<false>(c, k, e), absent);
+      if (has<false>(c, k, e)) (e % 2 ? o.p[e / 2].y : o.p[e / 2].x) = param_at(p, dt, col<false>(c, k, e), absent);
+    return o;
   }
 }
 
-__device__ __forceinline__ float2 warp_sum2(float a, float b) {
+// Zero where the row has no column (without the vector path; on it a chunk is there or not).
+template <bool VEC>
+__device__ __forceinline__ float2 only(const Cols &c, int k, int i, float2 v) {
+  if (!VEC) {
+    if (!has<false>(c, k, 2 * i)) v.x = 0.f;
+    if (!has<false>(c, k, 2 * i + 1)) v.y = 0.f;
+  }
+  return v;
+}
+
+// The rows to come. On the vector path they are copied into a ring of STAGES places in shared memory, of which every
+// thread writes and reads its own columns only: its own wait orders them, and no registers hold them meanwhile.
+// Without it the next row's loads wait in registers.
+// One matrix's part of the ring: [stage][chunk][piece][thread].
+template <typename XT, int C>
+struct Ring {
+  static constexpr int PIECES = Raw8<XT>::PIECES;
+  uint4 *base;
+  __device__ __forceinline__ uint4 *at(int stage, int k, int p) const {
+    return base + ((stage * C + k) * PIECES + p) * blockDim.x + threadIdx.x;
+  }
+  __device__ __forceinline__ void fetch(const XT *row, const Cols &c, int stage) const {
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (has<true>(c, k, 0)) {
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p)
+          copy_async16(at(stage, k, p), reinterpret_cast<const uint4 *>(row + col<true>(c, k, 0)) + p);
+      }
+  }
+  __device__ __forceinline__ Oct get(const Cols &c, int k, int stage) const {
+    Raw8<XT> r;
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) r.w[p] = has<true>(c, k, 0) ? *at(stage, k, p) : make_uint4(0, 0, 0, 0);
+    return r.get();
+  }
+};
+
+__device__ __forceinline__ float2 warp_sum2(float2 v, int lanes = 32) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
+    if (o >= lanes) continue;
+    v = __fadd2_rn(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
   }
-  return make_float2(a, b);
+  return v;
+}
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 // The exchange between the W warps that hold a row: every warp puts a pair, and after one barrier of the row's own (a
-// named one, since a block may hold several rows) lane i of every warp reads the pair of warp i. Calls alternate
-// between two buffers: a thread can write one again only after the barrier of the call in between, which every
-// reader of that buffer has reached.
+// named one, since a block may hold several rows) lane i of every warp reads the pair of warp i, for i below the next
+// power of two `lanes` (and again for every further `lanes` lanes, so that sums over `lanes` lanes reach all). Calls
+// alternate between two buffers: a thread can write one again only after the barrier of the call in between, which
+// every reader of that buffer has reached.
 struct Group {
   float2 (*buf)[32];
-  int W, w, id, turn;
+  int W, w, id, lanes, turn;
   __device__ __forceinline__ float2 exchange(float a, float b) {
     float2 *r = buf[turn];
-    const int lane = threadIdx.x % 32;
+    const int lane = threadIdx.x % 32, from = lane & (lanes - 1);
     if (lane == 0) r[w] = make_float2(a, b);
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(W * 32) : "memory");
     turn ^= 1;
-    return lane < W ? r[lane] : make_float2(0.f, 0.f);
+    return from < W ? r[from] : make_float2(0.f, 0.f);
   }
 };
+
+__device__ __forceinline__ Group group_of(float2 (*buf)[32], int W, int t, int slot) {
+  int lanes = 1;
+  while (lanes < W) lanes *= 2;
+  return {buf, W, t / 32, slot + 1, lanes, 0};
+}
 
 // Sums over a block of 32 warps, for the kernels that give a block to a row.
 __device__ __forceinline__ float block_sum(float v, float (*red)[32], int &turn) {
@@ -187,8 +210,9 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[32], int &turn)
 
 // The most warps of a block, by the chunks C per thread and the row's width, and the blocks that the compiler is to
 // leave registers for on a multiprocessor.
-constexpr int fwd_blocks(int C, int MAXW) { return C == 1 ? 4 : MAXW == 16 ? 2 : 1; }
-constexpr int bwd_blocks(int C, int MAXW) { return C == 1 ? 3 : 1; }
+constexpr int fwd_blocks(int C, int MAXW) { return C == 1 ? 4 : C == 2 ? 32 / MAXW : MAXW == 4 ? 6 : 1; }
+constexpr int bwd_blocks(int C, int MAXW) { return C == 1 ? 3 : MAXW == 8 ? 2 : 1; }
+constexpr int STAGES = 3;
 
 struct ForwardArgs {
   const void *x, *w, *b;
@@ -199,79 +223,98 @@ struct ForwardArgs {
   int wdt, D;
 };
 
-// blockDim.x / (32 W) rows at a time, W warps each. The next row's loads are issued before the current row's sums are
-// exchanged, so that the barrier and the stores run under them. Mean and variance take one exchange: each warp sums
-// its own columns and their squared distances from the warp's own mean, and
+// blockDim.x / (32 W) rows at a time, W warps each, with the next rows on their way. Mean and variance take one
+// exchange: each warp sums its own columns and their squared distances from the warp's own mean, and
 //   sum (x - mean)^2 = sum over warps of (own squares + n_w (mean_w - mean)^2).
 template <typename XT, typename YT, int C, int MAXW, int FIXED>
 __global__ void __launch_bounds__(MAXW * 32, fwd_blocks(C, MAXW)) layernorm_forward_kernel(const ForwardArgs a,
                                                                                            int warps) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  __shared__ float2 red[BLOCK_WARPS][2][32];
   constexpr bool VEC = FIXED == 0;
+  extern __shared__ uint4 ahead[];
+  __shared__ float2 red[BLOCK_WARPS][2][32];
   const int W = VEC ? warps : FIXED;
   const int T = W * 32, rows = blockDim.x / T, slot = threadIdx.x / T, t = threadIdx.x - slot * T, D = a.D;
-  Group grp{red[slot], W, t / 32, slot + 1, 0};
+  Group grp = group_of(red[slot], W, t, slot);
   const float inv = 1.f / static_cast<float>(D);
   const Cols c = cols_of<VEC>(t, T, D);
+  const Ring<XT, C> ring{ahead};
   // columns of this warp, and of the warp whose pair this lane reads in the exchange
   const float n_w = warp_sum(static_cast<float>(max(c.count, 0))), inv_n = n_w > 0.f ? 1.f / n_w : 0.f;
   float n_lane = n_w;
   if (W > 1) n_lane = grp.exchange(n_w, 0.f).x;
   const long long step = static_cast<long long>(gridDim.x) * rows;
   long long row = static_cast<long long>(blockIdx.x) * rows + slot;
-  Raw8<XT> raw[C];
-  if (row < a.N) {
+  auto x_of = [&](long long r) { return static_cast<const XT *>(a.x) + r * a.ldx; };
+  Raw8<XT> raw[VEC ? 1 : C];
+  int stage = 0;
+  if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < C; ++k)
-      load_chunk<XT, VEC>(static_cast<const XT *>(a.x) + row * a.ldx, c, k, raw[k]);
+    for (int i = 0; i < STAGES - 1; ++i) {
+      if (row + i * step < a.N) ring.fetch(x_of(row + i * step), c, i);
+      copy_async_commit();
+    }
+  } else if (row < a.N) {
+#pragma unroll
+    for (int k = 0; k < C; ++k) load_chunk<XT, false>(x_of(row), c, k, raw[k]);
   }
   for (; row < a.N; row += step) {
-    float v[C][8];
+    Oct v[C];
+    if constexpr (VEC) {
+      copy_async_wait<STAGES - 2>();
 #pragma unroll
-    for (int k = 0; k < C; ++k) raw[k].get(v[k]);
-    if (row + step < a.N) {
+      for (int k = 0; k < C; ++k) v[k] = ring.get(c, k, stage);
+      // the place of the row before this one, whose values are long used, takes the row STAGES - 1 ahead
+      const int free = stage == 0 ? STAGES - 1 : stage - 1;
+      const long long r = row + (STAGES - 1) * step;
+      if (r < a.N) ring.fetch(x_of(r), c, free);
+      copy_async_commit();
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+    } else {
 #pragma unroll
-      for (int k = 0; k < C; ++k)
-        load_chunk<XT, VEC>(static_cast<const XT *>(a.x) + (row + step) * a.ldx, c, k, raw[k]);
-    }
-    float s = 0.f;
+      for (int k = 0; k < C; ++k) v[k] = raw[k].get();
+      if (row + step < a.N) {
 #pragma unroll
-    for (int k = 0; k < C; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[k][e];
-    s = warp_sum(s);
-    const float own = s * inv_n;
-    float q = 0.f;
-#pragma unroll
-    for (int k = 0; k < C; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = v[k][e] - own;
-        if (has<VEC>(c, k, e)) q = fmaf(d, d, q);
+        for (int k = 0; k < C; ++k) load_chunk<XT, false>(x_of(row + step), c, k, raw[k]);
       }
-    q = warp_sum(q);
-    float mean = own;
-    if (W > 1) {
-      const float2 r = grp.exchange(own, q);
-      mean = warp_sum(n_lane * r.x) * inv;
-      const float d = r.x - mean;
-      q = warp_sum(fmaf(n_lane * d, d, r.y));
     }
-    const float rstd = 1.f / sqrtf(q * inv + a.eps);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, v[k].p[i]);
+    const float own = warp_sum(s.x + s.y) * inv_n;
+    float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (!VEC || has<true>(c, k, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 d = only<VEC>(c, k, i, __fadd2_rn(v[k].p[i], make_float2(-own, -own)));
+          q = __ffma2_rn(d, d, q);
+        }
+      }
+    float sq = warp_sum(q.x + q.y), mean = own;
+    if (W > 1) {
+      const float2 r = grp.exchange(own, sq);
+      mean = lanes_sum(n_lane * r.x, grp.lanes) * inv;
+      const float d = r.x - mean;
+      sq = lanes_sum(fmaf(n_lane * d, d, r.y), grp.lanes);
+    }
+    const float rstd = rsqrtf(sq * inv + a.eps);
     if (t == 0) {
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
     YT *y = static_cast<YT *>(a.y) + row * a.ldy;
+    const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      float w[8], b[8];
-      param_chunk<VEC>(a.w, a.wdt, c, k, 1.f, w);
-      param_chunk<VEC>(a.b, a.wdt, c, k, 0.f, b);
+      const Oct w = param_chunk<VEC>(a.w, a.wdt, c, k, 1.f), b = param_chunk<VEC>(a.b, a.wdt, c, k, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = fmaf((v[k][e] - mean) * rstd, w[e], b[e]);
+      for (int i = 0; i < 4; ++i)
+        v[k].p[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[k].p[i], m2), r2), w.p[i], b.p[i]);
       store_chunk<YT, VEC>(y, c, k, v[k]);
     }
   }
@@ -320,105 +363,153 @@ struct BackwardArgs {
 
 // Rows and prefetch as in the forward kernel. Each thread keeps its columns of dw and db over all rows of its slot, in
 // registers, or in shared memory for rows of more than 8192 columns (MAXW = 32: 1024 threads have 64 registers each,
-// and the next row is fetched ahead only where it fits them); the block's slots are added in order at the end.
+// and the rest of shared memory has no room for a ring, so the next row waits in registers where it fits them); the
+// block's slots are added in order at the end.
 template <typename XT, typename YT, int C, int MAXW, int FIXED>
 __global__ void __launch_bounds__(MAXW * 32, bwd_blocks(C, MAXW)) layernorm_backward_kernel(const BackwardArgs a,
                                                                                             int warps) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  constexpr bool IN_SHARED = MAXW == 32, AHEAD = !IN_SHARED || sizeof(XT) + sizeof(YT) == 4;
-  extern __shared__ float4 sums[];   // IN_SHARED: [4 C][threads]: two of dw, two of db for each chunk
+  constexpr bool VEC = FIXED == 0, IN_SHARED = MAXW == 32, RING = VEC && !IN_SHARED;
+  constexpr bool AHEAD = !RING && (!IN_SHARED || sizeof(XT) + sizeof(YT) == 4);
+  extern __shared__ uint4 ahead[];   // the rings, or IN_SHARED: [4 C][threads]: two of dw, two of db for each chunk
   __shared__ float2 red[BLOCK_WARPS][2][32];
-  __shared__ float join[C == 1 ? BLOCK_WARPS * 256 : 1];
-  constexpr bool VEC = FIXED == 0;
+  __shared__ __align__(16) float join[C == 1 ? BLOCK_WARPS * 256 : 1];
   const int W = VEC ? warps : FIXED;
   const int T = W * 32, rows = blockDim.x / T, slot = threadIdx.x / T, t = threadIdx.x - slot * T, D = a.D;
-  Group grp{red[slot], W, t / 32, slot + 1, 0};
+  Group grp = group_of(red[slot], W, t, slot);
   const float inv = 1.f / static_cast<float>(D);
   const Cols c = cols_of<VEC>(t, T, D);
-  float aw[C][8], ab[C][8];
+  float4 *sums = reinterpret_cast<float4 *>(ahead);
+  const Ring<XT, C> ring_x{ahead};
+  const Ring<YT, C> ring_dy{ahead + STAGES * C * Raw8<XT>::PIECES * blockDim.x};
+  Oct aw[C], ab[C];
 #pragma unroll
   for (int k = 0; k < C; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aw[k][e] = ab[k][e] = 0.f;
-  if constexpr (IN_SHARED) {
+    for (int i = 0; i < 4; ++i) aw[k].p[i] = ab[k].p[i] = make_float2(0.f, 0.f);
+  auto sums_get = [&](int k) {
+    if constexpr (IN_SHARED) {
 #pragma unroll
-    for (int i = 0; i < 4 * C; ++i) sums[i * T + t] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+      for (int h = 0; h < 2; ++h) {
+        const float4 u = sums[(4 * k + h) * T + t], v = sums[(4 * k + 2 + h) * T + t];
+        aw[k].p[2 * h] = make_float2(u.x, u.y);
+        aw[k].p[2 * h + 1] = make_float2(u.z, u.w);
+        ab[k].p[2 * h] = make_float2(v.x, v.y);
+        ab[k].p[2 * h + 1] = make_float2(v.z, v.w);
+      }
+    }
+  };
+  auto sums_put = [&](int k) {
+    if constexpr (IN_SHARED) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 u = aw[k].p[2 * h], u1 = aw[k].p[2 * h + 1], v = ab[k].p[2 * h], v1 = ab[k].p[2 * h + 1];
+        sums[(4 * k + h) * T + t] = make_float4(u.x, u.y, u1.x, u1.y);
+        sums[(4 * k + 2 + h) * T + t] = make_float4(v.x, v.y, v1.x, v1.y);
+      }
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < C; ++k) sums_put(k);
   const long long step = static_cast<long long>(gridDim.x) * rows;
   long long row = static_cast<long long>(blockIdx.x) * rows + slot;
-  Raw8<XT> rx[C];
-  Raw8<YT> rdy[C];
-  float mean = 0.f, rstd = 0.f;
+  auto x_of = [&](long long r) { return static_cast<const XT *>(a.x) + r * a.ldx; };
+  auto dy_of = [&](long long r) { return static_cast<const YT *>(a.dy) + r * a.lddy; };
+  Raw8<XT> rx[RING ? 1 : C];
+  Raw8<YT> rdy[RING ? 1 : C];
   auto fetch = [&](long long r) {
+    if constexpr (!RING) {
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      load_chunk<XT, VEC>(static_cast<const XT *>(a.x) + r * a.ldx, c, k, rx[k]);
-      load_chunk<YT, VEC>(static_cast<const YT *>(a.dy) + r * a.lddy, c, k, rdy[k]);
-    }
-    mean = a.mean[r];
-    rstd = a.rstd[r];
-  };
-  if (AHEAD && row < a.N) fetch(row);
-  for (; row < a.N; row += step) {
-    if constexpr (!AHEAD) fetch(row);
-    float xh[C][8], g[C][8];
-    const float mu = mean, rs = rstd;
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-      rx[k].get(xh[k]);
-      rdy[k].get(g[k]);
-    }
-    if (AHEAD && row + step < a.N) fetch(row + step);
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-      float w[8];
-      param_chunk<VEC>(a.w, a.wdt, c, k, 1.f, w);
-      if constexpr (IN_SHARED) {
-        Raw8<float> r;
-        r.a = sums[(4 * k) * T + t];
-        r.b = sums[(4 * k + 1) * T + t];
-        r.get(aw[k]);
-        r.a = sums[(4 * k + 2) * T + t];
-        r.b = sums[(4 * k + 3) * T + t];
-        r.get(ab[k]);
+      for (int k = 0; k < C; ++k) {
+        load_chunk<XT, VEC>(x_of(r), c, k, rx[k]);
+        load_chunk<YT, VEC>(dy_of(r), c, k, rdy[k]);
       }
+    }
+  };
+  float mean = 0.f, rstd = 0.f;
+  int stage = 0;
+  if (row < a.N) {
+    mean = a.mean[row];
+    rstd = a.rstd[row];
+    if constexpr (AHEAD) fetch(row);
+  }
+  if constexpr (RING) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[k][e] = (xh[k][e] - mu) * rs;
-        // where the row has no column dy is 0, but xh need not be finite
-        if (has<VEC>(c, k, e)) {
-          aw[k][e] = fmaf(g[k][e], xh[k][e], aw[k][e]);
-          ab[k][e] += g[k][e];
-          g[k][e] *= w[e];
-          s1 += g[k][e];
-          s2 = fmaf(g[k][e], xh[k][e], s2);
+    for (int i = 0; i < STAGES - 1; ++i) {
+      if (row + i * step < a.N) {
+        ring_x.fetch(x_of(row + i * step), c, i);
+        ring_dy.fetch(dy_of(row + i * step), c, i);
+      }
+      copy_async_commit();
+    }
+  }
+  for (; row < a.N; row += step) {
+    if constexpr (!RING && !AHEAD) fetch(row);
+    const float rs = rstd;
+    const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rs, rs);
+    if (row + step < a.N) {
+      mean = a.mean[row + step];
+      rstd = a.rstd[row + step];
+    }
+    Oct xh[C], g[C];
+    if constexpr (RING) {
+      copy_async_wait<STAGES - 2>();
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        xh[k] = ring_x.get(c, k, stage);
+        g[k] = ring_dy.get(c, k, stage);
+      }
+      // the place of the row before this one, whose values are long used, takes the row STAGES - 1 ahead
+      const int free = stage == 0 ? STAGES - 1 : stage - 1;
+      const long long r = row + (STAGES - 1) * step;
+      if (r < a.N) {
+        ring_x.fetch(x_of(r), c, free);
+        ring_dy.fetch(dy_of(r), c, free);
+      }
+      copy_async_commit();
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        xh[k] = rx[k].get();
+        g[k] = rdy[k].get();
+      }
+      if (AHEAD && row + step < a.N) fetch(row + step);
+    }
+    float2 s1 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      const Oct w = param_chunk<VEC>(a.w, a.wdt, c, k, 1.f);
+      sums_get(k);
+      // where the row has no column dy is 0, but xh need not be finite
+      if (!VEC || has<true>(c, k, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 h = only<VEC>(c, k, i, __fmul2_rn(__fadd2_rn(xh[k].p[i], m2), r2));
+          xh[k].p[i] = h;
+          aw[k].p[i] = __ffma2_rn(g[k].p[i], h, aw[k].p[i]);
+          ab[k].p[i] = __fadd2_rn(ab[k].p[i], g[k].p[i]);
+          g[k].p[i] = __fmul2_rn(g[k].p[i], w.p[i]);
+          s1 = __fadd2_rn(s1, g[k].p[i]);
+          s2 = __ffma2_rn(g[k].p[i], h, s2);
         }
       }
-      if constexpr (IN_SHARED) {
-        Raw8<float> r;
-        r.set(aw[k]);
-        sums[(4 * k) * T + t] = r.a;
-        sums[(4 * k + 1) * T + t] = r.b;
-        r.set(ab[k]);
-        sums[(4 * k + 2) * T + t] = r.a;
-        sums[(4 * k + 3) * T + t] = r.b;
-      }
+      sums_put(k);
     }
-    float2 sum = warp_sum2(s1, s2);
+    float2 sum = warp_sum2(make_float2(s1.x + s1.y, s2.x + s2.y));
     if (W > 1) {
       sum = grp.exchange(sum.x, sum.y);
-      sum = warp_sum2(sum.x, sum.y);
+      sum = warp_sum2(sum, grp.lanes);
     }
-    s1 = sum.x * inv;
-    s2 = sum.y * inv;
     if (a.dx != nullptr) {
+      const float2 c1 = make_float2(-sum.x * inv, -sum.x * inv), c2 = make_float2(-sum.y * inv, -sum.y * inv);
       XT *dx = static_cast<XT *>(a.dx) + row * a.lddx;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[k][e] = rs * (g[k][e] - s1 - xh[k][e] * s2);
+        for (int i = 0; i < 4; ++i)
+          g[k].p[i] = __fmul2_rn(__ffma2_rn(xh[k].p[i], c2, __fadd2_rn(g[k].p[i], c1)), r2);
         store_chunk<XT, VEC>(dx, c, k, g[k]);
       }
     }
@@ -429,15 +520,7 @@ __global__ void __launch_bounds__(MAXW * 32, bwd_blocks(C, MAXW)) layernorm_back
   if (C > 1 || rows == 1) {
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      if constexpr (IN_SHARED) {
-        Raw8<float> r;
-        r.a = sums[(4 * k) * T + t];
-        r.b = sums[(4 * k + 1) * T + t];
-        r.get(aw[k]);
-        r.a = sums[(4 * k + 2) * T + t];
-        r.b = sums[(4 * k + 3) * T + t];
-        r.get(ab[k]);
-      }
+      sums_get(k);
       store_chunk<float, VEC>(pw, c, k, aw[k]);
       store_chunk<float, VEC>(pb, c, k, ab[k]);
     }
@@ -446,10 +529,8 @@ __global__ void __launch_bounds__(MAXW * 32, bwd_blocks(C, MAXW)) layernorm_back
   // several slots only where C = 1: rows * D <= BLOCK_WARPS * 256 columns
   for (int z = 0; z < 2; ++z) {
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (has<VEC>(c, 0, e)) join[slot * D + col<VEC>(c, 0, e)] = z == 0 ? aw[0][e] : ab[0][e];
-    }
+    const Oct o = z == 0 ? aw[0] : ab[0];
+    store_chunk<float, VEC>(join + slot * D, c, 0, o);
     __syncthreads();
     for (int j = threadIdx.x; j < D; j += blockDim.x) {
       float s = 0.f;
@@ -551,9 +632,9 @@ muon_status status_of(cudaError_t e) { return e == cudaSuccess ? MUON_OK : MUON_
 // compiled: each column is an access of its own there, and its offset has to be a constant to take no register.
 struct Shape {
   int C, W, rows;
+  int threads() const { return W * rows * 32; }
 };
-Shape shape_for(long long D, bool vec) {
-  const int C = D <= 1024 ? 1 : 2;
+Shape shape_of(long long D, bool vec, int C) {
   int W = static_cast<int>((D + 256 * C - 1) / (256 * C));
   if (!vec) {
     int p = 1;
@@ -562,23 +643,40 @@ Shape shape_for(long long D, bool vec) {
   }
   return {C, W, C == 1 ? std::max(1, BLOCK_WARPS / W) : 1};
 }
+// The forward pass takes four chunks where it can: the shuffles and the exchange of a row are shared by more columns.
+Shape fwd_shape(long long D, bool vec) { return shape_of(D, vec, D <= 1024 ? 1 : vec ? 4 : 2); }
+Shape bwd_shape(long long D, bool vec) { return shape_of(D, vec, D <= 1024 ? 1 : 2); }
 
 // Blocks of the backward pass, each of which leaves one partial row of dw and db: as many as the GPU holds at once,
 // so that there are few partial rows to add.
 long long parts_for(long long N, long long D, bool vec) {
   if (D > MAX_ROW) return std::max(1LL, std::min(N, 64LL));
-  const Shape h = shape_for(D, vec);
-  const long long resident = h.C == 1 ? bwd_blocks(1, BLOCK_WARPS) : std::max(1, 16 / h.W);
+  const Shape h = bwd_shape(D, vec);
+  const long long resident = std::max(1, (h.C == 1 ? 768 : 512) / h.threads());
   return std::max(1LL, std::min((N + h.rows - 1) / h.rows, 152 * resident));
 }
 long long part_pitch(long long D) { return (D + 7) / 8 * 8; }
 
+constexpr int SM_SHARED = 227 * 1024;
+constexpr int STATIC_SHARED = 16 * 1024;   // more than any kernel's static share
+
+// Once for each kernel that may take more than 48 KB.
+template <typename K>
+cudaError_t allow_shared(K kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_SHARED - STATIC_SHARED);
+}
+
 template <typename XT, typename YT, int C, int MAXW, int FIXED>
 cudaError_t forward_launch(const ForwardArgs &a, const Shape &h, cudaStream_t s) {
-  const int threads = h.W * h.rows * 32;
+  auto kernel = layernorm_forward_kernel<XT, YT, C, MAXW, FIXED>;
+  static const cudaError_t allowed = allow_shared(kernel);
+  if (allowed != cudaSuccess) return allowed;
+  const size_t smem = FIXED == 0 ? static_cast<size_t>(STAGES) * C * 8 * sizeof(XT) * h.threads() : 0;
   const long long sms = device_sm_count();
-  const dim3 grid(static_cast<unsigned>(std::min((a.N + h.rows - 1) / h.rows, sms * (2048 / threads))));
-  return launch_pdl(layernorm_forward_kernel<XT, YT, C, MAXW, FIXED>, grid, dim3(threads), 0, s, a, h.W);
+  const size_t held = smem + 6 * 1024;   // with the kernel's static share and the system's
+  const long long resident = std::min<long long>(fwd_blocks(C, MAXW) * MAXW * 32 / h.threads(), SM_SHARED / held);
+  const dim3 grid(static_cast<unsigned>(std::min((a.N + h.rows - 1) / h.rows, sms * resident)));
+  return launch_pdl(kernel, grid, dim3(h.threads()), smem, s, a, h.W);
 }
 
 template <typename XT, typename YT>
@@ -587,11 +685,11 @@ cudaError_t forward_route(const ForwardArgs &a, bool vec, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(std::min<long long>(a.N, device_sm_count() * 2))), block(LONG_THREADS);
     return launch_pdl(layernorm_forward_long_kernel<XT, YT>, grid, block, 0, s, a);
   }
-  const Shape h = shape_for(a.D, vec);
-  if (vec) {
-    if (h.C == 1) return forward_launch<XT, YT, 1, BLOCK_WARPS, 0>(a, h, s);
-    return h.W <= 16 ? forward_launch<XT, YT, 2, 16, 0>(a, h, s) : forward_launch<XT, YT, 2, 32, 0>(a, h, s);
-  }
+  const Shape h = fwd_shape(a.D, vec);
+  if (vec)
+    return h.C == 1    ? forward_launch<XT, YT, 1, BLOCK_WARPS, 0>(a, h, s)
+           : h.W <= 4  ? forward_launch<XT, YT, 4, 4, 0>(a, h, s)
+                       : forward_launch<XT, YT, 4, 16, 0>(a, h, s);
   if (h.C == 1)
     return h.W == 1   ? forward_launch<XT, YT, 1, BLOCK_WARPS, 1>(a, h, s)
            : h.W == 2 ? forward_launch<XT, YT, 1, BLOCK_WARPS, 2>(a, h, s)
@@ -605,14 +703,12 @@ cudaError_t forward_route(const ForwardArgs &a, bool vec, cudaStream_t s) {
 template <typename XT, typename YT, int C, int MAXW, int FIXED>
 cudaError_t backward_launch(const BackwardArgs &a, const Shape &h, cudaStream_t s) {
   auto kernel = layernorm_backward_kernel<XT, YT, C, MAXW, FIXED>;
-  const int threads = h.W * h.rows * 32;
-  const size_t smem = MAXW == 32 ? static_cast<size_t>(threads) * 4 * C * sizeof(float4) : 0;
-  if (MAXW == 32) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(MAXW * 32 * 4 * C * sizeof(float4)));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(a.parts)), dim3(threads), smem, s, a, h.W);
+  static const cudaError_t allowed = allow_shared(kernel);
+  if (allowed != cudaSuccess) return allowed;
+  const size_t per_thread = MAXW == 32 ? 4 * C * sizeof(float4)
+                            : FIXED == 0 ? static_cast<size_t>(STAGES) * C * 8 * (sizeof(XT) + sizeof(YT)) : 0;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(a.parts)), dim3(h.threads()), per_thread * h.threads(), s, a,
+                    h.W);
 }
 
 template <typename XT, typename YT>
@@ -629,11 +725,12 @@ cudaError_t backward_route(const BackwardArgs &a, bool vec, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(std::min<long long>(a.N, device_sm_count() * 2))), block(LONG_THREADS);
     return launch_pdl(layernorm_dx_long_kernel<XT, YT>, grid, block, 0, s, a);
   }
-  const Shape h = shape_for(a.D, vec);
-  if (vec) {
-    if (h.C == 1) return backward_launch<XT, YT, 1, BLOCK_WARPS, 0>(a, h, s);
-    return h.W <= 16 ? backward_launch<XT, YT, 2, 16, 0>(a, h, s) : backward_launch<XT, YT, 2, 32, 0>(a, h, s);
-  }
+  const Shape h = bwd_shape(a.D, vec);
+  if (vec)
+    return h.C == 1    ? backward_launch<XT, YT, 1, BLOCK_WARPS, 0>(a, h, s)
+           : h.W <= 8  ? backward_launch<XT, YT, 2, 8, 0>(a, h, s)
+           : h.W <= 16 ? backward_launch<XT, YT, 2, 16, 0>(a, h, s)
+                       : backward_launch<XT, YT, 2, 32, 0>(a, h, s);
   if (h.C == 1)
     return h.W == 1   ? backward_launch<XT, YT, 1, BLOCK_WARPS, 1>(a, h, s)
            : h.W == 2 ? backward_launch<XT, YT, 1, BLOCK_WARPS, 2>(a, h, s)

@@ -7,6 +7,8 @@
 
 #include <utility>
 
+#include "ptx.cuh"
+
 namespace muon {
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -60,6 +62,65 @@ __device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16 *p, lo
 }
 __device__ __forceinline__ void store1(float *p, long long i, float v) { p[i] = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, long long i, float v) { p[i] = __float2bfloat16_rn(v); }
+
+// Eight values as four pairs: pairs go through the two-wide fp32 instructions.
+struct Oct {
+  float2 p[4];
+};
+
+// Eight values as they lie in memory.
+template <typename XT>
+struct Raw8 {
+  static constexpr int PIECES = sizeof(XT) / 2;   // 16-byte pieces
+  uint4 w[PIECES];
+  __device__ __forceinline__ Oct get() const {
+    Oct o;
+    if constexpr (sizeof(XT) == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        o.p[2 * i] = make_float2(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
+        o.p[2 * i + 1] = make_float2(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
+      }
+    } else {
+      const unsigned u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o.p[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    }
+    return o;
+  }
+  __device__ __forceinline__ void load(const XT *p) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+  }
+  __device__ __forceinline__ void set(const XT *f) {
+    if constexpr (sizeof(XT) == 4) {
+      const unsigned *u = reinterpret_cast<const unsigned *>(f);
+      w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+      w[PIECES - 1] = make_uint4(u[4], u[5], u[6], u[7]);
+    } else {
+      const unsigned short *h = reinterpret_cast<const unsigned short *>(f);
+      w[0] = make_uint4(h[0] | (static_cast<unsigned>(h[1]) << 16), h[2] | (static_cast<unsigned>(h[3]) << 16),
+                        h[4] | (static_cast<unsigned>(h[5]) << 16), h[6] | (static_cast<unsigned>(h[7]) << 16));
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_oct(T *p, const Oct &o) {
+  const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
+  store8(p, f);
+}
+
+// Asynchronous copies to shared memory, 16 bytes each.
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Launch with programmatic stream serialization (the kernel waits for its predecessor itself).
 template <typename... KArgs, typename... Args>
