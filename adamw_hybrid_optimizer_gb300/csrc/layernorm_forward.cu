@@ -1,0 +1,261 @@
+// Layer norm over the rows of an N x D matrix, forward.
+//
+//   mu = mean(x), v = mean((x - mu)^2), r = 1 / sqrt(v + eps), y = (x - mu) r w + b
+//
+// Bound by bandwidth: a row is read once into registers (as fp32), its sums are exchanged between the warps that hold
+// it, and the result is stored. The variance is taken around a mean, so no E[x^2] - mu^2 cancels.
+//
+//   layernorm_forward_kernel       rows of up to 16384 columns
+//   layernorm_forward_long_kernel  longer rows: a block per row, re-reading it (from L2) for each sweep
+#include "layernorm.cuh"
+
+namespace muon {
+namespace {
+
+struct ForwardArgs {
+  const void *x, *w, *b;
+  void *y;
+  long long ldx, ldy, N;
+  float *mean, *rstd;
+  float eps;
+  int wdt, D;
+};
+
+// R rows at a time, W warps each, with the next rows on their way. Mean and variance take one exchange: each warp sums
+// its own columns and their squared distances from the warp's own mean, and
+//   sum (x - mean)^2 = sum over warps of (own squares + n_w (mean_w - mean)^2).
+template <typename XT, typename YT, int C, int W, int R, bool VEC>
+struct Forward {
+  static constexpr int T = W * 32, THREADS = T * R;
+  static constexpr bool SHARED = VEC && C > 1 && C * T * 8 <= 8192;
+  static constexpr int STAGES = C * T * 8 * sizeof(XT) <= 16384 ? 3 : 2;
+  static constexpr int RING = VEC ? STAGES * C * Raw8<XT>::PIECES * THREADS : 0;   // in 16-byte pieces
+  static constexpr size_t BYTES = 16 * static_cast<size_t>(RING + (SHARED ? 4 * C * THREADS : 0));
+  static constexpr int by_registers = C == 4 ? (W <= 4 ? 768 : 512) : 1024;   // threads of a multiprocessor
+  static constexpr int BLOCKS = std::max(1, by_registers / THREADS);
+};
+
+template <typename XT, typename YT, int C, int W, int R, bool VEC>
+__global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, VEC>::BLOCKS))
+    layernorm_forward_kernel(const ForwardArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  using F = Forward<XT, YT, C, W, R, VEC>;
+  constexpr int T = F::T, STAGES = F::STAGES;
+  extern __shared__ uint4 shared[];
+  __shared__ float2 red[2][R][W];
+  const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T;
+  const Cols c = cols_of<VEC>(t, T, a.D);
+  Exchange<W, R> exchange{red, slot, t / 32, 0};
+  const Ring<XT, C, F::THREADS> ring{shared + threadIdx.x};
+  float4 *kept = reinterpret_cast<float4 *>(shared + F::RING) + threadIdx.x;
+  Params<C, F::THREADS, VEC, F::SHARED> weight{a.w, a.wdt, 1.f, kept}, bias{a.b, a.wdt, 0.f, kept + 2 * C * F::THREADS};
+  weight.init(c);
+  bias.init(c);
+  const float inv = 1.f / static_cast<float>(a.D);
+  // columns of this warp, and of the warp whose pair this lane reads in the exchange
+  const float n_w = warp_sum(static_cast<float>(max(c.count, 0))), inv_n = n_w > 0.f ? 1.f / n_w : 0.f;
+  float n_lane = n_w;
+  if constexpr (W > 1) n_lane = exchange.put_get(n_w, 0.f).x;
+  const long long step = static_cast<long long>(gridDim.x) * R;
+  const long long x_step = step * a.ldx, y_step = step * a.ldy;
+  long long row = static_cast<long long>(blockIdx.x) * R + slot;
+  const XT *x = static_cast<const XT *>(a.x) + row * a.ldx;   // the next row to fetch
+  YT *y = static_cast<YT *>(a.y) + row * a.ldy;
+  long long fetched = row;
+  Raw8<XT> raw[VEC ? 1 : C];
+  auto fetch = [&](int stage) {
+    if (fetched < a.N) {
+      if constexpr (VEC) {
+        ring.fetch(x, c, stage);
+      } else {
+#pragma unroll
+        for (int k = 0; k < C; ++k) load_chunk<XT, false>(x, c, k, raw[k]);
+      }
+    }
+    if constexpr (VEC) copy_async_commit();
+    fetched += step;
+    x += x_step;
+  };
+  fetch(0);
+  if constexpr (VEC && STAGES == 3) fetch(1);
+  int stage = 0;
+  for (; row - slot < a.N; row += step) {   // the same count for the whole block
+    const bool live = R == 1 || row < a.N;
+    Oct v[C];
+    if constexpr (VEC) {
+      copy_async_wait<STAGES - 2>();
+#pragma unroll
+      for (int k = 0; k < C; ++k) v[k] = ring.get(k, stage);
+      // the place of the row before this one, whose values are long used, takes the row STAGES - 1 ahead
+      fetch(stage == 0 ? STAGES - 1 : stage - 1);
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int k = 0; k < C; ++k) v[k] = raw[k].get();
+      fetch(0);
+    }
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (has<VEC>(c, k, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, v[k].p[i]);
+      }
+    const float own = warp_sum(s.x + s.y) * inv_n;
+    float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (has<VEC>(c, k, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 d = only<VEC>(c, k, i, __fadd2_rn(v[k].p[i], make_float2(-own, -own)));
+          q = __ffma2_rn(d, d, q);
+        }
+      }
+    float sq = warp_sum(q.x + q.y), mean = own;
+    if constexpr (W > 1) {
+      const float2 r = exchange.put_get(own, sq);
+      mean = lanes_sum<Exchange<W, R>::LANES>(n_lane * r.x) * inv;
+      const float d = r.x - mean;
+      sq = lanes_sum<Exchange<W, R>::LANES>(fmaf(n_lane * d, d, r.y));
+    }
+    const float rstd = rsqrtf(sq * inv + a.eps);
+    if (live) {
+      if (t == 0) {
+        if (a.mean != nullptr) a.mean[row] = mean;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+      }
+      const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const Oct w = weight.get(c, k), b = bias.get(c, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[k].p[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[k].p[i], m2), r2), w.p[i], b.p[i]);
+        store_chunk<YT, VEC>(y, c, k, v[k]);
+      }
+    }
+    y += y_step;
+  }
+}
+
+template <typename XT, typename YT>
+__global__ void __launch_bounds__(LONG_THREADS) layernorm_forward_long_kernel(const ForwardArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  __shared__ float red[2][32];
+  int turn = 0;
+  const float inv = 1.f / static_cast<float>(a.D);
+  for (long long row = blockIdx.x; row < a.N; row += gridDim.x) {
+    const XT *x = static_cast<const XT *>(a.x) + row * a.ldx;
+    YT *y = static_cast<YT *>(a.y) + row * a.ldy;
+    float s = 0.f;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < a.D; c += LONG_THREADS) s += load1(x, c);
+    const float mean = block_sum(s, red, turn) * inv;
+    float q = 0.f;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < a.D; c += LONG_THREADS) {
+      const float d = load1(x, c) - mean;
+      q = fmaf(d, d, q);
+    }
+    const float rstd = 1.f / sqrtf(block_sum(q, red, turn) * inv + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+#pragma unroll 4
+    for (int c = threadIdx.x; c < a.D; c += LONG_THREADS)
+      store1(y, c, fmaf((load1(x, c) - mean) * rstd, param_at(a.w, a.wdt, c, 1.f), param_at(a.b, a.wdt, c, 0.f)));
+  }
+}
+
+// ------------------------------------------------------------------------------------------ host
+
+template <typename XT, typename YT, int C, int W, int R, bool VEC>
+cudaError_t forward_launch(const ForwardArgs &a, cudaStream_t s) {
+  using F = Forward<XT, YT, C, W, R, VEC>;
+  auto kernel = layernorm_forward_kernel<XT, YT, C, W, R, VEC>;
+  static const cudaError_t allowed = allow_shared(kernel);
+  if (allowed != cudaSuccess) return allowed;
+  const long long resident = std::max<long long>(1, std::min<long long>(F::BLOCKS, SM_SHARED / (F::BYTES + 2048)));
+  const dim3 grid(static_cast<unsigned>(std::min((a.N + R - 1) / R, device_sm_count() * resident)));
+  return launch_pdl(kernel, grid, dim3(F::THREADS), F::BYTES, s, a);
+}
+
+// One chunk of eight columns per thread and several rows in a block up to 1024 columns; four chunks above, so that the
+// shuffles and the exchange of a row are shared by more columns (two without the vector path, whose rows wait in
+// registers).
+template <typename XT, typename YT>
+cudaError_t forward_route(const ForwardArgs &a, bool vec, cudaStream_t s) {
+  if (a.D > MAX_ROW) {
+    const dim3 grid(static_cast<unsigned>(std::min<long long>(a.N, device_sm_count() * 2))), block(LONG_THREADS);
+    return launch_pdl(layernorm_forward_long_kernel<XT, YT>, grid, block, 0, s, a);
+  }
+  if (a.D <= 1024) {
+    switch (warps_of(a.D, 1)) {
+      case 1: return vec ? forward_launch<XT, YT, 1, 1, 8, true>(a, s) : forward_launch<XT, YT, 1, 1, 8, false>(a, s);
+      case 2: return vec ? forward_launch<XT, YT, 1, 2, 4, true>(a, s) : forward_launch<XT, YT, 1, 2, 4, false>(a, s);
+      case 3: return vec ? forward_launch<XT, YT, 1, 3, 2, true>(a, s) : forward_launch<XT, YT, 1, 3, 2, false>(a, s);
+      default: return vec ? forward_launch<XT, YT, 1, 4, 2, true>(a, s) : forward_launch<XT, YT, 1, 4, 2, false>(a, s);
+    }
+  }
+  if (vec) {
+    switch (warps_of(a.D, 4)) {
+      case 2: return forward_launch<XT, YT, 4, 2, 1, true>(a, s);
+      case 3: return forward_launch<XT, YT, 4, 3, 1, true>(a, s);
+      case 4: return forward_launch<XT, YT, 4, 4, 1, true>(a, s);
+      case 6: return forward_launch<XT, YT, 4, 6, 1, true>(a, s);
+      case 8: return forward_launch<XT, YT, 4, 8, 1, true>(a, s);
+      case 12: return forward_launch<XT, YT, 4, 12, 1, true>(a, s);
+      default: return forward_launch<XT, YT, 4, 16, 1, true>(a, s);
+    }
+  }
+  switch (warps_of(a.D, 2)) {
+    case 3:
+    case 4: return forward_launch<XT, YT, 2, 4, 1, false>(a, s);
+    case 6:
+    case 8: return forward_launch<XT, YT, 2, 8, 1, false>(a, s);
+    case 12:
+    case 16: return forward_launch<XT, YT, 2, 16, 1, false>(a, s);
+    default: return forward_launch<XT, YT, 2, 32, 1, false>(a, s);
+  }
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status layernorm_forward(const void *x, muon_dtype xdt, int64_t ldx, const void *weight, const void *bias,
+                              muon_dtype wdt, void *y, muon_dtype ydt, int64_t ldy, float *mean, float *rstd, int64_t N,
+                              int64_t D, float eps, muon_stream_t stream) {
+  if (N > 0 && (x == nullptr || y == nullptr)) return MUON_ERR_INVALID_ARG;
+  muon_status st = check_dims(N, D);
+  if (st != MUON_OK) return st;
+  if (ldx < D || ldy < D || !std::isfinite(eps) || eps < 0.f) return MUON_ERR_INVALID_ARG;
+  if (!dtype_ok(xdt) || !dtype_ok(ydt) || !dtype_ok(wdt)) return MUON_ERR_DTYPE;
+  if (!natural(x, xdt) || !natural(y, ydt) || !natural(weight, wdt) || !natural(bias, wdt) ||
+      !natural(mean, MUON_F32) || !natural(rstd, MUON_F32))
+    return MUON_ERR_ALIGNMENT;
+  if ((st = device_check()) != MUON_OK) return st;
+  if (N == 0) return MUON_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const ForwardArgs a{x, weight, bias, y, ldx, ldy, N, mean, rstd, eps, wdt, static_cast<int>(D)};
+  const bool vec = aligned16(x) && aligned16(y) && aligned16(weight) && aligned16(bias) && ldx % 8 == 0 && ldy % 8 == 0 &&
+                   D % 8 == 0;
+  launch_begin(KK_LN_FWD, s);
+  cudaError_t e;
+  if (xdt == MUON_F32)
+    e = ydt == MUON_F32 ? forward_route<float, float>(a, vec, s) : forward_route<float, __nv_bfloat16>(a, vec, s);
+  else
+    e = ydt == MUON_F32 ? forward_route<__nv_bfloat16, float>(a, vec, s)
+                        : forward_route<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
+  launch_end(s);
+  return status_of(e);
+}
+
+}  // extern "C"
