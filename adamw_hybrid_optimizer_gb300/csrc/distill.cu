@@ -116,13 +116,10 @@ __device__ __forceinline__ Oct grad_of(Oct o, float m, float c, float si) {
 
 // Granules of one row. VEC: granule g holds logits 8 g - shift + e, where shift is the row's start past a boundary
 // (the same for z and dz, whose pitches differ by a multiple of eight); otherwise shift is 0 and every access is
-// of one element. All granules but the first and the last are whole.
+// of one element. All granules but the first and the last (the edges) are whole.
 struct Granules {
   int shift, count, V;
   __device__ __forceinline__ int first(int g) const { return 8 * g - shift; }
-  __device__ __forceinline__ bool inner(int g) const {
-    return static_cast<unsigned>(g - 1) < static_cast<unsigned>(max(count - 2, 0));
-  }
   __device__ __forceinline__ bool has(int g, int e) const {
     return first(g) + e >= 0 && first(g) + e < V;
   }
@@ -135,6 +132,26 @@ __device__ __forceinline__ Granules granules(long long row, long long ld, int V)
   return {shift, (V + shift + 7) / 8, V};
 }
 
+// The part of a row that block `rank` of `slices` has: granules [g0, g1), of which [inner, inner + n) are not edges.
+// Inner granule inner + i belongs to thread i mod THREADS; the row's first edge to thread HEAD and its last to thread
+// TAIL, of two warps.
+struct Slice {
+  int g0, g1, inner, n;
+  bool head, tail;
+};
+constexpr int HEAD = 0, TAIL = 32;
+
+__device__ __forceinline__ Slice slice_of(const Granules &G, int rank, int slices) {
+  Slice s;
+  s.g0 = static_cast<int>(static_cast<long long>(G.count) * rank / slices);
+  s.g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices);
+  s.inner = max(s.g0, 1);
+  s.n = max(min(s.g1, G.count - 1) - s.inner, 0);
+  s.head = s.g0 == 0 && s.g1 > 0;
+  s.tail = s.g1 == G.count && s.g1 > s.g0 && G.count > 1;
+  return s;
+}
+
 template <typename T>
 __device__ __forceinline__ T neg_inf();
 template <>
@@ -145,7 +162,7 @@ __device__ __forceinline__ __nv_bfloat16 neg_inf<__nv_bfloat16>() { return __ush
 // Places that the row does not have read as -inf.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_granule(const T *p, const Granules &G, int g, Raw8<T> &r) {
-  if (VEC && (G.inner(g) || G.whole(g))) {
+  if (VEC && G.whole(g)) {
     r.load(p + G.first(g));
     return;
   }
@@ -160,7 +177,7 @@ __device__ __forceinline__ void load_granule(const T *p, const Granules &G, int 
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, const Oct &o) {
-  if (VEC && (G.inner(g) || G.whole(g))) {
+  if (VEC && G.whole(g)) {
     store_oct(p + G.first(g), o);
     return;
   }
@@ -171,47 +188,58 @@ __device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, co
 }
 
 template <typename DT, bool VEC>
-__device__ __forceinline__ void zero_granules(DT *dz, const Granules &G, int g0, int g1) {
+__device__ __forceinline__ void zero_granules(DT *dz, const Granules &G, const Slice &S) {
   Oct o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.p[i] = make_float2(0.f, 0.f);
-  for (int g = g0 + threadIdx.x; g < g1; g += THREADS) store_granule<DT, VEC>(dz, G, g, o);
+  for (int g = S.g0 + threadIdx.x; g < S.g1; g += THREADS) store_granule<DT, VEC>(dz, G, g, o);
 }
 
-// A thread's granules g0 + threadIdx.x, + THREADS, ... below g1, in batches: while one is used the loads of the next
-// are in flight.
+// A thread's granules of a slice, in batches: while one is used the loads of the next are in flight. run calls
+// inner(i, values) and edge(g, values).
 template <typename ZT, bool VEC>
 struct Stream {
   static constexpr int U = sizeof(ZT) == 2 ? 4 : 2;
   const ZT *z;
+  const ZT *next;   // of the thread's next batch to fetch
   const Granules &G;
-  int g, g1;
-  Raw8<ZT> a[U], b[U];
-  __device__ __forceinline__ void fetch(Raw8<ZT> *r, int at) const {
+  const Slice &S;
+  int fetched, used;
+  Raw8<ZT> a[U], b[U], e;
+  __device__ __forceinline__ void fetch(Raw8<ZT> *r) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (at + u * THREADS < g1) load_granule<ZT, VEC>(z, G, at + u * THREADS, r[u]);
+      if (fetched + u * THREADS < S.n) {
+        if constexpr (VEC) r[u].load(next + u * THREADS * 8);
+        else load_granule<ZT, false>(z, G, S.inner + fetched + u * THREADS, r[u]);
+      }
+    fetched += U * THREADS;
+    next += U * THREADS * 8;
   }
-  __device__ __forceinline__ Stream(const ZT *z_, const Granules &G_, int g0, int g1_)
-      : z(z_), G(G_), g(g0 + static_cast<int>(threadIdx.x)), g1(g1_) {
-    fetch(a, g);
+  __device__ __forceinline__ Stream(const ZT *z_, const Granules &G_, const Slice &S_)
+      : z(z_), next(z_ + G_.first(S_.inner) + 8 * threadIdx.x), G(G_), S(S_), fetched(threadIdx.x), used(threadIdx.x) {
+    if (S.head && threadIdx.x == HEAD) load_granule<ZT, false>(z, G, 0, e);
+    if (S.tail && threadIdx.x == TAIL) load_granule<ZT, false>(z, G, G.count - 1, e);
+    fetch(a);
   }
   template <typename F>
-  __device__ __forceinline__ void use(const Raw8<ZT> *r, F &&f) {
+  __device__ __forceinline__ void use(const Raw8<ZT> *r, F &&inner) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (g + u * THREADS < g1) f(g + u * THREADS, r[u].get());
-    g += U * THREADS;
+      if (used + u * THREADS < S.n) inner(used + u * THREADS, r[u].get());
+    used += U * THREADS;
   }
-  template <typename F>
-  __device__ __forceinline__ void run(F &&f) {
-    while (g < g1) {
-      fetch(b, g + U * THREADS);
-      use(a, f);
-      if (g >= g1) break;
-      fetch(a, g + U * THREADS);
-      use(b, f);
+  template <typename F, typename E>
+  __device__ __forceinline__ void run(F &&inner, E &&edge) {
+    while (used < S.n) {
+      fetch(b);
+      use(a, inner);
+      if (used >= S.n) break;
+      fetch(a);
+      use(b, inner);
     }
+    if (S.head && threadIdx.x == HEAD) edge(0, e.get());
+    if (S.tail && threadIdx.x == TAIL) edge(G.count - 1, e.get());
   }
 };
 
@@ -389,6 +417,19 @@ __device__ __forceinline__ float weight_of(const DistillArgs &a, long long row) 
   return a.weights != nullptr ? a.weights[row] : 1.f;
 }
 
+// dz of a slice without the q part: si * exp((z - m) / T).
+template <typename ZT, typename DT, bool VEC>
+__device__ __forceinline__ void write_grad(Stream<ZT, VEC> &stream, DT *dz, const Granules &G, const Slice &S, float m,
+                                           float c, float si) {
+  DT *inner = dz + G.first(S.inner);
+  stream.run(
+      [&](int i, const Oct &o) {
+        if constexpr (VEC) store_oct(inner + 8 * i, grad_of(o, m, c, si));
+        else store_granule<DT, false>(dz, G, S.inner + i, grad_of(o, m, c, si));
+      },
+      [&](int g, const Oct &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
+}
+
 template <typename ZT, bool VEC>
 __global__ void __launch_bounds__(THREADS, 2) distill_forward_kernel(const DistillArgs a) {
   pdl_wait();
@@ -402,8 +443,7 @@ __global__ void __launch_bounds__(THREADS, 2) distill_forward_kernel(const Disti
   const long long row = blockIdx.x / slices;
   const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
   const Granules G = granules<VEC>(row, a.ldz, a.V);
-  const int g0 = static_cast<int>(static_cast<long long>(G.count) * rank / slices);
-  const int g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices);
+  const Slice S = slice_of(G, rank, slices);
   const bool entry = rank == 0 && static_cast<int>(threadIdx.x) < a.K;
   const float w = weight_of(a, row);
   Entry e{};
@@ -412,10 +452,11 @@ __global__ void __launch_bounds__(THREADS, 2) distill_forward_kernel(const Disti
     if (rank == 0 && threadIdx.x == 0) store_nothing(a, row);
     return;
   }
-  Stream<ZT, VEC> stream(z, G, g0, g1);
+  Stream<ZT, VEC> stream(z, G, S);
   if (entry) e.z = entry_logit<ZT, true>(e, z, 0, 0);
   Run run;
-  stream.run([&](int, const Oct &o) { run.add(o, c); });
+  auto add = [&](int, const Oct &o) { run.add(o, c); };
+  stream.run(add, add);
   Soft student = run.soft(), teacher{-INFINITY, 0.f};
   if (rank == 0) teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
   merge_all(red, 0, c, student, teacher);
@@ -446,27 +487,26 @@ __global__ void __launch_bounds__(THREADS, 2) distill_backward_kernel(const Dist
   const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
   DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
   const Granules G = granules<VEC>(row, a.ldz, a.V);
-  const int g0 = static_cast<int>(static_cast<long long>(G.count) * rank / a.slices);
-  const int g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / a.slices);
-  const int lo = max(G.first(g0), 0), hi = min(G.first(g1), a.V);
+  const Slice S = slice_of(G, rank, a.slices);
+  const int lo = max(G.first(S.g0), 0), hi = min(G.first(S.g1), a.V);
   const float w = weight_of(a, row);
   Entry e{};
   if (static_cast<int>(threadIdx.x) < a.K) e = load_entry(a, row, threadIdx.x);
   if (w == 0.f) {
-    zero_granules<DT, VEC>(dz, G, g0, g1);
+    zero_granules<DT, VEC>(dz, G, S);
     return;
   }
-  Stream<ZT, VEC> stream(z, G, g0, g1);
+  Stream<ZT, VEC> stream(z, G, S);
   const float m = a.stats[2 * row], l = a.stats[2 * row + 1], up = a.grad != nullptr ? a.grad[row] : 1.f;
   if (static_cast<int>(threadIdx.x) < a.K) e.z = entry_logit<ZT, false>(e, z, lo, hi);
   Soft teacher = put_teacher<ZT, false>(a, row, z, s, lo, hi, c, e), student{-INFINITY, 0.f};
   merge_all(red, 0, c, student, teacher);   // its barrier also ends the reads of z that dz may overwrite
   if (teacher.s == 0.f) {
-    zero_granules<DT, VEC>(dz, G, g0, g1);
+    zero_granules<DT, VEC>(dz, G, S);
     return;
   }
   const float inv = expf(-l), scale = up * w * a.temp;
-  stream.run([&](int g, const Oct &o) { store_granule<DT, VEC>(dz, G, g, grad_of(o, m, c, scale * inv)); });
+  write_grad<ZT, DT, VEC>(stream, dz, G, S, m, c, scale * inv);
   __syncthreads();
   subtract_teacher(a, s, dz, lo, hi, c, m, inv, scale, teacher);
 }
@@ -484,33 +524,35 @@ __global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const Distil
   const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
   DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
   const Granules G = granules<VEC>(row, a.ldz, a.V);
+  const Slice S = slice_of(G, 0, 1);
   const float w = weight_of(a, row);
   Entry e{};
   if (static_cast<int>(threadIdx.x) < a.K) e = load_entry(a, row, threadIdx.x);
   if (w == 0.f) {
     if (threadIdx.x == 0) store_nothing(a, row);
-    zero_granules<DT, VEC>(dz, G, 0, G.count);
+    zero_granules<DT, VEC>(dz, G, S);
     return;
   }
   if (static_cast<int>(threadIdx.x) < a.K) e.z = entry_logit<ZT, true>(e, z, 0, 0);
   Run run;
   {
-    Stream<ZT, VEC> stream(z, G, 0, G.count);
-    stream.run([&](int, const Oct &o) { run.add(o, c); });
+    Stream<ZT, VEC> stream(z, G, S);
+    auto add = [&](int, const Oct &o) { run.add(o, c); };
+    stream.run(add, add);
   }
   Soft student = run.soft(), teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
   merge_all(red, 0, c, student, teacher);
   if (teacher.s == 0.f) {
     if (threadIdx.x == 0) store_nothing(a, row);
-    zero_granules<DT, VEC>(dz, G, 0, G.count);
+    zero_granules<DT, VEC>(dz, G, S);
     return;
   }
   no_softmax(student);
   const float part = loss_part(a, s, teacher, student.m, c);
   if (threadIdx.x % 32 == 0) red.loss[0][threadIdx.x / 32] = part;
   const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s;
-  Stream<ZT, VEC> stream(z, G, 0, G.count);
-  stream.run([&](int g, const Oct &o) { store_granule<DT, VEC>(dz, G, g, grad_of(o, student.m, c, scale * inv)); });
+  Stream<ZT, VEC> stream(z, G, S);
+  write_grad<ZT, DT, VEC>(stream, dz, G, S, student.m, c, scale * inv);
   __syncthreads();
   if (threadIdx.x == 0) store_loss(a, row, w, red.loss[0], student);
   subtract_teacher(a, s, dz, 0, a.V, c, student.m, inv, scale, teacher);
@@ -518,22 +560,33 @@ __global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const Distil
 
 // ------------------------------------------------------------------------------------------ joint form
 
-// Granule `at` of the slice in shared memory, in 16-byte pieces `room` apart, so that a warp's accesses to one piece
-// are contiguous. Every place is written and read by one thread only, so a thread's own wait is all the ordering it
-// needs.
+// The slice in shared memory: inner granule i at place i, the row's first edge at place room - 2 and its last at
+// room - 1, in 16-byte pieces `room` apart, so that a warp's accesses to one piece are contiguous. Every place is
+// written and read by one thread only, so a thread's own wait is all the ordering it needs.
 template <typename ZT>
 struct Kept {
   static constexpr int PIECES = Raw8<ZT>::PIECES;
   uint4 *base;
-  int room;   // granules
-  // z: row `row` of N. A granule that the row has only part of is copied whole where the rest of it lies in the rows
-  // around (V >= 8), whose values get() leaves out; only the ends of the whole matrix are read element by element.
-  __device__ __forceinline__ void fetch(const ZT *z, const Granules &G, int g, int at, bool first_row,
-                                        bool last_row) const {
-    if (G.inner(g) || ((G.first(g) >= 0 || !first_row) && (G.first(g) + 8 <= G.V || !last_row))) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(z + G.first(g));
+  int room;
+  __device__ __forceinline__ void fetch(int at, const ZT *src) const {
 #pragma unroll
-      for (int p = 0; p < PIECES; ++p) copy_async16(base + p * room + at, src + p);
+    for (int p = 0; p < PIECES; ++p) copy_async16(base + p * room + at, reinterpret_cast<const uint4 *>(src) + p);
+  }
+  __device__ __forceinline__ Oct get(int at) const {
+    Raw8<ZT> r;
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) r.w[p] = base[p * room + at];
+    return r.get();
+  }
+  // An edge that the row has only part of is copied whole where the rest of it lies in the rows around (V >= 8), whose
+  // values edge() leaves out; only the ends of the whole matrix are read element by element.
+  __device__ __forceinline__ void fetch_edges(const ZT *z, const Granules &G, const Slice &S, bool first_row,
+                                              bool last_row) const {
+    const bool head = S.head && threadIdx.x == HEAD;
+    if (!head && !(S.tail && threadIdx.x == TAIL)) return;
+    const int g = head ? 0 : G.count - 1, at = room - (head ? 2 : 1);
+    if ((G.first(g) >= 0 || !first_row) && (G.first(g) + 8 <= G.V || !last_row)) {
+      fetch(at, z + G.first(g));
     } else {
       Raw8<ZT> r;
       load_granule<ZT, false>(z, G, g, r);
@@ -541,19 +594,19 @@ struct Kept {
       for (int p = 0; p < PIECES; ++p) base[p * room + at] = r.w[p];
     }
   }
-  __device__ __forceinline__ Oct get(const Granules &G, int g, int at) const {
-    Raw8<ZT> r;
+  // f(g, values) of the edges that are the thread's
+  template <typename F>
+  __device__ __forceinline__ void edges(const Granules &G, const Slice &S, F &&f) const {
+    const bool head = S.head && threadIdx.x == HEAD;
+    if (!head && !(S.tail && threadIdx.x == TAIL)) return;
+    const int g = head ? 0 : G.count - 1;
+    Oct o = get(room - (head ? 2 : 1));
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p) r.w[p] = base[p * room + at];
-    Oct o = r.get();
-    if (!G.inner(g)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!G.has(g, 2 * i)) o.p[i].x = -INFINITY;
-        if (!G.has(g, 2 * i + 1)) o.p[i].y = -INFINITY;
-      }
+    for (int i = 0; i < 4; ++i) {
+      if (!G.has(g, 2 * i)) o.p[i].x = -INFINITY;
+      if (!G.has(g, 2 * i + 1)) o.p[i].y = -INFINITY;
     }
-    return o;
+    f(g, o);
   }
 };
 
@@ -572,25 +625,24 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
   long long row = blockIdx.x / slices;
   int turn = 0;
   const bool entry = static_cast<int>(threadIdx.x) < a.K;
+  const int t = threadIdx.x;
   auto z_of = [&](long long r) { return static_cast<const ZT *>(a.z) + r * a.ldz; };
-  auto from = [&](const Granules &G) { return static_cast<int>(static_cast<long long>(G.count) * rank / slices); };
-  auto to = [&](const Granules &G) { return static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices); };
   float w_next = weight_of(a, row);   // the grid has no more clusters than there are rows
   Entry e_next{};
-  if (entry) e_next = load_entry(a, row, threadIdx.x);
+  if (entry) e_next = load_entry(a, row, t);
+  Granules G_next = granules<true>(row, a.ldz, a.V);
+  Slice S_next = slice_of(G_next, rank, slices);
   if (w_next != 0.f) {
-    const Granules G = granules<true>(row, a.ldz, a.V);
-    const int g0 = from(G), n = to(G) - g0;
-    for (int at = threadIdx.x; at < n; at += THREADS)
-      kept.fetch(z_of(row), G, g0 + at, at, row == 0, row + 1 == a.N);
+    const ZT *src = z_of(row) + G_next.first(S_next.inner) + 8 * t;
+    for (int i = t; i < S_next.n; i += THREADS, src += 8 * THREADS) kept.fetch(i, src);
+    kept.fetch_edges(z_of(row), G_next, S_next, row == 0, row + 1 == a.N);
   }
   copy_async_commit();
   if (entry) e_next.z = entry_logit<ZT, true>(e_next, z_of(row), 0, 0);
   for (; row < a.N; row += step) {
     DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
-    const Granules G = granules<true>(row, a.ldz, a.V);
-    const int g0 = from(G), n = to(G) - g0;
-    const int lo = max(G.first(g0), 0), hi = min(G.first(g0 + n), a.V);
+    const Granules G = G_next;
+    const Slice S = S_next;
     const float w = w_next;
     const Entry e = e_next;
     // the next row: its weight and entries now, its logits and the entries' own as this one's gradient is written
@@ -598,10 +650,10 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
     const bool more = next < a.N;
     if (more) {
       w_next = weight_of(a, next);
-      if (entry) e_next = load_entry(a, next, threadIdx.x);
+      if (entry) e_next = load_entry(a, next, t);
     }
-    const Granules Gn = granules<true>(next, a.ldz, a.V);
-    const int n0 = from(Gn);
+    G_next = granules<true>(next, a.ldz, a.V);
+    S_next = slice_of(G_next, rank, slices);
     const ZT *zn = z_of(next);
     const bool used = w != 0.f;   // the same for the whole cluster
     const Teacher s = teacher_at(entries + turn * teacher_bytes(a.K), a.K);
@@ -609,18 +661,23 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
     if (used) {
       Run run;
       copy_async_wait<0>();
-      for (int at = threadIdx.x; at < n; at += THREADS) run.add(kept.get(G, g0 + at, at), c);
+#pragma unroll 2
+      for (int i = t; i < S.n; i += THREADS) run.add(kept.get(i), c);
+      kept.edges(G, S, [&](int, const Oct &o) { run.add(o, c); });
       student = run.soft();
       teacher = put_teacher<ZT, true>(a, row, z_of(row), s, 0, 0, c, e);
       merge_all(red, turn, c, student, teacher);
       if (slices > 1) merge_cluster(&put[turn], slices, c, student);
     }
-    const int nn = more && w_next != 0.f ? to(Gn) - n0 : 0;
+    const bool wanted = more && w_next != 0.f;
+    const int nn = wanted ? S_next.n : 0;
+    const ZT *src = zn + G_next.first(S_next.inner) + 8 * t;
     if (more && entry) e_next.z = entry_logit<ZT, true>(e_next, zn, 0, 0);
     if (!used || teacher.s == 0.f) {
-      if (rank == 0 && threadIdx.x == 0) store_nothing(a, row);
-      zero_granules<DT, true>(dz, G, g0, g0 + n);
-      for (int at = threadIdx.x; at < nn; at += THREADS) kept.fetch(zn, Gn, n0 + at, at, false, next + 1 == a.N);
+      if (rank == 0 && t == 0) store_nothing(a, row);
+      zero_granules<DT, true>(dz, G, S);
+      for (int i = t; i < nn; i += THREADS, src += 8 * THREADS) kept.fetch(i, src);
+      if (wanted) kept.fetch_edges(zn, G_next, S_next, false, next + 1 == a.N);
       copy_async_commit();
       if (used) turn ^= 1;
       continue;
@@ -628,19 +685,26 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
     no_softmax(student);
     if (rank == 0) {
       const float part = loss_part(a, s, teacher, student.m, c);
-      if (threadIdx.x % 32 == 0) red.loss[turn][threadIdx.x / 32] = part;
+      if (t % 32 == 0) red.loss[turn][t / 32] = part;
     }
-    const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s, si = scale * inv;
-    for (int at = threadIdx.x; at < max(n, nn); at += THREADS) {
-      if (at < n) store_granule<DT, true>(dz, G, g0 + at, grad_of(kept.get(G, g0 + at, at), student.m, c, si));
-      // the granule's values have gone into the store: its place may take the next row's
-      if (at < nn) kept.fetch(zn, Gn, n0 + at, at, false, next + 1 == a.N);
+    const float m = student.m, scale = a.grad_scale * w * a.temp, inv = 1.f / student.s, si = scale * inv;
+    // a granule's values have gone into the store when its place is given to the next row's
+    kept.edges(G, S, [&](int g, const Oct &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
+    if (wanted) kept.fetch_edges(zn, G_next, S_next, false, next + 1 == a.N);
+    DT *dst = dz + G.first(S.inner) + 8 * t;
+    int i = t;
+#pragma unroll 2
+    for (; i < min(S.n, nn); i += THREADS, src += 8 * THREADS, dst += 8 * THREADS) {
+      store_oct(dst, grad_of(kept.get(i), m, c, si));
+      kept.fetch(i, src);
     }
+    for (int j = i; j < S.n; j += THREADS, dst += 8 * THREADS) store_oct(dst, grad_of(kept.get(j), m, c, si));
+    for (; i < nn; i += THREADS, src += 8 * THREADS) kept.fetch(i, src);
     copy_async_commit();
-    // what follows may run beside the next row: it has its own half of everything shared
+    // what follows may run beside the next row, which has its own half of everything shared
     __syncthreads();
-    if (rank == 0 && threadIdx.x == 0) store_loss(a, row, w, red.loss[turn], student);
-    subtract_teacher(a, s, dz, lo, hi, c, student.m, inv, scale, teacher);
+    if (rank == 0 && t == 0) store_loss(a, row, w, red.loss[turn], student);
+    subtract_teacher(a, s, dz, max(G.first(S.g0), 0), min(G.first(S.g1), a.V), c, m, inv, scale, teacher);
     turn ^= 1;
   }
   if (slices > 1) cluster_sync();   // no block leaves while another reads its shared memory
@@ -783,8 +847,9 @@ cudaError_t launch_step(DistillArgs a, bool vec, cudaStream_t s) {
   const size_t granule = 8 * sizeof(ZT), granules = (static_cast<size_t>(a.V) + 7 + 7) / 8;
   const size_t half = (SM_SHARED / 2 - BLOCK_SHARED - both) / granule, all = (SM_SHARED - BLOCK_SHARED - both) / granule;
   int slices = row_slices(a, 2, 4096, MAX_CLUSTER);
-  while (slices < MAX_CLUSTER && (granules + slices - 1) / slices + 1 > half) ++slices;
-  const size_t room = (granules + slices - 1) / slices + 1;
+  // a slice's granules and two places for edges
+  while (slices < MAX_CLUSTER && (granules + slices - 1) / slices + 2 > half) ++slices;
+  const size_t room = (granules + slices - 1) / slices + 2;
   if (!vec || room > all || a.V < 8) {
     const dim3 grid(static_cast<unsigned>(a.N)), block(THREADS);
     return vec ? launch_pdl(distill_reread_kernel<ZT, DT, true>, grid, block, entries, s, a)
