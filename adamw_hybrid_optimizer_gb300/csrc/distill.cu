@@ -90,7 +90,7 @@ struct Run {
   float m = -INFINITY;
   float2 s = {0.f, 0.f};
   // Eight logits; a granule of -inf leaves the sum alone.
-  __device__ __forceinline__ void add(const Oct &o, float c) {
+  __device__ __forceinline__ void add(const Vals<8> &o, float c) {
     const float mx = fmaxf(fmaxf(fmaxf(o.p[0].x, o.p[0].y), fmaxf(o.p[1].x, o.p[1].y)),
                            fmaxf(fmaxf(o.p[2].x, o.p[2].y), fmaxf(o.p[3].x, o.p[3].y)));
     if (mx > m) {
@@ -106,7 +106,7 @@ struct Run {
 };
 
 // si * exp((z - m) / T) of eight logits
-__device__ __forceinline__ Oct grad_of(Oct o, float m, float c, float si) {
+__device__ __forceinline__ Vals<8> grad_of(Vals<8> o, float m, float c, float si) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.p[i] = __fmul2_rn(exp2_scaled(o.p[i], m, c), make_float2(si, si));
   return o;
@@ -161,24 +161,20 @@ __device__ __forceinline__ __nv_bfloat16 neg_inf<__nv_bfloat16>() { return __ush
 
 // Places that the row does not have read as -inf.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_granule(const T *p, const Granules &G, int g, Raw8<T> &r) {
+__device__ __forceinline__ void load_granule(const T *p, const Granules &G, int g, Raw<T, 8> &r) {
   if (VEC && G.whole(g)) {
     r.load(p + G.first(g));
     return;
   }
-  T f[8];
+  r.clear();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    f[e] = neg_inf<T>();
-    if (G.has(g, e)) f[e] = p[G.first(g) + e];
-  }
-  r.set(f);
+  for (int e = 0; e < 8; ++e) r.put(e, G.has(g, e) ? p[G.first(g) + e] : neg_inf<T>());
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, const Oct &o) {
+__device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, const Vals<8> &o) {
   if (VEC && G.whole(g)) {
-    store_oct(p + G.first(g), o);
+    store_vals(p + G.first(g), o);
     return;
   }
   const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
@@ -189,7 +185,7 @@ __device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, co
 
 template <typename DT, bool VEC>
 __device__ __forceinline__ void zero_granules(DT *dz, const Granules &G, const Slice &S) {
-  Oct o;
+  Vals<8> o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.p[i] = make_float2(0.f, 0.f);
   for (int g = S.g0 + threadIdx.x; g < S.g1; g += THREADS) store_granule<DT, VEC>(dz, G, g, o);
@@ -205,8 +201,8 @@ struct Stream {
   const Granules &G;
   const Slice &S;
   int fetched, used;
-  Raw8<ZT> a[U], b[U], e;
-  __device__ __forceinline__ void fetch(Raw8<ZT> *r) {
+  Raw<ZT, 8> a[U], b[U], e;
+  __device__ __forceinline__ void fetch(Raw<ZT, 8> *r) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (fetched + u * THREADS < S.n) {
@@ -223,7 +219,7 @@ struct Stream {
     fetch(a);
   }
   template <typename F>
-  __device__ __forceinline__ void use(const Raw8<ZT> *r, F &&inner) {
+  __device__ __forceinline__ void use(const Raw<ZT, 8> *r, F &&inner) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (used + u * THREADS < S.n) inner(used + u * THREADS, r[u].get());
@@ -423,11 +419,11 @@ __device__ __forceinline__ void write_grad(Stream<ZT, VEC> &stream, DT *dz, cons
                                            float c, float si) {
   DT *inner = dz + G.first(S.inner);
   stream.run(
-      [&](int i, const Oct &o) {
-        if constexpr (VEC) store_oct(inner + 8 * i, grad_of(o, m, c, si));
+      [&](int i, const Vals<8> &o) {
+        if constexpr (VEC) store_vals(inner + 8 * i, grad_of(o, m, c, si));
         else store_granule<DT, false>(dz, G, S.inner + i, grad_of(o, m, c, si));
       },
-      [&](int g, const Oct &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
+      [&](int g, const Vals<8> &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
 }
 
 template <typename ZT, bool VEC>
@@ -455,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 2) distill_forward_kernel(const Disti
   Stream<ZT, VEC> stream(z, G, S);
   if (entry) e.z = entry_logit<ZT, true>(e, z, 0, 0);
   Run run;
-  auto add = [&](int, const Oct &o) { run.add(o, c); };
+  auto add = [&](int, const Vals<8> &o) { run.add(o, c); };
   stream.run(add, add);
   Soft student = run.soft(), teacher{-INFINITY, 0.f};
   if (rank == 0) teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
@@ -537,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const Distil
   Run run;
   {
     Stream<ZT, VEC> stream(z, G, S);
-    auto add = [&](int, const Oct &o) { run.add(o, c); };
+    auto add = [&](int, const Vals<8> &o) { run.add(o, c); };
     stream.run(add, add);
   }
   Soft student = run.soft(), teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
@@ -565,17 +561,20 @@ __global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const Distil
 // written and read by one thread only, so a thread's own wait is all the ordering it needs.
 template <typename ZT>
 struct Kept {
-  static constexpr int PIECES = Raw8<ZT>::PIECES;
+  static constexpr int PIECES = static_cast<int>(sizeof(ZT)) / 2;
   uint4 *base;
   int room;
   __device__ __forceinline__ void fetch(int at, const ZT *src) const {
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p) copy_async16(base + p * room + at, reinterpret_cast<const uint4 *>(src) + p);
+    for (int p = 0; p < PIECES; ++p) copy_async<16>(base + p * room + at, reinterpret_cast<const uint4 *>(src) + p);
   }
-  __device__ __forceinline__ Oct get(int at) const {
-    Raw8<ZT> r;
+  __device__ __forceinline__ Vals<8> get(int at) const {
+    Raw<ZT, 8> r;
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p) r.w[p] = base[p * room + at];
+    for (int p = 0; p < PIECES; ++p) {
+      const uint4 u = base[p * room + at];
+      r.w[4 * p] = u.x, r.w[4 * p + 1] = u.y, r.w[4 * p + 2] = u.z, r.w[4 * p + 3] = u.w;
+    }
     return r.get();
   }
   // An edge that the row has only part of is copied whole where the rest of it lies in the rows around (V >= 8), whose
@@ -588,10 +587,11 @@ struct Kept {
     if ((G.first(g) >= 0 || !first_row) && (G.first(g) + 8 <= G.V || !last_row)) {
       fetch(at, z + G.first(g));
     } else {
-      Raw8<ZT> r;
+      Raw<ZT, 8> r;
       load_granule<ZT, false>(z, G, g, r);
 #pragma unroll
-      for (int p = 0; p < PIECES; ++p) base[p * room + at] = r.w[p];
+      for (int p = 0; p < PIECES; ++p)
+        base[p * room + at] = make_uint4(r.w[4 * p], r.w[4 * p + 1], r.w[4 * p + 2], r.w[4 * p + 3]);
     }
   }
   // f(g, values) of the edges that are the thread's
@@ -600,7 +600,7 @@ struct Kept {
     const bool head = S.head && threadIdx.x == HEAD;
     if (!head && !(S.tail && threadIdx.x == TAIL)) return;
     const int g = head ? 0 : G.count - 1;
-    Oct o = get(room - (head ? 2 : 1));
+    Vals<8> o = get(room - (head ? 2 : 1));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!G.has(g, 2 * i)) o.p[i].x = -INFINITY;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
       copy_async_wait<0>();
 #pragma unroll 2
       for (int i = t; i < S.n; i += THREADS) run.add(kept.get(i), c);
-      kept.edges(G, S, [&](int, const Oct &o) { run.add(o, c); });
+      kept.edges(G, S, [&](int, const Vals<8> &o) { run.add(o, c); });
       student = run.soft();
       teacher = put_teacher<ZT, true>(a, row, z_of(row), s, 0, 0, c, e);
       merge_all(red, turn, c, student, teacher);
@@ -689,16 +689,16 @@ __global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const Distill
     }
     const float m = student.m, scale = a.grad_scale * w * a.temp, inv = 1.f / student.s, si = scale * inv;
     // a granule's values have gone into the store when its place is given to the next row's
-    kept.edges(G, S, [&](int g, const Oct &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
+    kept.edges(G, S, [&](int g, const Vals<8> &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
     if (wanted) kept.fetch_edges(zn, G_next, S_next, false, next + 1 == a.N);
     DT *dst = dz + G.first(S.inner) + 8 * t;
     int i = t;
 #pragma unroll 2
     for (; i < min(S.n, nn); i += THREADS, src += 8 * THREADS, dst += 8 * THREADS) {
-      store_oct(dst, grad_of(kept.get(i), m, c, si));
+      store_vals(dst, grad_of(kept.get(i), m, c, si));
       kept.fetch(i, src);
     }
-    for (int j = i; j < S.n; j += THREADS, dst += 8 * THREADS) store_oct(dst, grad_of(kept.get(j), m, c, si));
+    for (int j = i; j < S.n; j += THREADS, dst += 8 * THREADS) store_vals(dst, grad_of(kept.get(j), m, c, si));
     for (; i < nn; i += THREADS, src += 8 * THREADS) kept.fetch(i, src);
     copy_async_commit();
     // what follows may run beside the next row, which has its own half of everything shared

@@ -7,12 +7,15 @@
 // their positions), and then sums each run of equal ids. No sum goes through an atomic: the same inputs give
 // the same bits.
 //
-//   embedding_forward_kernel  one warp per row of up to 1024 columns: a gather that reads and writes each byte once.
+// Rows that do not all start on 16-byte boundaries (an odd width) still go through whole vectors: a lane's values come
+// out of the two aligned granules around them, and lie where the granules of the row that is written are.
+//
+//   embedding_forward_kernel  a gather that reads and writes each byte once; several rows per warp where they are short.
 //   embedding_zero_kernel     zeroes the gradient (not called when it accumulates).
-//   embedding_cluster_sort_kernel  the sort of up to 65536 ids in one cluster's shared memory, under the zero kernel.
+//   embedding_cluster_sort_kernel  the sort of up to 131072 ids in one cluster's shared memory, under the zero kernel.
 //   radix_*_kernel            one pass of a longer sort: digit counts per tile, their scan, the stable scatter.
-//   embedding_sum_kernel      one warp per 32 sorted positions and 256 columns; rows of dout go to registers eight
-//                             at a time whether or not they belong to one id, since most ids occur once or twice.
+//   embedding_sum_kernel      one warp per 32 sorted positions and 256 columns; the rows to come are in flight whether or
+//                             not they belong to the id being summed, since most ids occur once or twice.
 //   embedding_join_kernel     ids whose run spans a whole group of 32 or more: adds the groups' sums in order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,8 +31,8 @@ namespace muon {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int FWD_COLS = 1024;   // columns per warp of the lookup
-constexpr int fwd_blocks(size_t value) { return value == 2 ? 6 : 4; }   // resident blocks of the lookup
+constexpr int FWD_BLOCKS = 5;    // resident blocks of the lookup
+constexpr int LOG_UNIT = 7, UNIT = 1 << LOG_UNIT;   // granules per warp and turn of the lookup: four per lane
 constexpr int SUM_COLS = 256;    // columns per warp of the gradient's sums: 8 per lane
 constexpr int GROUP = 32;        // sorted positions per warp of the gradient's sums
 constexpr int SORT_TILE = 4096;  // keys per block of a sort pass
@@ -41,52 +44,170 @@ __device__ __forceinline__ long long load_id(const void *ids, int itype, long lo
                            : static_cast<const long long *>(ids)[i];
 }
 
+// ------------------------------------------------------------------------------------------ granules
+
+// A granule is 8 values of bf16 or, where a matrix is fp32, 4: one access of 16 (8 for bf16 beside fp32) bytes.
+template <typename A, typename B>
+constexpr int granule_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
+
+// Values d .. d + GE - 1 of the 2 GE in lo and hi; d < GE is the same for the whole row.
+template <typename T, int GE>
+__device__ __forceinline__ Raw<T, GE> cut(const Raw<T, GE> &lo, const Raw<T, GE> &hi, int d) {
+  constexpr int W = Raw<T, GE>::WORDS;
+  unsigned w[2 * W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = lo.w[i], w[W + i] = hi.w[i];
+  int words = sizeof(T) == 4 ? d : d / 2;
+#pragma unroll
+  for (int by = W / 2; by > 0; by /= 2)
+    if (words & by) {
+#pragma unroll
+      for (int i = 0; i + by < 2 * W; ++i) w[i] = w[i + by];
+    }
+  Raw<T, GE> r;
+#pragma unroll
+  for (int i = 0; i < W; ++i) r.w[i] = sizeof(T) == 2 && (d & 1) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+  return r;
+}
+
+// GE values of a matrix (base aligned, `total` values from its first to its last) from value `at` on: two aligned
+// granules, joined when the values are used.
+template <typename T, int GE>
+struct Window {
+  Raw<T, GE> lo, hi;
+  int d;   // -1: read one by one, into lo
+  __device__ __forceinline__ void load(const T *base, long long at, long long total) {
+    d = static_cast<int>(at & (GE - 1));
+    const long long from = at - d;
+    if (from >= 0 && from + 2 * GE <= total) {
+      lo.load(base + from);
+      hi.load(base + from + GE);
+    } else {
+      d = -1;
+      lo.clear();
+#pragma unroll
+      for (int e = 0; e < GE; ++e)
+        if (at + e >= 0 && at + e < total) lo.put(e, base[at + e]);
+    }
+  }
+  __device__ __forceinline__ Vals<GE> get() const { return (d < 0 ? lo : cut(lo, hi, d)).get(); }
+};
+
+// Values [first, first + GE) of a row that has [0, D).
+template <typename T, int GE>
+__device__ __forceinline__ void store_edge(T *row, int first, int D, const Vals<GE> &o) {
+#pragma unroll
+  for (int e = 0; e < GE; ++e)
+    if (first + e >= 0 && first + e < D) store1(row, first + e, e % 2 ? o.p[e / 2].y : o.p[e / 2].x);
+}
+
 // ------------------------------------------------------------------------------------------ lookup
 
-// Warps take (row, 1024 columns) units in turn. A unit's four 16-byte loads per lane (of bf16) are all in flight before
-// the first is used, and the id of the next unit is loaded under them, so that a unit waits for one latency, not two.
-template <typename TT, typename OT, bool VEC>
-__global__ void __launch_bounds__(THREADS, fwd_blocks(sizeof(TT))) embedding_forward_kernel(
-    const void *ids, int itype, const TT *table, long long ldt, OT *out, long long ldo, long long n, long long V, int D,
-    int tiles, float scale) {
+struct LookupArgs {
+  const void *ids, *table;
+  void *out;
+  long long ldt, ldo, n, V;
+  int itype, D, per_row, tiles, log_rows;   // granules per row (a power of two below UNIT), units per long row, and
+  float scale;                              // log2 of the rows per unit of short ones
+};
+
+// Warps take units in turn: 128 granules of a long row, or of as many short rows as fit, four granules per lane. All
+// loads of a unit are in flight before the first is used, and the ids of the next unit are loaded under them, so that
+// a unit waits for one latency, not two. ALIGNED: every row starts on a granule and has whole ones.
+template <typename TT, typename OT, bool ALIGNED>
+__global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(const LookupArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  constexpr int GE = granule_of<TT, OT>(), U = UNIT / 32;
+  const int lane = threadIdx.x % 32;
+  const long long units = a.tiles > 1 ? a.n * a.tiles : (a.n + (1 << a.log_rows) - 1) >> a.log_rows;
+  const long long warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
+  const TT *table = static_cast<const TT *>(a.table);
+  // row and granule of the lane's granule q of unit u
+  auto row_of = [&](long long u, int q) {
+    return a.tiles > 1 ? u / a.tiles : (u << a.log_rows) + ((q * 32 + lane) >> (LOG_UNIT - a.log_rows));
+  };
+  auto granule = [&](long long u, int q) {
+    return a.tiles > 1 ? static_cast<int>(u % a.tiles) * UNIT + q * 32 + lane : (q * 32 + lane) & (a.per_row - 1);
+  };
+  auto ids_of = [&](long long u, long long *id) {
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const long long r = row_of(u, q);
+      id[q] = u < units && r < a.n ? load_id(a.ids, a.itype, r) : -1;
+    }
+  };
+  long long u = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32, next[U];
+  ids_of(u, next);
+  for (; u < units; u += warps) {
+    long long id[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) id[q] = next[q] < 0 || next[q] >= a.V ? -1 : next[q];
+    if constexpr (ALIGNED) {
+      Raw<TT, GE> r[U];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        r[q].clear();
+        const int c = granule(u, q) * GE;
+        if (id[q] >= 0 && c < a.D) r[q].load(table + id[q] * a.ldt + c);
+      }
+      ids_of(u + warps, next);
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const long long row = row_of(u, q);
+        const int c = granule(u, q) * GE;
+        if (row >= a.n || c >= a.D) continue;
+        Vals<GE> o = r[q].get();
+#pragma unroll
+        for (int i = 0; i < GE / 2; ++i)
+          o.p[i] = id[q] < 0 ? make_float2(0.f, 0.f) : __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
+        store_vals(static_cast<OT *>(a.out) + row * a.ldo + c, o);
+      }
+    } else {
+      Window<TT, GE> r[U];
+      auto first_of = [&](int q) {   // the granules of the row that is written
+        return granule(u, q) * GE - static_cast<int>((row_of(u, q) * a.ldo) & (GE - 1));
+      };
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+        if (id[q] >= 0 && first_of(q) < a.D)
+          r[q].load(table, id[q] * a.ldt + first_of(q), (a.V - 1) * a.ldt + a.D);
+      ids_of(u + warps, next);
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const long long row = row_of(u, q);
+        const int c = first_of(q);
+        if (row >= a.n || c >= a.D) continue;
+        Vals<GE> o;
+#pragma unroll
+        for (int i = 0; i < GE / 2; ++i) o.p[i] = make_float2(0.f, 0.f);
+        if (id[q] >= 0) {
+          o = r[q].get();
+#pragma unroll
+          for (int i = 0; i < GE / 2; ++i) o.p[i] = __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
+        }
+        OT *dst = static_cast<OT *>(a.out) + row * a.ldo;
+        if (c >= 0 && c + GE <= a.D) store_vals(dst + c, o);
+        else store_edge(dst, c, a.D, o);
+      }
+    }
+  }
+}
+
+// Bases that are not 16-byte aligned: value by value.
+template <typename TT, typename OT>
+__global__ void __launch_bounds__(THREADS) embedding_forward_scalar_kernel(const LookupArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const int lane = threadIdx.x % 32;
-  const long long units = n * tiles, warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
-  long long u = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32;
-  long long i = u / tiles, next_id = u < units ? load_id(ids, itype, i) : 0;
-  for (; u < units; u += warps) {
-    const long long id = next_id, row = i;
-    const int c0 = static_cast<int>(u - i * tiles) * FWD_COLS;
-    const bool in = id >= 0 && id < V;
-    const TT *src = table + (in ? id : 0) * ldt;
-    OT *dst = out + row * ldo;
-    i = (u + warps) / tiles;
-    if constexpr (VEC) {
-      Raw8<TT> r[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = c0 + (k * 32 + lane) * 8;
-        if (c < D) r[k].load(src + c);
-      }
-      if (u + warps < units) next_id = load_id(ids, itype, i);
-      const float2 s2 = make_float2(scale, scale);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = c0 + (k * 32 + lane) * 8;
-        Oct o = r[k].get();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o.p[q] = in ? __fmul2_rn(o.p[q], s2) : make_float2(0.f, 0.f);
-        if (c < D) store_oct(dst + c, o);
-      }
-    } else {
-      if (u + warps < units) next_id = load_id(ids, itype, i);
+  const long long warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
+  for (long long i = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32; i < a.n; i += warps) {
+    const long long id = load_id(a.ids, a.itype, i);
+    const bool in = id >= 0 && id < a.V;
+    const TT *src = static_cast<const TT *>(a.table) + (in ? id : 0) * a.ldt;
+    OT *dst = static_cast<OT *>(a.out) + i * a.ldo;
 #pragma unroll 8
-      for (int k = 0; k < FWD_COLS / 32; ++k) {
-        const int c = c0 + k * 32 + lane;
-        if (c < D) store1(dst, c, in ? load1(src, c) * scale : 0.f);
-      }
-    }
+    for (int c = lane; c < a.D; c += 32) store1(dst, c, in ? load1(src, c) * a.scale : 0.f);
   }
 }
 
@@ -208,7 +329,7 @@ __global__ void __launch_bounds__(THREADS) radix_scatter_kernel(const SortPass p
   }
 }
 
-// The whole sort in one cluster, for n <= 8 * 8192: block b holds the sorted positions [b * chunk, (b + 1) * chunk) in
+// The whole sort in one cluster, for n <= 16 * 8192: block b holds the sorted positions [b * chunk, (b + 1) * chunk) in
 // its shared memory, and a pass moves every item to its place in any block's. A thread keeps its items in registers
 // while their places are computed, so one buffer is enough. Warp w of a block has the block's items [w * per, ...), 32
 // at a time; an item's place is its digit's first place, plus the digit's items in earlier blocks, warps, rounds and
@@ -217,7 +338,7 @@ constexpr int CS_THREADS = 512;    // few enough registers to run beside the zer
 constexpr int CS_WARPS = CS_THREADS / 32;
 constexpr int CS_ROUNDS = 16;                              // items per thread
 constexpr int CS_CHUNK = CS_THREADS * CS_ROUNDS;           // items per block
-constexpr int CS_BLOCKS = 8;
+constexpr int CS_BLOCKS = 16;
 
 struct ClusterSort {
   const void *ids;
@@ -350,18 +471,32 @@ __global__ void __launch_bounds__(CS_THREADS, 2) embedding_cluster_sort_kernel(c
 
 // ------------------------------------------------------------------------------------------ sums
 
-template <typename GT>
-__global__ void __launch_bounds__(THREADS) embedding_zero_kernel(GT *g, long long ldg, long long V, int D, int vec) {
+// rows x `bytes` at a pitch, in 16-byte accesses from the first boundary of a row on (one row of everything where the
+// rows leave no gaps).
+__global__ void __launch_bounds__(THREADS) embedding_zero_kernel(unsigned char *g, long long pitch, long long rows,
+                                                                 long long bytes) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const long long tid = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
   const long long stride = static_cast<long long>(gridDim.x) * THREADS;
-  if (vec) {
-    const int per = D / 8;
-    const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (long long u = tid; u < V * per; u += stride) store8(g + u / per * ldg + u % per * 8, z);
-  } else {
-    for (long long u = tid; u < V * D; u += stride) store1(g, u / D * ldg + u % D, 0.f);
+  if (rows == 1) {
+    const long long head = (16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15;
+    const long long lead = head < bytes ? head : bytes, whole = (bytes - lead) / 16;
+    uint4 *q = reinterpret_cast<uint4 *>(g + lead);
+#pragma unroll 4
+    for (long long i = tid; i < whole; i += stride) q[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = tid; i < lead; i += stride) g[i] = 0;
+    for (long long i = lead + whole * 16 + tid; i < bytes; i += stride) g[i] = 0;
+  } else {   // warps take rows
+    const int lane = threadIdx.x % 32;
+    for (long long r = tid / 32; r < rows; r += stride / 32) {
+      unsigned char *p = g + r * pitch;
+      const long long head = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+      const long long lead = head < bytes ? head : bytes, whole = (bytes - lead) / 16;
+      for (long long i = lane; i < whole; i += 32) reinterpret_cast<uint4 *>(p + lead)[i] = make_uint4(0, 0, 0, 0);
+      for (long long i = lane; i < lead; i += 32) p[i] = 0;
+      for (long long i = lead + whole * 16 + lane; i < bytes; i += 32) p[i] = 0;
+    }
   }
 }
 
@@ -378,73 +513,114 @@ struct SumArgs {
   float scale;
 };
 
-// A lane's eight of a row's 256 columns: contiguous on the vector path (which needs a width of whole eights).
-template <bool VEC>
-__device__ __forceinline__ int sum_col(int c0, int lane, int e) {
-  return VEC ? c0 + lane * 8 + e : c0 + e * 32 + lane;
+// How the sums see memory. ALIGNED: every row of dout and dtable starts on a granule and has whole ones. CUT: bases
+// are aligned, rows are not; a lane's columns are those of its granules of the gradient row, `shift` values past a
+// boundary, and dout's values come out of the two granules around them. SCALAR: value by value, columns 32 apart.
+enum Access { SCALAR, ALIGNED, CUT };
+
+// The lane's eight of 256 columns of a tile: PG granules, 32 granules apart (SCALAR: single columns).
+template <int ACCESS, int GE>
+__device__ __forceinline__ int sum_col(int tile, int lane, int e, int shift) {
+  return ACCESS == SCALAR ? tile * SUM_COLS + e * 32 + lane
+                          : (tile * (SUM_COLS / GE) + e / GE * 32 + lane) * GE + e % GE - shift;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_cols(const T *p, int c0, int lane, int D, Raw8<T> &r) {
-  if constexpr (VEC) {
-    if (c0 + lane * 8 < D) r.load(p + c0 + lane * 8);
-  } else {
-    T f[8];
+// Eight values of a row of dout on their way.
+template <typename OT, int GE, int ACCESS>
+struct RowPart {
+  Raw<OT, GE> g[ACCESS == CUT ? 1 : 8 / GE];
+  Window<OT, GE> win[ACCESS == CUT ? 8 / GE : 1];
+  __device__ __forceinline__ void load(const SumArgs &a, unsigned pos, int tile, int lane, int shift) {
+    const OT *base = static_cast<const OT *>(a.dout);
+    const long long at = static_cast<long long>(pos) * a.ldo;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      f[e] = T(0.f);
-      if (sum_col<false>(c0, lane, e) < D) f[e] = p[sum_col<false>(c0, lane, e)];
+    for (int j = 0; j < 8 / GE; ++j) {
+      const int c = sum_col<ACCESS, GE>(tile, lane, j * GE, shift);
+      if constexpr (ACCESS == ALIGNED) {
+        if (c < a.D) g[j].load(base + at + c);
+      } else if constexpr (ACCESS == CUT) {
+        if (c < a.D) win[j].load(base, at + c, (a.n - 1) * a.ldo + a.D);
+      } else {
+        g[j].clear();
+#pragma unroll
+        for (int e = 0; e < GE; ++e) {
+          const int ce = sum_col<SCALAR, GE>(tile, lane, j * GE + e, 0);
+          if (ce < a.D) g[j].put(e, base[at + ce]);
+        }
+      }
     }
-    r.set(f);
   }
+  __device__ __forceinline__ void add_to(Vals<8> &acc) const {
+#pragma unroll
+    for (int j = 0; j < 8 / GE; ++j) {
+      const Vals<GE> v = ACCESS == CUT ? win[ACCESS == CUT ? j : 0].get() : g[ACCESS == CUT ? 0 : j].get();
+#pragma unroll
+      for (int i = 0; i < GE / 2; ++i) acc.p[j * GE / 2 + i] = __fadd2_rn(acc.p[j * GE / 2 + i], v.p[i]);
+    }
+  }
+};
+
+template <int ACCESS, int GE>
+__device__ __forceinline__ int shift_of(const SumArgs &a, unsigned key) {
+  return ACCESS == CUT ? static_cast<int>((static_cast<long long>(key) * a.ldg) & (GE - 1)) : 0;
 }
 
 // The gradient row's columns: scale * acc, added to what is there if asked.
-template <typename GT, bool VEC>
-__device__ __forceinline__ void store_row(GT *p, int c0, int lane, int D, const Oct &acc, float scale,
-                                          int accumulate) {
-  if (VEC && c0 + lane * 8 >= D) return;
-  Oct o;
+template <typename GT, int GE, int ACCESS>
+__device__ __forceinline__ void store_row(const SumArgs &a, unsigned key, int tile, int lane, const Vals<8> &acc) {
+  GT *p = static_cast<GT *>(a.g) + static_cast<long long>(key) * a.ldg;
+  const int shift = shift_of<ACCESS, GE>(a, key);
+  const float2 s2 = make_float2(a.scale, a.scale);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) o.p[q] = make_float2(0.f, 0.f);
-  if (accumulate) {
-    Raw8<GT> r;
-    load_cols<GT, VEC>(p, c0, lane, D, r);
-    o = r.get();
-  }
-  const float2 s2 = make_float2(scale, scale);
+  for (int j = 0; j < 8 / GE; ++j) {
+    const int c = sum_col<ACCESS, GE>(tile, lane, j * GE, shift);
+    Vals<GE> o;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) o.p[q] = __ffma2_rn(acc.p[q], s2, o.p[q]);
-  if constexpr (VEC) {
-    store_oct(p + c0 + lane * 8, o);
-  } else {
-    const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
+    for (int i = 0; i < GE / 2; ++i) o.p[i] = make_float2(0.f, 0.f);
+    if (ACCESS != SCALAR && c >= 0 && c + GE <= a.D) {
+      if (a.accumulate) {
+        Raw<GT, GE> r;
+        r.load(p + c);
+        o = r.get();
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (sum_col<false>(c0, lane, e) < D) store1(p, sum_col<false>(c0, lane, e), f[e]);
+      for (int i = 0; i < GE / 2; ++i) o.p[i] = __ffma2_rn(acc.p[j * GE / 2 + i], s2, o.p[i]);
+      store_vals(p + c, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < GE; ++e) {
+        const int ce = sum_col<ACCESS, GE>(tile, lane, j * GE + e, shift);
+        if (ce < 0 || ce >= a.D) continue;
+        const float2 v = acc.p[(j * GE + e) / 2];
+        store1(p, ce, fmaf(e % 2 ? v.y : v.x, a.scale, a.accumulate ? load1(p, ce) : 0.f));
+      }
+    }
   }
 }
 
-// Partial sums keep the lane's own eight columns together whatever the path: written and read by the same mapping.
-__device__ __forceinline__ void store_part(float *p, int c0, int lane, const Oct &acc) {
-  store_oct(p + c0 + lane * 8, acc);
+// Partial sums keep the lane's own eight columns together: written and read by the same mapping.
+__device__ __forceinline__ void store_part(float *p, int tile, int lane, const Vals<8> &acc) {
+  store_vals(p + tile * SUM_COLS + lane * 8, acc);
 }
 
 // A run of equal ids that starts in group c belongs to it, unless the run covers the whole of the next group and
 // goes on (a long run): then every group sums its own part, into part[2c + 1] where the run starts and part[2c]
 // where it came from the group before, and the join kernel adds the parts. So a warp sums at most 63 positions. While
-// it adds four rows the loads of the next four are in flight, whether or not they belong to one id.
-template <typename OT, typename GT, bool VEC>
-__global__ void __launch_bounds__(THREADS, sizeof(OT) == 2 ? 3 : 2) embedding_sum_kernel(const SumArgs a) {
+// it adds U rows the loads of the next U are in flight, whether or not they belong to one id.
+template <typename OT, typename GT, int ACCESS>
+__global__ void __launch_bounds__(THREADS, 2) embedding_sum_kernel(const SumArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
+  constexpr int GE = granule_of<OT, GT>();
+  constexpr int U = ACCESS == CUT ? 2 : sizeof(OT) == 2 ? 8 : 4;
+  using Part = RowPart<OT, GE, ACCESS>;
   const int lane = threadIdx.x % 32;
   const long long units = static_cast<long long>(a.groups) * a.tiles;
   const long long warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
   const unsigned none = static_cast<unsigned>(a.V);
   for (long long u = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32; u < units; u += warps) {
     const long long c = u / a.tiles;
-    const int tile = static_cast<int>(u - c * a.tiles), c0 = tile * SUM_COLS;
+    const int tile = static_cast<int>(u - c * a.tiles);
     const long long s = c * GROUP;
     auto key_at = [&](long long i) { return i >= 0 && i < a.n ? a.key[i] : NO_KEY; };
     const unsigned k0 = key_at(s + lane), k1 = key_at(s + GROUP + lane);
@@ -469,30 +645,29 @@ __global__ void __launch_bounds__(THREADS, sizeof(OT) == 2 ? 3 : 2) embedding_su
     if (tail_part && tile == 0 && lane == 0) a.list[atomicAdd(a.list_count, 1u)] = static_cast<unsigned>(c);
     if (begin >= end) continue;
 
-    const OT *dout = static_cast<const OT *>(a.dout);
-    GT *g = static_cast<GT *>(a.g);
     auto at = [&](unsigned lo, unsigned hi, int i) {
       return __shfl_sync(0xffffffffu, i < GROUP ? lo : hi, i % GROUP);
     };
-    constexpr int U = 4;
-    Raw8<OT> raw[2][U];
-    auto fetch = [&](int i0, Raw8<OT> *r) {
+    Part raw[2][U];
+    auto fetch = [&](int i0, Part *r) {
 #pragma unroll
       for (int q = 0; q < U; ++q)
-        if (i0 + q < end)
-          load_cols<OT, VEC>(dout + static_cast<long long>(at(p0, p1, i0 + q)) * a.ldo, c0, lane, a.D, r[q]);
+        if (i0 + q < end) {
+          const unsigned pos = at(p0, p1, i0 + q);
+          r[q].load(a, pos, tile, lane, ACCESS == CUT ? shift_of<ACCESS, GE>(a, at(k0, k1, i0 + q)) : 0);
+        }
     };
-    Oct acc;
+    Vals<8> acc;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc.p[q] = make_float2(0.f, 0.f);
+    for (int i = 0; i < 4; ++i) acc.p[i] = make_float2(0.f, 0.f);
     unsigned cur = at(k0, k1, begin);
     auto flush = [&](bool tail) {
-      if (to_lead) store_part(a.part + 2 * c * a.ldp, c0, lane, acc);
-      else if (tail) store_part(a.part + (2 * c + 1) * a.ldp, c0, lane, acc);
-      else store_row<GT, VEC>(g + static_cast<long long>(cur) * a.ldg, c0, lane, a.D, acc, a.scale, a.accumulate);
+      if (to_lead) store_part(a.part + 2 * c * a.ldp, tile, lane, acc);
+      else if (tail) store_part(a.part + (2 * c + 1) * a.ldp, tile, lane, acc);
+      else store_row<GT, GE, ACCESS>(a, cur, tile, lane, acc);
       to_lead = false;
     };
-    auto add = [&](int i0, const Raw8<OT> *r) {
+    auto add = [&](int i0, const Part *r) {
 #pragma unroll
       for (int q = 0; q < U; ++q) {
         if (i0 + q >= end) break;
@@ -503,9 +678,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(OT) == 2 ? 3 : 2) embedding_su
 #pragma unroll
           for (int h = 0; h < 4; ++h) acc.p[h] = make_float2(0.f, 0.f);
         }
-        const Oct o = r[q].get();
-#pragma unroll
-        for (int h = 0; h < 4; ++h) acc.p[h] = __fadd2_rn(acc.p[h], o.p[h]);
+        r[q].add_to(acc);
       }
     };
     fetch(begin, raw[0]);
@@ -521,33 +694,40 @@ __global__ void __launch_bounds__(THREADS, sizeof(OT) == 2 ? 3 : 2) embedding_su
 
 // One block per long run and 256 columns: warp w adds parts w, w + 8, ... of the run, and the warps' sums are added
 // in order.
-template <typename GT, bool VEC>
+template <typename OT, typename GT, int ACCESS>
 __global__ void __launch_bounds__(THREADS) embedding_join_kernel(const SumArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  constexpr int WARPS = THREADS / 32;
+  constexpr int WARPS = THREADS / 32, GE = granule_of<OT, GT>();
   __shared__ float2 red[WARPS][SUM_COLS / 2];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const long long units = static_cast<long long>(*a.list_count) * a.tiles;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const long long c = a.list[u / a.tiles];
-    const int c0 = static_cast<int>(u % a.tiles) * SUM_COLS;
+    const int tile = static_cast<int>(u % a.tiles);
     const unsigned k = a.key[c * GROUP + GROUP - 1];
-    long long lo = c + 2, hi = a.groups;   // the first group after c + 1 whose first key is not k
+    // the first group after c + 1 whose first key is not k: 32 probes at a time
+    long long lo = c + 2, hi = a.groups;   // groups below lo are the run's, hi is not (or the end)
     while (lo < hi) {
-      const long long mid = (lo + hi) / 2;
-      if (a.key[mid * GROUP] == k) lo = mid + 1;
-      else hi = mid;
+      const long long stride = (hi - lo + 31) / 32, probe = lo + lane * stride;
+      const unsigned yes = __ballot_sync(0xffffffffu, probe < hi && a.key[probe * GROUP] == k);
+      const int ok = __popc(yes);   // the run's probes are the first ones
+      if (ok == 0) hi = lo;
+      else {
+        const long long reached = lo + (ok - 1) * stride + 1, limit = lo + ok * stride;
+        hi = ok < 32 && limit < hi ? limit : hi;
+        lo = reached;
+      }
     }
     const long long parts = lo - c;
-    Oct acc;
+    Vals<8> acc;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc.p[q] = make_float2(0.f, 0.f);
+    for (int i = 0; i < 4; ++i) acc.p[i] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (long long i = w; i < parts; i += WARPS) {
-      Raw8<float> r;
-      r.load(a.part + (i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.ldp + c0 + lane * 8);
-      const Oct o = r.get();
+      Raw<float, 8> r;
+      r.load(a.part + (i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.ldp + tile * SUM_COLS + lane * 8);
+      const Vals<8> o = r.get();
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc.p[q] = __fadd2_rn(acc.p[q], o.p[q]);
     }
@@ -559,11 +739,10 @@ __global__ void __launch_bounds__(THREADS) embedding_join_kernel(const SumArgs a
       for (int q = 0; q < 4; ++q) {
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k2 = 0; k2 < WARPS; ++k2) s = __fadd2_rn(s, red[k2][q * 32 + lane]);
+        for (int i = 0; i < WARPS; ++i) s = __fadd2_rn(s, red[i][q * 32 + lane]);
         acc.p[q] = s;
       }
-      store_row<GT, VEC>(static_cast<GT *>(a.g) + static_cast<long long>(k) * a.ldg, c0, lane, a.D, acc, a.scale,
-                         a.accumulate);
+      store_row<GT, GE, ACCESS>(a, k, tile, lane, acc);
     }
     __syncthreads();
   }
@@ -586,7 +765,7 @@ EmbeddingLayout embedding_layout(long long n, long long D) {
   };
   L.groups = (n + GROUP - 1) / GROUP;
   L.tiles = (n + SORT_TILE - 1) / SORT_TILE;
-  L.ldp = (D + SUM_COLS - 1) / SUM_COLS * SUM_COLS;
+  L.ldp = (D + 7 + SUM_COLS - 1) / SUM_COLS * SUM_COLS;   // rows past a boundary reach up to 7 columns further
   L.list = take(4 * (1 + static_cast<size_t>(n) / GROUP));
   for (int k = 0; k < 2; ++k) L.key[k] = take(4 * static_cast<size_t>(n));
   for (int k = 0; k < 2; ++k) L.pos[k] = take(4 * static_cast<size_t>(n));
@@ -621,16 +800,25 @@ muon_status check_embedding(const void *ids, muon_itype itype, const void *table
 muon_status status_of(cudaError_t e) { return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA; }
 
 template <typename TT, typename OT>
-cudaError_t launch_forward(bool vec, dim3 grid, cudaStream_t s, const void *ids, int itype, const void *table,
-                           long long ldt, void *out, long long ldo, long long n, long long V, int D, int tiles,
-                           float scale) {
+cudaError_t launch_lookup(LookupArgs a, cudaStream_t s) {
+  constexpr int GE = granule_of<TT, OT>();
+  const long long sms = device_sm_count();
   const dim3 block(THREADS);
-  const TT *t = static_cast<const TT *>(table);
-  OT *o = static_cast<OT *>(out);
-  return vec ? launch_pdl(embedding_forward_kernel<TT, OT, true>, grid, block, 0, s, ids, itype, t, ldt, o, ldo, n, V,
-                          D, tiles, scale)
-             : launch_pdl(embedding_forward_kernel<TT, OT, false>, grid, block, 0, s, ids, itype, t, ldt, o, ldo, n, V,
-                          D, tiles, scale);
+  if (!aligned16(a.table) || !aligned16(a.out)) {
+    const long long blocks = std::min((a.n + THREADS / 32 - 1) / (THREADS / 32), sms * 8);
+    return launch_pdl(embedding_forward_scalar_kernel<TT, OT>, dim3(static_cast<unsigned>(blocks)), block, 0, s, a);
+  }
+  const bool aligned = a.D % GE == 0 && a.ldt % GE == 0 && a.ldo % GE == 0;
+  const int granules = (a.D + (aligned ? 0 : GE - 1) + GE - 1) / GE;
+  a.per_row = 8;
+  while (a.per_row < granules && a.per_row < UNIT) a.per_row *= 2;
+  a.tiles = (granules + UNIT - 1) / UNIT;
+  a.log_rows = 0;
+  while ((a.per_row << a.log_rows) < UNIT) ++a.log_rows;
+  const long long units = a.tiles > 1 ? a.n * a.tiles : (a.n + (1 << a.log_rows) - 1) >> a.log_rows;
+  const dim3 grid(static_cast<unsigned>(std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * FWD_BLOCKS)));
+  return aligned ? launch_pdl(embedding_forward_kernel<TT, OT, true>, grid, block, 0, s, a)
+                 : launch_pdl(embedding_forward_kernel<TT, OT, false>, grid, block, 0, s, a);
 }
 
 muon_status launch_sort(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
@@ -674,14 +862,16 @@ muon_status launch_sort(const void *ids, int itype, long long n, long long V, lo
   return MUON_OK;
 }
 
-// The sort in one cluster (n <= CS_BLOCKS * CS_CHUNK). Blocks of 4096 items each up to eight of them: a block's rounds
-// cost more than the cluster's barriers.
+// The sort in one cluster (n <= CS_BLOCKS * CS_CHUNK). Blocks of up to 2048 items each while there are eight: a block's
+// rounds cost more than the cluster's barriers.
 muon_status launch_cluster_sort(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
                                 const EmbeddingLayout &L, bool after_zero, const unsigned **key, const unsigned **pos,
                                 cudaStream_t s) {
   static const cudaError_t allowed = cudaFuncSetAttribute(
       embedding_cluster_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(ClusterShared)));
-  if (allowed != cudaSuccess) return MUON_ERR_CUDA;
+  static const cudaError_t wide =   // 16 blocks
+      cudaFuncSetAttribute(embedding_cluster_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (allowed != cudaSuccess || wide != cudaSuccess) return MUON_ERR_CUDA;
   int key_bits = 1;
   while ((V >> key_bits) != 0) ++key_bits;
   ClusterSort a{};
@@ -694,7 +884,8 @@ muon_status launch_cluster_sort(const void *ids, int itype, long long n, long lo
   a.list_count = reinterpret_cast<unsigned *>(ws + L.list);
   a.n = static_cast<int>(n);
   a.blocks = 1;
-  while (a.blocks < CS_BLOCKS && a.blocks * 4096 < n) a.blocks *= 2;
+  while (a.blocks < 8 && a.blocks * 2048 < n) a.blocks *= 2;
+  while (a.blocks < CS_BLOCKS && a.blocks * CS_CHUNK < n) a.blocks *= 2;
   a.chunk = (a.n + a.blocks - 1) / a.blocks;
   a.passes = (key_bits + MAX_DIGIT_BITS - 1) / MAX_DIGIT_BITS;
   a.bits = (key_bits + a.passes - 1) / a.passes;
@@ -721,26 +912,32 @@ muon_status launch_cluster_sort(const void *ids, int itype, long long n, long lo
   return status_of(e);
 }
 
-template <typename OT, typename GT, bool VEC>
-muon_status launch_sums(const SumArgs &a, cudaStream_t s) {
+template <typename OT, typename GT, int ACCESS>
+muon_status launch_sums(SumArgs a, cudaStream_t s) {
+  a.tiles = (a.D + (ACCESS == CUT ? granule_of<OT, GT>() - 1 : 0) + SUM_COLS - 1) / SUM_COLS;
   const long long sms = device_sm_count();
   const long long units = static_cast<long long>(a.groups) * a.tiles;
   const long long blocks = std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * 4096);
   launch_begin(KK_EMBED_SUM, s);
-  muon_status st = status_of(launch_pdl(embedding_sum_kernel<OT, GT, VEC>, dim3(static_cast<unsigned>(blocks)),
+  muon_status st = status_of(launch_pdl(embedding_sum_kernel<OT, GT, ACCESS>, dim3(static_cast<unsigned>(blocks)),
                                         dim3(THREADS), 0, s, a));
   launch_end(s);
   if (st != MUON_OK || a.groups < 3) return st;   // no run can be long
+  // no more long runs than a third of the groups
+  const long long joins = std::min(static_cast<long long>(a.groups / 2 + 1) * a.tiles, sms * 4);
   launch_begin(KK_EMBED_JOIN, s);
-  st = status_of(launch_pdl(embedding_join_kernel<GT, VEC>, dim3(static_cast<unsigned>(sms * 4)), dim3(THREADS), 0, s,
-                            a));
+  st = status_of(launch_pdl(embedding_join_kernel<OT, GT, ACCESS>, dim3(static_cast<unsigned>(joins)), dim3(THREADS), 0,
+                            s, a));
   launch_end(s);
   return st;
 }
 
 template <typename OT, typename GT>
-muon_status launch_sums_vec(bool vec, const SumArgs &a, cudaStream_t s) {
-  return vec ? launch_sums<OT, GT, true>(a, s) : launch_sums<OT, GT, false>(a, s);
+muon_status launch_sums_for(const SumArgs &a, cudaStream_t s) {
+  constexpr int GE = granule_of<OT, GT>();
+  if (!aligned16(a.dout) || !aligned16(a.g)) return launch_sums<OT, GT, SCALAR>(a, s);
+  if (a.D % GE == 0 && a.ldo % GE == 0 && a.ldg % GE == 0) return launch_sums<OT, GT, ALIGNED>(a, s);
+  return launch_sums<OT, GT, CUT>(a, s);
 }
 
 }  // namespace
@@ -758,21 +955,23 @@ muon_status embedding_forward(const void *ids, muon_itype itype, const void *tab
   if ((st = device_check()) != MUON_OK) return st;
   if (n == 0) return MUON_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool vec = aligned16(table) && aligned16(out) && ldt % 8 == 0 && ldo % 8 == 0 && D % 8 == 0;
-  const int tiles = static_cast<int>((D + FWD_COLS - 1) / FWD_COLS), Di = static_cast<int>(D);
-  const long long units = n * tiles, sms = device_sm_count();
-  const dim3 grid(static_cast<unsigned>(std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * fwd_blocks(tdt == MUON_F32 ? 4 : 2))));
+  LookupArgs a{};
+  a.ids = ids;
+  a.table = table;
+  a.out = out;
+  a.ldt = ldt;
+  a.ldo = ldo;
+  a.n = n;
+  a.V = V;
+  a.itype = itype;
+  a.D = static_cast<int>(D);
+  a.scale = scale;
   launch_begin(KK_EMBED_FWD, s);
   cudaError_t e;
-  if (tdt == MUON_F32 && odt == MUON_F32)
-    e = launch_forward<float, float>(vec, grid, s, ids, itype, table, ldt, out, ldo, n, V, Di, tiles, scale);
-  else if (tdt == MUON_F32)
-    e = launch_forward<float, __nv_bfloat16>(vec, grid, s, ids, itype, table, ldt, out, ldo, n, V, Di, tiles, scale);
-  else if (odt == MUON_F32)
-    e = launch_forward<__nv_bfloat16, float>(vec, grid, s, ids, itype, table, ldt, out, ldo, n, V, Di, tiles, scale);
+  if (tdt == MUON_F32)
+    e = odt == MUON_F32 ? launch_lookup<float, float>(a, s) : launch_lookup<float, __nv_bfloat16>(a, s);
   else
-    e = launch_forward<__nv_bfloat16, __nv_bfloat16>(vec, grid, s, ids, itype, table, ldt, out, ldo, n, V, Di, tiles,
-                                                     scale);
+    e = odt == MUON_F32 ? launch_lookup<__nv_bfloat16, float>(a, s) : launch_lookup<__nv_bfloat16, __nv_bfloat16>(a, s);
   launch_end(s);
   return status_of(e);
 }
@@ -795,16 +994,15 @@ muon_status embedding_backward(const void *ids, muon_itype itype, const void *do
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long sms = device_sm_count();
   const int Di = static_cast<int>(D);
-  const bool gvec = aligned16(dtable) && ldg % 8 == 0 && D % 8 == 0;
   if (!accumulate) {
-    const long long work = V * (gvec ? D / 8 : D);
-    const dim3 grid(static_cast<unsigned>(std::min((work + THREADS - 1) / THREADS, sms * 4))), block(THREADS);   // room for the sort beside it
+    const long long size = gdt == MUON_F32 ? 4 : 2;
+    const bool dense = ldg == D || V == 1;
+    const long long rows = dense ? 1 : V, bytes = (dense ? V * D : D) * size;
+    const long long work = dense ? bytes / 64 + 1 : V * 32;   // threads that find something to do
+    const dim3 grid(static_cast<unsigned>(std::min((work + THREADS - 1) / THREADS, sms * 4)));   // room for the sort
     launch_begin(KK_EMBED_ZERO, s);
-    st = status_of(gdt == MUON_F32
-                       ? launch_pdl(embedding_zero_kernel<float>, grid, block, 0, s, static_cast<float *>(dtable), ldg,
-                                    V, Di, static_cast<int>(gvec))
-                       : launch_pdl(embedding_zero_kernel<__nv_bfloat16>, grid, block, 0, s,
-                                    static_cast<__nv_bfloat16 *>(dtable), ldg, V, Di, static_cast<int>(gvec)));
+    st = status_of(launch_pdl(embedding_zero_kernel, grid, dim3(THREADS), 0, s, static_cast<unsigned char *>(dtable),
+                              static_cast<long long>(ldg) * size, rows, bytes));
     launch_end(s);
     if (st != MUON_OK) return st;
   }
@@ -826,15 +1024,13 @@ muon_status embedding_backward(const void *ids, muon_itype itype, const void *do
   a.V = V;
   a.ldp = L.ldp;
   a.D = Di;
-  a.tiles = static_cast<int>((D + SUM_COLS - 1) / SUM_COLS);
   a.groups = static_cast<int>(L.groups);
   a.accumulate = accumulate != 0;
   a.scale = scale;
-  const bool vec = aligned16(dout) && ldo % 8 == 0 && aligned16(dtable) && ldg % 8 == 0 && D % 8 == 0;
   if (odt == MUON_F32)
-    return gdt == MUON_F32 ? launch_sums_vec<float, float>(vec, a, s) : launch_sums_vec<float, __nv_bfloat16>(vec, a, s);
-  return gdt == MUON_F32 ? launch_sums_vec<__nv_bfloat16, float>(vec, a, s)
-                         : launch_sums_vec<__nv_bfloat16, __nv_bfloat16>(vec, a, s);
+    return gdt == MUON_F32 ? launch_sums_for<float, float>(a, s) : launch_sums_for<float, __nv_bfloat16>(a, s);
+  return gdt == MUON_F32 ? launch_sums_for<__nv_bfloat16, float>(a, s)
+                         : launch_sums_for<__nv_bfloat16, __nv_bfloat16>(a, s);
 }
 
 }  // extern "C"

@@ -25,150 +25,224 @@ __device__ __forceinline__ float param_at(const void *p, int dt, int c, float ab
                         : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c]);
 }
 
-// The columns of thread t of the T that hold a row: chunk k's eight are contiguous on the vector path (which needs a
-// width of whole eights), and one per sweep of the group otherwise, so that a warp's accesses stay contiguous whatever
-// the alignment. Both number a thread's columns 8 k + e in increasing order, so one count says which of them the row
-// has.
+// How memory is accessed:
+//   SCALAR   one value at a time: bases or pitches that fit neither of the others
+//   ALIGNED  every row starts on a boundary of a granule, and the width is whole granules
+//   SHIFTED  rows start `shift` values past a boundary (an odd width); the first and the last granule of a row may be
+//            partial. A row slot sees rows whose index differs by multiples of 8, which all have the same shift, so
+//            its threads' columns stay the same.
+enum Mode { SCALAR, ALIGNED, SHIFTED };
+
+// A granule is 8 values of bf16 or, where a matrix is fp32, 4: an access of one is 16 (8 for bf16 beside fp32) bytes,
+// next to the neighbouring thread's.
+template <typename A, typename B>
+constexpr int granule_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
+
+// The columns of thread t of the T that hold a row, eight to a chunk: PG granules, each T granules after the one
+// before, or in SCALAR single columns T apart.
+template <int MODE_, int GE_, int T_>
 struct Cols {
-  int t, T, count;
+  static constexpr int MODE = MODE_, GE = MODE_ == SCALAR ? 8 : GE_, PG = 8 / GE, T = T_;
+  int t, D, shift, total, mine;   // total: the row's granules; mine: the thread's (SCALAR: its columns)
+  __device__ __forceinline__ Cols(int t_, int D_, int shift_) : t(t_), D(D_), shift(MODE == SHIFTED ? shift_ : 0) {
+    total = MODE == SCALAR ? D : (D + shift + GE - 1) / GE;
+    mine = max((total - t + T - 1) / T, 0);
+  }
+  __device__ __forceinline__ int granule(int k, int j) const { return (k * PG + j) * T + t; }
+  __device__ __forceinline__ int first(int k, int j) const { return granule(k, j) * GE - shift; }
+  __device__ __forceinline__ int col(int k, int e) const {
+    return MODE == SCALAR ? (8 * k + e) * T + t : first(k, e / GE) + e % GE;
+  }
+  __device__ __forceinline__ bool has(int k, int j) const { return (MODE == SCALAR ? 8 * k : k * PG + j) < mine; }
+  __device__ __forceinline__ bool edge(int k, int j) const {
+    return MODE == SHIFTED && (granule(k, j) == 0 || granule(k, j) == total - 1);
+  }
+  __device__ __forceinline__ bool in(int k, int e) const {   // of a granule that the thread has
+    return MODE == SCALAR ? 8 * k + e < mine : MODE == ALIGNED || (col(k, e) >= 0 && col(k, e) < D);
+  }
+  // pair i of chunk k with zeros where the row has no column; its granule is there
+  __device__ __forceinline__ float2 only(int k, int i, float2 v) const {
+    if (MODE == SCALAR || edge(k, 2 * i / GE)) {
+      if (!in(k, 2 * i)) v.x = 0.f;
+      if (!in(k, 2 * i + 1)) v.y = 0.f;
+    }
+    return v;
+  }
+  __device__ __forceinline__ int columns() const {
+    if (MODE == SCALAR) return mine;
+    int n = mine * GE;
+    if (MODE == SHIFTED && mine > 0) {
+      if (t == 0) n -= shift;
+      if ((total - 1) % T == t) n -= total * GE - shift - D;
+    }
+    return n;
+  }
 };
-template <bool VEC>
-__device__ __forceinline__ Cols cols_of(int t, int T, int D) {
-  if (VEC) return {t, T, (D / 8 - t + T - 1) / T * 8};
-  return {t, T, (D - t + T - 1) / T};
+
+// A chunk as it lies in memory.
+template <typename XT, int GE>
+struct RawChunk {
+  Raw<XT, GE> g[8 / GE];
+  __device__ __forceinline__ Vals<8> get() const {
+    Vals<8> o;
+#pragma unroll
+    for (int j = 0; j < 8 / GE; ++j) {
+      const Vals<GE> v = g[j].get();
+#pragma unroll
+      for (int i = 0; i < GE / 2; ++i) o.p[j * GE / 2 + i] = v.p[i];
+    }
+    return o;
+  }
+};
+
+// One granule. In SHIFTED an edge is read whole where the part outside the row lies in the rows around (below / above:
+// there are such), whose values are left out later; only the ends of the matrix are read value by value.
+template <typename XT, typename CT>
+__device__ __forceinline__ bool whole_granule(const CT &c, int k, int j, bool below, bool above) {
+  return !c.edge(k, j) || ((c.first(k, j) >= 0 || below) && (c.first(k, j) + CT::GE <= c.D || above));
 }
-template <bool VEC>
-__device__ __forceinline__ int col(const Cols &c, int k, int e) {
-  return VEC ? (k * c.T + c.t) * 8 + e : (k * 8 + e) * c.T + c.t;
-}
-template <bool VEC>
-__device__ __forceinline__ bool has(const Cols &c, int k, int e) {
-  return (VEC ? 8 * k : 8 * k + e) < c.count;
+template <typename XT, typename CT>
+__device__ __forceinline__ void load_values(const XT *p, const CT &c, int k, int j, Raw<XT, CT::GE> &r) {
+  r.clear();
+#pragma unroll
+  for (int e = 0; e < CT::GE; ++e)
+    if (c.in(k, j * CT::GE + e)) r.put(e, p[c.col(k, j * CT::GE + e)]);
 }
 
-template <typename XT>
-__device__ __forceinline__ XT zero_of() { return XT(0.f); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 zero_of<__nv_bfloat16>() { return __ushort_as_bfloat16(0); }
-
-// Columns that the row does not have read as 0.
-template <typename XT, bool VEC>
-__device__ __forceinline__ void load_chunk(const XT *p, const Cols &c, int k, Raw8<XT> &r) {
-  XT f[8];
+// Columns that the thread does not have read as 0.
+template <typename XT, typename CT>
+__device__ __forceinline__ void load_chunk(const XT *p, const CT &c, int k, bool below, bool above,
+                                           RawChunk<XT, CT::GE> &r) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = zero_of<XT>();
-  if constexpr (VEC) {
-    if (has<true>(c, k, 0)) r.load(p + col<true>(c, k, 0));
-    else r.set(f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (has<false>(c, k, e)) f[e] = p[col<false>(c, k, e)];
-    r.set(f);
+  for (int j = 0; j < CT::PG; ++j) {
+    if (!c.has(k, j)) r.g[j].clear();
+    else if (CT::MODE != SCALAR && whole_granule<XT>(c, k, j, below, above)) r.g[j].load(p + c.first(k, j));
+    else load_values(p, c, k, j, r.g[j]);
   }
 }
 
-template <typename XT, bool VEC>
-__device__ __forceinline__ void store_chunk(XT *p, const Cols &c, int k, const Oct &o) {
-  const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
-  if constexpr (VEC) {
-    if (has<true>(c, k, 0)) store8(p + col<true>(c, k, 0), f);
-  } else {
+template <typename XT, typename CT>
+__device__ __forceinline__ void store_values(XT *p, const CT &c, int k, int j, const Vals<8> &o) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (has<false>(c, k, e)) store1(p, col<false>(c, k, e), f[e]);
+  for (int e = 0; e < CT::GE; ++e) {
+    const float2 v = o.p[(j * CT::GE + e) / 2];
+    if (c.in(k, j * CT::GE + e)) store1(p, c.col(k, j * CT::GE + e), e % 2 ? v.y : v.x);
   }
 }
 
-// The thread's weights (or biases): `absent` where there are none.
-template <bool VEC>
-__device__ __forceinline__ Oct param_chunk(const void *p, int dt, const Cols &c, int k, float absent) {
-  Oct o;
+template <typename XT, typename CT>
+__device__ __forceinline__ void store_chunk(XT *p, const CT &c, int k, const Vals<8> &o) {
+#pragma unroll
+  for (int j = 0; j < CT::PG; ++j) {
+    if (!c.has(k, j)) continue;
+    if (CT::MODE == SCALAR || c.edge(k, j)) {
+      store_values(p, c, k, j, o);
+    } else {
+      Vals<CT::GE> v;
+#pragma unroll
+      for (int i = 0; i < CT::GE / 2; ++i) v.p[i] = o.p[j * CT::GE / 2 + i];
+      store_vals(p + c.first(k, j), v);
+    }
+  }
+}
+
+// fp32 sums of the thread's columns to a row that starts on a boundary itself
+template <typename CT>
+__device__ __forceinline__ void store_sums(float *p, const CT &c, int k, const Vals<8> &o) {
+  if (CT::MODE == ALIGNED) {
+    store_chunk(p, c, k, o);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < CT::PG; ++j)
+    if (c.has(k, j)) store_values(p, c, k, j, o);
+}
+
+// The thread's weights (or biases): `absent` where there are none. wide: the vector may be read a granule at a time.
+template <typename CT>
+__device__ __forceinline__ Vals<8> param_chunk(const void *p, int dt, bool wide, const CT &c, int k, float absent) {
+  Vals<8> o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.p[i] = make_float2(absent, absent);
   if (p == nullptr) return o;
-  if constexpr (VEC) {
-    if (!has<true>(c, k, 0)) return o;
+  if (CT::MODE == ALIGNED && wide) {
     if (dt == MUON_F32) {
-      Raw8<float> r;
-      r.load(static_cast<const float *>(p) + col<true>(c, k, 0));
+      RawChunk<float, CT::GE> r;
+      load_chunk(static_cast<const float *>(p), c, k, false, false, r);
       return r.get();
     }
-    Raw8<__nv_bfloat16> r;
-    r.load(static_cast<const __nv_bfloat16 *>(p) + col<true>(c, k, 0));
+    RawChunk<__nv_bfloat16, CT::GE> r;
+    load_chunk(static_cast<const __nv_bfloat16 *>(p), c, k, false, false, r);
     return r.get();
-  } else {
+  }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (has<false>(c, k, e)) (e % 2 ? o.p[e / 2].y : o.p[e / 2].x) = param_at(p, dt, col<false>(c, k, e), absent);
-    return o;
-  }
+  for (int e = 0; e < 8; ++e)
+    if (c.has(k, e / CT::GE) && c.in(k, e)) (e % 2 ? o.p[e / 2].y : o.p[e / 2].x) = param_at(p, dt, c.col(k, e), absent);
+  return o;
 }
 
-// Zero where the row has no column (without the vector path; on it a chunk is there or not).
-template <bool VEC>
-__device__ __forceinline__ float2 only(const Cols &c, int k, int i, float2 v) {
-  if (!VEC) {
-    if (!has<false>(c, k, 2 * i)) v.x = 0.f;
-    if (!has<false>(c, k, 2 * i + 1)) v.y = 0.f;
-  }
-  return v;
-}
-
-// The rows to come. On the vector path they are copied into a ring of STAGES places in shared memory, of which every
-// thread writes and reads its own columns only: its own wait orders them, and no registers hold them meanwhile.
-// Without it the next row's loads wait in registers. Layout: [stage][chunk][piece][thread].
-template <typename XT, int C, int THREADS>
+// The rows to come. In ALIGNED and SHIFTED they are copied into a ring of STAGES places in shared memory, of which
+// every thread writes and reads its own columns only: its own wait orders them, and no registers hold them meanwhile.
+// In SCALAR the next row's loads wait in registers. Layout: [stage][chunk][granule][thread].
+template <typename XT, typename CT, int C, int THREADS>
 struct Ring {
-  static constexpr int PIECES = Raw8<XT>::PIECES;
-  uint4 *base;   // of this thread
-  __device__ __forceinline__ void fetch(const XT *row, const Cols &c, int stage) const {
-    uint4 *to = base + stage * (C * PIECES * THREADS);
+  using R = Raw<XT, CT::GE>;
+  unsigned char *base;   // of this thread
+  __device__ __forceinline__ unsigned char *at(int stage, int k, int j) const {
+    return base + ((stage * C + k) * CT::PG + j) * (THREADS * R::BYTES);
+  }
+  __device__ __forceinline__ void fetch(const XT *row, const CT &c, int stage, bool below, bool above) const {
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (has<true>(c, k, 0)) {
 #pragma unroll
-        for (int p = 0; p < PIECES; ++p)
-          copy_async16(to + (k * PIECES + p) * THREADS, reinterpret_cast<const uint4 *>(row + col<true>(c, k, 0)) + p);
+      for (int j = 0; j < CT::PG; ++j) {
+        if (!c.has(k, j)) continue;
+        if (whole_granule<XT>(c, k, j, below, above)) {
+          copy_async<R::BYTES>(at(stage, k, j), row + c.first(k, j));
+        } else {
+          R r;
+          load_values(row, c, k, j, r);
+          r.store(reinterpret_cast<XT *>(at(stage, k, j)));
+        }
       }
   }
-  __device__ __forceinline__ Oct get(int k, int stage) const {
-    const uint4 *from = base + stage * (C * PIECES * THREADS);
-    Raw8<XT> r;
+  __device__ __forceinline__ Vals<8> get(int k, int stage) const {
+    RawChunk<XT, CT::GE> r;
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p) r.w[p] = from[(k * PIECES + p) * THREADS];
+    for (int j = 0; j < CT::PG; ++j) r.g[j].load(reinterpret_cast<const XT *>(at(stage, k, j)));
     return r.get();
   }
 };
 
 // A vector of weights (or biases), as each thread wants its own columns of it row after row: in registers where there
 // is one chunk, as fp32 in shared memory up to 8192 columns of several chunks, and read where it is beyond that (and
-// without the vector path, for several chunks).
-template <int C, int THREADS, bool VEC, bool SHARED>
+// in SCALAR, for several chunks).
+template <typename CT, int C, int THREADS, bool SHARED>
 struct Params {
   const void *p;
   int dt;
+  bool wide;
   float absent;
   float4 *base;   // SHARED: of this thread, [2 chunk + half][thread]
-  Oct one;
-  __device__ __forceinline__ void init(const Cols &c) {
-    if constexpr (C == 1) one = param_chunk<VEC>(p, dt, c, 0, absent);
+  Vals<8> one;
+  __device__ __forceinline__ void init(const CT &c) {
+    if constexpr (C == 1) one = param_chunk(p, dt, wide, c, 0, absent);
     if constexpr (SHARED) {
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        const Oct o = param_chunk<VEC>(p, dt, c, k, absent);
+        const Vals<8> o = param_chunk(p, dt, wide, c, k, absent);
         base[(2 * k) * THREADS] = make_float4(o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y);
         base[(2 * k + 1) * THREADS] = make_float4(o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y);
       }
     }
   }
-  __device__ __forceinline__ Oct get(const Cols &c, int k) const {
+  __device__ __forceinline__ Vals<8> get(const CT &c, int k) const {
     if constexpr (C == 1) return one;
     if constexpr (SHARED) {
       const float4 u = base[(2 * k) * THREADS], v = base[(2 * k + 1) * THREADS];
       return {{make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)}};
     }
-    return param_chunk<VEC>(p, dt, c, k, absent);
+    return param_chunk(p, dt, wide, c, k, absent);
   }
 };
 
@@ -244,9 +318,18 @@ inline muon_status check_dims(int64_t N, int64_t D) {
   return N > (1ll << 30) || D > (1ll << 20) ? MUON_ERR_SHAPE : MUON_OK;
 }
 
-// Warps for a row of D columns held in C chunks per thread: what it takes, rounded up to a width that is compiled.
-inline int warps_of(long long D, int C) {
-  const int need = static_cast<int>((D + 256 * C - 1) / (256 * C));
+// The mode for matrices whose bases are all 16-byte aligned (or not), the pitch of the first, and whether all pitches
+// are the same modulo 8.
+inline Mode mode_of(bool bases, bool pitches, long long ld, long long D) {
+  if (!bases || !pitches || D < 8) return SCALAR;
+  return ld % 8 == 0 && D % 8 == 0 ? ALIGNED : SHIFTED;
+}
+
+// Warps for a row of D columns held in C chunks per thread: what it takes (a SHIFTED row has a granule more), rounded
+// up to a width that is compiled; SCALAR knows only the largest of each kind.
+inline int warps_of(long long D, int C, Mode mode) {
+  const int need = static_cast<int>((D + (mode == SHIFTED ? 7 : 0) + 256 * C - 1) / (256 * C));
+  if (mode == SCALAR) return need <= 4 && C == 1 ? 4 : need <= 16 ? 16 : 32;
   for (int w : {1, 2, 3, 4, 6, 8, 12, 16}) if (need <= w) return w;
   return 32;
 }

@@ -25,45 +25,48 @@ struct BackwardArgs {
   const float *mean, *rstd;
   float *part;      // [2][parts][ldp]: dw's partial rows, then db's; null: neither is wanted
   long long parts, ldp;
-  int wdt, D;
+  int wdt, wide, D;
 };
 
 // Rows as in the forward kernel: R at a time, W warps each, with the next rows on their way. A thread's columns of dw
 // and db are in registers, or in shared memory for rows of more than 8192 columns (1024 threads have 64 registers
 // each), which leaves no room for a ring: the next row waits in registers there, where it fits them.
-template <typename XT, typename YT, int C, int W, int R, bool VEC>
+template <typename XT, typename YT, int C, int W, int R, int MODE>
 struct Backward {
   static constexpr int T = W * 32, THREADS = T * R;
-  static constexpr bool IN_SHARED = W == 32, RING = VEC && !IN_SHARED;
+  using CT = Cols<MODE, granule_of<XT, YT>(), T>;
+  static constexpr bool IN_SHARED = W == 32, RING = MODE != SCALAR && !IN_SHARED;
   static constexpr bool AHEAD = !IN_SHARED || sizeof(XT) + sizeof(YT) == 4;
   static constexpr bool SHARED = RING && C > 1;
   static constexpr int STAGES = C * T * 8 * (sizeof(XT) + sizeof(YT)) <= 16384 ? 3 : 2;
-  static constexpr int RING_X = RING ? STAGES * C * Raw8<XT>::PIECES * THREADS : 0;   // in 16-byte pieces
-  static constexpr int RING_DY = RING ? STAGES * C * Raw8<YT>::PIECES * THREADS : 0;
-  static constexpr size_t BYTES =
-      16 * static_cast<size_t>(RING_X + RING_DY + (SHARED ? 2 * C * THREADS : 0) + (IN_SHARED ? 4 * C * THREADS : 0));
+  static constexpr int RING_X = RING ? STAGES * C * 8 * sizeof(XT) * THREADS : 0;   // bytes
+  static constexpr int RING_DY = RING ? STAGES * C * 8 * sizeof(YT) * THREADS : 0;
+  static constexpr size_t BYTES = static_cast<size_t>(RING_X) + RING_DY + (SHARED ? 32 * C * THREADS : 0) +
+                                  (IN_SHARED ? 64 * C * THREADS : 0);
   static constexpr int BLOCKS = std::max(1, (C == 1 ? 768 : 512) / THREADS);
 };
 
-template <typename XT, typename YT, int C, int W, int R, bool VEC>
-__global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, VEC>::BLOCKS))
+template <typename XT, typename YT, int C, int W, int R, int MODE>
+__global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::BLOCKS))
     layernorm_backward_kernel(const BackwardArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  using B = Backward<XT, YT, C, W, R, VEC>;
+  using B = Backward<XT, YT, C, W, R, MODE>;
+  using CT = typename B::CT;
   constexpr int T = B::T, STAGES = B::STAGES, THREADS = B::THREADS;
-  extern __shared__ uint4 shared[];
+  extern __shared__ __align__(16) unsigned char shared[];
   __shared__ float2 red[2][R][W];
   __shared__ __align__(16) float join[R > 1 ? R * T * 8 : 1];
   const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T, D = a.D;
-  const Cols c = cols_of<VEC>(t, T, D);
+  const long long step = static_cast<long long>(gridDim.x) * R;
+  long long row = static_cast<long long>(blockIdx.x) * R + slot;
+  const CT c(t, D, static_cast<int>((row * a.ldx) & (CT::GE - 1)));
   Exchange<W, R> exchange{red, slot, t / 32, 0};
-  const Ring<XT, C, THREADS> ring_x{shared + threadIdx.x};
-  const Ring<YT, C, THREADS> ring_dy{shared + B::RING_X + threadIdx.x};
+  const Ring<XT, CT, C, THREADS> ring_x{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
+  const Ring<YT, CT, C, THREADS> ring_dy{shared + B::RING_X + threadIdx.x * Raw<YT, CT::GE>::BYTES};
   float4 *kept = reinterpret_cast<float4 *>(shared + B::RING_X + B::RING_DY) + threadIdx.x;
-  Params<C, THREADS, VEC, B::SHARED> weight{a.w, a.wdt, 1.f, kept};
-  weight.init(c);
-  Oct aw[C], ab[C];
+  Params<CT, C, THREADS, B::SHARED> weight{a.w, a.wdt, a.wide != 0, 1.f, kept};
+  Vals<8> aw[C], ab[C];
 #pragma unroll
   for (int k = 0; k < C; ++k)
 #pragma unroll
@@ -94,25 +97,24 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, VEC>::BL
 #pragma unroll
   for (int k = 0; k < C; ++k) sums_put(k);
   const float inv = 1.f / static_cast<float>(D);
-  const long long step = static_cast<long long>(gridDim.x) * R;
   const long long x_step = step * a.ldx, dy_step = step * a.lddy, dx_step = step * a.lddx;
-  long long row = static_cast<long long>(blockIdx.x) * R + slot;
   const XT *x = static_cast<const XT *>(a.x) + row * a.ldx;   // x and dy: the next row to fetch
   const YT *dy = static_cast<const YT *>(a.dy) + row * a.lddy;
   XT *dx = a.dx != nullptr ? static_cast<XT *>(a.dx) + row * a.lddx : nullptr;
   long long fetched = row;
-  Raw8<XT> rx[B::RING ? 1 : C];
-  Raw8<YT> rdy[B::RING ? 1 : C];
+  RawChunk<XT, CT::GE> rx[B::RING ? 1 : C];
+  RawChunk<YT, CT::GE> rdy[B::RING ? 1 : C];
   auto fetch = [&](int stage) {
     if (fetched < a.N) {
+      const bool below = fetched > 0, above = fetched + 1 < a.N;
       if constexpr (B::RING) {
-        ring_x.fetch(x, c, stage);
-        ring_dy.fetch(dy, c, stage);
+        ring_x.fetch(x, c, stage, below, above);
+        ring_dy.fetch(dy, c, stage, below, above);
       } else {
 #pragma unroll
         for (int k = 0; k < C; ++k) {
-          load_chunk<XT, VEC>(x, c, k, rx[k]);
-          load_chunk<YT, VEC>(dy, c, k, rdy[k]);
+          load_chunk(x, c, k, below, above, rx[k]);
+          load_chunk(dy, c, k, below, above, rdy[k]);
         }
       }
     }
@@ -128,6 +130,7 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, VEC>::BL
   }
   if constexpr (B::AHEAD) fetch(0);
   if constexpr (B::RING && STAGES == 3) fetch(1);
+  weight.init(c);
   int stage = 0;
   for (; row - slot < a.N; row += step) {   // the same count for the whole block
     const bool live = R == 1 || row < a.N;
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, VEC>::BL
       mean = a.mean[row + step];
       rstd = a.rstd[row + step];
     }
-    Oct xh[C], g[C];
+    Vals<8> xh[C], g[C];
     if constexpr (B::RING) {
       copy_async_wait<STAGES - 2>();
 #pragma unroll
@@ -160,20 +163,18 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, VEC>::BL
     if (live) {
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        const Oct w = weight.get(c, k);
+        const Vals<8> w = weight.get(c, k);
         sums_get(k);
-        // where the row has no column dy is 0 (or not looked at), but xh need not be finite
-        if (has<VEC>(c, k, 0)) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 h = only<VEC>(c, k, i, __fmul2_rn(__fadd2_rn(xh[k].p[i], m2), r2));
-            xh[k].p[i] = h;
-            aw[k].p[i] = __ffma2_rn(g[k].p[i], h, aw[k].p[i]);
-            ab[k].p[i] = __fadd2_rn(ab[k].p[i], g[k].p[i]);
-            g[k].p[i] = __fmul2_rn(g[k].p[i], w.p[i]);
-            s1 = __fadd2_rn(s1, g[k].p[i]);
-            s2 = __ffma2_rn(g[k].p[i], h, s2);
-          }
+        for (int i = 0; i < 4; ++i) {
+          if (!c.has(k, 2 * i / CT::GE)) continue;
+          const float2 h = c.only(k, i, __fmul2_rn(__fadd2_rn(xh[k].p[i], m2), r2)), d = c.only(k, i, g[k].p[i]);
+          xh[k].p[i] = h;
+          aw[k].p[i] = __ffma2_rn(d, h, aw[k].p[i]);
+          ab[k].p[i] = __fadd2_rn(ab[k].p[i], d);
+          g[k].p[i] = __fmul2_rn(d, w.p[i]);
+          s1 = __fadd2_rn(s1, g[k].p[i]);
+          s2 = __ffma2_rn(g[k].p[i], h, s2);
         }
         sums_put(k);
       }
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, VEC>::BL
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             g[k].p[i] = __fmul2_rn(__ffma2_rn(xh[k].p[i], c2, __fadd2_rn(g[k].p[i], c1)), r2);
-          store_chunk<XT, VEC>(dx, c, k, g[k]);
+          store_chunk(dx, c, k, g[k]);
         }
       }
       dx += dx_step;
@@ -201,13 +202,13 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, VEC>::BL
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       sums_get(k);
-      store_chunk<float, VEC>(pw, c, k, aw[k]);
-      store_chunk<float, VEC>(pb, c, k, ab[k]);
+      store_sums(pw, c, k, aw[k]);
+      store_sums(pb, c, k, ab[k]);
     }
   } else {   // the block's rows are added in order
     for (int z = 0; z < 2; ++z) {
       __syncthreads();
-      store_chunk<float, VEC>(join + slot * D, c, 0, z == 0 ? aw[0] : ab[0]);
+      store_sums(join + slot * D, c, 0, z == 0 ? aw[0] : ab[0]);
       __syncthreads();
       for (int j = threadIdx.x; j < D; j += THREADS) {
         float s = 0.f;
@@ -301,43 +302,65 @@ __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(con
 
 // ------------------------------------------------------------------------------------------ host
 
-// Chunks per thread, warps per row and rows per block for D columns: see backward_route.
+// Chunks per thread, warps per row and rows per block for D columns: one chunk of eight columns per thread and several
+// rows in a block up to 1024 columns, two chunks above.
 struct Shape {
   int C, W, R;
 };
-Shape shape_of(long long D, bool vec) {
-  if (D <= 1024) {
-    const int W = warps_of(D, 1);
+Shape shape_of(long long D, Mode mode) {
+  if (D + (mode == SHIFTED ? 7 : 0) <= 1024) {
+    const int W = warps_of(D, 1, mode);
     return {1, W, W == 1 ? 8 : W == 2 ? 4 : 2};
   }
-  int W = warps_of(D, 2);
-  if (!vec) W = W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;
-  return {2, W, 1};
+  return {2, std::max(3, warps_of(D, 2, mode)), 1};
 }
+bool long_row(long long D, Mode mode) { return D + (mode == SHIFTED ? 7 : 0) > MAX_ROW; }
 
 // Blocks of the backward pass, each of which leaves one partial row of dw and db: as many as the GPU holds at once,
-// so that there are few partial rows to add.
-long long parts_for(long long N, long long D, bool vec) {
-  if (D > MAX_ROW) return std::max(1LL, std::min(N, 64LL));
-  const Shape h = shape_of(D, vec);
+// so that there are few partial rows to add. In SHIFTED a slot's rows lie multiples of eight apart.
+long long parts_for(long long N, long long D, Mode mode) {
+  if (long_row(D, mode)) return std::max(1LL, std::min(N, 64LL));
+  const Shape h = shape_of(D, mode);
   const long long resident = std::max(1, (h.C == 1 ? 768 : 512) / (h.W * h.R * 32));
-  return std::max(1LL, std::min((N + h.R - 1) / h.R, 152 * resident));
+  const long long blocks = std::max(1LL, std::min((N + h.R - 1) / h.R, 152 * resident));
+  return mode == SHIFTED ? (blocks + 7) / 8 * 8 : blocks;
 }
 long long part_pitch(long long D) { return (D + 7) / 8 * 8; }
 
-template <typename XT, typename YT, int C, int W, int R, bool VEC>
+template <typename XT, typename YT, int C, int W, int R, int MODE>
 cudaError_t backward_launch(const BackwardArgs &a, cudaStream_t s) {
-  using B = Backward<XT, YT, C, W, R, VEC>;
-  auto kernel = layernorm_backward_kernel<XT, YT, C, W, R, VEC>;
+  using B = Backward<XT, YT, C, W, R, MODE>;
+  auto kernel = layernorm_backward_kernel<XT, YT, C, W, R, MODE>;
   static const cudaError_t allowed = allow_shared(kernel);
   if (allowed != cudaSuccess) return allowed;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(a.parts)), dim3(B::THREADS), B::BYTES, s, a);
 }
 
-// One chunk of eight columns per thread and several rows in a block up to 1024 columns, two chunks above.
+template <typename XT, typename YT, int MODE>
+cudaError_t backward_route_mode(const BackwardArgs &a, cudaStream_t s) {
+  const Shape h = shape_of(a.D, static_cast<Mode>(MODE));
+  if (h.C == 1) {
+    switch (h.W) {
+      case 1: return backward_launch<XT, YT, 1, 1, 8, MODE>(a, s);
+      case 2: return backward_launch<XT, YT, 1, 2, 4, MODE>(a, s);
+      case 3: return backward_launch<XT, YT, 1, 3, 2, MODE>(a, s);
+      default: return backward_launch<XT, YT, 1, 4, 2, MODE>(a, s);
+    }
+  }
+  switch (h.W) {
+    case 3: return backward_launch<XT, YT, 2, 3, 1, MODE>(a, s);
+    case 4: return backward_launch<XT, YT, 2, 4, 1, MODE>(a, s);
+    case 6: return backward_launch<XT, YT, 2, 6, 1, MODE>(a, s);
+    case 8: return backward_launch<XT, YT, 2, 8, 1, MODE>(a, s);
+    case 12: return backward_launch<XT, YT, 2, 12, 1, MODE>(a, s);
+    case 16: return backward_launch<XT, YT, 2, 16, 1, MODE>(a, s);
+    default: return backward_launch<XT, YT, 2, 32, 1, MODE>(a, s);
+  }
+}
+
 template <typename XT, typename YT>
-cudaError_t backward_route(const BackwardArgs &a, bool vec, cudaStream_t s) {
-  if (a.D > MAX_ROW) {
+cudaError_t backward_route(const BackwardArgs &a, Mode mode, cudaStream_t s) {
+  if (long_row(a.D, mode)) {
     // the columns first: dx may take the place of dy or x
     if (a.part != nullptr) {
       const dim3 cgrid(static_cast<unsigned>((a.D + 255) / 256), static_cast<unsigned>(a.parts));
@@ -349,32 +372,12 @@ cudaError_t backward_route(const BackwardArgs &a, bool vec, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(std::min<long long>(a.N, device_sm_count() * 2))), block(LONG_THREADS);
     return launch_pdl(layernorm_dx_long_kernel<XT, YT>, grid, block, 0, s, a);
   }
-  const int W = shape_of(a.D, vec).W;
-  if (a.D <= 1024) {
-    switch (W) {
-      case 1: return vec ? backward_launch<XT, YT, 1, 1, 8, true>(a, s) : backward_launch<XT, YT, 1, 1, 8, false>(a, s);
-      case 2: return vec ? backward_launch<XT, YT, 1, 2, 4, true>(a, s) : backward_launch<XT, YT, 1, 2, 4, false>(a, s);
-      case 3: return vec ? backward_launch<XT, YT, 1, 3, 2, true>(a, s) : backward_launch<XT, YT, 1, 3, 2, false>(a, s);
-      default:
-        return vec ? backward_launch<XT, YT, 1, 4, 2, true>(a, s) : backward_launch<XT, YT, 1, 4, 2, false>(a, s);
-    }
-  }
-  if (vec) {
-    switch (W) {
-      case 3: return backward_launch<XT, YT, 2, 3, 1, true>(a, s);
-      case 4: return backward_launch<XT, YT, 2, 4, 1, true>(a, s);
-      case 6: return backward_launch<XT, YT, 2, 6, 1, true>(a, s);
-      case 8: return backward_launch<XT, YT, 2, 8, 1, true>(a, s);
-      case 12: return backward_launch<XT, YT, 2, 12, 1, true>(a, s);
-      case 16: return backward_launch<XT, YT, 2, 16, 1, true>(a, s);
-      default: return backward_launch<XT, YT, 2, 32, 1, true>(a, s);
-    }
-  }
-  switch (W) {
-    case 4: return backward_launch<XT, YT, 2, 4, 1, false>(a, s);
-    case 8: return backward_launch<XT, YT, 2, 8, 1, false>(a, s);
-    case 16: return backward_launch<XT, YT, 2, 16, 1, false>(a, s);
-    default: return backward_launch<XT, YT, 2, 32, 1, false>(a, s);
+  if (mode == ALIGNED) return backward_route_mode<XT, YT, ALIGNED>(a, s);
+  if (mode == SHIFTED) return backward_route_mode<XT, YT, SHIFTED>(a, s);
+  switch (shape_of(a.D, mode).W) {
+    case 4: return backward_launch<XT, YT, 1, 4, 2, SCALAR>(a, s);
+    case 16: return backward_launch<XT, YT, 2, 16, 1, SCALAR>(a, s);
+    default: return backward_launch<XT, YT, 2, 32, 1, SCALAR>(a, s);
   }
 }
 
@@ -387,7 +390,9 @@ extern "C" {
 
 size_t layernorm_workspace_bytes(int64_t N, int64_t D) {
   if (N < 0 || D < 1) return 0;
-  return align_up(static_cast<size_t>(8) * std::max(parts_for(N, D, true), parts_for(N, D, false)) * part_pitch(D), 256);
+  long long parts = 0;
+  for (Mode mode : {SCALAR, ALIGNED, SHIFTED}) parts = std::max(parts, parts_for(N, D, mode));
+  return align_up(static_cast<size_t>(8) * parts * part_pitch(D), 256);
 }
 
 muon_status layernorm_backward(const void *dy, muon_dtype ydt, int64_t lddy, const void *x, muon_dtype xdt, int64_t ldx,
@@ -411,19 +416,19 @@ muon_status layernorm_backward(const void *dy, muon_dtype ydt, int64_t lddy, con
   }
   if ((st = device_check()) != MUON_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool vec = aligned16(dy) && aligned16(x) && aligned16(weight) && aligned16(dx) && lddy % 8 == 0 &&
-                   ldx % 8 == 0 && (dx == nullptr || lddx % 8 == 0) && D % 8 == 0;
+  const Mode mode = mode_of(aligned16(dy) && aligned16(x) && aligned16(dx),
+                            (ldx - lddy) % 8 == 0 && (dx == nullptr || (ldx - lddx) % 8 == 0), ldx, D);
   BackwardArgs a{dy, x, weight, dx, lddy, ldx, lddx, N, mean, rstd, sums ? static_cast<float *>(ws) : nullptr,
-                 parts_for(N, D, vec), part_pitch(D), wdt, static_cast<int>(D)};
+                 parts_for(N, D, mode), part_pitch(D), wdt, aligned16(weight) ? 1 : 0, static_cast<int>(D)};
   if (N == 0) a.parts = 0;
   if (N > 0) {
     launch_begin(KK_LN_BWD, s);
     cudaError_t e;
     if (xdt == MUON_F32)
-      e = ydt == MUON_F32 ? backward_route<float, float>(a, vec, s) : backward_route<float, __nv_bfloat16>(a, vec, s);
+      e = ydt == MUON_F32 ? backward_route<float, float>(a, mode, s) : backward_route<float, __nv_bfloat16>(a, mode, s);
     else
-      e = ydt == MUON_F32 ? backward_route<__nv_bfloat16, float>(a, vec, s)
-                          : backward_route<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
+      e = ydt == MUON_F32 ? backward_route<__nv_bfloat16, float>(a, mode, s)
+                          : backward_route<__nv_bfloat16, __nv_bfloat16>(a, mode, s);
     launch_end(s);
     if (e != cudaSuccess) return MUON_ERR_CUDA;
   }

@@ -18,72 +18,75 @@ struct ForwardArgs {
   long long ldx, ldy, N;
   float *mean, *rstd;
   float eps;
-  int wdt, D;
+  int wdt, wide, D;
 };
 
 // R rows at a time, W warps each, with the next rows on their way. Mean and variance take one exchange: each warp sums
 // its own columns and their squared distances from the warp's own mean, and
 //   sum (x - mean)^2 = sum over warps of (own squares + n_w (mean_w - mean)^2).
-template <typename XT, typename YT, int C, int W, int R, bool VEC>
+template <typename XT, typename YT, int C, int W, int R, int MODE>
 struct Forward {
   static constexpr int T = W * 32, THREADS = T * R;
-  static constexpr bool SHARED = VEC && C > 1 && C * T * 8 <= 8192;
+  using CT = Cols<MODE, granule_of<XT, YT>(), T>;
+  static constexpr bool RING = MODE != SCALAR, SHARED = RING && C > 1 && C * T * 8 <= 8192;
   static constexpr int STAGES = C * T * 8 * sizeof(XT) <= 16384 ? 3 : 2;
-  static constexpr int RING = VEC ? STAGES * C * Raw8<XT>::PIECES * THREADS : 0;   // in 16-byte pieces
-  static constexpr size_t BYTES = 16 * static_cast<size_t>(RING + (SHARED ? 4 * C * THREADS : 0));
-  static constexpr int by_registers = C == 4 ? (W <= 4 ? 768 : 512) : 1024;   // threads of a multiprocessor
+  static constexpr int ROWS = RING ? STAGES * C * 8 * sizeof(XT) * THREADS : 0;   // bytes of the ring
+  static constexpr size_t BYTES = static_cast<size_t>(ROWS) + (SHARED ? 64 * C * THREADS : 0);
+  static constexpr int by_registers = C == 4 ? (W <= 4 ? 768 : W <= 8 ? 512 : 1024) : 1024;   // threads of an SM
   static constexpr int BLOCKS = std::max(1, by_registers / THREADS);
 };
 
-template <typename XT, typename YT, int C, int W, int R, bool VEC>
-__global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, VEC>::BLOCKS))
+template <typename XT, typename YT, int C, int W, int R, int MODE>
+__global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BLOCKS))
     layernorm_forward_kernel(const ForwardArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  using F = Forward<XT, YT, C, W, R, VEC>;
+  using F = Forward<XT, YT, C, W, R, MODE>;
+  using CT = typename F::CT;
   constexpr int T = F::T, STAGES = F::STAGES;
-  extern __shared__ uint4 shared[];
+  extern __shared__ __align__(16) unsigned char shared[];
   __shared__ float2 red[2][R][W];
   const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T;
-  const Cols c = cols_of<VEC>(t, T, a.D);
-  Exchange<W, R> exchange{red, slot, t / 32, 0};
-  const Ring<XT, C, F::THREADS> ring{shared + threadIdx.x};
-  float4 *kept = reinterpret_cast<float4 *>(shared + F::RING) + threadIdx.x;
-  Params<C, F::THREADS, VEC, F::SHARED> weight{a.w, a.wdt, 1.f, kept}, bias{a.b, a.wdt, 0.f, kept + 2 * C * F::THREADS};
-  weight.init(c);
-  bias.init(c);
-  const float inv = 1.f / static_cast<float>(a.D);
-  // columns of this warp, and of the warp whose pair this lane reads in the exchange
-  const float n_w = warp_sum(static_cast<float>(max(c.count, 0))), inv_n = n_w > 0.f ? 1.f / n_w : 0.f;
-  float n_lane = n_w;
-  if constexpr (W > 1) n_lane = exchange.put_get(n_w, 0.f).x;
   const long long step = static_cast<long long>(gridDim.x) * R;
-  const long long x_step = step * a.ldx, y_step = step * a.ldy;
   long long row = static_cast<long long>(blockIdx.x) * R + slot;
+  const CT c(t, a.D, static_cast<int>((row * a.ldx) & (CT::GE - 1)));
+  Exchange<W, R> exchange{red, slot, t / 32, 0};
+  const Ring<XT, CT, C, F::THREADS> ring{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
+  float4 *kept = reinterpret_cast<float4 *>(shared + F::ROWS) + threadIdx.x;
+  Params<CT, C, F::THREADS, F::SHARED> weight{a.w, a.wdt, a.wide != 0, 1.f, kept},
+      bias{a.b, a.wdt, a.wide != 0, 0.f, kept + 2 * C * F::THREADS};
+  const long long x_step = step * a.ldx, y_step = step * a.ldy;
   const XT *x = static_cast<const XT *>(a.x) + row * a.ldx;   // the next row to fetch
   YT *y = static_cast<YT *>(a.y) + row * a.ldy;
   long long fetched = row;
-  Raw8<XT> raw[VEC ? 1 : C];
+  RawChunk<XT, CT::GE> raw[F::RING ? 1 : C];
   auto fetch = [&](int stage) {
     if (fetched < a.N) {
-      if constexpr (VEC) {
-        ring.fetch(x, c, stage);
+      if constexpr (F::RING) {
+        ring.fetch(x, c, stage, fetched > 0, fetched + 1 < a.N);
       } else {
 #pragma unroll
-        for (int k = 0; k < C; ++k) load_chunk<XT, false>(x, c, k, raw[k]);
+        for (int k = 0; k < C; ++k) load_chunk(x, c, k, false, false, raw[k]);
       }
     }
-    if constexpr (VEC) copy_async_commit();
+    if constexpr (F::RING) copy_async_commit();
     fetched += step;
     x += x_step;
   };
   fetch(0);
-  if constexpr (VEC && STAGES == 3) fetch(1);
+  if constexpr (F::RING && STAGES == 3) fetch(1);
+  weight.init(c);
+  bias.init(c);
+  const float inv = 1.f / static_cast<float>(a.D);
+  // columns of this warp, and of the warp whose pair this lane reads in the exchange
+  const float n_w = warp_sum(static_cast<float>(c.columns())), inv_n = n_w > 0.f ? 1.f / n_w : 0.f;
+  float n_lane = n_w;
+  if constexpr (W > 1) n_lane = exchange.put_get(n_w, 0.f).x;
   int stage = 0;
   for (; row - slot < a.N; row += step) {   // the same count for the whole block
     const bool live = R == 1 || row < a.N;
-    Oct v[C];
-    if constexpr (VEC) {
+    Vals<8> v[C];
+    if constexpr (F::RING) {
       copy_async_wait<STAGES - 2>();
 #pragma unroll
       for (int k = 0; k < C; ++k) v[k] = ring.get(k, stage);
@@ -98,21 +101,19 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, VEC>::BLO
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (has<VEC>(c, k, 0)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, v[k].p[i]);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (c.has(k, 2 * i / CT::GE)) s = __fadd2_rn(s, c.only(k, i, v[k].p[i]));
     const float own = warp_sum(s.x + s.y) * inv_n;
     float2 q = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (has<VEC>(c, k, 0)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 d = only<VEC>(c, k, i, __fadd2_rn(v[k].p[i], make_float2(-own, -own)));
+      for (int i = 0; i < 4; ++i)
+        if (c.has(k, 2 * i / CT::GE)) {
+          const float2 d = c.only(k, i, __fadd2_rn(v[k].p[i], make_float2(-own, -own)));
           q = __ffma2_rn(d, d, q);
         }
-      }
     float sq = warp_sum(q.x + q.y), mean = own;
     if constexpr (W > 1) {
       const float2 r = exchange.put_get(own, sq);
@@ -129,11 +130,11 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, VEC>::BLO
       const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        const Oct w = weight.get(c, k), b = bias.get(c, k);
+        const Vals<8> w = weight.get(c, k), b = bias.get(c, k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           v[k].p[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[k].p[i], m2), r2), w.p[i], b.p[i]);
-        store_chunk<YT, VEC>(y, c, k, v[k]);
+        store_chunk(y, c, k, v[k]);
       }
     }
     y += y_step;
@@ -173,54 +174,54 @@ __global__ void __launch_bounds__(LONG_THREADS) layernorm_forward_long_kernel(co
 
 // ------------------------------------------------------------------------------------------ host
 
-template <typename XT, typename YT, int C, int W, int R, bool VEC>
+template <typename XT, typename YT, int C, int W, int R, int MODE>
 cudaError_t forward_launch(const ForwardArgs &a, cudaStream_t s) {
-  using F = Forward<XT, YT, C, W, R, VEC>;
-  auto kernel = layernorm_forward_kernel<XT, YT, C, W, R, VEC>;
+  using F = Forward<XT, YT, C, W, R, MODE>;
+  auto kernel = layernorm_forward_kernel<XT, YT, C, W, R, MODE>;
   static const cudaError_t allowed = allow_shared(kernel);
   if (allowed != cudaSuccess) return allowed;
   const long long resident = std::max<long long>(1, std::min<long long>(F::BLOCKS, SM_SHARED / (F::BYTES + 2048)));
-  const dim3 grid(static_cast<unsigned>(std::min((a.N + R - 1) / R, device_sm_count() * resident)));
-  return launch_pdl(kernel, grid, dim3(F::THREADS), F::BYTES, s, a);
+  long long blocks = std::min((a.N + R - 1) / R, device_sm_count() * resident);
+  if (MODE == SHIFTED) blocks = (blocks + 7) / 8 * 8;   // a slot's rows lie multiples of eight apart
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(F::THREADS), F::BYTES, s, a);
 }
 
-// One chunk of eight columns per thread and several rows in a block up to 1024 columns; four chunks above, so that the
-// shuffles and the exchange of a row are shared by more columns (two without the vector path, whose rows wait in
-// registers).
+template <typename XT, typename YT, int MODE>
+cudaError_t forward_route_mode(const ForwardArgs &a, cudaStream_t s) {
+  // One chunk of eight columns per thread and several rows in a block up to 1024 columns; four chunks above, so that
+  // the shuffles and the exchange of a row are shared by more columns.
+  const bool short_row = a.D + (MODE == SHIFTED ? 7 : 0) <= 1024;
+  if (short_row) {
+    switch (warps_of(a.D, 1, static_cast<Mode>(MODE))) {
+      case 1: return forward_launch<XT, YT, 1, 1, 8, MODE>(a, s);
+      case 2: return forward_launch<XT, YT, 1, 2, 4, MODE>(a, s);
+      case 3: return forward_launch<XT, YT, 1, 3, 2, MODE>(a, s);
+      default: return forward_launch<XT, YT, 1, 4, 2, MODE>(a, s);
+    }
+  }
+  switch (warps_of(a.D, 4, static_cast<Mode>(MODE))) {
+    case 1:
+    case 2: return forward_launch<XT, YT, 4, 2, 1, MODE>(a, s);
+    case 3: return forward_launch<XT, YT, 4, 3, 1, MODE>(a, s);
+    case 4: return forward_launch<XT, YT, 4, 4, 1, MODE>(a, s);
+    case 6: return forward_launch<XT, YT, 4, 6, 1, MODE>(a, s);
+    case 8: return forward_launch<XT, YT, 4, 8, 1, MODE>(a, s);
+    case 12: return forward_launch<XT, YT, 4, 12, 1, MODE>(a, s);
+    default: return forward_launch<XT, YT, 4, 16, 1, MODE>(a, s);
+  }
+}
+
 template <typename XT, typename YT>
-cudaError_t forward_route(const ForwardArgs &a, bool vec, cudaStream_t s) {
-  if (a.D > MAX_ROW) {
+cudaError_t forward_route(const ForwardArgs &a, Mode mode, cudaStream_t s) {
+  if (a.D + (mode == SHIFTED ? 7 : 0) > MAX_ROW) {
     const dim3 grid(static_cast<unsigned>(std::min<long long>(a.N, device_sm_count() * 2))), block(LONG_THREADS);
     return launch_pdl(layernorm_forward_long_kernel<XT, YT>, grid, block, 0, s, a);
   }
-  if (a.D <= 1024) {
-    switch (warps_of(a.D, 1)) {
-      case 1: return vec ? forward_launch<XT, YT, 1, 1, 8, true>(a, s) : forward_launch<XT, YT, 1, 1, 8, false>(a, s);
-      case 2: return vec ? forward_launch<XT, YT, 1, 2, 4, true>(a, s) : forward_launch<XT, YT, 1, 2, 4, false>(a, s);
-      case 3: return vec ? forward_launch<XT, YT, 1, 3, 2, true>(a, s) : forward_launch<XT, YT, 1, 3, 2, false>(a, s);
-      default: return vec ? forward_launch<XT, YT, 1, 4, 2, true>(a, s) : forward_launch<XT, YT, 1, 4, 2, false>(a, s);
-    }
-  }
-  if (vec) {
-    switch (warps_of(a.D, 4)) {
-      case 2: return forward_launch<XT, YT, 4, 2, 1, true>(a, s);
-      case 3: return forward_launch<XT, YT, 4, 3, 1, true>(a, s);
-      case 4: return forward_launch<XT, YT, 4, 4, 1, true>(a, s);
-      case 6: return forward_launch<XT, YT, 4, 6, 1, true>(a, s);
-      case 8: return forward_launch<XT, YT, 4, 8, 1, true>(a, s);
-      case 12: return forward_launch<XT, YT, 4, 12, 1, true>(a, s);
-      default: return forward_launch<XT, YT, 4, 16, 1, true>(a, s);
-    }
-  }
-  switch (warps_of(a.D, 2)) {
-    case 3:
-    case 4: return forward_launch<XT, YT, 2, 4, 1, false>(a, s);
-    case 6:
-    case 8: return forward_launch<XT, YT, 2, 8, 1, false>(a, s);
-    case 12:
-    case 16: return forward_launch<XT, YT, 2, 16, 1, false>(a, s);
-    default: return forward_launch<XT, YT, 2, 32, 1, false>(a, s);
-  }
+  if (mode == ALIGNED) return forward_route_mode<XT, YT, ALIGNED>(a, s);
+  if (mode == SHIFTED) return forward_route_mode<XT, YT, SHIFTED>(a, s);
+  if (a.D <= 1024) return forward_launch<XT, YT, 1, 4, 2, SCALAR>(a, s);
+  if (a.D <= 8192) return forward_launch<XT, YT, 2, 16, 1, SCALAR>(a, s);
+  return forward_launch<XT, YT, 2, 32, 1, SCALAR>(a, s);
 }
 
 }  // namespace
@@ -244,16 +245,16 @@ muon_status layernorm_forward(const void *x, muon_dtype xdt, int64_t ldx, const 
   if ((st = device_check()) != MUON_OK) return st;
   if (N == 0) return MUON_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const ForwardArgs a{x, weight, bias, y, ldx, ldy, N, mean, rstd, eps, wdt, static_cast<int>(D)};
-  const bool vec = aligned16(x) && aligned16(y) && aligned16(weight) && aligned16(bias) && ldx % 8 == 0 && ldy % 8 == 0 &&
-                   D % 8 == 0;
+  const bool wide = aligned16(weight) && aligned16(bias);
+  const ForwardArgs a{x, weight, bias, y, ldx, ldy, N, mean, rstd, eps, wdt, wide ? 1 : 0, static_cast<int>(D)};
+  const Mode mode = mode_of(aligned16(x) && aligned16(y), (ldx - ldy) % 8 == 0, ldx, D);
   launch_begin(KK_LN_FWD, s);
   cudaError_t e;
   if (xdt == MUON_F32)
-    e = ydt == MUON_F32 ? forward_route<float, float>(a, vec, s) : forward_route<float, __nv_bfloat16>(a, vec, s);
+    e = ydt == MUON_F32 ? forward_route<float, float>(a, mode, s) : forward_route<float, __nv_bfloat16>(a, mode, s);
   else
-    e = ydt == MUON_F32 ? forward_route<__nv_bfloat16, float>(a, vec, s)
-                        : forward_route<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
+    e = ydt == MUON_F32 ? forward_route<__nv_bfloat16, float>(a, mode, s)
+                        : forward_route<__nv_bfloat16, __nv_bfloat16>(a, mode, s);
   launch_end(s);
   return status_of(e);
 }

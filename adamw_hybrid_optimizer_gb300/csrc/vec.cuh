@@ -63,58 +63,97 @@ __device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16 *p, lo
 __device__ __forceinline__ void store1(float *p, long long i, float v) { p[i] = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, long long i, float v) { p[i] = __float2bfloat16_rn(v); }
 
-// Eight values as four pairs: pairs go through the two-wide fp32 instructions.
-struct Oct {
-  float2 p[4];
-};
-
-// Eight values as they lie in memory.
-template <typename XT>
-struct Raw8 {
-  static constexpr int PIECES = sizeof(XT) / 2;   // 16-byte pieces
-  uint4 w[PIECES];
-  __device__ __forceinline__ Oct get() const {
-    Oct o;
-    if constexpr (sizeof(XT) == 4) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        o.p[2 * i] = make_float2(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
-        o.p[2 * i + 1] = make_float2(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
-      }
-    } else {
-      const unsigned u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o.p[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
-    }
-    return o;
-  }
-  __device__ __forceinline__ void load(const XT *p) {
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
-  }
-  __device__ __forceinline__ void set(const XT *f) {
-    if constexpr (sizeof(XT) == 4) {
-      const unsigned *u = reinterpret_cast<const unsigned *>(f);
-      w[0] = make_uint4(u[0], u[1], u[2], u[3]);
-      w[PIECES - 1] = make_uint4(u[4], u[5], u[6], u[7]);
-    } else {
-      const unsigned short *h = reinterpret_cast<const unsigned short *>(f);
-      w[0] = make_uint4(h[0] | (static_cast<unsigned>(h[1]) << 16), h[2] | (static_cast<unsigned>(h[3]) << 16),
-                        h[4] | (static_cast<unsigned>(h[5]) << 16), h[6] | (static_cast<unsigned>(h[7]) << 16));
-    }
-  }
+// N values as pairs: pairs go through the two-wide fp32 instructions.
+template <int N>
+struct Vals {
+  float2 p[N / 2];
 };
 
 template <typename T>
-__device__ __forceinline__ void store_oct(T *p, const Oct &o) {
-  const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
-  store8(p, f);
+__device__ __forceinline__ T bits_to(unsigned u);
+template <>
+__device__ __forceinline__ float bits_to<float>(unsigned u) { return __uint_as_float(u); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 bits_to<__nv_bfloat16>(unsigned u) {
+  return __ushort_as_bfloat16(static_cast<unsigned short>(u));
 }
 
-// Asynchronous copies to shared memory, 16 bytes each.
-__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// N values as they lie in memory, read and written as one access of 8 or 16 bytes (or two of 16).
+template <typename T, int N>
+struct Raw {
+  static constexpr int BYTES = N * sizeof(T), WORDS = BYTES / 4;
+  unsigned w[WORDS];
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (BYTES == 8) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(p);
+      w[0] = u.x, w[1] = u.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T *p) const {
+    if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i)
+        reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+  // value e from its bits (the low 16 of a bf16), e ascending from an all-zero start
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void put(int e, T x) {
+    if constexpr (sizeof(T) == 4) {
+      w[e] = __float_as_uint(x);
+    } else {
+      const unsigned u = __bfloat16_as_ushort(x);
+      w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | (u << 16) : (w[e / 2] & 0xffff0000u) | u;
+    }
+  }
+  __device__ __forceinline__ Vals<N> get() const {
+    Vals<N> o;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (sizeof(T) == 4) o.p[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      else o.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    return o;
+  }
+  __device__ __forceinline__ void from(const Vals<N> &o) {   // rounds to nearest
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[2 * i] = __float_as_uint(o.p[i].x);
+        w[2 * i + 1] = __float_as_uint(o.p[i].y);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(o.p[i].x, o.p[i].y);
+        w[i] = *reinterpret_cast<const unsigned *>(&h);
+      }
+    }
+  }
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void store_vals(T *p, const Vals<N> &o) {
+  Raw<T, N> r;
+  r.from(o);
+  r.store(p);
+}
+
+// Asynchronous copies to shared memory, of 8 or 16 bytes.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

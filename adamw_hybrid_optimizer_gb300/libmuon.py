@@ -371,6 +371,14 @@ def ns_apply(h, x, out, ws, stream=None):
 # ------------------------------------------------------------------------------------------------------------
 
 
+def _current_stream(stream) -> int:
+    """_stream, without building a stream object for the current one (most of the binding's time otherwise)."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _itype_code(t) -> int:
     import torch
     if t.dtype == torch.int32:
@@ -408,7 +416,7 @@ def embedding_forward(ids, table, out, scale: float = 1.0, stream=None):
     ldo = _matrix(out, "out", "embedding_forward", (n, D))
     st = lib().embedding_forward(_vector(ids, "ids", "embedding_forward", n), _itype_code(ids), table.data_ptr(),
                                  _dtype_code(table), ldt, out.data_ptr(), _dtype_code(out), ldo, n, V, D, scale,
-                                 _stream(stream))
+                                 _current_stream(stream))
     _check(st, "embedding_forward")
 
 
@@ -425,7 +433,7 @@ def embedding_backward(ids, dout, dtable, ws, scale: float = 1.0, padding_idx: i
     st = lib().embedding_backward(_vector(ids, "ids", "embedding_backward", n), _itype_code(ids), dout.data_ptr(),
                                   _dtype_code(dout), ldo, dtable.data_ptr(), _dtype_code(dtable), ldg, n, V, D, scale,
                                   padding_idx, int(bool(accumulate)), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                  _stream(stream))
+                                  _current_stream(stream))
     _check(st, "embedding_backward")
 
 
@@ -442,7 +450,7 @@ def layernorm_forward(x, weight, bias, y, mean, rstd, eps: float = 1e-5, stream=
                                  _vector(bias, "bias", "layernorm_forward", D), wdt, y.data_ptr(), _dtype_code(y), ldy,
                                  _vector(mean, "mean", "layernorm_forward", N, torch.float32),
                                  _vector(rstd, "rstd", "layernorm_forward", N, torch.float32), N, D, eps,
-                                 _stream(stream))
+                                 _current_stream(stream))
     _check(st, "layernorm_forward")
 
 
@@ -475,7 +483,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, accumu
                                   _vector(dweight, "dweight", where, D), _vector(dbias, "dbias", where, D),
                                   _dtype_code(g) if g is not None else MUON_F32, int(bool(accumulate)), N, D,
                                   ws.data_ptr() if ws is not None else None,
-                                  ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream))
+                                  ws.numel() * ws.element_size() if ws is not None else 0, _current_stream(stream))
     _check(st, where)
 
 
@@ -499,7 +507,7 @@ def distill_forward(logits, t_idx, t_val, temperature: float, weights, losses, s
     import torch
     N, V, K, head, st_ptr = _distill("distill_forward", logits, t_idx, t_val, weights, stats)
     st = lib().distill_forward(*head, _vector(losses, "losses", "distill_forward", N, torch.float32), st_ptr, N, V, K,
-                               temperature, _stream(stream))
+                               temperature, _current_stream(stream))
     _check(st, "distill_forward")
 
 
@@ -509,7 +517,7 @@ def distill_backward(logits, t_idx, t_val, temperature: float, weights, stats, g
     N, V, K, head, st_ptr = _distill("distill_backward", logits, t_idx, t_val, weights, stats)
     ldd = _matrix(dlogits, "dlogits", "distill_backward", (N, V))
     st = lib().distill_backward(*head, st_ptr, _vector(grad, "grad", "distill_backward", N, torch.float32),
-                                dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature, _stream(stream))
+                                dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature, _current_stream(stream))
     _check(st, "distill_backward")
 
 
@@ -522,7 +530,7 @@ def distill_forward_backward(logits, t_idx, t_val, temperature: float, weights, 
     ldd = _matrix(dlogits, "dlogits", where, (N, V))
     st = lib().distill_forward_backward(*head, grad_scale, _vector(losses, "losses", where, N, torch.float32), st_ptr,
                                         dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature,
-                                        _stream(stream))
+                                        _current_stream(stream))
     _check(st, where)
 
 

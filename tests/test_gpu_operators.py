@@ -67,7 +67,8 @@ def byte_ws(n):
 # n, V, D: none; one; odd widths on either side of a warp's 256 and 1024 columns; a few ids that fill many groups of
 # 32 sorted positions; a vocabulary of three digits; runs that end on group boundaries
 EMBED = [(0, 7, 5), (1, 1, 1), (3, 5, 7), (33, 10, 256), (65, 2, 40), (257, 50, 300), (1000, 3, 776), (5000, 17, 24),
-         (4097, 600, 130), (70000, 40, 8), (9000, 300000, 16), (8192, 1000, 1030), (96, 1, 64), (140000, 900, 8)]
+         (4097, 600, 130), (70000, 40, 8), (9000, 300000, 16), (8192, 1000, 1030), (96, 1, 64), (140000, 900, 8), (100000, 5000, 72),
+         (600, 90, 133), (3000, 40, 1337)]
 
 
 def make_ids(n, V, seed, it):
@@ -153,7 +154,7 @@ def test_embedding_rows_past_32_bit_offsets(L):
 # ------------------------------------------------------------------------------------------------ layer norm
 
 # widths on either side of every layout's limit, odd ones, one column, one row, and rows too long for registers
-LN = [(0, 16), (1, 1), (5, 7), (9, 255), (4, 256), (33, 300), (17, 512), (300, 768), (13, 769), (70, 1000), (8, 1023),
+LN = [(0, 16), (2, 9), (37, 1021), (9, 1030), (700, 771), (12, 8190), (10, 12001), (6, 16380), (1, 1), (5, 7), (9, 255), (4, 256), (33, 300), (17, 512), (300, 768), (13, 769), (70, 1000), (8, 1023),
       (6, 1024), (11, 1025), (5, 2048), (21, 3000), (40, 4096), (3, 4097), (5, 8192), (3, 10007), (4, 16384),
       (3, 16385), (5, 20000), (2, 65537)]
 K_LN = 128 * U
