@@ -9,22 +9,21 @@
 // A row of weight 0, or without a valid entry, has loss 0 and gradient 0, and its logits are not used. m and l are
 // kept apart (stats), so that p = exp((z - m) / T - l) keeps its precision for logits of any size. All three forms
 // are bound by bandwidth: forward reads the logits once, with a running maximum and sum; backward reads them once
-// and writes the gradient; the joint form keeps a row in shared memory between its two passes.
+// and writes the gradient; the joint form reads a row twice, the second time from L2, and there are no more rows on
+// their way at once than L2 holds.
 //
-// A row is cut into granules of eight logits on 16-byte boundaries of memory: a row whose start is not on one (an odd
-// vocabulary) has a short granule at each end, and everything between is whole vectors.
+// A row is cut into granules of eight logits (four where a matrix is fp32) on boundaries of memory: a row whose start
+// is not on one (an odd vocabulary) has a short granule at each end, and everything between is whole vectors.
 //
-//   distill_forward_kernel   a cluster of 1 to 8 blocks per row, each with a slice of it: few rows still fill the GPU
-//   distill_backward_kernel  a block per row and slice
-//   distill_joint_kernel     a cluster per row, the slices in shared memory; while a thread writes the gradient of a
-//                            granule it starts the copy of the next row's granule into the same place
-//   distill_reread_kernel    the joint form for rows that do not fit: a block per row, which reads it twice
+//   distill_forward_kernel   losses and stats: a block per row, or a cluster of 2 to 8 where there are few rows
+//   distill_backward_kernel  the gradient: a block per row and slice of a row
+//   distill_joint_kernel     both: blocks and clusters as in the forward kernel
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
-#include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -33,8 +32,6 @@
 namespace muon {
 namespace {
 
-constexpr int THREADS = 512;
-constexpr int WARPS = THREADS / 32;
 constexpr int MAX_K = 1024;
 constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -78,9 +75,11 @@ __device__ __forceinline__ Soft merge(const Soft &a, const Soft &b, float c) {
   return {m, fmaf(a.s, exp_scaled(a.m - ref, c), b.s * exp_scaled(b.m - ref, c))};
 }
 
+// Over all lanes, or over groups of LANES that hold copies of the same values.
+template <int LANES>
 __device__ __forceinline__ Soft warp_merge(Soft a, float c) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = LANES / 2; o > 0; o >>= 1)
     a = merge(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, c);
   return a;
 }
@@ -89,10 +88,12 @@ __device__ __forceinline__ Soft warp_merge(Soft a, float c) {
 struct Run {
   float m = -INFINITY;
   float2 s = {0.f, 0.f};
-  // Eight logits; a granule of -inf leaves the sum alone.
-  __device__ __forceinline__ void add(const Vals<8> &o, float c) {
-    const float mx = fmaxf(fmaxf(fmaxf(o.p[0].x, o.p[0].y), fmaxf(o.p[1].x, o.p[1].y)),
-                           fmaxf(fmaxf(o.p[2].x, o.p[2].y), fmaxf(o.p[3].x, o.p[3].y)));
+  // A granule of -inf leaves the sum alone.
+  template <int N>
+  __device__ __forceinline__ void add(const Vals<N> &o, float c) {
+    float mx = fmaxf(o.p[0].x, o.p[0].y);
+#pragma unroll
+    for (int i = 1; i < N / 2; ++i) mx = fmaxf(mx, fmaxf(o.p[i].x, o.p[i].y));
     if (mx > m) {
       const float f = exp_scaled(m - mx, c);
       s = __fmul2_rn(s, make_float2(f, f));
@@ -100,48 +101,50 @@ struct Run {
     }
     const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, exp2_scaled(o.p[i], ref, c));
+    for (int i = 0; i < N / 2; ++i) s = __fadd2_rn(s, exp2_scaled(o.p[i], ref, c));
   }
   __device__ __forceinline__ Soft soft() const { return {m, s.x + s.y}; }
 };
 
-// si * exp((z - m) / T) of eight logits
-__device__ __forceinline__ Vals<8> grad_of(Vals<8> o, float m, float c, float si) {
+// si * exp((z - m) / T)
+template <int N>
+__device__ __forceinline__ Vals<N> grad_of(Vals<N> o, float m, float c, float si) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o.p[i] = __fmul2_rn(exp2_scaled(o.p[i], m, c), make_float2(si, si));
+  for (int i = 0; i < N / 2; ++i) o.p[i] = __fmul2_rn(exp2_scaled(o.p[i], m, c), make_float2(si, si));
   return o;
 }
 
 // ------------------------------------------------------------------------------------------ granules
 
-// Granules of one row. VEC: granule g holds logits 8 g - shift + e, where shift is the row's start past a boundary
-// (the same for z and dz, whose pitches differ by a multiple of eight); otherwise shift is 0 and every access is
-// of one element. All granules but the first and the last (the edges) are whole.
+template <typename A, typename B>
+constexpr int granule_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
+
+// Granules of GE logits of one row. VEC: granule g holds logits GE g - shift + e, where shift is the row's start past a
+// boundary (the same for z and dz, whose pitches differ by a multiple of eight); otherwise shift is 0 and every access
+// is of one element. All granules but the first and the last (the edges) are whole.
+template <int GE>
 struct Granules {
   int shift, count, V;
-  __device__ __forceinline__ int first(int g) const { return 8 * g - shift; }
-  __device__ __forceinline__ bool has(int g, int e) const {
-    return first(g) + e >= 0 && first(g) + e < V;
-  }
-  __device__ __forceinline__ bool whole(int g) const { return first(g) >= 0 && first(g) + 8 <= V; }
+  __device__ __forceinline__ int first(int g) const { return GE * g - shift; }
+  __device__ __forceinline__ bool has(int g, int e) const { return first(g) + e >= 0 && first(g) + e < V; }
 };
 
-template <bool VEC>
-__device__ __forceinline__ Granules granules(long long row, long long ld, int V) {
-  const int shift = VEC ? static_cast<int>((row * ld) & 7) : 0;
-  return {shift, (V + shift + 7) / 8, V};
+template <int GE, bool VEC>
+__device__ __forceinline__ Granules<GE> granules(long long row, long long ld, int V) {
+  const int shift = VEC ? static_cast<int>((row * ld) & (GE - 1)) : 0;
+  return {shift, (V + shift + GE - 1) / GE, V};
 }
 
 // The part of a row that block `rank` of `slices` has: granules [g0, g1), of which [inner, inner + n) are not edges.
-// Inner granule inner + i belongs to thread i mod THREADS; the row's first edge to thread HEAD and its last to thread
-// TAIL, of two warps.
+// Inner granule inner + i belongs to thread i mod TH; the row's first edge to thread HEAD and its last to thread TAIL.
 struct Slice {
   int g0, g1, inner, n;
   bool head, tail;
 };
-constexpr int HEAD = 0, TAIL = 32;
+constexpr int HEAD = 0, TAIL = 16;
 
-__device__ __forceinline__ Slice slice_of(const Granules &G, int rank, int slices) {
+template <int GE>
+__device__ __forceinline__ Slice slice_of(const Granules<GE> &G, int rank, int slices) {
   Slice s;
   s.g0 = static_cast<int>(static_cast<long long>(G.count) * rank / slices);
   s.g1 = static_cast<int>(static_cast<long long>(G.count) * (rank + 1) / slices);
@@ -159,71 +162,67 @@ __device__ __forceinline__ float neg_inf<float>() { return -INFINITY; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 neg_inf<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff80); }
 
-// Places that the row does not have read as -inf.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_granule(const T *p, const Granules &G, int g, Raw<T, 8> &r) {
-  if (VEC && G.whole(g)) {
-    r.load(p + G.first(g));
-    return;
-  }
+// Element by element; places that the row does not have read as -inf.
+template <typename T, int GE>
+__device__ __forceinline__ void load_values(const T *p, const Granules<GE> &G, int g, Raw<T, GE> &r) {
   r.clear();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r.put(e, G.has(g, e) ? p[G.first(g) + e] : neg_inf<T>());
+  for (int e = 0; e < GE; ++e) r.put(e, G.has(g, e) ? p[G.first(g) + e] : neg_inf<T>());
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_granule(T *p, const Granules &G, int g, const Vals<8> &o) {
-  if (VEC && G.whole(g)) {
-    store_vals(p + G.first(g), o);
-    return;
+template <typename T, int GE>
+__device__ __forceinline__ void store_values(T *p, const Granules<GE> &G, int g, const Vals<GE> &o) {
+#pragma unroll
+  for (int e = 0; e < GE; ++e)
+    if (G.has(g, e)) store1(p, G.first(g) + e, e % 2 ? o.p[e / 2].y : o.p[e / 2].x);
+}
+
+template <typename DT, int GE, int TH, bool VEC>
+__device__ __forceinline__ void zero_granules(DT *dz, const Granules<GE> &G, const Slice &S) {
+  Vals<GE> o;
+#pragma unroll
+  for (int i = 0; i < GE / 2; ++i) o.p[i] = make_float2(0.f, 0.f);
+  for (int i = threadIdx.x; i < S.n; i += TH) {
+    if constexpr (VEC) store_vals(dz + G.first(S.inner + i), o);
+    else store_values(dz, G, S.inner + i, o);
   }
-  const float f[8] = {o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y, o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (G.has(g, e)) store1(p, G.first(g) + e, f[e]);
+  if (S.head && threadIdx.x == HEAD) store_values(dz, G, 0, o);
+  if (S.tail && threadIdx.x == TAIL) store_values(dz, G, G.count - 1, o);
 }
 
-template <typename DT, bool VEC>
-__device__ __forceinline__ void zero_granules(DT *dz, const Granules &G, const Slice &S) {
-  Vals<8> o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o.p[i] = make_float2(0.f, 0.f);
-  for (int g = S.g0 + threadIdx.x; g < S.g1; g += THREADS) store_granule<DT, VEC>(dz, G, g, o);
-}
-
-// A thread's granules of a slice, in batches: while one is used the loads of the next are in flight. run calls
+// A thread's granules of a slice, in batches: while one is used the loads of the next are in flight. run() calls
 // inner(i, values) and edge(g, values).
-template <typename ZT, bool VEC>
+template <typename ZT, int GE, int TH, bool VEC>
 struct Stream {
-  static constexpr int U = sizeof(ZT) == 2 ? 4 : 2;
-  const ZT *z;
-  const ZT *next;   // of the thread's next batch to fetch
-  const Granules &G;
+  static constexpr int U = 64 / (GE * static_cast<int>(sizeof(ZT)));   // 64 bytes to a batch
+  const ZT *z, *next;   // the row; the thread's next batch to fetch
+  const Granules<GE> &G;
   const Slice &S;
   int fetched, used;
-  Raw<ZT, 8> a[U], b[U], e;
-  __device__ __forceinline__ void fetch(Raw<ZT, 8> *r) {
+  Raw<ZT, GE> a[U], b[U], e;
+  __device__ __forceinline__ void fetch(Raw<ZT, GE> *r) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (fetched + u * THREADS < S.n) {
-        if constexpr (VEC) r[u].load(next + u * THREADS * 8);
-        else load_granule<ZT, false>(z, G, S.inner + fetched + u * THREADS, r[u]);
+      if (fetched + u * TH < S.n) {
+        if constexpr (VEC) r[u].load(next + u * TH * GE);
+        else load_values(z, G, S.inner + fetched + u * TH, r[u]);
       }
-    fetched += U * THREADS;
-    next += U * THREADS * 8;
+    fetched += U * TH;
+    next += U * TH * GE;
   }
-  __device__ __forceinline__ Stream(const ZT *z_, const Granules &G_, const Slice &S_)
-      : z(z_), next(z_ + G_.first(S_.inner) + 8 * threadIdx.x), G(G_), S(S_), fetched(threadIdx.x), used(threadIdx.x) {
-    if (S.head && threadIdx.x == HEAD) load_granule<ZT, false>(z, G, 0, e);
-    if (S.tail && threadIdx.x == TAIL) load_granule<ZT, false>(z, G, G.count - 1, e);
+  __device__ __forceinline__ Stream(const ZT *z_, const Granules<GE> &G_, const Slice &S_)
+      : z(z_), next(z_ + G_.first(S_.inner) + GE * static_cast<int>(threadIdx.x)), G(G_), S(S_),
+        fetched(threadIdx.x), used(threadIdx.x) {
+    if (S.head && threadIdx.x == HEAD) load_values(z, G, 0, e);
+    if (S.tail && threadIdx.x == TAIL) load_values(z, G, G.count - 1, e);
     fetch(a);
   }
   template <typename F>
-  __device__ __forceinline__ void use(const Raw<ZT, 8> *r, F &&inner) {
+  __device__ __forceinline__ void use(const Raw<ZT, GE> *r, F &&inner) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (used + u * THREADS < S.n) inner(used + u * THREADS, r[u].get());
-    used += U * THREADS;
+      if (used + u * TH < S.n) inner(used + u * TH, r[u].get());
+    used += U * TH;
   }
   template <typename F, typename E>
   __device__ __forceinline__ void run(F &&inner, E &&edge) {
@@ -236,6 +235,17 @@ struct Stream {
     }
     if (S.head && threadIdx.x == HEAD) edge(0, e.get());
     if (S.tail && threadIdx.x == TAIL) edge(G.count - 1, e.get());
+  }
+  // si * exp((z - m) / T) to dz
+  template <typename DT>
+  __device__ __forceinline__ void write_grad(DT *dz, float m, float c, float si) {
+    DT *first = dz + G.first(S.inner);
+    run(
+        [&](int i, const Vals<GE> &o) {
+          if constexpr (VEC) store_vals(first + GE * i, grad_of(o, m, c, si));
+          else store_values(dz, G, S.inner + i, grad_of(o, m, c, si));
+        },
+        [&](int g, const Vals<GE> &o) { store_values(dz, G, g, grad_of(o, m, c, si)); });
   }
 };
 
@@ -289,47 +299,50 @@ __device__ __forceinline__ void put_entry(const Teacher &s, int k, const Entry &
 
 // A thread's first entry (k = threadIdx.x) is loaded ahead; the rest of a long list, and the padding that
 // subtract_teacher's vectors read, when the first is put.
-template <typename ZT, bool ALL>
+template <typename ZT, int TH, bool ALL>
 __device__ __forceinline__ Soft put_teacher(const DistillArgs &a, long long row, const ZT *z, const Teacher &s, int lo,
                                             int hi, float c, const Entry &ahead) {
   Soft sum{-INFINITY, 0.f};
   if (static_cast<int>(threadIdx.x) < a.K) put_entry(s, threadIdx.x, ahead, c, sum);
-  for (int k = THREADS + threadIdx.x; k < a.K; k += THREADS) {
+  for (int k = TH + threadIdx.x; k < a.K; k += TH) {
     Entry e = load_entry(a, row, k);
     e.z = entry_logit<ZT, ALL>(e, z, lo, hi);
     put_entry(s, k, e, c, sum);
   }
-  for (int k = a.K + threadIdx.x; k < ((a.K + 3) & ~3); k += THREADS) s.idx[k] = -1;
+  for (int k = a.K + threadIdx.x; k < ((a.K + 3) & ~3); k += TH) s.idx[k] = -1;
   return sum;
 }
 
-// One exchange for the student's and the teacher's sums: every warp puts its pair, and after one barrier every warp
-// merges all of them. Calls alternate between two buffers.
+// What a block's warps exchange.
+template <int TH>
 struct BlockRed {
-  float4 buf[2][WARPS];
-  float loss[2][WARPS];
+  float4 sums[TH / 32];
+  float loss[TH / 32];
 };
 
-// A thread can write a buffer again only after the barrier of the call in between, which every reader of that buffer
-// has reached.
-__device__ __forceinline__ void merge_all(BlockRed &r, int turn, float c, Soft &student, Soft &teacher) {
-  student = warp_merge(student, c);
-  teacher = warp_merge(teacher, c);
+// The student's and the teacher's sums in one exchange: every warp puts its pairs, and after one barrier every warp
+// merges all of them.
+template <int TH>
+__device__ __forceinline__ void merge_all(BlockRed<TH> &r, float c, Soft &student, Soft &teacher) {
+  student = warp_merge<32>(student, c);
+  teacher = warp_merge<32>(teacher, c);
   const int lane = threadIdx.x % 32;
-  if (lane == 0) r.buf[turn][threadIdx.x / 32] = make_float4(student.m, student.s, teacher.m, teacher.s);
+  if (lane == 0) r.sums[threadIdx.x / 32] = make_float4(student.m, student.s, teacher.m, teacher.s);
   __syncthreads();
-  const float4 v = lane < WARPS ? r.buf[turn][lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-  student = warp_merge({v.x, v.y}, c);
-  teacher = warp_merge({v.z, v.w}, c);
+  const float4 v = r.sums[lane % (TH / 32)];
+  student = warp_merge<TH / 32>({v.x, v.y}, c);
+  teacher = warp_merge<TH / 32>({v.z, v.w}, c);
 }
 
 // The thread's part of sum_k q_k (log q_k - (z_k - m) / T); an entry whose q is 0 adds nothing, whatever the student
 // gives it.
+template <int TH>
 __device__ __forceinline__ float loss_part(const DistillArgs &a, const Teacher &s, const Soft &teacher, float m,
                                            float c) {
+  if (static_cast<int>(threadIdx.x & ~31u) >= a.K) return 0.f;   // the whole warp
   const float tl = logf(teacher.s), tinv = 1.f / teacher.s;
   float part = 0.f;
-  for (int k = threadIdx.x; k < a.K; k += THREADS) {
+  for (int k = threadIdx.x; k < a.K; k += TH) {
     if (s.idx[k] < 0) continue;
     const float d = s.t[k] - teacher.m;
     const float q = exp_scaled(d, c) * tinv;
@@ -338,10 +351,12 @@ __device__ __forceinline__ float loss_part(const DistillArgs &a, const Teacher &
   return warp_sum(part);
 }
 
+template <int TH>
 __device__ __forceinline__ void store_loss(const DistillArgs &a, long long row, float w, const float *parts,
                                            const Soft &student) {
   float kl = 0.f;
-  for (int i = 0; i < WARPS; ++i) kl += parts[i];
+#pragma unroll
+  for (int i = 0; i < TH / 32; ++i) kl += parts[i];
   const float l = logf(student.s);
   a.losses[row] = w * a.temp * a.temp * (kl + l);
   a.stats[2 * row] = student.m;
@@ -356,11 +371,11 @@ __device__ __forceinline__ void store_nothing(const DistillArgs &a, long long ro
 
 // Where the p parts of columns [lo, hi) are written: the first entry of each index there subtracts the q of all
 // entries of that index.
-template <typename DT>
+template <int TH, typename DT>
 __device__ __forceinline__ void subtract_teacher(const DistillArgs &a, const Teacher &s, DT *dz, int lo, int hi,
                                                  float c, float m, float inv, float scale, const Soft &teacher) {
   const float tinv = 1.f / teacher.s;
-  for (int k = threadIdx.x; k < a.K; k += THREADS) {
+  for (int k = threadIdx.x; k < a.K; k += TH) {
     const int id = s.idx[k];
     if (id < lo || id >= hi) continue;   // absent entries are -1, below every lo
     bool first = true;
@@ -395,7 +410,7 @@ __device__ __forceinline__ float2 load_remote(const float2 *p, unsigned rank) {
 }
 
 // The student's sums of all slices of the row: every block puts its own and reads the others', in rank order, so that
-// all blocks get the same bits. `put` alternates between two places like the block's own exchange.
+// all blocks get the same bits. 
 __device__ __forceinline__ void merge_cluster(float2 *put, int blocks, float c, Soft &student) {
   if (threadIdx.x == 0) *put = make_float2(student.m, student.s);
   cluster_sync();
@@ -413,299 +428,142 @@ __device__ __forceinline__ float weight_of(const DistillArgs &a, long long row) 
   return a.weights != nullptr ? a.weights[row] : 1.f;
 }
 
-// dz of a slice without the q part: si * exp((z - m) / T).
-template <typename ZT, typename DT, bool VEC>
-__device__ __forceinline__ void write_grad(Stream<ZT, VEC> &stream, DT *dz, const Granules &G, const Slice &S, float m,
-                                           float c, float si) {
-  DT *inner = dz + G.first(S.inner);
-  stream.run(
-      [&](int i, const Vals<8> &o) {
-        if constexpr (VEC) store_vals(inner + 8 * i, grad_of(o, m, c, si));
-        else store_granule<DT, false>(dz, G, S.inner + i, grad_of(o, m, c, si));
-      },
-      [&](int g, const Vals<8> &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
-}
+// Blocks of a multiprocessor for TH threads, at 64 registers each.
+constexpr int blocks_of(int TH) { return std::min(32, 1024 / TH); }
 
-template <typename ZT, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) distill_forward_kernel(const DistillArgs a) {
+template <typename ZT, int TH, bool VEC>
+__global__ void __launch_bounds__(TH, blocks_of(TH)) distill_forward_kernel(const DistillArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
+  constexpr int GE = granule_of<ZT, ZT>();
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ BlockRed red;
+  __shared__ BlockRed<TH> red;
   __shared__ float2 put;
   const Teacher s = teacher_at(smem, a.K);
   const float c = a.inv_t * LOG2E;
-  const int slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t = threadIdx.x, slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long long row = blockIdx.x / slices;
   const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
-  const Granules G = granules<VEC>(row, a.ldz, a.V);
+  const Granules<GE> G = granules<GE, VEC>(row, a.ldz, a.V);
   const Slice S = slice_of(G, rank, slices);
-  const bool entry = rank == 0 && static_cast<int>(threadIdx.x) < a.K;
+  const bool entry = rank == 0 && t < a.K;
   const float w = weight_of(a, row);
   Entry e{};
-  if (entry) e = load_entry(a, row, threadIdx.x);
+  if (entry) e = load_entry(a, row, t);
   if (w == 0.f) {   // the same for the whole cluster
-    if (rank == 0 && threadIdx.x == 0) store_nothing(a, row);
+    if (rank == 0 && t == 0) store_nothing(a, row);
     return;
   }
-  Stream<ZT, VEC> stream(z, G, S);
+  Stream<ZT, GE, TH, VEC> stream(z, G, S);
   if (entry) e.z = entry_logit<ZT, true>(e, z, 0, 0);
   Run run;
-  auto add = [&](int, const Vals<8> &o) { run.add(o, c); };
+  auto add = [&](int, const Vals<GE> &o) { run.add(o, c); };
   stream.run(add, add);
   Soft student = run.soft(), teacher{-INFINITY, 0.f};
-  if (rank == 0) teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
-  merge_all(red, 0, c, student, teacher);
+  if (rank == 0) teacher = put_teacher<ZT, TH, true>(a, row, z, s, 0, 0, c, e);
+  merge_all<TH>(red, c, student, teacher);
   if (slices > 1) merge_cluster(&put, slices, c, student);
   if (rank == 0) {
     no_softmax(student);
-    const float part = loss_part(a, s, teacher, student.m, c);
-    if (threadIdx.x % 32 == 0) red.loss[0][threadIdx.x / 32] = part;
+    const float part = loss_part<TH>(a, s, teacher, student.m, c);
+    if (t % 32 == 0) red.loss[t / 32] = part;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (t == 0) {
       if (teacher.s == 0.f) store_nothing(a, row);
-      else store_loss(a, row, w, red.loss[0], student);
+      else store_loss<TH>(a, row, w, red.loss, student);
     }
   }
   if (slices > 1) cluster_sync();   // no block leaves while another reads its shared memory
 }
 
-template <typename ZT, typename DT, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) distill_backward_kernel(const DistillArgs a) {
+template <typename ZT, typename DT, int TH, bool VEC>
+__global__ void __launch_bounds__(TH, blocks_of(TH)) distill_backward_kernel(const DistillArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
+  constexpr int GE = granule_of<ZT, DT>();
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ BlockRed red;
+  __shared__ BlockRed<TH> red;
   const Teacher s = teacher_at(smem, a.K);
   const float c = a.inv_t * LOG2E;
+  const int t = threadIdx.x;
   const long long row = blockIdx.x / a.slices;
-  const int rank = static_cast<int>(blockIdx.x - row * a.slices);
   const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
   DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
-  const Granules G = granules<VEC>(row, a.ldz, a.V);
-  const Slice S = slice_of(G, rank, a.slices);
+  const Granules<GE> G = granules<GE, VEC>(row, a.ldz, a.V);
+  const Slice S = slice_of(G, static_cast<int>(blockIdx.x - row * a.slices), a.slices);
   const int lo = max(G.first(S.g0), 0), hi = min(G.first(S.g1), a.V);
   const float w = weight_of(a, row);
   Entry e{};
-  if (static_cast<int>(threadIdx.x) < a.K) e = load_entry(a, row, threadIdx.x);
+  if (t < a.K) e = load_entry(a, row, t);
   if (w == 0.f) {
-    zero_granules<DT, VEC>(dz, G, S);
+    zero_granules<DT, GE, TH, VEC>(dz, G, S);
     return;
   }
-  Stream<ZT, VEC> stream(z, G, S);
+  Stream<ZT, GE, TH, VEC> stream(z, G, S);
   const float m = a.stats[2 * row], l = a.stats[2 * row + 1], up = a.grad != nullptr ? a.grad[row] : 1.f;
-  if (static_cast<int>(threadIdx.x) < a.K) e.z = entry_logit<ZT, false>(e, z, lo, hi);
-  Soft teacher = put_teacher<ZT, false>(a, row, z, s, lo, hi, c, e), student{-INFINITY, 0.f};
-  merge_all(red, 0, c, student, teacher);   // its barrier also ends the reads of z that dz may overwrite
+  if (t < a.K) e.z = entry_logit<ZT, false>(e, z, lo, hi);
+  Soft teacher = put_teacher<ZT, TH, false>(a, row, z, s, lo, hi, c, e), student{-INFINITY, 0.f};
+  merge_all<TH>(red, c, student, teacher);   // its barrier also ends the reads of z that dz may overwrite
   if (teacher.s == 0.f) {
-    zero_granules<DT, VEC>(dz, G, S);
+    zero_granules<DT, GE, TH, VEC>(dz, G, S);
     return;
   }
   const float inv = expf(-l), scale = up * w * a.temp;
-  write_grad<ZT, DT, VEC>(stream, dz, G, S, m, c, scale * inv);
+  stream.write_grad(dz, m, c, scale * inv);
   __syncthreads();
-  subtract_teacher(a, s, dz, lo, hi, c, m, inv, scale, teacher);
+  subtract_teacher<TH>(a, s, dz, lo, hi, c, m, inv, scale, teacher);
 }
 
-// The joint form without room for the row: a block per row, whose second reading is left to L2.
-template <typename ZT, typename DT, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) distill_reread_kernel(const DistillArgs a) {
+template <typename ZT, typename DT, int TH, bool VEC>
+__global__ void __launch_bounds__(TH, blocks_of(TH)) distill_joint_kernel(const DistillArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
+  constexpr int GE = granule_of<ZT, DT>();
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ BlockRed red;
+  __shared__ BlockRed<TH> red;
+  __shared__ float2 put;
   const Teacher s = teacher_at(smem, a.K);
   const float c = a.inv_t * LOG2E;
-  const long long row = blockIdx.x;
+  const int t = threadIdx.x, slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const long long row = blockIdx.x / slices;
   const ZT *z = static_cast<const ZT *>(a.z) + row * a.ldz;
   DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
-  const Granules G = granules<VEC>(row, a.ldz, a.V);
-  const Slice S = slice_of(G, 0, 1);
+  const Granules<GE> G = granules<GE, VEC>(row, a.ldz, a.V);
+  const Slice S = slice_of(G, rank, slices);
   const float w = weight_of(a, row);
   Entry e{};
-  if (static_cast<int>(threadIdx.x) < a.K) e = load_entry(a, row, threadIdx.x);
-  if (w == 0.f) {
-    if (threadIdx.x == 0) store_nothing(a, row);
-    zero_granules<DT, VEC>(dz, G, S);
+  if (t < a.K) e = load_entry(a, row, t);
+  if (w == 0.f) {   // the same for the whole cluster
+    if (rank == 0 && t == 0) store_nothing(a, row);
+    zero_granules<DT, GE, TH, VEC>(dz, G, S);
     return;
   }
-  if (static_cast<int>(threadIdx.x) < a.K) e.z = entry_logit<ZT, true>(e, z, 0, 0);
   Run run;
   {
-    Stream<ZT, VEC> stream(z, G, S);
-    auto add = [&](int, const Vals<8> &o) { run.add(o, c); };
+    Stream<ZT, GE, TH, VEC> stream(z, G, S);
+    if (t < a.K) e.z = entry_logit<ZT, true>(e, z, 0, 0);
+    auto add = [&](int, const Vals<GE> &o) { run.add(o, c); };
     stream.run(add, add);
   }
-  Soft student = run.soft(), teacher = put_teacher<ZT, true>(a, row, z, s, 0, 0, c, e);
-  merge_all(red, 0, c, student, teacher);
+  // every block has all entries' logits before any block of the cluster writes its part of the gradient
+  Soft student = run.soft(), teacher = put_teacher<ZT, TH, true>(a, row, z, s, 0, 0, c, e);
+  merge_all<TH>(red, c, student, teacher);
+  if (slices > 1) merge_cluster(&put, slices, c, student);
   if (teacher.s == 0.f) {
-    if (threadIdx.x == 0) store_nothing(a, row);
-    zero_granules<DT, VEC>(dz, G, S);
-    return;
-  }
-  no_softmax(student);
-  const float part = loss_part(a, s, teacher, student.m, c);
-  if (threadIdx.x % 32 == 0) red.loss[0][threadIdx.x / 32] = part;
-  const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s;
-  Stream<ZT, VEC> stream(z, G, S);
-  write_grad<ZT, DT, VEC>(stream, dz, G, S, student.m, c, scale * inv);
-  __syncthreads();
-  if (threadIdx.x == 0) store_loss(a, row, w, red.loss[0], student);
-  subtract_teacher(a, s, dz, 0, a.V, c, student.m, inv, scale, teacher);
-}
-
-// ------------------------------------------------------------------------------------------ joint form
-
-// The slice in shared memory: inner granule i at place i, the row's first edge at place room - 2 and its last at
-// room - 1, in 16-byte pieces `room` apart, so that a warp's accesses to one piece are contiguous. Every place is
-// written and read by one thread only, so a thread's own wait is all the ordering it needs.
-template <typename ZT>
-struct Kept {
-  static constexpr int PIECES = static_cast<int>(sizeof(ZT)) / 2;
-  uint4 *base;
-  int room;
-  __device__ __forceinline__ void fetch(int at, const ZT *src) const {
-#pragma unroll
-    for (int p = 0; p < PIECES; ++p) copy_async<16>(base + p * room + at, reinterpret_cast<const uint4 *>(src) + p);
-  }
-  __device__ __forceinline__ Vals<8> get(int at) const {
-    Raw<ZT, 8> r;
-#pragma unroll
-    for (int p = 0; p < PIECES; ++p) {
-      const uint4 u = base[p * room + at];
-      r.w[4 * p] = u.x, r.w[4 * p + 1] = u.y, r.w[4 * p + 2] = u.z, r.w[4 * p + 3] = u.w;
-    }
-    return r.get();
-  }
-  // An edge that the row has only part of is copied whole where the rest of it lies in the rows around (V >= 8), whose
-  // values edge() leaves out; only the ends of the whole matrix are read element by element.
-  __device__ __forceinline__ void fetch_edges(const ZT *z, const Granules &G, const Slice &S, bool first_row,
-                                              bool last_row) const {
-    const bool head = S.head && threadIdx.x == HEAD;
-    if (!head && !(S.tail && threadIdx.x == TAIL)) return;
-    const int g = head ? 0 : G.count - 1, at = room - (head ? 2 : 1);
-    if ((G.first(g) >= 0 || !first_row) && (G.first(g) + 8 <= G.V || !last_row)) {
-      fetch(at, z + G.first(g));
-    } else {
-      Raw<ZT, 8> r;
-      load_granule<ZT, false>(z, G, g, r);
-#pragma unroll
-      for (int p = 0; p < PIECES; ++p)
-        base[p * room + at] = make_uint4(r.w[4 * p], r.w[4 * p + 1], r.w[4 * p + 2], r.w[4 * p + 3]);
-    }
-  }
-  // f(g, values) of the edges that are the thread's
-  template <typename F>
-  __device__ __forceinline__ void edges(const Granules &G, const Slice &S, F &&f) const {
-    const bool head = S.head && threadIdx.x == HEAD;
-    if (!head && !(S.tail && threadIdx.x == TAIL)) return;
-    const int g = head ? 0 : G.count - 1;
-    Vals<8> o = get(room - (head ? 2 : 1));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!G.has(g, 2 * i)) o.p[i].x = -INFINITY;
-      if (!G.has(g, 2 * i + 1)) o.p[i].y = -INFINITY;
-    }
-    f(g, o);
-  }
-};
-
-template <typename ZT, typename DT>
-__global__ void __launch_bounds__(THREADS, 2) distill_joint_kernel(const DistillArgs a, int room) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_launch_dependents();
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ BlockRed red;
-  __shared__ float2 put[2];
-  const Kept<ZT> kept{reinterpret_cast<uint4 *>(smem), room};
-  unsigned char *entries = smem + static_cast<size_t>(room) * sizeof(ZT) * 8;
-  const float c = a.inv_t * LOG2E;
-  const int slices = a.slices, rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const long long step = gridDim.x / slices;
-  long long row = blockIdx.x / slices;
-  int turn = 0;
-  const bool entry = static_cast<int>(threadIdx.x) < a.K;
-  const int t = threadIdx.x;
-  auto z_of = [&](long long r) { return static_cast<const ZT *>(a.z) + r * a.ldz; };
-  float w_next = weight_of(a, row);   // the grid has no more clusters than there are rows
-  Entry e_next{};
-  if (entry) e_next = load_entry(a, row, t);
-  Granules G_next = granules<true>(row, a.ldz, a.V);
-  Slice S_next = slice_of(G_next, rank, slices);
-  if (w_next != 0.f) {
-    const ZT *src = z_of(row) + G_next.first(S_next.inner) + 8 * t;
-    for (int i = t; i < S_next.n; i += THREADS, src += 8 * THREADS) kept.fetch(i, src);
-    kept.fetch_edges(z_of(row), G_next, S_next, row == 0, row + 1 == a.N);
-  }
-  copy_async_commit();
-  if (entry) e_next.z = entry_logit<ZT, true>(e_next, z_of(row), 0, 0);
-  for (; row < a.N; row += step) {
-    DT *dz = static_cast<DT *>(a.dz) + row * a.ldd;
-    const Granules G = G_next;
-    const Slice S = S_next;
-    const float w = w_next;
-    const Entry e = e_next;
-    // the next row: its weight and entries now, its logits and the entries' own as this one's gradient is written
-    const long long next = row + step;
-    const bool more = next < a.N;
-    if (more) {
-      w_next = weight_of(a, next);
-      if (entry) e_next = load_entry(a, next, t);
-    }
-    G_next = granules<true>(next, a.ldz, a.V);
-    S_next = slice_of(G_next, rank, slices);
-    const ZT *zn = z_of(next);
-    const bool used = w != 0.f;   // the same for the whole cluster
-    const Teacher s = teacher_at(entries + turn * teacher_bytes(a.K), a.K);
-    Soft teacher{-INFINITY, 0.f}, student{-INFINITY, 0.f};
-    if (used) {
-      Run run;
-      copy_async_wait<0>();
-#pragma unroll 2
-      for (int i = t; i < S.n; i += THREADS) run.add(kept.get(i), c);
-      kept.edges(G, S, [&](int, const Vals<8> &o) { run.add(o, c); });
-      student = run.soft();
-      teacher = put_teacher<ZT, true>(a, row, z_of(row), s, 0, 0, c, e);
-      merge_all(red, turn, c, student, teacher);
-      if (slices > 1) merge_cluster(&put[turn], slices, c, student);
-    }
-    const bool wanted = more && w_next != 0.f;
-    const int nn = wanted ? S_next.n : 0;
-    const ZT *src = zn + G_next.first(S_next.inner) + 8 * t;
-    if (more && entry) e_next.z = entry_logit<ZT, true>(e_next, zn, 0, 0);
-    if (!used || teacher.s == 0.f) {
-      if (rank == 0 && t == 0) store_nothing(a, row);
-      zero_granules<DT, true>(dz, G, S);
-      for (int i = t; i < nn; i += THREADS, src += 8 * THREADS) kept.fetch(i, src);
-      if (wanted) kept.fetch_edges(zn, G_next, S_next, false, next + 1 == a.N);
-      copy_async_commit();
-      if (used) turn ^= 1;
-      continue;
-    }
+    if (rank == 0 && t == 0) store_nothing(a, row);
+    zero_granules<DT, GE, TH, VEC>(dz, G, S);
+  } else {
     no_softmax(student);
+    Stream<ZT, GE, TH, VEC> stream(z, G, S);
     if (rank == 0) {
-      const float part = loss_part(a, s, teacher, student.m, c);
-      if (t % 32 == 0) red.loss[turn][t / 32] = part;
+      const float part = loss_part<TH>(a, s, teacher, student.m, c);
+      if (t % 32 == 0) red.loss[t / 32] = part;
     }
-    const float m = student.m, scale = a.grad_scale * w * a.temp, inv = 1.f / student.s, si = scale * inv;
-    // a granule's values have gone into the store when its place is given to the next row's
-    kept.edges(G, S, [&](int g, const Vals<8> &o) { store_granule<DT, false>(dz, G, g, grad_of(o, m, c, si)); });
-    if (wanted) kept.fetch_edges(zn, G_next, S_next, false, next + 1 == a.N);
-    DT *dst = dz + G.first(S.inner) + 8 * t;
-    int i = t;
-#pragma unroll 2
-    for (; i < min(S.n, nn); i += THREADS, src += 8 * THREADS, dst += 8 * THREADS) {
-      store_vals(dst, grad_of(kept.get(i), m, c, si));
-      kept.fetch(i, src);
-    }
-    for (int j = i; j < S.n; j += THREADS, dst += 8 * THREADS) store_vals(dst, grad_of(kept.get(j), m, c, si));
-    for (; i < nn; i += THREADS, src += 8 * THREADS) kept.fetch(i, src);
-    copy_async_commit();
-    // what follows may run beside the next row, which has its own half of everything shared
+    const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s;
+    stream.write_grad(dz, student.m, c, scale * inv);
     __syncthreads();
-    if (rank == 0 && t == 0) store_loss(a, row, w, red.loss[turn], student);
-    subtract_teacher(a, s, dz, max(G.first(S.g0), 0), min(G.first(S.g1), a.V), c, m, inv, scale, teacher);
-    turn ^= 1;
+    if (rank == 0 && t == 0) store_loss<TH>(a, row, w, red.loss, student);
+    subtract_teacher<TH>(a, s, dz, max(G.first(S.g0), 0), min(G.first(S.g1), a.V), c, student.m, inv, scale, teacher);
   }
   if (slices > 1) cluster_sync();   // no block leaves while another reads its shared memory
 }
@@ -753,11 +611,11 @@ DistillArgs distill_args(const void *logits, int64_t ldz, const void *t_idx, muo
 
 // A dependent launch of clusters of `cluster` blocks.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), long long blocks, int cluster, size_t smem, cudaStream_t s,
-                            Args &&...args) {
+cudaError_t launch_clusters(void (*kernel)(KArgs...), long long blocks, int threads, int cluster, size_t smem,
+                            cudaStream_t s, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -772,96 +630,70 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), long long blocks, int clus
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Blocks per row: as many as it takes to give every multiprocessor `per_sm` blocks, each with at least `least` logits.
-int row_slices(const DistillArgs &a, int per_sm, int least, int most) {
-  const long long want = static_cast<long long>(device_sm_count()) * per_sm;
+// Blocks per row: 1, or as many as it takes to give every multiprocessor its blocks, each with at least 4096 logits.
+int row_slices(const DistillArgs &a, int TH) {
+  const long long want = static_cast<long long>(device_sm_count()) * blocks_of(TH);
   int n = 1;
-  while (n < most && a.N * n < want && a.V / (2 * n) >= least) n *= 2;
+  while (n < MAX_CLUSTER && a.N * n < want && a.V / (2 * n) >= 4096) n *= 2;
   return n;
 }
 
-template <typename ZT>
-cudaError_t launch_fwd(DistillArgs a, bool vec, cudaStream_t s) {
-  a.slices = row_slices(a, 2, 4096, MAX_CLUSTER);
-  const size_t smem = teacher_bytes(a.K);
-  return vec ? launch_clusters(distill_forward_kernel<ZT, true>, a.N * a.slices, a.slices, smem, s, a)
-             : launch_clusters(distill_forward_kernel<ZT, false>, a.N * a.slices, a.slices, smem, s, a);
+// Threads of a row's block: a warp for short rows, whose time is the chain of their loads and exchanges, so that as many
+// rows as can be are on their way; 256 for long ones. (8192 x 50304 bf16, forward: 306, 186 and 145 us with 1024, 512 and
+// 256 threads.)
+int row_threads(int V) { return V < 4096 ? 32 : V < 16384 ? 128 : 256; }
+
+// The joint form's second reading wants a row still in L2 (129 MB, and its gradient goes there too): wider blocks, and
+// so fewer rows at once, for rows of more than 131072 and 262144 bytes. (4096 x 128256 bf16: 464, 426 and 453 us with
+// 256, 512 and 1024 threads; 2048 x 128256 fp32: 494, 460 and 425 us.)
+int joint_threads(int V, size_t row_bytes) {
+  return row_bytes <= 131072 ? row_threads(V) : row_bytes <= 270000 ? 512 : 1024;
 }
 
-template <typename ZT, typename DT>
-cudaError_t launch_bwd(DistillArgs a, bool vec, cudaStream_t s) {
-  // a block's start (its teacher entries) is paid back by some 32 Ki logits
-  a.slices = row_slices(a, 3, 4096, MAX_CLUSTER);
-  while (a.V / a.slices > 65536) a.slices *= 2;
-  const size_t smem = teacher_bytes(a.K);
-  const dim3 grid(static_cast<unsigned>(a.N * a.slices)), block(THREADS);
-  return vec ? launch_pdl(distill_backward_kernel<ZT, DT, true>, grid, block, smem, s, a)
-             : launch_pdl(distill_backward_kernel<ZT, DT, false>, grid, block, smem, s, a);
-}
-
-constexpr int SM_SHARED = 227 * 1024;          // what blocks of one multiprocessor can have together
-constexpr int BLOCK_SHARED = 2048;             // a block's static share and the system's, rounded up
-std::mutex g_joint_mu;
-
-// Clusters of this shape that the GPU holds at once (a persistent grid of more would leave the rest for last).
-template <typename ZT, typename DT>
-cudaError_t joint_clusters(int cluster, size_t smem, int *n) {
-  static int cached[MAX_CLUSTER + 1][3];       // by cluster size and blocks per multiprocessor; 0: not asked yet
-  auto kernel = distill_joint_kernel<ZT, DT>;
-  std::lock_guard<std::mutex> lk(g_joint_mu);
-  const int per_sm = static_cast<int>(std::min<size_t>(2, SM_SHARED / (smem + BLOCK_SHARED)));
-  int &c = cached[cluster][per_sm];
-  if (c == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SM_SHARED - BLOCK_SHARED);
-    if (e != cudaSuccess) return e;
-    if (cluster == 1) {
-      c = device_sm_count() * per_sm;
-    } else {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-      cfg.blockDim = dim3(THREADS);
-      cfg.dynamicSmemBytes = smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&c, kernel, &cfg);
-      if (e != cudaSuccess) {
-        c = 0;
-        return e;
-      }
-    }
+// f with the thread count as a type
+template <typename F>
+cudaError_t with_threads(int TH, F &&f) {
+  switch (TH) {
+    case 32: return f(std::integral_constant<int, 32>());
+    case 128: return f(std::integral_constant<int, 128>());
+    case 256: return f(std::integral_constant<int, 256>());
+    case 512: return f(std::integral_constant<int, 512>());
+    default: return f(std::integral_constant<int, 1024>());
   }
-  *n = std::max(1, c);
-  return cudaSuccess;
 }
 
-template <typename ZT, typename DT>
-cudaError_t launch_step(DistillArgs a, bool vec, cudaStream_t s) {
-  const size_t entries = teacher_bytes(a.K), both = 2 * entries;
-  // slices of at most half a multiprocessor's shared memory, or of all of it where eight of those are too few
-  const size_t granule = 8 * sizeof(ZT), granules = (static_cast<size_t>(a.V) + 7 + 7) / 8;
-  const size_t half = (SM_SHARED / 2 - BLOCK_SHARED - both) / granule, all = (SM_SHARED - BLOCK_SHARED - both) / granule;
-  int slices = row_slices(a, 2, 4096, MAX_CLUSTER);
-  // a slice's granules and two places for edges
-  while (slices < MAX_CLUSTER && (granules + slices - 1) / slices + 2 > half) ++slices;
-  const size_t room = (granules + slices - 1) / slices + 2;
-  if (!vec || room > all || a.V < 8) {
-    const dim3 grid(static_cast<unsigned>(a.N)), block(THREADS);
-    return vec ? launch_pdl(distill_reread_kernel<ZT, DT, true>, grid, block, entries, s, a)
-               : launch_pdl(distill_reread_kernel<ZT, DT, false>, grid, block, entries, s, a);
-  }
-  a.slices = slices;
-  const size_t smem = room * granule + both;
-  int clusters = 0;
-  const cudaError_t e = joint_clusters<ZT, DT>(slices, smem, &clusters);
-  if (e != cudaSuccess) return e;
-  return launch_clusters(distill_joint_kernel<ZT, DT>, std::min<long long>(a.N, clusters) * slices, slices, smem, s, a,
-                         static_cast<int>(room));
+template <typename ZT, bool VEC>
+cudaError_t launch_fwd(DistillArgs a, cudaStream_t s) {
+  return with_threads(row_threads(a.V), [&](auto th) {
+    constexpr int TH = std::min(256, decltype(th)::value);
+    a.slices = row_slices(a, TH);
+    return launch_clusters(distill_forward_kernel<ZT, TH, VEC>, a.N * a.slices, TH, a.slices, teacher_bytes(a.K), s, a);
+  });
+}
+
+template <typename ZT, typename DT, bool VEC>
+cudaError_t launch_bwd(DistillArgs a, cudaStream_t s) {
+  return with_threads(row_threads(a.V), [&](auto th) {
+    constexpr int TH = std::min(256, decltype(th)::value);
+    // slices of at most 65536 logits, so that the last blocks end close together
+    a.slices = row_slices(a, TH);
+    while (a.V / a.slices > 65536) a.slices *= 2;
+    return launch_pdl(distill_backward_kernel<ZT, DT, TH, VEC>, dim3(static_cast<unsigned>(a.N * a.slices)), dim3(TH),
+                      teacher_bytes(a.K), s, a);
+  });
+}
+
+template <typename ZT, typename DT, bool VEC>
+cudaError_t launch_step(DistillArgs a, cudaStream_t s) {
+  // where a cluster shares a row the blocks are as in the forward kernel
+  int threads = row_threads(a.V);
+  a.slices = row_slices(a, threads);
+  if (a.slices == 1) threads = joint_threads(a.V, static_cast<size_t>(a.V) * sizeof(ZT));
+  return with_threads(threads, [&](auto th) {
+    constexpr int TH = decltype(th)::value;
+    return launch_clusters(distill_joint_kernel<ZT, DT, TH, VEC>, a.N * a.slices, TH, a.slices, teacher_bytes(a.K), s,
+                           a);
+  });
 }
 
 }  // namespace
@@ -884,10 +716,10 @@ muon_status distill_forward(const void *logits, muon_dtype zdt, int64_t ldz, con
   DistillArgs a = distill_args(logits, ldz, t_idx, itype, t_val, tdt, weights, N, V, K, temperature);
   a.losses = losses;
   a.stats = stats;
-  const bool vec = aligned16(logits);
+  const bool vec = V >= 8 && aligned16(logits);
   launch_begin(KK_DISTILL_FWD, s);
-  const cudaError_t e = zdt == MUON_F32 ? launch_fwd<float>(a, vec, s)
-                                        : launch_fwd<__nv_bfloat16>(a, vec, s);
+  const cudaError_t e = zdt == MUON_F32 ? (vec ? launch_fwd<float, true>(a, s) : launch_fwd<float, false>(a, s))
+                                        : (vec ? launch_fwd<__nv_bfloat16, true>(a, s) : launch_fwd<__nv_bfloat16, false>(a, s));
   launch_end(s);
   return status_of(e);
 }
@@ -910,14 +742,16 @@ muon_status distill_backward(const void *logits, muon_dtype zdt, int64_t ldz, co
   a.grad = grad;
   a.dz = dlogits;
   a.ldd = ldd;
-  const bool vec = aligned16(logits) && aligned16(dlogits) && (ldz - ldd) % 8 == 0;
+  const bool vec = V >= 8 && aligned16(logits) && aligned16(dlogits) && (ldz - ldd) % 8 == 0;
   launch_begin(KK_DISTILL_BWD, s);
-  cudaError_t e;
-  if (zdt == MUON_F32)
-    e = ddt == MUON_F32 ? launch_bwd<float, float>(a, vec, s) : launch_bwd<float, __nv_bfloat16>(a, vec, s);
-  else
-    e = ddt == MUON_F32 ? launch_bwd<__nv_bfloat16, float>(a, vec, s)
-                        : launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
+  auto run = [&](auto z, auto d) {
+    using ZT = decltype(z);
+    using DT = decltype(d);
+    return vec ? launch_bwd<ZT, DT, true>(a, s) : launch_bwd<ZT, DT, false>(a, s);
+  };
+  const __nv_bfloat16 h{};
+  const cudaError_t e = zdt == MUON_F32 ? (ddt == MUON_F32 ? run(0.f, 0.f) : run(0.f, h))
+                                        : (ddt == MUON_F32 ? run(h, 0.f) : run(h, h));
   launch_end(s);
   return status_of(e);
 }
@@ -943,14 +777,16 @@ muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t
   a.dz = dlogits;
   a.ldd = ldd;
   a.grad_scale = grad_scale;
-  const bool vec = aligned16(logits) && aligned16(dlogits) && (ldz - ldd) % 8 == 0;
+  const bool vec = V >= 8 && aligned16(logits) && aligned16(dlogits) && (ldz - ldd) % 8 == 0;
   launch_begin(KK_DISTILL_STEP, s);
-  cudaError_t e;
-  if (zdt == MUON_F32)
-    e = ddt == MUON_F32 ? launch_step<float, float>(a, vec, s) : launch_step<float, __nv_bfloat16>(a, vec, s);
-  else
-    e = ddt == MUON_F32 ? launch_step<__nv_bfloat16, float>(a, vec, s)
-                        : launch_step<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
+  auto run = [&](auto z, auto d) {
+    using ZT = decltype(z);
+    using DT = decltype(d);
+    return vec ? launch_step<ZT, DT, true>(a, s) : launch_step<ZT, DT, false>(a, s);
+  };
+  const __nv_bfloat16 h{};
+  const cudaError_t e = zdt == MUON_F32 ? (ddt == MUON_F32 ? run(0.f, 0.f) : run(0.f, h))
+                                        : (ddt == MUON_F32 ? run(h, 0.f) : run(h, h));
   launch_end(s);
   return status_of(e);
 }
