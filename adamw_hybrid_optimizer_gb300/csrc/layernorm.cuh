@@ -28,10 +28,11 @@ __device__ __forceinline__ float param_at(const void *p, int dt, int c, float ab
 // How memory is accessed:
 //   SCALAR   one value at a time: bases or pitches that fit neither of the others
 //   ALIGNED  every row starts on a boundary of a granule, and the width is whole granules
+//   FULL     ALIGNED, and the row gives every thread all of its granules, so that nothing is asked
 //   SHIFTED  rows start `shift` values past a boundary (an odd width); the first and the last granule of a row may be
 //            partial. A row slot sees rows whose index differs by multiples of 8, which all have the same shift, so
 //            its threads' columns stay the same.
-enum Mode { SCALAR, ALIGNED, SHIFTED };
+enum Mode { SCALAR, ALIGNED, SHIFTED, FULL };
 
 // A granule is 8 values of bf16 or, where a matrix is fp32, 4: an access of one is 16 (8 for bf16 beside fp32) bytes,
 // next to the neighbouring thread's.
@@ -43,22 +44,26 @@ constexpr int granule_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
 template <int MODE_, int GE_, int T_>
 struct Cols {
   static constexpr int MODE = MODE_, GE = MODE_ == SCALAR ? 8 : GE_, PG = 8 / GE, T = T_;
-  int t, D, shift, total, mine;   // total: the row's granules; mine: the thread's (SCALAR: its columns)
+  int t, D, shift, total, mine, last;   // total: the row's granules; mine: the thread's (SCALAR: its columns); last: the
+                                        // row's last granule as the thread's k PG + j, or -1
   __device__ __forceinline__ Cols(int t_, int D_, int shift_) : t(t_), D(D_), shift(MODE == SHIFTED ? shift_ : 0) {
     total = MODE == SCALAR ? D : (D + shift + GE - 1) / GE;
     mine = max((total - t + T - 1) / T, 0);
+    last = (total - 1) % T == t ? (total - 1) / T : -1;
   }
   __device__ __forceinline__ int granule(int k, int j) const { return (k * PG + j) * T + t; }
   __device__ __forceinline__ int first(int k, int j) const { return granule(k, j) * GE - shift; }
   __device__ __forceinline__ int col(int k, int e) const {
     return MODE == SCALAR ? (8 * k + e) * T + t : first(k, e / GE) + e % GE;
   }
-  __device__ __forceinline__ bool has(int k, int j) const { return (MODE == SCALAR ? 8 * k : k * PG + j) < mine; }
+  __device__ __forceinline__ bool has(int k, int j) const {
+    return MODE == FULL || (MODE == SCALAR ? 8 * k : k * PG + j) < mine;
+  }
   __device__ __forceinline__ bool edge(int k, int j) const {
-    return MODE == SHIFTED && (granule(k, j) == 0 || granule(k, j) == total - 1);
+    return MODE == SHIFTED && ((k == 0 && j == 0 && t == 0) || k * PG + j == last);
   }
   __device__ __forceinline__ bool in(int k, int e) const {   // of a granule that the thread has
-    return MODE == SCALAR ? 8 * k + e < mine : MODE == ALIGNED || (col(k, e) >= 0 && col(k, e) < D);
+    return MODE == SCALAR ? 8 * k + e < mine : MODE != SHIFTED || (col(k, e) >= 0 && col(k, e) < D);
   }
   // pair i of chunk k with zeros where the row has no column; its granule is there
   __device__ __forceinline__ float2 only(int k, int i, float2 v) const {
@@ -73,7 +78,7 @@ struct Cols {
     int n = mine * GE;
     if (MODE == SHIFTED && mine > 0) {
       if (t == 0) n -= shift;
-      if ((total - 1) % T == t) n -= total * GE - shift - D;
+      if (last >= 0) n -= total * GE - shift - D;
     }
     return n;
   }
@@ -149,7 +154,7 @@ __device__ __forceinline__ void store_chunk(XT *p, const CT &c, int k, const Val
 // fp32 sums of the thread's columns to a row that starts on a boundary itself
 template <typename CT>
 __device__ __forceinline__ void store_sums(float *p, const CT &c, int k, const Vals<8> &o) {
-  if (CT::MODE == ALIGNED) {
+  if (CT::MODE == ALIGNED || CT::MODE == FULL) {
     store_chunk(p, c, k, o);
     return;
   }
@@ -165,7 +170,7 @@ __device__ __forceinline__ Vals<8> param_chunk(const void *p, int dt, bool wide,
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.p[i] = make_float2(absent, absent);
   if (p == nullptr) return o;
-  if (CT::MODE == ALIGNED && wide) {
+  if ((CT::MODE == ALIGNED || CT::MODE == FULL) && wide) {
     if (dt == MUON_F32) {
       RawChunk<float, CT::GE> r;
       load_chunk(static_cast<const float *>(p), c, k, false, false, r);
@@ -215,31 +220,36 @@ struct Ring {
 };
 
 // A vector of weights (or biases), as each thread wants its own columns of it row after row: in registers where there
-// is one chunk, as fp32 in shared memory up to 8192 columns of several chunks, and read where it is beyond that (and
-// in SCALAR, for several chunks).
+// is one chunk, as fp32 in shared memory up to 8192 columns of several chunks, and read where it is beyond that (and in
+// SCALAR, for several chunks). The block's rows share it, but for SHIFTED ones, whose columns depend on the slot: there
+// each thread has its own copy.
 template <typename CT, int C, int THREADS, bool SHARED>
 struct Params {
+  static constexpr bool OWN = CT::MODE == SHIFTED;
+  static constexpr int STRIDE = OWN ? THREADS : CT::T, BYTES = SHARED ? 32 * C * STRIDE : 0;
   const void *p;
   int dt;
   bool wide;
   float absent;
-  float4 *base;   // SHARED: of this thread, [2 chunk + half][thread]
+  float4 *base;   // SHARED: [2 chunk + half][STRIDE], of this thread
   Vals<8> one;
-  __device__ __forceinline__ void init(const CT &c) {
+  // what the rows share is put by the threads of the block's first row, and read after a barrier
+  __device__ __forceinline__ void init(const CT &c, int slot) {
     if constexpr (C == 1) one = param_chunk(p, dt, wide, c, 0, absent);
     if constexpr (SHARED) {
+      if (!OWN && slot != 0) return;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const Vals<8> o = param_chunk(p, dt, wide, c, k, absent);
-        base[(2 * k) * THREADS] = make_float4(o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y);
-        base[(2 * k + 1) * THREADS] = make_float4(o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y);
+        base[(2 * k) * STRIDE] = make_float4(o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y);
+        base[(2 * k + 1) * STRIDE] = make_float4(o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y);
       }
     }
   }
   __device__ __forceinline__ Vals<8> get(const CT &c, int k) const {
     if constexpr (C == 1) return one;
     if constexpr (SHARED) {
-      const float4 u = base[(2 * k) * THREADS], v = base[(2 * k + 1) * THREADS];
+      const float4 u = base[(2 * k) * STRIDE], v = base[(2 * k + 1) * STRIDE];
       return {{make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)}};
     }
     return param_chunk(p, dt, wide, c, k, absent);
@@ -325,14 +335,8 @@ inline Mode mode_of(bool bases, bool pitches, long long ld, long long D) {
   return ld % 8 == 0 && D % 8 == 0 ? ALIGNED : SHIFTED;
 }
 
-// Warps for a row of D columns held in C chunks per thread: what it takes (a SHIFTED row has a granule more), rounded
-// up to a width that is compiled; SCALAR knows only the largest of each kind.
-inline int warps_of(long long D, int C, Mode mode) {
-  const int need = static_cast<int>((D + (mode == SHIFTED ? 7 : 0) + 256 * C - 1) / (256 * C));
-  if (mode == SCALAR) return need <= 4 && C == 1 ? 4 : need <= 16 ? 16 : 32;
-  for (int w : {1, 2, 3, 4, 6, 8, 12, 16}) if (need <= w) return w;
-  return 32;
-}
+// The columns that a row's threads have to hold: a SHIFTED row may have a granule more.
+inline long long width_of(long long D, Mode mode) { return D + (mode == SHIFTED ? 7 : 0); }
 
 }  // namespace
 }  // namespace muon

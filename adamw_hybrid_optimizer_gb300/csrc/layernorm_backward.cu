@@ -38,11 +38,13 @@ struct Backward {
   static constexpr bool IN_SHARED = W == 32, RING = MODE != SCALAR && !IN_SHARED;
   static constexpr bool AHEAD = !IN_SHARED || sizeof(XT) + sizeof(YT) == 4;
   static constexpr bool SHARED = RING && C > 1;
+  using PT = Params<CT, C, THREADS, SHARED>;
   static constexpr int STAGES = C * T * 8 * (sizeof(XT) + sizeof(YT)) <= 16384 ? 3 : 2;
   static constexpr int RING_X = RING ? STAGES * C * 8 * sizeof(XT) * THREADS : 0;   // bytes
   static constexpr int RING_DY = RING ? STAGES * C * 8 * sizeof(YT) * THREADS : 0;
-  static constexpr size_t BYTES = static_cast<size_t>(RING_X) + RING_DY + (SHARED ? 32 * C * THREADS : 0) +
-                                  (IN_SHARED ? 64 * C * THREADS : 0);
+  static constexpr size_t LOOP = static_cast<size_t>(RING_X) + RING_DY + PT::BYTES +
+                                 (IN_SHARED ? 64 * C * THREADS : 0);
+  static constexpr size_t BYTES = std::max<size_t>(LOOP, R > 1 ? 32 * C * THREADS : 0);   // the rows' sums at the end
   static constexpr int BLOCKS = std::max(1, (C == 1 ? 768 : 512) / THREADS);
 };
 
@@ -56,7 +58,6 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
   constexpr int T = B::T, STAGES = B::STAGES, THREADS = B::THREADS;
   extern __shared__ __align__(16) unsigned char shared[];
   __shared__ float2 red[2][R][W];
-  __shared__ __align__(16) float join[R > 1 ? R * T * 8 : 1];
   const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T, D = a.D;
   const long long step = static_cast<long long>(gridDim.x) * R;
   long long row = static_cast<long long>(blockIdx.x) * R + slot;
@@ -64,8 +65,10 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
   Exchange<W, R> exchange{red, slot, t / 32, 0};
   const Ring<XT, CT, C, THREADS> ring_x{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
   const Ring<YT, CT, C, THREADS> ring_dy{shared + B::RING_X + threadIdx.x * Raw<YT, CT::GE>::BYTES};
-  float4 *kept = reinterpret_cast<float4 *>(shared + B::RING_X + B::RING_DY) + threadIdx.x;
-  Params<CT, C, THREADS, B::SHARED> weight{a.w, a.wdt, a.wide != 0, 1.f, kept};
+  using PT = typename B::PT;
+  float4 *kept = reinterpret_cast<float4 *>(shared + B::RING_X + B::RING_DY) +
+                 (PT::OWN ? static_cast<int>(threadIdx.x) : t);
+  PT weight{a.w, a.wdt, a.wide != 0, 1.f, kept};
   Vals<8> aw[C], ab[C];
 #pragma unroll
   for (int k = 0; k < C; ++k)
@@ -130,7 +133,8 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
   }
   if constexpr (B::AHEAD) fetch(0);
   if constexpr (B::RING && STAGES == 3) fetch(1);
-  weight.init(c);
+  weight.init(c, slot);
+  if constexpr (B::SHARED && R > 1) __syncthreads();
   int stage = 0;
   for (; row - slot < a.N; row += step) {   // the same count for the whole block
     const bool live = R == 1 || row < a.N;
@@ -205,15 +209,19 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
       store_sums(pw, c, k, aw[k]);
       store_sums(pb, c, k, ab[k]);
     }
-  } else {   // the block's rows are added in order
+  } else {   // the block's rows are added in order, where the ring was
+    float *join = reinterpret_cast<float *>(shared);
+    const int pitch = (D + 3) & ~3;
+    if constexpr (B::RING) copy_async_wait<0>();
     for (int z = 0; z < 2; ++z) {
       __syncthreads();
-      store_sums(join + slot * D, c, 0, z == 0 ? aw[0] : ab[0]);
+#pragma unroll
+      for (int k = 0; k < C; ++k) store_sums(join + slot * pitch, c, k, z == 0 ? aw[k] : ab[k]);
       __syncthreads();
       for (int j = threadIdx.x; j < D; j += THREADS) {
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) s += join[r * D + j];
+        for (int r = 0; r < R; ++r) s += join[r * pitch + j];
         (z == 0 ? pw : pb)[j] = s;
       }
     }
@@ -302,19 +310,23 @@ __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(con
 
 // ------------------------------------------------------------------------------------------ host
 
-// Chunks per thread, warps per row and rows per block for D columns: one chunk of eight columns per thread and several
-// rows in a block up to 1024 columns, two chunks above.
+// Chunks per thread, warps per row and rows per block for D columns: a warp per row up to 768 columns, then as few
+// warps as two chunks of eight columns per thread allow (the sums of dw and db take 32 registers there).
 struct Shape {
   int C, W, R;
 };
-Shape shape_of(long long D, Mode mode) {
-  if (D + (mode == SHIFTED ? 7 : 0) <= 1024) {
-    const int W = warps_of(D, 1, mode);
-    return {1, W, W == 1 ? 8 : W == 2 ? 4 : 2};
-  }
-  return {2, std::max(3, warps_of(D, 2, mode)), 1};
+Shape shape_of(long long columns, Mode mode) {
+  const long long D = width_of(columns, mode);
+  if (mode == SCALAR) return D <= 1024 ? Shape{1, 4, 2} : Shape{2, D <= 8192 ? 16 : 32, 1};
+  if (D <= 256) return {1, 1, 8};
+  if (mode == SHIFTED && D <= 1024) return {1, D <= 512 ? 2 : 4, D <= 512 ? 4 : 2};   // few warps have edges
+  if (D <= 512) return {2, 1, 8};
+  if (D <= 768) return {3, 1, 8};
+  if (D <= 1024) return {2, 2, 4};
+  for (int W : {4, 8, 16}) if (D <= 512 * W) return {2, W, 1};
+  return {2, 32, 1};
 }
-bool long_row(long long D, Mode mode) { return D + (mode == SHIFTED ? 7 : 0) > MAX_ROW; }
+bool long_row(long long D, Mode mode) { return width_of(D, mode) > MAX_ROW; }
 
 // Blocks of the backward pass, each of which leaves one partial row of dw and db: as many as the GPU holds at once,
 // so that there are few partial rows to add. In SHIFTED a slot's rows lie multiples of eight apart.
@@ -336,25 +348,29 @@ cudaError_t backward_launch(const BackwardArgs &a, cudaStream_t s) {
   return launch_pdl(kernel, dim3(static_cast<unsigned>(a.parts)), dim3(B::THREADS), B::BYTES, s, a);
 }
 
+template <typename XT, typename YT, int C, int W, int R, int MODE>
+cudaError_t backward_shape(const BackwardArgs &a, cudaStream_t s) {
+  if (MODE == ALIGNED && a.D == 256 * C * W) return backward_launch<XT, YT, C, W, R, FULL>(a, s);
+  return backward_launch<XT, YT, C, W, R, MODE>(a, s);
+}
+
 template <typename XT, typename YT, int MODE>
 cudaError_t backward_route_mode(const BackwardArgs &a, cudaStream_t s) {
   const Shape h = shape_of(a.D, static_cast<Mode>(MODE));
-  if (h.C == 1) {
-    switch (h.W) {
-      case 1: return backward_launch<XT, YT, 1, 1, 8, MODE>(a, s);
-      case 2: return backward_launch<XT, YT, 1, 2, 4, MODE>(a, s);
-      case 3: return backward_launch<XT, YT, 1, 3, 2, MODE>(a, s);
-      default: return backward_launch<XT, YT, 1, 4, 2, MODE>(a, s);
-    }
+  if (h.C == 1 && h.W == 1) return backward_shape<XT, YT, 1, 1, 8, MODE>(a, s);
+  if constexpr (MODE == SHIFTED) {
+    if (h.C == 1)
+      return h.W == 2 ? backward_shape<XT, YT, 1, 2, 4, MODE>(a, s) : backward_shape<XT, YT, 1, 4, 2, MODE>(a, s);
+  } else {
+    if (h.W == 1)
+      return h.C == 2 ? backward_shape<XT, YT, 2, 1, 8, MODE>(a, s) : backward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
+    if (h.W == 2) return backward_shape<XT, YT, 2, 2, 4, MODE>(a, s);
   }
   switch (h.W) {
-    case 3: return backward_launch<XT, YT, 2, 3, 1, MODE>(a, s);
-    case 4: return backward_launch<XT, YT, 2, 4, 1, MODE>(a, s);
-    case 6: return backward_launch<XT, YT, 2, 6, 1, MODE>(a, s);
-    case 8: return backward_launch<XT, YT, 2, 8, 1, MODE>(a, s);
-    case 12: return backward_launch<XT, YT, 2, 12, 1, MODE>(a, s);
-    case 16: return backward_launch<XT, YT, 2, 16, 1, MODE>(a, s);
-    default: return backward_launch<XT, YT, 2, 32, 1, MODE>(a, s);
+    case 4: return backward_shape<XT, YT, 2, 4, 1, MODE>(a, s);
+    case 8: return backward_shape<XT, YT, 2, 8, 1, MODE>(a, s);
+    case 16: return backward_shape<XT, YT, 2, 16, 1, MODE>(a, s);
+    default: return backward_shape<XT, YT, 2, 32, 1, MODE>(a, s);
   }
 }
 

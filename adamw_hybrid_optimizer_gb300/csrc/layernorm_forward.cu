@@ -29,11 +29,12 @@ struct Forward {
   static constexpr int T = W * 32, THREADS = T * R;
   using CT = Cols<MODE, granule_of<XT, YT>(), T>;
   static constexpr bool RING = MODE != SCALAR, SHARED = RING && C > 1 && C * T * 8 <= 8192;
+  using PT = Params<CT, C, THREADS, SHARED>;
   static constexpr int STAGES = C * T * 8 * sizeof(XT) <= 16384 ? 3 : 2;
   static constexpr int ROWS = RING ? STAGES * C * 8 * sizeof(XT) * THREADS : 0;   // bytes of the ring
-  static constexpr size_t BYTES = static_cast<size_t>(ROWS) + (SHARED ? 64 * C * THREADS : 0);
-  static constexpr int by_registers = C == 4 ? (W <= 4 ? 768 : W <= 8 ? 512 : 1024) : 1024;   // threads of an SM
-  static constexpr int BLOCKS = std::max(1, by_registers / THREADS);
+  static constexpr size_t BYTES = static_cast<size_t>(ROWS) + 2 * PT::BYTES;
+  static constexpr int by_registers = C == 4 ? (T <= 128 ? 768 : T <= 256 ? 512 : 1024) : C == 3 ? 768 : 1024;
+  static constexpr int BLOCKS = std::max(1, by_registers / THREADS);   // of a multiprocessor
 };
 
 template <typename XT, typename YT, int C, int W, int R, int MODE>
@@ -52,9 +53,9 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
   const CT c(t, a.D, static_cast<int>((row * a.ldx) & (CT::GE - 1)));
   Exchange<W, R> exchange{red, slot, t / 32, 0};
   const Ring<XT, CT, C, F::THREADS> ring{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
-  float4 *kept = reinterpret_cast<float4 *>(shared + F::ROWS) + threadIdx.x;
-  Params<CT, C, F::THREADS, F::SHARED> weight{a.w, a.wdt, a.wide != 0, 1.f, kept},
-      bias{a.b, a.wdt, a.wide != 0, 0.f, kept + 2 * C * F::THREADS};
+  using PT = typename F::PT;
+  float4 *kept = reinterpret_cast<float4 *>(shared + F::ROWS) + (PT::OWN ? static_cast<int>(threadIdx.x) : t);
+  PT weight{a.w, a.wdt, a.wide != 0, 1.f, kept}, bias{a.b, a.wdt, a.wide != 0, 0.f, kept + PT::BYTES / 16};
   const long long x_step = step * a.ldx, y_step = step * a.ldy;
   const XT *x = static_cast<const XT *>(a.x) + row * a.ldx;   // the next row to fetch
   YT *y = static_cast<YT *>(a.y) + row * a.ldy;
@@ -75,8 +76,9 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
   };
   fetch(0);
   if constexpr (F::RING && STAGES == 3) fetch(1);
-  weight.init(c);
-  bias.init(c);
+  weight.init(c, slot);
+  bias.init(c, slot);
+  if constexpr (F::SHARED && R > 1) __syncthreads();
   const float inv = 1.f / static_cast<float>(a.D);
   // columns of this warp, and of the warp whose pair this lane reads in the exchange
   const float n_w = warp_sum(static_cast<float>(c.columns())), inv_n = n_w > 0.f ? 1.f / n_w : 0.f;
@@ -186,34 +188,38 @@ cudaError_t forward_launch(const ForwardArgs &a, cudaStream_t s) {
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(F::THREADS), F::BYTES, s, a);
 }
 
+template <typename XT, typename YT, int C, int W, int R, int MODE>
+cudaError_t forward_shape(const ForwardArgs &a, cudaStream_t s) {
+  if (MODE == ALIGNED && a.D == 256 * C * W) return forward_launch<XT, YT, C, W, R, FULL>(a, s);
+  return forward_launch<XT, YT, C, W, R, MODE>(a, s);
+}
+
+// Rows of up to 1024 columns: a warp each, eight to a block, since the shuffles and the exchange of a row cost a thread
+// the same whatever it holds (65536 x 768 bf16: 36 us, and 41 us with three warps to a row). SHIFTED rows are spread
+// over more warps, of which only two have edges to deal with. Longer rows: two chunks of eight columns per thread, and
+// four beyond 8192 columns (65536 x 4096 bf16: 161 us with two, 164 to 195 us with four, which leave a multiprocessor
+// half the warps beside the weights in shared memory).
 template <typename XT, typename YT, int MODE>
 cudaError_t forward_route_mode(const ForwardArgs &a, cudaStream_t s) {
-  // One chunk of eight columns per thread and several rows in a block up to 1024 columns; four chunks above, so that
-  // the shuffles and the exchange of a row are shared by more columns.
-  const bool short_row = a.D + (MODE == SHIFTED ? 7 : 0) <= 1024;
-  if (short_row) {
-    switch (warps_of(a.D, 1, static_cast<Mode>(MODE))) {
-      case 1: return forward_launch<XT, YT, 1, 1, 8, MODE>(a, s);
-      case 2: return forward_launch<XT, YT, 1, 2, 4, MODE>(a, s);
-      case 3: return forward_launch<XT, YT, 1, 3, 2, MODE>(a, s);
-      default: return forward_launch<XT, YT, 1, 4, 2, MODE>(a, s);
-    }
+  const long long D = width_of(a.D, static_cast<Mode>(MODE));
+  if (D <= 256) return forward_shape<XT, YT, 1, 1, 8, MODE>(a, s);
+  if constexpr (MODE == SHIFTED) {
+    if (D <= 512) return forward_shape<XT, YT, 1, 2, 4, MODE>(a, s);
+    if (D <= 1024) return forward_shape<XT, YT, 1, 4, 2, MODE>(a, s);
+  } else {
+    if (D <= 512) return forward_shape<XT, YT, 2, 1, 8, MODE>(a, s);
+    if (D <= 768) return forward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
+    if (D <= 1024) return forward_shape<XT, YT, 4, 1, 8, MODE>(a, s);
   }
-  switch (warps_of(a.D, 4, static_cast<Mode>(MODE))) {
-    case 1:
-    case 2: return forward_launch<XT, YT, 4, 2, 1, MODE>(a, s);
-    case 3: return forward_launch<XT, YT, 4, 3, 1, MODE>(a, s);
-    case 4: return forward_launch<XT, YT, 4, 4, 1, MODE>(a, s);
-    case 6: return forward_launch<XT, YT, 4, 6, 1, MODE>(a, s);
-    case 8: return forward_launch<XT, YT, 4, 8, 1, MODE>(a, s);
-    case 12: return forward_launch<XT, YT, 4, 12, 1, MODE>(a, s);
-    default: return forward_launch<XT, YT, 4, 16, 1, MODE>(a, s);
-  }
+  if (D <= 2048) return forward_shape<XT, YT, 2, 4, 1, MODE>(a, s);
+  if (D <= 4096) return forward_shape<XT, YT, 2, 8, 1, MODE>(a, s);
+  if (D <= 8192) return forward_shape<XT, YT, 2, 16, 1, MODE>(a, s);
+  return forward_shape<XT, YT, 4, 16, 1, MODE>(a, s);
 }
 
 template <typename XT, typename YT>
 cudaError_t forward_route(const ForwardArgs &a, Mode mode, cudaStream_t s) {
-  if (a.D + (mode == SHIFTED ? 7 : 0) > MAX_ROW) {
+  if (width_of(a.D, mode) > MAX_ROW) {
     const dim3 grid(static_cast<unsigned>(std::min<long long>(a.N, device_sm_count() * 2))), block(LONG_THREADS);
     return launch_pdl(layernorm_forward_long_kernel<XT, YT>, grid, block, 0, s, a);
   }
