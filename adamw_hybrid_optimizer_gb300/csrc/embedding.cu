@@ -11,8 +11,9 @@
 // out of the two aligned granules around them, and lie where the granules of the row that is written are.
 //
 //   embedding_forward_kernel  a gather that reads and writes each byte once; several rows per warp where they are short.
-//   embedding_zero_kernel     zeroes the gradient (not called when it accumulates).
-//   embedding_cluster_sort_kernel  the sort of up to 131072 ids in one cluster's shared memory, under the zero kernel.
+//   embedding_prepare_kernel  one cluster sorts up to 131072 ids in its shared memory, while the other blocks zero the
+//                             gradient (unless it accumulates).
+//   embedding_zero_kernel     the zeroes alone, before a longer sort.
 //   radix_*_kernel            one pass of a longer sort: digit counts per tile, their scan, the stable scatter.
 //   embedding_sum_kernel      one warp per 32 sorted positions and 256 columns; the rows to come are in flight whether or
 //                             not they belong to the id being summed, since most ids occur once or twice.
@@ -329,12 +330,55 @@ __global__ void __launch_bounds__(THREADS) radix_scatter_kernel(const SortPass p
   }
 }
 
+// What is to be zeroed: rows x `bytes` at a pitch (one row of everything where the rows leave no gaps).
+struct ZeroArgs {
+  unsigned char *g;
+  long long pitch, rows, bytes;
+};
+constexpr long long ZERO_BLOCK = 256 * 1024;   // bytes of one row per block; of many rows, whole rows of about that
+
+__device__ __forceinline__ void zero_stretch(unsigned char *p, long long bytes, int first, int threads) {
+  const long long head = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+  const long long lead = head < bytes ? head : bytes, whole = (bytes - lead) / 16;
+  uint4 *q = reinterpret_cast<uint4 *>(p + lead);
+#pragma unroll 4
+  for (long long i = first; i < whole; i += threads) q[i] = make_uint4(0, 0, 0, 0);
+  for (long long i = first; i < lead; i += threads) p[i] = 0;
+  for (long long i = lead + whole * 16 + first; i < bytes; i += threads) p[i] = 0;
+}
+
+__host__ __device__ __forceinline__ long long zero_rows_per_block(const ZeroArgs &z) {
+  return z.bytes >= ZERO_BLOCK ? 1 : ZERO_BLOCK / z.bytes;
+}
+long long zero_blocks(const ZeroArgs &z) {
+  if (z.rows == 1) return (z.bytes + ZERO_BLOCK - 1) / ZERO_BLOCK;
+  return (z.rows + zero_rows_per_block(z) - 1) / zero_rows_per_block(z);
+}
+
+// The share of block b of zero_blocks().
+__device__ __forceinline__ void zero_share(const ZeroArgs &z, long long b) {
+  if (z.rows == 1) {
+    const long long from = b * ZERO_BLOCK;
+    if (from < z.bytes) zero_stretch(z.g + from, min(ZERO_BLOCK, z.bytes - from), threadIdx.x, blockDim.x);
+  } else {   // warps take rows
+    const long long per = zero_rows_per_block(z), end = min((b + 1) * per, z.rows);   // none past the last block
+    for (long long r = b * per + threadIdx.x / 32; r < end; r += blockDim.x / 32)
+      zero_stretch(z.g + r * z.pitch, z.bytes, threadIdx.x % 32, 32);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS) embedding_zero_kernel(const ZeroArgs z) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  zero_share(z, blockIdx.x);
+}
+
 // The whole sort in one cluster, for n <= 16 * 8192: block b holds the sorted positions [b * chunk, (b + 1) * chunk) in
 // its shared memory, and a pass moves every item to its place in any block's. A thread keeps its items in registers
 // while their places are computed, so one buffer is enough. Warp w of a block has the block's items [w * per, ...), 32
 // at a time; an item's place is its digit's first place, plus the digit's items in earlier blocks, warps, rounds and
 // lanes: stable, like the passes above.
-constexpr int CS_THREADS = 512;    // few enough registers to run beside the zero kernel's blocks
+constexpr int CS_THREADS = 512;
 constexpr int CS_WARPS = CS_THREADS / 32;
 constexpr int CS_ROUNDS = 16;                              // items per thread
 constexpr int CS_CHUNK = CS_THREADS * CS_ROUNDS;           // items per block
@@ -347,7 +391,7 @@ struct ClusterSort {
   unsigned *key, *pos;      // sorted
   unsigned *list_count;
   int n, blocks, chunk, passes, bits;
-  int after_zero;           // the launch before is the zero kernel, under which this one runs
+  ZeroArgs zero;            // for the blocks after the first cluster
 };
 
 struct ClusterShared {
@@ -358,11 +402,13 @@ struct ClusterShared {
   unsigned warp_total[CS_WARPS];
 };
 
-__global__ void __launch_bounds__(CS_THREADS, 2) embedding_cluster_sort_kernel(const ClusterSort a) {
-  // The zero kernel passes its own wait before it lets this kernel start, so whatever came before it is complete; this
-  // kernel waits for the zero kernel only at its end, so that the sums, which wait for this one, follow both.
-  if (!a.after_zero) pdl_wait();
+__global__ void __launch_bounds__(CS_THREADS, 2) embedding_prepare_kernel(const ClusterSort a) {
+  pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
+  if (blockIdx.x >= a.blocks) {   // whole clusters
+    zero_share(a.zero, blockIdx.x - a.blocks);
+    return;
+  }
   extern __shared__ __align__(16) unsigned char cluster_smem[];
   ClusterShared &s = *reinterpret_cast<ClusterShared *>(cluster_smem);
   const int rank = a.blocks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -466,39 +512,9 @@ __global__ void __launch_bounds__(CS_THREADS, 2) embedding_cluster_sort_kernel(c
     else __syncthreads();
   }
   if (rank == 0 && threadIdx.x == 0) *a.list_count = 0;
-  if (a.after_zero) pdl_wait();
 }
 
 // ------------------------------------------------------------------------------------------ sums
-
-// rows x `bytes` at a pitch, in 16-byte accesses from the first boundary of a row on (one row of everything where the
-// rows leave no gaps).
-__global__ void __launch_bounds__(THREADS) embedding_zero_kernel(unsigned char *g, long long pitch, long long rows,
-                                                                 long long bytes) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_launch_dependents();
-  const long long tid = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
-  const long long stride = static_cast<long long>(gridDim.x) * THREADS;
-  if (rows == 1) {
-    const long long head = (16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15;
-    const long long lead = head < bytes ? head : bytes, whole = (bytes - lead) / 16;
-    uint4 *q = reinterpret_cast<uint4 *>(g + lead);
-#pragma unroll 4
-    for (long long i = tid; i < whole; i += stride) q[i] = make_uint4(0, 0, 0, 0);
-    for (long long i = tid; i < lead; i += stride) g[i] = 0;
-    for (long long i = lead + whole * 16 + tid; i < bytes; i += stride) g[i] = 0;
-  } else {   // warps take rows
-    const int lane = threadIdx.x % 32;
-    for (long long r = tid / 32; r < rows; r += stride / 32) {
-      unsigned char *p = g + r * pitch;
-      const long long head = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
-      const long long lead = head < bytes ? head : bytes, whole = (bytes - lead) / 16;
-      for (long long i = lane; i < whole; i += 32) reinterpret_cast<uint4 *>(p + lead)[i] = make_uint4(0, 0, 0, 0);
-      for (long long i = lane; i < lead; i += 32) p[i] = 0;
-      for (long long i = lead + whole * 16 + lane; i < bytes; i += 32) p[i] = 0;
-    }
-  }
-}
 
 struct SumArgs {
   const unsigned *key, *pos;   // sorted
@@ -507,7 +523,8 @@ struct SumArgs {
   void *g;
   long long ldg;
   float *part;                 // [2 * groups][ldp]: sums of the runs that the join kernel finishes
-  unsigned *list, *list_count; // groups where such a run starts
+  uint2 *list;                 // (group where such a run starts, groups that it touches)
+  unsigned *list_count;
   long long n, V, ldp;
   int D, tiles, groups, accumulate;
   float scale;
@@ -603,6 +620,25 @@ __device__ __forceinline__ void store_part(float *p, int tile, int lane, const V
   store_vals(p + tile * SUM_COLS + lane * 8, acc);
 }
 
+// Groups that the long run of k which starts in group c touches: 32 probes at a time for the first group after c + 1
+// whose first key is not k.
+__device__ __forceinline__ unsigned run_groups(const SumArgs &a, long long c, unsigned k, int lane) {
+  long long lo = c + 2, hi = a.groups;   // groups below lo are the run's, hi is not (or the end)
+  while (lo < hi) {
+    const long long stride = (hi - lo + 31) / 32, probe = lo + lane * stride;
+    const unsigned yes = __ballot_sync(0xffffffffu, probe < hi && a.key[probe < hi ? probe * GROUP : 0] == k);
+    const int ok = __popc(yes);   // the run's probes are the first ones
+    if (ok == 0) {
+      hi = lo;
+    } else {
+      const long long limit = lo + ok * stride;
+      lo += (ok - 1) * stride + 1;
+      if (ok < 32 && limit < hi) hi = limit;
+    }
+  }
+  return static_cast<unsigned>(lo - c);
+}
+
 // A run of equal ids that starts in group c belongs to it, unless the run covers the whole of the next group and
 // goes on (a long run): then every group sums its own part, into part[2c + 1] where the run starts and part[2c]
 // where it came from the group before, and the join kernel adds the parts. So a warp sums at most 63 positions. While
@@ -642,7 +678,10 @@ __global__ void __launch_bounds__(THREADS, 2) embedding_sum_kernel(const SumArgs
       tail_part = far_after == last;
       if (!tail_part) end += __popc(__ballot_sync(0xffffffffu, k1 == last));
     }
-    if (tail_part && tile == 0 && lane == 0) a.list[atomicAdd(a.list_count, 1u)] = static_cast<unsigned>(c);
+    if (tail_part && tile == 0) {
+      const unsigned parts = run_groups(a, c, last, lane);
+      if (lane == 0) a.list[atomicAdd(a.list_count, 1u)] = make_uint2(static_cast<unsigned>(c), parts);
+    }
     if (begin >= end) continue;
 
     auto at = [&](unsigned lo, unsigned hi, int i) {
@@ -703,23 +742,10 @@ __global__ void __launch_bounds__(THREADS) embedding_join_kernel(const SumArgs a
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const long long units = static_cast<long long>(*a.list_count) * a.tiles;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const long long c = a.list[u / a.tiles];
+    const uint2 run = a.list[u / a.tiles];
+    const long long c = run.x, parts = run.y;
     const int tile = static_cast<int>(u % a.tiles);
     const unsigned k = a.key[c * GROUP + GROUP - 1];
-    // the first group after c + 1 whose first key is not k: 32 probes at a time
-    long long lo = c + 2, hi = a.groups;   // groups below lo are the run's, hi is not (or the end)
-    while (lo < hi) {
-      const long long stride = (hi - lo + 31) / 32, probe = lo + lane * stride;
-      const unsigned yes = __ballot_sync(0xffffffffu, probe < hi && a.key[probe * GROUP] == k);
-      const int ok = __popc(yes);   // the run's probes are the first ones
-      if (ok == 0) hi = lo;
-      else {
-        const long long reached = lo + (ok - 1) * stride + 1, limit = lo + ok * stride;
-        hi = ok < 32 && limit < hi ? limit : hi;
-        lo = reached;
-      }
-    }
-    const long long parts = lo - c;
     Vals<8> acc;
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc.p[i] = make_float2(0.f, 0.f);
@@ -766,7 +792,7 @@ EmbeddingLayout embedding_layout(long long n, long long D) {
   L.groups = (n + GROUP - 1) / GROUP;
   L.tiles = (n + SORT_TILE - 1) / SORT_TILE;
   L.ldp = (D + 7 + SUM_COLS - 1) / SUM_COLS * SUM_COLS;   // rows past a boundary reach up to 7 columns further
-  L.list = take(4 * (1 + static_cast<size_t>(n) / GROUP));
+  L.list = take(8 * (1 + static_cast<size_t>(n) / GROUP));   // the count, then the pairs
   for (int k = 0; k < 2; ++k) L.key[k] = take(4 * static_cast<size_t>(n));
   for (int k = 0; k < 2; ++k) L.pos[k] = take(4 * static_cast<size_t>(n));
   L.hist = take(4 * static_cast<size_t>(L.tiles) << MAX_DIGIT_BITS);
@@ -862,15 +888,16 @@ muon_status launch_sort(const void *ids, int itype, long long n, long long V, lo
   return MUON_OK;
 }
 
-// The sort in one cluster (n <= CS_BLOCKS * CS_CHUNK). Blocks of up to 2048 items each while there are eight: a block's
-// rounds cost more than the cluster's barriers.
-muon_status launch_cluster_sort(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
-                                const EmbeddingLayout &L, bool after_zero, const unsigned **key, const unsigned **pos,
-                                cudaStream_t s) {
-  static const cudaError_t allowed = cudaFuncSetAttribute(
-      embedding_cluster_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(ClusterShared)));
+// The sort in one cluster (n <= CS_BLOCKS * CS_CHUNK) and the zeroes beside it (z.rows = 0: none). Blocks of up to 2048
+// items each while there are eight: a block's rounds cost more than the cluster's barriers.
+muon_status launch_prepare(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
+                           const EmbeddingLayout &L, const ZeroArgs &z, const unsigned **key, const unsigned **pos,
+                           cudaStream_t s) {
+  static const cudaError_t allowed =
+      cudaFuncSetAttribute(embedding_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(ClusterShared)));
   static const cudaError_t wide =   // 16 blocks
-      cudaFuncSetAttribute(embedding_cluster_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      cudaFuncSetAttribute(embedding_prepare_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (allowed != cudaSuccess || wide != cudaSuccess) return MUON_ERR_CUDA;
   int key_bits = 1;
   while ((V >> key_bits) != 0) ++key_bits;
@@ -889,9 +916,11 @@ muon_status launch_cluster_sort(const void *ids, int itype, long long n, long lo
   a.chunk = (a.n + a.blocks - 1) / a.blocks;
   a.passes = (key_bits + MAX_DIGIT_BITS - 1) / MAX_DIGIT_BITS;
   a.bits = (key_bits + a.passes - 1) / a.passes;
-  a.after_zero = after_zero ? 1 : 0;
+  a.zero = z;
+  const long long zeros = z.rows > 0 ? (zero_blocks(z) + a.blocks - 1) / a.blocks * a.blocks : 0;   // whole clusters
+  if (zeros > (1ll << 30)) return MUON_ERR_SHAPE;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.blocks + zeros));
   cfg.blockDim = dim3(CS_THREADS);
   cfg.dynamicSmemBytes = sizeof(ClusterShared);
   cfg.stream = s;
@@ -905,11 +934,21 @@ muon_status launch_cluster_sort(const void *ids, int itype, long long n, long lo
   cfg.attrs = attr;
   cfg.numAttrs = a.blocks > 1 ? 2 : 1;
   launch_begin(KK_EMBED_SORT, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, embedding_cluster_sort_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, embedding_prepare_kernel, a);
   launch_end(s);
   *key = a.key;
   *pos = a.pos;
   return status_of(e);
+}
+
+muon_status launch_zero(const ZeroArgs &z, cudaStream_t s) {
+  const long long blocks = zero_blocks(z);
+  if (blocks > (1ll << 30)) return MUON_ERR_SHAPE;
+  launch_begin(KK_EMBED_ZERO, s);
+  const muon_status st =
+      status_of(launch_pdl(embedding_zero_kernel, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), 0, s, z));
+  launch_end(s);
+  return st;
 }
 
 template <typename OT, typename GT, int ACCESS>
@@ -992,26 +1031,20 @@ muon_status embedding_backward(const void *ids, muon_itype itype, const void *do
   if (n > 0 && ws_bytes < L.total) return MUON_ERR_WORKSPACE;
   if ((st = device_check()) != MUON_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const long long sms = device_sm_count();
   const int Di = static_cast<int>(D);
+  ZeroArgs z{};
   if (!accumulate) {
     const long long size = gdt == MUON_F32 ? 4 : 2;
     const bool dense = ldg == D || V == 1;
-    const long long rows = dense ? 1 : V, bytes = (dense ? V * D : D) * size;
-    const long long work = dense ? bytes / 64 + 1 : V * 32;   // threads that find something to do
-    const dim3 grid(static_cast<unsigned>(std::min((work + THREADS - 1) / THREADS, sms * 4)));   // room for the sort
-    launch_begin(KK_EMBED_ZERO, s);
-    st = status_of(launch_pdl(embedding_zero_kernel, grid, dim3(THREADS), 0, s, static_cast<unsigned char *>(dtable),
-                              static_cast<long long>(ldg) * size, rows, bytes));
-    launch_end(s);
-    if (st != MUON_OK) return st;
+    z = {static_cast<unsigned char *>(dtable), static_cast<long long>(ldg) * size, dense ? 1 : V, (dense ? V * D : D) * size};
   }
+  const bool clustered = n > 0 && n <= CS_BLOCKS * CS_CHUNK;
+  if (!clustered && z.rows > 0 && (st = launch_zero(z, s)) != MUON_OK) return st;
   if (n == 0) return MUON_OK;
   char *base = static_cast<char *>(ws);
   SumArgs a{};
-  st = n <= CS_BLOCKS * CS_CHUNK
-           ? launch_cluster_sort(ids, itype, n, V, padding_idx, base, L, !accumulate, &a.key, &a.pos, s)
-           : launch_sort(ids, itype, n, V, padding_idx, base, L, &a.key, &a.pos, s);
+  st = clustered ? launch_prepare(ids, itype, n, V, padding_idx, base, L, z, &a.key, &a.pos, s)
+                 : launch_sort(ids, itype, n, V, padding_idx, base, L, &a.key, &a.pos, s);
   if (st != MUON_OK) return st;
   a.dout = dout;
   a.ldo = ldo;
@@ -1019,7 +1052,7 @@ muon_status embedding_backward(const void *ids, muon_itype itype, const void *do
   a.ldg = ldg;
   a.part = reinterpret_cast<float *>(base + L.part);
   a.list_count = reinterpret_cast<unsigned *>(base + L.list);
-  a.list = a.list_count + 1;
+  a.list = reinterpret_cast<uint2 *>(a.list_count) + 1;
   a.n = n;
   a.V = V;
   a.ldp = L.ldp;

@@ -65,9 +65,23 @@ struct Cols {
   __device__ __forceinline__ bool in(int k, int e) const {   // of a granule that the thread has
     return MODE == SCALAR ? 8 * k + e < mine : MODE != SHIFTED || (col(k, e) >= 0 && col(k, e) < D);
   }
-  // pair i of chunk k with zeros where the row has no column; its granule is there
+  // SHIFTED: puts `fill` where the row has no column, in the edges of the threads that have them
+  template <int C>
+  __device__ __forceinline__ void fill_edges(Vals<8> *v, float fill) const {
+    if (MODE != SHIFTED || !(t == 0 || last >= 0)) return;
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+#pragma unroll
+      for (int j = 0; j < PG; ++j)
+        if (edge(k, j)) {
+#pragma unroll
+          for (int e = j * GE; e < (j + 1) * GE; ++e)
+            if (!in(k, e)) (e % 2 ? v[k].p[e / 2].y : v[k].p[e / 2].x) = fill;
+        }
+  }
+  // SCALAR: pair i of chunk k with zeros where the row has no column
   __device__ __forceinline__ float2 only(int k, int i, float2 v) const {
-    if (MODE == SCALAR || edge(k, 2 * i / GE)) {
+    if (MODE == SCALAR) {
       if (!in(k, 2 * i)) v.x = 0.f;
       if (!in(k, 2 * i + 1)) v.y = 0.f;
     }

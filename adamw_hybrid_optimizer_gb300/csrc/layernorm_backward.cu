@@ -16,7 +16,7 @@ namespace muon {
 namespace {
 
 constexpr int REDUCE_COLS = 32;
-constexpr int REDUCE_WARPS = 16;
+constexpr int REDUCE_WARPS = 32;
 
 struct BackwardArgs {
   const void *dy, *x, *w;
@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
       }
       if constexpr (B::AHEAD) fetch(0);
     }
+    c.template fill_edges<C>(xh, -m2.x);   // xh = 0 there
+    c.template fill_edges<C>(g, 0.f);
     float2 s1 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
     if (live) {
 #pragma unroll
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(256) layernorm_columns_kernel(const BackwardAr
   a.part[(a.parts + blockIdx.y) * a.ldp + c] = sb;
 }
 
-// dw (blockIdx.y = 0) and db (1): 32 columns per block, warp w adds partial rows w, w + 16, ...
+// dw (blockIdx.y = 0) and db (1): 32 columns per block, warp w adds partial rows w, w + 32, ...
 __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(const float *part, long long parts,
                                                                              long long ldp, int D, void *dw, void *db,
                                                                              int gdt, int accumulate) {
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(con
   const float *p = part + blockIdx.y * parts * ldp;
   float s = 0.f;
   if (c < D) {
-#pragma unroll 8
+#pragma unroll 16
     for (long long r = w; r < parts; r += REDUCE_WARPS) s += p[r * ldp + c];
   }
   red[w][lane] = s;
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(con
 // ------------------------------------------------------------------------------------------ host
 
 // Chunks per thread, warps per row and rows per block for D columns: a warp per row up to 768 columns, then as few
-// warps as two chunks of eight columns per thread allow (the sums of dw and db take 32 registers there).
+// warps as two or three chunks of eight columns per thread allow (the sums of dw and db take 16 registers for each).
 struct Shape {
   int C, W, R;
 };
@@ -319,10 +321,10 @@ Shape shape_of(long long columns, Mode mode) {
   const long long D = width_of(columns, mode);
   if (mode == SCALAR) return D <= 1024 ? Shape{1, 4, 2} : Shape{2, D <= 8192 ? 16 : 32, 1};
   if (D <= 256) return {1, 1, 8};
-  if (mode == SHIFTED && D <= 1024) return {1, D <= 512 ? 2 : 4, D <= 512 ? 4 : 2};   // few warps have edges
   if (D <= 512) return {2, 1, 8};
   if (D <= 768) return {3, 1, 8};
   if (D <= 1024) return {2, 2, 4};
+  if (D <= 1536) return {3, 2, 4};
   for (int W : {4, 8, 16}) if (D <= 512 * W) return {2, W, 1};
   return {2, 32, 1};
 }
@@ -357,15 +359,12 @@ cudaError_t backward_shape(const BackwardArgs &a, cudaStream_t s) {
 template <typename XT, typename YT, int MODE>
 cudaError_t backward_route_mode(const BackwardArgs &a, cudaStream_t s) {
   const Shape h = shape_of(a.D, static_cast<Mode>(MODE));
-  if (h.C == 1 && h.W == 1) return backward_shape<XT, YT, 1, 1, 8, MODE>(a, s);
-  if constexpr (MODE == SHIFTED) {
-    if (h.C == 1)
-      return h.W == 2 ? backward_shape<XT, YT, 1, 2, 4, MODE>(a, s) : backward_shape<XT, YT, 1, 4, 2, MODE>(a, s);
-  } else {
-    if (h.W == 1)
-      return h.C == 2 ? backward_shape<XT, YT, 2, 1, 8, MODE>(a, s) : backward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
-    if (h.W == 2) return backward_shape<XT, YT, 2, 2, 4, MODE>(a, s);
-  }
+  if (h.W == 1)
+    return h.C == 1   ? backward_shape<XT, YT, 1, 1, 8, MODE>(a, s)
+           : h.C == 2 ? backward_shape<XT, YT, 2, 1, 8, MODE>(a, s)
+                      : backward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
+  if (h.W == 2)
+    return h.C == 2 ? backward_shape<XT, YT, 2, 2, 4, MODE>(a, s) : backward_shape<XT, YT, 3, 2, 4, MODE>(a, s);
   switch (h.W) {
     case 4: return backward_shape<XT, YT, 2, 4, 1, MODE>(a, s);
     case 8: return backward_shape<XT, YT, 2, 8, 1, MODE>(a, s);

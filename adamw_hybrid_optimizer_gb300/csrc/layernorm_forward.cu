@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
       for (int k = 0; k < C; ++k) v[k] = raw[k].get();
       fetch(0);
     }
+    c.template fill_edges<C>(v, 0.f);
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k)
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
       for (int i = 0; i < 4; ++i)
         if (c.has(k, 2 * i / CT::GE)) s = __fadd2_rn(s, c.only(k, i, v[k].p[i]));
     const float own = warp_sum(s.x + s.y) * inv_n;
+    c.template fill_edges<C>(v, own);   // at no distance
     float2 q = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k)
@@ -195,22 +197,17 @@ cudaError_t forward_shape(const ForwardArgs &a, cudaStream_t s) {
 }
 
 // Rows of up to 1024 columns: a warp each, eight to a block, since the shuffles and the exchange of a row cost a thread
-// the same whatever it holds (65536 x 768 bf16: 36 us, and 41 us with three warps to a row). SHIFTED rows are spread
-// over more warps, of which only two have edges to deal with. Longer rows: two chunks of eight columns per thread, and
-// four beyond 8192 columns (65536 x 4096 bf16: 161 us with two, 164 to 195 us with four, which leave a multiprocessor
-// half the warps beside the weights in shared memory).
+// the same whatever it holds (65536 x 768 bf16: 36 us, and 41 us with three warps to a row). Longer rows: two chunks of
+// eight columns per thread, and four beyond 8192 columns (65536 x 4096 bf16: 161 us with two, 164 to 195 us with four,
+// which leave a multiprocessor half the warps beside the weights in shared memory).
 template <typename XT, typename YT, int MODE>
 cudaError_t forward_route_mode(const ForwardArgs &a, cudaStream_t s) {
   const long long D = width_of(a.D, static_cast<Mode>(MODE));
   if (D <= 256) return forward_shape<XT, YT, 1, 1, 8, MODE>(a, s);
-  if constexpr (MODE == SHIFTED) {
-    if (D <= 512) return forward_shape<XT, YT, 1, 2, 4, MODE>(a, s);
-    if (D <= 1024) return forward_shape<XT, YT, 1, 4, 2, MODE>(a, s);
-  } else {
-    if (D <= 512) return forward_shape<XT, YT, 2, 1, 8, MODE>(a, s);
-    if (D <= 768) return forward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
-    if (D <= 1024) return forward_shape<XT, YT, 4, 1, 8, MODE>(a, s);
-  }
+  if (D <= 512) return forward_shape<XT, YT, 2, 1, 8, MODE>(a, s);
+  if (D <= 768) return forward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
+  if (D <= 1024) return forward_shape<XT, YT, 4, 1, 8, MODE>(a, s);
+  if (D <= 1536) return forward_shape<XT, YT, 3, 2, 4, MODE>(a, s);
   if (D <= 2048) return forward_shape<XT, YT, 2, 4, 1, MODE>(a, s);
   if (D <= 4096) return forward_shape<XT, YT, 2, 8, 1, MODE>(a, s);
   if (D <= 8192) return forward_shape<XT, YT, 2, 16, 1, MODE>(a, s);
