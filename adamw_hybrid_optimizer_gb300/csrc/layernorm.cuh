@@ -29,9 +29,10 @@ __device__ __forceinline__ float param_at(const void *p, int dt, int c, float ab
 //   SCALAR   one value at a time: bases or pitches that fit neither of the others
 //   ALIGNED  every row starts on a boundary of a granule, and the width is whole granules
 //   FULL     ALIGNED, and the row gives every thread all of its granules, so that nothing is asked
-//   SHIFTED  rows start `shift` values past a boundary (an odd width); the first and the last granule of a row may be
-//            partial. A row slot sees rows whose index differs by multiples of 8, which all have the same shift, so
-//            its threads' columns stay the same.
+//   SHIFTED  rows start past a boundary (an odd width): a row is a few single values up to the first boundary (the head),
+//            whole granules, and a few single values (the tail). Sixteen threads have one of these each, beside their
+//            granules. A row slot sees rows whose index differs by multiples of 8, which all start alike, so its threads'
+//            columns stay the same.
 enum Mode { SCALAR, ALIGNED, SHIFTED, FULL };
 
 // A granule is 8 values of bf16 or, where a matrix is fp32, 4: an access of one is 16 (8 for bf16 beside fp32) bytes,
@@ -40,44 +41,31 @@ template <typename A, typename B>
 constexpr int granule_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
 
 // The columns of thread t of the T that hold a row, eight to a chunk: PG granules, each T granules after the one
-// before, or in SCALAR single columns T apart.
+// before, or in SCALAR single columns T apart; and in SHIFTED, for some threads, the single column `extra` (else -1).
 template <int MODE_, int GE_, int T_>
 struct Cols {
   static constexpr int MODE = MODE_, GE = MODE_ == SCALAR ? 8 : GE_, PG = 8 / GE, T = T_;
-  int t, D, shift, total, mine, last;   // total: the row's granules; mine: the thread's (SCALAR: its columns); last: the
-                                        // row's last granule as the thread's k PG + j, or -1
-  __device__ __forceinline__ Cols(int t_, int D_, int shift_) : t(t_), D(D_), shift(MODE == SHIFTED ? shift_ : 0) {
-    total = MODE == SCALAR ? D : (D + shift + GE - 1) / GE;
+  int t, D, head, mine, extra;   // mine: the thread's granules (SCALAR: its columns)
+  // start: the row's first value's place, in values
+  __device__ __forceinline__ Cols(int t_, int D_, long long start) : t(t_), D(D_), head(0), extra(-1) {
+    if (MODE == SHIFTED) head = static_cast<int>(-start & (GE - 1));
+    const int total = MODE == SCALAR ? D : (D - head) / GE;
     mine = max((total - t + T - 1) / T, 0);
-    last = (total - 1) % T == t ? (total - 1) / T : -1;
+    if (MODE == SHIFTED) {
+      const int tail = head + total * GE;
+      if (t < 8 && t < head) extra = t;
+      if (t >= 8 && t < 16 && tail + t - 8 < D) extra = tail + t - 8;
+    }
   }
-  __device__ __forceinline__ int granule(int k, int j) const { return (k * PG + j) * T + t; }
-  __device__ __forceinline__ int first(int k, int j) const { return granule(k, j) * GE - shift; }
+  __device__ __forceinline__ int first(int k, int j) const { return ((k * PG + j) * T + t) * GE + head; }
   __device__ __forceinline__ int col(int k, int e) const {
     return MODE == SCALAR ? (8 * k + e) * T + t : first(k, e / GE) + e % GE;
   }
   __device__ __forceinline__ bool has(int k, int j) const {
     return MODE == FULL || (MODE == SCALAR ? 8 * k : k * PG + j) < mine;
   }
-  __device__ __forceinline__ bool edge(int k, int j) const {
-    return MODE == SHIFTED && ((k == 0 && j == 0 && t == 0) || k * PG + j == last);
-  }
   __device__ __forceinline__ bool in(int k, int e) const {   // of a granule that the thread has
-    return MODE == SCALAR ? 8 * k + e < mine : MODE != SHIFTED || (col(k, e) >= 0 && col(k, e) < D);
-  }
-  // SHIFTED: puts `fill` where the row has no column, in the edges of the threads that have them
-  template <int C>
-  __device__ __forceinline__ void fill_edges(Vals<8> *v, float fill) const {
-    if (MODE != SHIFTED || !(t == 0 || last >= 0)) return;
-#pragma unroll
-    for (int k = 0; k < C; ++k)
-#pragma unroll
-      for (int j = 0; j < PG; ++j)
-        if (edge(k, j)) {
-#pragma unroll
-          for (int e = j * GE; e < (j + 1) * GE; ++e)
-            if (!in(k, e)) (e % 2 ? v[k].p[e / 2].y : v[k].p[e / 2].x) = fill;
-        }
+    return MODE == SCALAR ? 8 * k + e < mine : true;
   }
   // SCALAR: pair i of chunk k with zeros where the row has no column
   __device__ __forceinline__ float2 only(int k, int i, float2 v) const {
@@ -87,16 +75,14 @@ struct Cols {
     }
     return v;
   }
-  __device__ __forceinline__ int columns() const {
-    if (MODE == SCALAR) return mine;
-    int n = mine * GE;
-    if (MODE == SHIFTED && mine > 0) {
-      if (t == 0) n -= shift;
-      if (last >= 0) n -= total * GE - shift - D;
-    }
-    return n;
-  }
+  __device__ __forceinline__ int columns() const { return MODE == SCALAR ? mine : mine * GE + (extra >= 0 ? 1 : 0); }
 };
+
+// The single column of a thread of a SHIFTED row
+template <typename XT, typename CT>
+__device__ __forceinline__ float load_extra(const XT *p, const CT &c) {
+  return CT::MODE == SHIFTED && c.extra >= 0 ? load1(p, c.extra) : 0.f;
+}
 
 // A chunk as it lies in memory.
 template <typename XT, int GE>
@@ -114,29 +100,21 @@ struct RawChunk {
   }
 };
 
-// One granule. In SHIFTED an edge is read whole where the part outside the row lies in the rows around (below / above:
-// there are such), whose values are left out later; only the ends of the matrix are read value by value.
-template <typename XT, typename CT>
-__device__ __forceinline__ bool whole_granule(const CT &c, int k, int j, bool below, bool above) {
-  return !c.edge(k, j) || ((c.first(k, j) >= 0 || below) && (c.first(k, j) + CT::GE <= c.D || above));
-}
-template <typename XT, typename CT>
-__device__ __forceinline__ void load_values(const XT *p, const CT &c, int k, int j, Raw<XT, CT::GE> &r) {
-  r.clear();
-#pragma unroll
-  for (int e = 0; e < CT::GE; ++e)
-    if (c.in(k, j * CT::GE + e)) r.put(e, p[c.col(k, j * CT::GE + e)]);
-}
-
 // Columns that the thread does not have read as 0.
 template <typename XT, typename CT>
-__device__ __forceinline__ void load_chunk(const XT *p, const CT &c, int k, bool below, bool above,
-                                           RawChunk<XT, CT::GE> &r) {
+__device__ __forceinline__ void load_chunk(const XT *p, const CT &c, int k, RawChunk<XT, CT::GE> &r) {
 #pragma unroll
   for (int j = 0; j < CT::PG; ++j) {
-    if (!c.has(k, j)) r.g[j].clear();
-    else if (CT::MODE != SCALAR && whole_granule<XT>(c, k, j, below, above)) r.g[j].load(p + c.first(k, j));
-    else load_values(p, c, k, j, r.g[j]);
+    if (CT::MODE != SCALAR && c.has(k, j)) {
+      r.g[j].load(p + c.first(k, j));
+    } else {
+      r.g[j].clear();
+      if constexpr (CT::MODE == SCALAR) {
+#pragma unroll
+        for (int e = 0; e < CT::GE; ++e)
+          if (c.in(k, e)) r.g[j].put(e, p[c.col(k, e)]);
+      }
+    }
   }
 }
 
@@ -154,7 +132,7 @@ __device__ __forceinline__ void store_chunk(XT *p, const CT &c, int k, const Val
 #pragma unroll
   for (int j = 0; j < CT::PG; ++j) {
     if (!c.has(k, j)) continue;
-    if (CT::MODE == SCALAR || c.edge(k, j)) {
+    if constexpr (CT::MODE == SCALAR) {
       store_values(p, c, k, j, o);
     } else {
       Vals<CT::GE> v;
@@ -187,11 +165,11 @@ __device__ __forceinline__ Vals<8> param_chunk(const void *p, int dt, bool wide,
   if ((CT::MODE == ALIGNED || CT::MODE == FULL) && wide) {
     if (dt == MUON_F32) {
       RawChunk<float, CT::GE> r;
-      load_chunk(static_cast<const float *>(p), c, k, false, false, r);
+      load_chunk(static_cast<const float *>(p), c, k, r);
       return r.get();
     }
     RawChunk<__nv_bfloat16, CT::GE> r;
-    load_chunk(static_cast<const __nv_bfloat16 *>(p), c, k, false, false, r);
+    load_chunk(static_cast<const __nv_bfloat16 *>(p), c, k, r);
     return r.get();
   }
 #pragma unroll
@@ -210,20 +188,12 @@ struct Ring {
   __device__ __forceinline__ unsigned char *at(int stage, int k, int j) const {
     return base + ((stage * C + k) * CT::PG + j) * (THREADS * R::BYTES);
   }
-  __device__ __forceinline__ void fetch(const XT *row, const CT &c, int stage, bool below, bool above) const {
+  __device__ __forceinline__ void fetch(const XT *row, const CT &c, int stage) const {
 #pragma unroll
     for (int k = 0; k < C; ++k)
 #pragma unroll
-      for (int j = 0; j < CT::PG; ++j) {
-        if (!c.has(k, j)) continue;
-        if (whole_granule<XT>(c, k, j, below, above)) {
-          copy_async<R::BYTES>(at(stage, k, j), row + c.first(k, j));
-        } else {
-          R r;
-          load_values(row, c, k, j, r);
-          r.store(reinterpret_cast<XT *>(at(stage, k, j)));
-        }
-      }
+      for (int j = 0; j < CT::PG; ++j)
+        if (c.has(k, j)) copy_async<R::BYTES>(at(stage, k, j), row + c.first(k, j));
   }
   __device__ __forceinline__ Vals<8> get(int k, int stage) const {
     RawChunk<XT, CT::GE> r;
@@ -348,9 +318,6 @@ inline Mode mode_of(bool bases, bool pitches, long long ld, long long D) {
   if (!bases || !pitches || D < 8) return SCALAR;
   return ld % 8 == 0 && D % 8 == 0 ? ALIGNED : SHIFTED;
 }
-
-// The columns that a row's threads have to hold: a SHIFTED row may have a granule more.
-inline long long width_of(long long D, Mode mode) { return D + (mode == SHIFTED ? 7 : 0); }
 
 }  // namespace
 }  // namespace muon

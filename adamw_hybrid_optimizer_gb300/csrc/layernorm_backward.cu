@@ -16,7 +16,7 @@ namespace muon {
 namespace {
 
 constexpr int REDUCE_COLS = 32;
-constexpr int REDUCE_WARPS = 32;
+constexpr int REDUCE_WARPS = 16;
 
 struct BackwardArgs {
   const void *dy, *x, *w;
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
   const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T, D = a.D;
   const long long step = static_cast<long long>(gridDim.x) * R;
   long long row = static_cast<long long>(blockIdx.x) * R + slot;
-  const CT c(t, D, static_cast<int>((row * a.ldx) & (CT::GE - 1)));
+  const CT c(t, D, row * a.ldx);
   Exchange<W, R> exchange{red, slot, t / 32, 0};
   const Ring<XT, CT, C, THREADS> ring_x{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
   const Ring<YT, CT, C, THREADS> ring_dy{shared + B::RING_X + threadIdx.x * Raw<YT, CT::GE>::BYTES};
@@ -109,15 +109,14 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
   RawChunk<YT, CT::GE> rdy[B::RING ? 1 : C];
   auto fetch = [&](int stage) {
     if (fetched < a.N) {
-      const bool below = fetched > 0, above = fetched + 1 < a.N;
       if constexpr (B::RING) {
-        ring_x.fetch(x, c, stage, below, above);
-        ring_dy.fetch(dy, c, stage, below, above);
+        ring_x.fetch(x, c, stage);
+        ring_dy.fetch(dy, c, stage);
       } else {
 #pragma unroll
         for (int k = 0; k < C; ++k) {
-          load_chunk(x, c, k, below, above, rx[k]);
-          load_chunk(dy, c, k, below, above, rdy[k]);
+          load_chunk(x, c, k, rx[k]);
+          load_chunk(dy, c, k, rdy[k]);
         }
       }
     }
@@ -126,10 +125,16 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
     x += x_step;
     dy += dy_step;
   };
-  float mean = 0.f, rstd = 0.f;
+  const float w_extra = MODE == SHIFTED && c.extra >= 0 ? param_at(a.w, a.wdt, c.extra, 1.f) : 0.f;
+  float aw_extra = 0.f, ab_extra = 0.f;
+  const XT *x_row = x;
+  const YT *dy_row = dy;
+  float mean = 0.f, rstd = 0.f, x_next = 0.f, dy_next = 0.f;
   if (row < a.N) {
     mean = a.mean[row];
     rstd = a.rstd[row];
+    x_next = load_extra(x_row, c);
+    dy_next = load_extra(dy_row, c);
   }
   if constexpr (B::AHEAD) fetch(0);
   if constexpr (B::RING && STAGES == 3) fetch(1);
@@ -140,9 +145,16 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
     const bool live = R == 1 || row < a.N;
     if constexpr (!B::AHEAD) fetch(0);
     const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+    const float x_extra = x_next, dy_extra = dy_next;
+    x_row += x_step;
+    dy_row += dy_step;
     if (row + step < a.N) {
       mean = a.mean[row + step];
       rstd = a.rstd[row + step];
+      if (MODE == SHIFTED) {
+        x_next = load_extra(x_row, c);
+        dy_next = load_extra(dy_row, c);
+      }
     }
     Vals<8> xh[C], g[C];
     if constexpr (B::RING) {
@@ -163,10 +175,17 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
       }
       if constexpr (B::AHEAD) fetch(0);
     }
-    c.template fill_edges<C>(xh, -m2.x);   // xh = 0 there
-    c.template fill_edges<C>(g, 0.f);
     float2 s1 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
+    float xh_extra = 0.f, g_extra = 0.f;
     if (live) {
+      if (MODE == SHIFTED && c.extra >= 0) {
+        xh_extra = (x_extra + m2.x) * r2.x;
+        aw_extra = fmaf(dy_extra, xh_extra, aw_extra);
+        ab_extra += dy_extra;
+        g_extra = dy_extra * w_extra;
+        s1.x = g_extra;
+        s2.x = g_extra * xh_extra;
+      }
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const Vals<8> w = weight.get(c, k);
@@ -197,6 +216,7 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
             g[k].p[i] = __fmul2_rn(__ffma2_rn(xh[k].p[i], c2, __fadd2_rn(g[k].p[i], c1)), r2);
           store_chunk(dx, c, k, g[k]);
         }
+        if (MODE == SHIFTED && c.extra >= 0) store1(dx, c.extra, fmaf(xh_extra, c2.x, g_extra + c1.x) * r2.x);
       }
       dx += dx_step;
     }
@@ -211,6 +231,10 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
       store_sums(pw, c, k, aw[k]);
       store_sums(pb, c, k, ab[k]);
     }
+    if (MODE == SHIFTED && c.extra >= 0) {
+      pw[c.extra] = aw_extra;
+      pb[c.extra] = ab_extra;
+    }
   } else {   // the block's rows are added in order, where the ring was
     float *join = reinterpret_cast<float *>(shared);
     const int pitch = (D + 3) & ~3;
@@ -219,6 +243,7 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < C; ++k) store_sums(join + slot * pitch, c, k, z == 0 ? aw[k] : ab[k]);
+      if (MODE == SHIFTED && c.extra >= 0) join[slot * pitch + c.extra] = z == 0 ? aw_extra : ab_extra;
       __syncthreads();
       for (int j = threadIdx.x; j < D; j += THREADS) {
         float s = 0.f;
@@ -278,7 +303,7 @@ __global__ void __launch_bounds__(256) layernorm_columns_kernel(const BackwardAr
   a.part[(a.parts + blockIdx.y) * a.ldp + c] = sb;
 }
 
-// dw (blockIdx.y = 0) and db (1): 32 columns per block, warp w adds partial rows w, w + 32, ...
+// dw (blockIdx.y = 0) and db (1): 32 columns per block, warp w adds partial rows w, w + 16, ...
 __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(const float *part, long long parts,
                                                                              long long ldp, int D, void *dw, void *db,
                                                                              int gdt, int accumulate) {
@@ -317,8 +342,7 @@ __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(con
 struct Shape {
   int C, W, R;
 };
-Shape shape_of(long long columns, Mode mode) {
-  const long long D = width_of(columns, mode);
+Shape shape_of(long long D, Mode mode) {
   if (mode == SCALAR) return D <= 1024 ? Shape{1, 4, 2} : Shape{2, D <= 8192 ? 16 : 32, 1};
   if (D <= 256) return {1, 1, 8};
   if (D <= 512) return {2, 1, 8};
@@ -328,12 +352,11 @@ Shape shape_of(long long columns, Mode mode) {
   for (int W : {4, 8, 16}) if (D <= 512 * W) return {2, W, 1};
   return {2, 32, 1};
 }
-bool long_row(long long D, Mode mode) { return width_of(D, mode) > MAX_ROW; }
 
 // Blocks of the backward pass, each of which leaves one partial row of dw and db: as many as the GPU holds at once,
 // so that there are few partial rows to add. In SHIFTED a slot's rows lie multiples of eight apart.
 long long parts_for(long long N, long long D, Mode mode) {
-  if (long_row(D, mode)) return std::max(1LL, std::min(N, 64LL));
+  if (D > MAX_ROW) return std::max(1LL, std::min(N, 64LL));
   const Shape h = shape_of(D, mode);
   const long long resident = std::max(1, (h.C == 1 ? 768 : 512) / (h.W * h.R * 32));
   const long long blocks = std::max(1LL, std::min((N + h.R - 1) / h.R, 152 * resident));
@@ -375,7 +398,7 @@ cudaError_t backward_route_mode(const BackwardArgs &a, cudaStream_t s) {
 
 template <typename XT, typename YT>
 cudaError_t backward_route(const BackwardArgs &a, Mode mode, cudaStream_t s) {
-  if (long_row(a.D, mode)) {
+  if (a.D > MAX_ROW) {
     // the columns first: dx may take the place of dy or x
     if (a.part != nullptr) {
       const dim3 cgrid(static_cast<unsigned>((a.D + 255) / 256), static_cast<unsigned>(a.parts));

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
   const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T;
   const long long step = static_cast<long long>(gridDim.x) * R;
   long long row = static_cast<long long>(blockIdx.x) * R + slot;
-  const CT c(t, a.D, static_cast<int>((row * a.ldx) & (CT::GE - 1)));
+  const CT c(t, a.D, row * a.ldx);
   Exchange<W, R> exchange{red, slot, t / 32, 0};
   const Ring<XT, CT, C, F::THREADS> ring{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
   using PT = typename F::PT;
@@ -64,16 +64,20 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
   auto fetch = [&](int stage) {
     if (fetched < a.N) {
       if constexpr (F::RING) {
-        ring.fetch(x, c, stage, fetched > 0, fetched + 1 < a.N);
+        ring.fetch(x, c, stage);
       } else {
 #pragma unroll
-        for (int k = 0; k < C; ++k) load_chunk(x, c, k, false, false, raw[k]);
+        for (int k = 0; k < C; ++k) load_chunk(x, c, k, raw[k]);
       }
     }
     if constexpr (F::RING) copy_async_commit();
     fetched += step;
     x += x_step;
   };
+  const float w_extra = MODE == SHIFTED && c.extra >= 0 ? param_at(a.w, a.wdt, c.extra, 1.f) : 0.f;
+  const float b_extra = MODE == SHIFTED && c.extra >= 0 ? param_at(a.b, a.wdt, c.extra, 0.f) : 0.f;
+  const XT *x_row = x;
+  float x_next = row < a.N ? load_extra(x_row, c) : 0.f;
   fetch(0);
   if constexpr (F::RING && STAGES == 3) fetch(1);
   weight.init(c, slot);
@@ -100,16 +104,18 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
       for (int k = 0; k < C; ++k) v[k] = raw[k].get();
       fetch(0);
     }
-    c.template fill_edges<C>(v, 0.f);
-    float2 s = make_float2(0.f, 0.f);
+    const float x_extra = x_next;
+    x_row += x_step;
+    if (MODE == SHIFTED && row + step < a.N) x_next = load_extra(x_row, c);
+    float2 s = make_float2(x_extra, 0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (c.has(k, 2 * i / CT::GE)) s = __fadd2_rn(s, c.only(k, i, v[k].p[i]));
     const float own = warp_sum(s.x + s.y) * inv_n;
-    c.template fill_edges<C>(v, own);   // at no distance
-    float2 q = make_float2(0.f, 0.f);
+    const float d_extra = MODE == SHIFTED && c.extra >= 0 ? x_extra - own : 0.f;
+    float2 q = make_float2(d_extra * d_extra, 0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k)
 #pragma unroll
@@ -140,6 +146,7 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
           v[k].p[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[k].p[i], m2), r2), w.p[i], b.p[i]);
         store_chunk(y, c, k, v[k]);
       }
+      if (MODE == SHIFTED && c.extra >= 0) store1(y, c.extra, fmaf((x_extra - mean) * rstd, w_extra, b_extra));
     }
     y += y_step;
   }
@@ -202,7 +209,7 @@ cudaError_t forward_shape(const ForwardArgs &a, cudaStream_t s) {
 // which leave a multiprocessor half the warps beside the weights in shared memory).
 template <typename XT, typename YT, int MODE>
 cudaError_t forward_route_mode(const ForwardArgs &a, cudaStream_t s) {
-  const long long D = width_of(a.D, static_cast<Mode>(MODE));
+  const int D = a.D;
   if (D <= 256) return forward_shape<XT, YT, 1, 1, 8, MODE>(a, s);
   if (D <= 512) return forward_shape<XT, YT, 2, 1, 8, MODE>(a, s);
   if (D <= 768) return forward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
@@ -216,7 +223,7 @@ cudaError_t forward_route_mode(const ForwardArgs &a, cudaStream_t s) {
 
 template <typename XT, typename YT>
 cudaError_t forward_route(const ForwardArgs &a, Mode mode, cudaStream_t s) {
-  if (width_of(a.D, mode) > MAX_ROW) {
+  if (a.D > MAX_ROW) {
     const dim3 grid(static_cast<unsigned>(std::min<long long>(a.N, device_sm_count() * 2))), block(LONG_THREADS);
     return launch_pdl(layernorm_forward_long_kernel<XT, YT>, grid, block, 0, s, a);
   }
