@@ -32,7 +32,8 @@ namespace muon {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int FWD_BLOCKS = 5;    // resident blocks of the lookup
+constexpr int FWD_BLOCKS = 5, CUT_BLOCKS = 3;    // resident blocks of the lookup's kernels
+constexpr int CUT_STAGES = 3;
 constexpr int LOG_UNIT = 7, UNIT = 1 << LOG_UNIT;   // granules per warp and turn of the lookup: four per lane
 constexpr int SUM_COLS = 256;    // columns per warp of the gradient's sums: 8 per lane
 constexpr int GROUP = 32;        // sorted positions per warp of the gradient's sums
@@ -69,6 +70,20 @@ __device__ __forceinline__ Raw<T, GE> cut(const Raw<T, GE> &lo, const Raw<T, GE>
 #pragma unroll
   for (int i = 0; i < W; ++i) r.w[i] = sizeof(T) == 2 && (d & 1) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
   return r;
+}
+
+// The granule of a matrix (base aligned, `total` values from its first to its last) that starts at value `from`, a
+// multiple of GE. Values outside the matrix are left 0.
+template <typename T, int GE>
+__device__ __forceinline__ void load_granule(const T *base, long long from, long long total, Raw<T, GE> &r) {
+  if (from >= 0 && from + GE <= total) {
+    r.load(base + from);
+    return;
+  }
+  r.clear();
+#pragma unroll
+  for (int e = 0; e < GE; ++e)
+    if (from + e >= 0 && from + e < total) r.put(e, base[from + e]);
 }
 
 // GE values of a matrix (base aligned, `total` values from its first to its last) from value `at` on: two aligned
@@ -108,28 +123,30 @@ struct LookupArgs {
   const void *ids, *table;
   void *out;
   long long ldt, ldo, n, V;
-  int itype, D, per_row, tiles, log_rows;   // granules per row (a power of two below UNIT), units per long row, and
-  float scale;                              // log2 of the rows per unit of short ones
+  int itype, D, tiles, log_rows;   // units per long row; log2 of the rows per unit of short ones
+  float scale;
 };
 
-// Warps take units in turn: 128 granules of a long row, or of as many short rows as fit, four granules per lane. All
-// loads of a unit are in flight before the first is used, and the ids of the next unit are loaded under them, so that
-// a unit waits for one latency, not two. ALIGNED: every row starts on a granule and has whole ones.
-template <typename TT, typename OT, bool ALIGNED>
+// Warps take units in turn: 128 granules of a long row, or of as many short rows as fit, four granules per lane.
+//
+// Rows that start on a granule and have whole ones: all loads of a unit are in flight before the first is used, and the
+// ids of the next unit are loaded under them, so that a unit waits for one latency, not two.
+template <typename TT, typename OT>
 __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(const LookupArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
   constexpr int GE = granule_of<TT, OT>(), U = UNIT / 32;
   const int lane = threadIdx.x % 32;
-  const long long units = a.tiles > 1 ? a.n * a.tiles : (a.n + (1 << a.log_rows) - 1) >> a.log_rows;
+  const bool many = a.tiles == 1;
+  const long long units = many ? (a.n + (1 << a.log_rows) - 1) >> a.log_rows : a.n * a.tiles;
   const long long warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
   const TT *table = static_cast<const TT *>(a.table);
-  // row and granule of the lane's granule q of unit u
+  // row and first column of the lane's granule q of unit u
   auto row_of = [&](long long u, int q) {
-    return a.tiles > 1 ? u / a.tiles : (u << a.log_rows) + ((q * 32 + lane) >> (LOG_UNIT - a.log_rows));
+    return many ? (u << a.log_rows) + ((q * 32 + lane) >> (LOG_UNIT - a.log_rows)) : u / a.tiles;
   };
-  auto granule = [&](long long u, int q) {
-    return a.tiles > 1 ? static_cast<int>(u % a.tiles) * UNIT + q * 32 + lane : (q * 32 + lane) & (a.per_row - 1);
+  auto first_of = [&](long long u, int q) {
+    return GE * (many ? (q * 32 + lane) & ((UNIT >> a.log_rows) - 1) : static_cast<int>(u % a.tiles) * UNIT + q * 32 + lane);
   };
   auto ids_of = [&](long long u, long long *id) {
 #pragma unroll
@@ -142,56 +159,123 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(
   ids_of(u, next);
   for (; u < units; u += warps) {
     long long id[U];
+    Raw<TT, GE> r[U];
 #pragma unroll
-    for (int q = 0; q < U; ++q) id[q] = next[q] < 0 || next[q] >= a.V ? -1 : next[q];
-    if constexpr (ALIGNED) {
-      Raw<TT, GE> r[U];
+    for (int q = 0; q < U; ++q) {
+      id[q] = next[q] < 0 || next[q] >= a.V ? -1 : next[q];
+      r[q].clear();
+      const int c = first_of(u, q);
+      if (id[q] >= 0 && c < a.D) r[q].load(table + id[q] * a.ldt + c);
+    }
+    ids_of(u + warps, next);
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        r[q].clear();
-        const int c = granule(u, q) * GE;
-        if (id[q] >= 0 && c < a.D) r[q].load(table + id[q] * a.ldt + c);
-      }
-      ids_of(u + warps, next);
+    for (int q = 0; q < U; ++q) {
+      const long long row = row_of(u, q);
+      const int c = first_of(u, q);
+      if (row >= a.n || c >= a.D) continue;
+      Vals<GE> o = r[q].get();
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const long long row = row_of(u, q);
-        const int c = granule(u, q) * GE;
-        if (row >= a.n || c >= a.D) continue;
-        Vals<GE> o = r[q].get();
+      for (int i = 0; i < GE / 2; ++i)
+        o.p[i] = id[q] < 0 ? make_float2(0.f, 0.f) : __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
+      store_vals(static_cast<OT *>(a.out) + row * a.ldo + c, o);
+    }
+  }
+}
+
+// Other rows: a unit's granules are those of the table around the output's, one more than it writes. The granules of the
+// next units are on their way to the warp's ring in shared memory, and the ids of the one after on theirs, while a unit
+// is stored. (65536 rows of 771 bf16: 49 us, and 76 us with two loads per lane and granule into registers; but where
+// rows are aligned the ring takes 194 us for 65536 rows of 4096, and registers 138 us.)
+template <typename TT, typename OT>
+__global__ void __launch_bounds__(THREADS, CUT_BLOCKS) embedding_forward_cut_kernel(const LookupArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  constexpr int GE = granule_of<TT, OT>(), U = UNIT / 32, WARPS = THREADS / 32, S = CUT_STAGES;
+  constexpr int B = Raw<TT, GE>::BYTES;
+  extern __shared__ __align__(16) unsigned char shared[];
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  unsigned char *ring = shared + w * (S * UNIT * B);
+  int *kept = reinterpret_cast<int *>(shared + WARPS * S * UNIT * B) + threadIdx.x;   // the ids of units in the ring
+  const bool many = a.tiles == 1;
+  const long long units = many ? (a.n + (1 << a.log_rows) - 1) >> a.log_rows : a.n * a.tiles;
+  const long long warps = static_cast<long long>(gridDim.x) * WARPS, total = (a.V - 1) * a.ldt + a.D;
+  const TT *table = static_cast<const TT *>(a.table);
+  const int per_row = UNIT >> (many ? a.log_rows : 0);
+  // row of the lane's granule q of unit u, the granule's place among the row's of the unit, and its first column
+  auto row_of = [&](long long u, int q) {
+    return many ? (u << a.log_rows) + ((q * 32 + lane) >> (LOG_UNIT - a.log_rows)) : u / a.tiles;
+  };
+  auto place = [&](int q) { return (q * 32 + lane) & (per_row - 1); };
+  auto first_of = [&](long long u, long long row, int q) {
+    const int g = (many ? 0 : static_cast<int>(u % a.tiles) * (UNIT - 1)) + place(q);
+    return g * GE - static_cast<int>((row * a.ldo) & (GE - 1));
+  };
+  auto ids_of = [&](long long u, int *id) {
 #pragma unroll
-        for (int i = 0; i < GE / 2; ++i)
-          o.p[i] = id[q] < 0 ? make_float2(0.f, 0.f) : __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
-        store_vals(static_cast<OT *>(a.out) + row * a.ldo + c, o);
-      }
-    } else {
-      Window<TT, GE> r[U];
-      auto first_of = [&](int q) {   // the granules of the row that is written
-        return granule(u, q) * GE - static_cast<int>((row_of(u, q) * a.ldo) & (GE - 1));
-      };
+    for (int q = 0; q < U; ++q) {
+      const long long r = row_of(u, q);
+      const long long v = u < units && r < a.n ? load_id(a.ids, a.itype, r) : -1;
+      id[q] = v >= 0 && v < a.V ? static_cast<int>(v) : -1;
+    }
+  };
+  auto fetch = [&](long long u, int stage, const int *id) {
 #pragma unroll
-      for (int q = 0; q < U; ++q)
-        if (id[q] >= 0 && first_of(q) < a.D)
-          r[q].load(table, id[q] * a.ldt + first_of(q), (a.V - 1) * a.ldt + a.D);
-      ids_of(u + warps, next);
-#pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const long long row = row_of(u, q);
-        const int c = first_of(q);
-        if (row >= a.n || c >= a.D) continue;
-        Vals<GE> o;
-#pragma unroll
-        for (int i = 0; i < GE / 2; ++i) o.p[i] = make_float2(0.f, 0.f);
-        if (id[q] >= 0) {
-          o = r[q].get();
-#pragma unroll
-          for (int i = 0; i < GE / 2; ++i) o.p[i] = __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
+    for (int q = 0; q < U; ++q) {
+      kept[(stage * U + q) * THREADS] = id[q];
+      if (id[q] < 0) continue;
+      const int c = first_of(u, row_of(u, q), q);
+      unsigned char *slot = ring + (stage * UNIT + q * 32 + lane) * B;
+      const long long at = id[q] * a.ldt + c;
+      if (c < a.D + GE) {
+        const long long from = at & ~static_cast<long long>(GE - 1);
+        if (from >= 0 && from + GE <= total) {
+          copy_async<B>(slot, table + from);
+        } else {
+          Raw<TT, GE> r;
+          load_granule(table, from, total, r);
+          r.store(reinterpret_cast<TT *>(slot));
         }
-        OT *dst = static_cast<OT *>(a.out) + row * a.ldo;
-        if (c >= 0 && c + GE <= a.D) store_vals(dst + c, o);
-        else store_edge(dst, c, a.D, o);
       }
     }
+    copy_async_commit();
+  };
+  long long u = static_cast<long long>(blockIdx.x) * WARPS + w;
+  int id[U];
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k) {
+    ids_of(u + k * warps, id);
+    fetch(u + k * warps, k, id);
+  }
+  ids_of(u + (S - 1) * warps, id);
+  int stage = 0;
+  for (; u < units; u += warps) {
+    copy_async_wait<S - 2>();
+    __syncwarp();
+    // the place of the unit before this one, which all lanes have read
+    fetch(u + (S - 1) * warps, stage == 0 ? S - 1 : stage - 1, id);
+    ids_of(u + S * warps, id);
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const long long row = row_of(u, q);
+      const int c = first_of(u, row, q), at = kept[(stage * U + q) * THREADS];
+      if (row >= a.n || c >= a.D || place(q) == per_row - 1) continue;
+      const unsigned char *slot = ring + (stage * UNIT + q * 32 + lane) * B;
+      Vals<GE> o;
+#pragma unroll
+      for (int i = 0; i < GE / 2; ++i) o.p[i] = make_float2(0.f, 0.f);
+      if (at >= 0) {
+        Raw<TT, GE> lo, hi;
+        lo.load(reinterpret_cast<const TT *>(slot));
+        hi.load(reinterpret_cast<const TT *>(slot + B));
+        o = cut(lo, hi, static_cast<int>((at * a.ldt + c) & (GE - 1))).get();
+#pragma unroll
+        for (int i = 0; i < GE / 2; ++i) o.p[i] = __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
+      }
+      OT *dst = static_cast<OT *>(a.out) + row * a.ldo;
+      if (c >= 0 && c + GE <= a.D) store_vals(dst + c, o);
+      else store_edge(dst, c, a.D, o);
+    }
+    stage = stage == S - 1 ? 0 : stage + 1;
   }
 }
 
@@ -692,8 +776,8 @@ __global__ void __launch_bounds__(THREADS, 2) embedding_sum_kernel(const SumArgs
 #pragma unroll
       for (int q = 0; q < U; ++q)
         if (i0 + q < end) {
-          const unsigned pos = at(p0, p1, i0 + q);
-          r[q].load(a, pos, tile, lane, ACCESS == CUT ? shift_of<ACCESS, GE>(a, at(k0, k1, i0 + q)) : 0);
+          const unsigned pos = at(p0, p1, i0 + q), k = ACCESS == CUT ? at(k0, k1, i0 + q) : 0u;
+          r[q].load(a, pos, tile, lane, shift_of<ACCESS, GE>(a, k));
         }
     };
     Vals<8> acc;
@@ -835,16 +919,24 @@ cudaError_t launch_lookup(LookupArgs a, cudaStream_t s) {
     return launch_pdl(embedding_forward_scalar_kernel<TT, OT>, dim3(static_cast<unsigned>(blocks)), block, 0, s, a);
   }
   const bool aligned = a.D % GE == 0 && a.ldt % GE == 0 && a.ldo % GE == 0;
-  const int granules = (a.D + (aligned ? 0 : GE - 1) + GE - 1) / GE;
-  a.per_row = 8;
-  while (a.per_row < granules && a.per_row < UNIT) a.per_row *= 2;
-  a.tiles = (granules + UNIT - 1) / UNIT;
+  // a row's granules of a unit: where it is cut out, one more than the most that it can touch
+  const int granules = aligned ? a.D / GE : (a.D + 2 * (GE - 1)) / GE + 1;
+  const int writes = aligned ? UNIT : UNIT - 1;
+  int per_row = 8;
+  while (per_row < granules && per_row < UNIT) per_row *= 2;
+  a.tiles = granules <= UNIT ? 1 : (granules - (aligned ? 0 : 1) + writes - 1) / writes;
   a.log_rows = 0;
-  while ((a.per_row << a.log_rows) < UNIT) ++a.log_rows;
+  while ((per_row << a.log_rows) < UNIT) ++a.log_rows;
   const long long units = a.tiles > 1 ? a.n * a.tiles : (a.n + (1 << a.log_rows) - 1) >> a.log_rows;
-  const dim3 grid(static_cast<unsigned>(std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * FWD_BLOCKS)));
-  return aligned ? launch_pdl(embedding_forward_kernel<TT, OT, true>, grid, block, 0, s, a)
-                 : launch_pdl(embedding_forward_kernel<TT, OT, false>, grid, block, 0, s, a);
+  auto grid = [&](int resident) {
+    return dim3(static_cast<unsigned>(std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * resident)));
+  };
+  if (aligned) return launch_pdl(embedding_forward_kernel<TT, OT>, grid(FWD_BLOCKS), block, 0, s, a);
+  constexpr size_t smem = THREADS * CUT_STAGES * (UNIT / 32) * (Raw<TT, GE>::BYTES + 4);
+  static const cudaError_t allowed = cudaFuncSetAttribute(
+      embedding_forward_cut_kernel<TT, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (allowed != cudaSuccess) return allowed;
+  return launch_pdl(embedding_forward_cut_kernel<TT, OT>, grid(CUT_BLOCKS), block, smem, s, a);
 }
 
 muon_status launch_sort(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
@@ -889,7 +981,7 @@ muon_status launch_sort(const void *ids, int itype, long long n, long long V, lo
 }
 
 // The sort in one cluster (n <= CS_BLOCKS * CS_CHUNK) and the zeroes beside it (z.rows = 0: none). Blocks of up to 2048
-// items each while there are eight: a block's rounds cost more than the cluster's barriers.
+// items each while there are sixteen of them: a block's rounds cost more than the cluster's barriers.
 muon_status launch_prepare(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
                            const EmbeddingLayout &L, const ZeroArgs &z, const unsigned **key, const unsigned **pos,
                            cudaStream_t s) {
@@ -911,8 +1003,7 @@ muon_status launch_prepare(const void *ids, int itype, long long n, long long V,
   a.list_count = reinterpret_cast<unsigned *>(ws + L.list);
   a.n = static_cast<int>(n);
   a.blocks = 1;
-  while (a.blocks < 8 && a.blocks * 2048 < n) a.blocks *= 2;
-  while (a.blocks < CS_BLOCKS && a.blocks * CS_CHUNK < n) a.blocks *= 2;
+  while (a.blocks < CS_BLOCKS && a.blocks * 2048 < n) a.blocks *= 2;
   a.chunk = (a.n + a.blocks - 1) / a.blocks;
   a.passes = (key_bits + MAX_DIGIT_BITS - 1) / MAX_DIGIT_BITS;
   a.bits = (key_bits + a.passes - 1) / a.passes;
@@ -953,6 +1044,7 @@ muon_status launch_zero(const ZeroArgs &z, cudaStream_t s) {
 
 template <typename OT, typename GT, int ACCESS>
 muon_status launch_sums(SumArgs a, cudaStream_t s) {
+  // CUT: a row reaches up to GE - 1 columns past its boundary
   a.tiles = (a.D + (ACCESS == CUT ? granule_of<OT, GT>() - 1 : 0) + SUM_COLS - 1) / SUM_COLS;
   const long long sms = device_sm_count();
   const long long units = static_cast<long long>(a.groups) * a.tiles;
