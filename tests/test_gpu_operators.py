@@ -466,6 +466,41 @@ def test_distill_masks_and_special_values(L, V):
     assert np.isfinite(got[others]).all() and np.isfinite(f64(d)[others]).all()
 
 
+# V, K and how often a dozen rows are repeated: a multiprocessor has several rows of each of these sizes
+@pytest.mark.parametrize("V,K,times", [(700, 6, 850), (1000, 64, 420), (1003, 64, 420), (9001, 33, 110), (14000, 300, 110),
+                                       (20011, 64, 60), (33000, 40, 30), (50304, 64, 30), (50303, 1024, 15)])
+@pytest.mark.parametrize("zdt,ddt", DTYPES)
+def test_distill_many_rows(L, V, K, times, zdt, ddt):
+    N, T = 12, 2.0
+    z, idx, t, w = distill_inputs(N, V, K, zdt, F, torch.int64, 71)
+    z[3], w[3] = float("nan"), 0.0
+    z[4], idx[4] = float("inf"), -1
+    z[5][K:] = -float("inf")
+    idx[5] = torch.arange(K)
+    z[5][:K] = torch.arange(K) % 7
+    r = ops.distill(f64(z), idx.numpy(), f64(t), T, f64(w))
+    e_loss, e_l, e_d = distill_tols(r, z, idx, t, T, f64(w), V)
+    args = (idx.to(DEV).repeat(times, 1), t.to(DEV).repeat(times, 1), T, w.to(DEV).repeat(times), 1.0)
+    ld = V if V % 8 else V + 8
+    buf = torch.full((N * times, ld), float("nan"), dtype=zdt, device=DEV)
+    pz = buf[:, :V]
+    pz.copy_(z.to(DEV).repeat(times, 1))
+    d = torch.full((N * times, ld), float("nan"), dtype=ddt, device=DEV)[:, :V]
+    losses, stats = torch.empty(N * times, device=DEV), torch.empty((N * times, 2), device=DEV)
+    L.distill_forward_backward(pz, *args, losses, stats, d)
+    assert np.all(np.abs(f64(losses[:N]) - r["losses"]) <= e_loss + 4 * U * np.abs(r["losses"]))
+    assert np.all(np.abs(f64(stats[:N])[:, 1] - r["stats"][:, 1]) <= e_l)
+    assert np.all(np.abs(f64(d[:N]) - r["dlogits"]) <= store_tol(r["dlogits"], ddt) + 2 * e_d) and gaps_untouched(d)
+    last = (times - 1) * N                # elsewhere a row may start elsewhere past a boundary, and sum in another order
+    assert np.all(np.abs(f64(losses).reshape(times, N) - r["losses"]) <= e_loss + 4 * U * np.abs(r["losses"]))
+    for i in (N, last // 2 // N * N, last):
+        assert np.all(np.abs(f64(d[i:i + N]) - r["dlogits"]) <= store_tol(r["dlogits"], ddt) + 2 * e_d)
+    if zdt == ddt:
+        again, s2 = torch.empty_like(losses), torch.empty_like(stats)
+        L.distill_forward_backward(pz, *args, again, s2, pz)
+        assert torch.equal(pz, d) and torch.equal(again, losses) and torch.equal(s2, stats)
+
+
 def test_distill_gradient_matches_differences(L):
     """fp32 gradient along a random direction against central differences of the fp64 loss."""
     N, V, K, T = 5, 300, 7, 2.0
