@@ -28,12 +28,13 @@ template <typename XT, typename YT, int C, int W, int R, int MODE>
 struct Forward {
   static constexpr int T = W * 32, THREADS = T * R;
   using CT = Cols<MODE, granule_of<XT, YT>(), T>;
-  static constexpr bool RING = MODE != SCALAR, SHARED = RING && C > 1 && C * T * 8 <= 8192;
-  using PT = Params<CT, C, THREADS, SHARED>;
+  static constexpr bool RING = MODE != SCALAR;
   static constexpr int STAGES = C * T * 8 * sizeof(XT) <= 16384 ? 3 : 2;
   static constexpr int ROWS = RING ? STAGES * C * 8 * sizeof(XT) * THREADS : 0;   // bytes of the ring
+  static constexpr bool SHARED = RING && C > 1 && ROWS + 64 * C * T <= 200 * 1024;   // the weights, beside the ring
+  using PT = Params<CT, C, THREADS, SHARED>;
   static constexpr size_t BYTES = static_cast<size_t>(ROWS) + 2 * PT::BYTES;
-  static constexpr int by_registers = C == 4 ? (T <= 128 ? 768 : T <= 256 ? 512 : 1024) : C == 3 ? 768 : 1024;
+  static constexpr int by_registers = C >= 3 ? 768 : 1024;   // threads
   static constexpr int BLOCKS = std::max(1, by_registers / THREADS);   // of a multiprocessor
 };
 
@@ -205,8 +206,9 @@ cudaError_t forward_shape(const ForwardArgs &a, cudaStream_t s) {
 
 // Rows of up to 1024 columns: a warp each, eight to a block, since the shuffles and the exchange of a row cost a thread
 // the same whatever it holds (65536 x 768 bf16: 36 us, and 41 us with three warps to a row). Longer rows: two chunks of
-// eight columns per thread, and four beyond 8192 columns (65536 x 4096 bf16: 161 us with two, 164 to 195 us with four,
-// which leave a multiprocessor half the warps beside the weights in shared memory).
+// eight columns per thread, or three up to 12288 (65536 x 4096 bf16: 161 us with two, 164 to 195 us with four, which leave
+// a multiprocessor half the warps beside the weights in shared memory; 8192 x 12000 bf16: 79 us with three chunks, 84 us
+// with two and 32 warps, and 128 us with four and the weights from L2; 8192 x 16384: 95 us, and 131 us with four).
 template <typename XT, typename YT, int MODE>
 cudaError_t forward_route_mode(const ForwardArgs &a, cudaStream_t s) {
   const int D = a.D;
@@ -218,7 +220,8 @@ cudaError_t forward_route_mode(const ForwardArgs &a, cudaStream_t s) {
   if (D <= 2048) return forward_shape<XT, YT, 2, 4, 1, MODE>(a, s);
   if (D <= 4096) return forward_shape<XT, YT, 2, 8, 1, MODE>(a, s);
   if (D <= 8192) return forward_shape<XT, YT, 2, 16, 1, MODE>(a, s);
-  return forward_shape<XT, YT, 4, 16, 1, MODE>(a, s);
+  if (D <= 12288) return forward_shape<XT, YT, 3, 16, 1, MODE>(a, s);
+  return forward_shape<XT, YT, 2, 32, 1, MODE>(a, s);
 }
 
 template <typename XT, typename YT>
