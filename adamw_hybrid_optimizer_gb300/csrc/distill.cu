@@ -43,7 +43,7 @@ struct DistillArgs {
   float *losses, *stats;      // stats: N x 2 (m, l), written by the forward forms, read by backward
   void *dz;
   long long ldz, ldd, N;
-  int V, K, itype, tdt, slices;
+  int V, K, itype, tdt, slices, bits;   // bits: of the table of the teacher's indices
   float inv_t, temp, grad_scale;
 };
 
@@ -265,6 +265,47 @@ __device__ __forceinline__ Teacher teacher_at(void *smem, int K) {
 }
 constexpr size_t teacher_bytes(int K) { return static_cast<size_t>((K + 3) & ~3) * 12; }
 
+// After them the forms that write the gradient of short rows (TABLE) have a flag that an index occurs twice and a table of
+// the indices, 2^bits >= 2 K places of which -1 are free.
+__device__ __forceinline__ int *twice_at(const Teacher &s, int K) { return s.idx + 3 * ((K + 3) & ~3); }
+int table_bits(int K) {
+  int bits = 1;
+  while ((1 << bits) < 2 * K) ++bits;
+  return bits;
+}
+size_t table_bytes(int K) { return 4 + (size_t{4} << table_bits(K)); }
+
+// With a warp to a row the search of all entries for each entry's index is most of the work (16384 x 2000 bf16, joint: 56
+// and 80 us with 64 and 200 entries, and 63 and 155 us with the search); beside longer rows the table costs as much as it
+// saves.
+template <int TH>
+constexpr bool TABLE = TH == 32;
+
+template <int TH>
+__device__ __forceinline__ void clear_table(const DistillArgs &a, const Teacher &s) {
+  int *twice = twice_at(s, a.K);
+  if (threadIdx.x == 0) *twice = 0;
+  for (int i = threadIdx.x; i < 1 << a.bits; i += TH) twice[1 + i] = -1;
+}
+
+// Once the table is clear and the entries are there. An index's search starts at the top bits of its product with an odd
+// constant near 2^32 / golden ratio, and ends since half of the places stay free.
+template <int TH>
+__device__ __forceinline__ void fill_table(const DistillArgs &a, const Teacher &s) {
+  int *twice = twice_at(s, a.K), *table = twice + 1;
+  for (int k = threadIdx.x; k < a.K; k += TH) {
+    const int id = s.idx[k];
+    if (id < 0) continue;
+    unsigned at = static_cast<unsigned>(id) * 0x9e3779b1u >> (32 - a.bits);
+    int found = atomicCAS(table + at, -1, id);
+    while (found != -1 && found != id) {
+      at = (at + 1) & ((1u << a.bits) - 1);
+      found = atomicCAS(table + at, -1, id);
+    }
+    if (found == id) *twice = 1;
+  }
+}
+
 // One entry as loaded. ok: it is valid.
 struct Entry {
   long long id;
@@ -304,12 +345,24 @@ __device__ __forceinline__ Soft put_teacher(const DistillArgs &a, long long row,
                                             int hi, float c, const Entry &ahead) {
   Soft sum{-INFINITY, 0.f};
   if (static_cast<int>(threadIdx.x) < a.K) put_entry(s, threadIdx.x, ahead, c, sum);
-  for (int k = TH + threadIdx.x; k < a.K; k += TH) {
+  constexpr int U = ALL && TH == 32 ? 4 : 1;   // entries on their way at once
+  int k = TH + threadIdx.x;
+  if constexpr (U > 1)
+    for (; k + (U - 1) * TH < a.K; k += U * TH) {
+      Entry e[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) e[u] = load_entry(a, row, k + u * TH);
+#pragma unroll
+      for (int u = 0; u < U; ++u) e[u].z = entry_logit<ZT, ALL>(e[u], z, lo, hi);
+#pragma unroll
+      for (int u = 0; u < U; ++u) put_entry(s, k + u * TH, e[u], c, sum);
+    }
+  for (; k < a.K; k += TH) {
     Entry e = load_entry(a, row, k);
     e.z = entry_logit<ZT, ALL>(e, z, lo, hi);
     put_entry(s, k, e, c, sum);
   }
-  for (int k = a.K + threadIdx.x; k < ((a.K + 3) & ~3); k += TH) s.idx[k] = -1;
+  for (k = a.K + threadIdx.x; k < ((a.K + 3) & ~3); k += TH) s.idx[k] = -1;
   return sum;
 }
 
@@ -369,18 +422,20 @@ __device__ __forceinline__ void store_nothing(const DistillArgs &a, long long ro
   a.stats[2 * row + 1] = 0.f;
 }
 
-// Where the p parts of columns [lo, hi) are written: the first entry of each index there subtracts the q of all
-// entries of that index.
+// Where the p parts of columns [lo, hi) are written: each entry subtracts its q, or, unless it is known that no index
+// occurs twice, the first entry of each index subtracts the q of all of its entries, in order.
 template <int TH, typename DT>
 __device__ __forceinline__ void subtract_teacher(const DistillArgs &a, const Teacher &s, DT *dz, int lo, int hi,
                                                  float c, float m, float inv, float scale, const Soft &teacher) {
   const float tinv = 1.f / teacher.s;
+  bool twice = true;
+  if constexpr (TABLE<TH>) twice = *twice_at(s, a.K) != 0;
   for (int k = threadIdx.x; k < a.K; k += TH) {
     const int id = s.idx[k];
     if (id < lo || id >= hi) continue;   // absent entries are -1, below every lo
     bool first = true;
-    float q = 0.f;
-    for (int i = 0; i < a.K; i += 4) {
+    float q = twice ? 0.f : exp_scaled(s.t[k] - teacher.m, c) * tinv;
+    for (int i = 0; twice && i < a.K; i += 4) {
       const int4 v = *reinterpret_cast<const int4 *>(s.idx + i);
       if (v.x != id && v.y != id && v.z != id && v.w != id) continue;
       const int u[4] = {v.x, v.y, v.z, v.w};
@@ -499,6 +554,7 @@ __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_backward_kernel(con
     zero_granules<DT, GE, TH, VEC>(dz, G, S);
     return;
   }
+  if constexpr (TABLE<TH>) clear_table<TH>(a, s);
   Stream<ZT, GE, TH, VEC> stream(z, G, S);
   const float m = a.stats[2 * row], l = a.stats[2 * row + 1], up = a.grad != nullptr ? a.grad[row] : 1.f;
   if (t < a.K) e.z = entry_logit<ZT, false>(e, z, lo, hi);
@@ -509,6 +565,7 @@ __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_backward_kernel(con
     return;
   }
   const float inv = expf(-l), scale = up * w * a.temp;
+  if constexpr (TABLE<TH>) fill_table<TH>(a, s);
   stream.write_grad(dz, m, c, scale * inv);
   __syncthreads();
   subtract_teacher<TH>(a, s, dz, lo, hi, c, m, inv, scale, teacher);
@@ -538,6 +595,7 @@ __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_joint_kernel(const 
     zero_granules<DT, GE, TH, VEC>(dz, G, S);
     return;
   }
+  if constexpr (TABLE<TH>) clear_table<TH>(a, s);
   Run run;
   {
     Stream<ZT, GE, TH, VEC> stream(z, G, S);
@@ -560,6 +618,7 @@ __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_joint_kernel(const 
       if (t % 32 == 0) red.loss[t / 32] = part;
     }
     const float scale = a.grad_scale * w * a.temp, inv = 1.f / student.s;
+    if constexpr (TABLE<TH>) fill_table<TH>(a, s);
     stream.write_grad(dz, student.m, c, scale * inv);
     __syncthreads();
     if (rank == 0 && t == 0) store_loss<TH>(a, row, w, red.loss, student);
@@ -605,6 +664,7 @@ DistillArgs distill_args(const void *logits, int64_t ldz, const void *t_idx, muo
   a.tdt = tdt;
   a.inv_t = 1.f / temperature;
   a.temp = temperature;
+  a.bits = table_bits(a.K);
   a.grad_scale = 1.f;
   return a;
 }
@@ -679,7 +739,7 @@ cudaError_t launch_bwd(DistillArgs a, cudaStream_t s) {
     a.slices = row_slices(a, TH);
     while (a.V / a.slices > 65536) a.slices *= 2;
     return launch_pdl(distill_backward_kernel<ZT, DT, TH, VEC>, dim3(static_cast<unsigned>(a.N * a.slices)), dim3(TH),
-                      teacher_bytes(a.K), s, a);
+                      teacher_bytes(a.K) + (TABLE<TH> ? table_bytes(a.K) : 0), s, a);
   });
 }
 
@@ -691,8 +751,7 @@ cudaError_t launch_step(DistillArgs a, cudaStream_t s) {
   if (a.slices == 1) threads = joint_threads(a.V, static_cast<size_t>(a.V) * sizeof(ZT));
   return with_threads(threads, [&](auto th) {
     constexpr int TH = decltype(th)::value;
-    return launch_clusters(distill_joint_kernel<ZT, DT, TH, VEC>, a.N * a.slices, TH, a.slices, teacher_bytes(a.K), s,
-                           a);
+    return launch_clusters(distill_joint_kernel<ZT, DT, TH, VEC>, a.N * a.slices, TH, a.slices, teacher_bytes(a.K) + (TABLE<TH> ? table_bytes(a.K) : 0), s, a);
   });
 }
 

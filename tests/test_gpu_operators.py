@@ -309,10 +309,11 @@ def test_layernorm_gradients_match_differences(L, D):
 
 # ------------------------------------------------------------------------------------------------ distillation
 
-# N, V, K: one logit; one row; fewer logits than a block's step and more; odd widths; the largest K
+# N, V, K: one logit; one row; fewer logits than a block's step and more; odd widths; the largest K; more entries than logits
 DISTILL = [(0, 10, 2), (1, 1, 1), (3, 5, 4), (7, 100, 1), (5, 1000, 33), (4, 4096, 64), (9, 5003, 20), (2, 32003, 128),
            (1, 50304, 64), (3, 20000, 1024), (200, 700, 8), (1, 128256, 64), (2, 260001, 16), (2, 600011, 16),
-           (400, 9001, 40), (3, 420001, 8), (300, 16001, 12), (5, 16384, 700), (9, 31, 5)]
+           (400, 9001, 40), (3, 420001, 8), (300, 16001, 12), (5, 16384, 700), (9, 31, 5),
+           (40, 3001, 1024), (40, 600, 1024), (33, 2000, 200)]
 
 
 def distill_inputs(N, V, K, zdt, tdt, it, seed):
