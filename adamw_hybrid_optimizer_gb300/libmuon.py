@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence, Tuple
+from typing import Dict, Optional, Sequence, Tuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "lib", "libmuon.so")
@@ -169,13 +169,27 @@ def _check(status: int, where: str):
         raise MuonError(status, where)
 
 
+_CODES: Dict = {}     # torch dtype -> (integer, muon_dtype or muon_itype); filled on first use
+
+
+def _code(dtype) -> Tuple[bool, int]:
+    """An import statement and attribute lookups per tensor are a tenth of a small call's time: hence the table."""
+    code = _CODES.get(dtype)
+    if code is None and not _CODES:
+        import torch
+        _CODES.update({torch.float32: (False, MUON_F32), torch.bfloat16: (False, MUON_BF16),
+                       torch.int32: (True, MUON_I32), torch.int64: (True, MUON_I64)})
+        code = _CODES.get(dtype)
+    if code is None:
+        raise MuonError(MUON_ERR_DTYPE, f"dtype {dtype}")
+    return code
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return MUON_F32
-    if t.dtype == torch.bfloat16:
-        return MUON_BF16
-    raise MuonError(MUON_ERR_DTYPE, f"dtype {t.dtype}")
+    integer, code = _code(t.dtype)
+    if integer:
+        raise MuonError(MUON_ERR_DTYPE, f"dtype {t.dtype}")
+    return code
 
 
 def _stream(stream) -> int:
@@ -371,41 +385,45 @@ def ns_apply(h, x, out, ws, stream=None):
 # ------------------------------------------------------------------------------------------------------------
 
 
+_raw_stream = None    # torch's functions for the current stream's handle and the current device
+
+
 def _current_stream(stream) -> int:
     """_stream, without building a stream object for the current one (most of the binding's time otherwise)."""
+    global _raw_stream
     if stream is not None:
         return _stream(stream)
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _raw_stream[0](_raw_stream[1]())
 
 
 def _itype_code(t) -> int:
-    import torch
-    if t.dtype == torch.int32:
-        return MUON_I32
-    if t.dtype == torch.int64:
-        return MUON_I64
-    raise MuonError(MUON_ERR_DTYPE, f"dtype {t.dtype}")
+    integer, code = _code(t.dtype)
+    if not integer:
+        raise MuonError(MUON_ERR_DTYPE, f"dtype {t.dtype}")
+    return code
 
 
 def _matrix(t, name: str, where: str, shape=None) -> int:
     """The row pitch of a 2-D CUDA tensor with contiguous columns (and of the given shape)."""
-    if t.dim() != 2 or not t.is_cuda or (shape is not None and tuple(t.shape) != shape):
+    own = t.shape
+    if len(own) != 2 or not t.is_cuda or (shape is not None and own != shape):
         raise ValueError(f"{where}: {name} must be a 2-D CUDA tensor" + (f" of shape {shape}" if shape else ""))
-    rows, cols = t.shape
     pitch, col = t.stride()
-    if cols > 1 and col != 1:
+    if col != 1 and own[1] > 1:
         raise ValueError(f"{where}: {name} needs contiguous columns")
-    return pitch if rows > 1 else max(pitch, cols)
+    return pitch if own[0] > 1 else max(pitch, own[1])
 
 
-def _vector(t, name: str, where: str, n: int, dtype=None) -> Optional[int]:
-    """The data pointer of an optional contiguous CUDA tensor of n elements (and of the given dtype)."""
+def _vector(t, name: str, where: str, n: int, fp32: bool = False) -> Optional[int]:
+    """The data pointer of an optional contiguous CUDA tensor of n elements (of fp32, if asked)."""
     if t is None:
         return None
-    if t.numel() != n or not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+    if t.numel() != n or not t.is_cuda or not t.is_contiguous() or (fp32 and _code(t.dtype) != (False, MUON_F32)):
         raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor of {n} elements"
-                         + (f" of {dtype}" if dtype is not None else ""))
+                         + (" of torch.float32" if fp32 else ""))
     return t.data_ptr()
 
 
@@ -439,7 +457,6 @@ def embedding_backward(ids, dout, dtable, ws, scale: float = 1.0, padding_idx: i
 
 def layernorm_forward(x, weight, bias, y, mean, rstd, eps: float = 1e-5, stream=None):
     """y = layer norm of x's rows; weight and bias (one dtype) may be None, and so may mean and rstd (fp32, N)."""
-    import torch
     N, D = x.shape
     ldx = _matrix(x, "x", "layernorm_forward")
     ldy = _matrix(y, "y", "layernorm_forward", (N, D))
@@ -448,8 +465,8 @@ def layernorm_forward(x, weight, bias, y, mean, rstd, eps: float = 1e-5, stream=
         raise ValueError("layernorm_forward: weight and bias of one dtype")
     st = lib().layernorm_forward(x.data_ptr(), _dtype_code(x), ldx, _vector(weight, "weight", "layernorm_forward", D),
                                  _vector(bias, "bias", "layernorm_forward", D), wdt, y.data_ptr(), _dtype_code(y), ldy,
-                                 _vector(mean, "mean", "layernorm_forward", N, torch.float32),
-                                 _vector(rstd, "rstd", "layernorm_forward", N, torch.float32), N, D, eps,
+                                 _vector(mean, "mean", "layernorm_forward", N, True),
+                                 _vector(rstd, "rstd", "layernorm_forward", N, True), N, D, eps,
                                  _current_stream(stream))
     _check(st, "layernorm_forward")
 
@@ -461,7 +478,6 @@ def layernorm_workspace_bytes(N: int, D: int) -> int:
 def layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, accumulate: bool = False, stream=None):
     """Layer norm's gradients from the forward pass's mean and rstd; dx, dweight and dbias may be None (and ws, if the
     latter two are). accumulate=True adds dweight and dbias to what they hold."""
-    import torch
     N, D = x.shape
     where = "layernorm_backward"
     ldx = _matrix(x, "x", where)
@@ -477,8 +493,8 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, accumu
     st = lib().layernorm_backward(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x), ldx,
                                   _vector(weight, "weight", where, D),
                                   _dtype_code(weight) if weight is not None else MUON_F32,
-                                  _vector(mean, "mean", where, N, torch.float32),
-                                  _vector(rstd, "rstd", where, N, torch.float32),
+                                  _vector(mean, "mean", where, N, True),
+                                  _vector(rstd, "rstd", where, N, True),
                                   dx.data_ptr() if dx is not None else None, lddx,
                                   _vector(dweight, "dweight", where, D), _vector(dbias, "dbias", where, D),
                                   _dtype_code(g) if g is not None else MUON_F32, int(bool(accumulate)), N, D,
@@ -488,7 +504,6 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, accumu
 
 
 def _distill(where, logits, t_idx, t_val, weights, stats):
-    import torch
     N, V = logits.shape
     ldz = _matrix(logits, "logits", where)
     if t_idx.dim() != 2 or t_idx.shape[0] != N or t_idx.shape != t_val.shape:
@@ -496,27 +511,25 @@ def _distill(where, logits, t_idx, t_val, weights, stats):
     K = t_idx.shape[1]
     return (N, V, K, (logits.data_ptr(), _dtype_code(logits), ldz, _vector(t_idx, "t_idx", where, N * K),
                       _itype_code(t_idx), _vector(t_val, "t_val", where, N * K), _dtype_code(t_val),
-                      _vector(weights, "weights", where, N, torch.float32)),
-            _vector(stats, "stats", where, 2 * N, torch.float32))
+                      _vector(weights, "weights", where, N, True)),
+            _vector(stats, "stats", where, 2 * N, True))
 
 
 def distill_forward(logits, t_idx, t_val, temperature: float, weights, losses, stats, stream=None):
     """losses[i] = weights[i] * T^2 * KL(teacher's top entries || student) of row i; stats (N, 2) for the backward pass.
 
     logits (N, V); t_idx, t_val (N, K) contiguous; weights None or fp32 (N); losses fp32 (N)."""
-    import torch
     N, V, K, head, st_ptr = _distill("distill_forward", logits, t_idx, t_val, weights, stats)
-    st = lib().distill_forward(*head, _vector(losses, "losses", "distill_forward", N, torch.float32), st_ptr, N, V, K,
+    st = lib().distill_forward(*head, _vector(losses, "losses", "distill_forward", N, True), st_ptr, N, V, K,
                                temperature, _current_stream(stream))
     _check(st, "distill_forward")
 
 
 def distill_backward(logits, t_idx, t_val, temperature: float, weights, stats, grad, dlogits, stream=None):
     """dlogits[i] = grad[i] * d losses[i] / d logits[i]; grad None (all 1) or fp32 (N). dlogits may be logits."""
-    import torch
     N, V, K, head, st_ptr = _distill("distill_backward", logits, t_idx, t_val, weights, stats)
     ldd = _matrix(dlogits, "dlogits", "distill_backward", (N, V))
-    st = lib().distill_backward(*head, st_ptr, _vector(grad, "grad", "distill_backward", N, torch.float32),
+    st = lib().distill_backward(*head, st_ptr, _vector(grad, "grad", "distill_backward", N, True),
                                 dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature, _current_stream(stream))
     _check(st, "distill_backward")
 
@@ -524,11 +537,10 @@ def distill_backward(logits, t_idx, t_val, temperature: float, weights, stats, g
 def distill_forward_backward(logits, t_idx, t_val, temperature: float, weights, grad_scale: float, losses, stats,
                              dlogits, stream=None):
     """distill_forward and distill_backward (with grad_scale for every row's grad) in one call."""
-    import torch
     where = "distill_forward_backward"
     N, V, K, head, st_ptr = _distill(where, logits, t_idx, t_val, weights, stats)
     ldd = _matrix(dlogits, "dlogits", where, (N, V))
-    st = lib().distill_forward_backward(*head, grad_scale, _vector(losses, "losses", where, N, torch.float32), st_ptr,
+    st = lib().distill_forward_backward(*head, grad_scale, _vector(losses, "losses", where, N, True), st_ptr,
                                         dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature,
                                         _current_stream(stream))
     _check(st, where)
