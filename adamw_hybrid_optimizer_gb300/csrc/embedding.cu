@@ -958,7 +958,7 @@ muon_status launch_sort(const void *ids, int itype, long long n, long long V, lo
   return MUON_OK;
 }
 
-// The sort in one cluster (n <= CS_BLOCKS * CS_CHUNK) and the zeroes beside it (z.rows = 0: none). Blocks of up to 2048
+// The sort in one cluster (n <= CS_BLOCKS * CS_CHUNK) and the zeroes beside it (z.rows = 0: none). Blocks of up to 1024
 // items each while there are sixteen of them: a block's rounds cost more than the cluster's barriers.
 muon_status launch_prepare(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
                            const EmbeddingLayout &L, const ZeroArgs &z, const unsigned **key, const unsigned **pos,
@@ -981,7 +981,7 @@ muon_status launch_prepare(const void *ids, int itype, long long n, long long V,
   a.list_count = reinterpret_cast<unsigned *>(ws + L.list);
   a.n = static_cast<int>(n);
   a.blocks = 1;
-  while (a.blocks < CS_BLOCKS && a.blocks * 2048 < n) a.blocks *= 2;
+  while (a.blocks < CS_BLOCKS && a.blocks * 1024 < n) a.blocks *= 2;
   a.chunk = (a.n + a.blocks - 1) / a.blocks;
   a.passes = (key_bits + MAX_DIGIT_BITS - 1) / MAX_DIGIT_BITS;
   a.bits = (key_bits + a.passes - 1) / a.passes;

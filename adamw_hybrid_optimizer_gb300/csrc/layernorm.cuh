@@ -31,8 +31,8 @@ __device__ __forceinline__ float param_at(const void *p, int dt, int c, float ab
 //   FULL     ALIGNED, and the row gives every thread all of its granules, so that nothing is asked
 //   SHIFTED  rows start past a boundary (an odd width): a row is a few single values up to the first boundary (the head),
 //            whole granules, and a few single values (the tail). Sixteen threads have one of these each, beside their
-//            granules. A row slot sees rows whose index differs by multiples of 8, which all start alike, so its threads'
-//            columns stay the same.
+//            granules. A block sees rows whose index differs by multiples of 8, which all start alike, so its threads' columns
+//            stay the same, and its rows share the weights.
 enum Mode { SCALAR, ALIGNED, SHIFTED, FULL };
 
 // A granule is 8 values of bf16 or, where a matrix is fp32, 4: an access of one is 16 (8 for bf16 beside fp32) bytes,
@@ -205,12 +205,10 @@ struct Ring {
 
 // A vector of weights (or biases), as each thread wants its own columns of it row after row: in registers where there
 // is one chunk, as fp32 in shared memory up to 8192 columns of several chunks, and read where it is beyond that (and in
-// SCALAR, for several chunks). The block's rows share it, but for SHIFTED ones, whose columns depend on the slot: there
-// each thread has its own copy.
+// SCALAR, for several chunks). The block's rows share it.
 template <typename CT, int C, int THREADS, bool SHARED>
 struct Params {
-  static constexpr bool OWN = CT::MODE == SHIFTED;
-  static constexpr int STRIDE = OWN ? THREADS : CT::T, BYTES = SHARED ? 32 * C * STRIDE : 0;
+  static constexpr int STRIDE = CT::T, BYTES = SHARED ? 32 * C * STRIDE : 0;
   const void *p;
   int dt;
   bool wide;
@@ -221,7 +219,7 @@ struct Params {
   __device__ __forceinline__ void init(const CT &c, int slot) {
     if constexpr (C == 1) one = param_chunk(p, dt, wide, c, 0, absent);
     if constexpr (SHARED) {
-      if (!OWN && slot != 0) return;
+      if (slot != 0) return;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const Vals<8> o = param_chunk(p, dt, wide, c, k, absent);
@@ -273,6 +271,16 @@ struct Exchange {
     return from < W ? r[from] : make_float2(0.f, 0.f);
   }
 };
+
+// Row slot `slot` of the R that a block holds starts at first_row, and the block's slots are rows_apart from each other;
+// the grid of SHIFTED is a multiple of eight blocks.
+template <int MODE>
+constexpr int rows_apart = MODE == SHIFTED ? 8 : 1;
+template <int R, int MODE>
+__device__ __forceinline__ long long first_row(int slot) {
+  const long long b = blockIdx.x;
+  return MODE == SHIFTED ? b % 8 + 8 * (b / 8 * R + slot) : b * R + slot;
+}
 
 // Sums over a block of 32 warps, for the kernels that give a block to a row.
 __device__ __forceinline__ float block_sum(float v, float (*red)[32], int &turn) {

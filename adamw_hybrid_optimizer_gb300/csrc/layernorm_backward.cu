@@ -28,6 +28,10 @@ struct BackwardArgs {
   int wdt, wide, D;
 };
 
+// Threads of a multiprocessor, by the registers that they need (131072 x 201 bf16: 51 us with 512, and 84 us with 768,
+// which spill).
+constexpr int resident_threads(int C, Mode mode) { return C == 1 && mode != SHIFTED ? 768 : 512; }
+
 // Rows as in the forward kernel: R at a time, W warps each, with the next rows on their way. A thread's columns of dw
 // and db are in registers, or in shared memory for rows of more than 8192 columns (1024 threads have 64 registers
 // each), which leaves no room for a ring: the next row waits in registers there, where it fits them.
@@ -45,7 +49,7 @@ struct Backward {
   static constexpr size_t LOOP = static_cast<size_t>(RING_X) + RING_DY + PT::BYTES +
                                  (IN_SHARED ? 64 * C * THREADS : 0);
   static constexpr size_t BYTES = std::max<size_t>(LOOP, R > 1 ? 32 * C * THREADS : 0);   // the rows' sums at the end
-  static constexpr int BLOCKS = std::max(1, (C == 1 ? 768 : 512) / THREADS);
+  static constexpr int BLOCKS = std::max(1, resident_threads(C, static_cast<Mode>(MODE)) / THREADS);
 };
 
 template <typename XT, typename YT, int C, int W, int R, int MODE>
@@ -60,14 +64,13 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
   __shared__ float2 red[2][R][W];
   const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T, D = a.D;
   const long long step = static_cast<long long>(gridDim.x) * R;
-  long long row = static_cast<long long>(blockIdx.x) * R + slot;
+  long long row = first_row<R, MODE>(slot);
   const CT c(t, D, row * a.ldx);
   Exchange<W, R> exchange{red, slot, t / 32, 0};
   const Ring<XT, CT, C, THREADS> ring_x{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
   const Ring<YT, CT, C, THREADS> ring_dy{shared + B::RING_X + threadIdx.x * Raw<YT, CT::GE>::BYTES};
   using PT = typename B::PT;
-  float4 *kept = reinterpret_cast<float4 *>(shared + B::RING_X + B::RING_DY) +
-                 (PT::OWN ? static_cast<int>(threadIdx.x) : t);
+  float4 *kept = reinterpret_cast<float4 *>(shared + B::RING_X + B::RING_DY) + t;
   PT weight{a.w, a.wdt, a.wide != 0, 1.f, kept};
   Vals<8> aw[C], ab[C];
 #pragma unroll
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(W *R * 32, (Backward<XT, YT, C, W, R, MODE>::B
   weight.init(c, slot);
   if constexpr (B::SHARED && R > 1) __syncthreads();
   int stage = 0;
-  for (; row - slot < a.N; row += step) {   // the same count for the whole block
+  for (; row - rows_apart<MODE> * slot < a.N; row += step) {   // the same count for the whole block
     const bool live = R == 1 || row < a.N;
     if constexpr (!B::AHEAD) fetch(0);
     const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
@@ -338,7 +341,9 @@ __global__ void __launch_bounds__(REDUCE_WARPS * 32) layernorm_reduce_kernel(con
 // ------------------------------------------------------------------------------------------ host
 
 // Chunks per thread, warps per row and rows per block for D columns: a warp per row up to 768 columns, then as few
-// warps as two or three chunks of eight columns per thread allow (the sums of dw and db take 16 registers for each).
+// warps as two or three chunks of eight columns per thread allow (the sums of dw and db take 16 registers for each). Two
+// at most in SHIFTED, whose single columns take the registers of the third (65536 x 1501 bf16: 147 us, and 230 us with
+// three).
 struct Shape {
   int C, W, R;
 };
@@ -346,19 +351,19 @@ Shape shape_of(long long D, Mode mode) {
   if (mode == SCALAR) return D <= 1024 ? Shape{1, 4, 2} : Shape{2, D <= 8192 ? 16 : 32, 1};
   if (D <= 256) return {1, 1, 8};
   if (D <= 512) return {2, 1, 8};
-  if (D <= 768) return {3, 1, 8};
+  if (D <= 768 && mode != SHIFTED) return {3, 1, 8};
   if (D <= 1024) return {2, 2, 4};
-  if (D <= 1536) return {3, 2, 4};
+  if (D <= 1536 && mode != SHIFTED) return {3, 2, 4};
   for (int W : {4, 8, 16}) if (D <= 512 * W) return {2, W, 1};
   return {2, 32, 1};
 }
 
 // Blocks of the backward pass, each of which leaves one partial row of dw and db: as many as the GPU holds at once,
-// so that there are few partial rows to add. In SHIFTED a slot's rows lie multiples of eight apart.
+// so that there are few partial rows to add. In SHIFTED a block's rows lie multiples of eight apart.
 long long parts_for(long long N, long long D, Mode mode) {
   if (D > MAX_ROW) return std::max(1LL, std::min(N, 64LL));
   const Shape h = shape_of(D, mode);
-  const long long resident = std::max(1, (h.C == 1 ? 768 : 512) / (h.W * h.R * 32));
+  const long long resident = std::max(1, resident_threads(h.C, mode) / (h.W * h.R * 32));
   const long long blocks = std::max(1LL, std::min((N + h.R - 1) / h.R, 152 * resident));
   return mode == SHIFTED ? (blocks + 7) / 8 * 8 : blocks;
 }
@@ -382,13 +387,12 @@ cudaError_t backward_shape(const BackwardArgs &a, cudaStream_t s) {
 template <typename XT, typename YT, int MODE>
 cudaError_t backward_route_mode(const BackwardArgs &a, cudaStream_t s) {
   const Shape h = shape_of(a.D, static_cast<Mode>(MODE));
-  if (h.W == 1)
-    return h.C == 1   ? backward_shape<XT, YT, 1, 1, 8, MODE>(a, s)
-           : h.C == 2 ? backward_shape<XT, YT, 2, 1, 8, MODE>(a, s)
-                      : backward_shape<XT, YT, 3, 1, 8, MODE>(a, s);
-  if (h.W == 2)
-    return h.C == 2 ? backward_shape<XT, YT, 2, 2, 4, MODE>(a, s) : backward_shape<XT, YT, 3, 2, 4, MODE>(a, s);
+  if constexpr (MODE != SHIFTED)
+    if (h.C == 3)
+      return h.W == 1 ? backward_shape<XT, YT, 3, 1, 8, MODE>(a, s) : backward_shape<XT, YT, 3, 2, 4, MODE>(a, s);
   switch (h.W) {
+    case 1: return h.C == 1 ? backward_shape<XT, YT, 1, 1, 8, MODE>(a, s) : backward_shape<XT, YT, 2, 1, 8, MODE>(a, s);
+    case 2: return backward_shape<XT, YT, 2, 2, 4, MODE>(a, s);
     case 4: return backward_shape<XT, YT, 2, 4, 1, MODE>(a, s);
     case 8: return backward_shape<XT, YT, 2, 8, 1, MODE>(a, s);
     case 16: return backward_shape<XT, YT, 2, 16, 1, MODE>(a, s);

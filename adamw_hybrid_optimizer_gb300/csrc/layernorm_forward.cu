@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
   __shared__ float2 red[2][R][W];
   const int slot = R == 1 ? 0 : threadIdx.x / T, t = threadIdx.x - slot * T;
   const long long step = static_cast<long long>(gridDim.x) * R;
-  long long row = static_cast<long long>(blockIdx.x) * R + slot;
+  long long row = first_row<R, MODE>(slot);
   const CT c(t, a.D, row * a.ldx);
   Exchange<W, R> exchange{red, slot, t / 32, 0};
   const Ring<XT, CT, C, F::THREADS> ring{shared + threadIdx.x * Raw<XT, CT::GE>::BYTES};
   using PT = typename F::PT;
-  float4 *kept = reinterpret_cast<float4 *>(shared + F::ROWS) + (PT::OWN ? static_cast<int>(threadIdx.x) : t);
+  float4 *kept = reinterpret_cast<float4 *>(shared + F::ROWS) + t;
   PT weight{a.w, a.wdt, a.wide != 0, 1.f, kept}, bias{a.b, a.wdt, a.wide != 0, 0.f, kept + PT::BYTES / 16};
   const long long x_step = step * a.ldx, y_step = step * a.ldy;
   const XT *x = static_cast<const XT *>(a.x) + row * a.ldx;   // the next row to fetch
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
   float n_lane = n_w;
   if constexpr (W > 1) n_lane = exchange.put_get(n_w, 0.f).x;
   int stage = 0;
-  for (; row - slot < a.N; row += step) {   // the same count for the whole block
+  for (; row - rows_apart<MODE> * slot < a.N; row += step) {   // the same count for the whole block
     const bool live = R == 1 || row < a.N;
     Vals<8> v[C];
     if constexpr (F::RING) {
@@ -194,7 +194,7 @@ cudaError_t forward_launch(const ForwardArgs &a, cudaStream_t s) {
   if (allowed != cudaSuccess) return allowed;
   const long long resident = std::max<long long>(1, std::min<long long>(F::BLOCKS, SM_SHARED / (F::BYTES + 2048)));
   long long blocks = std::min((a.N + R - 1) / R, device_sm_count() * resident);
-  if (MODE == SHIFTED) blocks = (blocks + 7) / 8 * 8;   // a slot's rows lie multiples of eight apart
+  if (MODE == SHIFTED) blocks = (blocks + 7) / 8 * 8;   // a block's rows lie multiples of eight apart
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(F::THREADS), F::BYTES, s, a);
 }
 
