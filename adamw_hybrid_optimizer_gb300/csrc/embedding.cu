@@ -108,64 +108,76 @@ struct LookupArgs {
   int itype, D, tiles, log_rows;   // units per long row; log2 of the rows per unit of short ones
   float scale;
   int past_table, past_out;   // values by which the bases are past a granule's boundary
+  // aligned rows: 2^32 / granules per row, and the rows and granules from a warp's unit to its next one
+  unsigned inverse;
+  int skip;
+  long long skip_rows;
 };
 
-// Warps take units in turn: 128 granules of a long row, or of as many short rows as fit, four granules per lane.
-//
-// Rows that start on a granule and have whole ones: all loads of a unit are in flight before the first is used, and the
-// ids of the next unit are loaded under them, so that a unit waits for one latency, not two.
+// Rows that start on a granule and have whole ones: warps take units of 128 granules in turn, four per lane, which follow
+// each other through the rows (of any length, so that no lane is idle: 65536 rows of 768 bf16 FIGURES). All loads of a unit
+// are in flight before the first is used, and the ids of the next unit are loaded under them, so that a unit waits for one
+// latency, not two.
 template <typename TT, typename OT>
 __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(const LookupArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
   constexpr int GE = granule_of<TT, OT>(), U = UNIT / 32;
-  const int lane = threadIdx.x % 32;
-  const bool many = a.tiles == 1;
-  const long long units = many ? (a.n + (1 << a.log_rows) - 1) >> a.log_rows : a.n * a.tiles;
-  const long long warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
+  const int lane = threadIdx.x % 32, per_row = a.D / GE;
+  const long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32;
   const TT *table = static_cast<const TT *>(a.table);
-  // row and first column of the lane's granule q of unit u
-  auto row_of = [&](long long u, int q) {
-    return many ? (u << a.log_rows) + ((q * 32 + lane) >> (LOG_UNIT - a.log_rows)) : u / a.tiles;
+  struct Place {
+    long long row;
+    int c;
   };
-  auto first_of = [&](long long u, int q) {
-    return GE * (many ? (q * 32 + lane) & ((UNIT >> a.log_rows) - 1) : static_cast<int>(u % a.tiles) * UNIT + q * 32 + lane);
+  // where granule `place` after the first one of row r is; place < per_row + UNIT, so that the high half of its product
+  // with 2^32 / per_row, rounded up, is the quotient
+  auto place_of = [&](long long r, int place) {
+    const int rows = per_row == 1 ? place : static_cast<int>(__umulhi(place, a.inverse));
+    return Place{r + rows, (place - rows * per_row) * GE};
   };
-  auto ids_of = [&](long long u, long long *id) {
+  long long row = w * UNIT / per_row;   // of the warp's unit, and its granule in it
+  int first = static_cast<int>(w * UNIT - row * per_row);
+  auto ids_of = [&](long long r, int g, int *id) {
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const long long r = row_of(u, q);
-      id[q] = u < units && r < a.n ? load_id(a.ids, a.itype, r) : -1;
+      const Place p = place_of(r, g + q * 32 + lane);
+      const long long v = p.row < a.n ? load_id(a.ids, a.itype, p.row) : -1;
+      id[q] = v >= 0 && v < a.V ? static_cast<int>(v) : -1;
     }
   };
-  long long u = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32, next[U];
-  ids_of(u, next);
-  for (; u < units; u += warps) {
-    long long id[U];
+  int next[U];
+  ids_of(row, first, next);
+  while (row < a.n) {
+    int id[U];
     Raw<TT, GE> r[U];
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      id[q] = next[q] < 0 || next[q] >= a.V ? -1 : next[q];
+      id[q] = next[q];
       r[q].clear();
-      const int c = first_of(u, q);
-      if (id[q] >= 0 && c < a.D) r[q].load(table + id[q] * a.ldt + c);
+      if (id[q] >= 0) r[q].load(table + id[q] * a.ldt + place_of(row, first + q * 32 + lane).c);
     }
-    ids_of(u + warps, next);
+    long long then = row + a.skip_rows;
+    int then_first = first + a.skip;
+    if (then_first >= per_row) ++then, then_first -= per_row;
+    ids_of(then, then_first, next);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const long long row = row_of(u, q);
-      const int c = first_of(u, q);
-      if (row >= a.n || c >= a.D) continue;
+      const Place p = place_of(row, first + q * 32 + lane);
+      if (p.row >= a.n) continue;
       Vals<GE> o = r[q].get();
 #pragma unroll
       for (int i = 0; i < GE / 2; ++i)
         o.p[i] = id[q] < 0 ? make_float2(0.f, 0.f) : __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
-      store_vals(static_cast<OT *>(a.out) + row * a.ldo + c, o);
+      store_vals(static_cast<OT *>(a.out) + p.row * a.ldo + p.c, o);
     }
+    row = then;
+    first = then_first;
   }
 }
 
-// Other rows: a unit's granules are those of the table around the output's, one more than it writes. The granules of the
+// Other rows: a unit is 128 granules of a long row, or of as many short rows as fit, and its granules are those of the
+// table around the output's, one more than it writes. The granules of the
 // next units are on their way to the warp's ring in shared memory, and the ids of the one after on theirs, while a unit
 // is stored. (65536 rows of 771 bf16: 49 us, and 76 us with two loads per lane and granule into registers; but where
 // rows are aligned the ring takes 194 us for 65536 rows of 4096, and registers 138 us.)
@@ -896,25 +908,31 @@ cudaError_t launch_lookup(LookupArgs a, cudaStream_t s) {
   const dim3 block(THREADS);
   a.past_table = past<TT, GE>(a.table);
   a.past_out = past<OT, GE>(a.out);
-  const bool aligned = a.D % GE == 0 && a.ldt % GE == 0 && a.ldo % GE == 0 && a.past_table == 0 && a.past_out == 0;
-  // a row's granules of a unit: where it is cut out, one more than the most that it can touch
-  const int granules = aligned ? a.D / GE : (a.D + 2 * (GE - 1)) / GE + 1;
-  const int writes = aligned ? UNIT : UNIT - 1;
+  const auto grid = [&](long long units, int resident) {
+    return dim3(static_cast<unsigned>(std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * resident)));
+  };
+  if (a.D % GE == 0 && a.ldt % GE == 0 && a.ldo % GE == 0 && a.past_table == 0 && a.past_out == 0) {
+    const long long per_row = a.D / GE;
+    const dim3 blocks = grid((a.n * per_row + UNIT - 1) / UNIT, FWD_BLOCKS);
+    const long long skip = static_cast<long long>(blocks.x) * (THREADS / 32) * UNIT;
+    a.inverse = static_cast<unsigned>(((1ull << 32) + per_row - 1) / per_row);
+    a.skip_rows = skip / per_row;
+    a.skip = static_cast<int>(skip % per_row);
+    return launch_pdl(embedding_forward_kernel<TT, OT>, blocks, block, 0, s, a);
+  }
+  // a row's granules of a unit: one more than the most that it can touch
+  const int granules = (a.D + 2 * (GE - 1)) / GE + 1;
   int per_row = 8;
   while (per_row < granules && per_row < UNIT) per_row *= 2;
-  a.tiles = granules <= UNIT ? 1 : (granules - (aligned ? 0 : 1) + writes - 1) / writes;
+  a.tiles = granules <= UNIT ? 1 : (granules - 1 + UNIT - 2) / (UNIT - 1);
   a.log_rows = 0;
   while ((per_row << a.log_rows) < UNIT) ++a.log_rows;
   const long long units = a.tiles > 1 ? a.n * a.tiles : (a.n + (1 << a.log_rows) - 1) >> a.log_rows;
-  auto grid = [&](int resident) {
-    return dim3(static_cast<unsigned>(std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * resident)));
-  };
-  if (aligned) return launch_pdl(embedding_forward_kernel<TT, OT>, grid(FWD_BLOCKS), block, 0, s, a);
   constexpr size_t smem = THREADS * CUT_STAGES * (UNIT / 32) * (Raw<TT, GE>::BYTES + 4);
   static const cudaError_t allowed = cudaFuncSetAttribute(
       embedding_forward_cut_kernel<TT, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (allowed != cudaSuccess) return allowed;
-  return launch_pdl(embedding_forward_cut_kernel<TT, OT>, grid(CUT_BLOCKS), block, smem, s, a);
+  return launch_pdl(embedding_forward_cut_kernel<TT, OT>, grid(units, CUT_BLOCKS), block, smem, s, a);
 }
 
 muon_status launch_sort(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
