@@ -32,9 +32,9 @@ namespace muon {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int FWD_BLOCKS = 5, CUT_BLOCKS = 3;    // resident blocks of the lookup's kernels
-constexpr int CUT_STAGES = 3;
-constexpr int LOG_UNIT = 7, UNIT = 1 << LOG_UNIT;   // granules per warp and turn of the lookup: four per lane
+constexpr int FWD_BLOCKS = 5, CUT_BLOCKS = 5;    // resident blocks of the lookup's kernels
+constexpr int CUT_STAGES = 2;
+constexpr int UNIT = 128;        // granules per warp and turn of the lookup: four per lane
 constexpr int SUM_COLS = 256;    // columns per warp of the gradient's sums: 8 per lane
 constexpr int SUM_BLOCKS = 3;    // resident blocks of the gradient's sums
 constexpr int GROUP = 32;        // sorted positions per warp of the gradient's sums
@@ -105,17 +105,48 @@ struct LookupArgs {
   const void *ids, *table;
   void *out;
   long long ldt, ldo, n, V;
-  int itype, D, tiles, log_rows;   // units per long row; log2 of the rows per unit of short ones
+  int itype, D;
   float scale;
   int past_table, past_out;   // values by which the bases are past a granule's boundary
-  // aligned rows: 2^32 / granules per row, and the rows and granules from a warp's unit to its next one
+  int per_row;                // granules of a row, and 2^32 / per_row, rounded up
   unsigned inverse;
-  int skip;
+  int skip;                   // granules, and whole rows, from a warp's unit to its next one
   long long skip_rows;
 };
 
+// A warp's unit of work: it starts at granule `first` of row `row`, and rows have a.per_row granules.
+struct LookupUnit {
+  long long row;
+  int first;
+  struct Place {
+    long long row;
+    int granule;
+  };
+  __device__ __forceinline__ LookupUnit(const LookupArgs &a, long long granule)
+      : row(granule / a.per_row), first(static_cast<int>(granule - row * a.per_row)) {}
+  // granule i < UNIT of the unit. first + i < per_row + UNIT, so that the high half of its product with 2^32 / per_row,
+  // rounded up, is the quotient
+  __device__ __forceinline__ Place place(const LookupArgs &a, int i) const {
+    const int at = first + i, rows = a.per_row == 1 ? at : static_cast<int>(__umulhi(at, a.inverse));
+    return {row + rows, at - rows * a.per_row};
+  }
+  __device__ __forceinline__ void next(const LookupArgs &a) {
+    row += a.skip_rows;
+    first += a.skip;
+    if (first >= a.per_row) ++row, first -= a.per_row;
+  }
+  // the ids of the lane's granules, -1 for what names no row
+  __device__ __forceinline__ void ids(const LookupArgs &a, int lane, int *id) const {
+#pragma unroll
+    for (int q = 0; q < UNIT / 32; ++q) {
+      const long long r = place(a, q * 32 + lane).row, v = r < a.n ? load_id(a.ids, a.itype, r) : -1;
+      id[q] = v >= 0 && v < a.V ? static_cast<int>(v) : -1;
+    }
+  }
+};
+
 // Rows that start on a granule and have whole ones: warps take units of 128 granules in turn, four per lane, which follow
-// each other through the rows (of any length, so that no lane is idle: 65536 rows of 768 bf16 FIGURES). All loads of a unit
+// each other through the rows (of any length, so that no lane is idle: 65536 rows of 768 bf16 24 us, and 29 us with units of whole rows). All loads of a unit
 // are in flight before the first is used, and the ids of the next unit are loaded under them, so that a unit waits for one
 // latency, not two.
 template <typename TT, typename OT>
@@ -123,64 +154,42 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
   constexpr int GE = granule_of<TT, OT>(), U = UNIT / 32;
-  const int lane = threadIdx.x % 32, per_row = a.D / GE;
-  const long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
   const TT *table = static_cast<const TT *>(a.table);
-  struct Place {
-    long long row;
-    int c;
-  };
-  // where granule `place` after the first one of row r is; place < per_row + UNIT, so that the high half of its product
-  // with 2^32 / per_row, rounded up, is the quotient
-  auto place_of = [&](long long r, int place) {
-    const int rows = per_row == 1 ? place : static_cast<int>(__umulhi(place, a.inverse));
-    return Place{r + rows, (place - rows * per_row) * GE};
-  };
-  long long row = w * UNIT / per_row;   // of the warp's unit, and its granule in it
-  int first = static_cast<int>(w * UNIT - row * per_row);
-  auto ids_of = [&](long long r, int g, int *id) {
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const Place p = place_of(r, g + q * 32 + lane);
-      const long long v = p.row < a.n ? load_id(a.ids, a.itype, p.row) : -1;
-      id[q] = v >= 0 && v < a.V ? static_cast<int>(v) : -1;
-    }
-  };
+  LookupUnit u(a, (static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32) * UNIT);
   int next[U];
-  ids_of(row, first, next);
-  while (row < a.n) {
+  u.ids(a, lane, next);
+  while (u.row < a.n) {
     int id[U];
     Raw<TT, GE> r[U];
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       id[q] = next[q];
       r[q].clear();
-      if (id[q] >= 0) r[q].load(table + id[q] * a.ldt + place_of(row, first + q * 32 + lane).c);
+      if (id[q] >= 0) r[q].load(table + id[q] * a.ldt + u.place(a, q * 32 + lane).granule * GE);
     }
-    long long then = row + a.skip_rows;
-    int then_first = first + a.skip;
-    if (then_first >= per_row) ++then, then_first -= per_row;
-    ids_of(then, then_first, next);
+    LookupUnit then = u;
+    then.next(a);
+    then.ids(a, lane, next);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const Place p = place_of(row, first + q * 32 + lane);
+      const auto p = u.place(a, q * 32 + lane);
       if (p.row >= a.n) continue;
       Vals<GE> o = r[q].get();
 #pragma unroll
       for (int i = 0; i < GE / 2; ++i)
         o.p[i] = id[q] < 0 ? make_float2(0.f, 0.f) : __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
-      store_vals(static_cast<OT *>(a.out) + p.row * a.ldo + p.c, o);
+      store_vals(static_cast<OT *>(a.out) + p.row * a.ldo + p.granule * GE, o);
     }
-    row = then;
-    first = then_first;
+    u = then;
   }
 }
 
-// Other rows: a unit is 128 granules of a long row, or of as many short rows as fit, and its granules are those of the
-// table around the output's, one more than it writes. The granules of the
-// next units are on their way to the warp's ring in shared memory, and the ids of the one after on theirs, while a unit
-// is stored. (65536 rows of 771 bf16: 49 us, and 76 us with two loads per lane and granule into registers; but where
-// rows are aligned the ring takes 194 us for 65536 rows of 4096, and registers 138 us.)
+// Other rows: a row's granules are those of the table around the output's, one more than are written; each is copied to
+// the warp's ring in shared memory, and an output granule is cut out of two. A unit's last granule is only copied: it is
+// the next unit's first. The granules of the next units are on their way, and the ids of the one after on theirs, while a
+// unit is stored. (65536 rows of 771 bf16: 41 us, and 76 us with two loads per lane and granule into registers; but
+// where rows are aligned the ring takes 194 us for 65536 rows of 4096, and registers 138 us.)
 template <typename TT, typename OT>
 __global__ void __launch_bounds__(THREADS, CUT_BLOCKS) embedding_forward_cut_kernel(const LookupArgs a) {
   pdl_wait();
@@ -191,34 +200,18 @@ __global__ void __launch_bounds__(THREADS, CUT_BLOCKS) embedding_forward_cut_ker
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   unsigned char *ring = shared + w * (S * UNIT * B);
   int *kept = reinterpret_cast<int *>(shared + WARPS * S * UNIT * B) + threadIdx.x;   // the ids of units in the ring
-  const bool many = a.tiles == 1;
-  const long long units = many ? (a.n + (1 << a.log_rows) - 1) >> a.log_rows : a.n * a.tiles;
-  const long long warps = static_cast<long long>(gridDim.x) * WARPS, total = (a.V - 1) * a.ldt + a.D;
+  const long long total = (a.V - 1) * a.ldt + a.D;
   const TT *table = static_cast<const TT *>(a.table);
-  const int per_row = UNIT >> (many ? a.log_rows : 0);
-  // row of the lane's granule q of unit u, the granule's place among the row's of the unit, and its first column
-  auto row_of = [&](long long u, int q) {
-    return many ? (u << a.log_rows) + ((q * 32 + lane) >> (LOG_UNIT - a.log_rows)) : u / a.tiles;
+  // first column of a granule, in the output row's own granules
+  auto column = [&](const LookupUnit::Place &p) {
+    return p.granule * GE - static_cast<int>((p.row * a.ldo + a.past_out) & (GE - 1));
   };
-  auto place = [&](int q) { return (q * 32 + lane) & (per_row - 1); };
-  auto first_of = [&](long long u, long long row, int q) {
-    const int g = (many ? 0 : static_cast<int>(u % a.tiles) * (UNIT - 1)) + place(q);
-    return g * GE - static_cast<int>((row * a.ldo + a.past_out) & (GE - 1));
-  };
-  auto ids_of = [&](long long u, int *id) {
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const long long r = row_of(u, q);
-      const long long v = u < units && r < a.n ? load_id(a.ids, a.itype, r) : -1;
-      id[q] = v >= 0 && v < a.V ? static_cast<int>(v) : -1;
-    }
-  };
-  auto fetch = [&](long long u, int stage, const int *id) {
+  auto fetch = [&](const LookupUnit &u, int stage, const int *id) {
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       kept[(stage * U + q) * THREADS] = id[q];
       if (id[q] < 0) continue;
-      const int c = first_of(u, row_of(u, q), q);
+      const int c = column(u.place(a, q * 32 + lane));
       unsigned char *slot = ring + (stage * UNIT + q * 32 + lane) * B;
       const long long at = id[q] * a.ldt + c;
       if (c < a.D + GE) {
@@ -234,26 +227,28 @@ __global__ void __launch_bounds__(THREADS, CUT_BLOCKS) embedding_forward_cut_ker
     }
     copy_async_commit();
   };
-  long long u = static_cast<long long>(blockIdx.x) * WARPS + w;
+  LookupUnit u(a, (static_cast<long long>(blockIdx.x) * WARPS + w) * (UNIT - 1)), ahead = u;
   int id[U];
 #pragma unroll
   for (int k = 0; k < S - 1; ++k) {
-    ids_of(u + k * warps, id);
-    fetch(u + k * warps, k, id);
+    ahead.ids(a, lane, id);
+    fetch(ahead, k, id);
+    ahead.next(a);
   }
-  ids_of(u + (S - 1) * warps, id);
+  ahead.ids(a, lane, id);
   int stage = 0;
-  for (; u < units; u += warps) {
+  for (; u.row < a.n; u.next(a)) {
     copy_async_wait<S - 2>();
     __syncwarp();
     // the place of the unit before this one, which all lanes have read
-    fetch(u + (S - 1) * warps, stage == 0 ? S - 1 : stage - 1, id);
-    ids_of(u + S * warps, id);
+    fetch(ahead, stage == 0 ? S - 1 : stage - 1, id);
+    ahead.next(a);
+    ahead.ids(a, lane, id);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const long long row = row_of(u, q);
-      const int c = first_of(u, row, q), at = kept[(stage * U + q) * THREADS];
-      if (row >= a.n || c >= a.D || place(q) == per_row - 1) continue;
+      const auto p = u.place(a, q * 32 + lane);
+      const int c = column(p), at = kept[(stage * U + q) * THREADS];
+      if (p.row >= a.n || c >= a.D || p.granule == a.per_row - 1 || q * 32 + lane == UNIT - 1) continue;
       const unsigned char *slot = ring + (stage * UNIT + q * 32 + lane) * B;
       Vals<GE> o;
 #pragma unroll
@@ -266,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, CUT_BLOCKS) embedding_forward_cut_ker
 #pragma unroll
         for (int i = 0; i < GE / 2; ++i) o.p[i] = __fmul2_rn(o.p[i], make_float2(a.scale, a.scale));
       }
-      OT *dst = static_cast<OT *>(a.out) + row * a.ldo;
+      OT *dst = static_cast<OT *>(a.out) + p.row * a.ldo;
       if (c >= 0 && c + GE <= a.D) store_vals(dst + c, o);
       else store_edge(dst, c, a.D, o);
     }
@@ -908,31 +903,23 @@ cudaError_t launch_lookup(LookupArgs a, cudaStream_t s) {
   const dim3 block(THREADS);
   a.past_table = past<TT, GE>(a.table);
   a.past_out = past<OT, GE>(a.out);
-  const auto grid = [&](long long units, int resident) {
-    return dim3(static_cast<unsigned>(std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * resident)));
-  };
-  if (a.D % GE == 0 && a.ldt % GE == 0 && a.ldo % GE == 0 && a.past_table == 0 && a.past_out == 0) {
-    const long long per_row = a.D / GE;
-    const dim3 blocks = grid((a.n * per_row + UNIT - 1) / UNIT, FWD_BLOCKS);
-    const long long skip = static_cast<long long>(blocks.x) * (THREADS / 32) * UNIT;
-    a.inverse = static_cast<unsigned>(((1ull << 32) + per_row - 1) / per_row);
-    a.skip_rows = skip / per_row;
-    a.skip = static_cast<int>(skip % per_row);
-    return launch_pdl(embedding_forward_kernel<TT, OT>, blocks, block, 0, s, a);
-  }
-  // a row's granules of a unit: one more than the most that it can touch
-  const int granules = (a.D + 2 * (GE - 1)) / GE + 1;
-  int per_row = 8;
-  while (per_row < granules && per_row < UNIT) per_row *= 2;
-  a.tiles = granules <= UNIT ? 1 : (granules - 1 + UNIT - 2) / (UNIT - 1);
-  a.log_rows = 0;
-  while ((per_row << a.log_rows) < UNIT) ++a.log_rows;
-  const long long units = a.tiles > 1 ? a.n * a.tiles : (a.n + (1 << a.log_rows) - 1) >> a.log_rows;
+  const bool aligned =
+      a.D % GE == 0 && a.ldt % GE == 0 && a.ldo % GE == 0 && a.past_table == 0 && a.past_out == 0;
+  // not aligned: the most granules that a row touches, and one more
+  a.per_row = aligned ? a.D / GE : (a.D + 2 * (GE - 1)) / GE + 1;
+  const long long unit = aligned ? UNIT : UNIT - 1, units = (a.n * a.per_row + unit - 1) / unit;
+  const dim3 grid(static_cast<unsigned>(
+      std::min((units + THREADS / 32 - 1) / (THREADS / 32), sms * (aligned ? FWD_BLOCKS : CUT_BLOCKS))));
+  const long long skip = static_cast<long long>(grid.x) * (THREADS / 32) * unit;
+  a.inverse = static_cast<unsigned>(((1ull << 32) + a.per_row - 1) / a.per_row);
+  a.skip_rows = skip / a.per_row;
+  a.skip = static_cast<int>(skip % a.per_row);
+  if (aligned) return launch_pdl(embedding_forward_kernel<TT, OT>, grid, block, 0, s, a);
   constexpr size_t smem = THREADS * CUT_STAGES * (UNIT / 32) * (Raw<TT, GE>::BYTES + 4);
   static const cudaError_t allowed = cudaFuncSetAttribute(
       embedding_forward_cut_kernel<TT, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (allowed != cudaSuccess) return allowed;
-  return launch_pdl(embedding_forward_cut_kernel<TT, OT>, grid(units, CUT_BLOCKS), block, smem, s, a);
+  return launch_pdl(embedding_forward_cut_kernel<TT, OT>, grid, block, smem, s, a);
 }
 
 muon_status launch_sort(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
