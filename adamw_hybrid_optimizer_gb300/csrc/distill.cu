@@ -486,6 +486,9 @@ __device__ __forceinline__ float weight_of(const DistillArgs &a, long long row) 
 // Blocks of a multiprocessor for TH threads, at 64 registers each.
 constexpr int blocks_of(int TH) { return std::min(32, 1024 / TH); }
 
+// Loss and stats. One pass with a running maximum and sum per thread, and one exchange of both softmaxes' pairs between
+// the block's warps. Bound by the rate at which a block's chains of loads start and end more than by memory's: 8192 x 50304
+// bf16 in 150 us, 5.5 TB/s; 4096 x 128256 in 171 us, 6.1 TB/s, and of fp32 in 291 us, 7.2 TB/s.
 template <typename ZT, int TH, bool VEC>
 __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_forward_kernel(const DistillArgs a) {
   pdl_wait();
@@ -531,6 +534,8 @@ __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_forward_kernel(cons
   if (slices > 1) cluster_sync();   // no block leaves while another reads its shared memory
 }
 
+// The gradient from the stats: no exchange but the teacher's, and every block has its own slice of a row. Bound by memory:
+// 4096 x 128256 bf16 in 315 us, 6.7 TB/s.
 template <typename ZT, typename DT, int TH, bool VEC>
 __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_backward_kernel(const DistillArgs a) {
   pdl_wait();
@@ -571,6 +576,9 @@ __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_backward_kernel(con
   subtract_teacher<TH>(a, s, dz, lo, hi, c, m, inv, scale, teacher);
 }
 
+// Loss and gradient: the forward kernel's pass, then the backward kernel's over the same row, out of L2. Memory sees each
+// logit and each gradient once (8192 x 50304 bf16: 312 us, 5.3 TB/s), and what bounds it is the two passes' instructions:
+// with a row kept in shared memory in between, and the next one on its way there, it took 400 us.
 template <typename ZT, typename DT, int TH, bool VEC>
 __global__ void __launch_bounds__(TH, blocks_of(TH)) distill_joint_kernel(const DistillArgs a) {
   pdl_wait();

@@ -315,9 +315,11 @@ muon_status ns_apply(const void *h, const void *x, void *out, int64_t K, int64_t
  * output layer and vectors stay on AdamW): the embedding lookup, layer norm and a loss at the vocabulary head, each
  * with its gradients, which adamw_step_grouped takes as they are written. The pages name the tensors, not these
  * operators' kernels. For all of them: a matrix has contiguous columns and a row pitch in elements (ld..., at least
- * its columns); pointers need the alignment of their element type (MUON_ERR_ALIGNMENT otherwise), and 16-byte
- * aligned pointers with pitches that are multiples of 8 take the vectorised path; sums are fp32, rounded once when
- * stored; no sum goes through an atomic, so the same inputs give the same bits. A call with no rows launches
+ * its columns); pointers need the alignment of their element type (MUON_ERR_ALIGNMENT otherwise); 16-byte
+ * vectors are used at any pitch and width by the embedding, and where the bases are 16-byte aligned and the pitches of a
+ * call's matrices differ by multiples of 8 by the other two (odd widths included), which otherwise access single values;
+ * sums are fp32, rounded once when stored; no sum goes through an atomic, so the same inputs at the same addresses modulo
+ * 16 give the same bits. A call with no rows launches
  * nothing (backward calls still write the weights' gradients, as zeros) and may pass null for the empty arrays.
  * ------------------------------------------------------------------------------------------------------------ */
 
@@ -396,8 +398,8 @@ muon_status distill_backward(const void *logits, muon_dtype zdt, int64_t ldz, co
                              int64_t K, float temperature, muon_stream_t stream);
 
 /* Both in one call, for a training step whose loss is grad_scale * sum of losses: losses and stats as
- * distill_forward writes them, dlogits as distill_backward writes it with grad = grad_scale for every row. The
- * logits are read from device memory once. */
+ * distill_forward writes them, dlogits as distill_backward writes it with grad = grad_scale for every row. A
+ * row is read a second time soon after the first, from L2 unless the rows on their way at once exceed it. */
 muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t ldz, const void *t_idx,
                                      muon_itype itype, const void *t_val, muon_dtype tdt, const float *weights,
                                      float grad_scale, float *losses, float *stats, void *dlogits, muon_dtype ddt,
