@@ -204,9 +204,9 @@ struct Ring {
 };
 
 // A vector of weights (or biases), as each thread wants its own columns of it row after row: in registers where there
-// is one chunk, as fp32 in shared memory up to 8192 columns of several chunks, and read where it is beyond that (and in
-// SCALAR, for several chunks). The block's rows share it.
-template <typename CT, int C, int THREADS, bool SHARED>
+// is one chunk, as fp32 in shared memory where there are several and they fit beside the ring, and otherwise read (from
+// cache) row after row. The block's rows share it.
+template <typename CT, int C, bool SHARED>
 struct Params {
   static constexpr int STRIDE = CT::T, BYTES = SHARED ? 32 * C * STRIDE : 0;
   const void *p;

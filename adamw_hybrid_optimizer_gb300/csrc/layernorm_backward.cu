@@ -44,7 +44,7 @@ struct Backward {
   static constexpr bool IN_SHARED = W == 32, RING = MODE != SCALAR && !IN_SHARED;
   static constexpr bool AHEAD = !IN_SHARED || sizeof(XT) + sizeof(YT) == 4;
   static constexpr bool SHARED = RING && C > 1;
-  using PT = Params<CT, C, THREADS, SHARED>;
+  using PT = Params<CT, C, SHARED>;
   static constexpr int STAGES = C * T * 8 * (sizeof(XT) + sizeof(YT)) <= 16384 ? 3 : 2;
   static constexpr int RING_X = RING ? STAGES * C * 8 * sizeof(XT) * THREADS : 0;   // bytes
   static constexpr int RING_DY = RING ? STAGES * C * 8 * sizeof(YT) * THREADS : 0;

@@ -33,7 +33,7 @@ struct Forward {
   static constexpr int STAGES = C * T * 8 * sizeof(XT) <= 16384 ? 3 : 2;
   static constexpr int ROWS = RING ? STAGES * C * 8 * sizeof(XT) * THREADS : 0;   // bytes of the ring
   static constexpr bool SHARED = RING && C > 1 && ROWS + 64 * C * T <= 200 * 1024;   // the weights, beside the ring
-  using PT = Params<CT, C, THREADS, SHARED>;
+  using PT = Params<CT, C, SHARED>;
   static constexpr size_t BYTES = static_cast<size_t>(ROWS) + 2 * PT::BYTES;
   static constexpr int by_registers = C >= 3 ? 768 : 1024;   // threads
   static constexpr int BLOCKS = std::max(1, by_registers / THREADS);   // of a multiprocessor
