@@ -15,9 +15,9 @@
 //                             gradient (unless it accumulates).
 //   embedding_zero_kernel     the zeroes alone, before a longer sort.
 //   radix_*_kernel            one pass of a longer sort: digit counts per tile, their scan, the stable scatter.
-//   embedding_sum_kernel      one warp per 32 sorted positions and 256 columns; the rows to come are in flight whether or
+//   embedding_sum_kernel      one warp per 16 or 32 sorted positions and 256 columns; the rows to come are in flight whether or
 //                             not they belong to the id being summed, since most ids occur once or twice.
-//   embedding_join_kernel     ids whose run spans a whole group of 32 or more: adds the groups' sums in order.
+//   embedding_join_kernel     ids whose run spans a whole group or more: adds the groups' sums in order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,7 +37,10 @@ constexpr int CUT_STAGES = 2;
 constexpr int UNIT = 128;        // granules per warp and turn of the lookup: four per lane
 constexpr int SUM_COLS = 256;    // columns per warp of the gradient's sums: 8 per lane
 constexpr int SUM_BLOCKS = 3;    // resident blocks of the gradient's sums
-constexpr int GROUP = 32;        // sorted positions per warp of the gradient's sums
+// Sorted positions per warp of the gradient's sums: 32, or 16 with blocks of four warps where there are at most FEW_UNITS
+// groups of 16 and 256 columns (152 multiprocessors, SUM_BLOCKS of 4 warps, twice).
+constexpr int FEW_UNITS = 3648;
+constexpr int group_of(int warps) { return 4 * warps; }
 constexpr int SORT_TILE = 4096;  // keys per block of a sort pass
 constexpr int MAX_DIGIT_BITS = 9;
 constexpr unsigned NO_KEY = 0xffffffffu;
@@ -585,7 +588,7 @@ struct SumArgs {
   uint2 *list;                 // (group where such a run starts, groups that it touches)
   unsigned *list_count;
   long long n, V, ldp;
-  int D, tiles, groups, accumulate, past_dout, past_g;   // past: values by which a base is past a boundary
+  int D, tiles, group, groups, accumulate, past_dout, past_g;   // past: values by which a base is past a boundary
   float scale;
 };
 
@@ -709,7 +712,7 @@ __device__ __forceinline__ unsigned run_groups(const SumArgs &a, long long c, un
   long long lo = c + 2, hi = a.groups;   // groups below lo are the run's, hi is not (or the end)
   while (lo < hi) {
     const long long stride = (hi - lo + 31) / 32, probe = lo + lane * stride;
-    const unsigned yes = __ballot_sync(0xffffffffu, probe < hi && a.key[probe < hi ? probe * GROUP : 0] == k);
+    const unsigned yes = __ballot_sync(0xffffffffu, probe < hi && a.key[probe < hi ? probe * a.group : 0] == k);
     const int ok = __popc(yes);   // the run's probes are the first ones
     if (ok == 0) {
       hi = lo;
@@ -724,7 +727,7 @@ __device__ __forceinline__ unsigned run_groups(const SumArgs &a, long long c, un
 
 // A run of equal ids that starts in group c belongs to it, unless the run covers the whole of the next group and
 // goes on (a long run): then every group sums its own part, into part[2c + 1] where the run starts and part[2c]
-// where it came from the group before, and the join kernel adds the parts. So a warp sums at most 63 positions. The rows
+// where it came from the group before, and the join kernel adds the parts. So a warp sums fewer positions than two groups have. The rows
 // to come are on their way to the warp's ring in shared memory, whether or not they belong to one id. The loop is short on
 // purpose: with a store for the end of a run unrolled into every place of a batch in registers, the code did not fit the
 // instruction cache (131072 rows of 64: 45 us, and 27 us now). Bound by memory, dout read once and the rows that ids name
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(WARPS * 32, SUM_BLOCKS) embedding_sum_kernel(c
   if (threadIdx.x == 0) pdl_launch_dependents();
   constexpr int GE = granule_of<OT, GT>();
   using Ring = SumRing<OT, GE, ACCESS, WARPS>;
-  constexpr int S = Ring::SLOTS;
+  constexpr int S = Ring::SLOTS, GROUP = group_of(WARPS);
   extern __shared__ __align__(16) unsigned char shared[];
   const int lane = threadIdx.x % 32;
   unsigned char *ring = shared + threadIdx.x / 32 * Ring::BYTES;
@@ -748,11 +751,12 @@ __global__ void __launch_bounds__(WARPS * 32, SUM_BLOCKS) embedding_sum_kernel(c
     const int tile = static_cast<int>(u - c * a.tiles);
     const long long s = c * GROUP;
     auto key_at = [&](long long i) { return i >= 0 && i < a.n ? a.key[i] : NO_KEY; };
-    const unsigned k0 = key_at(s + lane), k1 = key_at(s + GROUP + lane);
-    const unsigned p0 = s + lane < a.n ? a.pos[s + lane] : 0u;
-    const unsigned p1 = s + GROUP + lane < a.n ? a.pos[s + GROUP + lane] : 0u;
+    const bool has = lane < GROUP;
+    const unsigned k0 = has ? key_at(s + lane) : NO_KEY, k1 = has ? key_at(s + GROUP + lane) : NO_KEY;
+    const unsigned p0 = has && s + lane < a.n ? a.pos[s + lane] : 0u;
+    const unsigned p1 = has && s + GROUP + lane < a.n ? a.pos[s + GROUP + lane] : 0u;
     const unsigned before = key_at(s - 1), far_before = key_at(s - GROUP - 1), far_after = key_at(s + 2 * GROUP);
-    const unsigned first = __shfl_sync(0xffffffffu, k0, 0), last = __shfl_sync(0xffffffffu, k0, 31);
+    const unsigned first = __shfl_sync(0xffffffffu, k0, 0), last = __shfl_sync(0xffffffffu, k0, GROUP - 1);
     const unsigned next = __shfl_sync(0xffffffffu, k1, 0);
     if (first >= none) continue;                       // only ids that take no gradient from here on
     int begin = 0;
@@ -823,7 +827,7 @@ __global__ void __launch_bounds__(THREADS) embedding_join_kernel(const SumArgs a
     const uint2 run = a.list[u / a.tiles];
     const long long c = run.x, parts = run.y;
     const int tile = static_cast<int>(u % a.tiles);
-    const unsigned k = a.key[c * GROUP + GROUP - 1];
+    const unsigned k = a.key[(c + 1) * a.group - 1];
     Vals<8> acc;
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc.p[i] = make_float2(0.f, 0.f);
@@ -857,6 +861,7 @@ __global__ void __launch_bounds__(THREADS) embedding_join_kernel(const SumArgs a
 struct EmbeddingLayout {
   size_t key[2], pos[2], hist, list, part, total;
   long long groups, tiles, ldp;
+  int group;
 };
 
 EmbeddingLayout embedding_layout(long long n, long long D) {
@@ -867,10 +872,11 @@ EmbeddingLayout embedding_layout(long long n, long long D) {
     at += align_up(bytes, 256);
     return a;
   };
-  L.groups = (n + GROUP - 1) / GROUP;
   L.tiles = (n + SORT_TILE - 1) / SORT_TILE;
   L.ldp = (D + 7 + SUM_COLS - 1) / SUM_COLS * SUM_COLS;   // rows past a boundary reach up to 7 columns further
-  L.list = take(8 * (1 + static_cast<size_t>(n) / GROUP));   // the count, then the pairs
+  L.group = group_of((n + 15) / 16 * ((D + SUM_COLS - 1) / SUM_COLS) <= FEW_UNITS ? 4 : 8);
+  L.groups = (n + L.group - 1) / L.group;
+  L.list = take(8 * (1 + static_cast<size_t>(L.groups)));   // the count, then the pairs
   for (int k = 0; k < 2; ++k) L.key[k] = take(4 * static_cast<size_t>(n));
   for (int k = 0; k < 2; ++k) L.pos[k] = take(4 * static_cast<size_t>(n));
   L.hist = take(4 * static_cast<size_t>(L.tiles) << MAX_DIGIT_BITS);
@@ -1051,9 +1057,9 @@ muon_status launch_sums(SumArgs a, cudaStream_t s) {
   a.tiles = (a.D + (ACCESS == CUT ? granule_of<OT, GT>() - 1 : 0) + SUM_COLS - 1) / SUM_COLS;
   const long long sms = device_sm_count();
   const long long units = static_cast<long long>(a.groups) * a.tiles;
-  // few units: the time is that of one of them, and half the warps have twice the rows on their way (16384 rows of 768
-  // fp32: 45 us, and 48 us with eight warps; 1024 rows of bf16: 27 and 31 us)
-  muon_status st = units <= sms * SUM_BLOCKS * 4 ? launch_sum<OT, GT, ACCESS, 4>(a, units, s)
+  // few units: the time is that of one of them, which is shorter, and half the warps have twice the rows on their way
+  // (8192 rows of 768 bf16: 28 us, and 33 us with groups of 32; 1024 rows: 23 and 27 us, and 31 us with eight warps too)
+  muon_status st = a.group == group_of(4) ? launch_sum<OT, GT, ACCESS, 4>(a, units, s)
                                                  : launch_sum<OT, GT, ACCESS, 8>(a, units, s);
   if (st != MUON_OK || a.groups < 3) return st;   // no run can be long
   // no more long runs than a third of the groups
@@ -1152,6 +1158,7 @@ muon_status embedding_backward(const void *ids, muon_itype itype, const void *do
   a.V = V;
   a.ldp = L.ldp;
   a.D = Di;
+  a.group = L.group;
   a.groups = static_cast<int>(L.groups);
   a.accumulate = accumulate != 0;
   a.scale = scale;
