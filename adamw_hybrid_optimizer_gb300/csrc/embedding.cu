@@ -15,8 +15,8 @@
 //                             gradient (unless it accumulates).
 //   embedding_zero_kernel     the zeroes alone, before a longer sort.
 //   radix_*_kernel            one pass of a longer sort: digit counts per tile, their scan, the stable scatter.
-//   embedding_sum_kernel      one warp per 16 or 32 sorted positions and 256 columns; the rows to come are in flight whether or
-//                             not they belong to the id being summed, since most ids occur once or twice.
+//   embedding_sum_kernel      one warp per 16 or 32 sorted positions and 256 columns; the rows to come are in flight
+//                             whether or not they belong to the id being summed, since most ids occur once or twice.
 //   embedding_join_kernel     ids whose run spans a whole group or more: adds the groups' sums in order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -727,12 +727,13 @@ __device__ __forceinline__ unsigned run_groups(const SumArgs &a, long long c, un
 
 // A run of equal ids that starts in group c belongs to it, unless the run covers the whole of the next group and
 // goes on (a long run): then every group sums its own part, into part[2c + 1] where the run starts and part[2c]
-// where it came from the group before, and the join kernel adds the parts. So a warp sums fewer positions than two groups have. The rows
-// to come are on their way to the warp's ring in shared memory, whether or not they belong to one id. The loop is short on
-// purpose: with a store for the end of a run unrolled into every place of a batch in registers, the code did not fit the
-// instruction cache (131072 rows of 64: 45 us, and 27 us now). Bound by memory, dout read once and the rows that ids name
-// written once, behind the sort and the zeroes: 32768 x 4096 bf16 in 64 us, 330 MB at 5.2 TB/s; the whole gradient of
-// 128256 rows in 212 us, 6.2 TB/s.
+// where it came from the group before, and the join kernel adds the parts. So a warp sums fewer positions than two
+// groups have. The rows to come are on their way to the warp's ring in shared memory, whether or not they belong to
+// one id. The loop is short on purpose: with a store for the end of a run unrolled into every place of a batch in
+// registers, the code did not fit the instruction cache (131072 rows of 64: 45 us, and 27 us now). Bound by memory,
+// dout read once and the rows that ids name written once, behind the sort and the zeroes: 32768 x 4096 bf16 in 64 us,
+// 330 MB at 5.2 TB/s; the whole gradient of 128256 rows in 212 us, 6.2 TB/s. Few tokens: by the latency of the
+// positions of one warp, some 90 instructions each.
 template <typename OT, typename GT, int ACCESS, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, SUM_BLOCKS) embedding_sum_kernel(const SumArgs a) {
   pdl_wait();

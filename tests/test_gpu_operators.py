@@ -68,7 +68,7 @@ def byte_ws(n):
 # 32 sorted positions; a vocabulary of three digits; runs that end on group boundaries
 EMBED = [(0, 7, 5), (1, 1, 1), (3, 5, 7), (33, 10, 256), (65, 2, 40), (257, 50, 300), (1000, 3, 776), (5000, 17, 24),
          (4097, 600, 130), (70000, 40, 8), (9000, 300000, 16), (8192, 1000, 1030), (96, 1, 64), (140000, 900, 8), (100000, 5000, 72),
-         (600, 90, 133), (3000, 40, 1337)]
+         (600, 90, 133), (3000, 40, 1337), (60000, 300, 513), (30000, 200, 776)]
 
 
 def make_ids(n, V, seed, it):
