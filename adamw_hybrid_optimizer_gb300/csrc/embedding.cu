@@ -929,8 +929,11 @@ cudaError_t launch_lookup(LookupArgs a, cudaStream_t s) {
   a.skip = static_cast<int>(skip % a.per_row);
   if (aligned) return launch_pdl(embedding_forward_kernel<TT, OT>, grid, block, 0, s, a);
   constexpr size_t smem = THREADS * CUT_STAGES * (UNIT / 32) * (Raw<TT, GE>::BYTES + 4);
-  static const cudaError_t allowed = cudaFuncSetAttribute(
-      embedding_forward_cut_kernel<TT, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static AttributesSet set;
+  const cudaError_t allowed = set.once([] {
+    return cudaFuncSetAttribute(embedding_forward_cut_kernel<TT, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem));
+  });
   if (allowed != cudaSuccess) return allowed;
   return launch_pdl(embedding_forward_cut_kernel<TT, OT>, grid, block, smem, s, a);
 }
@@ -981,12 +984,14 @@ muon_status launch_sort(const void *ids, int itype, long long n, long long V, lo
 muon_status launch_prepare(const void *ids, int itype, long long n, long long V, long long padding, char *ws,
                            const EmbeddingLayout &L, const ZeroArgs &z, const unsigned **key, const unsigned **pos,
                            cudaStream_t s) {
-  static const cudaError_t allowed =
-      cudaFuncSetAttribute(embedding_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(ClusterShared)));
-  static const cudaError_t wide =   // 16 blocks
-      cudaFuncSetAttribute(embedding_prepare_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (allowed != cudaSuccess || wide != cudaSuccess) return MUON_ERR_CUDA;
+  static AttributesSet set;
+  const cudaError_t allowed = set.once([] {
+    const cudaError_t e = cudaFuncSetAttribute(embedding_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(ClusterShared)));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(embedding_prepare_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);   // 16 blocks
+  });
+  if (allowed != cudaSuccess) return MUON_ERR_CUDA;
   int key_bits = 1;
   while ((V >> key_bits) != 0) ++key_bits;
   ClusterSort a{};
@@ -1042,7 +1047,9 @@ template <typename OT, typename GT, int ACCESS, int WARPS>
 muon_status launch_sum(const SumArgs &a, long long units, cudaStream_t s) {
   const auto kernel = embedding_sum_kernel<OT, GT, ACCESS, WARPS>;
   constexpr int smem = WARPS * SumRing<OT, granule_of<OT, GT>(), ACCESS, WARPS>::BYTES;
-  static const cudaError_t allowed = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static AttributesSet set;
+  const cudaError_t allowed =
+      set.once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (allowed != cudaSuccess) return MUON_ERR_CUDA;
   const long long blocks = std::min((units + WARPS - 1) / WARPS, 4096ll * device_sm_count());
   launch_begin(KK_EMBED_SUM, s);

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cmath>
 #include <utility>
 #include <vector>
@@ -51,6 +52,28 @@ int device_sm_count();
 // The current device's capability check and the per-wait limit set by muon_set_timeout_ns (libmuon.cu).
 muon_status device_check();
 unsigned long long wait_timeout_ns();
+
+// Whether a kernel's function attributes are set, by device: an attribute belongs to the device that is current when it is
+// set. `set` runs at the first launch on each device, and again after it has failed (threads may run it twice, to the same
+// effect).
+class AttributesSet {
+  static constexpr int DEVICES = 64;
+  std::atomic<bool> done_[DEVICES] = {};
+
+ public:
+  template <typename F>
+  cudaError_t once(F &&set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < DEVICES;   // beyond them: every time
+    if (kept && done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess && kept) done_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
+
 // The registered per-tile timeline buffer of the GEMM kernels (null unless muon_debug_timeline set one).
 void debug_timeline(unsigned long long **buf, int *cap_per_cta);
 

@@ -299,7 +299,7 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[32], int &turn)
 constexpr int SM_SHARED = 227 * 1024;
 constexpr int STATIC_SHARED = 12 * 1024;   // more than any kernel's static share
 
-// Once for each kernel: it may take more than 48 KB, and the multiprocessor is to hold as many blocks of it as fit.
+// Once for each kernel and device: it may take more than 48 KB, and the multiprocessor is to hold as many blocks of it as fit.
 template <typename K>
 cudaError_t allow_shared(K kernel) {
   const cudaError_t e =

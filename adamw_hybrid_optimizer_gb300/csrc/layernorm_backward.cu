@@ -376,7 +376,8 @@ template <typename XT, typename YT, int C, int W, int R, int MODE>
 cudaError_t backward_launch(const BackwardArgs &a, cudaStream_t s) {
   using B = Backward<XT, YT, C, W, R, MODE>;
   auto kernel = layernorm_backward_kernel<XT, YT, C, W, R, MODE>;
-  static const cudaError_t allowed = allow_shared(kernel);
+  static AttributesSet set;
+  const cudaError_t allowed = set.once([&] { return allow_shared(kernel); });
   if (allowed != cudaSuccess) return allowed;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(a.parts)), dim3(B::THREADS), B::BYTES, s, a);
 }

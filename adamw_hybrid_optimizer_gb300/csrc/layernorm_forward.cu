@@ -191,7 +191,8 @@ template <typename XT, typename YT, int C, int W, int R, int MODE>
 cudaError_t forward_launch(const ForwardArgs &a, cudaStream_t s) {
   using F = Forward<XT, YT, C, W, R, MODE>;
   auto kernel = layernorm_forward_kernel<XT, YT, C, W, R, MODE>;
-  static const cudaError_t allowed = allow_shared(kernel);
+  static AttributesSet set;
+  const cudaError_t allowed = set.once([&] { return allow_shared(kernel); });
   if (allowed != cudaSuccess) return allowed;
   const long long resident = std::max<long long>(1, std::min<long long>(F::BLOCKS, SM_SHARED / (F::BYTES + 2048)));
   long long blocks = std::min((a.N + R - 1) / R, device_sm_count() * resident);
