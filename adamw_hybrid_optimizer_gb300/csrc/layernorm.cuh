@@ -320,6 +320,12 @@ inline muon_status check_dims(int64_t N, int64_t D) {
   return N > (1ll << 30) || D > (1ll << 20) ? MUON_ERR_SHAPE : MUON_OK;
 }
 
+// An output that takes the place of an input has its dtype and pitch (of a single row: its dtype), so that every value is
+// written where it was read.
+inline bool in_place_ok(const void *in, int idt, long long ldi, const void *out, int odt, long long ldo, long long N) {
+  return N == 0 || in != out || (idt == odt && (N == 1 || ldi == ldo));
+}
+
 // The mode for matrices whose bases are all 16-byte aligned (or not), the pitch of the first, and whether all pitches
 // are the same modulo 8.
 inline Mode mode_of(bool bases, bool pitches, long long ld, long long D) {

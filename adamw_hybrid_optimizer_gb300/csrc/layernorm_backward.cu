@@ -451,6 +451,8 @@ muon_status layernorm_backward(const void *dy, muon_dtype ydt, int64_t lddy, con
   if (st != MUON_OK) return st;
   if (lddy < D || ldx < D || (dx != nullptr && lddx < D)) return MUON_ERR_INVALID_ARG;
   if (!dtype_ok(xdt) || !dtype_ok(ydt) || !dtype_ok(wdt) || !dtype_ok(gdt)) return MUON_ERR_DTYPE;
+  if (dx != nullptr && (!in_place_ok(dy, ydt, lddy, dx, xdt, lddx, N) || !in_place_ok(x, xdt, ldx, dx, xdt, lddx, N)))
+    return MUON_ERR_INVALID_ARG;
   if (!natural(dy, ydt) || !natural(x, xdt) || !natural(weight, wdt) || !natural(mean, MUON_F32) ||
       !natural(rstd, MUON_F32) || !natural(dx, xdt) || !natural(dweight, gdt) || !natural(dbias, gdt))
     return MUON_ERR_ALIGNMENT;

@@ -254,6 +254,7 @@ muon_status layernorm_forward(const void *x, muon_dtype xdt, int64_t ldx, const 
   if (st != MUON_OK) return st;
   if (ldx < D || ldy < D || !std::isfinite(eps) || eps < 0.f) return MUON_ERR_INVALID_ARG;
   if (!dtype_ok(xdt) || !dtype_ok(ydt) || !dtype_ok(wdt)) return MUON_ERR_DTYPE;
+  if (!in_place_ok(x, xdt, ldx, y, ydt, ldy, N)) return MUON_ERR_INVALID_ARG;
   if (!natural(x, xdt) || !natural(y, ydt) || !natural(weight, wdt) || !natural(bias, wdt) ||
       !natural(mean, MUON_F32) || !natural(rstd, MUON_F32))
     return MUON_ERR_ALIGNMENT;

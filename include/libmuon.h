@@ -348,7 +348,7 @@ muon_status embedding_backward(const void *ids, muon_itype itype, const void *do
 /* Layer norm of N rows of D: y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps), var the mean of
  * (x - mean)^2.
  *   x       device N x D of xdt, pitch ldx.   y  device N x D of ydt, pitch ldy; may be x itself (same dtype and
- *           pitch).
+ *           pitch, MUON_ERR_INVALID_ARG otherwise), else must not overlap it.
  *   weight, bias  device, D of wdt each; either may be NULL (1 and 0).
  *   mean, rstd    device fp32, N each, kept for the backward pass; either may be NULL.
  * Limits: N <= 2^30, D <= 2^20 (MUON_ERR_SHAPE). */
@@ -362,7 +362,8 @@ size_t layernorm_workspace_bytes(int64_t N, int64_t D);
 /* Layer norm's gradients, from x and the mean and rstd of the forward pass: with xh = (x - mean) rstd and
  * g = dy weight, dx = rstd (g - mean(g) - xh mean(g xh)), dweight = sum over rows of dy xh, dbias = sum of dy.
  *   dy      device N x D of ydt, pitch lddy.   x as in the forward pass.   weight  NULL: 1.
- *   dx      device N x D of xdt, pitch lddx, or NULL; may be dy or x itself (same dtype and pitch).
+ *   dx      device N x D of xdt, pitch lddx, or NULL; may be dy or x itself (same dtype and pitch,
+ *           MUON_ERR_INVALID_ARG otherwise), else must not overlap them.
  *   dweight, dbias  device, D of gdt each; either may be NULL. Not all three outputs may be NULL.
  *   accumulate  0: dweight and dbias are written. Else: the sums are added to what they hold.
  *   ws      device workspace of ws_bytes >= layernorm_workspace_bytes(N, D), 256-byte aligned, no initialisation;
