@@ -427,6 +427,15 @@ def _vector(t, name: str, where: str, n: int, fp32: bool = False) -> Optional[in
     return t.data_ptr()
 
 
+def _workspace(ws, where: str) -> Tuple[Optional[int], int]:
+    """The address and bytes of an optional workspace: device memory without gaps, since the kernels write to it."""
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be a contiguous CUDA tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def embedding_forward(ids, table, out, scale: float = 1.0, stream=None):
     """out[i] = scale * table[ids[i]]; ids: int32 or int64 of any shape, table (V, D), out (ids.numel(), D)."""
     n, (V, D) = ids.numel(), table.shape
@@ -450,7 +459,7 @@ def embedding_backward(ids, dout, dtable, ws, scale: float = 1.0, padding_idx: i
     ldg = _matrix(dtable, "dtable", "embedding_backward")
     st = lib().embedding_backward(_vector(ids, "ids", "embedding_backward", n), _itype_code(ids), dout.data_ptr(),
                                   _dtype_code(dout), ldo, dtable.data_ptr(), _dtype_code(dtable), ldg, n, V, D, scale,
-                                  padding_idx, int(bool(accumulate)), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  padding_idx, int(bool(accumulate)), *_workspace(ws, "embedding_backward"),
                                   _current_stream(stream))
     _check(st, "embedding_backward")
 
@@ -498,8 +507,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, accumu
                                   dx.data_ptr() if dx is not None else None, lddx,
                                   _vector(dweight, "dweight", where, D), _vector(dbias, "dbias", where, D),
                                   _dtype_code(g) if g is not None else MUON_F32, int(bool(accumulate)), N, D,
-                                  ws.data_ptr() if ws is not None else None,
-                                  ws.numel() * ws.element_size() if ws is not None else 0, _current_stream(stream))
+                                  *_workspace(ws, where), _current_stream(stream))
     _check(st, where)
 
 

@@ -61,3 +61,76 @@ def test_layernorm_without_rows_has_nothing_in_place():
         pytest.skip("the calls would run")
     assert accepted(ln_fwd(x=None, y=None, ydt=BF, N=0))
     assert accepted(ln_fwd(y=A, ydt=BF, N=0))
+
+
+class OnDevice:
+    """As much of a CUDA tensor as the binding looks at."""
+
+    def __init__(self, *shape, dtype, is_cuda=True, contiguous=True, at=A):
+        self.shape, self.dtype, self.is_cuda, self._contiguous, self._at = shape, dtype, is_cuda, contiguous, at
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return (self.shape[1], 1)
+
+    def is_contiguous(self):
+        return self._contiguous
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return self._at
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Notes what would reach the library, and calls nothing."""
+    class Recorder:
+        def __init__(self):
+            self.made = []
+
+        def __getattr__(self, name):
+            if name.endswith("workspace_bytes"):
+                return getattr(real, name)
+            return lambda *args: self.made.append((name, args)) or L.MUON_OK
+
+    real, rec = L.lib(), Recorder()
+    monkeypatch.setattr(L, "lib", lambda: rec)
+    return rec.made
+
+
+def backward_calls(ws, n=40, V=30):
+    import torch
+    f, i = torch.float32, torch.int64
+    t = lambda *shape: OnDevice(*shape, dtype=f)  # noqa: E731
+    return {"embedding_backward": lambda: L.embedding_backward(OnDevice(n, dtype=i), t(n, D), t(V, D), ws, stream=0),
+            "layernorm_backward": lambda: L.layernorm_backward(t(n, D), t(n, D), t(D), t(n), t(n), t(n, D), t(D), t(D), ws,
+                                                               stream=0)}
+
+
+@pytest.mark.parametrize("name", ["embedding_backward", "layernorm_backward"])
+def test_workspace_is_device_memory_without_gaps(calls, name):
+    """The kernels write to it: an address of the host is not theirs, and an expanded tensor has fewer bytes than elements."""
+    import torch
+    u8 = torch.uint8
+    for ws in (OnDevice(1 << 20, dtype=u8, is_cuda=False), OnDevice(1 << 20, dtype=u8, contiguous=False)):
+        with pytest.raises(ValueError):
+            backward_calls(ws)[name]()
+    assert calls == []
+    backward_calls(OnDevice(1 << 20, dtype=u8, at=C))[name]()
+    backward_calls(OnDevice(1 << 18, dtype=torch.float32, at=C))[name]()
+    for made, args in calls:
+        assert made == name and (C, 1 << 20) in zip(args, args[1:])
+    assert len(calls) == 2
+    del calls[:]
+    backward_calls(None)[name]()      # the call itself says whether it needs one
+    assert (None, 0) in zip(calls[0][1], calls[0][1][1:])
