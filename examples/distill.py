@@ -25,6 +25,12 @@ from adamw_hybrid_optimizer_gb300 import HybridMuonAdamW, libmuon as L  # noqa: 
 EPS = 1e-5
 
 
+def first_derivative_only(name):
+    """For backward: under create_graph gradients are recorded, and the kernels' would pass for constants."""
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{name} has no second derivative")
+
+
 class Embedding(torch.autograd.Function):
     """scale * table[ids]; the gradient is summed by sorted tokens, the same bits for the same inputs."""
 
@@ -38,6 +44,7 @@ class Embedding(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
+        first_derivative_only("Embedding")
         ids, table = ctx.saved_tensors
         grad = torch.empty_like(table)
         ws = torch.empty(L.embedding_workspace_bytes(ids.numel(), *table.shape), dtype=torch.uint8, device=table.device)
@@ -57,6 +64,7 @@ class LayerNorm(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        first_derivative_only("LayerNorm")
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = torch.empty_like(x), torch.empty_like(weight), torch.empty_like(weight)
         ws = torch.empty(L.layernorm_workspace_bytes(*x.shape), dtype=torch.uint8, device=x.device)
@@ -79,6 +87,7 @@ class DistillLoss(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, upstream):
+        first_derivative_only("DistillLoss")
         dlogits, ctx.dlogits = ctx.dlogits, None
         return dlogits.mul_(upstream), None, None, None, None
 
