@@ -74,14 +74,18 @@ class LayerNorm(torch.autograd.Function):
 
 class DistillLoss(torch.autograd.Function):
     """Mean over the rows of weights * T^2 KL(teacher || student). The logits' memory becomes their gradient's, so
-    they must be used for nothing else."""
+    they must be used for nothing else: a leaf is refused, and what another operation has kept of them for its own gradient
+    is an error there."""
 
     @staticmethod
     def forward(ctx, logits, t_idx, t_val, temperature, weights):
+        if logits.is_leaf and logits.requires_grad:
+            raise RuntimeError("DistillLoss overwrites its logits, which are a leaf that requires a gradient")
         n = logits.shape[0]
         losses = torch.empty(n, dtype=torch.float32, device=logits.device)
         stats = torch.empty((n, 2), dtype=torch.float32, device=logits.device)
         L.distill_forward_backward(logits, t_idx, t_val, temperature, weights, 1.0 / n, losses, stats, logits)
+        torch.autograd.graph.increment_version(logits)   # autograd does not see what a kernel writes
         ctx.dlogits = logits.detach()
         return losses.sum() / n
 

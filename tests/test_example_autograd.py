@@ -94,3 +94,24 @@ def test_distill_gradient_is_that_of_the_plain_loss():
     q, lp = torch.softmax(t / T, 1), torch.log_softmax(z2 / T, 1).gather(1, idx)
     want, = torch.autograd.grad(3.0 * (weights * T * T * (q * (q.log() - lp)).sum(1)).mean(), z2)
     assert torch.allclose(got, want, rtol=1e-4, atol=1e-6)
+
+
+def test_logits_kept_for_another_gradient_are_an_error():
+    """The logits' memory holds their gradient after the loss: what another operation had kept of them is gone."""
+    idx, t, weights = teacher()
+    z = rand(N, V, seed=6).requires_grad_()
+    logits = z * 1.0
+    other = logits.square().sum()           # keeps the logits for its own gradient
+    ex.DistillLoss.apply(logits, idx, t, T, weights)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        other.backward()
+
+
+def test_logits_that_are_a_leaf_are_refused():
+    """A leaf's values would be its own gradient from then on."""
+    idx, t, weights = teacher()
+    z = rand(N, V, seed=6).requires_grad_()
+    before = z.detach().clone()
+    with pytest.raises(RuntimeError):
+        ex.DistillLoss.apply(z, idx, t, T, weights)
+    assert torch.equal(z.detach(), before)
