@@ -1,7 +1,7 @@
 // Embedding lookup with scaling, and the table's gradient by sorted tokens.
 //
 //   out_i = scale * E[id_i]                         (an id outside [0, V) names no row: zeros)
-//   dE_v  = scale * sum_{i : id_i = v} dout_i       (in increasing i, fp32, rounded once at the end)
+//   dE_v  = scale * sum_{i : id_i = v} dout_i       (fp32 in a fixed order, rounded once at the end)
 //
 // The gradient sorts the ids with their positions (a stable radix sort, so that equal ids keep the order of
 // their positions), and then sums each run of equal ids. No sum goes through an atomic: the same inputs give
@@ -17,7 +17,8 @@
 //   radix_*_kernel            one pass of a longer sort: digit counts per tile, their scan, the stable scatter.
 //   embedding_sum_kernel      one warp per 16 or 32 sorted positions and 256 columns; the rows to come are in flight
 //                             whether or not they belong to the id being summed, since most ids occur once or twice.
-//   embedding_join_kernel     ids whose run spans a whole group or more: adds the groups' sums in order.
+//   embedding_join_kernel     ids whose run covers the group after its first and goes on: adds the groups' sums, eighths of
+//                             them at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -815,7 +816,7 @@ __global__ void __launch_bounds__(WARPS * 32, SUM_BLOCKS) embedding_sum_kernel(c
 }
 
 // One block per long run and 256 columns: warp w adds parts w, w + 8, ... of the run, and the warps' sums are added
-// in order. Bound by latency: 9 us for the 7 MB of 32768 ids.
+// from warp 0 on. Bound by latency: 9 us for the 7 MB of 32768 ids.
 template <typename OT, typename GT, int ACCESS>
 __global__ void __launch_bounds__(THREADS) embedding_join_kernel(const SumArgs a) {
   pdl_wait();

@@ -334,8 +334,12 @@ muon_status embedding_forward(const void *ids, muon_itype itype, const void *tab
  * partial sums of ids that occur often. 0 for n < 0, V < 1 or D < 1. */
 size_t embedding_workspace_bytes(int64_t n, int64_t V, int64_t D);
 
-/* The table's gradient: dtable_v = scale * sum over i with ids[i] = v of dout_i, added in increasing i. Ids outside
- * [0, V) and ids equal to padding_idx (-1: none) contribute nothing.
+/* The table's gradient: dtable_v = scale * sum over i with ids[i] = v of dout_i. Ids outside [0, V) and
+ * ids equal to padding_idx (-1: none) contribute nothing. The sums are fp32, in an order that the ids, n and D alone give:
+ * with the positions sorted by id (equal ids by position, those that contribute nothing last) and cut into groups of
+ * 16 (where ceil(n / 16) * ceil(D / 256) <= 3648) or 32, an id is added in increasing i unless it covers the whole of the
+ * group after the one where it starts and goes on; then its part of each group is added in increasing i, those of its
+ * groups w, w + 8, w + 16, ... (counted from its first) for each w < 8, and these eight sums from w = 0 on.
  *   dout    device n x D of odt, pitch ldo.   dtable  device V x D of gdt, pitch ldg.
  *   accumulate  0: every row of dtable is written (zeros where no id names it). Else: the sums are added to what
  *               dtable holds, and rows that no id names are not touched.
