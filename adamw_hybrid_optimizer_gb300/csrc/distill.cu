@@ -9,8 +9,8 @@
 // A row of weight 0, or without a valid entry, has loss 0 and gradient 0, and its logits are not used. m and l are
 // kept apart (stats), so that p = exp((z - m) / T - l) keeps its precision for logits of any size. All three forms
 // are bound by bandwidth: forward reads the logits once, with a running maximum and sum; backward reads them once
-// and writes the gradient; the joint form reads a row twice, the second time from L2, and there are no more rows on
-// their way at once than L2 holds.
+// and writes the gradient; the joint form reads a row twice, the second time from L2 as far as the rows on their way at
+// once and their gradients fit it.
 //
 // A row is cut into granules of eight logits (four where a matrix is fp32) on boundaries of memory: a row whose start
 // is not on one (an odd vocabulary) has a short granule at each end, and everything between is whole vectors.
@@ -47,7 +47,10 @@ struct DistillArgs {
   float inv_t, temp, grad_scale;
 };
 
-// exp(x * c), c = log2(e) / T; the difference x is taken in the logits' own unit, where it is exact or nearly so
+// exp(x * c), c = log2(e) / T; the difference x is taken in the logits' own unit, where it is exact or nearly so. The
+// product is rounded before the exponential, which is good to two units in the last place: a relative error of 2^-22, and
+// of |x / T| 2^-23 beside it (3e-6 at a weight of exp(-25)). Results below 2^-126 are 0, as weights too small to be seen
+// beside the largest, 1.
 __device__ __forceinline__ float exp_scaled(float x, float c) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * c));
@@ -715,8 +718,10 @@ int row_slices(const DistillArgs &a, int TH) {
 int row_threads(int V) { return V < 4096 ? 32 : V < 16384 ? 128 : 256; }
 
 // The joint form's second reading wants a row still in L2 (129 MB, and its gradient goes there too): wider blocks, and
-// so fewer rows at once, for rows of more than 131072 and 262144 bytes. (4096 x 128256 bf16: 464, 426 and 453 us with
-// 256, 512 and 1024 threads; 2048 x 128256 fp32: 494, 460 and 425 us.)
+// so fewer rows at once (608, 304 and 152), for rows of more than 131072 and 270000 bytes of logits. The limits lie
+// between the lengths that were measured, 100608, 256512 and 513024 bytes, with a gradient of the logits' type; longer rows
+// than those are more than L2 holds. (4096 x 128256 bf16: 464, 426 and 453 us with 256, 512 and 1024 threads;
+// 2048 x 128256 fp32: 494, 460 and 425 us.)
 int joint_threads(int V, size_t row_bytes) {
   return row_bytes <= 131072 ? row_threads(V) : row_bytes <= 270000 ? 512 : 1024;
 }

@@ -152,8 +152,9 @@ struct LookupUnit {
 // Rows that start on a granule and have whole ones: warps take units of 128 granules in turn, four per lane, which follow
 // each other through the rows (of any length, so that no lane is idle: 65536 rows of 768 bf16 take 24 us, and 29 us with
 // units of whole rows). All loads of a unit are in flight before the first is used, and the ids of the next unit are loaded
-// under them, so that a unit waits for one latency, not two. Bound by memory: rows that occur once come from there and all
-// go there (65536 of 4096 bf16 out of 128256: 139 us, 1074 MB through L2 at 7.7 TB/s, 701 MB of them from or to memory).
+// under them, so that a unit waits for one latency, not two. No one unit is at its limit (32768 of 4096 bf16 out of 50304:
+// memory at 61% of its peak, L2 at 42%, instructions issued in 58% of the cycles): the time is the loads' latency with half
+// of the warps that a multiprocessor can hold. 65536 of 4096 bf16 out of 128256: 139 us for 701 MB, distinct rows counted once, 5.0 TB/s.
 template <typename TT, typename OT>
 __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(const LookupArgs a) {
   pdl_wait();
@@ -193,8 +194,9 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(
 // Other rows: a row's granules are those of the table around the output's, one more than are written; each is copied to
 // the warp's ring in shared memory, and an output granule is cut out of two. A unit's last granule is only copied: it is
 // the next unit's first. The granules of the next units are on their way, and the ids of the one after on theirs, while a
-// unit is stored. (65536 rows of 771 bf16: 41 us, and 76 us with two loads per lane and granule into registers; but
-// where rows are aligned the ring takes 194 us for 65536 rows of 4096, and registers 138 us.)
+// unit is stored. Bound by instructions, those that cut a granule out of two first (32768 of 1001 bf16: issued in 64% of the
+// cycles, memory at 12% of its peak). (65536 rows of 771 bf16: 41 us, and 76 us with two loads per lane and granule into
+// registers; but where rows are aligned the ring takes 194 us for 65536 rows of 4096, and registers 138 us.)
 template <typename TT, typename OT>
 __global__ void __launch_bounds__(THREADS, CUT_BLOCKS) embedding_forward_cut_kernel(const LookupArgs a) {
   pdl_wait();
@@ -733,7 +735,8 @@ __device__ __forceinline__ unsigned run_groups(const SumArgs &a, long long c, un
 // one id. The loop is short on purpose: with a store for the end of a run unrolled into every place of a batch in
 // registers, the code did not fit the instruction cache (131072 rows of 64: 45 us, and 27 us now). Bound by memory,
 // dout read once and the rows that ids name written once, behind the sort and the zeroes: 32768 x 4096 bf16 in 64 us,
-// 330 MB at 5.2 TB/s; the whole gradient of 128256 rows in 212 us, 6.2 TB/s. Few tokens: by the latency of the
+// 330 MB at 5.1 TB/s (memory at 64% of its peak, instructions issued in 65% of the cycles); the whole gradient of 128256
+// rows in 212 us, 6.2 TB/s. Few tokens: by the latency of the
 // positions of one warp, some 90 instructions each.
 template <typename OT, typename GT, int ACCESS, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, SUM_BLOCKS) embedding_sum_kernel(const SumArgs a) {

@@ -361,13 +361,17 @@ Shape shape_of(long long D, Mode mode) {
   return {2, 32, 1};
 }
 
-// Blocks of the backward pass, each of which leaves one partial row of dw and db: as many as the GPU holds at once,
-// so that there are few partial rows to add. In SHIFTED a block's rows lie multiples of eight apart.
+// Blocks of the backward pass, each of which leaves one partial row of dw and db: as many as the registers of SMS
+// multiprocessors hold at once, so that there are few partial rows to add. The count goes by the shape alone, since the
+// workspace is sized by it; where that many rings do not fit the shared memory (fp32: one of two blocks fits at 513 to
+// 768 columns and at 1025 to 1536 of whole granules, three of four up to 2048) the others are a second wave. In SHIFTED a
+// block's rows lie multiples of eight apart.
+constexpr long long SMS = 152;
 long long parts_for(long long N, long long D, Mode mode) {
   if (D > MAX_ROW) return std::max(1LL, std::min(N, 64LL));
   const Shape h = shape_of(D, mode);
   const long long resident = std::max(1, resident_threads(h.C, mode) / (h.W * h.R * 32));
-  const long long blocks = std::max(1LL, std::min((N + h.R - 1) / h.R, 152 * resident));
+  const long long blocks = std::max(1LL, std::min((N + h.R - 1) / h.R, SMS * resident));
   return mode == SHIFTED ? (blocks + 7) / 8 * 8 : blocks;
 }
 long long part_pitch(long long D) { return (D + 7) / 8 * 8; }

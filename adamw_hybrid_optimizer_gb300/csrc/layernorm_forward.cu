@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(W *R * 32, (Forward<XT, YT, C, W, R, MODE>::BL
       const float d = r.x - mean;
       sq = lanes_sum<Exchange<W, R>::LANES>(fmaf(n_lane * d, d, r.y));
     }
-    const float rstd = rsqrtf(sq * inv + a.eps);
+    const float rstd = rsqrtf(sq * inv + a.eps);   // within 2 units in the last place
     if (live) {
       if (t == 0) {
         if (a.mean != nullptr) a.mean[row] = mean;
