@@ -154,7 +154,8 @@ struct LookupUnit {
 // units of whole rows). All loads of a unit are in flight before the first is used, and the ids of the next unit are loaded
 // under them, so that a unit waits for one latency, not two. No one unit is at its limit (32768 of 4096 bf16 out of 50304:
 // memory at 61% of its peak, L2 at 42%, instructions issued in 58% of the cycles): the time is the loads' latency with half
-// of the warps that a multiprocessor can hold. 65536 of 4096 bf16 out of 128256: 139 us for 701 MB, distinct rows counted once, 5.0 TB/s.
+// of the warps that a multiprocessor can hold. 65536 of 4096 bf16 out of 128256: 139 us for 701 MB (distinct rows counted
+// once), 5.0 TB/s.
 template <typename TT, typename OT>
 __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) embedding_forward_kernel(const LookupArgs a) {
   pdl_wait();
