@@ -42,7 +42,15 @@ enum KernelKind : int32_t {
   KK_DISTILL_FWD = 20,
   KK_DISTILL_BWD = 21,
   KK_DISTILL_STEP = 22,
-  KK_COUNT = 23
+  KK_ADAMW8 = 23,
+  KK_CE_LOGITS = 24,
+  KK_CE_COMBINE = 25,
+  KK_CE_DLOGITS = 26,
+  KK_CE_DH = 27,
+  KK_CE_DW = 28,
+  KK_CE_REDUCE = 29,
+  KK_CE_ROWS = 30,
+  KK_COUNT = 31
 };
 
 // Launch bookkeeping (libmuon.cu): counts launches and, while tracing, records an event pair.
@@ -444,6 +452,8 @@ struct AdamwConst {
   float inv_sqrt_bc2;   // 1 / sqrt(1 - beta2^t)
   float eps;
 };
+// Checks AdamW hyperparameters and derives the kernels' constants (libmuon.cu).
+muon_status adamw_constants(const adamw_hparams *hp, AdamwConst *out);
 muon_status launch_adamw(void *p, int pdt, const void *g, int gdt, float *m, float *v, long long n,
                          const AdamwConst &c, cudaStream_t s);
 muon_status launch_adamw_master(float *master, __nv_bfloat16 *p, const void *g, int gdt, float *m, float *v,

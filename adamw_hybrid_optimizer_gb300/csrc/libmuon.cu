@@ -114,6 +114,29 @@ void launch_end(cudaStream_t s) {
   g_pending_kind = -1;
 }
 
+// Validates AdamW hyperparameters and derives the kernel constants.
+muon_status adamw_constants(const adamw_hparams *hp, AdamwConst *out) {
+  if (hp->step < 1 || !std::isfinite(hp->lr) || !std::isfinite(hp->beta1) || !std::isfinite(hp->beta2) ||
+      !std::isfinite(hp->eps) || !std::isfinite(hp->weight_decay) || hp->beta1 < 0.f || hp->beta1 >= 1.f ||
+      hp->beta2 < 0.f || hp->beta2 >= 1.f || (hp->l2 != 0 && hp->l2 != 1))
+    return MUON_ERR_INVALID_ARG;
+  const double t = static_cast<double>(hp->step);
+  const double bc1 = 1.0 - std::pow(static_cast<double>(hp->beta1), t);
+  const double bc2 = 1.0 - std::pow(static_cast<double>(hp->beta2), t);
+  AdamwConst &c = *out;
+  c.l2 = hp->l2;
+  c.l2_wd = hp->l2 ? hp->weight_decay : 0.f;
+  c.decay = hp->l2 ? 1.f : static_cast<float>(1.0 - static_cast<double>(hp->lr) * hp->weight_decay);
+  c.beta1 = hp->beta1;
+  c.one_minus_beta1 = static_cast<float>(1.0 - hp->beta1);
+  c.beta2 = hp->beta2;
+  c.one_minus_beta2 = static_cast<float>(1.0 - hp->beta2);
+  c.step_size = static_cast<float>(hp->lr / bc1);
+  c.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
+  c.eps = hp->eps;
+  return MUON_OK;
+}
+
 muon_status device_check() { return check_device(); }
 
 // ------------------------------------------------------------------------------------------ autotune table
@@ -847,29 +870,6 @@ muon_status ns_orthogonalize(const void *x, muon_dtype xdt, void *out, muon_dtyp
   return MUON_OK;
 }
 
-// Validates AdamW hyperparameters and derives the kernel constants.
-static muon_status adamw_constants(const adamw_hparams *hp, AdamwConst *out) {
-  if (hp->step < 1 || !std::isfinite(hp->lr) || !std::isfinite(hp->beta1) || !std::isfinite(hp->beta2) ||
-      !std::isfinite(hp->eps) || !std::isfinite(hp->weight_decay) || hp->beta1 < 0.f || hp->beta1 >= 1.f ||
-      hp->beta2 < 0.f || hp->beta2 >= 1.f || (hp->l2 != 0 && hp->l2 != 1))
-    return MUON_ERR_INVALID_ARG;
-  const double t = static_cast<double>(hp->step);
-  const double bc1 = 1.0 - std::pow(static_cast<double>(hp->beta1), t);
-  const double bc2 = 1.0 - std::pow(static_cast<double>(hp->beta2), t);
-  AdamwConst &c = *out;
-  c.l2 = hp->l2;
-  c.l2_wd = hp->l2 ? hp->weight_decay : 0.f;
-  c.decay = hp->l2 ? 1.f : static_cast<float>(1.0 - static_cast<double>(hp->lr) * hp->weight_decay);
-  c.beta1 = hp->beta1;
-  c.one_minus_beta1 = static_cast<float>(1.0 - hp->beta1);
-  c.beta2 = hp->beta2;
-  c.one_minus_beta2 = static_cast<float>(1.0 - hp->beta2);
-  c.step_size = static_cast<float>(hp->lr / bc1);
-  c.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
-  c.eps = hp->eps;
-  return MUON_OK;
-}
-
 muon_status adamw_step(void *param, muon_dtype pdt, const void *grad, muon_dtype gdt, float *exp_avg,
                        float *exp_avg_sq, int64_t n, const adamw_hparams *hp, muon_stream_t stream) {
   if (param == nullptr || grad == nullptr || exp_avg == nullptr || exp_avg_sq == nullptr || hp == nullptr)
@@ -1492,6 +1492,14 @@ const char *muon_kernel_name(int32_t kind) {
     case KK_DISTILL_FWD: return "distill_forward";
     case KK_DISTILL_BWD: return "distill_backward";
     case KK_DISTILL_STEP: return "distill_forward_backward";
+    case KK_ADAMW8: return "adamw8";
+    case KK_CE_LOGITS: return "linear_cross_entropy_logits";
+    case KK_CE_COMBINE: return "linear_cross_entropy_combine";
+    case KK_CE_DLOGITS: return "linear_cross_entropy_dlogits";
+    case KK_CE_DH: return "linear_cross_entropy_dh";
+    case KK_CE_DW: return "linear_cross_entropy_dw";
+    case KK_CE_REDUCE: return "linear_cross_entropy_reduce";
+    case KK_CE_ROWS: return "linear_cross_entropy_rows";
     default: return "unknown";
   }
 }

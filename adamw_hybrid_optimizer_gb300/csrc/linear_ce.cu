@@ -1,0 +1,987 @@
+// The cross entropy of a linear head, z = h W^T, without keeping the N x V logits, and its gradients.
+//
+//     lse_i = log sum_v exp z_iv,   loss_i = w_i (lse_i - z_it),   dz_iv = g_i w_i (exp(z_iv - lse_i) - [v = t_i])
+//     dh = dz W,   dW = dz^T h
+//
+// Rows go through in pieces of at most PIECE_ELEMS / V (plan()); nothing of size N x V outlives a piece. Per piece:
+//   logits  z a tile of 256 x 256 at a time on the tensor cores; a tile's accumulators leave as one running maximum and sum
+//           of exponentials for each row and half tile (online softmax) and the target's logit
+//   combine the halves' pairs into lse and the loss
+//   rows    h without the rows that have no part in the loss, for dw
+//   dlogits the product again, dz = g w (exp(z - lse) - [v = t]) from the accumulators, rounded to bf16 as an operand of the
+//           two products that follow (for fp32 gradients: as the sum of two bf16 terms, which holds 16 bits of it)
+//   dh      dz W, the contraction over V cut into slices where the tiles alone would leave SMs without work
+//   dw      dz^T h, added up over the pieces in fp32
+//   reduce  adds slices in their order and rounds once
+//
+// One kernel computes all the products (ce_gemm_kernel), a persistent one of CTA pairs as the Newton-Schulz GEMMs of
+// ns_gemm.cu are: tcgen05 cta_group::2 MMAs of 256 x 256 x 16 from operands that TMA brings in 64-deep stages, two
+// accumulators in tensor memory so that one tile's epilogue runs under the next one's MMAs. Bound by the tensor cores
+// wherever there are a few hundred rows, by the reading of W below that.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "tensor_map.h"
+#include "vec.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int BM = 128;                      // accumulator rows per CTA: 256 per pair
+constexpr int BN = 256;
+constexpr int BK = 64;
+constexpr int STAGES = 6;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int B_BYTES = (BN / 2) * BK * 2;   // this CTA's half of B
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int EPI_WARPS = 8;
+constexpr int GEMM_THREADS = 32 * (2 + EPI_WARPS);
+constexpr int BUF_BYTES = 32 * 128;          // an epilogue warp's staging: 32 rows of 128 bytes
+constexpr int GROUP = 16;                    // row tiles that take a column of tiles together
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr long long PIECE_ELEMS = 1ll << 30; // dz elements of a piece
+constexpr long long PAIRS = 76;              // SM pairs of a GB300: slices are counted by it, so that sums have one order
+constexpr int MAX_SPLIT = 64;
+
+enum Kind : int { LOGITS = 0, DLOGITS = 1, DH = 2, DW = 3 };
+
+struct Ctrl {
+  uint64_t full[STAGES], empty[STAGES];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + EPI_WARPS * BUF_BYTES + sizeof(Ctrl) + 1024;
+static_assert(SMEM <= 232448, "shared memory over budget");
+
+struct CeArgs {
+  CUtensorMap map_a, map_b, map_out;   // map_out: dz, for DLOGITS
+  int rows, cols;                      // of the output
+  int m_pairs, n_tiles;
+  int k_iters, k_wrap;                 // 64-deep steps; from k_wrap on A's second plane and B again (two terms of dz)
+  int split, k_per;
+  int planes;                          // DLOGITS: terms of dz
+  long long total;                     // tile pairs times slices
+  // LOGITS, DLOGITS
+  const void *targets;
+  int itype;
+  const float *weights, *grad, *lse;
+  float grad_scale;
+  float2 *partials;                    // [cols / 128, rounded up][rows]: maximum and sum of exponentials
+  float *z_target;                     // [rows]
+  // DH, DW
+  void *out;
+  long long ld_out, slice_stride;      // elements; slice s goes to out + s * slice_stride
+  int out_f32, accumulate, vec;
+  uint32_t *err;
+  unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ long long target_of(const void *t, int itype, long long i) {
+  return itype == MUON_I32 ? static_cast<long long>(static_cast<const int *>(t)[i]) : static_cast<const long long *>(t)[i];
+}
+
+// Unit u: slice, then groups of GROUP row-tile pairs, in a group column after column of tiles. A wave of 76 pairs then
+// reads GROUP row tiles and five column tiles, which L2 holds, whatever the matrix' size.
+__device__ __forceinline__ void decode(const CeArgs &a, long long u, int &slice, int &ti, int &tj) {
+  const int tiles = a.m_pairs * a.n_tiles;
+  slice = static_cast<int>(u / tiles);
+  int r = static_cast<int>(u - static_cast<long long>(slice) * tiles);
+  const int per_group = GROUP * a.n_tiles;
+  const int g = r / per_group;
+  r -= g * per_group;
+  const int in_group = min(GROUP, a.m_pairs - g * GROUP);
+  tj = r / in_group;
+  ti = g * GROUP + (r - tj * in_group);
+}
+
+// The warp's staging buffer: line i holds 128 bytes of output row i, its 16-byte piece q at q ^ (i & 7), the order in
+// which TMA reads a box of 128-byte rows with the 128-byte swizzle; rows and columns of pieces are free of bank conflicts.
+__device__ __forceinline__ uint4 *piece(uint8_t *buf, int i, int q) {
+  return reinterpret_cast<uint4 *>(buf + i * 128 + ((q ^ (i & 7)) << 4));
+}
+
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const unsigned *>(&h);
+}
+
+// One tile's part of a warp (128 columns from col0) as a running maximum and sum of exponentials per row.
+__device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, int row, int col0, int part) {
+  long long t = -1;
+  if (row < a.rows) t = target_of(a.targets, a.itype, row);
+  float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int c0 = col0 + 32 * c;
+    if (c0 >= a.cols) break;
+    float v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(tmem + 32 * c, v);
+    const long long hit = t - c0;
+    if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) z = hit == j ? v[j] : z;
+      if (hit >= 0 && hit < 32 && c0 + hit < a.cols) a.z_target[row] = z;
+    }
+    if (c0 + 32 > a.cols) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = c0 + j < a.cols ? v[j] : -INFINITY;
+    }
+    float top[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top[j] = fmaxf(v[j], v[j + 4]);
+#pragma unroll
+    for (int j = 8; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+    const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+    const float ref = mn == -INFINITY ? 0.f : mn * LOG2E;   // nothing above -inf so far: exponentials of zero
+    float sum[4] = {s * exp2_fast(fmaf(m, LOG2E, -ref)), 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_fast(fmaf(v[j], LOG2E, -ref));
+    s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    m = mn;
+  }
+  if (row < a.rows && col0 < a.cols) a.partials[static_cast<long long>(part) * a.rows + row] = make_float2(m, s);
+}
+
+// One tile's part of a warp as dz, in bf16 terms, through the staging buffer and TMA (which leaves out what lies past the
+// rows or columns).
+__device__ __forceinline__ void epilogue_dlogits(const CeArgs &a, uint32_t tmem, int row, int warp_row0, int col0, int lane,
+                                                 uint8_t *buf) {
+  long long t = -1;
+  float scale = 0.f, base = 0.f;
+  bool live = false;
+  if (row < a.rows) {
+    t = target_of(a.targets, a.itype, row);
+    const float w = a.weights != nullptr ? a.weights[row] : 1.f;
+    live = t >= 0 && t < a.cols && w != 0.f;
+    scale = w * (a.grad != nullptr ? a.grad[row] : a.grad_scale);
+    base = -a.lse[row] * LOG2E;
+  }
+  if (warp_row0 >= a.rows) return;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int c0 = col0 + 64 * c;
+    if (c0 >= a.cols) break;
+#pragma unroll 1
+    for (int plane = 0; plane < a.planes; ++plane) {
+      if (lane == 0) bulk_wait_group_read<0>();   // the buffer's last store has read it
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(tmem + 64 * c + 32 * h, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = live ? scale * exp2_fast(fmaf(v[j], LOG2E, base)) : 0.f;
+        const long long hit = t - (c0 + 32 * h);
+        if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = live && hit == j ? v[j] - scale : v[j];
+        }
+        if (plane > 0) {   // what the first term leaves
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *piece(buf, lane, 4 * h + q) = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                                                    pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&a.map_out, buf, c0, warp_row0, plane);
+        bulk_commit_group();
+      }
+    }
+  }
+}
+
+// E elements of one output row from their fp32 values (stored as T), 16 bytes or singly.
+template <typename T, int E>
+__device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec, bool accumulate) {
+  if (vec && left >= E) {
+    Raw<T, E> r;
+    if (accumulate) {
+      r.load(dst);
+      const Vals<E> old = r.get();
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) f[2 * e] += old.p[e].x, f[2 * e + 1] += old.p[e].y;
+    }
+    Vals<E> o;
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) o.p[e] = make_float2(f[2 * e], f[2 * e + 1]);
+    store_vals(dst, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < left) store1(dst, e, accumulate ? load1(dst, e) + f[e] : f[e]);
+  }
+}
+
+// One tile's part of a warp as rows of the output: 32 rows of 32 fp32 values at a time through the staging buffer, so that
+// eight lanes write 128 bytes of a row (64 as bf16).
+__device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
+                                             uint8_t *buf) {
+  if (warp_row0 >= a.rows) return;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int c0 = col0 + 32 * c;
+    if (c0 >= a.cols) break;
+    {
+      float v[32];
+      __syncwarp();   // the buffer's last rows have been read
+      tmem_ld_32x32b_x32(tmem + 32 * c, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *piece(buf, lane, q) = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                          __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+    }
+    __syncwarp();
+    const int left0 = a.cols - c0;
+    if (a.out_f32) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = 4 * k + (lane >> 3), q = lane & 7;
+        const uint4 w = *piece(buf, i, q);
+        float f[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+        if (warp_row0 + i < a.rows)
+          store_piece<float, 4>(static_cast<float *>(a.out) + slice * a.slice_stride +
+                                    static_cast<long long>(warp_row0 + i) * a.ld_out + c0 + 4 * q,
+                                f, left0 - 4 * q, a.vec, a.accumulate);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = 8 * k + (lane >> 2), q = lane & 3;
+        const uint4 w = *piece(buf, i, 2 * q), x = *piece(buf, i, 2 * q + 1);
+        float f[8] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w),
+                      __uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+        if (warp_row0 + i < a.rows)
+          store_piece<__nv_bfloat16, 8>(static_cast<__nv_bfloat16 *>(a.out) +
+                                            static_cast<long long>(warp_row0 + i) * a.ld_out + c0 + 8 * q,
+                                        f, left0 - 8 * q, a.vec, a.accumulate);
+      }
+    }
+  }
+}
+
+// A: LOGITS, DLOGITS h (K-major), DH dz (K-major), DW dz (MN-major: dz^T). B: LOGITS, DLOGITS W (K-major), DH W and DW h
+// (MN-major). An MN-major operand is loaded as boxes of 64 columns x 64 steps.
+template <int KIND>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeArgs args) {
+  constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *staging = smem + STAGES * STAGE_BYTES;
+  Ctrl *ctrl = reinterpret_cast<Ctrl *>(staging + EPI_WARPS * BUF_BYTES);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctrl->acc_full[s], 1);
+      mbar_init(&ctrl->acc_empty[s], 2 * EPI_WARPS);   // both CTAs' epilogue warps, on the even CTA's copy
+    }
+    mbar_init(&ctrl->drain, 1);
+    ctrl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane < 2) tma_prefetch_desc(lane ? &args.map_b : &args.map_a);
+  if (warp == 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();   // both CTAs' barriers are initialised before either signals the other
+  tc_fence_after();
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  WaitCtl ctl{&ctrl->abort_flag, args.err, args.timeout_ns};
+  const int rank = static_cast<int>(cluster_ctarank());
+  const long long first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t leader_full0 = mapa_shared(smem_u32(&ctrl->full[0]), 0);
+      uint32_t stage = 0, phase = 0;
+      int last_parity[STAGES];
+      for (int s = 0; s < STAGES; ++s) last_parity[s] = -1;
+      bool ok = true;
+      for (long long u = first; ok && u < args.total; u += stride) {
+        int slice, ti, tj;
+        decode(args, u, slice, ti, tj);
+        const int row0 = (2 * ti + rank) * BM, col0 = tj * BN + (BN / 2) * rank;
+        const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
+        for (int kk = k0; kk < k1; ++kk) {
+          if (!wait_bounded(&ctrl->empty[stage], phase ^ 1u, ctl, ERR_WAIT_EMPTY)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) {   // both CTAs' copies complete on the even CTA's barrier
+            mbar_arrive_expect_tx(&ctrl->full[stage], 2 * STAGE_BYTES);
+            last_parity[stage] = static_cast<int>(phase);
+          }
+          const uint32_t fb = leader_full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
+          uint8_t *sa = smem + stage * STAGE_BYTES, *sb = sa + A_BYTES;
+          const int plane = kk >= args.k_wrap ? 1 : 0;
+          const int k = (kk - (plane ? args.k_wrap : 0)) * BK;
+          if constexpr (A_MN) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tma_load_3d_pair(sa + q * (64 * BK * 2), &args.map_a, fb, row0 + 64 * q, k, plane);
+          } else {
+            tma_load_3d_pair(sa, &args.map_a, fb, k, row0, plane);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tma_load_3d_pair(sb + q * (64 * BK * 2), &args.map_b, fb, col0 + 64 * q, k, 0);
+          } else {
+            tma_load_3d_pair(sb, &args.map_b, fb, k, col0, 0);
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every armed stage's copies have landed before the CTA may exit
+      for (int s = 0; s < STAGES; ++s)
+        if (last_parity[s] >= 0) drain_wait(&ctrl->full[s], static_cast<uint32_t>(last_parity[s]), ctl);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, BN, A_MN, B_MN);
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true, issued = false;
+      for (long long u = first; ok && u < args.total; u += stride) {
+        if (!wait_bounded(&ctrl->acc_empty[acc], acc_phase ^ 1u, ctl, ERR_WAIT_ACC_EMPTY)) break;
+        tc_fence_after();
+        int slice, ti, tj;
+        decode(args, u, slice, ti, tj);
+        const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
+        for (int kk = k0; kk < k1; ++kk) {
+          if (!wait_bounded(&ctrl->full[stage], phase, ctl, ERR_WAIT_FULL)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k) {
+            const uint64_t adesc =
+                A_MN ? smem_desc_sw128(sa + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sa + k * 32, 16, 1024);
+            const uint64_t bdesc =
+                B_MN ? smem_desc_sw128(sb + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sb + k * 32, 16, 1024);
+            tc_mma_bf16_pair(tmem_base + acc * BN, adesc, bdesc, idesc, ((kk - k0) | k) != 0 ? 1u : 0u);
+          }
+          issued = true;
+          tc_commit_pair_mc(&ctrl->empty[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(&ctrl->acc_full[acc], 0x3);
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (issued) {   // all MMAs have completed before tensor memory is released
+        tc_commit_pair_mc(&ctrl->drain, 0x1);
+        drain_wait(&ctrl->drain, 0u, ctl);
+      }
+    }
+  } else {
+    const uint32_t leader_acc_empty0 = mapa_shared(smem_u32(&ctrl->acc_empty[0]), 0);
+    const int lane_base = (warp % 4) * 32;   // the lanes of tensor memory that this warp may read
+    const int half = (warp - 2) / 4;         // 128 of the tile's 256 columns
+    uint8_t *buf = staging + (warp - 2) * BUF_BYTES;
+    uint32_t acc = 0, acc_phase = 0;
+    for (long long u = first; u < args.total; u += stride) {
+      int slice, ti, tj;
+      decode(args, u, slice, ti, tj);
+      const bool ok = wait_bounded(&ctrl->acc_full[acc], acc_phase, ctl, ERR_WAIT_ACC_FULL);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const int warp_row0 = (2 * ti + rank) * BM + lane_base, col0 = tj * BN + 128 * half;
+      const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 128 * half;
+      if constexpr (KIND == LOGITS) epilogue_logits(args, tmem, warp_row0 + lane, col0, 2 * tj + half);
+      else if constexpr (KIND == DLOGITS) epilogue_dlogits(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
+      else epilogue_out(args, tmem, slice, warp_row0, col0, lane, buf);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(leader_acc_empty0 + acc * static_cast<uint32_t>(sizeof(uint64_t)));
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (KIND == DLOGITS && lane == 0) bulk_wait_group_all();
+  }
+
+  // neither CTA leaves while the other may still signal it
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------------------------------ the small kernels
+
+struct CombineArgs {
+  const float2 *partials;
+  const float *z_target, *weights;
+  const void *targets;
+  int itype, parts, rows;
+  long long V;
+  float *losses, *lse;
+};
+
+// 32 rows per block, a lane each; eight warps share the parts. lse = m + log(sum of s_p exp(m_p - m)).
+__global__ void __launch_bounds__(256) ce_combine_kernel(const CombineArgs a) {
+  __shared__ float2 sh[8][32];
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int row = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  auto join = [&](float2 p) {
+    const float mn = fmaxf(m, p.x);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    s = s * exp2_fast((m - ref) * LOG2E) + p.y * exp2_fast((p.x - ref) * LOG2E);
+    m = mn;
+  };
+  if (row < a.rows) {
+#pragma unroll 4
+    for (int p = warp; p < a.parts; p += 8) join(a.partials[static_cast<long long>(p) * a.rows + row]);
+  }
+  sh[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp > 0 || row >= a.rows) return;
+  for (int w = 1; w < 8; ++w) join(sh[w][lane]);
+  const long long t = target_of(a.targets, a.itype, row);
+  const float w = a.weights != nullptr ? a.weights[row] : 1.f;
+  const bool live = t >= 0 && t < a.V && w != 0.f;
+  const float lse = m + logf(s);
+  a.lse[row] = live ? lse : 0.f;
+  a.losses[row] = live ? w * (lse - a.z_target[row]) : 0.f;
+}
+
+struct RowsArgs {
+  const __nv_bfloat16 *h;
+  __nv_bfloat16 *out;
+  long long ldh, ld_out, V;
+  const void *targets;
+  const float *weights;
+  int itype, rows, D;
+};
+
+// h with zeros for the rows that have no part in the loss: dw's product multiplies every row, and a row of padding may
+// hold NaN. A warp per row, 16 bytes per lane and turn (both pitches are multiples of 8; what lies past D is not read).
+__global__ void __launch_bounds__(256) ce_rows_kernel(const RowsArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const int row = blockIdx.x * 8 + threadIdx.x / 32;
+  if (row >= a.rows) return;
+  const long long t = target_of(a.targets, a.itype, row);
+  const bool live = t >= 0 && t < a.V && (a.weights == nullptr || a.weights[row] != 0.f);
+  const __nv_bfloat16 *src = a.h + row * a.ldh;
+  __nv_bfloat16 *dst = a.out + row * a.ld_out;
+#pragma unroll 4
+  for (int c = 8 * lane; c + 8 <= a.D; c += 256)
+    *reinterpret_cast<uint4 *>(dst + c) = live ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
+  for (int c = a.D / 8 * 8 + lane; c < a.D; c += 32) dst[c] = live ? src[c] : __float2bfloat16_rn(0.f);
+}
+
+struct ReduceArgs {
+  const float *parts;          // n of rows x ld_part, slice_stride apart
+  long long slice_stride, ld_part, ld_out;
+  int n, rows, cols, accumulate;
+  void *out;
+};
+
+// out (+)= the slices in their order; n = 0: zeros. Four columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) ce_reduce_kernel(const ReduceArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  const long long per_row = (a.cols + 3) / 4, total = per_row * a.rows;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.out) & (4 * sizeof(T) - 1)) == 0 && a.ld_out % 4 == 0;
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<long long>(gridDim.x) * 256) {
+    const long long row = i / per_row, c = 4 * (i - row * per_row);
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    const float *src = a.parts + row * a.ld_part + c;
+#pragma unroll 4
+    for (int k = 0; k < a.n; ++k) {   // the slices' rows are padded to whole 16 bytes
+      const float4 q = *reinterpret_cast<const float4 *>(src + k * a.slice_stride);
+      f[0] += q.x, f[1] += q.y, f[2] += q.z, f[3] += q.w;
+    }
+    store_piece<T, 4>(static_cast<T *>(a.out) + row * a.ld_out + c, f, static_cast<int>(min(4ll, a.cols - c)), vec,
+                      a.accumulate != 0);
+  }
+}
+
+// ------------------------------------------------------------------------------------------ plan
+
+// Slices of a contraction of k 64-deep steps over `tiles` tile pairs: the count for which the longest SM pair's steps are
+// fewest, each slice counted with TILE_STEPS more for its start and epilogue, and with what its sums' way through memory
+// costs. From sizes alone.
+constexpr int TILE_STEPS = 6;
+int choose_split(long long tiles, long long k) {
+  if (tiles >= 4 * PAIRS) return 1;
+  int best = 1;
+  double best_cost = 0;
+  for (int s = 1; s <= MAX_SPLIT && (s == 1 || k / s >= 8); ++s) {
+    const long long per = (k + s - 1) / s, n = (k + per - 1) / per;
+    const double waves = static_cast<double>((tiles * n + PAIRS - 1) / PAIRS);
+    // a slice's tile is 256 KB written and read: 0.08 us of the whole GPU's bandwidth, a fifth of a step of every pair
+    const double cost = waves * static_cast<double>(per + TILE_STEPS) + (n > 1 ? 0.2 * static_cast<double>(tiles * n) / PAIRS + 12 : 0);
+    if (s == 1 || cost < best_cost) {
+      best = static_cast<int>(n);
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+std::atomic<long long> g_piece_rows{0};   // muon_debug_loss_rows
+
+struct Plan {
+  long long rows, pieces, Vp, Dp;     // rows of a piece; pitches of dz and of fp32 scratch rows
+  int planes, parts;
+  int split_dh, split_dw;
+  size_t partials, z_target, dz, h_live, slices, dw_sum, total;
+};
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+Plan plan(int64_t N, int64_t V, int64_t D, int terms, bool dw_f32) {
+  Plan p{};
+  long long rows = g_piece_rows.load();
+  if (rows <= 0) rows = PIECE_ELEMS / V;
+  rows = std::max(256ll, rows / 256 * 256);
+  p.rows = std::max<long long>(1, std::min<long long>(N, rows));
+  p.pieces = ceil_div(N, p.rows);
+  p.Vp = ceil_div(V, 64) * 64;
+  p.Dp = ceil_div(D, 4) * 4;
+  p.planes = terms;
+  p.parts = static_cast<int>(ceil_div(V, BN / 2));
+  size_t off = 1024;   // the control block
+  auto take = [&](size_t &at, long long bytes) {
+    at = off;
+    off = align_up(off + static_cast<size_t>(bytes), 1024);
+  };
+  take(p.partials, 8ll * p.parts * p.rows);
+  take(p.z_target, 4 * p.rows);
+  if (terms > 0) {
+    const long long kh = ceil_div(V, BK) * terms, kw = ceil_div(p.rows, BK) * terms;
+    p.split_dh = choose_split(ceil_div(p.rows, 2 * BM) * ceil_div(D, BN), kh);
+    p.split_dw = choose_split(ceil_div(V, 2 * BM) * ceil_div(D, BN), kw);
+    take(p.dz, 2ll * terms * p.rows * p.Vp);
+    take(p.h_live, 2 * p.rows * round8(D));
+    const long long dh = p.split_dh > 1 ? 4ll * p.split_dh * p.rows * p.Dp : 0;
+    const long long dw = p.split_dw > 1 ? 4ll * p.split_dw * V * p.Dp : 0;
+    take(p.slices, std::max(dh, dw));
+    if (p.pieces > 1 && !dw_f32) take(p.dw_sum, 4ll * V * p.Dp);
+  }
+  p.total = off;
+  return p;
+}
+
+// ------------------------------------------------------------------------------------------ launches
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+template <int KIND>
+muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
+  static AttributesSet set;
+  static std::atomic<int> clusters[64];
+  if (set.once([] {
+        return cudaFuncSetAttribute(ce_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(SMEM));
+      }) != cudaSuccess)
+    return MUON_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(GEMM_THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
+  int n = clusters[dev].load(std::memory_order_relaxed);   // pairs that can be resident at once
+  if (n == 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (device_sm_count() / 2)));
+    if (cudaOccupancyMaxActiveClusters(&n, ce_gemm_kernel<KIND>, &cfg) != cudaSuccess || n < 1) n = device_sm_count() / 2;
+    clusters[dev].store(n, std::memory_order_relaxed);
+  }
+  a.m_pairs = static_cast<int>(ceil_div(a.rows, 2 * BM));
+  a.n_tiles = static_cast<int>(ceil_div(a.cols, BN));
+  if (a.split < 1) a.split = 1;
+  a.k_per = static_cast<int>(ceil_div(a.k_iters, a.split));
+  a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
+  a.total = static_cast<long long>(a.m_pairs) * a.n_tiles * a.split;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(n, a.total)));
+  launch_begin(kind, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, ce_gemm_kernel<KIND>, a);
+  launch_end(s);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+muon_status launch_reduce(const ReduceArgs &r, int dtype, cudaStream_t s) {
+  const long long work = ceil_div(r.cols, 4) * r.rows;
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(ceil_div(work, 256), 8ll * device_sm_count())));
+  launch_begin(KK_CE_REDUCE, s);
+  const cudaError_t e = dtype == MUON_F32 ? launch_pdl(ce_reduce_kernel<float>, grid, dim3(256), 0, s, r)
+                                          : launch_pdl(ce_reduce_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, r);
+  launch_end(s);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+// What a call has in hand.
+struct Call {
+  const char *h, *w;
+  long long ldh, ldw;
+  const void *targets;
+  int itype;
+  const float *weights;
+  long long N, V, D;
+  float *losses, *lse;
+  const float *lse_in, *grad;
+  float grad_scale;
+  char *dh, *dw;
+  int dhdt, dwdt;
+  long long lddh, lddw;
+  int accumulate;
+  char *ws;
+  bool forward, backward;
+  int terms;
+};
+
+size_t size_of(int dt) { return dt == MUON_F32 ? 4 : 2; }
+
+// Rows of a matrix of one row may have any pitch: none is used.
+long long pitch8(long long ld, long long rows, long long cols) { return rows == 1 ? round8(cols) : ld; }
+
+muon_status run(const Call &c, cudaStream_t s) {
+  const Plan p = plan(c.N, c.V, c.D, c.terms, c.dw == nullptr || c.dwdt == MUON_F32);
+  muon_status st;
+  const long long kd = ceil_div(c.D, BK), kv = ceil_div(c.V, BK);
+  CeArgs base;
+  memset(&base, 0, sizeof(base));
+  base.targets = nullptr;
+  base.itype = c.itype;
+  base.grad_scale = c.grad_scale;
+  base.planes = p.planes;
+  base.err = reinterpret_cast<uint32_t *>(c.ws);
+  base.timeout_ns = wait_timeout_ns();
+  base.partials = reinterpret_cast<float2 *>(c.ws + p.partials);
+  base.z_target = reinterpret_cast<float *>(c.ws + p.z_target);
+  __nv_bfloat16 *dz = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.dz);
+  float *slices = reinterpret_cast<float *>(c.ws + p.slices);
+  float *dw_sum = p.dw_sum ? reinterpret_cast<float *>(c.ws + p.dw_sum) : nullptr;
+  if (c.N == 0) {
+    if (c.dw == nullptr || c.accumulate) return MUON_OK;
+    return launch_reduce(ReduceArgs{nullptr, 0, 0, c.lddw, 0, static_cast<int>(c.V), static_cast<int>(c.D), 0, c.dw}, c.dwdt,
+                         s);
+  }
+  for (long long r0 = 0; r0 < c.N; r0 += p.rows) {
+    const long long rows = std::min(p.rows, c.N - r0);
+    const char *h = c.h + r0 * c.ldh * 2;
+    const long long ldh = pitch8(c.ldh, c.N, c.D), ldw = pitch8(c.ldw, c.V, c.D);
+    CeArgs a = base;
+    a.rows = static_cast<int>(rows);
+    a.cols = static_cast<int>(c.V);
+    a.k_iters = a.k_wrap = static_cast<int>(kd);
+    a.targets = static_cast<const char *>(c.targets) + r0 * (c.itype == MUON_I32 ? 4 : 8);
+    a.weights = c.weights != nullptr ? c.weights + r0 : nullptr;
+    if (!make_bf16_map(&a.map_a, h, c.D, rows, 1, ldh, ldh * rows, BM) ||
+        !make_bf16_map(&a.map_b, c.w, c.D, c.V, 1, ldw, ldw * c.V, BN / 2))
+      return MUON_ERR_CUDA;
+    if (c.forward) {
+      CeArgs f = a;
+      if ((st = launch_gemm<LOGITS>(f, KK_CE_LOGITS, s)) != MUON_OK) return st;
+      const CombineArgs cb{a.partials, a.z_target, a.weights, a.targets, a.itype, p.parts, a.rows, c.V, c.losses + r0,
+                           c.lse + r0};
+      launch_begin(KK_CE_COMBINE, s);
+      const cudaError_t e =
+          launch_pdl(ce_combine_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(256), 0, s, cb);
+      launch_end(s);
+      if (e != cudaSuccess) return MUON_ERR_CUDA;
+    }
+    if (!c.backward) continue;
+    {
+      CeArgs f = a;
+      f.lse = (c.forward ? c.lse : c.lse_in) + r0;
+      f.grad = c.grad != nullptr ? c.grad + r0 : nullptr;
+      if (!make_bf16_map(&f.map_out, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, 32)) return MUON_ERR_CUDA;
+      if ((st = launch_gemm<DLOGITS>(f, KK_CE_DLOGITS, s)) != MUON_OK) return st;
+    }
+    if (c.dh != nullptr) {
+      char *out = c.dh + r0 * c.lddh * static_cast<long long>(size_of(c.dhdt));
+      CeArgs f = base;
+      f.rows = static_cast<int>(rows);
+      f.cols = static_cast<int>(c.D);
+      f.k_iters = static_cast<int>(kv * p.planes);
+      f.k_wrap = static_cast<int>(kv);
+      f.split = p.split_dh;
+      if (!make_bf16_map(&f.map_a, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, BM) ||
+          !make_bf16_map(&f.map_b, c.w, c.D, c.V, 1, ldw, ldw * c.V, BK))
+        return MUON_ERR_CUDA;
+      const bool cut = p.split_dh > 1;
+      f.out = cut ? static_cast<void *>(slices) : out;
+      f.out_f32 = cut || c.dhdt == MUON_F32;
+      f.ld_out = cut ? p.Dp : c.lddh;
+      f.slice_stride = rows * p.Dp;
+      f.vec = aligned(f.out, 16) && f.ld_out % (f.out_f32 ? 4 : 8) == 0;
+      if ((st = launch_gemm<DH>(f, KK_CE_DH, s)) != MUON_OK) return st;
+      if (cut && (st = launch_reduce(ReduceArgs{slices, f.slice_stride, p.Dp, c.lddh, f.split, f.rows, f.cols, 0, out},
+                                     c.dhdt, s)) != MUON_OK)
+        return st;
+    }
+    if (c.dw != nullptr) {
+      __nv_bfloat16 *h_live = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.h_live);
+      const RowsArgs ra{reinterpret_cast<const __nv_bfloat16 *>(h), h_live, ldh, round8(c.D), c.V, a.targets, a.weights,
+                        a.itype, a.rows, static_cast<int>(c.D)};
+      launch_begin(KK_CE_ROWS, s);
+      const cudaError_t e = launch_pdl(ce_rows_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 8))), dim3(256), 0, s, ra);
+      launch_end(s);
+      if (e != cudaSuccess) return MUON_ERR_CUDA;
+      CeArgs f = base;
+      f.rows = static_cast<int>(c.V);
+      f.cols = static_cast<int>(c.D);
+      f.k_wrap = static_cast<int>(ceil_div(rows, BK));
+      f.k_iters = f.k_wrap * p.planes;
+      f.split = p.split_dw;
+      if (!make_bf16_map(&f.map_a, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, BK) ||
+          !make_bf16_map(&f.map_b, h_live, c.D, rows, 1, round8(c.D), round8(c.D) * rows, BK))
+        return MUON_ERR_CUDA;
+      // several pieces add up in fp32: in the gradient itself, or in scratch that the last piece rounds
+      void *sum = dw_sum != nullptr ? static_cast<void *>(dw_sum) : c.dw;
+      const long long ld = dw_sum != nullptr ? p.Dp : c.lddw;
+      const int dt = dw_sum != nullptr ? static_cast<int>(MUON_F32) : c.dwdt;
+      const int add = r0 > 0 || (dw_sum == nullptr && c.accumulate);
+      const bool cut = p.split_dw > 1;
+      f.out = cut ? static_cast<void *>(slices) : sum;
+      f.out_f32 = cut || dt == MUON_F32;
+      f.ld_out = cut ? p.Dp : ld;
+      f.slice_stride = c.V * p.Dp;
+      f.accumulate = cut ? 0 : add;
+      f.vec = aligned(f.out, 16) && f.ld_out % (f.out_f32 ? 4 : 8) == 0;
+      if ((st = launch_gemm<DW>(f, KK_CE_DW, s)) != MUON_OK) return st;
+      if (cut && (st = launch_reduce(ReduceArgs{slices, f.slice_stride, p.Dp, ld, f.split, f.rows, f.cols, add, sum}, dt,
+                                     s)) != MUON_OK)
+        return st;
+    }
+  }
+  if (c.dw != nullptr && dw_sum != nullptr)
+    return launch_reduce(ReduceArgs{dw_sum, 0, p.Dp, c.lddw, 1, static_cast<int>(c.V), static_cast<int>(c.D), c.accumulate,
+                                    c.dw},
+                         c.dwdt, s);
+  return MUON_OK;
+}
+
+// ------------------------------------------------------------------------------------------ checks
+
+constexpr int64_t MAX_ROWS = 1 << 26, MAX_COLS = 1 << 26, MAX_D = 65536;
+
+muon_status check_sizes(int64_t N, int64_t V, int64_t D) {
+  if (N < 0 || V < 1 || D < 1) return MUON_ERR_INVALID_ARG;
+  if (N > MAX_ROWS || V > MAX_COLS || D > MAX_D || N * V > (1ll << 40)) return MUON_ERR_SHAPE;
+  return MUON_OK;
+}
+
+muon_status check_inputs(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt, int64_t ldw,
+                         const void *targets, muon_itype itype, const float *weights, int64_t N, int64_t V, int64_t D) {
+  muon_status st = check_sizes(N, V, D);
+  if (st != MUON_OK) return st;
+  if (w == nullptr || (N > 0 && (h == nullptr || targets == nullptr)) || ldh < D || ldw < D) return MUON_ERR_INVALID_ARG;
+  if (hdt != MUON_BF16 || wdt != MUON_BF16 || (itype != MUON_I32 && itype != MUON_I64)) return MUON_ERR_DTYPE;
+  if (!aligned(h, 16) || !aligned(w, 16) || (N > 1 && ldh % 8 != 0) || (V > 1 && ldw % 8 != 0) ||
+      !aligned(targets, itype == MUON_I32 ? 4 : 8) || !aligned(weights, 4))
+    return MUON_ERR_ALIGNMENT;
+  return MUON_OK;
+}
+
+muon_status check_outputs(const void *dh, muon_dtype dhdt, int64_t lddh, const void *dw, muon_dtype dwdt, int64_t lddw,
+                          int64_t N, int64_t D, int *terms) {
+  if (dh == nullptr && dw == nullptr && N > 0) return MUON_ERR_INVALID_ARG;
+  *terms = 1;
+  if (dh != nullptr) {
+    if (lddh < D) return MUON_ERR_INVALID_ARG;
+    if (!valid_dtype(dhdt)) return MUON_ERR_DTYPE;
+    if (!aligned(dh, size_of(dhdt))) return MUON_ERR_ALIGNMENT;
+    if (dhdt == MUON_F32) *terms = 2;
+  }
+  if (dw != nullptr) {
+    if (lddw < D) return MUON_ERR_INVALID_ARG;
+    if (!valid_dtype(dwdt)) return MUON_ERR_DTYPE;
+    if (!aligned(dw, size_of(dwdt))) return MUON_ERR_ALIGNMENT;
+    if (dwdt == MUON_F32) *terms = 2;
+  }
+  return MUON_OK;
+}
+
+muon_status check_ws(const void *ws, size_t ws_bytes, int64_t N, int64_t V, int64_t D, int terms) {
+  if (ws == nullptr) return MUON_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return MUON_ERR_ALIGNMENT;
+  if (ws_bytes < linear_cross_entropy_workspace_bytes(N, V, D, terms)) return MUON_ERR_WORKSPACE;
+  return MUON_OK;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int terms) {
+  if (check_sizes(N, V, D) != MUON_OK || terms < 0 || terms > 2) return 0;
+  return plan(N, V, D, terms, false).total;
+}
+
+muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
+                                         int64_t ldw, const void *targets, muon_itype itype, const float *weights,
+                                         float *losses, float *lse, int64_t N, int64_t V, int64_t D, void *ws,
+                                         size_t ws_bytes, muon_stream_t stream) {
+  muon_status st = check_inputs(h, hdt, ldh, w, wdt, ldw, targets, itype, weights, N, V, D);
+  if (st != MUON_OK) return st;
+  if (N > 0 && (losses == nullptr || lse == nullptr)) return MUON_ERR_INVALID_ARG;
+  if (!aligned(losses, 4) || !aligned(lse, 4)) return MUON_ERR_ALIGNMENT;
+  if ((st = check_ws(ws, ws_bytes, N, V, D, 0)) != MUON_OK || (st = device_check()) != MUON_OK) return st;
+  Call c{};
+  c.h = static_cast<const char *>(h);
+  c.w = static_cast<const char *>(w);
+  c.ldh = ldh;
+  c.ldw = ldw;
+  c.targets = targets;
+  c.itype = itype;
+  c.weights = weights;
+  c.N = N;
+  c.V = V;
+  c.D = D;
+  c.losses = losses;
+  c.lse = lse;
+  c.ws = static_cast<char *>(ws);
+  c.forward = true;
+  return run(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
+                                          int64_t ldw, const void *targets, muon_itype itype, const float *weights,
+                                          const float *lse, const float *grad, void *dh, muon_dtype dhdt, int64_t lddh,
+                                          void *dw, muon_dtype dwdt, int64_t lddw, int accumulate, int64_t N, int64_t V,
+                                          int64_t D, void *ws, size_t ws_bytes, muon_stream_t stream) {
+  muon_status st = check_inputs(h, hdt, ldh, w, wdt, ldw, targets, itype, weights, N, V, D);
+  if (st != MUON_OK) return st;
+  Call c{};
+  if (N > 0 && lse == nullptr) return MUON_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(grad, 4)) return MUON_ERR_ALIGNMENT;
+  if ((st = check_outputs(dh, dhdt, lddh, dw, dwdt, lddw, N, D, &c.terms)) != MUON_OK ||
+      (st = check_ws(ws, ws_bytes, N, V, D, c.terms)) != MUON_OK || (st = device_check()) != MUON_OK)
+    return st;
+  c.h = static_cast<const char *>(h);
+  c.w = static_cast<const char *>(w);
+  c.ldh = ldh;
+  c.ldw = ldw;
+  c.targets = targets;
+  c.itype = itype;
+  c.weights = weights;
+  c.N = N;
+  c.V = V;
+  c.D = D;
+  c.lse_in = lse;
+  c.grad = grad;
+  c.grad_scale = 1.f;
+  c.dh = static_cast<char *>(dh);
+  c.dw = static_cast<char *>(dw);
+  c.dhdt = dhdt;
+  c.dwdt = dwdt;
+  c.lddh = lddh;
+  c.lddw = lddw;
+  c.accumulate = accumulate != 0;
+  c.ws = static_cast<char *>(ws);
+  c.backward = true;
+  return run(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+muon_status linear_cross_entropy_forward_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w,
+                                                  muon_dtype wdt, int64_t ldw, const void *targets, muon_itype itype,
+                                                  const float *weights, float grad_scale, float *losses, float *lse,
+                                                  void *dh, muon_dtype dhdt, int64_t lddh, void *dw, muon_dtype dwdt,
+                                                  int64_t lddw, int accumulate, int64_t N, int64_t V, int64_t D, void *ws,
+                                                  size_t ws_bytes, muon_stream_t stream) {
+  muon_status st = check_inputs(h, hdt, ldh, w, wdt, ldw, targets, itype, weights, N, V, D);
+  if (st != MUON_OK) return st;
+  Call c{};
+  if ((N > 0 && (losses == nullptr || lse == nullptr)) || !std::isfinite(grad_scale)) return MUON_ERR_INVALID_ARG;
+  if (!aligned(losses, 4) || !aligned(lse, 4)) return MUON_ERR_ALIGNMENT;
+  if ((st = check_outputs(dh, dhdt, lddh, dw, dwdt, lddw, N, D, &c.terms)) != MUON_OK ||
+      (st = check_ws(ws, ws_bytes, N, V, D, c.terms)) != MUON_OK || (st = device_check()) != MUON_OK)
+    return st;
+  c.h = static_cast<const char *>(h);
+  c.w = static_cast<const char *>(w);
+  c.ldh = ldh;
+  c.ldw = ldw;
+  c.targets = targets;
+  c.itype = itype;
+  c.weights = weights;
+  c.N = N;
+  c.V = V;
+  c.D = D;
+  c.losses = losses;
+  c.lse = lse;
+  c.grad_scale = grad_scale;
+  c.dh = static_cast<char *>(dh);
+  c.dw = static_cast<char *>(dw);
+  c.dhdt = dhdt;
+  c.dwdt = dwdt;
+  c.lddh = lddh;
+  c.lddw = lddw;
+  c.accumulate = accumulate != 0;
+  c.ws = static_cast<char *>(ws);
+  c.forward = c.backward = true;
+  return run(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+muon_status muon_debug_loss_rows(int64_t rows) {
+  if (rows < 0) return MUON_ERR_INVALID_ARG;
+  g_piece_rows.store(rows);
+  return MUON_OK;
+}
+
+}  // extern "C"

@@ -43,6 +43,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace muon {
 
@@ -1097,9 +1098,10 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// 3-D bf16 map (inner, rows, batch) with a box of (64, box_rows, 1) and 128-byte swizzle.
-bool make_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long batch, long long ld,
-              long long mstride, int box_rows) {
+}  // namespace
+
+bool make_bf16_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long batch, long long ld,
+                   long long mstride, int box_rows) {
   auto enc = get_encode_fn();
   if (enc == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
@@ -1112,6 +1114,10 @@ bool make_map(CUtensorMap *map, const void *base, long long inner, long long row
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
+
+constexpr auto make_map = make_bf16_map;
 
 template <int EPI, bool B_MN, int STAGES, int SLOTS>
 muon_status launch_shape(const GemmGroup &g, int32_t kind, cudaStream_t s) {

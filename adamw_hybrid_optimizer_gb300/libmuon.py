@@ -29,6 +29,7 @@ MUON_BF16 = 1
 MUON_I32 = 0
 MUON_I64 = 1
 MUON_MAX_NS_STEPS = 32
+ADAMW8_BLOCK = 256
 
 # the C signatures, checked against include/libmuon.h by tests/test_abi.py
 _c_int64 = ctypes.c_int64
@@ -59,6 +60,13 @@ class adamw_tensor(ctypes.Structure):
                 ("pdt", ctypes.c_int), ("gdt", ctypes.c_int), ("hp", ctypes.POINTER(adamw_hparams))]
 
 
+class adamw8_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("pdt", ctypes.c_int), ("gdt", ctypes.c_int),
+                ("hp", ctypes.POINTER(adamw_hparams))]
+
+
 SIGNATURES = {
     "muon_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
     "muon_step_batched": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _c_int64, _c_int64, _c_int64,
@@ -79,6 +87,7 @@ SIGNATURES = {
                                          ctypes.POINTER(adamw_hparams), _vp]),
     "adamw_workspace_bytes_grouped": (ctypes.c_size_t, [_c_int64]),
     "adamw_step_grouped": (ctypes.c_int, [ctypes.POINTER(adamw_tensor), _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "adamw8_step_grouped": (ctypes.c_int, [ctypes.POINTER(adamw8_tensor), _c_int64, _vp]),
     "hybrid_step": (ctypes.c_int, [ctypes.POINTER(muon_bucket), ctypes.c_int, ctypes.POINTER(muon_hparams), _vp,
                                    ctypes.c_size_t, ctypes.POINTER(adamw_tensor), _c_int64, _vp, ctypes.c_size_t,
                                    _vp]),
@@ -106,6 +115,20 @@ SIGNATURES = {
     "distill_forward_backward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _vp, ctypes.c_int,
                                                 _vp, ctypes.c_float, _vp, _vp, _vp, ctypes.c_int, _c_int64, _c_int64,
                                                 _c_int64, _c_int64, ctypes.c_float, _vp]),
+    "linear_cross_entropy_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64, ctypes.c_int]),
+    "linear_cross_entropy_forward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64, _vp,
+                                                    ctypes.c_int, _vp, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp,
+                                                    ctypes.c_size_t, _vp]),
+    "linear_cross_entropy_backward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64, _vp,
+                                                     ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_int, _c_int64, _vp,
+                                                     ctypes.c_int, _c_int64, ctypes.c_int, _c_int64, _c_int64, _c_int64,
+                                                     _vp, ctypes.c_size_t, _vp]),
+    "linear_cross_entropy_forward_backward": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64,
+                                                             _vp, ctypes.c_int, _vp, ctypes.c_float, _vp, _vp, _vp,
+                                                             ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64,
+                                                             ctypes.c_int, _c_int64, _c_int64, _c_int64, _vp,
+                                                             ctypes.c_size_t, _vp]),
+    "muon_debug_loss_rows": (ctypes.c_int, [_c_int64]),
     "muon_plan_buckets": (ctypes.c_int, [_c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "muon_autotune": (ctypes.c_int, [ctypes.POINTER(muon_bucket), ctypes.c_int, ctypes.POINTER(muon_hparams), _vp,
                                      ctypes.c_size_t, _vp]),
@@ -345,6 +368,37 @@ def adamw_step_grouped(tensors, ws, stream=None):
                                     _stream(stream)), "adamw_step_grouped")
 
 
+def make_adamw8_tensors(specs):
+    """specs: sequence of (param, grad, exp_avg, exp_avg_sq, scales, hp[, master]) for adamw8_step_grouped, all contiguous CUDA
+    tensors: the moments torch.float8_e4m3fn, scales fp32 with two values per ADAMW8_BLOCK elements. Returns a ctypes
+    adamw8_tensor array that keeps the tensors and the hparams structs it points at alive."""
+    import torch
+    arr = (adamw8_tensor * len(specs))()
+    keep = []
+    where = "make_adamw8_tensors"
+    for i, spec in enumerate(specs):
+        p, g, m, v, s, hp = spec[:6]
+        ms = spec[6] if len(spec) > 6 else None
+        n = p.numel()
+        if m.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"{where}: moments of torch.float8_e4m3fn")
+        if ms is not None and _dtype_code(p) != MUON_BF16:
+            raise ValueError(f"{where}: a master copy needs bf16 params")
+        arr[i] = adamw8_tensor(_vector(p, "param", where, n), _vector(g, "grad", where, n),
+                               _vector(m, "exp_avg", where, n), _vector(v, "exp_avg_sq", where, n),
+                               _vector(s, "scales", where, 2 * ((n + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK), True),
+                               _vector(ms, "master", where, n, True), n, _dtype_code(p), _dtype_code(g),
+                               ctypes.pointer(hp))
+        keep += [p, g, m, v, s, hp] + ([ms] if ms is not None else [])
+    arr.tensors = keep
+    return arr
+
+
+def adamw8_step_grouped(tensors, stream=None):
+    """tensors: a ctypes adamw8_tensor array (see make_adamw8_tensors)."""
+    _check(lib().adamw8_step_grouped(tensors, len(tensors), _current_stream(stream)), "adamw8_step_grouped")
+
+
 def hybrid_step(buckets, hp, ws, tensors, adamw_ws, stream=None):
     """buckets (make_buckets) with hp / ws as for muon_step_grouped, tensors (make_adamw_tensors) with adamw_ws as
     for adamw_step_grouped; either list may be empty."""
@@ -552,6 +606,67 @@ def distill_forward_backward(logits, t_idx, t_val, temperature: float, weights, 
                                         dlogits.data_ptr(), _dtype_code(dlogits), ldd, N, V, K, temperature,
                                         _current_stream(stream))
     _check(st, where)
+
+
+def linear_cross_entropy_workspace_bytes(N: int, V: int, D: int, terms: int) -> int:
+    """terms: 0 without gradients, 1 for bf16 gradients, 2 if one is fp32."""
+    return int(lib().linear_cross_entropy_workspace_bytes(int(N), int(V), int(D), int(terms)))
+
+
+def _linear_ce(where, h, w, targets, weights):
+    (N, D), V = h.shape, w.shape[0]
+    return (N, V, D), (h.data_ptr(), _dtype_code(h), _matrix(h, "h", where), w.data_ptr(), _dtype_code(w),
+                       _matrix(w, "w", where, (V, D)), _vector(targets, "targets", where, N), _itype_code(targets),
+                       _vector(weights, "weights", where, N, True))
+
+
+def _linear_ce_gradients(where, dh, dw, sizes, accumulate):
+    N, V, D = sizes
+    out = ()
+    for t, name, rows in ((dh, "dh", N), (dw, "dw", V)):
+        out += (None, MUON_BF16, D) if t is None else (t.data_ptr(), _dtype_code(t), _matrix(t, name, where, (rows, D)))
+    return (*out, int(bool(accumulate)), N, V, D)
+
+
+def linear_cross_entropy_forward(h, w, targets, weights, losses, lse, ws, stream=None):
+    """losses[i] = weights[i] * (lse[i] - logit of targets[i]) of the head h w^T, whose logits are not kept.
+
+    h (N, D) and w (V, D) bf16; targets int32 or int64 (N); weights None or fp32 (N); losses, lse fp32 (N)."""
+    where = "linear_cross_entropy_forward"
+    sizes, head = _linear_ce(where, h, w, targets, weights)
+    st = lib().linear_cross_entropy_forward(*head, _vector(losses, "losses", where, sizes[0], True),
+                                            _vector(lse, "lse", where, sizes[0], True), *sizes, *_workspace(ws, where),
+                                            _current_stream(stream))
+    _check(st, where)
+
+
+def linear_cross_entropy_backward(h, w, targets, weights, lse, grad, dh, dw, ws, accumulate: bool = False, stream=None):
+    """dh and dw (either may be None) from the forward pass's lse and the gradient of each row's loss: grad None (all 1) or fp32
+    (N). accumulate=True adds dw to what it holds."""
+    where = "linear_cross_entropy_backward"
+    sizes, head = _linear_ce(where, h, w, targets, weights)
+    st = lib().linear_cross_entropy_backward(*head, _vector(lse, "lse", where, sizes[0], True),
+                                             _vector(grad, "grad", where, sizes[0], True),
+                                             *_linear_ce_gradients(where, dh, dw, sizes, accumulate),
+                                             *_workspace(ws, where), _current_stream(stream))
+    _check(st, where)
+
+
+def linear_cross_entropy_forward_backward(h, w, targets, weights, grad_scale: float, losses, lse, dh, dw, ws,
+                                          accumulate: bool = False, stream=None):
+    """linear_cross_entropy_forward and linear_cross_entropy_backward (with grad_scale for every row's grad) in one call."""
+    where = "linear_cross_entropy_forward_backward"
+    sizes, head = _linear_ce(where, h, w, targets, weights)
+    st = lib().linear_cross_entropy_forward_backward(*head, grad_scale, _vector(losses, "losses", where, sizes[0], True),
+                                                     _vector(lse, "lse", where, sizes[0], True),
+                                                     *_linear_ce_gradients(where, dh, dw, sizes, accumulate),
+                                                     *_workspace(ws, where), _current_stream(stream))
+    _check(st, where)
+
+
+def muon_debug_loss_rows(rows: int):
+    """Rows per piece of the linear_cross_entropy calls (0: the default)."""
+    _check(lib().muon_debug_loss_rows(int(rows)), "muon_debug_loss_rows")
 
 
 def muon_plan_buckets(shapes: Sequence[Tuple[int, int]]):

@@ -251,6 +251,35 @@ size_t adamw_workspace_bytes_grouped(int64_t n);
 muon_status adamw_step_grouped(const adamw_tensor *tensors, int64_t n, void *ws, size_t ws_bytes,
                                muon_stream_t stream);
 
+/* Consecutive elements that share a scale in adamw8_step_grouped's moments. */
+#define ADAMW8_BLOCK 256
+
+/* One tensor of an AdamW call whose moments are held in 8 bits. An element's first moment is exp_avg[i] * scales[2b] and the
+ * root of its second moment exp_avg_sq[i] * scales[2b + 1], b = i / ADAMW8_BLOCK, the codes being e4m3 values (1 sign, 4
+ * exponent, 3 fraction bits, largest 448, no infinities). All zeros is the state before the first step. */
+typedef struct {
+  void *param;               /* device, n elements of pdt */
+  const void *grad;          /* device, n elements of gdt */
+  void *exp_avg;             /* device, n e4m3 codes */
+  void *exp_avg_sq;          /* device, n e4m3 codes (of roots: none negative) */
+  float *scales;             /* device fp32, 2 * ceil(n / ADAMW8_BLOCK), 8-byte aligned */
+  float *master;             /* NULL, or device fp32, n elements: the master weights taking the update (pdt MUON_BF16) */
+  int64_t n;                 /* >= 1 */
+  muon_dtype pdt, gdt;
+  const adamw_hparams *hp;   /* HOST struct, read during the call only; tensors may share one */
+} adamw8_tensor;
+
+/* AdamW (adamw_step's update, or adamw_step_master's where a tensor has a master) on n tensors with their moments in 8 bits
+ * ([P2] "The optimizer's memory budget"), in one launch per 96 tensors. The update takes the new moments in fp32; then each
+ * block's scales become its largest magnitudes / 448 (of 2^-100 at least) and the codes the moments over them, rounded to
+ * nearest, ties to even. A second moment above zero keeps a code above zero. A moment that is not finite becomes NaN, and
+ * counts for no scale. The results depend on no tensor's place in the call: they are those of n calls.
+ *   tensors  HOST array of n descriptors (1 <= n <= 2^20). Tensors must not overlap. Any alignment of the elements' own
+ *            size works (MUON_ERR_ALIGNMENT otherwise); with 16-byte aligned weights and gradients and 8-byte aligned codes
+ *            the accesses are vectors.
+ * Errors: as for adamw_step_grouped, all checked before any launch. */
+muon_status adamw8_step_grouped(const adamw8_tensor *tensors, int64_t n, muon_stream_t stream);
+
 /* The whole hybrid optimizer step in one call ([P1] "Usage Examples": one optimizer whose step updates the
  * hidden matrices with Muon and every other parameter with AdamW): muon_step_grouped on the buckets, then
  * adamw_step_grouped on the AdamW tensors, on the caller's stream; the results are those of the two calls.
@@ -410,6 +439,61 @@ muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t
                                      float grad_scale, float *losses, float *stats, void *dlogits, muon_dtype ddt,
                                      int64_t ldd, int64_t N, int64_t V, int64_t K, float temperature,
                                      muon_stream_t stream);
+
+/* The cross entropy of a linear head, z = h w^T, without keeping the N x V logits:
+ *   losses_i = weights_i * (lse_i - z_i,targets_i),   lse_i = log sum_v exp z_iv.
+ * A row whose target lies outside [0, V) (padding: -100, say) or whose weight is 0 has loss 0, lse 0 and no part in any
+ * gradient, whatever its h (NaN included). The logits are fp32 sums of bf16 products, computed in tiles that are reduced
+ * before they leave the SM; rows go through in pieces, so that scratch does not grow with N beyond a piece's.
+ *   h       device N x D, pitch ldh.   w  device V x D, pitch ldw. Both MUON_BF16 (what the tensor cores take;
+ *           MUON_ERR_DTYPE otherwise), their rows 16-byte aligned: the base, and the pitch a multiple of 8
+ *           (MUON_ERR_ALIGNMENT otherwise). D itself, N and V are any.
+ *   targets device N of itype, contiguous.   weights  device fp32, N, or NULL (all 1).
+ *   losses, lse  device fp32, N each; lse is kept for the backward pass.
+ *   ws      device workspace of ws_bytes >= linear_cross_entropy_workspace_bytes(N, V, D, terms), terms as the call needs
+ *           them, 256-byte aligned, zero-filled before its first use; its first 256 bytes are the control block that
+ *           muon_check reads.
+ * Limits: N, V <= 2^26, N * V <= 2^40, D <= 65536 (MUON_ERR_SHAPE). The same inputs give the same bits. */
+muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
+                                         int64_t ldw, const void *targets, muon_itype itype, const float *weights,
+                                         float *losses, float *lse, int64_t N, int64_t V, int64_t D, void *ws,
+                                         size_t ws_bytes, muon_stream_t stream);
+
+/* Bytes of workspace. terms: 0 for linear_cross_entropy_forward; 1 for the calls with gradients if both are bf16; 2 if one
+ * is fp32. The call without gradients takes any of them. A piece has at most 2^30 logits, or 256 rows: without gradients 8
+ * bytes for each 128 of them; with gradients 2 * terms bytes more for each, what dh's or dw's fp32 sums need where few tiles
+ * share a long contraction, and, for more than one piece, fp32 sums of dw. 0 for N < 0, V < 1, D < 1, sizes beyond the limits
+ * or other terms. */
+size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int terms);
+
+/* Its gradients from linear_cross_entropy_forward's lse: with dz_iv = grad_i * weights_i * (exp(z_iv - lse_i) -
+ * [v = targets_i]), dh = dz w and dw = dz^T h. The logits are computed again. dz goes into both products as bf16, rounded once
+ * (relative 2^-8 of each element, as bf16 gradients are); where dh or dw is MUON_F32, as two bf16 terms that hold it to 2^-16,
+ * which doubles the work of both products. Sums are fp32.
+ *   grad    device fp32, N: the gradient that reaches each row's loss, or NULL (all 1).
+ *   dh      device N x D of dhdt, pitch lddh, or NULL.   dw  device V x D of dwdt, pitch lddw, or NULL (not both NULL);
+ *           neither may overlap h or w.
+ *   accumulate  0: dw is written. Else: the sums are added to what it holds (dh is written in either case). */
+muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
+                                          int64_t ldw, const void *targets, muon_itype itype, const float *weights,
+                                          const float *lse, const float *grad, void *dh, muon_dtype dhdt, int64_t lddh,
+                                          void *dw, muon_dtype dwdt, int64_t lddw, int accumulate, int64_t N, int64_t V,
+                                          int64_t D, void *ws, size_t ws_bytes, muon_stream_t stream);
+
+/* Both in one call, for a training step whose loss is grad_scale * sum of losses: losses and lse as
+ * linear_cross_entropy_forward writes them, dh and dw as linear_cross_entropy_backward does with grad = grad_scale for every
+ * row. */
+muon_status linear_cross_entropy_forward_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w,
+                                                  muon_dtype wdt, int64_t ldw, const void *targets, muon_itype itype,
+                                                  const float *weights, float grad_scale, float *losses, float *lse,
+                                                  void *dh, muon_dtype dhdt, int64_t lddh, void *dw, muon_dtype dwdt,
+                                                  int64_t lddw, int accumulate, int64_t N, int64_t V, int64_t D, void *ws,
+                                                  size_t ws_bytes, muon_stream_t stream);
+
+/* Rows of the pieces that the linear_cross_entropy calls run in, rounded down to a multiple of 256 and at least that, or the
+ * default (2^30 logits' worth) for 0. A workspace belongs to the setting under which it was sized. For tests and
+ * measurements. MUON_ERR_INVALID_ARG for negative values. */
+muon_status muon_debug_loss_rows(int64_t rows);
 
 /* Shape bucketing, host only ([P1] "Parameter Processing and Padding": stacking into (K, ...);
  * [P4] section 2.2 "Batching"). Groups n matrices by exact (rows, cols), buckets numbered in

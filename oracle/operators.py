@@ -70,3 +70,27 @@ def distill(z, t_idx, t_val, T, weights=None):
         np.add.at(Q[i], idx, q)
         dz[i] = w[i] * T * (P[i] - Q[i])
     return {"losses": losses, "stats": stats, "dlogits": dz, "p": P, "q": Q}
+
+
+def linear_cross_entropy(h, w, targets, weights=None, grad=None):
+    """Returns a dict: losses, lse, dz (the logits' gradient with `grad` reaching the losses), dh, dw, and logits."""
+    h, w = np.asarray(h, np.float64), np.asarray(w, np.float64)
+    N, V = h.shape[0], w.shape[0]
+    wt = np.ones(N) if weights is None else np.asarray(weights, np.float64)
+    up = np.ones(N) if grad is None else np.asarray(grad, np.float64)
+    z = np.zeros((N, V))
+    losses, lse, dz = np.zeros(N), np.zeros(N), np.zeros((N, V))
+    live = np.zeros(N, bool)
+    for i, t in enumerate(targets):
+        if not 0 <= t < V or wt[i] == 0:
+            continue
+        live[i] = True
+        z[i] = w @ h[i]
+        top = z[i].max()
+        lse[i] = top + np.log(np.exp(z[i] - top).sum())
+        losses[i] = wt[i] * (lse[i] - z[i, t])
+        dz[i] = np.exp(z[i] - lse[i])
+        dz[i, t] -= 1.0
+        dz[i] *= up[i] * wt[i]
+    clean = np.where(live[:, None], h, 0.0)      # what a row without a part in the loss holds does not matter
+    return {"losses": losses, "lse": lse, "dz": dz, "dh": dz @ w, "dw": dz.T @ clean, "logits": z}
