@@ -19,7 +19,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <vector>
+#include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -29,8 +30,12 @@ namespace muon {
 namespace {
 
 constexpr int BLOCK = ADAMW8_BLOCK;
-constexpr int THREADS = 128;
-constexpr int BLOCKS_PER_SM = 8;
+// Resident blocks: 32 warps of 64 registers where weights and gradients are bf16, 24 of 80 where one is fp32 or there is a
+// master. (1.05 G elements, bf16: 1631 us with 4 blocks, 1679 with 3.5, 1980 with 4.5, whose 56 registers spill; 77 M
+// elements, fp32: 188 us with 3, 201 with 3.5.)
+constexpr int THREADS = 256;
+constexpr int NARROW_BLOCKS = 4;
+constexpr int WIDE_BLOCKS = 3;
 constexpr float TOP = 448.f;            // the largest e4m3 value
 constexpr float LEAST = 0x1p-9f;        // the smallest above zero
 // A block whose moments are all below this is scaled as if this were its largest, so that 448 / largest stays finite.
@@ -50,162 +55,197 @@ struct Tensor8 {
 
 struct Group8 {
   Tensor8 t[ADAMW_GROUP_MAX];
-  int ntensors, chunk;       // blocks a warp takes in one turn
+  int ntensors;
   long long total_blocks;
 };
 static_assert(sizeof(Group8) <= 32764, "kernel parameter block too large");
 
-__device__ __forceinline__ float2 decode2(unsigned short codes) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(codes, __NV_E4M3)));
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float2 decode2(unsigned codes) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<unsigned short>(codes), __NV_E4M3)));
 }
-__device__ __forceinline__ unsigned encode2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ unsigned encode2(float2 x) { return __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3); }
+
+// The square root by one Newton step on an approximate one, in fma: with s = v y, y about 1 / sqrt(v), it is
+// s + (v - s^2) y / 2, as close as fp32 gets in all but a few cases in a million. Not for v = 0, whose root is itself.
+__device__ __forceinline__ float2 root2(float2 v) {
+  const float2 y = make_float2(rsqrtf(v.x), rsqrtf(v.y));
+  const float2 s = __fmul2_rn(v, y);
+  const float2 e = __ffma2_rn(make_float2(-s.x, -s.y), s, v);
+  const float2 r = __ffma2_rn(e, __fmul2_rn(y, both(0.5f)), s);
+  return make_float2(v.x > 0.f ? r.x : v.x, v.y > 0.f ? r.y : v.y);
 }
 
-// The largest of the warp's magnitudes; NaN counts as zero.
-__device__ __forceinline__ float warp_largest(const float (&x)[8]) {
+// To two units in the last place: the weights take it times the learning rate.
+__device__ __forceinline__ float quick_divide(float a, float b) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(b));
+  return a * y;
+}
+
+// The largest of the warp's magnitudes, NaN counting as zero.
+__device__ __forceinline__ float warp_largest(const Vals<8> &x) {
   float t = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) t = fmaxf(t, fabsf(x[k]));
+  for (int k = 0; k < 4; ++k) t = fmaxf(t, fmaxf(fabsf(x.p[k].x), fabsf(x.p[k].y)));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(t)));
 }
 
-// As warp_largest over the finite values; the infinite ones become NaN, which e4m3 holds.
-__device__ __noinline__ float warp_largest_finite(float (&x)[8]) {
+// As above over the finite values: infinite ones become NaN, which e4m3 holds.
+__device__ __forceinline__ float warp_largest_finite(Vals<8> &x) {
+  const float t = warp_largest(x);
+  if (!isinf(t)) return t;
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (isinf(x[k])) x[k] = __uint_as_float(0x7fffffffu);
+  for (int k = 0; k < 4; ++k) {
+    if (isinf(x.p[k].x)) x.p[k].x = __uint_as_float(0x7fffffffu);
+    if (isinf(x.p[k].y)) x.p[k].y = __uint_as_float(0x7fffffffu);
+  }
   return warp_largest(x);
 }
 
 // The update of one block: 8 elements per lane. Every rounding is spelled out, so that each way of loading the elements
-// gives the same bits. pf: weights in and out; gf: gradients; cm, cr: codes in and out; s: scales in and out.
-__device__ __forceinline__ void update(float (&pf)[8], float (&gf)[8], uint2 &cm, uint2 &cr, float2 &s,
-                                       const AdamwConst &c) {
+// gives the same bits. w: weights in and out; g: gradients; cm, cr: codes in and out; s: scales in and out.
+__device__ __forceinline__ void update(Vals<8> &w, Vals<8> &g, uint2 &cm, uint2 &cr, float2 &s, const AdamwConst &c) {
   if (c.l2) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) gf[k] = fmaf(c.l2_wd, pf[k], gf[k]);
+    for (int k = 0; k < 4; ++k) g.p[k] = __ffma2_rn(both(c.l2_wd), w.p[k], g.p[k]);
   }
-  float m[8], r[8];
-  const float km = __fmul_rn(s.x, c.beta1), kr = __fmul_rn(__fmul_rn(s.y, s.y), c.beta2);
+  Vals<8> m, r;
+  const float2 km = both(__fmul_rn(s.x, c.beta1)), kr = both(__fmul_rn(__fmul_rn(s.y, s.y), c.beta2));
 #pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    const unsigned wm = k < 4 ? cm.x : cm.y, wr = k < 4 ? cr.x : cr.y;
-    const float2 dm = decode2(static_cast<unsigned short>(wm >> (8 * (k & 2))));
-    const float2 dr = decode2(static_cast<unsigned short>(wr >> (8 * (k & 2))));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float g = gf[k + e], q = e ? dr.y : dr.x;
-      m[k + e] = fmaf(km, e ? dm.y : dm.x, __fmul_rn(c.one_minus_beta1, g));
-      const float v = fmaf(kr, __fmul_rn(q, q), __fmul_rn(__fmul_rn(c.one_minus_beta2, g), g));
-      r[k + e] = __fsqrt_rn(v);
-    }
+  for (int k = 0; k < 4; ++k) {
+    const int shift = 16 * (k & 1);
+    const float2 q = decode2((k < 2 ? cr.x : cr.y) >> shift);
+    m.p[k] = __ffma2_rn(km, decode2((k < 2 ? cm.x : cm.y) >> shift), __fmul2_rn(both(c.one_minus_beta1), g.p[k]));
+    r.p[k] = root2(__ffma2_rn(kr, __fmul2_rn(q, q), __fmul2_rn(__fmul2_rn(both(c.one_minus_beta2), g.p[k]), g.p[k])));
+    const float2 d = __ffma2_rn(r.p[k], both(c.inv_sqrt_bc2), both(c.eps));
+    w.p[k] = __ffma2_rn(both(-c.step_size), make_float2(quick_divide(m.p[k].x, d.x), quick_divide(m.p[k].y, d.y)),
+                        __fmul2_rn(w.p[k], both(c.decay)));
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    pf[k] = fmaf(-c.step_size, __fdiv_rn(m[k], fmaf(r[k], c.inv_sqrt_bc2, c.eps)), __fmul_rn(pf[k], c.decay));
-  float tm = warp_largest(m), tr = warp_largest(r);
-  if (isinf(tm)) tm = warp_largest_finite(m);
-  if (isinf(tr)) tr = warp_largest_finite(r);
-  tm = fmaxf(tm, FLOOR);
-  tr = fmaxf(tr, FLOOR);
-  const float im = __fdiv_rn(TOP, tm), ir = __fdiv_rn(TOP, tr);
+  const float tm = fmaxf(warp_largest_finite(m), FLOOR), tr = fmaxf(warp_largest_finite(r), FLOOR);
+  const float2 im = both(__fmul_rn(TOP, __frcp_rn(tm))), ir = both(__fmul_rn(TOP, __frcp_rn(tr)));
   s = make_float2(__fmul_rn(tm, 1.f / TOP), __fmul_rn(tr, 1.f / TOP));
+  unsigned em[4], er[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    m[k] = __fmul_rn(m[k], im);
-    const float y = __fmul_rn(r[k], ir);
-    r[k] = r[k] > 0.f ? fmaxf(y, LEAST) : y;
+  for (int k = 0; k < 4; ++k) {
+    em[k] = encode2(__fmul2_rn(m.p[k], im));
+    float2 y = __fmul2_rn(r.p[k], ir);
+    if (r.p[k].x > 0.f) y.x = fmaxf(y.x, LEAST);
+    if (r.p[k].y > 0.f) y.y = fmaxf(y.y, LEAST);
+    er[k] = encode2(y);
   }
-  cm.x = encode2(m[0], m[1]) | encode2(m[2], m[3]) << 16;
-  cm.y = encode2(m[4], m[5]) | encode2(m[6], m[7]) << 16;
-  cr.x = encode2(r[0], r[1]) | encode2(r[2], r[3]) << 16;
-  cr.y = encode2(r[4], r[5]) | encode2(r[6], r[7]) << 16;
+  cm = make_uint2(em[0] | em[1] << 16, em[2] | em[3] << 16);
+  cr = make_uint2(er[0] | er[1] << 16, er[2] | er[3] << 16);
 }
 
-// Blocks [b0, b1) of a tensor by one warp. Lane l of a full block of aligned arrays has its elements 8 l .. 8 l + 7, else
-// elements l, l + 32, ...: the sums over a block are maxima, so both give the same bits.
+// A full block of aligned arrays as it lies in memory: lane l has elements 8 l .. 8 l + 7. W: the weights that take the
+// update.
+template <typename W, typename GT>
+struct Block8 {
+  Raw<W, 8> w;
+  Raw<GT, 8> g;
+  uint2 cm, cr;
+  float2 s;
+  __device__ __forceinline__ void load(const Tensor8 &d, const W *weights, long long b, int lane) {
+    const long long o = b * BLOCK + 8 * lane;
+    w.load(weights + o);
+    g.load(static_cast<const GT *>(d.g) + o);
+    cm = *reinterpret_cast<const uint2 *>(d.m + o);
+    cr = *reinterpret_cast<const uint2 *>(d.r + o);
+    s = d.scales[b];
+  }
+};
+
+// Blocks b, b + stride, ... of a tensor by one warp; returns the first that is past its end. Full blocks of aligned arrays
+// are loaded one turn ahead; a lane of any other has elements l, l + 32, ...: the sums over a block are maxima, so both give
+// the same bits.
 template <typename PT, typename GT, bool MASTER>
-__device__ __forceinline__ void span(const Tensor8 &d, long long b0, long long b1, int lane) {
+__device__ __forceinline__ long long span(const Tensor8 &d, long long b, long long stride, int lane) {
+  using W = typename std::conditional<MASTER, float, PT>::type;
+  W *weights = MASTER ? reinterpret_cast<W *>(d.master) : static_cast<W *>(d.p);
   PT *p = static_cast<PT *>(d.p);
   const GT *g = static_cast<const GT *>(d.g);
   uint8_t *m = d.m, *r = d.r;
-  float *ms = d.master;
-  const long long n = d.n;
+  const long long n = d.n, end = (n + BLOCK - 1) / BLOCK, whole = d.vec ? n / BLOCK : 0;
+  if (b < whole) {
+    Block8<W, GT> next;
+    next.load(d, weights, b, lane);
 #pragma unroll 1
-  for (long long b = b0; b < b1; ++b) {
-    float pf[8], gf[8];
-    uint2 cm, cr;
+    do {
+      Block8<W, GT> x = next;
+      const long long o = b * BLOCK + 8 * lane, at = b;
+      b += stride;
+      if (b < whole) next.load(d, weights, b, lane);
+      Vals<8> w = x.w.get(), gv = x.g.get();
+      update(w, gv, x.cm, x.cr, x.s, d.c);
+      if constexpr (MASTER) store_vals(weights + o, w);
+      store_vals(p + o, w);
+      *reinterpret_cast<uint2 *>(m + o) = x.cm;
+      *reinterpret_cast<uint2 *>(r + o) = x.cr;
+      if (lane == 0) d.scales[at] = x.s;
+    } while (b < whole);
+  }
+#pragma unroll 1
+  for (; b < end; b += stride) {
+    const long long o = b * BLOCK + lane;
+    Vals<8> w, gv;
+    uint2 cm = make_uint2(0u, 0u), cr = cm;
     float2 s = d.scales[b];
-    if (d.vec && (b + 1) * BLOCK <= n) {
-      const long long o = b * BLOCK + 8 * lane;
-      if constexpr (MASTER) load8(ms + o, pf);
-      else load8(p + o, pf);
-      load8(g + o, gf);
-      cm = *reinterpret_cast<const uint2 *>(m + o);
-      cr = *reinterpret_cast<const uint2 *>(r + o);
-      update(pf, gf, cm, cr, s, d.c);
-      if constexpr (MASTER) store8(ms + o, pf);
-      store8(p + o, pf);
-      *reinterpret_cast<uint2 *>(m + o) = cm;
-      *reinterpret_cast<uint2 *>(r + o) = cr;
-    } else {
-      const long long o = b * BLOCK + lane;
-      cm = cr = make_uint2(0u, 0u);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const long long i = o + 32 * k;
-        const bool in = i < n;
-        pf[k] = !in ? 0.f : MASTER ? ms[i] : load1(p, i);
-        gf[k] = in ? load1(g, i) : 0.f;
-        const unsigned um = in ? m[i] : 0u, ur = in ? r[i] : 0u;
-        (k < 4 ? cm.x : cm.y) |= um << (8 * (k & 3));
-        (k < 4 ? cr.x : cr.y) |= ur << (8 * (k & 3));
-      }
-      update(pf, gf, cm, cr, s, d.c);
+    for (int k = 0; k < 8; ++k) {
+      const long long i = o + 32 * k;
+      const bool in = i < n;
+      (k & 1 ? w.p[k / 2].y : w.p[k / 2].x) = in ? load1(weights, i) : 0.f;
+      (k & 1 ? gv.p[k / 2].y : gv.p[k / 2].x) = in ? load1(g, i) : 0.f;
+      (k < 4 ? cm.x : cm.y) |= (in ? m[i] : 0u) << (8 * (k & 3));
+      (k < 4 ? cr.x : cr.y) |= (in ? r[i] : 0u) << (8 * (k & 3));
+    }
+    update(w, gv, cm, cr, s, d.c);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const long long i = o + 32 * k;
-        if (i >= n) continue;
-        if constexpr (MASTER) ms[i] = pf[k];
-        store1(p, i, pf[k]);
-        m[i] = static_cast<uint8_t>((k < 4 ? cm.x : cm.y) >> (8 * (k & 3)));
-        r[i] = static_cast<uint8_t>((k < 4 ? cr.x : cr.y) >> (8 * (k & 3)));
-      }
+    for (int k = 0; k < 8; ++k) {
+      const long long i = o + 32 * k;
+      if (i >= n) continue;
+      const float x = k & 1 ? w.p[k / 2].y : w.p[k / 2].x;
+      if constexpr (MASTER) store1(weights, i, x);
+      store1(p, i, x);
+      m[i] = static_cast<uint8_t>((k < 4 ? cm.x : cm.y) >> (8 * (k & 3)));
+      r[i] = static_cast<uint8_t>((k < 4 ? cr.x : cr.y) >> (8 * (k & 3)));
     }
     if (lane == 0) d.scales[b] = s;
   }
+  return b;
 }
 
-__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) adamw8_kernel(const __grid_constant__ Group8 G) {
+// Warps take the launch's blocks in turn, so that those in flight at any time lie next to each other.
+template <bool WIDE>
+__global__ void __launch_bounds__(THREADS, WIDE ? WIDE_BLOCKS : NARROW_BLOCKS) adamw8_kernel(const __grid_constant__ Group8 G) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const int lane = threadIdx.x % 32;
-  const long long warp = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32;
-  const long long stride = static_cast<long long>(gridDim.x) * (THREADS / 32) * G.chunk;
-  for (long long first = warp * G.chunk; first < G.total_blocks; first += stride) {
-    const long long last = min(first + G.chunk, G.total_blocks);
-    int lo = 0, hi = G.ntensors - 1;   // the last tensor that begins at or before `first`
+  const long long stride = static_cast<long long>(gridDim.x) * (THREADS / 32);
+  long long b = static_cast<long long>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32;
+  while (b < G.total_blocks) {
+    int lo = 0, hi = G.ntensors - 1;   // the last tensor that begins at or before b
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (G.t[mid].block_begin <= first) lo = mid;
+      if (G.t[mid].block_begin <= b) lo = mid;
       else hi = mid - 1;
     }
-    for (long long b = first; b < last; ++lo) {
-      const Tensor8 &d = G.t[lo];
-      const long long b0 = b - d.block_begin, b1 = min(last - d.block_begin, (d.n + BLOCK - 1) / BLOCK);
-      if (d.master != nullptr) {
-        if (d.gdt == MUON_F32) span<__nv_bfloat16, float, true>(d, b0, b1, lane);
-        else span<__nv_bfloat16, __nv_bfloat16, true>(d, b0, b1, lane);
-      } else if (d.pdt == MUON_F32) {
-        if (d.gdt == MUON_F32) span<float, float, false>(d, b0, b1, lane);
-        else span<float, __nv_bfloat16, false>(d, b0, b1, lane);
-      } else {
-        if (d.gdt == MUON_F32) span<__nv_bfloat16, float, false>(d, b0, b1, lane);
-        else span<__nv_bfloat16, __nv_bfloat16, false>(d, b0, b1, lane);
-      }
-      b = d.block_begin + b1;
+    const Tensor8 &d = G.t[lo];
+    long long own = b - d.block_begin;
+    if constexpr (!WIDE) {
+      own = span<__nv_bfloat16, __nv_bfloat16, false>(d, own, stride, lane);
+    } else if (d.master != nullptr) {
+      if (d.gdt == MUON_F32) own = span<__nv_bfloat16, float, true>(d, own, stride, lane);
+      else own = span<__nv_bfloat16, __nv_bfloat16, true>(d, own, stride, lane);
+    } else if (d.pdt == MUON_F32) {
+      if (d.gdt == MUON_F32) own = span<float, float, false>(d, own, stride, lane);
+      else own = span<float, __nv_bfloat16, false>(d, own, stride, lane);
+    } else {
+      own = span<__nv_bfloat16, float, false>(d, own, stride, lane);
     }
+    b = d.block_begin + own;
   }
 }
 
@@ -224,30 +264,41 @@ muon_status check_tensor8(const adamw8_tensor &x) {
   return MUON_OK;
 }
 
-}  // namespace
-}  // namespace muon
+// Constants of a call's tensors, most of which share their hyperparameters: two powers each otherwise.
+class Constants {
+  adamw_hparams hp_{};
+  AdamwConst c_{};
+  bool any_ = false;
 
-using namespace muon;
+ public:
+  muon_status get(const adamw_hparams *hp, AdamwConst *out) {
+    if (!any_ || memcmp(hp, &hp_, sizeof(hp_)) != 0) {
+      const muon_status st = adamw_constants(hp, &c_);
+      if (st != MUON_OK) return st;
+      hp_ = *hp;
+      any_ = true;
+    }
+    *out = c_;
+    return MUON_OK;
+  }
+};
 
-extern "C" {
+bool is_wide(const adamw8_tensor &x) { return x.master != nullptr || x.pdt == MUON_F32 || x.gdt == MUON_F32; }
 
-muon_status adamw8_step_grouped(const adamw8_tensor *tensors, int64_t n, muon_stream_t stream) {
-  if (tensors == nullptr || n < 1 || n > (1 << 20)) return MUON_ERR_INVALID_ARG;
-  muon_status st;
-  AdamwConst c{};
-  for (int64_t i = 0; i < n; ++i)
-    if ((st = check_tensor8(tensors[i])) != MUON_OK || (st = adamw_constants(tensors[i].hp, &c)) != MUON_OK) return st;
-  if ((st = device_check()) != MUON_OK) return st;
-  const long long warps = static_cast<long long>(device_sm_count()) * BLOCKS_PER_SM * (THREADS / 32);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+// The tensors of one kind, ADAMW_GROUP_MAX a launch.
+template <bool WIDE>
+muon_status launch_kind(const adamw8_tensor *tensors, int64_t n, cudaStream_t s) {
+  constexpr int PER_SM = WIDE ? WIDE_BLOCKS : NARROW_BLOCKS;
   Group8 G;
+  Constants constants;
   for (int64_t i = 0; i < n;) {
     G.ntensors = 0;
     G.total_blocks = 0;
     for (; i < n && G.ntensors < ADAMW_GROUP_MAX; ++i) {
       const adamw8_tensor &x = tensors[i];
+      if (is_wide(x) != WIDE) continue;
       Tensor8 &d = G.t[G.ntensors++];
-      adamw_constants(x.hp, &d.c);
+      constants.get(x.hp, &d.c);   // checked by the caller
       d.p = x.param;
       d.g = x.grad;
       d.m = static_cast<uint8_t *>(x.exp_avg);
@@ -262,16 +313,35 @@ muon_status adamw8_step_grouped(const adamw8_tensor *tensors, int64_t n, muon_st
               aligned(x.exp_avg_sq, 8);
       G.total_blocks += (x.n + BLOCK - 1) / BLOCK;
     }
-    // a few turns per warp, so that the last one is a small part of the pass
-    G.chunk = static_cast<int>(std::min(8ll, std::max(1ll, G.total_blocks / (8 * warps))));
-    const long long turns = (G.total_blocks + G.chunk - 1) / G.chunk;
-    const long long blocks = std::min(warps / (THREADS / 32), (turns + THREADS / 32 - 1) / (THREADS / 32));
+    if (G.ntensors == 0) break;
+    const long long blocks = std::min<long long>(static_cast<long long>(device_sm_count()) * PER_SM,
+                                                 (G.total_blocks + THREADS / 32 - 1) / (THREADS / 32));
     launch_begin(KK_ADAMW8, s);
-    const cudaError_t e = launch_pdl(adamw8_kernel, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), 0, s, G);
+    const cudaError_t e = launch_pdl(adamw8_kernel<WIDE>, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), 0, s, G);
     launch_end(s);
     if (e != cudaSuccess) return MUON_ERR_CUDA;
   }
   return MUON_OK;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status adamw8_step_grouped(const adamw8_tensor *tensors, int64_t n, muon_stream_t stream) {
+  if (tensors == nullptr || n < 1 || n > (1 << 20)) return MUON_ERR_INVALID_ARG;
+  muon_status st;
+  AdamwConst c{};
+  Constants constants;
+  for (int64_t i = 0; i < n; ++i)
+    if ((st = check_tensor8(tensors[i])) != MUON_OK || (st = constants.get(tensors[i].hp, &c)) != MUON_OK) return st;
+  if ((st = device_check()) != MUON_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = launch_kind<false>(tensors, n, s)) != MUON_OK) return st;
+  return launch_kind<true>(tensors, n, s);
 }
 
 }  // extern "C"

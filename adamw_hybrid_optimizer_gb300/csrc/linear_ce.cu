@@ -50,6 +50,10 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr long long PIECE_ELEMS = 1ll << 30; // dz elements of a piece
 constexpr long long PAIRS = 76;              // SM pairs of a GB300: slices are counted by it, so that sums have one order
 constexpr int MAX_SPLIT = 64;
+// An accumulator of the tensor cores loses up to a unit in the last place with each step of 16 products, always towards
+// zero: over a long contraction that is 2e-5 of the result. For fp32 gradients it adds up 64 64-deep steps, and the
+// epilogue adds that to what the output holds.
+constexpr int SEGMENT = 64;
 
 enum Kind : int { LOGITS = 0, DLOGITS = 1, DH = 2, DW = 3 };
 
@@ -70,6 +74,7 @@ struct CeArgs {
   int m_pairs, n_tiles;
   int k_iters, k_wrap;                 // 64-deep steps; from k_wrap on A's second plane and B again (two terms of dz)
   int split, k_per;
+  int k_seg;                           // steps that one accumulator adds up before they join the output
   int planes;                          // DLOGITS: terms of dz
   long long total;                     // tile pairs times slices
   // LOGITS, DLOGITS
@@ -240,7 +245,7 @@ __device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec
 // One tile's part of a warp as rows of the output: 32 rows of 32 fp32 values at a time through the staging buffer, so that
 // eight lanes write 128 bytes of a row (64 as bf16).
 __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
-                                             uint8_t *buf) {
+                                             uint8_t *buf, bool accumulate) {
   if (warp_row0 >= a.rows) return;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -266,7 +271,7 @@ __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int
         if (warp_row0 + i < a.rows)
           store_piece<float, 4>(static_cast<float *>(a.out) + slice * a.slice_stride +
                                     static_cast<long long>(warp_row0 + i) * a.ld_out + c0 + 4 * q,
-                                f, left0 - 4 * q, a.vec, a.accumulate);
+                                f, left0 - 4 * q, a.vec, accumulate);
       }
     } else {
 #pragma unroll
@@ -278,7 +283,7 @@ __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int
         if (warp_row0 + i < a.rows)
           store_piece<__nv_bfloat16, 8>(static_cast<__nv_bfloat16 *>(a.out) +
                                             static_cast<long long>(warp_row0 + i) * a.ld_out + c0 + 8 * q,
-                                        f, left0 - 8 * q, a.vec, a.accumulate);
+                                        f, left0 - 8 * q, a.vec, accumulate);
       }
     }
   }
@@ -377,37 +382,43 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true, issued = false;
       for (long long u = first; ok && u < args.total; u += stride) {
-        if (!wait_bounded(&ctrl->acc_empty[acc], acc_phase ^ 1u, ctl, ERR_WAIT_ACC_EMPTY)) break;
-        tc_fence_after();
         int slice, ti, tj;
         decode(args, u, slice, ti, tj);
         const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
-        for (int kk = k0; kk < k1; ++kk) {
-          if (!wait_bounded(&ctrl->full[stage], phase, ctl, ERR_WAIT_FULL)) {
+        for (int ks = k0; ok && ks < k1; ks += args.k_seg) {
+          if (!wait_bounded(&ctrl->acc_empty[acc], acc_phase ^ 1u, ctl, ERR_WAIT_ACC_EMPTY)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES;
+          const int ke = min(k1, ks + args.k_seg);
+          for (int kk = ks; kk < ke; ++kk) {
+            if (!wait_bounded(&ctrl->full[stage], phase, ctl, ERR_WAIT_FULL)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES;
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) {
-            const uint64_t adesc =
-                A_MN ? smem_desc_sw128(sa + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sa + k * 32, 16, 1024);
-            const uint64_t bdesc =
-                B_MN ? smem_desc_sw128(sb + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sb + k * 32, 16, 1024);
-            tc_mma_bf16_pair(tmem_base + acc * BN, adesc, bdesc, idesc, ((kk - k0) | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint64_t adesc =
+                  A_MN ? smem_desc_sw128(sa + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sa + k * 32, 16, 1024);
+              const uint64_t bdesc =
+                  B_MN ? smem_desc_sw128(sb + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sb + k * 32, 16, 1024);
+              tc_mma_bf16_pair(tmem_base + acc * BN, adesc, bdesc, idesc, ((kk - ks) | k) != 0 ? 1u : 0u);
+            }
+            issued = true;
+            tc_commit_pair_mc(&ctrl->empty[stage], 0x3);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          issued = true;
-          tc_commit_pair_mc(&ctrl->empty[stage], 0x3);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (!ok) break;
+          tc_commit_pair_mc(&ctrl->acc_full[acc], 0x3);
+          acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
         }
-        if (!ok) break;
-        tc_commit_pair_mc(&ctrl->acc_full[acc], 0x3);
-        acc ^= 1u;
-        if (acc == 0) acc_phase ^= 1u;
       }
       if (issued) {   // all MMAs have completed before tensor memory is released
         tc_commit_pair_mc(&ctrl->drain, 0x1);
@@ -420,22 +431,27 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
     const int half = (warp - 2) / 4;         // 128 of the tile's 256 columns
     uint8_t *buf = staging + (warp - 2) * BUF_BYTES;
     uint32_t acc = 0, acc_phase = 0;
-    for (long long u = first; u < args.total; u += stride) {
+    bool ok = true;
+    for (long long u = first; ok && u < args.total; u += stride) {
       int slice, ti, tj;
       decode(args, u, slice, ti, tj);
-      const bool ok = wait_bounded(&ctrl->acc_full[acc], acc_phase, ctl, ERR_WAIT_ACC_FULL);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
+      const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
       const int warp_row0 = (2 * ti + rank) * BM + lane_base, col0 = tj * BN + 128 * half;
-      const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 128 * half;
-      if constexpr (KIND == LOGITS) epilogue_logits(args, tmem, warp_row0 + lane, col0, 2 * tj + half);
-      else if constexpr (KIND == DLOGITS) epilogue_dlogits(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
-      else epilogue_out(args, tmem, slice, warp_row0, col0, lane, buf);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(leader_acc_empty0 + acc * static_cast<uint32_t>(sizeof(uint64_t)));
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+      for (int ks = k0; ks < k1; ks += args.k_seg) {
+        ok = wait_bounded(&ctrl->acc_full[acc], acc_phase, ctl, ERR_WAIT_ACC_FULL);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 128 * half;
+        if constexpr (KIND == LOGITS) epilogue_logits(args, tmem, warp_row0 + lane, col0, 2 * tj + half);
+        else if constexpr (KIND == DLOGITS) epilogue_dlogits(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
+        else epilogue_out(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(leader_acc_empty0 + acc * static_cast<uint32_t>(sizeof(uint64_t)));
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
     }
     if (KIND == DLOGITS && lane == 0) bulk_wait_group_all();
   }
@@ -653,6 +669,7 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   if (a.split < 1) a.split = 1;
   a.k_per = static_cast<int>(ceil_div(a.k_iters, a.split));
   a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
+  a.k_seg = a.out_f32 && a.planes > 1 ? SEGMENT : a.k_per;
   a.total = static_cast<long long>(a.m_pairs) * a.n_tiles * a.split;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(n, a.total)));
   launch_begin(kind, s);
