@@ -8,8 +8,10 @@
 //           of exponentials for each row and half tile (online softmax) and the target's logit
 //   combine the halves' pairs into lse and the loss
 //   rows    h without the rows that have no part in the loss, for dw
-//   dlogits the product again, dz = g w (exp(z - lse) - [v = t]) from the accumulators, rounded to bf16 as an operand of the
-//           two products that follow (for fp32 gradients: as the sum of two bf16 terms, which holds 16 bits of it)
+//   dlogits dz = g w (exp(z - lse) - [v = t]), rounded to bf16 as an operand of the two products that follow: in the joint
+//           call from the exponentials, which the logits' epilogue has kept; else from the product, computed again (a tenth
+//           of the joint call's time instead of a quarter). For fp32 gradients dz is the sum of two bf16 terms, which holds
+//           16 bits of it, and always from the product
 //   dh      dz W, the contraction over V cut into slices where the tiles alone would leave SMs without work
 //   dw      dz^T h, added up over the pieces in fp32
 //   reduce  adds slices in their order and rounds once
@@ -20,6 +22,7 @@
 // wherever there are a few hundred rows, by the reading of W below that.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -55,7 +58,8 @@ constexpr int MAX_SPLIT = 64;
 // epilogue adds that to what the output holds.
 constexpr int SEGMENT = 64;
 
-enum Kind : int { LOGITS = 0, DLOGITS = 1, DH = 2, DW = 3 };
+// LOGITS leaves statistics alone, LOGITS_EXP the tile's exponentials too (for the joint call).
+enum Kind : int { LOGITS = 0, LOGITS_EXP = 1, DLOGITS = 2, DH = 3, DW = 4 };
 
 struct Ctrl {
   uint64_t full[STAGES], empty[STAGES];
@@ -69,7 +73,7 @@ constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + EPI_WARPS * 
 static_assert(SMEM <= 232448, "shared memory over budget");
 
 struct CeArgs {
-  CUtensorMap map_a, map_b, map_out;   // map_out: dz, for DLOGITS
+  CUtensorMap map_a, map_b, map_out;   // map_out: dz, the exponentials in its place, or the output
   int rows, cols;                      // of the output
   int m_pairs, n_tiles;
   int k_iters, k_wrap;                 // 64-deep steps; from k_wrap on A's second plane and B again (two terms of dz)
@@ -77,7 +81,7 @@ struct CeArgs {
   int k_seg;                           // steps that one accumulator adds up before they join the output
   int planes;                          // DLOGITS: terms of dz
   long long total;                     // tile pairs times slices
-  // LOGITS, DLOGITS
+  // LOGITS, LOGITS_EXP, DLOGITS
   const void *targets;
   int itype;
   const float *weights, *grad, *lse;
@@ -87,7 +91,7 @@ struct CeArgs {
   // DH, DW
   void *out;
   long long ld_out, slice_stride;      // elements; slice s goes to out + s * slice_stride
-  int out_f32, accumulate, vec;
+  int out_f32, accumulate, vec, tma;
   uint32_t *err;
   unsigned long long timeout_ns;
 };
@@ -127,43 +131,78 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
   return *reinterpret_cast<const unsigned *>(&h);
 }
 
-// One tile's part of a warp (128 columns from col0) as a running maximum and sum of exponentials per row.
-__device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, int row, int col0, int part) {
-  long long t = -1;
-  if (row < a.rows) t = target_of(a.targets, a.itype, row);
-  float m = -INFINITY, s = 0.f;
-#pragma unroll 1
+__device__ __forceinline__ unsigned pack2_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const unsigned *>(&h);
+}
+
+// One tile's part of a warp (128 columns from col0) as its maximum and the sum of its exponentials relative to that, for
+// each row; with KEEP the exponentials too, in fp16: none is above 1, so 2^-12 of each is kept, or 2^-25 of the largest.
+template <bool KEEP>
+__device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, int row, int warp_row0, int col0, int part,
+                                                int lane, uint8_t *buf) {
+  if (col0 >= a.cols || warp_row0 >= a.rows) return;
+  const long long t = row < a.rows ? target_of(a.targets, a.itype, row) - col0 : -1;
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  const int left = a.cols - col0;   // columns that there are
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int c0 = col0 + 32 * c;
-    if (c0 >= a.cols) break;
     float v[32];
     __syncwarp();
     tmem_ld_32x32b_x32(tmem + 32 * c, v);
-    const long long hit = t - c0;
+    if (32 * c + 32 <= left) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) top[j & 3] = 32 * c + j < left ? fmaxf(top[j & 3], v[j]) : top[j & 3];
+    }
+    const long long hit = t - 32 * c;
     if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
       float z = 0.f;
 #pragma unroll
       for (int j = 0; j < 32; ++j) z = hit == j ? v[j] : z;
-      if (hit >= 0 && hit < 32 && c0 + hit < a.cols) a.z_target[row] = z;
+      if (hit >= 0 && hit < 32 && t < left) a.z_target[row] = z;
     }
-    if (c0 + 32 > a.cols) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = c0 + j < a.cols ? v[j] : -INFINITY;
-    }
-    float top[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top[j] = fmaxf(v[j], v[j + 4]);
-#pragma unroll
-    for (int j = 8; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
-    const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-    const float ref = mn == -INFINITY ? 0.f : mn * LOG2E;   // nothing above -inf so far: exponentials of zero
-    float sum[4] = {s * exp2_fast(fmaf(m, LOG2E, -ref)), 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_fast(fmaf(v[j], LOG2E, -ref));
-    s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    m = mn;
   }
-  if (row < a.rows && col0 < a.cols) a.partials[static_cast<long long>(part) * a.rows + row] = make_float2(m, s);
+  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  const float ref = m == -INFINITY ? 0.f : m * LOG2E;   // nothing above -inf: exponentials of zero
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(tmem + 32 * c, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
+    if (32 * c + 32 > left) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 32 * c + j < left ? v[j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) sum[j & 3] += v[j];
+    if constexpr (KEEP) {
+      if (c % 2 == 0) {
+        if (lane == 0) bulk_wait_group_read<0>();   // the buffer's last store has read it
+        __syncwarp();
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *piece(buf, lane, 4 * (c & 1) + q) =
+            make_uint4(pack2_half(v[8 * q], v[8 * q + 1]), pack2_half(v[8 * q + 2], v[8 * q + 3]),
+                       pack2_half(v[8 * q + 4], v[8 * q + 5]), pack2_half(v[8 * q + 6], v[8 * q + 7]));
+      if (c % 2 == 1) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0 && 32 * (c - 1) < left) {
+          tma_store_3d(&a.map_out, buf, col0 + 32 * (c - 1), warp_row0, 0);
+          bulk_commit_group();
+        }
+      }
+    }
+  }
+  if (row < a.rows)
+    a.partials[static_cast<long long>(part) * a.rows + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 // One tile's part of a warp as dz, in bf16 terms, through the staging buffer and TMA (which leaves out what lies past the
@@ -242,8 +281,46 @@ __device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec
   }
 }
 
-// One tile's part of a warp as rows of the output: 32 rows of 32 fp32 values at a time through the staging buffer, so that
-// eight lanes write 128 bytes of a row (64 as bf16).
+// One tile's part of a warp as rows of the output: lines of 128 bytes (64 bf16 or 32 fp32 values) through the staging
+// buffer and TMA where the output's rows are 16-byte aligned and nothing is added to. Else 32 columns of fp32 at a time
+// through the buffer, so that eight lanes write 128 bytes of a row (64 as bf16).
+__device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
+                                                 uint8_t *buf) {
+  if (warp_row0 >= a.rows) return;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int c0 = col0 + 32 * c;
+    if (c0 >= a.cols) break;
+    float v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(tmem + 32 * c, v);
+    if (a.out_f32 || c % 2 == 0) {
+      if (lane == 0) bulk_wait_group_read<0>();   // the buffer's last store has read it
+      __syncwarp();
+    }
+    if (a.out_f32) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *piece(buf, lane, q) = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                          __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *piece(buf, lane, 4 * (c & 1) + q) = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                                                        pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+    }
+    if (a.out_f32 || c % 2 == 1 || c0 + 32 >= a.cols) {
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        // the map counts 2-byte elements: an fp32 column is two of them
+        tma_store_3d(&a.map_out, buf, a.out_f32 ? 2 * c0 : c0 - 32 * (c & 1), warp_row0, slice);
+        bulk_commit_group();
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
                                              uint8_t *buf, bool accumulate) {
   if (warp_row0 >= a.rows) return;
@@ -289,7 +366,7 @@ __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int
   }
 }
 
-// A: LOGITS, DLOGITS h (K-major), DH dz (K-major), DW dz (MN-major: dz^T). B: LOGITS, DLOGITS W (K-major), DH W and DW h
+// A: h (K-major) for the logits, DH dz (K-major), DW dz (MN-major: dz^T). B: W (K-major) for the logits, DH W and DW h
 // (MN-major). An MN-major operand is loaded as boxes of 64 columns x 64 steps.
 template <int KIND>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeArgs args) {
@@ -443,8 +520,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
         if (!ok) break;
         tc_fence_after();
         const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 128 * half;
-        if constexpr (KIND == LOGITS) epilogue_logits(args, tmem, warp_row0 + lane, col0, 2 * tj + half);
+        if constexpr (KIND == LOGITS || KIND == LOGITS_EXP)
+          epilogue_logits<KIND == LOGITS_EXP>(args, tmem, warp_row0 + lane, warp_row0, col0, 2 * tj + half, lane, buf);
         else if constexpr (KIND == DLOGITS) epilogue_dlogits(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
+        else if (args.tma) epilogue_out_tma(args, tmem, slice, warp_row0, col0, lane, buf);
         else epilogue_out(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
         tc_fence_before();
         __syncwarp();
@@ -453,7 +532,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
         if (acc == 0) acc_phase ^= 1u;
       }
     }
-    if (KIND == DLOGITS && lane == 0) bulk_wait_group_all();
+    if (lane == 0) bulk_wait_group_all();
   }
 
   // neither CTA leaves while the other may still signal it
@@ -477,13 +556,15 @@ struct CombineArgs {
   float *losses, *lse;
 };
 
-// 32 rows per block, a lane each; eight warps share the parts. lse = m + log(sum of s_p exp(m_p - m)).
+// Eight rows per block, whose pairs of one part fill a 32-byte sector; 32 threads share a row's parts.
+// lse = m + log(sum of s_p exp(m_p - m)).
+constexpr int COMBINE_ROWS = 8;
 __global__ void __launch_bounds__(256) ce_combine_kernel(const CombineArgs a) {
-  __shared__ float2 sh[8][32];
+  __shared__ float2 sh[8][COMBINE_ROWS];
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int row = blockIdx.x * 32 + lane;
+  const int own = threadIdx.x % COMBINE_ROWS, stream = threadIdx.x / COMBINE_ROWS;
+  const int row = blockIdx.x * COMBINE_ROWS + own;
   float m = -INFINITY, s = 0.f;
   auto join = [&](float2 p) {
     const float mn = fmaxf(m, p.x);
@@ -492,19 +573,82 @@ __global__ void __launch_bounds__(256) ce_combine_kernel(const CombineArgs a) {
     m = mn;
   };
   if (row < a.rows) {
-#pragma unroll 4
-    for (int p = warp; p < a.parts; p += 8) join(a.partials[static_cast<long long>(p) * a.rows + row]);
+    const float2 *src = a.partials + row;
+    int p = stream;
+    for (; p + 7 * 32 < a.parts; p += 8 * 32) {
+      float2 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = src[static_cast<long long>(p + 32 * k) * a.rows];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) join(x[k]);
+    }
+    for (; p < a.parts; p += 32) join(src[static_cast<long long>(p) * a.rows]);
   }
-  sh[warp][lane] = make_float2(m, s);
+#pragma unroll
+  for (int o = COMBINE_ROWS; o < 32; o *= 2)
+    join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+  if (threadIdx.x % 32 < COMBINE_ROWS) sh[threadIdx.x / 32][own] = make_float2(m, s);
   __syncthreads();
-  if (warp > 0 || row >= a.rows) return;
-  for (int w = 1; w < 8; ++w) join(sh[w][lane]);
+  if (threadIdx.x >= COMBINE_ROWS || row >= a.rows) return;
+  for (int w = 1; w < 8; ++w) join(sh[w][own]);
   const long long t = target_of(a.targets, a.itype, row);
   const float w = a.weights != nullptr ? a.weights[row] : 1.f;
   const bool live = t >= 0 && t < a.V && w != 0.f;
   const float lse = m + logf(s);
   a.lse[row] = live ? lse : 0.f;
   a.losses[row] = live ? w * (lse - a.z_target[row]) : 0.f;
+}
+
+struct ScaleArgs {
+  uint16_t *x;                 // exponentials in, dz out: rows of ld elements
+  long long ld;
+  const float2 *partials;
+  const float *weights, *lse;
+  const void *targets;
+  int itype, rows, V;
+  float grad_scale;
+};
+
+// dz from the kept exponentials, in their place: dz = g w (exp(m_part - lse) e - [v = t]). A block takes SCALE_ROWS rows of
+// 2048 columns, 8 columns of each row per thread: the rows' maxima lie next to each other. Bound by HBM.
+constexpr int SCALE_ROWS = 4;
+__global__ void __launch_bounds__(256) ce_scale_kernel(const ScaleArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  const int c0 = blockIdx.y * 2048 + 8 * static_cast<int>(threadIdx.x);
+  if (c0 >= a.V) return;
+  const long long r0 = static_cast<long long>(blockIdx.x) * SCALE_ROWS;
+  const int n = static_cast<int>(min(static_cast<long long>(SCALE_ROWS), a.rows - r0));
+  uint4 e[SCALE_ROWS];
+  float m[SCALE_ROWS];
+#pragma unroll
+  for (int i = 0; i < SCALE_ROWS; ++i) {
+    if (i >= n) break;
+    e[i] = __ldcs(reinterpret_cast<const uint4 *>(a.x + (r0 + i) * a.ld + c0));
+    m[i] = a.partials[static_cast<long long>(c0 / (BN / 2)) * a.rows + r0 + i].x;
+  }
+#pragma unroll
+  for (int i = 0; i < SCALE_ROWS; ++i) {
+    if (i >= n) break;
+    const long long row = r0 + i, t = target_of(a.targets, a.itype, row);
+    const float w = a.weights != nullptr ? a.weights[row] : 1.f;
+    const bool live = t >= 0 && t < a.V && w != 0.f;
+    const float g = w * a.grad_scale, f = g * exp2_fast((m[i] - a.lse[row]) * LOG2E);
+    float v[8];
+    const unsigned in[4] = {e[i].x, e[i].y, e[i].z, e[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&in[k]));
+      v[2 * k] = live ? f * x.x : 0.f;
+      v[2 * k + 1] = live ? f * x.y : 0.f;
+    }
+    if (live && t - c0 >= 0 && t - c0 < 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = t - c0 == k ? v[k] - g : v[k];
+    }
+    *reinterpret_cast<uint4 *>(a.x + row * a.ld + c0) =
+        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+  }
 }
 
 struct RowsArgs {
@@ -670,6 +814,13 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   a.k_per = static_cast<int>(ceil_div(a.k_iters, a.split));
   a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
   a.k_seg = a.out_f32 && a.planes > 1 ? SEGMENT : a.k_per;
+  if (KIND == DH || KIND == DW) {   // rows and columns past the output's are not stored; slices follow each other
+    const long long e = a.out_f32 ? 2 : 1;
+    a.tma = a.vec && !a.accumulate && a.k_per <= a.k_seg;
+    if (a.tma && !make_bf16_map(&a.map_out, a.out, a.cols * e, a.rows, a.split, a.ld_out * e,
+                                (a.split > 1 ? a.slice_stride : a.ld_out * a.rows) * e, 32))
+      return MUON_ERR_CUDA;
+  }
   a.total = static_cast<long long>(a.m_pairs) * a.n_tiles * a.split;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(n, a.total)));
   launch_begin(kind, s);
@@ -748,23 +899,36 @@ muon_status run(const Call &c, cudaStream_t s) {
     if (!make_bf16_map(&a.map_a, h, c.D, rows, 1, ldh, ldh * rows, BM) ||
         !make_bf16_map(&a.map_b, c.w, c.D, c.V, 1, ldw, ldw * c.V, BN / 2))
       return MUON_ERR_CUDA;
+    // one bf16 term: the exponentials are kept in dz's place; two: the logits are computed again
+    const bool keep = c.forward && c.backward && p.planes == 1;
+    if (c.backward && !make_bf16_map(&a.map_out, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, 32)) return MUON_ERR_CUDA;
     if (c.forward) {
       CeArgs f = a;
-      if ((st = launch_gemm<LOGITS>(f, KK_CE_LOGITS, s)) != MUON_OK) return st;
+      if ((st = keep ? launch_gemm<LOGITS_EXP>(f, KK_CE_LOGITS, s) : launch_gemm<LOGITS>(f, KK_CE_LOGITS, s)) != MUON_OK)
+        return st;
       const CombineArgs cb{a.partials, a.z_target, a.weights, a.targets, a.itype, p.parts, a.rows, c.V, c.losses + r0,
                            c.lse + r0};
       launch_begin(KK_CE_COMBINE, s);
       const cudaError_t e =
-          launch_pdl(ce_combine_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(256), 0, s, cb);
+          launch_pdl(ce_combine_kernel, dim3(static_cast<unsigned>(ceil_div(rows, COMBINE_ROWS))), dim3(256), 0, s, cb);
       launch_end(s);
       if (e != cudaSuccess) return MUON_ERR_CUDA;
     }
     if (!c.backward) continue;
-    {
+    if (keep) {
+      const ScaleArgs sa{reinterpret_cast<uint16_t *>(dz), p.Vp, a.partials, a.weights, c.lse + r0, a.targets, a.itype,
+                         a.rows, static_cast<int>(c.V), c.grad_scale};
+      launch_begin(KK_CE_DLOGITS, s);
+      const cudaError_t e = launch_pdl(ce_scale_kernel,
+                                       dim3(static_cast<unsigned>(ceil_div(rows, SCALE_ROWS)),
+                                            static_cast<unsigned>(ceil_div(c.V, 2048))),
+                                       dim3(256), 0, s, sa);
+      launch_end(s);
+      if (e != cudaSuccess) return MUON_ERR_CUDA;
+    } else {
       CeArgs f = a;
       f.lse = (c.forward ? c.lse : c.lse_in) + r0;
       f.grad = c.grad != nullptr ? c.grad + r0 : nullptr;
-      if (!make_bf16_map(&f.map_out, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, 32)) return MUON_ERR_CUDA;
       if ((st = launch_gemm<DLOGITS>(f, KK_CE_DLOGITS, s)) != MUON_OK) return st;
     }
     if (c.dh != nullptr) {
