@@ -6,12 +6,10 @@
 // Rows go through in pieces of at most PIECE_ELEMS / V (plan()); nothing of size N x V outlives a piece. Per piece:
 //   logits  z a tile of 256 x 256 at a time on the tensor cores; a tile's accumulators leave as one running maximum and sum
 //           of exponentials for each row and half tile (online softmax) and the target's logit
-//   combine the halves' pairs into lse and the loss
-//   rows    h without the rows that have no part in the loss, for dw
+//   combine the parts' pairs into lse and the loss; and h without the rows that have no part in the loss, for dw
 //   dlogits dz = g w (exp(z - lse) - [v = t]), rounded to bf16 as an operand of the two products that follow: in the joint
-//           call from the exponentials, which the logits' epilogue has kept; else from the product, computed again (a tenth
-//           of the joint call's time instead of a quarter). For fp32 gradients dz is the sum of two bf16 terms, which holds
-//           16 bits of it, and always from the product
+//           call from the exponentials, which the logits' epilogue has kept; else from the product, computed again. For fp32
+//           gradients dz is the sum of two bf16 terms, which holds 16 bits of it, and always from the product
 //   dh      dz W, the contraction over V cut into slices where the tiles alone would leave SMs without work
 //   dw      dz^T h, added up over the pieces in fp32
 //   reduce  adds slices in their order and rounds once
@@ -38,20 +36,24 @@ namespace muon {
 namespace {
 
 constexpr int BM = 128;                      // accumulator rows per CTA: 256 per pair
-constexpr int BN = 256;
 constexpr int BK = 64;
+__host__ __device__ constexpr int tile_rows(bool pair) { return pair ? 2 * BM : BM; }
+__host__ __device__ constexpr int tile_cols(bool pair) { return pair ? 256 : 128; }
 constexpr int STAGES = 6;
 constexpr int A_BYTES = BM * BK * 2;
-constexpr int B_BYTES = (BN / 2) * BK * 2;   // this CTA's half of B
+constexpr int B_COLS = 128;                  // of B in a CTA: half of a pair's tile
+constexpr int B_BYTES = B_COLS * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr uint32_t TMEM_COLS = 512;
 constexpr int EPI_WARPS = 8;
-constexpr int GEMM_THREADS = 32 * (2 + EPI_WARPS);
+constexpr int JOB_WARPS = 12;                // run a pass over memory beside the MMAs
+constexpr int FIRST_JOB_WARP = 2 + EPI_WARPS;
+__host__ __device__ constexpr int gemm_threads(bool job) { return 32 * (FIRST_JOB_WARP + (job ? JOB_WARPS : 0)); }
 constexpr int BUF_BYTES = 32 * 128;          // an epilogue warp's staging: 32 rows of 128 bytes
 constexpr int GROUP = 16;                    // row tiles that take a column of tiles together
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr long long PIECE_ELEMS = 1ll << 30; // dz elements of a piece
-constexpr long long PAIRS = 76;              // SM pairs of a GB300: slices are counted by it, so that sums have one order
+constexpr long long SMS = 152;               // of a GB300: slices are counted by it, so that sums have one order
+constexpr int64_t FEW_ROWS = 128;            // up to here a CTA works alone (see ce_gemm_kernel)
 constexpr int MAX_SPLIT = 64;
 // An accumulator of the tensor cores loses up to a unit in the last place with each step of 16 products, always towards
 // zero: over a long contraction that is 2e-5 of the result. For fp32 gradients it adds up 64 64-deep steps, and the
@@ -70,12 +72,30 @@ struct Ctrl {
 };
 
 constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + EPI_WARPS * BUF_BYTES + sizeof(Ctrl) + 1024;
-static_assert(SMEM <= 232448, "shared memory over budget");
+static_assert(sizeof(Ctrl) <= 512 && SMEM <= 232448, "shared memory over budget");
+
+// What a row of exponentials needs to become dz: -lse log2(e), g w, and the target, -1 for a row that has no part in the
+// loss. Four floats in memory, written by ce_combine_kernel.
+struct RowState {
+  float base, g;
+  int target;
+  static __device__ __forceinline__ RowState of(const float4 &v) { return RowState{v.x, v.y, __float_as_int(v.z)}; }
+};
+
+// dz from the exponentials that LOGITS_EXP kept, in their place: dz = g w (exp(m_part - lse) e - [v = t]).
+struct ScaleJob {
+  uint16_t *x;                 // rows of ld elements
+  long long ld;
+  const float2 *partials;      // [parts][rows]
+  const float4 *row_state;
+  int rows, cols, part_shift;
+};
 
 struct CeArgs {
   CUtensorMap map_a, map_b, map_out;   // map_out: dz, the exponentials in its place, or the output
   int rows, cols;                      // of the output
-  int m_pairs, n_tiles;
+  int m_tiles, n_tiles;
+  int a_box;                           // rows of A that a stage loads: all, or, for a CTA alone, those that there are
   int k_iters, k_wrap;                 // 64-deep steps; from k_wrap on A's second plane and B again (two terms of dz)
   int split, k_per;
   int k_seg;                           // steps that one accumulator adds up before they join the output
@@ -86,12 +106,13 @@ struct CeArgs {
   int itype;
   const float *weights, *grad, *lse;
   float grad_scale;
-  float2 *partials;                    // [cols / 128, rounded up][rows]: maximum and sum of exponentials
+  float2 *partials;                    // [parts][rows]: maximum and sum of exponentials
   float *z_target;                     // [rows]
   // DH, DW
   void *out;
   long long ld_out, slice_stride;      // elements; slice s goes to out + s * slice_stride
   int out_f32, accumulate, vec, tma;
+  ScaleJob job;
   uint32_t *err;
   unsigned long long timeout_ns;
 };
@@ -106,16 +127,16 @@ __device__ __forceinline__ long long target_of(const void *t, int itype, long lo
   return itype == MUON_I32 ? static_cast<long long>(static_cast<const int *>(t)[i]) : static_cast<const long long *>(t)[i];
 }
 
-// Unit u: slice, then groups of GROUP row-tile pairs, in a group column after column of tiles. A wave of 76 pairs then
+// Unit u: slice, then groups of GROUP row tiles, in a group column after column of tiles. A wave of 76 pairs then
 // reads GROUP row tiles and five column tiles, which L2 holds, whatever the matrix' size.
 __device__ __forceinline__ void decode(const CeArgs &a, long long u, int &slice, int &ti, int &tj) {
-  const int tiles = a.m_pairs * a.n_tiles;
+  const int tiles = a.m_tiles * a.n_tiles;
   slice = static_cast<int>(u / tiles);
   int r = static_cast<int>(u - static_cast<long long>(slice) * tiles);
   const int per_group = GROUP * a.n_tiles;
   const int g = r / per_group;
   r -= g * per_group;
-  const int in_group = min(GROUP, a.m_pairs - g * GROUP);
+  const int in_group = min(GROUP, a.m_tiles - g * GROUP);
   tj = r / in_group;
   ti = g * GROUP + (r - tj * in_group);
 }
@@ -136,9 +157,9 @@ __device__ __forceinline__ unsigned pack2_half(float a, float b) {
   return *reinterpret_cast<const unsigned *>(&h);
 }
 
-// One tile's part of a warp (128 columns from col0) as its maximum and the sum of its exponentials relative to that, for
+// One tile's part of a warp (32 NC columns from col0) as its maximum and the sum of its exponentials relative to that, for
 // each row; with KEEP the exponentials too, in fp16: none is above 1, so 2^-12 of each is kept, or 2^-25 of the largest.
-template <bool KEEP>
+template <bool KEEP, int NC>
 __device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, int row, int warp_row0, int col0, int part,
                                                 int lane, uint8_t *buf) {
   if (col0 >= a.cols || warp_row0 >= a.rows) return;
@@ -146,7 +167,7 @@ __device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, 
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   const int left = a.cols - col0;   // columns that there are
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < NC; ++c) {
     float v[32];
     __syncwarp();
     tmem_ld_32x32b_x32(tmem + 32 * c, v);
@@ -169,7 +190,7 @@ __device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, 
   const float ref = m == -INFINITY ? 0.f : m * LOG2E;   // nothing above -inf: exponentials of zero
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < NC; ++c) {
     float v[32];
     __syncwarp();
     tmem_ld_32x32b_x32(tmem + 32 * c, v);
@@ -207,6 +228,7 @@ __device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, 
 
 // One tile's part of a warp as dz, in bf16 terms, through the staging buffer and TMA (which leaves out what lies past the
 // rows or columns).
+template <int NC>
 __device__ __forceinline__ void epilogue_dlogits(const CeArgs &a, uint32_t tmem, int row, int warp_row0, int col0, int lane,
                                                  uint8_t *buf) {
   long long t = -1;
@@ -221,7 +243,7 @@ __device__ __forceinline__ void epilogue_dlogits(const CeArgs &a, uint32_t tmem,
   }
   if (warp_row0 >= a.rows) return;
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < NC / 2; ++c) {
     const int c0 = col0 + 64 * c;
     if (c0 >= a.cols) break;
 #pragma unroll 1
@@ -284,11 +306,12 @@ __device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec
 // One tile's part of a warp as rows of the output: lines of 128 bytes (64 bf16 or 32 fp32 values) through the staging
 // buffer and TMA where the output's rows are 16-byte aligned and nothing is added to. Else 32 columns of fp32 at a time
 // through the buffer, so that eight lanes write 128 bytes of a row (64 as bf16).
+template <int NC>
 __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
                                                  uint8_t *buf) {
   if (warp_row0 >= a.rows) return;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < NC; ++c) {
     const int c0 = col0 + 32 * c;
     if (c0 >= a.cols) break;
     float v[32];
@@ -321,11 +344,12 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
   }
 }
 
+template <int NC>
 __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
                                              uint8_t *buf, bool accumulate) {
   if (warp_row0 >= a.rows) return;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < NC; ++c) {
     const int c0 = col0 + 32 * c;
     if (c0 >= a.cols) break;
     {
@@ -366,11 +390,70 @@ __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int
   }
 }
 
+// Units first, first + stride, ... by a group of threads: SCALE_ROWS rows (whose maxima lie next to each other) and 8 columns
+// per thread. All of a unit's loads are on their way before anything is stored. Bound by HBM: 4 bytes per logit.
+constexpr int SCALE_ROWS = 4;
+__device__ __forceinline__ void scale_units(const ScaleJob &a, long long first, long long stride, int thread, int threads) {
+  const int blocks = (a.cols + 8 * threads - 1) / (8 * threads);   // of columns
+  const long long units = static_cast<long long>((a.rows + SCALE_ROWS - 1) / SCALE_ROWS) * blocks;
+#pragma unroll 1
+  for (long long u = first; u < units; u += stride) {
+    const int group = static_cast<int>(u / blocks);
+    const int c0 = (static_cast<int>(u - static_cast<long long>(group) * blocks) * threads + thread) * 8;
+    if (c0 >= a.cols) continue;
+    const int r0 = group * SCALE_ROWS;
+    uint16_t *x = a.x + r0 * a.ld + c0;
+    const float2 *part = a.partials + static_cast<long long>(c0 >> a.part_shift) * a.rows;
+    uint4 e[SCALE_ROWS];
+    float4 state[SCALE_ROWS];
+    float m[SCALE_ROWS];
+#pragma unroll
+    for (int i = 0; i < SCALE_ROWS; ++i) {
+      const int own = min(r0 + i, a.rows - 1);   // the last row again where there is no further one
+      e[i] = __ldcs(reinterpret_cast<const uint4 *>(a.x + own * a.ld + c0));
+      m[i] = __ldg(&part[own].x);
+      state[i] = __ldg(a.row_state + own);
+    }
+#pragma unroll
+    for (int i = 0; i < SCALE_ROWS; ++i) {
+      const RowState r = RowState::of(state[i]);
+      const float f = r.g * exp2_fast(fmaf(m[i], LOG2E, r.base));
+      const int hit = r.target - c0;
+      const unsigned in[4] = {e[i].x, e[i].y, e[i].z, e[i].w};
+      unsigned out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float2 y = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&in[k])), make_float2(f, f));
+        if (hit == 2 * k) y.x -= r.g;
+        if (hit == 2 * k + 1) y.y -= r.g;
+        out[k] = r.target < 0 ? 0u : pack2(y.x, y.y);   // zeros for a row without a part, whatever its exponentials are
+      }
+      if (r0 + i < a.rows) *reinterpret_cast<uint4 *>(x + i * a.ld) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) ce_scale_kernel(const ScaleJob a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  scale_units(a, blockIdx.x, gridDim.x, threadIdx.x, 256);
+}
+
 // A: h (K-major) for the logits, DH dz (K-major), DW dz (MN-major: dz^T). B: W (K-major) for the logits, DH W and DW h
 // (MN-major). An MN-major operand is loaded as boxes of 64 columns x 64 steps.
-template <int KIND>
-__global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeArgs args) {
+//
+// PAIR: the two CTAs of a pair share a tile of 256 x 256, which halves what each reads of B. Else a CTA has a tile of
+// 128 x 128 alone: for up to 128 rows, where half of a pair's MMAs would multiply rows that there are not, and where W has to
+// come in faster than a pair's MMAs take it (8 x 50304 x 768, forward: FIGURE).
+//
+// JOB: more warps run a ScaleJob, which belongs to other rows than the product's, so that its HBM traffic passes under the
+// MMAs (8192 x 50304 x 768: 1528 -> 1360 us, 4096 x 128256 x 4096: 8.16 -> 7.93 ms). Twelve of them, since each waits for
+// its loads: 1666 us with four, 1358 with eight, 1335 with twelve on another box.
+template <int KIND, bool PAIR, bool JOB>
+__global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __grid_constant__ CeArgs args) {
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
+  constexpr int CTAS = PAIR ? 2 : 1, BN = tile_cols(PAIR), NC = BN / 64;   // NC: chunks of 32 columns per epilogue warp
+  constexpr uint32_t TMEM_COLS = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *staging = smem + STAGES * STAGE_BYTES;
@@ -384,7 +467,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctrl->acc_full[s], 1);
-      mbar_init(&ctrl->acc_empty[s], 2 * EPI_WARPS);   // both CTAs' epilogue warps, on the even CTA's copy
+      mbar_init(&ctrl->acc_empty[s], CTAS * EPI_WARPS);   // a pair's epilogue warps all use the even CTA's copy
     }
     mbar_init(&ctrl->drain, 1);
     ctrl->abort_flag = 0;
@@ -392,23 +475,31 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
   }
   if (warp == 0 && lane < 2) tma_prefetch_desc(lane ? &args.map_b : &args.map_a);
   if (warp == 1) {
-    tmem_alloc_pair(&ctrl->tmem_base, TMEM_COLS);
-    tmem_relinquish_pair();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&ctrl->tmem_base, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&ctrl->tmem_base, TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncwarp();
-  cluster_sync();   // both CTAs' barriers are initialised before either signals the other
+  if constexpr (PAIR) cluster_sync();   // both CTAs' barriers are initialised before either signals the other
+  else __syncthreads();
   tc_fence_after();
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const uint32_t tmem_base = ctrl->tmem_base;
   WaitCtl ctl{&ctrl->abort_flag, args.err, args.timeout_ns};
-  const int rank = static_cast<int>(cluster_ctarank());
-  const long long first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const long long first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
+  // the even CTA's copy of a barrier, as a cluster address
+  auto leader = [](uint64_t *bar) { return PAIR ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar); };
 
   if (warp == 0) {
     if (lane == 0) {
-      const uint32_t leader_full0 = mapa_shared(smem_u32(&ctrl->full[0]), 0);
+      const uint32_t leader_full0 = leader(&ctrl->full[0]);
       uint32_t stage = 0, phase = 0;
       int last_parity[STAGES];
       for (int s = 0; s < STAGES; ++s) last_parity[s] = -1;
@@ -416,32 +507,37 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
       for (long long u = first; ok && u < args.total; u += stride) {
         int slice, ti, tj;
         decode(args, u, slice, ti, tj);
-        const int row0 = (2 * ti + rank) * BM, col0 = tj * BN + (BN / 2) * rank;
+        const int row0 = (CTAS * ti + rank) * BM, col0 = tj * BN + B_COLS * rank;
         const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
         for (int kk = k0; kk < k1; ++kk) {
           if (!wait_bounded(&ctrl->empty[stage], phase ^ 1u, ctl, ERR_WAIT_EMPTY)) {
             ok = false;
             break;
           }
-          if (rank == 0) {   // both CTAs' copies complete on the even CTA's barrier
-            mbar_arrive_expect_tx(&ctrl->full[stage], 2 * STAGE_BYTES);
+          if (rank == 0) {   // a pair's copies complete on the even CTA's barrier
+            mbar_arrive_expect_tx(&ctrl->full[stage], PAIR ? 2 * STAGE_BYTES : args.a_box * BK * 2 + B_BYTES);
             last_parity[stage] = static_cast<int>(phase);
           }
-          const uint32_t fb = leader_full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
           uint8_t *sa = smem + stage * STAGE_BYTES, *sb = sa + A_BYTES;
+          auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y, int z) {
+            if constexpr (PAIR)
+              tma_load_3d_pair(dst, map, leader_full0 + stage * static_cast<uint32_t>(sizeof(uint64_t)), x, y, z);
+            else
+              tma_load_3d(dst, map, &ctrl->full[stage], x, y, z);
+          };
           const int plane = kk >= args.k_wrap ? 1 : 0;
           const int k = (kk - (plane ? args.k_wrap : 0)) * BK;
           if constexpr (A_MN) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) tma_load_3d_pair(sa + q * (64 * BK * 2), &args.map_a, fb, row0 + 64 * q, k, plane);
+            for (int q = 0; q < 2; ++q) load(sa + q * (64 * BK * 2), &args.map_a, row0 + 64 * q, k, plane);
           } else {
-            tma_load_3d_pair(sa, &args.map_a, fb, k, row0, plane);
+            load(sa, &args.map_a, k, row0, plane);
           }
           if constexpr (B_MN) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) tma_load_3d_pair(sb + q * (64 * BK * 2), &args.map_b, fb, col0 + 64 * q, k, 0);
+            for (int q = 0; q < 2; ++q) load(sb + q * (64 * BK * 2), &args.map_b, col0 + 64 * q, k, 0);
           } else {
-            tma_load_3d_pair(sb, &args.map_b, fb, k, col0, 0);
+            load(sb, &args.map_b, k, col0, 0);
           }
           if (++stage == STAGES) {
             stage = 0;
@@ -455,7 +551,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, BN, A_MN, B_MN);
+      constexpr uint32_t idesc = idesc_bf16_f32(CTAS * BM, BN, A_MN, B_MN);
+      auto commit = [](uint64_t *bar) {
+        if constexpr (PAIR) tc_commit_pair_mc(bar, 0x3);
+        else tc_commit(bar);
+      };
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true, issued = false;
       for (long long u = first; ok && u < args.total; u += stride) {
@@ -482,30 +582,33 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
                   A_MN ? smem_desc_sw128(sa + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sa + k * 32, 16, 1024);
               const uint64_t bdesc =
                   B_MN ? smem_desc_sw128(sb + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc_sw128(sb + k * 32, 16, 1024);
-              tc_mma_bf16_pair(tmem_base + acc * BN, adesc, bdesc, idesc, ((kk - ks) | k) != 0 ? 1u : 0u);
+              const uint32_t add = ((kk - ks) | k) != 0 ? 1u : 0u;
+              if constexpr (PAIR) tc_mma_bf16_pair(tmem_base + acc * BN, adesc, bdesc, idesc, add);
+              else tc_mma_bf16(tmem_base + acc * BN, adesc, bdesc, idesc, add);
             }
             issued = true;
-            tc_commit_pair_mc(&ctrl->empty[stage], 0x3);
+            commit(&ctrl->empty[stage]);   // frees the stage, in both CTAs of a pair
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
             }
           }
           if (!ok) break;
-          tc_commit_pair_mc(&ctrl->acc_full[acc], 0x3);
+          commit(&ctrl->acc_full[acc]);
           acc ^= 1u;
           if (acc == 0) acc_phase ^= 1u;
         }
       }
       if (issued) {   // all MMAs have completed before tensor memory is released
-        tc_commit_pair_mc(&ctrl->drain, 0x1);
+        if constexpr (PAIR) tc_commit_pair_mc(&ctrl->drain, 0x1);
+        else tc_commit(&ctrl->drain);
         drain_wait(&ctrl->drain, 0u, ctl);
       }
     }
-  } else {
-    const uint32_t leader_acc_empty0 = mapa_shared(smem_u32(&ctrl->acc_empty[0]), 0);
+  } else if (warp < FIRST_JOB_WARP) {
+    const uint32_t leader_acc_empty0 = leader(&ctrl->acc_empty[0]);
     const int lane_base = (warp % 4) * 32;   // the lanes of tensor memory that this warp may read
-    const int half = (warp - 2) / 4;         // 128 of the tile's 256 columns
+    const int half = (warp - 2) / 4;         // of the tile's columns
     uint8_t *buf = staging + (warp - 2) * BUF_BYTES;
     uint32_t acc = 0, acc_phase = 0;
     bool ok = true;
@@ -513,39 +616,76 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) ce_gemm_kernel(const __grid_c
       int slice, ti, tj;
       decode(args, u, slice, ti, tj);
       const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
-      const int warp_row0 = (2 * ti + rank) * BM + lane_base, col0 = tj * BN + 128 * half;
+      const int warp_row0 = (CTAS * ti + rank) * BM + lane_base, col0 = tj * BN + 32 * NC * half;
       for (int ks = k0; ks < k1; ks += args.k_seg) {
         ok = wait_bounded(&ctrl->acc_full[acc], acc_phase, ctl, ERR_WAIT_ACC_FULL);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 128 * half;
+        const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 32 * NC * half;
         if constexpr (KIND == LOGITS || KIND == LOGITS_EXP)
-          epilogue_logits<KIND == LOGITS_EXP>(args, tmem, warp_row0 + lane, warp_row0, col0, 2 * tj + half, lane, buf);
-        else if constexpr (KIND == DLOGITS) epilogue_dlogits(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
-        else if (args.tma) epilogue_out_tma(args, tmem, slice, warp_row0, col0, lane, buf);
-        else epilogue_out(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
+          epilogue_logits<KIND == LOGITS_EXP, NC>(args, tmem, warp_row0 + lane, warp_row0, col0, 2 * tj + half, lane, buf);
+        else if constexpr (KIND == DLOGITS)
+          epilogue_dlogits<NC>(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
+        else if (args.tma)
+          epilogue_out_tma<NC>(args, tmem, slice, warp_row0, col0, lane, buf);
+        else
+          epilogue_out<NC>(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
         tc_fence_before();
         __syncwarp();
+        // the MMA warp reads none of this warp's stores, so the signal need not wait for them
         if (lane == 0) mbar_arrive_cluster_relaxed(leader_acc_empty0 + acc * static_cast<uint32_t>(sizeof(uint64_t)));
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
     }
     if (lane == 0) bulk_wait_group_all();
+  } else if constexpr (JOB) {
+    scale_units(args.job, blockIdx.x, gridDim.x, threadIdx.x - 32 * FIRST_JOB_WARP, 32 * JOB_WARPS);
   }
 
-  // neither CTA leaves while the other may still signal it
+  // neither CTA of a pair leaves while the other may still signal it
   tc_fence_before();
   __syncwarp();
-  cluster_sync();
+  if constexpr (PAIR) cluster_sync();
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else tmem_dealloc(tmem_base, TMEM_COLS);
   }
 }
 
 // ------------------------------------------------------------------------------------------ the small kernels
+
+struct RowsArgs {
+  const __nv_bfloat16 *h;
+  __nv_bfloat16 *out;
+  long long ldh, ld_out, V;
+  const void *targets;
+  const float *weights;
+  int itype, rows, D;
+};
+
+// h with zeros for the rows that have no part in the loss: dw's product multiplies every row, and a row of padding may
+// hold NaN. One warp, 16 bytes per lane and turn (both pitches are multiples of 8; what lies past D is not read).
+__device__ __forceinline__ void copy_live_row(const RowsArgs &a, long long row, int lane) {
+  if (row >= a.rows) return;
+  const long long t = target_of(a.targets, a.itype, row);
+  const bool live = t >= 0 && t < a.V && (a.weights == nullptr || a.weights[row] != 0.f);
+  const __nv_bfloat16 *src = a.h + row * a.ldh;
+  __nv_bfloat16 *dst = a.out + row * a.ld_out;
+#pragma unroll 4
+  for (int c = 8 * lane; c + 8 <= a.D; c += 256)
+    *reinterpret_cast<uint4 *>(dst + c) = live ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
+  for (int c = a.D / 8 * 8 + lane; c < a.D; c += 32) dst[c] = live ? src[c] : __float2bfloat16_rn(0.f);
+}
+
+__global__ void __launch_bounds__(256) ce_rows_kernel(const RowsArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  copy_live_row(a, static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32, threadIdx.x % 32);
+}
 
 struct CombineArgs {
   const float2 *partials;
@@ -554,15 +694,23 @@ struct CombineArgs {
   int itype, parts, rows;
   long long V;
   float *losses, *lse;
+  float grad_scale;
+  float4 *row_state;   // or null
+  int own_blocks;      // blocks past these copy h's rows
+  RowsArgs copy;
 };
 
 // Eight rows per block, whose pairs of one part fill a 32-byte sector; 32 threads share a row's parts.
 // lse = m + log(sum of s_p exp(m_p - m)).
 constexpr int COMBINE_ROWS = 8;
-__global__ void __launch_bounds__(256) ce_combine_kernel(const CombineArgs a) {
+__global__ void __launch_bounds__(256) ce_combine_kernel(const __grid_constant__ CombineArgs a) {
   __shared__ float2 sh[8][COMBINE_ROWS];
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= a.own_blocks) {
+    copy_live_row(a.copy, static_cast<long long>(blockIdx.x - a.own_blocks) * 8 + threadIdx.x / 32, threadIdx.x % 32);
+    return;
+  }
   const int own = threadIdx.x % COMBINE_ROWS, stream = threadIdx.x / COMBINE_ROWS;
   const int row = blockIdx.x * COMBINE_ROWS + own;
   float m = -INFINITY, s = 0.f;
@@ -597,85 +745,8 @@ __global__ void __launch_bounds__(256) ce_combine_kernel(const CombineArgs a) {
   const float lse = m + logf(s);
   a.lse[row] = live ? lse : 0.f;
   a.losses[row] = live ? w * (lse - a.z_target[row]) : 0.f;
-}
-
-struct ScaleArgs {
-  uint16_t *x;                 // exponentials in, dz out: rows of ld elements
-  long long ld;
-  const float2 *partials;
-  const float *weights, *lse;
-  const void *targets;
-  int itype, rows, V;
-  float grad_scale;
-};
-
-// dz from the kept exponentials, in their place: dz = g w (exp(m_part - lse) e - [v = t]). A block takes SCALE_ROWS rows of
-// 2048 columns, 8 columns of each row per thread: the rows' maxima lie next to each other. Bound by HBM.
-constexpr int SCALE_ROWS = 4;
-__global__ void __launch_bounds__(256) ce_scale_kernel(const ScaleArgs a) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_launch_dependents();
-  const int c0 = blockIdx.y * 2048 + 8 * static_cast<int>(threadIdx.x);
-  if (c0 >= a.V) return;
-  const long long r0 = static_cast<long long>(blockIdx.x) * SCALE_ROWS;
-  const int n = static_cast<int>(min(static_cast<long long>(SCALE_ROWS), a.rows - r0));
-  uint4 e[SCALE_ROWS];
-  float m[SCALE_ROWS];
-#pragma unroll
-  for (int i = 0; i < SCALE_ROWS; ++i) {
-    if (i >= n) break;
-    e[i] = __ldcs(reinterpret_cast<const uint4 *>(a.x + (r0 + i) * a.ld + c0));
-    m[i] = a.partials[static_cast<long long>(c0 / (BN / 2)) * a.rows + r0 + i].x;
-  }
-#pragma unroll
-  for (int i = 0; i < SCALE_ROWS; ++i) {
-    if (i >= n) break;
-    const long long row = r0 + i, t = target_of(a.targets, a.itype, row);
-    const float w = a.weights != nullptr ? a.weights[row] : 1.f;
-    const bool live = t >= 0 && t < a.V && w != 0.f;
-    const float g = w * a.grad_scale, f = g * exp2_fast((m[i] - a.lse[row]) * LOG2E);
-    float v[8];
-    const unsigned in[4] = {e[i].x, e[i].y, e[i].z, e[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&in[k]));
-      v[2 * k] = live ? f * x.x : 0.f;
-      v[2 * k + 1] = live ? f * x.y : 0.f;
-    }
-    if (live && t - c0 >= 0 && t - c0 < 8) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = t - c0 == k ? v[k] - g : v[k];
-    }
-    *reinterpret_cast<uint4 *>(a.x + row * a.ld + c0) =
-        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-  }
-}
-
-struct RowsArgs {
-  const __nv_bfloat16 *h;
-  __nv_bfloat16 *out;
-  long long ldh, ld_out, V;
-  const void *targets;
-  const float *weights;
-  int itype, rows, D;
-};
-
-// h with zeros for the rows that have no part in the loss: dw's product multiplies every row, and a row of padding may
-// hold NaN. A warp per row, 16 bytes per lane and turn (both pitches are multiples of 8; what lies past D is not read).
-__global__ void __launch_bounds__(256) ce_rows_kernel(const RowsArgs a) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_launch_dependents();
-  const int lane = threadIdx.x % 32;
-  const int row = blockIdx.x * 8 + threadIdx.x / 32;
-  if (row >= a.rows) return;
-  const long long t = target_of(a.targets, a.itype, row);
-  const bool live = t >= 0 && t < a.V && (a.weights == nullptr || a.weights[row] != 0.f);
-  const __nv_bfloat16 *src = a.h + row * a.ldh;
-  __nv_bfloat16 *dst = a.out + row * a.ld_out;
-#pragma unroll 4
-  for (int c = 8 * lane; c + 8 <= a.D; c += 256)
-    *reinterpret_cast<uint4 *>(dst + c) = live ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
-  for (int c = a.D / 8 * 8 + lane; c < a.D; c += 32) dst[c] = live ? src[c] : __float2bfloat16_rn(0.f);
+  if (a.row_state != nullptr)
+    a.row_state[row] = make_float4(-lse * LOG2E, w * a.grad_scale, __int_as_float(live ? static_cast<int>(t) : -1), 0.f);
 }
 
 struct ReduceArgs {
@@ -709,19 +780,28 @@ __global__ void __launch_bounds__(256) ce_reduce_kernel(const ReduceArgs a) {
 
 // ------------------------------------------------------------------------------------------ plan
 
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+long long round_up(long long a, long long b) { return ceil_div(a, b) * b; }
+
+// Rows from which on the joint call goes by halves (Run::joint). Below, the halves' products lose more to their last wave of
+// tiles than the scale pass costs: 1024 x 32000 x 1024 174 us whole and 200 us by halves, 2048 x 50304 x 768 396 and 391 us.
+constexpr long long HALVES = 2048;
+
 // Slices of a contraction of k 64-deep steps over `tiles` tile pairs: the count for which the longest SM pair's steps are
 // fewest, each slice counted with TILE_STEPS more for its start and epilogue, and with what its sums' way through memory
 // costs. From sizes alone.
 constexpr int TILE_STEPS = 6;
-int choose_split(long long tiles, long long k) {
-  if (tiles >= 4 * PAIRS) return 1;
+int choose_split(bool pair, long long rows, long long cols, long long k) {
+  const long long tiles = ceil_div(rows, tile_rows(pair)) * ceil_div(cols, tile_cols(pair)), at_once = pair ? SMS / 2 : SMS;
+  if (tiles >= 4 * at_once) return 1;
   int best = 1;
   double best_cost = 0;
   for (int s = 1; s <= MAX_SPLIT && (s == 1 || k / s >= 8); ++s) {
     const long long per = (k + s - 1) / s, n = (k + per - 1) / per;
-    const double waves = static_cast<double>((tiles * n + PAIRS - 1) / PAIRS);
-    // a slice's tile is 256 KB written and read: 0.08 us of the whole GPU's bandwidth, a fifth of a step of every pair
-    const double cost = waves * static_cast<double>(per + TILE_STEPS) + (n > 1 ? 0.2 * static_cast<double>(tiles * n) / PAIRS + 12 : 0);
+    const double waves = static_cast<double>(ceil_div(tiles * n, at_once));
+    // a slice's tile is written and read: 0.08 us of the whole GPU's bandwidth for a pair's, a fifth of a step of one pair
+    const double way = n > 1 ? 0.2 * static_cast<double>(tiles * n) / static_cast<double>(at_once) + 12 : 0;
+    const double cost = waves * static_cast<double>(per + TILE_STEPS) + way;
     if (s == 1 || cost < best_cost) {
       best = static_cast<int>(n);
       best_cost = cost;
@@ -734,12 +814,12 @@ std::atomic<long long> g_piece_rows{0};   // muon_debug_loss_rows
 
 struct Plan {
   long long rows, pieces, Vp, Dp;     // rows of a piece; pitches of dz and of fp32 scratch rows
-  int planes, parts;
-  int split_dh, split_dw;
-  size_t partials, z_target, dz, h_live, slices, dw_sum, total;
+  int planes, parts, part_cols;
+  bool pair;                          // the products over rows: logits, dlogits, dh
+  long long half;                     // rows of a piece's first half in the joint call, or all
+  int split_dh, split_half, split_dw;
+  size_t partials, z_target, row_state, dz, h_live, slices, dw_sum, total;
 };
-
-long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 Plan plan(int64_t N, int64_t V, int64_t D, int terms, bool dw_f32) {
   Plan p{};
@@ -751,7 +831,9 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms, bool dw_f32) {
   p.Vp = ceil_div(V, 64) * 64;
   p.Dp = ceil_div(D, 4) * 4;
   p.planes = terms;
-  p.parts = static_cast<int>(ceil_div(V, BN / 2));
+  p.pair = p.rows > FEW_ROWS;
+  p.part_cols = tile_cols(p.pair) / 2;
+  p.parts = static_cast<int>(ceil_div(V, p.part_cols));
   size_t off = 1024;   // the control block
   auto take = [&](size_t &at, long long bytes) {
     at = off;
@@ -761,11 +843,14 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms, bool dw_f32) {
   take(p.z_target, 4 * p.rows);
   if (terms > 0) {
     const long long kh = ceil_div(V, BK) * terms, kw = ceil_div(p.rows, BK) * terms;
-    p.split_dh = choose_split(ceil_div(p.rows, 2 * BM) * ceil_div(D, BN), kh);
-    p.split_dw = choose_split(ceil_div(V, 2 * BM) * ceil_div(D, BN), kw);
+    p.half = terms == 1 && p.rows >= HALVES ? round_up(p.rows / 2, tile_rows(true)) : p.rows;
+    p.split_dh = choose_split(p.pair, p.rows, D, kh);
+    p.split_half = choose_split(p.pair, p.half, D, kh);
+    p.split_dw = choose_split(true, V, D, kw);
+    take(p.row_state, 16 * p.rows);
     take(p.dz, 2ll * terms * p.rows * p.Vp);
     take(p.h_live, 2 * p.rows * round8(D));
-    const long long dh = p.split_dh > 1 ? 4ll * p.split_dh * p.rows * p.Dp : 0;
+    const long long dh = 4 * p.Dp * std::max(p.split_dh > 1 ? p.split_dh * p.rows : 0, p.split_half > 1 ? p.split_half * p.half : 0);
     const long long dw = p.split_dw > 1 ? 4ll * p.split_dw * V * p.Dp : 0;
     take(p.slices, std::max(dh, dw));
     if (p.pieces > 1 && !dw_f32) take(p.dw_sum, 4ll * V * p.Dp);
@@ -778,17 +863,18 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms, bool dw_f32) {
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-template <int KIND>
+template <int KIND, bool PAIR, bool JOB>
 muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
+  constexpr auto kernel = ce_gemm_kernel<KIND, PAIR, JOB>;
   static AttributesSet set;
   static std::atomic<int> clusters[64];
   if (set.once([] {
-        return cudaFuncSetAttribute(ce_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(SMEM));
       }) != cudaSuccess)
     return MUON_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(GEMM_THREADS);
+  cfg.blockDim = dim3(gemm_threads(JOB));
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -799,17 +885,17 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = PAIR ? 2 : 1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
-  int n = clusters[dev].load(std::memory_order_relaxed);   // pairs that can be resident at once
+  int n = PAIR ? clusters[dev].load(std::memory_order_relaxed) : device_sm_count();   // CTAs or pairs that run at once
   if (n == 0) {
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (device_sm_count() / 2)));
-    if (cudaOccupancyMaxActiveClusters(&n, ce_gemm_kernel<KIND>, &cfg) != cudaSuccess || n < 1) n = device_sm_count() / 2;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = device_sm_count() / 2;
     clusters[dev].store(n, std::memory_order_relaxed);
   }
-  a.m_pairs = static_cast<int>(ceil_div(a.rows, 2 * BM));
-  a.n_tiles = static_cast<int>(ceil_div(a.cols, BN));
+  a.m_tiles = static_cast<int>(ceil_div(a.rows, tile_rows(PAIR)));
+  a.n_tiles = static_cast<int>(ceil_div(a.cols, tile_cols(PAIR)));
   if (a.split < 1) a.split = 1;
   a.k_per = static_cast<int>(ceil_div(a.k_iters, a.split));
   a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
@@ -821,12 +907,25 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
                                 (a.split > 1 ? a.slice_stride : a.ld_out * a.rows) * e, 32))
       return MUON_ERR_CUDA;
   }
-  a.total = static_cast<long long>(a.m_pairs) * a.n_tiles * a.split;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(n, a.total)));
+  a.total = static_cast<long long>(a.m_tiles) * a.n_tiles * a.split;
+  cfg.gridDim = dim3(static_cast<unsigned>((PAIR ? 2 : 1) * std::min<long long>(n, a.total)));
   launch_begin(kind, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, ce_gemm_kernel<KIND>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   launch_end(s);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+template <int KIND>
+muon_status launch_rows(bool pair, CeArgs &a, int32_t kind, cudaStream_t s) {
+  return pair ? launch_gemm<KIND, true, false>(a, kind, s) : launch_gemm<KIND, false, false>(a, kind, s);
+}
+
+// As launch_rows for a pair's tiles, with a job beside the product if there is one.
+template <int KIND>
+muon_status launch_beside(const ScaleJob *job, CeArgs &a, int32_t kind, cudaStream_t s) {
+  if (job == nullptr) return launch_gemm<KIND, true, false>(a, kind, s);
+  a.job = *job;
+  return launch_gemm<KIND, true, true>(a, kind, s);
 }
 
 muon_status launch_reduce(const ReduceArgs &r, int dtype, cudaStream_t s) {
@@ -864,136 +963,215 @@ size_t size_of(int dt) { return dt == MUON_F32 ? 4 : 2; }
 // Rows of a matrix of one row may have any pitch: none is used.
 long long pitch8(long long ld, long long rows, long long cols) { return rows == 1 ? round8(cols) : ld; }
 
-muon_status run(const Call &c, cudaStream_t s) {
-  const Plan p = plan(c.N, c.V, c.D, c.terms, c.dw == nullptr || c.dwdt == MUON_F32);
-  muon_status st;
-  const long long kd = ceil_div(c.D, BK), kv = ceil_div(c.V, BK);
-  CeArgs base;
-  memset(&base, 0, sizeof(base));
-  base.targets = nullptr;
-  base.itype = c.itype;
-  base.grad_scale = c.grad_scale;
-  base.planes = p.planes;
-  base.err = reinterpret_cast<uint32_t *>(c.ws);
-  base.timeout_ns = wait_timeout_ns();
-  base.partials = reinterpret_cast<float2 *>(c.ws + p.partials);
-  base.z_target = reinterpret_cast<float *>(c.ws + p.z_target);
-  __nv_bfloat16 *dz = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.dz);
-  float *slices = reinterpret_cast<float *>(c.ws + p.slices);
-  float *dw_sum = p.dw_sum ? reinterpret_cast<float *>(c.ws + p.dw_sum) : nullptr;
-  if (c.N == 0) {
-    if (c.dw == nullptr || c.accumulate) return MUON_OK;
-    return launch_reduce(ReduceArgs{nullptr, 0, 0, c.lddw, 0, static_cast<int>(c.V), static_cast<int>(c.D), 0, c.dw}, c.dwdt,
-                         s);
+// One call's launches, a piece at a time.
+class Run {
+  const Call &c;
+  const Plan p;
+  cudaStream_t s;
+  CeArgs base_;
+  long long r0_ = 0, rows_ = 0;      // the piece
+  const char *h_ = nullptr;          // its rows
+  long long ldh_, ldw_;
+  float2 *partials_;
+  float *z_target_, *slices_, *dw_sum_;
+  float4 *row_state_;
+  __nv_bfloat16 *dz_, *h_live_;
+
+  template <typename T>
+  T *at(size_t offset) const {
+    return offset ? reinterpret_cast<T *>(c.ws + offset) : nullptr;
   }
-  for (long long r0 = 0; r0 < c.N; r0 += p.rows) {
-    const long long rows = std::min(p.rows, c.N - r0);
-    const char *h = c.h + r0 * c.ldh * 2;
-    const long long ldh = pitch8(c.ldh, c.N, c.D), ldw = pitch8(c.ldw, c.V, c.D);
-    CeArgs a = base;
-    a.rows = static_cast<int>(rows);
-    a.cols = static_cast<int>(c.V);
-    a.k_iters = a.k_wrap = static_cast<int>(kd);
-    a.targets = static_cast<const char *>(c.targets) + r0 * (c.itype == MUON_I32 ? 4 : 8);
-    a.weights = c.weights != nullptr ? c.weights + r0 : nullptr;
-    if (!make_bf16_map(&a.map_a, h, c.D, rows, 1, ldh, ldh * rows, BM) ||
-        !make_bf16_map(&a.map_b, c.w, c.D, c.V, 1, ldw, ldw * c.V, BN / 2))
+  // the matrices as operands: rows [r, r + n) of the piece
+  bool h_map(CUtensorMap *m, long long r, long long n) const {
+    return make_bf16_map(m, h_ + r * ldh_ * 2, c.D, n, 1, ldh_, ldh_ * n, a_box());
+  }
+  int a_box() const { return p.pair ? BM : static_cast<int>(round8(rows_)); }
+  bool w_map(CUtensorMap *m, int box) const { return make_bf16_map(m, c.w, c.D, c.V, 1, ldw_, ldw_ * c.V, box); }
+  bool dz_map(CUtensorMap *m, long long r, long long n, int box) const {
+    return make_bf16_map(m, dz_ + r * p.Vp, c.V, n, p.planes, p.Vp, p.Vp * rows_, box);
+  }
+  const void *targets(long long r) const {
+    return static_cast<const char *>(c.targets) + (r0_ + r) * (c.itype == MUON_I32 ? 4 : 8);
+  }
+  const float *weights(long long r) const { return c.weights != nullptr ? c.weights + r0_ + r : nullptr; }
+  RowsArgs copy_args(long long r, long long n) const {
+    return RowsArgs{reinterpret_cast<const __nv_bfloat16 *>(h_ + r * ldh_ * 2), h_live_ + r * round8(c.D), ldh_, round8(c.D),
+                    c.V, targets(r), weights(r), c.itype, static_cast<int>(n), static_cast<int>(c.D)};
+  }
+  // the statistics of rows [r, r + n) lie after those of the piece's earlier rows
+  float2 *partials(long long r) const { return partials_ + r * p.parts; }
+  ScaleJob job(long long r, long long n) const {
+    return ScaleJob{reinterpret_cast<uint16_t *>(dz_ + r * p.Vp), p.Vp, partials(r), row_state_ + r, static_cast<int>(n),
+                    static_cast<int>(c.V), p.part_cols == 128 ? 7 : 6};
+  }
+  bool product(CeArgs &f, long long r, long long n) const {
+    f = base_;
+    f.rows = static_cast<int>(n);
+    f.cols = static_cast<int>(c.V);
+    f.a_box = a_box();
+    f.k_iters = f.k_wrap = static_cast<int>(ceil_div(c.D, BK));
+    f.targets = targets(r);
+    f.weights = weights(r);
+    f.partials = partials(r);
+    f.z_target = z_target_ + r;
+    return h_map(&f.map_a, r, n) && w_map(&f.map_b, B_COLS);
+  }
+
+  // losses and lse of rows [r, r + n), the exponentials too if `keep`, with a job beside the product if there is one
+  muon_status losses(long long r, long long n, bool keep, const ScaleJob *beside) {
+    CeArgs f;
+    if (!product(f, r, n) || (keep && !dz_map(&f.map_out, r, n, 32))) return MUON_ERR_CUDA;
+    muon_status st = beside != nullptr ? launch_beside<LOGITS_EXP>(beside, f, KK_CE_LOGITS, s)
+                     : keep            ? launch_rows<LOGITS_EXP>(p.pair, f, KK_CE_LOGITS, s)
+                                       : launch_rows<LOGITS>(p.pair, f, KK_CE_LOGITS, s);
+    if (st != MUON_OK) return st;
+    const long long own = ceil_div(n, COMBINE_ROWS), copies = keep && c.dw != nullptr ? ceil_div(n, 8) : 0;
+    const CombineArgs cb{partials(r),         z_target_ + r, weights(r),
+                         targets(r),          c.itype,       p.parts,
+                         static_cast<int>(n), c.V,           c.losses + r0_ + r,
+                         c.lse + r0_ + r,     c.grad_scale,  keep ? row_state_ + r : nullptr,
+                         static_cast<int>(own), copies ? copy_args(r, n) : RowsArgs{}};
+    return small(KK_CE_COMBINE, ce_combine_kernel, own + copies, cb);
+  }
+
+  template <typename Args, typename Given>
+  muon_status small(int32_t kind, void (*kernel)(Args), long long blocks, const Given &args) {
+    launch_begin(kind, s);
+    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, args);
+    launch_end(s);
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  }
+
+  muon_status dlogits() {
+    CeArgs f;
+    if (!product(f, 0, rows_) || !dz_map(&f.map_out, 0, rows_, 32)) return MUON_ERR_CUDA;
+    f.lse = (c.forward ? c.lse : c.lse_in) + r0_;
+    f.grad = c.grad != nullptr ? c.grad + r0_ : nullptr;
+    return launch_rows<DLOGITS>(p.pair, f, KK_CE_DLOGITS, s);
+  }
+
+  void output(CeArgs &f, void *out, int dtype, long long ld, bool cut, long long slice_rows, bool add) const {
+    f.out = cut ? static_cast<void *>(slices_) : out;
+    f.out_f32 = cut || dtype == MUON_F32;
+    f.ld_out = cut ? p.Dp : ld;
+    f.slice_stride = slice_rows * p.Dp;
+    f.accumulate = cut ? 0 : add;
+    f.vec = aligned(f.out, 16) && f.ld_out % (f.out_f32 ? 4 : 8) == 0;
+  }
+
+  muon_status dh(long long r, long long n, int split, const ScaleJob *beside) {
+    char *out = c.dh + (r0_ + r) * c.lddh * static_cast<long long>(size_of(c.dhdt));
+    CeArgs f = base_;
+    f.rows = static_cast<int>(n);
+    f.cols = static_cast<int>(c.D);
+    f.k_wrap = static_cast<int>(ceil_div(c.V, BK));
+    f.k_iters = f.k_wrap * p.planes;
+    f.split = split;
+    f.a_box = a_box();
+    if (!dz_map(&f.map_a, r, n, f.a_box) || !w_map(&f.map_b, BK)) return MUON_ERR_CUDA;
+    const bool cut = split > 1;
+    output(f, out, c.dhdt, c.lddh, cut, n, false);
+    const muon_status st = beside != nullptr ? launch_beside<DH>(beside, f, KK_CE_DH, s) : launch_rows<DH>(p.pair, f, KK_CE_DH, s);
+    if (st != MUON_OK || !cut) return st;
+    return launch_reduce(ReduceArgs{slices_, f.slice_stride, p.Dp, c.lddh, f.split, f.rows, f.cols, 0, out}, c.dhdt, s);
+  }
+
+  muon_status dw() {
+    CeArgs f = base_;
+    f.rows = static_cast<int>(c.V);
+    f.cols = static_cast<int>(c.D);
+    f.k_wrap = static_cast<int>(ceil_div(rows_, BK));
+    f.k_iters = f.k_wrap * p.planes;
+    f.split = p.split_dw;
+    if (!dz_map(&f.map_a, 0, rows_, BK) ||
+        !make_bf16_map(&f.map_b, h_live_, c.D, rows_, 1, round8(c.D), round8(c.D) * rows_, BK))
       return MUON_ERR_CUDA;
+    // several pieces add up in fp32: in the gradient itself, or in scratch that the last piece rounds
+    void *sum = dw_sum_ != nullptr ? static_cast<void *>(dw_sum_) : c.dw;
+    const long long ld = dw_sum_ != nullptr ? p.Dp : c.lddw;
+    const int dt = dw_sum_ != nullptr ? static_cast<int>(MUON_F32) : c.dwdt;
+    const bool add = r0_ > 0 || (dw_sum_ == nullptr && c.accumulate), cut = p.split_dw > 1;
+    output(f, sum, dt, ld, cut, c.V, add);
+    const muon_status st = launch_gemm<DW, true, false>(f, KK_CE_DW, s);
+    if (st != MUON_OK || !cut) return st;
+    return launch_reduce(ReduceArgs{slices_, f.slice_stride, p.Dp, ld, f.split, f.rows, f.cols, add, sum}, dt, s);
+  }
+
+  // dz of the piece (and h_live) from losses: by halves, so that the first half's exponentials become dz beside the second
+  // half's logits, and the second half's beside the first half's dh.
+  muon_status joint() {
+    muon_status st;
+    const long long a = p.half, b = rows_ - a;
+    if (b < HALVES / 4 || c.dh == nullptr) {   // also a last piece with little more than a first half
+      if ((st = losses(0, rows_, true, nullptr)) != MUON_OK) return st;
+      const ScaleJob all = job(0, rows_);
+      // a block per unit: blocks that take several in turn are 2 to 4 % slower
+      const long long units = ceil_div(rows_, SCALE_ROWS) * ceil_div(c.V, 2048);
+      if ((st = small(KK_CE_DLOGITS, ce_scale_kernel, std::min(units, 1ll << 30), all)) != MUON_OK) return st;
+      return c.dh != nullptr ? dh(0, rows_, p.split_dh, nullptr) : MUON_OK;
+    }
+    const ScaleJob first = job(0, a), second = job(a, b);
+    if ((st = losses(0, a, true, nullptr)) != MUON_OK || (st = losses(a, b, true, &first)) != MUON_OK ||
+        (st = dh(0, a, p.split_half, &second)) != MUON_OK)
+      return st;
+    return dh(a, b, p.split_half, nullptr);
+  }
+
+  muon_status piece() {
+    muon_status st;
     // one bf16 term: the exponentials are kept in dz's place; two: the logits are computed again
     const bool keep = c.forward && c.backward && p.planes == 1;
-    if (c.backward && !make_bf16_map(&a.map_out, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, 32)) return MUON_ERR_CUDA;
-    if (c.forward) {
-      CeArgs f = a;
-      if ((st = keep ? launch_gemm<LOGITS_EXP>(f, KK_CE_LOGITS, s) : launch_gemm<LOGITS>(f, KK_CE_LOGITS, s)) != MUON_OK)
-        return st;
-      const CombineArgs cb{a.partials, a.z_target, a.weights, a.targets, a.itype, p.parts, a.rows, c.V, c.losses + r0,
-                           c.lse + r0};
-      launch_begin(KK_CE_COMBINE, s);
-      const cudaError_t e =
-          launch_pdl(ce_combine_kernel, dim3(static_cast<unsigned>(ceil_div(rows, COMBINE_ROWS))), dim3(256), 0, s, cb);
-      launch_end(s);
-      if (e != cudaSuccess) return MUON_ERR_CUDA;
-    }
-    if (!c.backward) continue;
     if (keep) {
-      const ScaleArgs sa{reinterpret_cast<uint16_t *>(dz), p.Vp, a.partials, a.weights, c.lse + r0, a.targets, a.itype,
-                         a.rows, static_cast<int>(c.V), c.grad_scale};
-      launch_begin(KK_CE_DLOGITS, s);
-      const cudaError_t e = launch_pdl(ce_scale_kernel,
-                                       dim3(static_cast<unsigned>(ceil_div(rows, SCALE_ROWS)),
-                                            static_cast<unsigned>(ceil_div(c.V, 2048))),
-                                       dim3(256), 0, s, sa);
-      launch_end(s);
-      if (e != cudaSuccess) return MUON_ERR_CUDA;
+      if ((st = joint()) != MUON_OK) return st;
     } else {
-      CeArgs f = a;
-      f.lse = (c.forward ? c.lse : c.lse_in) + r0;
-      f.grad = c.grad != nullptr ? c.grad + r0 : nullptr;
-      if ((st = launch_gemm<DLOGITS>(f, KK_CE_DLOGITS, s)) != MUON_OK) return st;
-    }
-    if (c.dh != nullptr) {
-      char *out = c.dh + r0 * c.lddh * static_cast<long long>(size_of(c.dhdt));
-      CeArgs f = base;
-      f.rows = static_cast<int>(rows);
-      f.cols = static_cast<int>(c.D);
-      f.k_iters = static_cast<int>(kv * p.planes);
-      f.k_wrap = static_cast<int>(kv);
-      f.split = p.split_dh;
-      if (!make_bf16_map(&f.map_a, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, BM) ||
-          !make_bf16_map(&f.map_b, c.w, c.D, c.V, 1, ldw, ldw * c.V, BK))
-        return MUON_ERR_CUDA;
-      const bool cut = p.split_dh > 1;
-      f.out = cut ? static_cast<void *>(slices) : out;
-      f.out_f32 = cut || c.dhdt == MUON_F32;
-      f.ld_out = cut ? p.Dp : c.lddh;
-      f.slice_stride = rows * p.Dp;
-      f.vec = aligned(f.out, 16) && f.ld_out % (f.out_f32 ? 4 : 8) == 0;
-      if ((st = launch_gemm<DH>(f, KK_CE_DH, s)) != MUON_OK) return st;
-      if (cut && (st = launch_reduce(ReduceArgs{slices, f.slice_stride, p.Dp, c.lddh, f.split, f.rows, f.cols, 0, out},
-                                     c.dhdt, s)) != MUON_OK)
+      if (c.forward && (st = losses(0, rows_, false, nullptr)) != MUON_OK) return st;
+      if (!c.backward) return MUON_OK;
+      if ((st = dlogits()) != MUON_OK) return st;
+      if (c.dh != nullptr && (st = dh(0, rows_, p.split_dh, nullptr)) != MUON_OK) return st;
+      if (c.dw != nullptr && (st = small(KK_CE_ROWS, ce_rows_kernel, ceil_div(rows_, 8), copy_args(0, rows_))) != MUON_OK)
         return st;
     }
-    if (c.dw != nullptr) {
-      __nv_bfloat16 *h_live = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.h_live);
-      const RowsArgs ra{reinterpret_cast<const __nv_bfloat16 *>(h), h_live, ldh, round8(c.D), c.V, a.targets, a.weights,
-                        a.itype, a.rows, static_cast<int>(c.D)};
-      launch_begin(KK_CE_ROWS, s);
-      const cudaError_t e = launch_pdl(ce_rows_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 8))), dim3(256), 0, s, ra);
-      launch_end(s);
-      if (e != cudaSuccess) return MUON_ERR_CUDA;
-      CeArgs f = base;
-      f.rows = static_cast<int>(c.V);
-      f.cols = static_cast<int>(c.D);
-      f.k_wrap = static_cast<int>(ceil_div(rows, BK));
-      f.k_iters = f.k_wrap * p.planes;
-      f.split = p.split_dw;
-      if (!make_bf16_map(&f.map_a, dz, c.V, rows, p.planes, p.Vp, p.Vp * rows, BK) ||
-          !make_bf16_map(&f.map_b, h_live, c.D, rows, 1, round8(c.D), round8(c.D) * rows, BK))
-        return MUON_ERR_CUDA;
-      // several pieces add up in fp32: in the gradient itself, or in scratch that the last piece rounds
-      void *sum = dw_sum != nullptr ? static_cast<void *>(dw_sum) : c.dw;
-      const long long ld = dw_sum != nullptr ? p.Dp : c.lddw;
-      const int dt = dw_sum != nullptr ? static_cast<int>(MUON_F32) : c.dwdt;
-      const int add = r0 > 0 || (dw_sum == nullptr && c.accumulate);
-      const bool cut = p.split_dw > 1;
-      f.out = cut ? static_cast<void *>(slices) : sum;
-      f.out_f32 = cut || dt == MUON_F32;
-      f.ld_out = cut ? p.Dp : ld;
-      f.slice_stride = c.V * p.Dp;
-      f.accumulate = cut ? 0 : add;
-      f.vec = aligned(f.out, 16) && f.ld_out % (f.out_f32 ? 4 : 8) == 0;
-      if ((st = launch_gemm<DW>(f, KK_CE_DW, s)) != MUON_OK) return st;
-      if (cut && (st = launch_reduce(ReduceArgs{slices, f.slice_stride, p.Dp, ld, f.split, f.rows, f.cols, add, sum}, dt,
-                                     s)) != MUON_OK)
-        return st;
-    }
+    return c.dw != nullptr ? dw() : MUON_OK;
   }
-  if (c.dw != nullptr && dw_sum != nullptr)
-    return launch_reduce(ReduceArgs{dw_sum, 0, p.Dp, c.lddw, 1, static_cast<int>(c.V), static_cast<int>(c.D), c.accumulate,
-                                    c.dw},
-                         c.dwdt, s);
-  return MUON_OK;
-}
+
+ public:
+  Run(const Call &call, cudaStream_t stream)
+      : c(call), p(plan(call.N, call.V, call.D, call.terms, call.dw == nullptr || call.dwdt == MUON_F32)), s(stream) {
+    memset(&base_, 0, sizeof(base_));
+    base_.itype = c.itype;
+    base_.grad_scale = c.grad_scale;
+    base_.planes = p.planes;
+    base_.err = reinterpret_cast<uint32_t *>(c.ws);
+    base_.timeout_ns = wait_timeout_ns();
+    ldh_ = pitch8(c.ldh, c.N, c.D);
+    ldw_ = pitch8(c.ldw, c.V, c.D);
+    partials_ = at<float2>(p.partials);
+    z_target_ = at<float>(p.z_target);
+    row_state_ = at<float4>(p.row_state);
+    dz_ = at<__nv_bfloat16>(p.dz);
+    h_live_ = at<__nv_bfloat16>(p.h_live);
+    slices_ = at<float>(p.slices);
+    dw_sum_ = at<float>(p.dw_sum);
+  }
+
+  muon_status all() {
+    const ReduceArgs last{dw_sum_, 0, p.Dp, c.lddw, 1, static_cast<int>(c.V), static_cast<int>(c.D), c.accumulate, c.dw};
+    if (c.N == 0) {
+      ReduceArgs zeros = last;
+      zeros.n = 0;
+      return c.dw != nullptr && !c.accumulate ? launch_reduce(zeros, c.dwdt, s) : MUON_OK;
+    }
+    for (r0_ = 0; r0_ < c.N; r0_ += p.rows) {
+      rows_ = std::min(p.rows, c.N - r0_);
+      h_ = c.h + r0_ * ldh_ * 2;
+      const muon_status st = piece();
+      if (st != MUON_OK) return st;
+    }
+    return c.dw != nullptr && dw_sum_ != nullptr ? launch_reduce(last, c.dwdt, s) : MUON_OK;
+  }
+};
+
+muon_status run(const Call &c, cudaStream_t s) { return Run(c, s).all(); }
 
 // ------------------------------------------------------------------------------------------ checks
 
