@@ -56,9 +56,11 @@ constexpr long long SMS = 152;               // of a GB300: slices are counted b
 constexpr int64_t FEW_ROWS = 128;            // up to here a CTA works alone (see ce_gemm_kernel)
 constexpr int MAX_SPLIT = 64;
 // An accumulator of the tensor cores loses up to a unit in the last place with each step of 16 products, always towards
-// zero: over a long contraction that is 2e-5 of the result. For fp32 gradients it adds up 64 64-deep steps, and the
-// epilogue adds that to what the output holds.
-constexpr int SEGMENT = 64;
+// zero: over a contraction of 128256 that is 2e-5 of the result (dh, 1024 x 128256 x 4096). For fp32 gradients it therefore
+// adds up all of the lower term's products, which are small, and then 16 steps of 64 of the upper one's; the epilogue adds
+// that to what the output holds, rounding to nearest: 1.3e-6. (2048 x 50304 x 768, both calls' products: 657 us with 64
+// steps, 691 with 32, 764 with 16, whose error is a third of the first's.)
+constexpr int SEGMENT = 16;
 
 // LOGITS leaves statistics alone, LOGITS_EXP the tile's exponentials too (for the joint call).
 enum Kind : int { LOGITS = 0, LOGITS_EXP = 1, DLOGITS = 2, DH = 3, DW = 4 };
@@ -96,9 +98,9 @@ struct CeArgs {
   int rows, cols;                      // of the output
   int m_tiles, n_tiles;
   int a_box;                           // rows of A that a stage loads: all, or, for a CTA alone, those that there are
-  int k_iters, k_wrap;                 // 64-deep steps; from k_wrap on A's second plane and B again (two terms of dz)
+  int k_iters, k_low;                  // 64-deep steps, the first k_low of them over A's second plane (dz's lower term)
   int split, k_per;
-  int k_seg;                           // steps that one accumulator adds up before they join the output
+  int k_seg;                           // steps past the lower term's that one accumulator adds up
   int planes;                          // DLOGITS: terms of dz
   long long total;                     // tile pairs times slices
   // LOGITS, LOGITS_EXP, DLOGITS
@@ -126,6 +128,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ long long target_of(const void *t, int itype, long long i) {
   return itype == MUON_I32 ? static_cast<long long>(static_cast<const int *>(t)[i]) : static_cast<const long long *>(t)[i];
 }
+
+// The end of the segment that begins at step ks: the lower term's steps and k_seg others.
+__device__ __forceinline__ int segment_end(const CeArgs &a, int ks, int k1) { return min(k1, max(ks, a.k_low) + a.k_seg); }
 
 // Unit u: slice, then groups of GROUP row tiles, in a group column after column of tiles. A wave of 76 pairs then
 // reads GROUP row tiles and five column tiles, which L2 holds, whatever the matrix' size.
@@ -304,12 +309,16 @@ __device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec
 }
 
 // One tile's part of a warp as rows of the output: lines of 128 bytes (64 bf16 or 32 fp32 values) through the staging
-// buffer and TMA where the output's rows are 16-byte aligned and nothing is added to. Else 32 columns of fp32 at a time
+// buffer and TMA where the output's rows are 16-byte aligned (add: to fp32 values that are there). Else 32 columns of fp32 at a time
 // through the buffer, so that eight lanes write 128 bytes of a row (64 as bf16).
 template <int NC>
 __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
-                                                 uint8_t *buf) {
+                                                 uint8_t *buf, bool add) {
   if (warp_row0 >= a.rows) return;
+  if (add) {   // what an earlier segment has put there is there: sums have one order
+    if (lane == 0) bulk_wait_group_all();
+    __syncwarp();
+  }
 #pragma unroll 1
   for (int c = 0; c < NC; ++c) {
     const int c0 = col0 + 32 * c;
@@ -336,8 +345,9 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
-        // the map counts 2-byte elements: an fp32 column is two of them
-        tma_store_3d(&a.map_out, buf, a.out_f32 ? 2 * c0 : c0 - 32 * (c & 1), warp_row0, slice);
+        const int x = a.out_f32 ? c0 : c0 - 32 * (c & 1);
+        if (add) tma_add_3d(&a.map_out, buf, x, warp_row0, slice);
+        else tma_store_3d(&a.map_out, buf, x, warp_row0, slice);
         bulk_commit_group();
       }
     }
@@ -443,8 +453,10 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(const ScaleJob a) {
 // (MN-major). An MN-major operand is loaded as boxes of 64 columns x 64 steps.
 //
 // PAIR: the two CTAs of a pair share a tile of 256 x 256, which halves what each reads of B. Else a CTA has a tile of
-// 128 x 128 alone: for up to 128 rows, where half of a pair's MMAs would multiply rows that there are not, and where W has to
-// come in faster than a pair's MMAs take it (8 x 50304 x 768, forward: FIGURE).
+// 128 x 128 alone: for up to 128 rows, where half of a pair's MMAs would multiply rows that there are not. Its stages then hold
+// only the rows of A that there are, in eights (a_box; what else lies there makes accumulator rows that nothing reads): TMA
+// takes as long for 128-byte lines that it fills with zeros as for others, and W does not come in at full rate beside them
+// (forward, 8 x 50304 x 768: 29.9 us by pairs, 18.5 us so; 1 x 128256 x 4096: 220 and 173 us).
 //
 // JOB: more warps run a ScaleJob, which belongs to other rows than the product's, so that its HBM traffic passes under the
 // MMAs (8192 x 50304 x 768: 1528 -> 1360 us, 4096 x 128256 x 4096: 8.16 -> 7.93 ms). Twelve of them, since each waits for
@@ -525,8 +537,8 @@ __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __g
             else
               tma_load_3d(dst, map, &ctrl->full[stage], x, y, z);
           };
-          const int plane = kk >= args.k_wrap ? 1 : 0;
-          const int k = (kk - (plane ? args.k_wrap : 0)) * BK;
+          const int plane = kk < args.k_low ? 1 : 0;
+          const int k = (plane ? kk : kk - args.k_low) * BK;
           if constexpr (A_MN) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) load(sa + q * (64 * BK * 2), &args.map_a, row0 + 64 * q, k, plane);
@@ -562,13 +574,13 @@ __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __g
         int slice, ti, tj;
         decode(args, u, slice, ti, tj);
         const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
-        for (int ks = k0; ok && ks < k1; ks += args.k_seg) {
+        for (int ks = k0, ke; ok && ks < k1; ks = ke) {
+          ke = segment_end(args, ks, k1);
           if (!wait_bounded(&ctrl->acc_empty[acc], acc_phase ^ 1u, ctl, ERR_WAIT_ACC_EMPTY)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const int ke = min(k1, ks + args.k_seg);
           for (int kk = ks; kk < ke; ++kk) {
             if (!wait_bounded(&ctrl->full[stage], phase, ctl, ERR_WAIT_FULL)) {
               ok = false;
@@ -617,7 +629,7 @@ __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __g
       decode(args, u, slice, ti, tj);
       const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
       const int warp_row0 = (CTAS * ti + rank) * BM + lane_base, col0 = tj * BN + 32 * NC * half;
-      for (int ks = k0; ks < k1; ks += args.k_seg) {
+      for (int ks = k0; ks < k1; ks = segment_end(args, ks, k1)) {
         ok = wait_bounded(&ctrl->acc_full[acc], acc_phase, ctl, ERR_WAIT_ACC_FULL);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -628,7 +640,7 @@ __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __g
         else if constexpr (KIND == DLOGITS)
           epilogue_dlogits<NC>(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
         else if (args.tma)
-          epilogue_out_tma<NC>(args, tmem, slice, warp_row0, col0, lane, buf);
+          epilogue_out_tma<NC>(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
         else
           epilogue_out<NC>(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
         tc_fence_before();
@@ -901,10 +913,10 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
   a.k_seg = a.out_f32 && a.planes > 1 ? SEGMENT : a.k_per;
   if (KIND == DH || KIND == DW) {   // rows and columns past the output's are not stored; slices follow each other
-    const long long e = a.out_f32 ? 2 : 1;
-    a.tma = a.vec && !a.accumulate && a.k_per <= a.k_seg;
-    if (a.tma && !make_bf16_map(&a.map_out, a.out, a.cols * e, a.rows, a.split, a.ld_out * e,
-                                (a.split > 1 ? a.slice_stride : a.ld_out * a.rows) * e, 32))
+    a.tma = a.vec && (a.out_f32 || !a.accumulate);
+    const long long apart = a.split > 1 ? a.slice_stride : a.ld_out * a.rows;
+    if (a.tma && !(a.out_f32 ? make_f32_map(&a.map_out, a.out, a.cols, a.rows, a.split, a.ld_out, apart, 32)
+                             : make_bf16_map(&a.map_out, a.out, a.cols, a.rows, a.split, a.ld_out, apart, 32)))
       return MUON_ERR_CUDA;
   }
   a.total = static_cast<long long>(a.m_tiles) * a.n_tiles * a.split;
@@ -1009,7 +1021,7 @@ class Run {
     f.rows = static_cast<int>(n);
     f.cols = static_cast<int>(c.V);
     f.a_box = a_box();
-    f.k_iters = f.k_wrap = static_cast<int>(ceil_div(c.D, BK));
+    f.k_iters = static_cast<int>(ceil_div(c.D, BK));
     f.targets = targets(r);
     f.weights = weights(r);
     f.partials = partials(r);
@@ -1064,8 +1076,8 @@ class Run {
     CeArgs f = base_;
     f.rows = static_cast<int>(n);
     f.cols = static_cast<int>(c.D);
-    f.k_wrap = static_cast<int>(ceil_div(c.V, BK));
-    f.k_iters = f.k_wrap * p.planes;
+    f.k_iters = static_cast<int>(ceil_div(c.V, BK)) * p.planes;
+    f.k_low = f.k_iters - f.k_iters / p.planes;
     f.split = split;
     f.a_box = a_box();
     if (!dz_map(&f.map_a, r, n, f.a_box) || !w_map(&f.map_b, BK)) return MUON_ERR_CUDA;
@@ -1080,8 +1092,8 @@ class Run {
     CeArgs f = base_;
     f.rows = static_cast<int>(c.V);
     f.cols = static_cast<int>(c.D);
-    f.k_wrap = static_cast<int>(ceil_div(rows_, BK));
-    f.k_iters = f.k_wrap * p.planes;
+    f.k_iters = static_cast<int>(ceil_div(rows_, BK)) * p.planes;
+    f.k_low = f.k_iters - f.k_iters / p.planes;
     f.split = p.split_dw;
     if (!dz_map(&f.map_a, 0, rows_, BK) ||
         !make_bf16_map(&f.map_b, h_live_, c.D, rows_, 1, round8(c.D), round8(c.D) * rows_, BK))

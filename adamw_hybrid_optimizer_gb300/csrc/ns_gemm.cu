@@ -1100,19 +1100,30 @@ EncodeTiledFn get_encode_fn() {
 
 }  // namespace
 
-bool make_bf16_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long batch, long long ld,
-                   long long mstride, int box_rows) {
+namespace {
+bool encode_map(CUtensorMap *map, CUtensorMapDataType type, int bytes, const void *base, long long inner, long long rows,
+                long long batch, long long ld, long long mstride, int box_rows) {
   auto enc = get_encode_fn();
   if (enc == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(batch)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(mstride) * 2};
-  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * bytes, static_cast<cuuint64_t>(mstride) * bytes};
+  cuuint32_t box[3] = {128u / bytes, static_cast<cuuint32_t>(box_rows), 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(map, type, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool make_bf16_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long batch, long long ld,
+                   long long mstride, int box_rows) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, rows, batch, ld, mstride, box_rows);
+}
+
+bool make_f32_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long batch, long long ld,
+                  long long mstride, int box_rows) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, inner, rows, batch, ld, mstride, box_rows);
 }
 
 namespace {
