@@ -811,8 +811,8 @@ int choose_split(bool pair, long long rows, long long cols, long long k) {
   for (int s = 1; s <= MAX_SPLIT && (s == 1 || k / s >= 8); ++s) {
     const long long per = (k + s - 1) / s, n = (k + per - 1) / per;
     const double waves = static_cast<double>(ceil_div(tiles * n, at_once));
-    // a slice's tile is written and read: 0.08 us of the whole GPU's bandwidth for a pair's, a fifth of a step of one pair
-    const double way = n > 1 ? 0.2 * static_cast<double>(tiles * n) / static_cast<double>(at_once) + 12 : 0;
+    // a pair's tile is 256 KB written, mostly under MMAs, and read again: up to 0.08 us of the GPU's bandwidth, 0.2 steps
+    const double way = n > 1 ? 0.2 * static_cast<double>(tiles * n) * (pair ? 1.0 : 0.25) + 12 : 0;
     const double cost = waves * static_cast<double>(per + TILE_STEPS) + way;
     if (s == 1 || cost < best_cost) {
       best = static_cast<int>(n);

@@ -9,7 +9,7 @@ caller decides by the group's kind, and a Muon group must hold 2-D tensors only.
 
 Muon matrices of one group are bucketed by shape (muon_plan_buckets); each bucket owns one fp32
 (K, A, B) momentum stack, and all buckets of a group are updated by one muon_step_grouped call per
-step. AdamW state is one fp32 exp_avg / exp_avg_sq pair per tensor and the group's step count. With
+step. AdamW state is one fp32 exp_avg / exp_avg_sq pair per tensor (or one in 8 bits, state_bits=8) and the group's step count. With
 master_weights=True (bf16 parameters), each parameter also keeps an fp32 master copy ("master" in its
 state) that takes the update; the parameter holds it rounded to bf16. All arithmetic runs in libmuon: the
 AdamW tensors of all groups in one grouped pass, issued with the last Muon group by hybrid_step.
@@ -33,7 +33,11 @@ CLASSIC = (3.4445, -4.7750, 2.0315)
 MUON_DEFAULTS = dict(lr=0.02, momentum=0.95, weight_decay=0.01, nesterov=True, cautious_wd=False, scale_mode=0,
                      ns_steps=5, ns_coefficients=None, eps=1e-7, master_weights=False, autotune=False)
 # is_adamw=False: Adam with L2 regularisation instead of decoupled decay ("dtensor-muon 0.1.0", "Key options")
-ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, is_adamw=True, master_weights=False)
+# state_bits=8: the moments are held as e4m3 codes with a scale per ADAMW8_BLOCK elements, a byte instead of four for each
+# ("The optimizer's memory budget"): "exp_avg" and "exp_avg_sq" in the state are torch.float8_e4m3fn, the latter of the second
+# moment's root, and "scales" (blocks, 2) is fp32
+ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, is_adamw=True, master_weights=False,
+                      state_bits=32)
 
 
 class _Bucket:
@@ -60,6 +64,10 @@ class _Bucket:
             self.grad_ptrs = L.pointer_array(grads, device)
             self._grad_key = key
         return grads
+
+
+def _codes8(p: torch.Tensor) -> torch.Tensor:
+    return torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
 
 
 class HybridMuonAdamW:
@@ -106,9 +114,16 @@ class HybridMuonAdamW:
                 ws_bytes = max(ws_bytes, L.muon_workspace_bytes_grouped(shapes) if buckets else 0)
             else:
                 group["step"] = 0
+                if group["state_bits"] not in (8, 32):
+                    raise ValueError("state_bits is 8 or 32")
                 for p in group["params"]:
-                    self.state[p] = {"exp_avg": torch.zeros(p.shape, dtype=torch.float32, device=p.device),
-                                     "exp_avg_sq": torch.zeros(p.shape, dtype=torch.float32, device=p.device)}
+                    if group["state_bits"] == 8:
+                        blocks = (p.numel() + L.ADAMW8_BLOCK - 1) // L.ADAMW8_BLOCK
+                        self.state[p] = {"exp_avg": _codes8(p), "exp_avg_sq": _codes8(p),
+                                         "scales": torch.zeros((blocks, 2), dtype=torch.float32, device=p.device)}
+                    else:
+                        self.state[p] = {"exp_avg": torch.zeros(p.shape, dtype=torch.float32, device=p.device),
+                                         "exp_avg_sq": torch.zeros(p.shape, dtype=torch.float32, device=p.device)}
                     if group["master_weights"]:
                         if p.dtype != torch.bfloat16:
                             raise ValueError("master_weights needs bf16 parameters")
@@ -123,9 +138,10 @@ class HybridMuonAdamW:
     @torch.no_grad()
     def step(self):
         """One step of every group. The AdamW tensors of all groups go through one grouped pass, issued in one
-        call (hybrid_step) with the last Muon group."""
+        call (hybrid_step) with the last Muon group; those with moments in 8 bits through one of their own."""
         muon_calls = []
         adamw_specs = []
+        adamw8_specs = []
         for group, buckets in zip(self.param_groups, self._buckets):
             if group["kind"] == "muon":
                 hp = L.make_muon_hparams(group["lr"], group["momentum"], group["weight_decay"], group["nesterov"],
@@ -160,8 +176,17 @@ class HybridMuonAdamW:
                     if not p.is_contiguous() or not p.grad.is_contiguous():
                         raise ValueError("AdamW needs contiguous parameters and gradients")
                     st = self.state[p]
-                    adamw_specs.append((p, p.grad, st["exp_avg"], st["exp_avg_sq"], hp)
-                                       + ((st["master"],) if "master" in st else ()))
+                    master = (st["master"],) if "master" in st else ()
+                    if group["state_bits"] == 8:
+                        adamw8_specs.append((p, p.grad, st["exp_avg"], st["exp_avg_sq"], st["scales"], hp) + master)
+                    else:
+                        adamw_specs.append((p, p.grad, st["exp_avg"], st["exp_avg_sq"], hp) + master)
+        adamw8 = L.make_adamw8_tensors(adamw8_specs) if adamw8_specs else None   # its checks before any launch
+        self._launch(muon_calls, adamw_specs)
+        if adamw8 is not None:
+            L.adamw8_step_grouped(adamw8)
+
+    def _launch(self, muon_calls, adamw_specs):
         if not adamw_specs:
             for bk, hp in muon_calls:
                 L.muon_step_grouped(bk, hp, self._ws)
@@ -196,6 +221,10 @@ class HybridMuonAdamW:
 
     def load_state_dict(self, sd):
         flat = [p for g in self.param_groups for p in g["params"]]
+        for i, p in enumerate(flat):
+            own = self.state[p]
+            if ("scales" in own) != ("scales" in sd["state"][i]):
+                raise ValueError("load_state_dict: moments in 8 bits on one side and in 32 on the other")
         for i, p in enumerate(flat):
             for k, v in sd["state"][i].items():
                 self.state[p][k].copy_(v)
