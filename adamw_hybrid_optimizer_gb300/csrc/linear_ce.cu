@@ -3,7 +3,7 @@
 //     lse_i = log sum_v exp z_iv,   loss_i = w_i (lse_i - z_it),   dz_iv = g_i w_i (exp(z_iv - lse_i) - [v = t_i])
 //     dh = dz W,   dW = dz^T h
 //
-// Rows go through in pieces of at most PIECE_ELEMS / V (plan()); nothing of size N x V outlives a piece. Per piece:
+// Rows go through in pieces (plan()); nothing of size N x V outlives a piece. Per piece:
 //   logits  z a tile of 256 x 256 at a time on the tensor cores; a tile's accumulators leave as one running maximum and sum
 //           of exponentials for each row and half tile (online softmax) and the target's logit
 //   combine the parts' pairs into lse and the loss; and h without the rows that have no part in the loss, for dw
@@ -51,16 +51,17 @@ __host__ __device__ constexpr int gemm_threads(bool job) { return 32 * (FIRST_JO
 constexpr int BUF_BYTES = 32 * 128;          // an epilogue warp's staging: 32 rows of 128 bytes
 constexpr int GROUP = 16;                    // row tiles that take a column of tiles together
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr long long PIECE_ELEMS = 1ll << 30; // dz elements of a piece
+constexpr long long MAX_PITCH = 1ll << 37;   // elements: a tensor map's strides are below 2^40 bytes
+constexpr long long PIECE_ELEMS = 1ll << 30; // of dz, or of h, in a piece
 constexpr long long SMS = 152;               // of a GB300: slices are counted by it, so that sums have one order
 constexpr int64_t FEW_ROWS = 128;            // up to here a CTA works alone (see ce_gemm_kernel)
 constexpr int MAX_SPLIT = 64;
 // An accumulator of the tensor cores loses up to a unit in the last place with each step of 16 products, always towards
 // zero: over a contraction of 128256 that is 2e-5 of the result (dh, 1024 x 128256 x 4096). For fp32 gradients it therefore
-// adds up all of the lower term's products, which are small, and then 16 steps of 64 of the upper one's; the epilogue adds
-// that to what the output holds, rounding to nearest: 1.3e-6. (2048 x 50304 x 768, both calls' products: 657 us with 64
-// steps, 691 with 32, 764 with 16, whose error is a third of the first's.)
-constexpr int SEGMENT = 16;
+// adds up all of the lower term's products, which are small, and then 32 steps of 64 of the upper one's; the epilogue adds
+// that to what the output holds, rounding to nearest: 2.5e-6, of which 1.3e-6 are the two terms' own. (2048 x 50304 x 768: 657
+// us with 64 steps, 691 with 32, 764 with 16, whose error is 1.4e-6.)
+constexpr int SEGMENT = 32;
 
 // LOGITS leaves statistics alone, LOGITS_EXP the tile's exponentials too (for the joint call).
 enum Kind : int { LOGITS = 0, LOGITS_EXP = 1, DLOGITS = 2, DH = 3, DW = 4 };
@@ -734,15 +735,19 @@ __global__ void __launch_bounds__(256) ce_combine_kernel(const __grid_constant__
   };
   if (row < a.rows) {
     const float2 *src = a.partials + row;
-    int p = stream;
-    for (; p + 7 * 32 < a.parts; p += 8 * 32) {
+    for (int p = stream; p < a.parts; p += 8 * 32) {   // eight at once, the last ones again where there are no further ones
       float2 x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = src[static_cast<long long>(p + 32 * k) * a.rows];
+      for (int k = 0; k < 8; ++k) x[k] = src[static_cast<long long>(min(p + 32 * k, a.parts - 1)) * a.rows];
+      float mn = m;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) join(x[k]);
+      for (int k = 0; k < 8; ++k) mn = fmaxf(mn, x[k].x);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      s *= exp2_fast((m - ref) * LOG2E);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += p + 32 * k < a.parts ? x[k].y * exp2_fast((x[k].x - ref) * LOG2E) : 0.f;
+      m = mn;
     }
-    for (; p < a.parts; p += 32) join(src[static_cast<long long>(p) * a.rows]);
   }
 #pragma unroll
   for (int o = COMBINE_ROWS; o < 32; o *= 2)
@@ -833,15 +838,15 @@ struct Plan {
   size_t partials, z_target, row_state, dz, h_live, slices, dw_sum, total;
 };
 
-Plan plan(int64_t N, int64_t V, int64_t D, int terms, bool dw_f32) {
+Plan plan(int64_t N, int64_t V, int64_t D, int terms) {
   Plan p{};
   long long rows = g_piece_rows.load();
-  if (rows <= 0) rows = PIECE_ELEMS / V;
+  p.Vp = round_up(V, 64);
+  if (rows <= 0) rows = PIECE_ELEMS / std::max<long long>(p.Vp, round8(D));
   rows = std::max(256ll, rows / 256 * 256);
   p.rows = std::max<long long>(1, std::min<long long>(N, rows));
   p.pieces = ceil_div(N, p.rows);
-  p.Vp = ceil_div(V, 64) * 64;
-  p.Dp = ceil_div(D, 4) * 4;
+  p.Dp = round_up(D, 4);
   p.planes = terms;
   p.pair = p.rows > FEW_ROWS;
   p.part_cols = tile_cols(p.pair) / 2;
@@ -865,7 +870,7 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms, bool dw_f32) {
     const long long dh = 4 * p.Dp * std::max(p.split_dh > 1 ? p.split_dh * p.rows : 0, p.split_half > 1 ? p.split_half * p.half : 0);
     const long long dw = p.split_dw > 1 ? 4ll * p.split_dw * V * p.Dp : 0;
     take(p.slices, std::max(dh, dw));
-    if (p.pieces > 1 && !dw_f32) take(p.dw_sum, 4ll * V * p.Dp);
+    if (p.pieces > 1) take(p.dw_sum, 4ll * V * p.Dp);
   }
   p.total = off;
   return p;
@@ -913,8 +918,8 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
   a.k_seg = a.out_f32 && a.planes > 1 ? SEGMENT : a.k_per;
   if (KIND == DH || KIND == DW) {   // rows and columns past the output's are not stored; slices follow each other
-    a.tma = a.vec && (a.out_f32 || !a.accumulate);
-    const long long apart = a.split > 1 ? a.slice_stride : a.ld_out * a.rows;
+    a.tma = a.vec && (a.out_f32 || !a.accumulate) && a.ld_out <= MAX_PITCH;
+    const long long apart = a.split > 1 ? a.slice_stride : a.ld_out;   // one slice has no next one
     if (a.tma && !(a.out_f32 ? make_f32_map(&a.map_out, a.out, a.cols, a.rows, a.split, a.ld_out, apart, 32)
                              : make_bf16_map(&a.map_out, a.out, a.cols, a.rows, a.split, a.ld_out, apart, 32)))
       return MUON_ERR_CUDA;
@@ -978,7 +983,7 @@ long long pitch8(long long ld, long long rows, long long cols) { return rows == 
 // One call's launches, a piece at a time.
 class Run {
   const Call &c;
-  const Plan p;
+  const Plan &p;
   cudaStream_t s;
   CeArgs base_;
   long long r0_ = 0, rows_ = 0;      // the piece
@@ -995,10 +1000,10 @@ class Run {
   }
   // the matrices as operands: rows [r, r + n) of the piece
   bool h_map(CUtensorMap *m, long long r, long long n) const {
-    return make_bf16_map(m, h_ + r * ldh_ * 2, c.D, n, 1, ldh_, ldh_ * n, a_box());
+    return make_bf16_map(m, h_ + r * ldh_ * 2, c.D, n, 1, ldh_, ldh_, a_box());
   }
   int a_box() const { return p.pair ? BM : static_cast<int>(round8(rows_)); }
-  bool w_map(CUtensorMap *m, int box) const { return make_bf16_map(m, c.w, c.D, c.V, 1, ldw_, ldw_ * c.V, box); }
+  bool w_map(CUtensorMap *m, int box) const { return make_bf16_map(m, c.w, c.D, c.V, 1, ldw_, ldw_, box); }
   bool dz_map(CUtensorMap *m, long long r, long long n, int box) const {
     return make_bf16_map(m, dz_ + r * p.Vp, c.V, n, p.planes, p.Vp, p.Vp * rows_, box);
   }
@@ -1096,7 +1101,7 @@ class Run {
     f.k_low = f.k_iters - f.k_iters / p.planes;
     f.split = p.split_dw;
     if (!dz_map(&f.map_a, 0, rows_, BK) ||
-        !make_bf16_map(&f.map_b, h_live_, c.D, rows_, 1, round8(c.D), round8(c.D) * rows_, BK))
+        !make_bf16_map(&f.map_b, h_live_, c.D, rows_, 1, round8(c.D), round8(c.D), BK))
       return MUON_ERR_CUDA;
     // several pieces add up in fp32: in the gradient itself, or in scratch that the last piece rounds
     void *sum = dw_sum_ != nullptr ? static_cast<void *>(dw_sum_) : c.dw;
@@ -1147,8 +1152,7 @@ class Run {
   }
 
  public:
-  Run(const Call &call, cudaStream_t stream)
-      : c(call), p(plan(call.N, call.V, call.D, call.terms, call.dw == nullptr || call.dwdt == MUON_F32)), s(stream) {
+  Run(const Call &call, const Plan &pl, cudaStream_t stream) : c(call), p(pl), s(stream) {
     memset(&base_, 0, sizeof(base_));
     base_.itype = c.itype;
     base_.grad_scale = c.grad_scale;
@@ -1163,7 +1167,7 @@ class Run {
     dz_ = at<__nv_bfloat16>(p.dz);
     h_live_ = at<__nv_bfloat16>(p.h_live);
     slices_ = at<float>(p.slices);
-    dw_sum_ = at<float>(p.dw_sum);
+    dw_sum_ = c.dw != nullptr && c.dwdt != MUON_F32 ? at<float>(p.dw_sum) : nullptr;
   }
 
   muon_status all() {
@@ -1183,8 +1187,6 @@ class Run {
   }
 };
 
-muon_status run(const Call &c, cudaStream_t s) { return Run(c, s).all(); }
-
 // ------------------------------------------------------------------------------------------ checks
 
 constexpr int64_t MAX_ROWS = 1 << 26, MAX_COLS = 1 << 26, MAX_D = 65536;
@@ -1201,15 +1203,18 @@ muon_status check_inputs(const void *h, muon_dtype hdt, int64_t ldh, const void 
   if (st != MUON_OK) return st;
   if (w == nullptr || (N > 0 && (h == nullptr || targets == nullptr)) || ldh < D || ldw < D) return MUON_ERR_INVALID_ARG;
   if (hdt != MUON_BF16 || wdt != MUON_BF16 || (itype != MUON_I32 && itype != MUON_I64)) return MUON_ERR_DTYPE;
+  if ((N > 1 && ldh > MAX_PITCH) || (V > 1 && ldw > MAX_PITCH)) return MUON_ERR_SHAPE;
   if (!aligned(h, 16) || !aligned(w, 16) || (N > 1 && ldh % 8 != 0) || (V > 1 && ldw % 8 != 0) ||
       !aligned(targets, itype == MUON_I32 ? 4 : 8) || !aligned(weights, 4))
     return MUON_ERR_ALIGNMENT;
   return MUON_OK;
 }
 
-muon_status check_outputs(const void *dh, muon_dtype dhdt, int64_t lddh, const void *dw, muon_dtype dwdt, int64_t lddw,
-                          int64_t N, int64_t D, int *terms) {
+muon_status check_outputs(const void *h, const void *w, const void *dh, muon_dtype dhdt, int64_t lddh, const void *dw,
+                          muon_dtype dwdt, int64_t lddw, int64_t N, int64_t D, int *terms) {
   if (dh == nullptr && dw == nullptr && N > 0) return MUON_ERR_INVALID_ARG;
+  if (N > 0 && ((dh != nullptr && (dh == h || dh == w || dh == dw)) || (dw != nullptr && (dw == h || dw == w))))
+    return MUON_ERR_INVALID_ARG;   // h and w are read again after the first gradient is written
   *terms = 1;
   if (dh != nullptr) {
     if (lddh < D) return MUON_ERR_INVALID_ARG;
@@ -1226,11 +1231,14 @@ muon_status check_outputs(const void *dh, muon_dtype dhdt, int64_t lddh, const v
   return MUON_OK;
 }
 
-muon_status check_ws(const void *ws, size_t ws_bytes, int64_t N, int64_t V, int64_t D, int terms) {
-  if (ws == nullptr) return MUON_ERR_INVALID_ARG;
-  if (!aligned(ws, 256)) return MUON_ERR_ALIGNMENT;
-  if (ws_bytes < linear_cross_entropy_workspace_bytes(N, V, D, terms)) return MUON_ERR_WORKSPACE;
-  return MUON_OK;
+// The plan is made once: the sizes that the workspace is checked for are those that the launches use.
+muon_status check_and_run(const Call &c, size_t ws_bytes, muon_stream_t stream) {
+  if (c.ws == nullptr) return MUON_ERR_INVALID_ARG;
+  if (!aligned(c.ws, 256)) return MUON_ERR_ALIGNMENT;
+  const Plan p = plan(c.N, c.V, c.D, c.terms);
+  if (ws_bytes < p.total) return MUON_ERR_WORKSPACE;
+  const muon_status st = device_check();
+  return st != MUON_OK ? st : Run(c, p, reinterpret_cast<cudaStream_t>(stream)).all();
 }
 
 }  // namespace
@@ -1242,7 +1250,7 @@ extern "C" {
 
 size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int terms) {
   if (check_sizes(N, V, D) != MUON_OK || terms < 0 || terms > 2) return 0;
-  return plan(N, V, D, terms, false).total;
+  return plan(N, V, D, terms).total;
 }
 
 muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
@@ -1253,7 +1261,6 @@ muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t 
   if (st != MUON_OK) return st;
   if (N > 0 && (losses == nullptr || lse == nullptr)) return MUON_ERR_INVALID_ARG;
   if (!aligned(losses, 4) || !aligned(lse, 4)) return MUON_ERR_ALIGNMENT;
-  if ((st = check_ws(ws, ws_bytes, N, V, D, 0)) != MUON_OK || (st = device_check()) != MUON_OK) return st;
   Call c{};
   c.h = static_cast<const char *>(h);
   c.w = static_cast<const char *>(w);
@@ -1269,7 +1276,7 @@ muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t 
   c.lse = lse;
   c.ws = static_cast<char *>(ws);
   c.forward = true;
-  return run(c, reinterpret_cast<cudaStream_t>(stream));
+  return check_and_run(c, ws_bytes, stream);
 }
 
 muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
@@ -1282,9 +1289,7 @@ muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t
   Call c{};
   if (N > 0 && lse == nullptr) return MUON_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(grad, 4)) return MUON_ERR_ALIGNMENT;
-  if ((st = check_outputs(dh, dhdt, lddh, dw, dwdt, lddw, N, D, &c.terms)) != MUON_OK ||
-      (st = check_ws(ws, ws_bytes, N, V, D, c.terms)) != MUON_OK || (st = device_check()) != MUON_OK)
-    return st;
+  if ((st = check_outputs(h, w, dh, dhdt, lddh, dw, dwdt, lddw, N, D, &c.terms)) != MUON_OK) return st;
   c.h = static_cast<const char *>(h);
   c.w = static_cast<const char *>(w);
   c.ldh = ldh;
@@ -1307,7 +1312,7 @@ muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t
   c.accumulate = accumulate != 0;
   c.ws = static_cast<char *>(ws);
   c.backward = true;
-  return run(c, reinterpret_cast<cudaStream_t>(stream));
+  return check_and_run(c, ws_bytes, stream);
 }
 
 muon_status linear_cross_entropy_forward_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w,
@@ -1321,9 +1326,7 @@ muon_status linear_cross_entropy_forward_backward(const void *h, muon_dtype hdt,
   Call c{};
   if ((N > 0 && (losses == nullptr || lse == nullptr)) || !std::isfinite(grad_scale)) return MUON_ERR_INVALID_ARG;
   if (!aligned(losses, 4) || !aligned(lse, 4)) return MUON_ERR_ALIGNMENT;
-  if ((st = check_outputs(dh, dhdt, lddh, dw, dwdt, lddw, N, D, &c.terms)) != MUON_OK ||
-      (st = check_ws(ws, ws_bytes, N, V, D, c.terms)) != MUON_OK || (st = device_check()) != MUON_OK)
-    return st;
+  if ((st = check_outputs(h, w, dh, dhdt, lddh, dw, dwdt, lddw, N, D, &c.terms)) != MUON_OK) return st;
   c.h = static_cast<const char *>(h);
   c.w = static_cast<const char *>(w);
   c.ldh = ldh;
@@ -1346,7 +1349,7 @@ muon_status linear_cross_entropy_forward_backward(const void *h, muon_dtype hdt,
   c.accumulate = accumulate != 0;
   c.ws = static_cast<char *>(ws);
   c.forward = c.backward = true;
-  return run(c, reinterpret_cast<cudaStream_t>(stream));
+  return check_and_run(c, ws_bytes, stream);
 }
 
 muon_status muon_debug_loss_rows(int64_t rows) {

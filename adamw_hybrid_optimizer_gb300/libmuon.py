@@ -391,11 +391,14 @@ def make_adamw8_tensors(specs):
                                ctypes.pointer(hp))
         keep += [p, g, m, v, s, hp] + ([ms] if ms is not None else [])
     arr.tensors = keep
+    arr.device = _one_device(where, *(t for t in keep if not isinstance(t, adamw_hparams))) if keep else None
     return arr
 
 
 def adamw8_step_grouped(tensors, stream=None):
-    """tensors: a ctypes adamw8_tensor array (see make_adamw8_tensors)."""
+    """tensors: a ctypes adamw8_tensor array (see make_adamw8_tensors), on the current device."""
+    if tensors.device is not None:
+        _check_current("adamw8_step_grouped", tensors.device)
     _check(lib().adamw8_step_grouped(tensors, len(tensors), _current_stream(stream)), "adamw8_step_grouped")
 
 
@@ -451,6 +454,25 @@ def _current_stream(stream) -> int:
         import torch
         _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     return _raw_stream[0](_raw_stream[1]())
+
+
+def _current_device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
+def _one_device(where: str, *tensors) -> int:
+    """The device of tensors that must all be on one."""
+    device, *others = {t.get_device() for t in tensors if t is not None}
+    if others:
+        raise ValueError(f"{where}: tensors on several devices")
+    return device
+
+
+def _check_current(where: str, device: int):
+    """Kernels run on the current device: on another one's memory they would fault."""
+    if device != _current_device():
+        raise ValueError(f"{where}: tensors on device {device}, which is not the current CUDA device")
 
 
 def _itype_code(t) -> int:
@@ -613,11 +635,13 @@ def linear_cross_entropy_workspace_bytes(N: int, V: int, D: int, terms: int) -> 
     return int(lib().linear_cross_entropy_workspace_bytes(int(N), int(V), int(D), int(terms)))
 
 
-def _linear_ce(where, h, w, targets, weights):
+def _linear_ce(where, h, w, targets, weights, *others):
     (N, D), V = h.shape, w.shape[0]
-    return (N, V, D), (h.data_ptr(), _dtype_code(h), _matrix(h, "h", where), w.data_ptr(), _dtype_code(w),
-                       _matrix(w, "w", where, (V, D)), _vector(targets, "targets", where, N), _itype_code(targets),
-                       _vector(weights, "weights", where, N, True))
+    head = (h.data_ptr(), _dtype_code(h), _matrix(h, "h", where), w.data_ptr(), _dtype_code(w),
+            _matrix(w, "w", where, (V, D)), _vector(targets, "targets", where, N), _itype_code(targets),
+            _vector(weights, "weights", where, N, True))
+    _check_current(where, _one_device(where, h, w, targets, weights, *others))
+    return (N, V, D), head
 
 
 def _linear_ce_gradients(where, dh, dw, sizes, accumulate):
@@ -633,7 +657,7 @@ def linear_cross_entropy_forward(h, w, targets, weights, losses, lse, ws, stream
 
     h (N, D) and w (V, D) bf16; targets int32 or int64 (N); weights None or fp32 (N); losses, lse fp32 (N)."""
     where = "linear_cross_entropy_forward"
-    sizes, head = _linear_ce(where, h, w, targets, weights)
+    sizes, head = _linear_ce(where, h, w, targets, weights, losses, lse, ws)
     st = lib().linear_cross_entropy_forward(*head, _vector(losses, "losses", where, sizes[0], True),
                                             _vector(lse, "lse", where, sizes[0], True), *sizes, *_workspace(ws, where),
                                             _current_stream(stream))
@@ -644,7 +668,7 @@ def linear_cross_entropy_backward(h, w, targets, weights, lse, grad, dh, dw, ws,
     """dh and dw (either may be None) from the forward pass's lse and the gradient of each row's loss: grad None (all 1) or fp32
     (N). accumulate=True adds dw to what it holds."""
     where = "linear_cross_entropy_backward"
-    sizes, head = _linear_ce(where, h, w, targets, weights)
+    sizes, head = _linear_ce(where, h, w, targets, weights, lse, grad, dh, dw, ws)
     st = lib().linear_cross_entropy_backward(*head, _vector(lse, "lse", where, sizes[0], True),
                                              _vector(grad, "grad", where, sizes[0], True),
                                              *_linear_ce_gradients(where, dh, dw, sizes, accumulate),
@@ -656,7 +680,7 @@ def linear_cross_entropy_forward_backward(h, w, targets, weights, grad_scale: fl
                                           accumulate: bool = False, stream=None):
     """linear_cross_entropy_forward and linear_cross_entropy_backward (with grad_scale for every row's grad) in one call."""
     where = "linear_cross_entropy_forward_backward"
-    sizes, head = _linear_ce(where, h, w, targets, weights)
+    sizes, head = _linear_ce(where, h, w, targets, weights, losses, lse, dh, dw, ws)
     st = lib().linear_cross_entropy_forward_backward(*head, grad_scale, _vector(losses, "losses", where, sizes[0], True),
                                                      _vector(lse, "lse", where, sizes[0], True),
                                                      *_linear_ce_gradients(where, dh, dw, sizes, accumulate),

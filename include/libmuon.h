@@ -453,17 +453,17 @@ muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t
  *   ws      device workspace of ws_bytes >= linear_cross_entropy_workspace_bytes(N, V, D, terms), terms as the call needs
  *           them, 256-byte aligned, zero-filled before its first use; its first 256 bytes are the control block that
  *           muon_check reads.
- * Limits: N, V <= 2^26, N * V <= 2^40, D <= 65536 (MUON_ERR_SHAPE). The same inputs give the same bits. */
+ * Limits: N, V <= 2^26, N * V <= 2^40, D <= 65536, ldh, ldw <= 2^37 (MUON_ERR_SHAPE). The same inputs give the same bits. */
 muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
                                          int64_t ldw, const void *targets, muon_itype itype, const float *weights,
                                          float *losses, float *lse, int64_t N, int64_t V, int64_t D, void *ws,
                                          size_t ws_bytes, muon_stream_t stream);
 
 /* Bytes of workspace. terms: 0 for linear_cross_entropy_forward; 1 for the calls with gradients if both are bf16; 2 if one
- * is fp32. The call without gradients takes any of them. A piece has at most 2^30 logits, or 256 rows: without gradients 8
- * bytes for each 128 of them; with gradients 2 * terms bytes more for each, what dh's or dw's fp32 sums need where few tiles
- * share a long contraction, and, for more than one piece, fp32 sums of dw. 0 for N < 0, V < 1, D < 1, sizes beyond the limits
- * or other terms. */
+ * is fp32. The call without gradients takes any of them. A piece has at most 2^30 logits and elements of h, or 256 rows:
+ * without gradients 8 bytes for each 128 logits (64 where a piece has up to 128 rows); with gradients 2 * terms bytes more for
+ * each logit and a copy of h, what dh's or dw's fp32 sums need where few tiles share a long contraction, and, for more than one
+ * piece, fp32 sums of dw. 0 for N < 0, V < 1, D < 1, sizes beyond the limits or other terms. */
 size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int terms);
 
 /* Its gradients from linear_cross_entropy_forward's lse: with dz_iv = grad_i * weights_i * (exp(z_iv - lse_i) -
@@ -472,7 +472,7 @@ size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int
  * which doubles the work of both products. Sums are fp32.
  *   grad    device fp32, N: the gradient that reaches each row's loss, or NULL (all 1).
  *   dh      device N x D of dhdt, pitch lddh, or NULL.   dw  device V x D of dwdt, pitch lddw, or NULL (not both NULL);
- *           neither may overlap h or w.
+ *           they may overlap neither each other nor h or w (MUON_ERR_INVALID_ARG where they start at one place).
  *   accumulate  0: dw is written. Else: the sums are added to what it holds (dh is written in either case). */
 muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
                                           int64_t ldw, const void *targets, muon_itype itype, const float *weights,

@@ -340,3 +340,70 @@ def test_wide_rows(L):
     torch.cuda.synchronize()
     check_forward(c, ref)
     check_gradients(c, ref, 1.0, dh, dw, 1)
+
+
+def test_two_streams_at_once(L):
+    """Calls with workspaces of their own, in flight together."""
+    cases = [Case(300, 3001, 96, seed=20), Case(90, 2500, 128, seed=21)]
+    want, got, spaces = [], [], []
+    for c in cases:
+        spaces.append(c.ws(L, 1))
+        want.append(outputs(c))
+        L.linear_cross_entropy_forward_backward(c.h, c.w, c.t, c.weights, 1.0, c.losses, c.lse, *want[-1], spaces[-1])
+        got.append(outputs(c))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        for c, s, g, ws in zip(cases, streams, got, spaces):
+            L.linear_cross_entropy_forward_backward(c.h, c.w, c.t, c.weights, 1.0, c.losses, c.lse, *g, ws, stream=s)
+    torch.cuda.synchronize()
+    for w, g, ws in zip(want, got, spaces):
+        assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1]) and L.muon_check(ws) == L.MUON_OK
+
+
+@pytest.mark.parametrize("N", [2047, 2048, 2305, 2600, 4100])
+def test_halves(L, N):
+    """From 2048 rows on the joint call goes by halves, the second of them short or left out; the losses are those of the
+    forward call, bit for bit."""
+    c = Case(N, 1030, 72, seed=N)
+    ref = c.oracle(np.full(N, 0.5))
+    dh, dw = outputs(c)
+    ws = c.ws(L, 1)
+    L.linear_cross_entropy_forward_backward(c.h, c.w, c.t, c.weights, 0.5, c.losses, c.lse, dh, dw, ws)
+    torch.cuda.synchronize()
+    check_forward(c, ref)
+    check_gradients(c, ref, 0.5, dh, dw, 1)
+    losses = c.losses.clone()
+    L.linear_cross_entropy_forward(c.h, c.w, c.t, c.weights, c.losses, c.lse, ws)
+    assert torch.equal(losses, c.losses)
+    alone = outputs(c)[1]
+    L.linear_cross_entropy_forward_backward(c.h, c.w, c.t, c.weights, 0.5, c.losses, c.lse, None, alone, ws)
+    assert torch.equal(alone, dw)
+
+
+@pytest.mark.parametrize("N", [1, 7, 8, 9, 64, 127, 128, 129])
+@pytest.mark.parametrize("V,D", [(3, 200), (64, 64), (65, 72), (5003, 40)])
+def test_few_rows(L, N, V, D):
+    """A CTA alone, whose stages hold only the rows that there are, and the first size of the other kind."""
+    c = Case(N, V, D, seed=N + V)
+    ref = c.oracle(f64(c.grad))
+    c.lse.copy_(torch.from_numpy(ref["lse"]).float())
+    for dt in (BF, F):
+        terms = 2 if dt == F else 1
+        ws = c.ws(L, terms)
+        dh, dw = outputs(c, dt, dt)
+        L.linear_cross_entropy_backward(c.h, c.w, c.t, c.weights, c.lse, c.grad, dh, dw, ws)
+        torch.cuda.synchronize()
+        check_gradients(c, ref, f64(c.grad), dh, dw, terms)
+    dh, dw = outputs(c)
+    L.linear_cross_entropy_forward_backward(c.h, c.w, c.t, c.weights, 1.0, c.losses, c.lse, dh, dw, ws)
+    torch.cuda.synchronize()
+    ref = c.oracle()
+    check_forward(c, ref)
+    check_gradients(c, ref, 1.0, dh, dw, 1)
+
+
+def test_another_device_is_refused(L):
+    c = Case(20, 30, 16, seed=1)
+    with pytest.raises(ValueError):
+        L.linear_cross_entropy_forward(c.h, c.w.cpu(), c.t, c.weights, c.losses, c.lse, c.ws(L, 0))

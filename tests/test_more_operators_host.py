@@ -10,7 +10,7 @@ from adamw_hybrid_optimizer_gb300 import libmuon as L
 from oracle import adamw as o32
 from oracle import adamw8 as o8
 from oracle import operators as ops
-from tests.test_operators_checks import OnDevice
+from tests.test_operators_checks import OnDevice as OnSomeDevice
 from tests.test_operators_devices import fake, objects  # noqa: F401
 
 FAKE = 1 << 20
@@ -22,6 +22,15 @@ BF, F = L.MUON_BF16, L.MUON_F32
 def built():
     import __graft_entry__
     __graft_entry__.build()
+
+
+class OnDevice(OnSomeDevice):
+    def __init__(self, *shape, device=0, **kw):
+        super().__init__(*shape, **kw)
+        self.device = device
+
+    def get_device(self):
+        return self.device
 
 
 @pytest.fixture
@@ -36,6 +45,7 @@ def calls(monkeypatch):
             return lambda *args: made.append((name, args)) or L.MUON_OK
 
     monkeypatch.setattr(L, "lib", lambda: Recorder())
+    monkeypatch.setattr(L, "_current_device", lambda: 0)
     return made
 
 
@@ -89,8 +99,8 @@ def test_oracle_scales_follow_the_largest_and_leave_out_what_is_not_finite():
 
 # ---------------------------------------------------------------------------------------- cross entropy: refusals
 
-def _ce(form, h=FAKE, hdt=BF, ldh=16, w=FAKE, wdt=BF, ldw=16, t=FAKE, it=0, wt=FAKE, losses=FAKE, lse=FAKE, grad=FAKE,
-        dh=FAKE, dhdt=BF, lddh=16, dw=FAKE, dwdt=BF, lddw=16, acc=0, N=4, V=30, D=16, ws=FAKE, nb=None, scale=1.0):
+def _ce(form, h=FAKE, hdt=BF, ldh=16, w=2 * FAKE, wdt=BF, ldw=16, t=FAKE, it=0, wt=FAKE, losses=FAKE, lse=FAKE, grad=FAKE,
+        dh=3 * FAKE, dhdt=BF, lddh=16, dw=4 * FAKE, dwdt=BF, lddw=16, acc=0, N=4, V=30, D=16, ws=FAKE, nb=None, scale=1.0):
     lib = L.lib()
     terms = 0 if form == "fwd" else 2 if F in (dhdt, dwdt) else 1
     nb = lib.linear_cross_entropy_workspace_bytes(max(N, 0), max(V, 1), max(D, 1), terms) if nb is None else nb
@@ -115,6 +125,7 @@ def test_cross_entropy_refusals(form):
     assert f(N=-1) == L.MUON_ERR_INVALID_ARG and f(V=0) == L.MUON_ERR_INVALID_ARG and f(D=0) == L.MUON_ERR_INVALID_ARG
     assert f(ldh=15) == L.MUON_ERR_INVALID_ARG and f(ldw=8) == L.MUON_ERR_INVALID_ARG
     assert f(D=17) == L.MUON_ERR_INVALID_ARG
+    assert f(ldh=1 << 40) == L.MUON_ERR_SHAPE and f(ldw=1 << 40) == L.MUON_ERR_SHAPE
     assert f(N=1 << 27) == L.MUON_ERR_SHAPE and f(V=1 << 27) == L.MUON_ERR_SHAPE
     assert f(N=1 << 22, V=1 << 22) == L.MUON_ERR_SHAPE
     assert f(D=70000, ldh=70000, ldw=70000, lddh=70000, lddw=70000) == L.MUON_ERR_SHAPE
@@ -128,6 +139,8 @@ def test_cross_entropy_refusals(form):
         assert f(losses=None) == L.MUON_ERR_INVALID_ARG and f(losses=FAKE + 1) == L.MUON_ERR_ALIGNMENT
     if form != "fwd":
         assert f(dh=None, dw=None) == L.MUON_ERR_INVALID_ARG
+        for kw in (dict(dh=FAKE), dict(dw=FAKE), dict(dh=2 * FAKE), dict(dw=2 * FAKE), dict(dw=3 * FAKE)):   # in place
+            assert f(**kw) == L.MUON_ERR_INVALID_ARG
         assert f(lddh=15) == L.MUON_ERR_INVALID_ARG and f(lddw=15) == L.MUON_ERR_INVALID_ARG
         assert f(dhdt=3) == L.MUON_ERR_DTYPE and f(dwdt=3) == L.MUON_ERR_DTYPE
         assert f(dh=FAKE + 1) == L.MUON_ERR_ALIGNMENT and f(dw=FAKE + 2, dwdt=F) == L.MUON_ERR_ALIGNMENT
@@ -150,6 +163,8 @@ def test_cross_entropy_workspace_sizes():
     assert 4 * N * V <= two <= 4 * N * V + N * V // 16 + 2 * N * D + 8 * 4 * N * D + (1 << 20)
     # beyond a piece only fp32 sums of dw come on top
     assert _need(16 * N, V, D, 1) <= one + 4 * V * D + (64 << 20)
+    # a short vocabulary or a wide h: rows of a piece are bounded by whichever is larger
+    assert _need(1 << 26, 1, 8, 1) < 32 << 30 and _need(1 << 22, 100, 65536, 1) < 16 << 30
     # the call without gradients takes a workspace of any kind
     for n in (1, 100, 5000):
         assert _need(n, 5000, 64, 0) <= min(_need(n, 5000, 64, 1), _need(n, 5000, 64, 2))
@@ -176,11 +191,15 @@ def test_cross_entropy_binding_refuses_what_the_c_call_cannot_see(calls):
         L.linear_cross_entropy_forward(a["h"], a["w"], a["targets"], a["weights"], a["losses"], a["lse"], a["ws"], stream=0)
 
     for bad in (dict(w=t(30, 8)), dict(targets=t(5, dtype=i)), dict(weights=t(4)), dict(losses=t(3, dtype=f)),
-                dict(h=t(4, 16, is_cuda=False)), dict(ws=t(9, dtype=torch.uint8, is_cuda=False)), dict(lse=t(4, dtype=i))):
+                dict(h=t(4, 16, is_cuda=False)), dict(ws=t(9, dtype=torch.uint8, is_cuda=False)), dict(lse=t(4, dtype=i)),
+                dict(w=t(30, 16, device=1)), dict(ws=t(1 << 20, dtype=torch.uint8, device=1))):
         with pytest.raises((ValueError, L.MuonError)):
             go(**bad)
     with pytest.raises(L.MuonError):
         go(targets=t(4, dtype=f))
+    assert calls == []
+    with pytest.raises(ValueError, match="current"):
+        L.linear_cross_entropy_forward(*(t(*x.shape, dtype=x.dtype, device=2) for x in ok.values()), stream=0)
     assert calls == []
     go()
     go(weights=None)
@@ -243,7 +262,7 @@ def test_adamw8_launches_and_devices(fake):  # noqa: F811
             assert fake.fake_launches() - before == want
 
 
-def test_adamw8_binding_refuses_what_the_c_call_cannot_see():
+def test_adamw8_binding_refuses_what_the_c_call_cannot_see(monkeypatch):
     f8, b, f = torch.float8_e4m3fn, torch.bfloat16, torch.float32
     t = lambda *s, dtype=b, **kw: OnDevice(*s, dtype=dtype, **kw)  # noqa: E731
     hp = L.make_adamw_hparams(1e-3, 0.9, 0.95, 1e-8, 0.1, 1)
@@ -257,5 +276,10 @@ def test_adamw8_binding_refuses_what_the_c_call_cannot_see():
     for bad in ((t(300, dtype=b),), (t(299, dtype=f),)):
         with pytest.raises(ValueError):
             L.make_adamw8_tensors([ok + list(bad)])
+    with pytest.raises(ValueError, match="devices"):
+        L.make_adamw8_tensors([ok, ok[:1] + [t(300, device=1)] + ok[2:]])
+    monkeypatch.setattr(L, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current"):
+        L.adamw8_step_grouped(arr, stream=0)
     with pytest.raises(ValueError):        # a master goes with bf16 weights
         L.make_adamw8_tensors([[t(300, dtype=f)] + ok[1:] + [t(300, dtype=f)]])
