@@ -39,11 +39,16 @@ constexpr int BM = 128;                      // accumulator rows per CTA: 256 pe
 constexpr int BK = 64;
 __host__ __device__ constexpr int tile_rows(bool pair) { return pair ? 2 * BM : BM; }
 __host__ __device__ constexpr int tile_cols(bool pair) { return pair ? 256 : 128; }
-constexpr int STAGES = 6;
-constexpr int A_BYTES = BM * BK * 2;
+// How a product's rows are cut: pairs of CTAs share tiles of 256 rows, or a CTA has a tile of up to 128, or of up to
+// FEW_ROWS, alone. See ce_gemm_kernel.
+enum Shape : int { PAIRED = 0, ALONE = 1, FEW = 2 };
+constexpr int FEW_ROWS = 32;
 constexpr int B_COLS = 128;                  // of B in a CTA: half of a pair's tile
 constexpr int B_BYTES = B_COLS * BK * 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int MAX_STAGES = 9;
+__host__ __device__ constexpr int stages(int shape) { return shape == FEW ? MAX_STAGES : 6; }
+__host__ __device__ constexpr int a_bytes(int shape) { return (shape == FEW ? FEW_ROWS : BM) * BK * 2; }
+__host__ __device__ constexpr int stage_bytes(int shape) { return a_bytes(shape) + B_BYTES; }
 constexpr int EPI_WARPS = 8;
 constexpr int JOB_WARPS = 12;                // run a pass over memory beside the MMAs
 constexpr int FIRST_JOB_WARP = 2 + EPI_WARPS;
@@ -54,7 +59,6 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr long long MAX_PITCH = 1ll << 37;   // elements: a tensor map's strides are below 2^40 bytes
 constexpr long long PIECE_ELEMS = 1ll << 30; // of dz, or of h, in a piece
 constexpr long long SMS = 152;               // of a GB300: slices are counted by it, so that sums have one order
-constexpr int64_t FEW_ROWS = 128;            // up to here a CTA works alone (see ce_gemm_kernel)
 constexpr int MAX_SPLIT = 64;
 // An accumulator of the tensor cores loses up to a unit in the last place with each step of 16 products, always towards
 // zero: over a contraction of 128256 that is 2e-5 of the result (dh, 1024 x 128256 x 4096). For fp32 gradients it therefore
@@ -67,15 +71,17 @@ constexpr int SEGMENT = 32;
 enum Kind : int { LOGITS = 0, LOGITS_EXP = 1, DLOGITS = 2, DH = 3, DW = 4 };
 
 struct Ctrl {
-  uint64_t full[STAGES], empty[STAGES];
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + EPI_WARPS * BUF_BYTES + sizeof(Ctrl) + 1024;
-static_assert(sizeof(Ctrl) <= 512 && SMEM <= 232448, "shared memory over budget");
+constexpr size_t smem_bytes(int shape) {
+  return static_cast<size_t>(stages(shape)) * stage_bytes(shape) + EPI_WARPS * BUF_BYTES + sizeof(Ctrl) + 1024;
+}
+static_assert(sizeof(Ctrl) <= 512 && smem_bytes(PAIRED) <= 232448 && smem_bytes(FEW) <= 232448, "shared memory over budget");
 
 // What a row of exponentials needs to become dz: -lse log2(e), g w, and the target, -1 for a row that has no part in the
 // loss. Four floats in memory, written by ce_combine_kernel.
@@ -453,18 +459,22 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(const ScaleJob a) {
 // A: h (K-major) for the logits, DH dz (K-major), DW dz (MN-major: dz^T). B: W (K-major) for the logits, DH W and DW h
 // (MN-major). An MN-major operand is loaded as boxes of 64 columns x 64 steps.
 //
-// PAIR: the two CTAs of a pair share a tile of 256 x 256, which halves what each reads of B. Else a CTA has a tile of
-// 128 x 128 alone: for up to 128 rows, where half of a pair's MMAs would multiply rows that there are not. Its stages then hold
-// only the rows of A that there are, in eights (a_box; what else lies there makes accumulator rows that nothing reads): TMA
-// takes as long for 128-byte lines that it fills with zeros as for others, and W does not come in at full rate beside them
-// (forward, 8 x 50304 x 768: 29.9 us by pairs, 18.5 us so; 1 x 128256 x 4096: 220 and 173 us).
+// PAIRED: the two CTAs of a pair share a tile of 256 x 256, which halves what each reads of B. ALONE: a CTA has a tile of
+// 128 x 128, for up to 128 rows, where half of a pair's MMAs would multiply rows that there are not. Its stages then hold only
+// the rows of A that there are, in eights (a_box): TMA takes as long for 128-byte lines that it fills with zeros as for
+// others, and W does not come in at full rate beside them (forward, 8 x 50304 x 768: 29.9 us by pairs, 18.5 us so;
+// 1 x 128256 x 4096: 220 and 173 us). FEW: for up to 32 rows A's part of a stage is that small, and nine stages fit instead of
+// six (1 x 128256 x 4096: 170 -> 164 us, 0.94 of the copy bandwidth). The MMA reads 128 rows of A in either case: past a_box
+// it finds what else lies in the stage, which makes accumulator rows that nothing reads.
 //
 // JOB: more warps run a ScaleJob, which belongs to other rows than the product's, so that its HBM traffic passes under the
 // MMAs (8192 x 50304 x 768: 1528 -> 1360 us, 4096 x 128256 x 4096: 8.16 -> 7.93 ms). Twelve of them, since each waits for
 // its loads: 1666 us with four, 1358 with eight, 1335 with twelve on another box.
-template <int KIND, bool PAIR, bool JOB>
+template <int KIND, int SHAPE, bool JOB>
 __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __grid_constant__ CeArgs args) {
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
+  constexpr bool PAIR = SHAPE == PAIRED;
+  constexpr int STAGES = stages(SHAPE), STAGE_BYTES = stage_bytes(SHAPE), A_BYTES = a_bytes(SHAPE);
   constexpr int CTAS = PAIR ? 2 : 1, BN = tile_cols(PAIR), NC = BN / 64;   // NC: chunks of 32 columns per epilogue warp
   constexpr uint32_t TMEM_COLS = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
@@ -832,7 +842,7 @@ std::atomic<long long> g_piece_rows{0};   // muon_debug_loss_rows
 struct Plan {
   long long rows, pieces, Vp, Dp;     // rows of a piece; pitches of dz and of fp32 scratch rows
   int planes, parts, part_cols;
-  bool pair;                          // the products over rows: logits, dlogits, dh
+  int shape;                          // of the products over rows: logits, dlogits, dh
   long long half;                     // rows of a piece's first half in the joint call, or all
   int split_dh, split_half, split_dw;
   size_t partials, z_target, row_state, dz, h_live, slices, dw_sum, total;
@@ -848,8 +858,8 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms) {
   p.pieces = ceil_div(N, p.rows);
   p.Dp = round_up(D, 4);
   p.planes = terms;
-  p.pair = p.rows > FEW_ROWS;
-  p.part_cols = tile_cols(p.pair) / 2;
+  p.shape = p.rows > BM ? PAIRED : p.rows > FEW_ROWS ? ALONE : FEW;
+  p.part_cols = tile_cols(p.shape == PAIRED) / 2;
   p.parts = static_cast<int>(ceil_div(V, p.part_cols));
   size_t off = 1024;   // the control block
   auto take = [&](size_t &at, long long bytes) {
@@ -861,8 +871,8 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms) {
   if (terms > 0) {
     const long long kh = ceil_div(V, BK) * terms, kw = ceil_div(p.rows, BK) * terms;
     p.half = terms == 1 && p.rows >= HALVES ? round_up(p.rows / 2, tile_rows(true)) : p.rows;
-    p.split_dh = choose_split(p.pair, p.rows, D, kh);
-    p.split_half = choose_split(p.pair, p.half, D, kh);
+    p.split_dh = choose_split(p.shape == PAIRED, p.rows, D, kh);
+    p.split_half = choose_split(p.shape == PAIRED, p.half, D, kh);
     p.split_dw = choose_split(true, V, D, kw);
     take(p.row_state, 16 * p.rows);
     take(p.dz, 2ll * terms * p.rows * p.Vp);
@@ -880,9 +890,11 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms) {
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-template <int KIND, bool PAIR, bool JOB>
+template <int KIND, int SHAPE, bool JOB>
 muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
-  constexpr auto kernel = ce_gemm_kernel<KIND, PAIR, JOB>;
+  constexpr auto kernel = ce_gemm_kernel<KIND, SHAPE, JOB>;
+  constexpr bool PAIR = SHAPE == PAIRED;
+  constexpr size_t SMEM = smem_bytes(SHAPE);
   static AttributesSet set;
   static std::atomic<int> clusters[64];
   if (set.once([] {
@@ -933,16 +945,18 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
 }
 
 template <int KIND>
-muon_status launch_rows(bool pair, CeArgs &a, int32_t kind, cudaStream_t s) {
-  return pair ? launch_gemm<KIND, true, false>(a, kind, s) : launch_gemm<KIND, false, false>(a, kind, s);
+muon_status launch_rows(int shape, CeArgs &a, int32_t kind, cudaStream_t s) {
+  return shape == PAIRED  ? launch_gemm<KIND, PAIRED, false>(a, kind, s)
+         : shape == ALONE ? launch_gemm<KIND, ALONE, false>(a, kind, s)
+                          : launch_gemm<KIND, FEW, false>(a, kind, s);
 }
 
 // As launch_rows for a pair's tiles, with a job beside the product if there is one.
 template <int KIND>
 muon_status launch_beside(const ScaleJob *job, CeArgs &a, int32_t kind, cudaStream_t s) {
-  if (job == nullptr) return launch_gemm<KIND, true, false>(a, kind, s);
+  if (job == nullptr) return launch_gemm<KIND, PAIRED, false>(a, kind, s);
   a.job = *job;
-  return launch_gemm<KIND, true, true>(a, kind, s);
+  return launch_gemm<KIND, PAIRED, true>(a, kind, s);
 }
 
 muon_status launch_reduce(const ReduceArgs &r, int dtype, cudaStream_t s) {
@@ -1002,7 +1016,7 @@ class Run {
   bool h_map(CUtensorMap *m, long long r, long long n) const {
     return make_bf16_map(m, h_ + r * ldh_ * 2, c.D, n, 1, ldh_, ldh_, a_box());
   }
-  int a_box() const { return p.pair ? BM : static_cast<int>(round8(rows_)); }
+  int a_box() const { return p.shape == PAIRED ? BM : static_cast<int>(round8(rows_)); }
   bool w_map(CUtensorMap *m, int box) const { return make_bf16_map(m, c.w, c.D, c.V, 1, ldw_, ldw_, box); }
   bool dz_map(CUtensorMap *m, long long r, long long n, int box) const {
     return make_bf16_map(m, dz_ + r * p.Vp, c.V, n, p.planes, p.Vp, p.Vp * rows_, box);
@@ -1039,8 +1053,8 @@ class Run {
     CeArgs f;
     if (!product(f, r, n) || (keep && !dz_map(&f.map_out, r, n, 32))) return MUON_ERR_CUDA;
     muon_status st = beside != nullptr ? launch_beside<LOGITS_EXP>(beside, f, KK_CE_LOGITS, s)
-                     : keep            ? launch_rows<LOGITS_EXP>(p.pair, f, KK_CE_LOGITS, s)
-                                       : launch_rows<LOGITS>(p.pair, f, KK_CE_LOGITS, s);
+                     : keep            ? launch_rows<LOGITS_EXP>(p.shape, f, KK_CE_LOGITS, s)
+                                       : launch_rows<LOGITS>(p.shape, f, KK_CE_LOGITS, s);
     if (st != MUON_OK) return st;
     const long long own = ceil_div(n, COMBINE_ROWS), copies = keep && c.dw != nullptr ? ceil_div(n, 8) : 0;
     const CombineArgs cb{partials(r),         z_target_ + r, weights(r),
@@ -1064,7 +1078,7 @@ class Run {
     if (!product(f, 0, rows_) || !dz_map(&f.map_out, 0, rows_, 32)) return MUON_ERR_CUDA;
     f.lse = (c.forward ? c.lse : c.lse_in) + r0_;
     f.grad = c.grad != nullptr ? c.grad + r0_ : nullptr;
-    return launch_rows<DLOGITS>(p.pair, f, KK_CE_DLOGITS, s);
+    return launch_rows<DLOGITS>(p.shape, f, KK_CE_DLOGITS, s);
   }
 
   void output(CeArgs &f, void *out, int dtype, long long ld, bool cut, long long slice_rows, bool add) const {
@@ -1088,7 +1102,7 @@ class Run {
     if (!dz_map(&f.map_a, r, n, f.a_box) || !w_map(&f.map_b, BK)) return MUON_ERR_CUDA;
     const bool cut = split > 1;
     output(f, out, c.dhdt, c.lddh, cut, n, false);
-    const muon_status st = beside != nullptr ? launch_beside<DH>(beside, f, KK_CE_DH, s) : launch_rows<DH>(p.pair, f, KK_CE_DH, s);
+    const muon_status st = beside != nullptr ? launch_beside<DH>(beside, f, KK_CE_DH, s) : launch_rows<DH>(p.shape, f, KK_CE_DH, s);
     if (st != MUON_OK || !cut) return st;
     return launch_reduce(ReduceArgs{slices_, f.slice_stride, p.Dp, c.lddh, f.split, f.rows, f.cols, 0, out}, c.dhdt, s);
   }
@@ -1109,7 +1123,7 @@ class Run {
     const int dt = dw_sum_ != nullptr ? static_cast<int>(MUON_F32) : c.dwdt;
     const bool add = r0_ > 0 || (dw_sum_ == nullptr && c.accumulate), cut = p.split_dw > 1;
     output(f, sum, dt, ld, cut, c.V, add);
-    const muon_status st = launch_gemm<DW, true, false>(f, KK_CE_DW, s);
+    const muon_status st = launch_gemm<DW, PAIRED, false>(f, KK_CE_DW, s);
     if (st != MUON_OK || !cut) return st;
     return launch_reduce(ReduceArgs{slices_, f.slice_stride, p.Dp, ld, f.split, f.rows, f.cols, add, sum}, dt, s);
   }
