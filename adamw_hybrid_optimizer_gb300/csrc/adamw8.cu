@@ -68,13 +68,14 @@ __device__ __forceinline__ float2 decode2(unsigned codes) {
 __device__ __forceinline__ unsigned encode2(float2 x) { return __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3); }
 
 // The square root by one Newton step on an approximate one, in fma: with s = v y, y about 1 / sqrt(v), it is
-// s + (v - s^2) y / 2, as close as fp32 gets in all but a few cases in a million. Not for v = 0, whose root is itself.
+// s + (v - s^2) y / 2, as close as fp32 gets in all but a few cases in a million. 0 and infinity, for which that is NaN, are
+// their own roots.
 __device__ __forceinline__ float2 root2(float2 v) {
   const float2 y = make_float2(rsqrtf(v.x), rsqrtf(v.y));
   const float2 s = __fmul2_rn(v, y);
   const float2 e = __ffma2_rn(make_float2(-s.x, -s.y), s, v);
   const float2 r = __ffma2_rn(e, __fmul2_rn(y, both(0.5f)), s);
-  return make_float2(v.x > 0.f ? r.x : v.x, v.y > 0.f ? r.y : v.y);
+  return make_float2(r.x == r.x ? r.x : v.x, r.y == r.y ? r.y : v.y);
 }
 
 // To two units in the last place: the weights take it times the learning rate.

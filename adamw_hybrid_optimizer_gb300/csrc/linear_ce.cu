@@ -8,8 +8,8 @@
 //           of exponentials for each row and half tile (online softmax) and the target's logit
 //   combine the parts' pairs into lse and the loss; and h without the rows that have no part in the loss, for dw
 //   dlogits dz = g w (exp(z - lse) - [v = t]), rounded to bf16 as an operand of the two products that follow: in the joint
-//           call from the exponentials, which the logits' epilogue has kept; else from the product, computed again. For fp32
-//           gradients dz is the sum of two bf16 terms, which holds 16 bits of it, and always from the product
+//           call of wide rows from the exponentials, which the logits' epilogue has kept; else from the product, computed
+//           again. For fp32 gradients dz is the sum of two bf16 terms, which holds 16 bits of it, and always from the product
 //   dh      dz W, the contraction over V cut into slices where the tiles alone would leave SMs without work
 //   dw      dz^T h, added up over the pieces in fp32
 //   reduce  adds slices in their order and rounds once
@@ -54,6 +54,10 @@ constexpr int JOB_WARPS = 12;                // run a pass over memory beside th
 constexpr int FIRST_JOB_WARP = 2 + EPI_WARPS;
 __host__ __device__ constexpr int gemm_threads(bool job) { return 32 * (FIRST_JOB_WARP + (job ? JOB_WARPS : 0)); }
 constexpr int BUF_BYTES = 32 * 128;          // an epilogue warp's staging: 32 rows of 128 bytes
+// Widths from which on the joint call keeps the exponentials rather than computing the logits twice: what they cost in memory
+// does not depend on the width (8192 x 32000: 541 us against 402 at 64, 672 and 620 at 384, 706 and 739 at 512; 8192 x 50304 x
+// 768: 1382 and 1624 us).
+constexpr int KEEP_WIDTH = 512;
 constexpr int GROUP = 16;                    // row tiles that take a column of tiles together
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr long long MAX_PITCH = 1ll << 37;   // elements: a tensor map's strides are below 2^40 bytes
@@ -97,7 +101,7 @@ struct ScaleJob {
   long long ld;
   const float2 *partials;      // [parts][rows]
   const float4 *row_state;
-  int rows, cols, part_shift;
+  int rows, cols, part_cols;
 };
 
 struct CeArgs {
@@ -170,50 +174,58 @@ __device__ __forceinline__ unsigned pack2_half(float a, float b) {
 }
 
 // One tile's part of a warp (32 NC columns from col0) as its maximum and the sum of its exponentials relative to that, for
-// each row; with KEEP the exponentials too, in fp16: none is above 1, so 2^-12 of each is kept, or 2^-25 of the largest.
+// each row; with KEEP the exponentials too, in fp16: none is above 1, so 2^-12 of each is kept, or 2^-25 of the largest. The
+// accumulators are read twice, since a thread has no room for a part's 128: 64 columns at a time, or 32 where warps beside
+// the product leave 80 registers. Both add in the same order. (8192 x 32000 x 64, where there is little else to do: 91 us
+// forward by 64 columns and in pairs, 115 us by 32 and one by one.)
 template <bool KEEP, int NC>
-__device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, int row, int warp_row0, int col0, int part,
-                                                int lane, uint8_t *buf) {
+__device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, int row, int warp_row0, int col0, int lane,
+                                                uint8_t *buf) {
+  constexpr int W = KEEP ? 32 : 64;
   if (col0 >= a.cols || warp_row0 >= a.rows) return;
-  const long long t = row < a.rows ? target_of(a.targets, a.itype, row) - col0 : -1;
-  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  const int left = a.cols - col0;   // columns that there are
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    float v[32];
+  const long long t = row < a.rows ? target_of(a.targets, a.itype, row) : -1;
+  float v[W];
+  auto fetch = [&](int c) {   // columns W c .. of the part; -inf past the last
+    uint32_t r[W / 32][32];
     __syncwarp();
-    tmem_ld_32x32b_x32(tmem + 32 * c, v);
-    if (32 * c + 32 <= left) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
-    } else {
+    for (int q = 0; q < W / 32; ++q) tmem_ld_32x32b_x32_async(tmem + W * c + 32 * q, r[q]);
+    tmem_ld_wait();
+    const int left = a.cols - col0 - W * c;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) top[j & 3] = 32 * c + j < left ? fmaxf(top[j & 3], v[j]) : top[j & 3];
+    for (int j = 0; j < W; ++j) v[j] = __uint_as_float(r[j / 32][j % 32]);
+    if (left < W) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[j] = j < left ? v[j] : -INFINITY;
     }
-    const long long hit = t - 32 * c;
-    if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
+  };
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 32 * NC / W; ++c) {
+    fetch(c);
+#pragma unroll
+    for (int j = 0; j < W; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+    const long long hit = t - col0 - W * c;
+    if (__any_sync(0xffffffffu, hit >= 0 && hit < W)) {
       float z = 0.f;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) z = hit == j ? v[j] : z;
-      if (hit >= 0 && hit < 32 && t < left) a.z_target[row] = z;
+      for (int j = 0; j < W; ++j) z = hit == j ? v[j] : z;
+      if (hit >= 0 && hit < W && t < a.cols) a.z_target[row] = z;
     }
   }
   const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   const float ref = m == -INFINITY ? 0.f : m * LOG2E;   // nothing above -inf: exponentials of zero
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    float v[32];
-    __syncwarp();
-    tmem_ld_32x32b_x32(tmem + 32 * c, v);
+  for (int c = 0; c < 32 * NC / W; ++c) {
+    if (32 * NC > W) fetch(c);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
-    if (32 * c + 32 > left) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = 32 * c + j < left ? v[j] : 0.f;
+    for (int j = 0; j < W; j += 2) {
+      const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), make_float2(LOG2E, LOG2E), make_float2(-ref, -ref));
+      v[j] = exp2_fast(x.x);
+      v[j + 1] = exp2_fast(x.y);
+      sum[j / 2 % 2] = __fadd2_rn(sum[j / 2 % 2], make_float2(v[j], v[j + 1]));
     }
-#pragma unroll
-    for (int j = 0; j < 32; ++j) sum[j & 3] += v[j];
     if constexpr (KEEP) {
       if (c % 2 == 0) {
         if (lane == 0) bulk_wait_group_read<0>();   // the buffer's last store has read it
@@ -225,17 +237,19 @@ __device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, 
             make_uint4(pack2_half(v[8 * q], v[8 * q + 1]), pack2_half(v[8 * q + 2], v[8 * q + 3]),
                        pack2_half(v[8 * q + 4], v[8 * q + 5]), pack2_half(v[8 * q + 6], v[8 * q + 7]));
       if (c % 2 == 1) {
+        const int c0 = col0 + 32 * (c - 1);
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0 && 32 * (c - 1) < left) {
-          tma_store_3d(&a.map_out, buf, col0 + 32 * (c - 1), warp_row0, 0);
+        if (lane == 0 && c0 < a.cols) {
+          tma_store_3d(&a.map_out, buf, c0, warp_row0, 0);
           bulk_commit_group();
         }
       }
     }
   }
   if (row < a.rows)
-    a.partials[static_cast<long long>(part) * a.rows + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    a.partials[static_cast<long long>(col0 / (32 * NC)) * a.rows + row] =
+        make_float2(m, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
 }
 
 // One tile's part of a warp as dz, in bf16 terms, through the staging buffer and TMA (which leaves out what lies past the
@@ -316,8 +330,7 @@ __device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec
 }
 
 // One tile's part of a warp as rows of the output: lines of 128 bytes (64 bf16 or 32 fp32 values) through the staging
-// buffer and TMA where the output's rows are 16-byte aligned (add: to fp32 values that are there). Else 32 columns of fp32 at a time
-// through the buffer, so that eight lanes write 128 bytes of a row (64 as bf16).
+// buffer and TMA, where the output's rows are 16-byte aligned. add: to fp32 values that are there.
 template <int NC>
 __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
                                                  uint8_t *buf, bool add) {
@@ -361,6 +374,8 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
   }
 }
 
+// As above for any other output: 32 columns of fp32 at a time through the buffer, so that eight lanes write 128 bytes of a
+// row (four lanes 64 as bf16).
 template <int NC>
 __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
                                              uint8_t *buf, bool accumulate) {
@@ -420,7 +435,7 @@ __device__ __forceinline__ void scale_units(const ScaleJob &a, long long first, 
     if (c0 >= a.cols) continue;
     const int r0 = group * SCALE_ROWS;
     uint16_t *x = a.x + r0 * a.ld + c0;
-    const float2 *part = a.partials + static_cast<long long>(c0 >> a.part_shift) * a.rows;
+    const float2 *part = a.partials + static_cast<long long>(c0 / a.part_cols) * a.rows;
     uint4 e[SCALE_ROWS];
     float4 state[SCALE_ROWS];
     float m[SCALE_ROWS];
@@ -647,7 +662,7 @@ __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __g
         tc_fence_after();
         const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 32 * NC * half;
         if constexpr (KIND == LOGITS || KIND == LOGITS_EXP)
-          epilogue_logits<KIND == LOGITS_EXP, NC>(args, tmem, warp_row0 + lane, warp_row0, col0, 2 * tj + half, lane, buf);
+          epilogue_logits<KIND == LOGITS_EXP, NC>(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
         else if constexpr (KIND == DLOGITS)
           epilogue_dlogits<NC>(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
         else if (args.tma)
@@ -841,7 +856,7 @@ std::atomic<long long> g_piece_rows{0};   // muon_debug_loss_rows
 
 struct Plan {
   long long rows, pieces, Vp, Dp;     // rows of a piece; pitches of dz and of fp32 scratch rows
-  int planes, parts, part_cols;
+  int planes, parts, part_cols;       // a part: the columns of a tile whose exponentials share a maximum
   int shape;                          // of the products over rows: logits, dlogits, dh
   long long half;                     // rows of a piece's first half in the joint call, or all
   int split_dh, split_half, split_dw;
@@ -877,7 +892,8 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms) {
     take(p.row_state, 16 * p.rows);
     take(p.dz, 2ll * terms * p.rows * p.Vp);
     take(p.h_live, 2 * p.rows * round8(D));
-    const long long dh = 4 * p.Dp * std::max(p.split_dh > 1 ? p.split_dh * p.rows : 0, p.split_half > 1 ? p.split_half * p.half : 0);
+    const long long dh =
+        4 * p.Dp * std::max(p.split_dh > 1 ? p.split_dh * p.rows : 0, p.split_half > 1 ? p.split_half * p.half : 0);
     const long long dw = p.split_dw > 1 ? 4ll * p.split_dw * V * p.Dp : 0;
     take(p.slices, std::max(dh, dw));
     if (p.pieces > 1) take(p.dw_sum, 4ll * V * p.Dp);
@@ -898,8 +914,7 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   static AttributesSet set;
   static std::atomic<int> clusters[64];
   if (set.once([] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(SMEM));
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM));
       }) != cudaSuccess)
     return MUON_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -951,10 +966,9 @@ muon_status launch_rows(int shape, CeArgs &a, int32_t kind, cudaStream_t s) {
                           : launch_gemm<KIND, FEW, false>(a, kind, s);
 }
 
-// As launch_rows for a pair's tiles, with a job beside the product if there is one.
+// As launch_rows for a pair's tiles, with a job beside the product.
 template <int KIND>
 muon_status launch_beside(const ScaleJob *job, CeArgs &a, int32_t kind, cudaStream_t s) {
-  if (job == nullptr) return launch_gemm<KIND, PAIRED, false>(a, kind, s);
   a.job = *job;
   return launch_gemm<KIND, PAIRED, true>(a, kind, s);
 }
@@ -1033,7 +1047,7 @@ class Run {
   float2 *partials(long long r) const { return partials_ + r * p.parts; }
   ScaleJob job(long long r, long long n) const {
     return ScaleJob{reinterpret_cast<uint16_t *>(dz_ + r * p.Vp), p.Vp, partials(r), row_state_ + r, static_cast<int>(n),
-                    static_cast<int>(c.V), p.part_cols == 128 ? 7 : 6};
+                    static_cast<int>(c.V), p.part_cols};
   }
   bool product(CeArgs &f, long long r, long long n) const {
     f = base_;
@@ -1102,7 +1116,8 @@ class Run {
     if (!dz_map(&f.map_a, r, n, f.a_box) || !w_map(&f.map_b, BK)) return MUON_ERR_CUDA;
     const bool cut = split > 1;
     output(f, out, c.dhdt, c.lddh, cut, n, false);
-    const muon_status st = beside != nullptr ? launch_beside<DH>(beside, f, KK_CE_DH, s) : launch_rows<DH>(p.shape, f, KK_CE_DH, s);
+    const muon_status st =
+        beside != nullptr ? launch_beside<DH>(beside, f, KK_CE_DH, s) : launch_rows<DH>(p.shape, f, KK_CE_DH, s);
     if (st != MUON_OK || !cut) return st;
     return launch_reduce(ReduceArgs{slices_, f.slice_stride, p.Dp, c.lddh, f.split, f.rows, f.cols, 0, out}, c.dhdt, s);
   }
@@ -1150,8 +1165,8 @@ class Run {
 
   muon_status piece() {
     muon_status st;
-    // one bf16 term: the exponentials are kept in dz's place; two: the logits are computed again
-    const bool keep = c.forward && c.backward && p.planes == 1;
+    // the exponentials are kept in dz's place, or the logits are computed again
+    const bool keep = c.forward && c.backward && p.planes == 1 && c.D >= KEEP_WIDTH;
     if (keep) {
       if ((st = joint()) != MUON_OK) return st;
     } else {

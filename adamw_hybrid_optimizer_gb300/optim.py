@@ -9,10 +9,11 @@ caller decides by the group's kind, and a Muon group must hold 2-D tensors only.
 
 Muon matrices of one group are bucketed by shape (muon_plan_buckets); each bucket owns one fp32
 (K, A, B) momentum stack, and all buckets of a group are updated by one muon_step_grouped call per
-step. AdamW state is one fp32 exp_avg / exp_avg_sq pair per tensor (or one in 8 bits, state_bits=8) and the group's step count. With
-master_weights=True (bf16 parameters), each parameter also keeps an fp32 master copy ("master" in its
-state) that takes the update; the parameter holds it rounded to bf16. All arithmetic runs in libmuon: the
-AdamW tensors of all groups in one grouped pass, issued with the last Muon group by hybrid_step.
+step. AdamW state is one fp32 exp_avg / exp_avg_sq pair per tensor (or one in 8 bits, with state_bits=8) and the
+group's step count. With master_weights=True (bf16 parameters), each parameter also keeps an fp32 master copy
+("master" in its state) that takes the update; the parameter holds it rounded to bf16. All arithmetic runs in
+libmuon: the AdamW tensors of all groups in one grouped pass, issued with the last Muon group by hybrid_step, and
+those with 8-bit moments in another.
 """
 from __future__ import annotations
 
