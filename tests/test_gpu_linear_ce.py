@@ -271,6 +271,25 @@ def test_outputs_of_any_pitch_and_place(L, dt, extra, off):
         assert (b == 7.0).all()
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("N,V", [(6, 29), (150, 270), (3, 20011)])
+@pytest.mark.parametrize("D,pitch", [(1, 8), (3, 8), (5, 8), (8, 16), (9, 16), (77, 80), (76, 88), (259, 264)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_what_lies_between_aligned_rows_stays(L, dt, N, V, D, pitch, accumulate):
+    """Rows on 16-byte boundaries whose width is no multiple of 16 bytes: their padding belongs to the caller."""
+    c = Case(N, V, D, seed=D)
+    bufs = [torch.full((rows, pitch), 7.0, dtype=dt, device=DEV) for rows in (N, V)]
+    dh, dw = (b[:, :D] for b in bufs)
+    terms = 2 if dt == F else 1
+    L.linear_cross_entropy_forward_backward(c.h, c.w, c.t, c.weights, 1.0, c.losses, c.lse, dh, dw, c.ws(L, terms),
+                                            accumulate=accumulate)
+    torch.cuda.synchronize()
+    check_gradients(c, c.oracle(), 1.0, dh, dw, terms, np.full((V, D), 7.0) if accumulate else None)
+    for b in bufs:
+        b[:, :D] = 7.0
+        assert (b == 7.0).all()
+
+
 def test_one_gradient_of_the_two(L):
     c = Case(90, 411, 64, seed=10)
     ref = c.oracle()
