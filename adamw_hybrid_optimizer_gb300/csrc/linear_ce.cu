@@ -1298,7 +1298,9 @@ extern "C" {
 
 size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int terms) {
   if (check_sizes(N, V, D) != MUON_OK || terms < 0 || terms > 2) return 0;
-  return plan(N, V, D, terms).total;
+  size_t most = 0;   // a call with fewer terms splits differently: its slices can be more than dz saves
+  for (int t = 0; t <= terms; ++t) most = std::max(most, plan(N, V, D, t).total);
+  return most;
 }
 
 muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,

@@ -460,7 +460,7 @@ muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t 
                                          size_t ws_bytes, muon_stream_t stream);
 
 /* Bytes of workspace. terms: 0 for linear_cross_entropy_forward; 1 for the calls with gradients if both are bf16; 2 if one
- * is fp32. The call without gradients takes any of them. A piece has at most 2^30 logits and elements of h, or 256 rows:
+ * is fp32. A call also takes a workspace for more terms than its own. A piece has at most 2^30 logits and elements of h, or 256 rows:
  * without gradients 8 bytes for each 128 logits (64 where a piece has up to 128 rows); with gradients 2 * terms bytes more for
  * each logit and a copy of h, what dh's or dw's fp32 sums need where few tiles share a long contraction, and, for more than one
  * piece, fp32 sums of dw. 0 for N < 0, V < 1, D < 1, sizes beyond the limits or other terms. */

@@ -117,6 +117,12 @@ def _need(N=4, V=30, D=16, terms=0):
     return L.linear_cross_entropy_workspace_bytes(N, V, D, terms)
 
 
+@pytest.mark.parametrize("N,V,D", [(2330, 2529, 843), (2400, 2940, 1257), (16, 32000, 1024), (1, 1, 1), (9000, 100, 8)])
+def test_cross_entropy_workspace_serves_calls_with_fewer_terms(N, V, D):
+    need = [_need(N, V, D, terms) for terms in range(3)]
+    assert 0 < need[0] <= need[1] <= need[2]
+
+
 @pytest.mark.parametrize("form", ["fwd", "bwd", "step"])
 def test_cross_entropy_refusals(form):
     f = lambda **kw: _ce(form, **kw)  # noqa: E731
