@@ -124,8 +124,7 @@ struct CeArgs {
   // DH, DW
   void *out;
   long long ld_out, slice_stride;      // elements; slice s goes to out + s * slice_stride
-  int out_f32, accumulate, vec;
-  int tma;                             // columns that leave by TMA, or 0
+  int out_f32, accumulate, vec, tma;
   ScaleJob job;
   uint32_t *err;
   unsigned long long timeout_ns;
@@ -331,9 +330,7 @@ __device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec
 }
 
 // One tile's part of a warp as rows of the output: lines of 128 bytes (64 bf16 or 32 fp32 values) through the staging
-// buffer and TMA, where the output's rows are 16-byte aligned. add: to fp32 values that are there. TMA ends a row at the next
-// 16-byte boundary, past its last value: it gets the columns that fill 16 bytes (a.tma of them), and the rest of a row is
-// written by the row's thread.
+// buffer and TMA, where the output's rows are 16-byte aligned. add: to fp32 values that are there.
 template <int NC>
 __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
                                                  uint8_t *buf, bool add) {
@@ -349,19 +346,6 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
     float v[32];
     __syncwarp();
     tmem_ld_32x32b_x32(tmem + 32 * c, v);
-    if (c0 + 32 > a.tma && warp_row0 + lane < a.rows) {
-      const long long at = slice * a.slice_stride + (warp_row0 + lane) * a.ld_out + c0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (c0 + j < a.tma || c0 + j >= a.cols) continue;
-        if (a.out_f32) {
-          float *d = static_cast<float *>(a.out) + at + j;
-          *d = add ? *d + v[j] : v[j];
-        } else {
-          static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(v[j]);
-        }
-      }
-    }
     if (a.out_f32 || c % 2 == 0) {
       if (lane == 0) bulk_wait_group_read<0>();   // the buffer's last store has read it
       __syncwarp();
@@ -382,10 +366,8 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
       __syncwarp();
       if (lane == 0) {
         const int x = a.out_f32 ? c0 : c0 - 32 * (c & 1);
-        if (x < a.tma) {
-          if (add) tma_add_3d(&a.map_out, buf, x, warp_row0, slice);
-          else tma_store_3d(&a.map_out, buf, x, warp_row0, slice);
-        }
+        if (add) tma_add_3d(&a.map_out, buf, x, warp_row0, slice);
+        else tma_store_3d(&a.map_out, buf, x, warp_row0, slice);
         bulk_commit_group();
       }
     }
@@ -962,12 +944,10 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   a.k_per = static_cast<int>(ceil_div(a.k_iters, a.split));
   a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
   a.k_seg = a.out_f32 && a.planes > 1 ? SEGMENT : a.k_per;
-  if (KIND == DH || KIND == DW) {   // rows past the output's are not stored; slices follow each other
-    const int whole = a.cols - a.cols % (a.out_f32 ? 4 : 8);
-    a.tma = a.vec && (a.out_f32 || !a.accumulate) && a.ld_out <= MAX_PITCH ? whole : 0;
+  if (KIND == DH || KIND == DW) {   // rows and columns past the output's are not stored; slices follow each other
     const long long apart = a.split > 1 ? a.slice_stride : a.ld_out;   // one slice has no next one
-    if (a.tma && !(a.out_f32 ? make_f32_map(&a.map_out, a.out, whole, a.rows, a.split, a.ld_out, apart, 32)
-                             : make_bf16_map(&a.map_out, a.out, whole, a.rows, a.split, a.ld_out, apart, 32)))
+    if (a.tma && !(a.out_f32 ? make_f32_map(&a.map_out, a.out, a.cols, a.rows, a.split, a.ld_out, apart, 32)
+                             : make_bf16_map(&a.map_out, a.out, a.cols, a.rows, a.split, a.ld_out, apart, 32)))
       return MUON_ERR_CUDA;
   }
   a.total = static_cast<long long>(a.m_tiles) * a.n_tiles * a.split;
@@ -1120,7 +1100,12 @@ class Run {
     f.ld_out = cut ? p.Dp : ld;
     f.slice_stride = slice_rows * p.Dp;
     f.accumulate = cut ? 0 : add;
-    f.vec = aligned(f.out, 16) && f.ld_out % (f.out_f32 ? 4 : 8) == 0;
+    const int piece = f.out_f32 ? 4 : 8;
+    f.vec = aligned(f.out, 16) && f.ld_out % piece == 0;
+    // TMA ends a row at a 16-byte boundary. What lies between a row's end and there is padding in scratch and the caller's
+    // in dh and dw.
+    const bool padded = c.D % piece == 0 || f.out == slices_ || f.out == dw_sum_;
+    f.tma = f.vec && padded && (f.out_f32 || !f.accumulate) && f.ld_out <= MAX_PITCH;
   }
 
   muon_status dh(long long r, long long n, int split, const ScaleJob *beside) {
