@@ -168,16 +168,20 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
   return *reinterpret_cast<const unsigned *>(&h);
 }
 
-__device__ __forceinline__ unsigned pack2_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
+// Exponentials are at most 1: kept in fp16 times 2^13, they have 11 bits down to 2^-27 of the part's largest and the last at
+// 2^-37, for the gradients of columns that no row gives much. (Four times 2^13 is still finite: 1 is a power of 2 off by up to
+// 2 where z is 2^25 and its product with log2(e) rounded.)
+constexpr float KEPT = 8192.f;
+__device__ __forceinline__ unsigned pack2_kept(float a, float b) {
+  const float2 x = __fmul2_rn(make_float2(a, b), make_float2(KEPT, KEPT));
+  const __half2 h = __floats2half2_rn(x.x, x.y);
   return *reinterpret_cast<const unsigned *>(&h);
 }
 
 // One tile's part of a warp (32 NC columns from col0) as its maximum and the sum of its exponentials relative to that, for
-// each row; with KEEP the exponentials too, in fp16: none is above 1, so 2^-12 of each is kept, or 2^-25 of the largest. The
-// accumulators are read twice, since a thread has no room for a part's 128: 64 columns at a time, or 32 where warps beside
-// the product leave 80 registers. Both add in the same order. (8192 x 32000 x 64, where there is little else to do: 91 us
-// forward by 64 columns and in pairs, 115 us by 32 and one by one.)
+// each row; with KEEP the exponentials too, in fp16 (pack2_kept). The accumulators are read twice, since a thread has no room
+// for a part's 128: 64 columns at a time, or 32 where warps beside the product leave 80 registers. Both add in the same order.
+// (8192 x 32000 x 64, where there is little else to do: 91 us forward by 64 columns and in pairs, 115 us by 32 and one by one.)
 template <bool KEEP, int NC>
 __device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, int row, int warp_row0, int col0, int lane,
                                                 uint8_t *buf) {
@@ -234,8 +238,8 @@ __device__ __forceinline__ void epilogue_logits(const CeArgs &a, uint32_t tmem, 
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *piece(buf, lane, 4 * (c & 1) + q) =
-            make_uint4(pack2_half(v[8 * q], v[8 * q + 1]), pack2_half(v[8 * q + 2], v[8 * q + 3]),
-                       pack2_half(v[8 * q + 4], v[8 * q + 5]), pack2_half(v[8 * q + 6], v[8 * q + 7]));
+            make_uint4(pack2_kept(v[8 * q], v[8 * q + 1]), pack2_kept(v[8 * q + 2], v[8 * q + 3]),
+                       pack2_kept(v[8 * q + 4], v[8 * q + 5]), pack2_kept(v[8 * q + 6], v[8 * q + 7]));
       if (c % 2 == 1) {
         const int c0 = col0 + 32 * (c - 1);
         fence_proxy_async_shared();
@@ -449,7 +453,7 @@ __device__ __forceinline__ void scale_units(const ScaleJob &a, long long first, 
 #pragma unroll
     for (int i = 0; i < SCALE_ROWS; ++i) {
       const RowState r = RowState::of(state[i]);
-      const float f = r.g * exp2_fast(fmaf(m[i], LOG2E, r.base));
+      const float f = r.g * (1.f / KEPT) * exp2_fast(fmaf(m[i], LOG2E, r.base));
       const int hit = r.target - c0;
       const unsigned in[4] = {e[i].x, e[i].y, e[i].z, e[i].w};
       unsigned out[4];

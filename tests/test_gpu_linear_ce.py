@@ -290,6 +290,29 @@ def test_what_lies_between_aligned_rows_stays(L, dt, N, V, D, pitch, accumulate)
         assert (b == 7.0).all()
 
 
+@pytest.mark.parametrize("N", [40, 300])
+@pytest.mark.parametrize("below", [8.0, 16.0])
+def test_joint_gradient_of_a_column_that_no_row_gives_much(L, N, below):
+    """Column 7's logits lie about `below` under the others', whose largest is near 3: for 16 its exponentials are 2^-26.4 to
+    2^-30.5 of the largest beside them. h is positive, so nothing cancels in its gradient. Three roundings of at most half a
+    step: the exponential's, whose last bit is 2^-37, so 2^-7.5 of the smallest; dz's and the output's in bf16. And 2^-12 for
+    the logits."""
+    V, D = 500, 512
+    g = torch.Generator().manual_seed(N)
+    h = (torch.rand((N, D), generator=g) + 0.5).to(DEV, BF)
+    w = (torch.randn((V, D), generator=g) * 0.05).to(DEV, BF)
+    w[7] = -below / D
+    t = torch.randint(8, V, (N,), generator=g).to(DEV)
+    losses, lse = torch.empty(N, device=DEV), torch.empty(N, device=DEV)
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    ws = torch.zeros(L.linear_cross_entropy_workspace_bytes(N, V, D, 1), dtype=torch.uint8, device=DEV)
+    L.linear_cross_entropy_forward_backward(h, w, t, None, 1.0, losses, lse, dh, dw, ws)
+    p = torch.softmax(h.double() @ w.double().t(), 1)[:, 7]
+    want = p @ h.double()
+    err = ((dw[7].double() - want) / want).abs().max().item()
+    assert p.max().item() < 1e-3 and err <= 2.0 ** -7.5 + 2 * 2.0 ** -8 + 2.0 ** -12
+
+
 def test_one_gradient_of_the_two(L):
     c = Case(90, 411, 64, seed=10)
     ref = c.oracle()
