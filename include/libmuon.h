@@ -460,10 +460,10 @@ muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t 
                                          size_t ws_bytes, muon_stream_t stream);
 
 /* Bytes of workspace. terms: 0 for linear_cross_entropy_forward; 1 for the calls with gradients if both are bf16; 2 if one
- * is fp32. A call also takes a workspace for more terms than its own. A piece has at most 2^30 logits and elements of h, or 256 rows:
- * without gradients 8 bytes for each 128 logits (64 where a piece has up to 128 rows); with gradients 2 * terms bytes more for
- * each logit and a copy of h, what dh's or dw's fp32 sums need where few tiles share a long contraction, and, for more than one
- * piece, fp32 sums of dw. 0 for N < 0, V < 1, D < 1, sizes beyond the limits or other terms. */
+ * is fp32. A call also takes a workspace for more terms than its own. A piece has at most 2^30 logits and elements of h, or
+ * 256 rows: without gradients 8 bytes for each 128 logits (64 where a piece has up to 128 rows); with gradients 2 * terms
+ * bytes more for each logit and a copy of h, what dh's or dw's fp32 sums need where few tiles share a long contraction, and,
+ * for more than one piece, fp32 sums of dw. 0 for N < 0, V < 1, D < 1, sizes beyond the limits or other terms. */
 size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int terms);
 
 /* Its gradients from linear_cross_entropy_forward's lse: with dz_iv = grad_i * weights_i * (exp(z_iv - lse_i) -
@@ -482,7 +482,8 @@ muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t
 
 /* Both in one call, for a training step whose loss is grad_scale * sum of losses: losses and lse as
  * linear_cross_entropy_forward writes them, dh and dw as linear_cross_entropy_backward does with grad = grad_scale for every
- * row. */
+ * row; from D = 512 on and for bf16 gradients with dz from exponentials that are kept in fp16 rather than computed again, a
+ * further 2^-12 of each element. */
 muon_status linear_cross_entropy_forward_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w,
                                                   muon_dtype wdt, int64_t ldw, const void *targets, muon_itype itype,
                                                   const float *weights, float grad_scale, float *losses, float *lse,
