@@ -66,10 +66,10 @@ constexpr long long SMS = 152;               // of a GB300: slices are counted b
 constexpr int MAX_SPLIT = 64;
 // An accumulator of the tensor cores loses up to a unit in the last place with each step of 16 products, always towards
 // zero: over a contraction of 128256 that is 2e-5 of the result (dh, 1024 x 128256 x 4096). For fp32 gradients it therefore
-// adds up all of the lower term's products, which are small, and then 32 steps of 64 of the upper one's; the epilogue adds
-// that to what the output holds, rounding to nearest: 2.5e-6, of which 1.3e-6 are the two terms' own. (2048 x 50304 x 768: 657
-// us with 64 steps, 691 with 32, 764 with 16, whose error is 1.4e-6.)
-constexpr int SEGMENT = 32;
+// adds up all of the lower term's products, which are small, and then 8 steps of 64 of the upper one's; the epilogue's threads
+// add that to sums of their own, rounding to nearest (add_segment). The error is then 7e-7. (2048 x 50304 x 768: 641 us with 32
+// steps, whose error is 2.5e-6, 657 with 16 and 1.3e-6, 679 with 8, 714 with 4 and 4e-7.)
+constexpr int SEGMENT = 8;
 
 // LOGITS leaves statistics alone, LOGITS_EXP the tile's exponentials too (for the joint call).
 enum Kind : int { LOGITS = 0, LOGITS_EXP = 1, DLOGITS = 2, DH = 3, DW = 4 };
@@ -334,15 +334,11 @@ __device__ __forceinline__ void store_piece(T *dst, float *f, int left, bool vec
 }
 
 // One tile's part of a warp as rows of the output: lines of 128 bytes (64 bf16 or 32 fp32 values) through the staging
-// buffer and TMA, where the output's rows are 16-byte aligned. add: to fp32 values that are there.
+// buffer and TMA, where the output's rows are 16-byte aligned; TMA adds to fp32 values that are there.
 template <int NC>
 __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
-                                                 uint8_t *buf, bool add) {
+                                                 uint8_t *buf) {
   if (warp_row0 >= a.rows) return;
-  if (add) {   // what an earlier segment has put there is there: sums have one order
-    if (lane == 0) bulk_wait_group_all();
-    __syncwarp();
-  }
 #pragma unroll 1
   for (int c = 0; c < NC; ++c) {
     const int c0 = col0 + 32 * c;
@@ -370,7 +366,7 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
       __syncwarp();
       if (lane == 0) {
         const int x = a.out_f32 ? c0 : c0 - 32 * (c & 1);
-        if (add) tma_add_3d(&a.map_out, buf, x, warp_row0, slice);
+        if (a.accumulate) tma_add_3d(&a.map_out, buf, x, warp_row0, slice);
         else tma_store_3d(&a.map_out, buf, x, warp_row0, slice);
         bulk_commit_group();
       }
@@ -382,7 +378,7 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
 // row (four lanes 64 as bf16).
 template <int NC>
 __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int slice, int warp_row0, int col0, int lane,
-                                             uint8_t *buf, bool accumulate) {
+                                             uint8_t *buf) {
   if (warp_row0 >= a.rows) return;
 #pragma unroll 1
   for (int c = 0; c < NC; ++c) {
@@ -408,7 +404,7 @@ __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int
         if (warp_row0 + i < a.rows)
           store_piece<float, 4>(static_cast<float *>(a.out) + slice * a.slice_stride +
                                     static_cast<long long>(warp_row0 + i) * a.ld_out + c0 + 4 * q,
-                                f, left0 - 4 * q, a.vec, accumulate);
+                                f, left0 - 4 * q, a.vec, a.accumulate != 0);
       }
     } else {
 #pragma unroll
@@ -420,9 +416,25 @@ __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int
         if (warp_row0 + i < a.rows)
           store_piece<__nv_bfloat16, 8>(static_cast<__nv_bfloat16 *>(a.out) +
                                             static_cast<long long>(warp_row0 + i) * a.ld_out + c0 + 8 * q,
-                                        f, left0 - 8 * q, a.vec, accumulate);
+                                        f, left0 - 8 * q, a.vec, a.accumulate != 0);
       }
     }
+  }
+}
+
+// A segment's accumulators (32 NC columns) added to sum, rounding to nearest; with `put` the sums take their place in tensor
+// memory, from where they go out as any tile does. (Added to the output segment by segment, through L2: 668 us with 32 steps,
+// 737 with 16, for 2048 x 50304 x 768.)
+template <int NC>
+__device__ __forceinline__ void add_segment(float (&sum)[32 * NC], uint32_t tmem, bool put) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(tmem + 32 * c, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) sum[32 * c + j] += v[j];
+    if (put) tmem_st_32x32b_x32(tmem + 32 * c, &sum[32 * c]);
   }
 }
 
@@ -486,10 +498,12 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(const ScaleJob a) {
 // six (1 x 128256 x 4096: 170 -> 164 us, 0.94 of the copy bandwidth). The MMA reads 128 rows of A in either case: past a_box
 // it finds what else lies in the stage, which makes accumulator rows that nothing reads.
 //
+// SUMS: a tile's accumulators come in segments of the contraction (SEGMENT), whose sums 8 warps hold, 128 in a thread.
+//
 // JOB: more warps run a ScaleJob, which belongs to other rows than the product's, so that its HBM traffic passes under the
 // MMAs (8192 x 50304 x 768: 1528 -> 1360 us, 4096 x 128256 x 4096: 8.16 -> 7.93 ms). Twelve of them, since each waits for
 // its loads: 1666 us with four, 1358 with eight, 1335 with twelve on another box.
-template <int KIND, int SHAPE, bool JOB>
+template <int KIND, int SHAPE, bool JOB, bool SUMS>
 __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __grid_constant__ CeArgs args) {
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
   constexpr bool PAIR = SHAPE == PAIRED;
@@ -659,20 +673,26 @@ __global__ void __launch_bounds__(gemm_threads(JOB), 1) ce_gemm_kernel(const __g
       decode(args, u, slice, ti, tj);
       const int k0 = slice * args.k_per, k1 = min(args.k_iters, k0 + args.k_per);
       const int warp_row0 = (CTAS * ti + rank) * BM + lane_base, col0 = tj * BN + 32 * NC * half;
+      float sum[SUMS ? 32 * NC : 1];
+#pragma unroll
+      for (int j = 0; j < (SUMS ? 32 * NC : 1); ++j) sum[j] = 0.f;
       for (int ks = k0; ks < k1; ks = segment_end(args, ks, k1)) {
         ok = wait_bounded(&ctrl->acc_full[acc], acc_phase, ctl, ERR_WAIT_ACC_FULL);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tmem = tmem_base + acc * BN + (static_cast<uint32_t>(lane_base) << 16) + 32 * NC * half;
-        if constexpr (KIND == LOGITS || KIND == LOGITS_EXP)
+        const bool whole = !SUMS || segment_end(args, ks, k1) == k1;   // the tile's last segment
+        if constexpr (SUMS) add_segment<NC>(sum, tmem, whole);
+        if (!whole) {
+        } else if constexpr (KIND == LOGITS || KIND == LOGITS_EXP)
           epilogue_logits<KIND == LOGITS_EXP, NC>(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
         else if constexpr (KIND == DLOGITS)
           epilogue_dlogits<NC>(args, tmem, warp_row0 + lane, warp_row0, col0, lane, buf);
         else if (args.tma)
-          epilogue_out_tma<NC>(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
+          epilogue_out_tma<NC>(args, tmem, slice, warp_row0, col0, lane, buf);
         else
-          epilogue_out<NC>(args, tmem, slice, warp_row0, col0, lane, buf, args.accumulate || ks > k0);
+          epilogue_out<NC>(args, tmem, slice, warp_row0, col0, lane, buf);
         tc_fence_before();
         __syncwarp();
         // the MMA warp reads none of this warp's stores, so the signal need not wait for them
@@ -910,9 +930,16 @@ Plan plan(int64_t N, int64_t V, int64_t D, int terms) {
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-template <int KIND, int SHAPE, bool JOB>
+template <int KIND, int SHAPE, bool JOB, bool SUMS = false>
 muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
-  constexpr auto kernel = ce_gemm_kernel<KIND, SHAPE, JOB>;
+  if (a.split < 1) a.split = 1;
+  a.k_per = static_cast<int>(ceil_div(a.k_iters, a.split));
+  a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
+  a.k_seg = SUMS ? SEGMENT : a.k_per;
+  if constexpr ((KIND == DH || KIND == DW) && !JOB && !SUMS)   // more than one segment
+    if (a.out_f32 && a.planes > 1 && a.k_per > SEGMENT && a.k_iters > a.k_low + SEGMENT)
+      return launch_gemm<KIND, SHAPE, JOB, true>(a, kind, s);
+  constexpr auto kernel = ce_gemm_kernel<KIND, SHAPE, JOB, SUMS>;
   constexpr bool PAIR = SHAPE == PAIRED;
   constexpr size_t SMEM = smem_bytes(SHAPE);
   static AttributesSet set;
@@ -944,10 +971,6 @@ muon_status launch_gemm(CeArgs &a, int32_t kind, cudaStream_t s) {
   }
   a.m_tiles = static_cast<int>(ceil_div(a.rows, tile_rows(PAIR)));
   a.n_tiles = static_cast<int>(ceil_div(a.cols, tile_cols(PAIR)));
-  if (a.split < 1) a.split = 1;
-  a.k_per = static_cast<int>(ceil_div(a.k_iters, a.split));
-  a.split = static_cast<int>(ceil_div(a.k_iters, a.k_per));
-  a.k_seg = a.out_f32 && a.planes > 1 ? SEGMENT : a.k_per;
   if (KIND == DH || KIND == DW) {   // rows and columns past the output's are not stored; slices follow each other
     const long long apart = a.split > 1 ? a.slice_stride : a.ld_out;   // one slice has no next one
     if (a.tma && !(a.out_f32 ? make_f32_map(&a.map_out, a.out, a.cols, a.rows, a.split, a.ld_out, apart, 32)
