@@ -67,8 +67,9 @@ constexpr int MAX_SPLIT = 64;
 // An accumulator of the tensor cores loses up to a unit in the last place with each step of 16 products, always towards
 // zero: over a contraction of 128256 that is 2e-5 of the result (dh, 1024 x 128256 x 4096). For fp32 gradients it therefore
 // adds up all of the lower term's products, which are small, and then 8 steps of 64 of the upper one's; the epilogue's threads
-// add that to sums of their own, rounding to nearest (add_segment). The error is then 7e-7. (2048 x 50304 x 768: 641 us with 32
-// steps, whose error is 2.5e-6, 657 with 16 and 1.3e-6, 679 with 8, 714 with 4 and 4e-7.)
+// add that to sums of their own, rounding to nearest (add_segment). The sums' error is then 7e-7, less than the 2^-17 to which
+// two terms hold dz. (2048 x 50304 x 768: 641 us with 32 steps, whose error is 2.5e-6, 657 with 16 and 1.3e-6, 679 with 8, 714
+// with 4 and 4e-7.)
 constexpr int SEGMENT = 8;
 
 // LOGITS leaves statistics alone, LOGITS_EXP the tile's exponentials too (for the joint call).
