@@ -7,9 +7,11 @@
 //   logits  z a tile of 256 x 256 at a time on the tensor cores; a tile's accumulators leave as one running maximum and sum
 //           of exponentials for each row and half tile (online softmax) and the target's logit
 //   combine the parts' pairs into lse and the loss; and h without the rows that have no part in the loss, for dw
-//   dlogits dz = g w (exp(z - lse) - [v = t]), rounded to bf16 as an operand of the two products that follow: in the joint
-//           call of wide rows from the exponentials, which the logits' epilogue has kept; else from the product, computed
-//           again. For fp32 gradients dz is the sum of two bf16 terms, which holds 16 bits of it, and always from the product
+//   dlogits dz = g w (exp(z - lse) - [v = t]), rounded to bf16 as an operand of the two products that follow, without a factor
+//           that all rows share, which the products' sums take: the targets' -1, most of dz, is then exact. It comes
+//           from the exponentials, which the logits' epilogue has kept, in the joint call of wide rows; else from the product,
+//           computed again. For fp32 gradients dz is the sum of two bf16 terms, which holds 16 bits of it, and always from
+//           the product
 //   dh      dz W, the contraction over V cut into slices where the tiles alone would leave SMs without work
 //   dw      dz^T h, added up over the pieces in fp32
 //   reduce  adds slices in their order and rounds once
@@ -119,12 +121,12 @@ struct CeArgs {
   const void *targets;
   int itype;
   const float *weights, *grad, *lse;
-  float grad_scale;
   float2 *partials;                    // [parts][rows]: maximum and sum of exponentials
   float *z_target;                     // [rows]
   // DH, DW
   void *out;
   long long ld_out, slice_stride;      // elements; slice s goes to out + s * slice_stride
+  float factor;                        // of the products
   int out_f32, accumulate, vec, tma;
   ScaleJob job;
   uint32_t *err;
@@ -269,7 +271,7 @@ __device__ __forceinline__ void epilogue_dlogits(const CeArgs &a, uint32_t tmem,
     t = target_of(a.targets, a.itype, row);
     const float w = a.weights != nullptr ? a.weights[row] : 1.f;
     live = t >= 0 && t < a.cols && w != 0.f;
-    scale = w * (a.grad != nullptr ? a.grad[row] : a.grad_scale);
+    scale = a.grad != nullptr ? w * a.grad[row] : w;
     base = -a.lse[row] * LOG2E;
   }
   if (warp_row0 >= a.rows) return;
@@ -347,6 +349,8 @@ __device__ __forceinline__ void epilogue_out_tma(const CeArgs &a, uint32_t tmem,
     float v[32];
     __syncwarp();
     tmem_ld_32x32b_x32(tmem + 32 * c, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= a.factor;
     if (a.out_f32 || c % 2 == 0) {
       if (lane == 0) bulk_wait_group_read<0>();   // the buffer's last store has read it
       __syncwarp();
@@ -389,6 +393,8 @@ __device__ __forceinline__ void epilogue_out(const CeArgs &a, uint32_t tmem, int
       float v[32];
       __syncwarp();   // the buffer's last rows have been read
       tmem_ld_32x32b_x32(tmem + 32 * c, v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= a.factor;
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         *piece(buf, lane, q) = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
@@ -757,7 +763,6 @@ struct CombineArgs {
   int itype, parts, rows;
   long long V;
   float *losses, *lse;
-  float grad_scale;
   float4 *row_state;   // or null
   int own_blocks;      // blocks past these copy h's rows
   RowsArgs copy;
@@ -813,7 +818,7 @@ __global__ void __launch_bounds__(256) ce_combine_kernel(const __grid_constant__
   a.lse[row] = live ? lse : 0.f;
   a.losses[row] = live ? w * (lse - a.z_target[row]) : 0.f;
   if (a.row_state != nullptr)
-    a.row_state[row] = make_float4(-lse * LOG2E, w * a.grad_scale, __int_as_float(live ? static_cast<int>(t) : -1), 0.f);
+    a.row_state[row] = make_float4(-lse * LOG2E, w, __int_as_float(live ? static_cast<int>(t) : -1), 0.f);
 }
 
 struct ReduceArgs {
@@ -1101,7 +1106,7 @@ class Run {
     const CombineArgs cb{partials(r),         z_target_ + r, weights(r),
                          targets(r),          c.itype,       p.parts,
                          static_cast<int>(n), c.V,           c.losses + r0_ + r,
-                         c.lse + r0_ + r,     c.grad_scale,  keep ? row_state_ + r : nullptr,
+                         c.lse + r0_ + r,     keep ? row_state_ + r : nullptr,
                          static_cast<int>(own), copies ? copy_args(r, n) : RowsArgs{}};
     return small(KK_CE_COMBINE, ce_combine_kernel, own + copies, cb);
   }
@@ -1216,7 +1221,7 @@ class Run {
   Run(const Call &call, const Plan &pl, cudaStream_t stream) : c(call), p(pl), s(stream) {
     memset(&base_, 0, sizeof(base_));
     base_.itype = c.itype;
-    base_.grad_scale = c.grad_scale;
+    base_.factor = c.grad_scale;
     base_.planes = p.planes;
     base_.err = reinterpret_cast<uint32_t *>(c.ws);
     base_.timeout_ns = wait_timeout_ns();

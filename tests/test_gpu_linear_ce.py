@@ -313,6 +313,19 @@ def test_joint_gradient_of_a_column_that_no_row_gives_much(L, N, below):
     assert p.max().item() < 1e-3 and err <= 2.0 ** -7.5 + 2 * 2.0 ** -8 + 2.0 ** -12
 
 
+def test_the_shared_factor_is_no_part_of_the_roundings_of_dz(L):
+    """Where no contraction is cut, fp32 gradients are their sum times grad_scale, rounded once."""
+    c = Case(300, 200, 70, weighted=False)
+    got = []
+    for scale in (1.0, 1 / 300):
+        dh, dw = (torch.full((rows, 70), 9.0, device=DEV) for rows in (300, 200))
+        L.linear_cross_entropy_forward_backward(c.h, c.w, c.t, None, scale, c.losses, c.lse, dh, dw, c.ws(L, 2))
+        got.append((dh, dw))
+    factor = torch.tensor(1 / 300, device=DEV)
+    for whole, part in zip(*got):
+        assert torch.equal(part, whole * factor)
+
+
 def test_one_gradient_of_the_two(L):
     c = Case(90, 411, 64, seed=10)
     ref = c.oracle()
