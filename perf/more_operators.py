@@ -38,8 +38,6 @@ def listed():
         # the gradients alone, from the forward pass's normalisers and a gradient for each row; nothing is a multiple
         # of a tile
         dict(name="head_bwd_odd", op="head_bwd", N=1001, V=32003, D=1000, gdt="bf16", idt="i64"),
-        # fp32 gradients of a small model's batch, for an optimizer that adds several up
-        dict(name="head_step_f32", op="head_step", N=2048, V=50304, D=768, gdt="f32", idt="i64"),
         # a model's vectors (norms, biases): many short tensors of odd lengths, latency alone
         dict(name="adamw8_vectors", op="adamw8", many=72, n=768, few=0, big=0, pdt="bf16", gdt="bf16", master=False,
              l2=False),
@@ -71,7 +69,7 @@ def draw(rng):
                      V=rng.choice([50304, 128256, _log(rng, 1000, 260000)]),
                      D=rng.choice([768, 4096, 8 * _log(rng, 8, 768), _log(rng, 65, 6000)]), idt=rng.choice(["i32", "i64"]))
             if c["op"] != "head_fwd":
-                c["gdt"] = rng.choice(["bf16", "bf16", "f32"])
+                c["gdt"] = "bf16"
             if _cost(c) <= most["head"] and c["N"] * c["V"] <= 1 << 29:
                 return c
         else:
