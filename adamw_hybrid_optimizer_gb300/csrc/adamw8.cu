@@ -9,7 +9,7 @@
 // two, so that the 18 of e4m3 cover 36 of v, and because the step needs the root anyway.
 //
 // A scale is its block's largest magnitude / 448, so the largest moment of a block is exact up to fp32 and decays
-// exactly; rounding to nearest. A second moment that is not zero never becomes zero. A moment that is not finite becomes
+// exactly; rounding to nearest. A second moment that fp32 holds above zero keeps a code above zero. A moment that is not finite becomes
 // NaN and leaves the others of its block alone.
 //
 // Bound by HBM: 10 bytes and a 16-byte pair of scales per 256 elements for bf16 weights and gradients (22 bytes with fp32
@@ -40,6 +40,8 @@ constexpr float TOP = 448.f;            // the largest e4m3 value
 constexpr float LEAST = 0x1p-9f;        // the smallest above zero
 // A block whose moments are all below this is scaled as if this were its largest, so that 448 / largest stays finite.
 constexpr float FLOOR = 0x1p-100f;
+// From here on beta2 times the square of a scale is a normal number (for beta2 of 2^-26 or more).
+constexpr float SMALL_SCALE = 0x1p-50f;
 
 // One tensor of a launch; its blocks are numbered from block_begin.
 struct Tensor8 {
@@ -106,18 +108,24 @@ __device__ __forceinline__ float warp_largest_finite(Vals<8> &x) {
 }
 
 // The update of one block: 8 elements per lane. Every rounding is spelled out, so that each way of loading the elements
-// gives the same bits. w: weights in and out; g: gradients; cm, cr: codes in and out; s: scales in and out.
-__device__ __forceinline__ void update(Vals<8> &w, Vals<8> &g, uint2 &cm, uint2 &cr, float2 &s, const AdamwConst &c) {
+// gives the same bits. w: weights in and out; g: gradients; cm, cr: codes in and out; s: scales in and out. The old second moment
+// is beta2 (scale code)^2: the square of a small scale underflows where that, up to 448^2 times as much, does not. Such a scale
+// therefore takes a power of two (up) that the codes give back (down), which changes no other rounding.
+template <bool SCALED>
+__device__ __forceinline__ void update_as(Vals<8> &w, Vals<8> &g, uint2 &cm, uint2 &cr, float2 &s, const AdamwConst &c, float up,
+                                          float down) {
   if (c.l2) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) g.p[k] = __ffma2_rn(both(c.l2_wd), w.p[k], g.p[k]);
   }
   Vals<8> m, r;
-  const float2 km = both(__fmul_rn(s.x, c.beta1)), kr = both(__fmul_rn(__fmul_rn(s.y, s.y), c.beta2));
+  const float sr = SCALED ? __fmul_rn(s.y, up) : s.y;
+  const float2 km = both(__fmul_rn(s.x, c.beta1)), kr = both(__fmul_rn(__fmul_rn(sr, sr), c.beta2));
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int shift = 16 * (k & 1);
-    const float2 q = decode2((k < 2 ? cr.x : cr.y) >> shift);
+    float2 q = decode2((k < 2 ? cr.x : cr.y) >> shift);
+    if constexpr (SCALED) q = __fmul2_rn(q, both(down));
     m.p[k] = __ffma2_rn(km, decode2((k < 2 ? cm.x : cm.y) >> shift), __fmul2_rn(both(c.one_minus_beta1), g.p[k]));
     r.p[k] = root2(__ffma2_rn(kr, __fmul2_rn(q, q), __fmul2_rn(__fmul2_rn(both(c.one_minus_beta2), g.p[k]), g.p[k])));
     const float2 d = __ffma2_rn(r.p[k], both(c.inv_sqrt_bc2), both(c.eps));
@@ -138,6 +146,16 @@ __device__ __forceinline__ void update(Vals<8> &w, Vals<8> &g, uint2 &cm, uint2 
   }
   cm = make_uint2(em[0] | em[1] << 16, em[2] | em[3] << 16);
   cr = make_uint2(er[0] | er[1] << 16, er[2] | er[3] << 16);
+}
+
+// Wide types wait for memory and take the multiplication for every scale (77 M elements, fp32: 187 us, 192 with the branch); bf16
+// ones, which issue more than they load, branch (1.05 G elements: 1647 us, 1708 without).
+template <bool WIDE>
+__device__ __forceinline__ void update(Vals<8> &w, Vals<8> &g, uint2 &cm, uint2 &cr, float2 &s, const AdamwConst &c) {
+  const bool small = s.y < SMALL_SCALE;
+  if constexpr (WIDE) update_as<true>(w, g, cm, cr, s, c, small ? 0x1p40f : 1.f, small ? 0x1p-40f : 1.f);
+  else if (small) update_as<true>(w, g, cm, cr, s, c, 0x1p40f, 0x1p-40f);
+  else update_as<false>(w, g, cm, cr, s, c, 1.f, 1.f);
 }
 
 // A full block of aligned arrays as it lies in memory: lane l has elements 8 l .. 8 l + 7. W: the weights that take the
@@ -164,6 +182,7 @@ struct Block8 {
 template <typename PT, typename GT, bool MASTER>
 __device__ __forceinline__ long long span(const Tensor8 &d, long long b, long long stride, int lane) {
   using W = typename std::conditional<MASTER, float, PT>::type;
+  constexpr bool WIDE = sizeof(W) == 4 || sizeof(GT) == 4;
   W *weights = MASTER ? reinterpret_cast<W *>(d.master) : static_cast<W *>(d.p);
   PT *p = static_cast<PT *>(d.p);
   const GT *g = static_cast<const GT *>(d.g);
@@ -179,7 +198,7 @@ __device__ __forceinline__ long long span(const Tensor8 &d, long long b, long lo
       b += stride;
       if (b < whole) next.load(d, weights, b, lane);
       Vals<8> w = x.w.get(), gv = x.g.get();
-      update(w, gv, x.cm, x.cr, x.s, d.c);
+      update<WIDE>(w, gv, x.cm, x.cr, x.s, d.c);
       if constexpr (MASTER) store_vals(weights + o, w);
       store_vals(p + o, w);
       *reinterpret_cast<uint2 *>(m + o) = x.cm;
@@ -202,7 +221,7 @@ __device__ __forceinline__ long long span(const Tensor8 &d, long long b, long lo
       (k < 4 ? cm.x : cm.y) |= (in ? m[i] : 0u) << (8 * (k & 3));
       (k < 4 ? cr.x : cr.y) |= (in ? r[i] : 0u) << (8 * (k & 3));
     }
-    update(w, gv, cm, cr, s, d.c);
+    update<WIDE>(w, gv, cm, cr, s, d.c);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const long long i = o + 32 * k;
