@@ -272,8 +272,9 @@ typedef struct {
 /* AdamW (adamw_step's update, or adamw_step_master's where a tensor has a master) on n tensors with their moments in 8 bits
  * ([P2] "The optimizer's memory budget"), in one launch per 96 tensors. The update takes the new moments in fp32; then each
  * block's scales become its largest magnitudes / 448 (of 2^-100 at least) and the codes the moments over them, rounded to
- * nearest, ties to even. A second moment that fp32 holds above zero keeps a code above zero. A moment that is not finite becomes NaN, and
- * counts for no scale. The results depend on no tensor's place in the call: they are those of n calls.
+ * nearest, ties to even; first moments whose gradient is zero (in a block where another's is not, and without L2) toward zero if
+ * their code is below 2^-6, so that they end. A second moment that fp32 holds above zero keeps a code above zero. A moment that is
+ * not finite becomes NaN, and counts for no scale. The results depend on no tensor's place in the call: they are those of n calls.
  *   tensors  HOST array of n descriptors (1 <= n <= 2^20). Tensors must not overlap. Any alignment of the elements' own
  *            size works (MUON_ERR_ALIGNMENT otherwise); with 16-byte aligned weights and gradients and 8-byte aligned codes
  *            the accesses are vectors.

@@ -17,8 +17,9 @@ def nearest_code(y):
     return np.clip(np.ldexp(np.round(np.ldexp(y, -e)), e), -TOP, TOP)
 
 
-def quantise(x, root=False):
-    """(codes, scales) of moments x (roots of second moments if root), blocks of BLOCK values, the last one short."""
+def quantise(x, root=False, still=None):
+    """(codes, scales) of moments x (roots of second moments if root), blocks of BLOCK values, the last one short. still: where
+    a first moment has no gradient; in a block where another has one, its codes below 2^-6 are rounded toward zero."""
     codes, scales = np.zeros_like(x), []
     for a in range(0, len(x), BLOCK):
         b = x[a:a + BLOCK]
@@ -27,6 +28,8 @@ def quantise(x, root=False):
         y = b * (TOP / top)
         if root:
             y = np.where(b > 0, np.maximum(y, LEAST), y)
+        if still is not None and not still[a:a + BLOCK].all():
+            y = np.where(still[a:a + BLOCK] & (np.abs(y) < 2.0 ** -6), np.trunc(y / LEAST) * LEAST, y)
         codes[a:a + BLOCK] = np.where(fine, nearest_code(np.where(fine, y, 0.0)), np.nan)
         scales.append(top / TOP)
     return codes, np.array(scales)

@@ -39,3 +39,59 @@ def test_small_roots_decay(L, x, off):
         assert np.all(np.abs(got_r - r) <= r * (2.0 ** -4 * (1 + err) + err))
         assert np.all(np.abs(got_p - p) <= (2e-6 + err) * np.abs(p - p0) + 2.0 ** -23 * np.abs(p0))
         st.g.zero_()
+
+
+def moving(t, n, gen):
+    """Gradients of step t: sizes of a factor of 1.2 or so around 1e-3, and none for every second element from step 41 on."""
+    g = torch.randn(n, generator=gen) * 1e-3 * torch.exp(0.2 * torch.randn(n, generator=torch.Generator().manual_seed(7)))
+    if t > 40:
+        g[::2] = 0.0
+    return g
+
+
+@pytest.mark.parametrize("pdt,gdt,master,off", [("bf16", "bf16", False, 0), ("bf16", "bf16", False, 1), ("f32", "f32", False, 0),
+                                                ("bf16", "f32", True, 0)])
+def test_a_moment_without_gradients_ends(L, pdt, gdt, master, off):
+    """Beside elements that go on: codes above 2^-6 lose more than half a step (beta1 is 0.9), those below a whole one, at every
+    step, so that 18 binades of at most 8 codes each are gone after 18 * 8 steps; the block's scale, of normal gradients, moves too,
+    which may put them back by a part of a code. Each step's codes are the oracle's of what was held, to half a step (a whole one
+    toward zero). The weights of such elements, without decay, then stay."""
+    hp = dict(HP, weight_decay=0.0)
+    n = 1100
+    st = State(n, pdt, gdt, master, off=off, zero=True, seed=4)
+    gen = torch.Generator().manual_seed(5)
+    for t in range(1, 361):
+        st.g.copy_(moving(t, n, gen))
+        before = st.values()
+        step(L, [st], t, hp=hp)
+        p0, g, m0, r0 = before
+        _, m, _ = o8.update(p0, g, m0, r0, t, **hp)
+        _, _, got, _ = st.values()
+        sm = o8.spread(f64(st.s)[:, 0], n)
+        faint = (g == 0) & (np.abs(m) < sm * 2.0 ** -6 * (1 - 1e-6))
+        half = np.maximum(np.abs(m) * 2.0 ** -4, sm * 2.0 ** -10) * (1 + 1e-6) + 1e-6 * (np.abs(m0) + np.abs(g))
+        assert np.all(np.abs(got - m)[~faint] <= half[~faint])
+        lost = np.abs(m) - np.abs(got)
+        assert np.all(lost[faint] >= -1e-6 * np.abs(m[faint])) and np.all(lost[faint] <= (sm * 2.0 ** -9 * (1 + 1e-5))[faint])
+        if t == 300:
+            kept = st.values()[0]
+    now, _, m, r = st.values()
+    assert not m[::2].any() and (r > 0).all() and m[1::2].any()
+    assert np.array_equal(now[::2], kept[::2]) and not np.array_equal(now[1::2], kept[1::2])
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_a_block_without_gradients_shrinks_as_one(L, off):
+    """Its codes stay, since all of its moments take the same factor; its scales take it, to fp32's rounding (once for the product
+    and once for each scaling). Codes are compared as values: a moment of -0 becomes 0."""
+    hp = dict(HP, weight_decay=0.0)
+    st = State(1000, "bf16", "bf16", seed=6, off=off)
+    st.g[256:512] = 0.0
+    st.g[900:] = 0.0
+    cm, cr = st.m[256:512].float(), st.r[256:512].float()
+    for t in range(1, 30):
+        s0 = f64(st.s)
+        step(L, [st], t, hp=hp)
+        assert torch.equal(st.m[256:512].float(), cm) and torch.equal(st.r[256:512].float(), cr)
+        s1 = f64(st.s)
+        assert np.allclose(s1[1], s0[1] * [HP["beta1"], HP["beta2"] ** 0.5], rtol=4e-7, atol=0)
