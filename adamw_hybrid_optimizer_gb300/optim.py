@@ -36,9 +36,12 @@ MUON_DEFAULTS = dict(lr=0.02, momentum=0.95, weight_decay=0.01, nesterov=True, c
 # is_adamw=False: Adam with L2 regularisation instead of decoupled decay ("dtensor-muon 0.1.0", "Key options")
 # state_bits=8: the moments are held as e4m3 codes with a scale per ADAMW8_BLOCK elements, a byte instead of four for each
 # ("The optimizer's memory budget"): "exp_avg" and "exp_avg_sq" in the state are torch.float8_e4m3fn, the latter of the second
-# moment's root, and "scales" (blocks, 2) is fp32
+# moment's root, and "scales" (blocks, 2) is fp32. Rounding to nearest undoes a step that is below half of a code's: betas up to
+# BETAS8 alone (held roots within 0.85 to 1.3 of fp32's; at 0.98 they stay at 1.7 times, and at 12 times where gradients shrink to a
+# tenth; above 15/16 first moments without gradients stay as well)
 ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, is_adamw=True, master_weights=False,
                       state_bits=32)
+BETAS8 = (15 / 16, 0.95)
 
 
 class _Bucket:
@@ -67,6 +70,13 @@ class _Bucket:
         return grads
 
 
+def _check_state_bits(group: Dict):
+    if group["state_bits"] not in (8, 32):
+        raise ValueError("state_bits is 8 or 32")
+    if group["state_bits"] == 8 and any(b > top for b, top in zip(group["betas"], BETAS8)):
+        raise ValueError(f"moments in 8 bits follow betas up to {BETAS8} only, not {tuple(group['betas'])}")
+
+
 def _codes8(p: torch.Tensor) -> torch.Tensor:
     return torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
 
@@ -87,6 +97,8 @@ class HybridMuonAdamW:
             group.update(g)
             group["kind"] = kind
             group["params"] = list(g["params"])
+            if kind == "adamw":
+                _check_state_bits(group)
             for p in group["params"]:
                 if not p.is_cuda:
                     raise ValueError("HybridMuonAdamW runs on the GPU only: parameters must be CUDA tensors")
@@ -115,8 +127,6 @@ class HybridMuonAdamW:
                 ws_bytes = max(ws_bytes, L.muon_workspace_bytes_grouped(shapes) if buckets else 0)
             else:
                 group["step"] = 0
-                if group["state_bits"] not in (8, 32):
-                    raise ValueError("state_bits is 8 or 32")
                 for p in group["params"]:
                     if group["state_bits"] == 8:
                         blocks = (p.numel() + L.ADAMW8_BLOCK - 1) // L.ADAMW8_BLOCK
@@ -140,6 +150,9 @@ class HybridMuonAdamW:
     def step(self):
         """One step of every group. The AdamW tensors of all groups go through one grouped pass, issued in one
         call (hybrid_step) with the last Muon group; those with moments in 8 bits through one of their own."""
+        for group in self.param_groups:   # a schedule may have changed them
+            if group["kind"] == "adamw":
+                _check_state_bits(group)
         muon_calls = []
         adamw_specs = []
         adamw8_specs = []

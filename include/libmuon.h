@@ -275,6 +275,10 @@ typedef struct {
  * nearest, ties to even; first moments whose gradient is zero (in a block where another's is not, and without L2) toward zero if
  * their code is below 2^-6, so that they end. A second moment that fp32 holds above zero keeps a code above zero. A moment that is
  * not finite becomes NaN, and counts for no scale. The results depend on no tensor's place in the call: they are those of n calls.
+ * Over many steps, rounding to nearest undoes a change below half of a code's step (3 to 6%). Held roots stay within 0.85 to 1.3 of
+ * fp32's for beta2 up to 0.95; at 0.97 they reach 1.6, at 0.98 and 0.99 most of them stay at 1.4 to 1.7, and at ten times fp32's
+ * where gradients become a tenth. First moments without gradients end for beta1 up to 15/16. Gradients below 2^-17 of their block's
+ * largest, but not zero, leave first moments of up to five of the smallest codes.
  *   tensors  HOST array of n descriptors (1 <= n <= 2^20). Tensors must not overlap. Any alignment of the elements' own
  *            size works (MUON_ERR_ALIGNMENT otherwise); with 16-byte aligned weights and gradients and 8-byte aligned codes
  *            the accesses are vectors.

@@ -95,3 +95,17 @@ def test_a_block_without_gradients_shrinks_as_one(L, off):
         assert torch.equal(st.m[256:512].float(), cm) and torch.equal(st.r[256:512].float(), cr)
         s1 = f64(st.s)
         assert np.allclose(s1[1], s0[1] * [HP["beta1"], HP["beta2"] ** 0.5], rtol=4e-7, atol=0)
+
+
+def test_roots_follow_those_of_fp32(L):
+    """400 steps of normal gradients of one size, at the default betas: within the bounds that the oracle keeps over 1000."""
+    n = 16384
+    st = State(n, "f32", "f32", zero=True, seed=8)
+    gen = torch.Generator().manual_seed(9)
+    v = np.zeros(n)
+    for t in range(1, 401):
+        st.g.copy_(torch.randn(n, generator=gen) * 1e-3)
+        v = HP["beta2"] * v + (1.0 - HP["beta2"]) * f64(st.g) ** 2
+        step(L, [st], t)
+    low, median, high = np.percentile(st.values()[3] / np.sqrt(v), (5, 50, 95))
+    assert 0.85 < low and 0.97 < median < 1.12 and high < 1.3
