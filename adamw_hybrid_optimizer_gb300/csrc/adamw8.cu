@@ -412,13 +412,19 @@ using namespace muon;
 
 extern "C" {
 
-muon_status adamw8_step_grouped(const adamw8_tensor *tensors, int64_t n, muon_stream_t stream) {
+muon_status adamw8_check_grouped(const adamw8_tensor *tensors, int64_t n) {
   if (tensors == nullptr || n < 1 || n > (1 << 20)) return MUON_ERR_INVALID_ARG;
   muon_status st;
   AdamwConst c{};
   Constants constants;
   for (int64_t i = 0; i < n; ++i)
     if ((st = check_tensor8(tensors[i])) != MUON_OK || (st = constants.get(tensors[i].hp, &c)) != MUON_OK) return st;
+  return MUON_OK;
+}
+
+muon_status adamw8_step_grouped(const adamw8_tensor *tensors, int64_t n, muon_stream_t stream) {
+  muon_status st = adamw8_check_grouped(tensors, n);
+  if (st != MUON_OK) return st;
   if ((st = device_check()) != MUON_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((st = launch_kind<false>(tensors, n, s)) != MUON_OK) return st;

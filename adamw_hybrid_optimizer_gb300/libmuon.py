@@ -88,6 +88,7 @@ SIGNATURES = {
     "adamw_workspace_bytes_grouped": (ctypes.c_size_t, [_c_int64]),
     "adamw_step_grouped": (ctypes.c_int, [ctypes.POINTER(adamw_tensor), _c_int64, _vp, ctypes.c_size_t, _vp]),
     "adamw8_step_grouped": (ctypes.c_int, [ctypes.POINTER(adamw8_tensor), _c_int64, _vp]),
+    "adamw8_check_grouped": (ctypes.c_int, [ctypes.POINTER(adamw8_tensor), _c_int64]),
     "hybrid_step": (ctypes.c_int, [ctypes.POINTER(muon_bucket), ctypes.c_int, ctypes.POINTER(muon_hparams), _vp,
                                    ctypes.c_size_t, ctypes.POINTER(adamw_tensor), _c_int64, _vp, ctypes.c_size_t,
                                    _vp]),
@@ -400,6 +401,13 @@ def adamw8_step_grouped(tensors, stream=None):
     if tensors.device is not None:
         _check_current("adamw8_step_grouped", tensors.device)
     _check(lib().adamw8_step_grouped(tensors, len(tensors), _current_stream(stream)), "adamw8_step_grouped")
+
+
+def adamw8_check_grouped(tensors):
+    """Raises what adamw8_step_grouped would, and launches nothing."""
+    if tensors.device is not None:
+        _check_current("adamw8_step_grouped", tensors.device)
+    _check(lib().adamw8_check_grouped(tensors, len(tensors)), "adamw8_step_grouped")
 
 
 def hybrid_step(buckets, hp, ws, tensors, adamw_ws, stream=None):

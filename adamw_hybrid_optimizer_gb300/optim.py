@@ -149,7 +149,8 @@ class HybridMuonAdamW:
     @torch.no_grad()
     def step(self):
         """One step of every group. The AdamW tensors of all groups go through one grouped pass, issued in one
-        call (hybrid_step) with the last Muon group; those with moments in 8 bits through one of their own."""
+        call (hybrid_step) with the last Muon group; those with moments in 8 bits through one of their own, which is
+        checked before any other part runs. A step that is refused does not count."""
         for group in self.param_groups:   # a schedule may have changed them
             if group["kind"] == "adamw":
                 _check_state_bits(group)
@@ -180,9 +181,8 @@ class HybridMuonAdamW:
                         self._tuned.add(id(group))
                     muon_calls.append((arr, hp))
             else:
-                group["step"] += 1
                 b1, b2 = group["betas"]
-                hp = L.make_adamw_hparams(group["lr"], b1, b2, group["eps"], group["weight_decay"], group["step"],
+                hp = L.make_adamw_hparams(group["lr"], b1, b2, group["eps"], group["weight_decay"], group["step"] + 1,
                                           l2=not group["is_adamw"])
                 for p in group["params"]:
                     if p.grad is None:
@@ -195,10 +195,16 @@ class HybridMuonAdamW:
                         adamw8_specs.append((p, p.grad, st["exp_avg"], st["exp_avg_sq"], st["scales"], hp) + master)
                     else:
                         adamw_specs.append((p, p.grad, st["exp_avg"], st["exp_avg_sq"], hp) + master)
-        adamw8 = L.make_adamw8_tensors(adamw8_specs) if adamw8_specs else None   # its checks before any launch
+        adamw8 = None
+        if adamw8_specs:
+            adamw8 = L.make_adamw8_tensors(adamw8_specs)
+            L.adamw8_check_grouped(adamw8)
         self._launch(muon_calls, adamw_specs)
         if adamw8 is not None:
             L.adamw8_step_grouped(adamw8)
+        for group in self.param_groups:
+            if group["kind"] == "adamw":
+                group["step"] += 1
 
     def _launch(self, muon_calls, adamw_specs):
         if not adamw_specs:

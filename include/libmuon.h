@@ -285,6 +285,10 @@ typedef struct {
  * Errors: as for adamw_step_grouped, all checked before any launch. */
 muon_status adamw8_step_grouped(const adamw8_tensor *tensors, int64_t n, muon_stream_t stream);
 
+/* adamw8_step_grouped's checks alone, on the host: what it would answer but for errors of CUDA and of the device. For a caller
+ * that issues other steps before it and wants none of them to run if it refuses. */
+muon_status adamw8_check_grouped(const adamw8_tensor *tensors, int64_t n);
+
 /* The whole hybrid optimizer step in one call ([P1] "Usage Examples": one optimizer whose step updates the
  * hidden matrices with Muon and every other parameter with AdamW): muon_step_grouped on the buckets, then
  * adamw_step_grouped on the AdamW tensors, on the caller's stream; the results are those of the two calls.
