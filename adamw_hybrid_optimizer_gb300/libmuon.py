@@ -396,17 +396,21 @@ def make_adamw8_tensors(specs):
     return arr
 
 
+def _check_tensors8_current(tensors):
+    device = getattr(tensors, "device", None)   # an array that the caller has filled knows none
+    if device is not None:
+        _check_current("adamw8_step_grouped", device)
+
+
 def adamw8_step_grouped(tensors, stream=None):
     """tensors: a ctypes adamw8_tensor array (see make_adamw8_tensors), on the current device."""
-    if tensors.device is not None:
-        _check_current("adamw8_step_grouped", tensors.device)
+    _check_tensors8_current(tensors)
     _check(lib().adamw8_step_grouped(tensors, len(tensors), _current_stream(stream)), "adamw8_step_grouped")
 
 
 def adamw8_check_grouped(tensors):
     """Raises what adamw8_step_grouped would, and launches nothing."""
-    if tensors.device is not None:
-        _check_current("adamw8_step_grouped", tensors.device)
+    _check_tensors8_current(tensors)
     _check(lib().adamw8_check_grouped(tensors, len(tensors)), "adamw8_step_grouped")
 
 

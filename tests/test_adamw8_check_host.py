@@ -38,3 +38,10 @@ def test_the_binding_raises(monkeypatch):
     monkeypatch.setattr(L, "_current_device", lambda: 1)
     with pytest.raises(ValueError, match="current"):
         L.adamw8_check_grouped(arr)
+
+
+def test_the_binding_takes_an_array_that_the_caller_has_filled():
+    """As adamw_step_grouped's does: not every array comes from make_adamw8_tensors."""
+    L.adamw8_check_grouped((L.adamw8_tensor * 2)(_tensor(), _tensor(gdt=F)))
+    with pytest.raises(L.MuonError):
+        L.adamw8_step_grouped((L.adamw8_tensor * 1)(_tensor(n=0)), stream=0)
