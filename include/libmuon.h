@@ -460,8 +460,8 @@ muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t
  *   targets device N of itype, contiguous.   weights  device fp32, N, or NULL (all 1).
  *   losses, lse  device fp32, N each; lse is kept for the backward pass.
  *   ws      device workspace of ws_bytes >= linear_cross_entropy_workspace_bytes(N, V, D, terms), terms as the call needs
- *           them, 256-byte aligned, zero-filled before its first use; its first 256 bytes are the control block that
- *           muon_check reads.
+ *           them, 256-byte aligned; its first 256 bytes, the control block that muon_check reads, are zero before its first
+ *           use.
  * Limits: N, V <= 2^26, N * V <= 2^40, D <= 65536, ldh, ldw <= 2^37 (MUON_ERR_SHAPE). The same inputs give the same bits. */
 muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t ldh, const void *w, muon_dtype wdt,
                                          int64_t ldw, const void *targets, muon_itype itype, const float *weights,

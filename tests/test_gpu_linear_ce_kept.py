@@ -194,3 +194,31 @@ def test_streams_and_a_captured_call(L):
         torch.cuda.synchronize()
         assert torch.equal(want[0][0], got[0][0]) and torch.equal(want[0][1], got[0][1])
     assert L.muon_check(ws) == L.MUON_OK
+
+
+@pytest.mark.parametrize("N,V,D,rows", [(5, 3001, 40, 0), (300, 901, 136, 0), (700, 500, 72, 256), (40, 20011, 64, 0)])
+@pytest.mark.parametrize("dt", [BF, torch.float32])
+def test_what_the_workspace_held_changes_no_bit(L, N, V, D, rows, dt):
+    """Of the other forms: only the control block has to be zero."""
+    c = Case(N, V, D, seed=N)
+    terms = 1 if dt == BF else 2
+    try:
+        L.muon_debug_loss_rows(rows)
+        ws = c.ws(L, terms)
+        want = None
+        for byte in (0, 255, 127):
+            ws[256:] = byte
+            got = [*outputs(c, dt, dt), *outputs(c, dt, dt)]
+            joint(L, c, 0.5, *got[:2], ws)
+            ws[256:] = byte
+            L.linear_cross_entropy_backward(c.h, c.w, c.t, c.weights, c.lse, c.grad, *got[2:], ws)
+            got += [c.losses.clone(), c.lse.clone()]
+            ws[256:] = byte
+            L.linear_cross_entropy_forward(c.h, c.w, c.t, c.weights, c.losses, c.lse, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(got[-2], c.losses) and torch.equal(got[-1], c.lse)
+            want = want or got
+            for x, y in zip(want, got):
+                assert torch.equal(x, y)
+    finally:
+        L.muon_debug_loss_rows(0)
