@@ -23,23 +23,29 @@ from examples.distill import Embedding, LayerNorm, Model, first_derivative_only 
 
 
 class LinearCrossEntropy(torch.autograd.Function):
-    """Mean over the rows of weights * cross entropy of the head h w^T; targets outside the vocabulary count for nothing."""
+    """Mean over the rows of weights * cross entropy of the head h w^T; targets outside the vocabulary count for nothing. The
+    gradients are made with the loss, of those inputs that require one (detach them where no gradient is wanted)."""
 
     @staticmethod
     def forward(ctx, h, w, targets, weights):
         n, V = h.shape[0], w.shape[0]
         losses, lse = (torch.empty(n, dtype=torch.float32, device=h.device) for _ in range(2))
-        dh, dw = torch.empty_like(h), torch.empty_like(w)
-        ws = torch.zeros(L.linear_cross_entropy_workspace_bytes(n, V, h.shape[1], 1), dtype=torch.uint8, device=h.device)
-        L.linear_cross_entropy_forward_backward(h, w, targets, weights, 1.0 / n, losses, lse, dh, dw, ws)
-        ctx.grads = dh, dw
-        return losses.sum() / n
+        dh, dw = (torch.empty_like(x) if wanted else None for x, wanted in zip((h, w), ctx.needs_input_grad))
+        some = dh is not None or dw is not None
+        ws = torch.empty(L.linear_cross_entropy_workspace_bytes(n, V, h.shape[1], int(some)), dtype=torch.uint8, device=h.device)
+        ws[:256].zero_()   # the control block
+        if some:
+            L.linear_cross_entropy_forward_backward(h, w, targets, weights, 1.0 / max(n, 1), losses, lse, dh, dw, ws)
+        else:
+            L.linear_cross_entropy_forward(h, w, targets, weights, losses, lse, ws)
+        ctx.save_for_backward(dh, dw)
+        return losses.sum() / max(n, 1)
 
     @staticmethod
     def backward(ctx, upstream):
         first_derivative_only("LinearCrossEntropy")
-        (dh, dw), ctx.grads = ctx.grads, None
-        return dh.mul_(upstream), dw.mul_(upstream), None, None
+        dh, dw = (None if g is None else g * upstream for g in ctx.saved_tensors)
+        return dh, dw, None, None
 
 
 def hidden(model, ids):
