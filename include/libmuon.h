@@ -491,8 +491,10 @@ muon_status linear_cross_entropy_backward(const void *h, muon_dtype hdt, int64_t
 
 /* Both in one call, for a training step whose loss is grad_scale * sum of losses: losses and lse as
  * linear_cross_entropy_forward writes them, dh and dw as linear_cross_entropy_backward does with grad = grad_scale for every
- * row, but dz is rounded without grad_scale, which the products' sums take; from D = 512 on and for bf16 gradients it comes from
- * exponentials that are kept in fp16 rather than computed again, a further 2^-12 of each element. */
+ * row, but dz is rounded without grad_scale, which the products' sums take. From D = 512 on and for bf16 gradients it comes from
+ * exponentials that are kept in fp16 rather than computed again: each is off by a further 2^-11 of itself, down to 2^-27 of the
+ * largest among the 128 columns (64 for up to 128 rows) that it was computed with, and by 2^-38 of that largest below, so that it is
+ * zero from there on. Where gradients of columns that far below their neighbours matter, the two calls hold them. */
 muon_status linear_cross_entropy_forward_backward(const void *h, muon_dtype hdt, int64_t ldh, const void *w,
                                                   muon_dtype wdt, int64_t ldw, const void *targets, muon_itype itype,
                                                   const float *weights, float grad_scale, float *losses, float *lse,

@@ -222,3 +222,26 @@ def test_what_the_workspace_held_changes_no_bit(L, N, V, D, rows, dt):
                 assert torch.equal(x, y)
     finally:
         L.muon_debug_loss_rows(0)
+
+
+@pytest.mark.parametrize("N", [40, 300])
+def test_a_column_too_far_below_the_others(L, N):
+    """Column 7's logits lie 30 or so under the others' largest: its exponentials are below 2^-38 of that, zero where they are
+    kept, and computed again by the backward call. h is positive, so nothing cancels: two roundings to bf16, and 2^-12 for the
+    logits."""
+    V, D = 500, 512
+    g = torch.Generator().manual_seed(N)
+    h = (torch.rand((N, D), generator=g) + 0.5).to(DEV, BF)
+    w = (torch.randn((V, D), generator=g) * 0.05).to(DEV, BF)
+    w[7] = -30.0 / D
+    t = torch.randint(8, V, (N,), generator=g).to(DEV)
+    losses, lse = torch.empty(N, device=DEV), torch.empty(N, device=DEV)
+    ws = torch.zeros(L.linear_cross_entropy_workspace_bytes(N, V, D, 1), dtype=torch.uint8, device=DEV)
+    kept, again = torch.empty_like(w), torch.empty_like(w)
+    L.linear_cross_entropy_forward_backward(h, w, t, None, 1.0, losses, lse, None, kept, ws)
+    L.linear_cross_entropy_backward(h, w, t, None, lse, None, None, again, ws)
+    z = h.double() @ w.double().t()
+    assert (z[:, 7] - z[:, :64].max(1).values).max().item() < -38 * np.log(2.0)
+    want = torch.softmax(z, 1)[:, 7] @ h.double()
+    assert not kept[7].any()
+    assert ((again[7].double() - want) / want).abs().max().item() <= 2 * 2.0 ** -8 + 2.0 ** -12
