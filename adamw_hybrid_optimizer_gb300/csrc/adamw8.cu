@@ -37,8 +37,8 @@ namespace {
 
 constexpr int BLOCK = ADAMW8_BLOCK;
 // Resident blocks: 32 warps of 64 registers where weights and gradients are bf16, 24 of 80 where one is fp32 or there is a
-// master. (1.05 G elements, bf16: 1631 us with 4 blocks, 1679 with 3.5, 1980 with 4.5, whose 56 registers spill; 77 M
-// elements, fp32: 188 us with 3, 201 with 3.5.)
+// master. (1.05 G elements, bf16: 1692 us with 4 blocks, 1721 with 3, 1739 with 3.5, 2145 with 5; 77 M elements, fp32: 185 us with
+// 3, 200 with 2, 203 with 3.5, 213 with 4. The kernels spill 20 and 36 bytes a thread so; with 5 and 4 blocks 164 and 244.)
 constexpr int THREADS = 256;
 constexpr int NARROW_BLOCKS = 4;
 constexpr int WIDE_BLOCKS = 3;

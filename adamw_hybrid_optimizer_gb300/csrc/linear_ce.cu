@@ -3,7 +3,7 @@
 //     lse_i = log sum_v exp z_iv,   loss_i = w_i (lse_i - z_it),   dz_iv = g_i w_i (exp(z_iv - lse_i) - [v = t_i])
 //     dh = dz W,   dW = dz^T h
 //
-// Rows go through in pieces (plan()); nothing of size N x V outlives a piece. Per piece:
+// Rows go through in pieces of up to 2^30 logits (plan()); of a piece, only gradients put its dz into memory. Per piece:
 //   logits  z a tile of 256 x 256 at a time on the tensor cores; a tile's accumulators leave as one running maximum and sum
 //           of exponentials for each row and half tile (online softmax) and the target's logit
 //   combine the parts' pairs into lse and the loss; and h without the rows that have no part in the loss, for dw

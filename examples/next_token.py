@@ -1,4 +1,4 @@
-"""A small language model trained to predict the next token, without its two largest arrays: the logits and fp32 moments.
+"""A small language model trained to predict the next token, without fp32 moments, and without logits beyond a bounded piece.
 
 The model is that of examples/distill.py (embedding lookup, residual blocks of layer norm and a two-layer MLP, a last
 norm). Its loss is the cross entropy of the vocabulary head, taken with both gradients in one call from the hidden states

@@ -449,7 +449,7 @@ muon_status distill_forward_backward(const void *logits, muon_dtype zdt, int64_t
                                      int64_t ldd, int64_t N, int64_t V, int64_t K, float temperature,
                                      muon_stream_t stream);
 
-/* The cross entropy of a linear head, z = h w^T, without keeping the N x V logits:
+/* The cross entropy of a linear head, z = h w^T, without keeping the N x V logits (a piece of them where gradients are made):
  *   losses_i = weights_i * (lse_i - z_i,targets_i),   lse_i = log sum_v exp z_iv.
  * A row whose target lies outside [0, V) (padding: -100, say) or whose weight is 0 has loss 0, lse 0 and no part in any
  * gradient, whatever its h (NaN included). The logits are fp32 sums of bf16 products, computed in tiles that are reduced
@@ -472,7 +472,8 @@ muon_status linear_cross_entropy_forward(const void *h, muon_dtype hdt, int64_t 
  * is fp32. A call also takes a workspace for more terms than its own. A piece has at most 2^30 logits and elements of h, or
  * 256 rows: without gradients 8 bytes for each 128 logits (64 where a piece has up to 128 rows); with gradients 2 * terms
  * bytes more for each logit and a copy of h, what dh's or dw's fp32 sums need where few tiles share a long contraction, and,
- * for more than one piece, fp32 sums of dw. 0 for N < 0, V < 1, D < 1, sizes beyond the limits or other terms. */
+ * for more than one piece, fp32 sums of dw. With gradients that is at least the size of the logits in bf16 up to 2^30 of them. A
+ * smaller N can need more, where slices begin to pay: what several N share is sized by the largest of theirs. 0 for N < 0, V < 1, D < 1, sizes beyond the limits or other terms. */
 size_t linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int terms);
 
 /* Its gradients from linear_cross_entropy_forward's lse: with dz_iv = grad_i * weights_i * (exp(z_iv - lse_i) -
