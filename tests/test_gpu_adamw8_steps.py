@@ -109,3 +109,26 @@ def test_roots_follow_those_of_fp32(L):
         step(L, [st], t)
     low, median, high = np.percentile(st.values()[3] / np.sqrt(v), (5, 50, 95))
     assert 0.85 < low and 0.97 < median < 1.12 and high < 1.3
+
+
+@pytest.mark.parametrize("pdt,gdt,master", [("bf16", "bf16", False), ("f32", "f32", False), ("bf16", "f32", True), ("bf16", "f32", False),
+                                            ("f32", "bf16", False)])
+@pytest.mark.parametrize("l2", [False, True])
+def test_alignment_changes_no_bit_of_sparse_and_small_gradients(L, pdt, gdt, master, l2):
+    """Full aligned blocks and single elements go different ways, and bf16 blocks branch where a scale is small or some element
+    has no gradient: the same bits."""
+    n = 3000
+    a, b = (State(n, pdt, gdt, master, off=o, zero=True, seed=10) for o in (0, 1))
+    gen = torch.Generator().manual_seed(11)
+    size = torch.ones(n) * 1e-3
+    size[256:1100] = 1e-21          # roots whose square fp32 holds, of scales whose square it does not
+    size[1100:1400] = 1e-17
+    for t in range(1, 41):
+        g = torch.randn(n, generator=gen) * size
+        g[torch.rand(n, generator=gen) < (0.0, 0.1, 0.9)[t % 3]] = 0.0
+        g[512:768] = 0.0 if t % 2 else g[512:768]
+        for s in (a, b):
+            s.g.copy_(g)
+            step(L, [s], t, l2=l2)
+    for x, y in zip(a.bits(), b.bits()):
+        assert torch.equal(x, y)
